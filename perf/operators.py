@@ -131,7 +131,9 @@ def _quantised(x, fmt):
     x = x.float()
     if fmt == "bf16":
         return x.to(torch.bfloat16), None
-    scale = (x.abs().amax(-1) / QMAX[fmt]).clamp_min(TINY)
+    largest = x.abs().amax(-1)
+    # a true quotient: torch multiplies by the reciprocal of a plain number
+    scale = (largest / torch.full_like(largest, QMAX[fmt])).clamp_min(TINY)
     y = x / scale[..., None]
     return (y.round().to(torch.int8) if fmt == "int8" else y.to(torch.float8_e4m3fn)), scale
 
