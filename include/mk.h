@@ -343,6 +343,164 @@ void mk_free(void* handle);
 
 const char* mk_last_error(void);
 
+/* ---------------------------------------------------------------------------
+ * Operators on paged caches and logits. They run beside the decode step, on
+ * memory the caller owns: no model handle, no allocation, no state kept
+ * between calls. All of them are asynchronous on `stream`, may be captured
+ * into a CUDA graph, and check on the host what the host can see (NULL
+ * pointers, shapes, alignment: MK_ERR_INVALID_ARG; shapes no kernel exists
+ * for: MK_ERR_UNSUPPORTED). What only the device can see (positions and page
+ * numbers out of range) never leads to an access outside the cache: the row
+ * in question is skipped and, when `status` (device int32, or NULL) is
+ * given, MK_ERR_INVALID_ARG is stored in it (the library never clears it).
+ * ------------------------------------------------------------------------- */
+
+/* How a page's rows are stored.
+ *  MK_KV_BF16  bf16 values, no scales;
+ *  MK_KV_E4M3  one FP8 E4M3 code a value (as in MX: no infinities, largest
+ *              448), one fp32 scale a row;
+ *  MK_KV_INT8  one signed byte a value in [-127, 127], one fp32 scale a row.
+ * A row is head_dim values of one position and one kv head; its value i is
+ * code[i] x scale. */
+enum mk_kv_format { MK_KV_BF16 = 0, MK_KV_E4M3 = 1, MK_KV_INT8 = 2 };
+
+/* Element types of rows, queries and logits given to the operators. */
+enum mk_dtype { MK_DT_F32 = 0, MK_DT_BF16 = 1, MK_DT_F16 = 2 };
+
+/* One layer's K and V pages in device memory. Row r of kv head h in page p
+ * starts p*page_stride + h*head_stride + r*row_stride elements after k (or
+ * v); its scale is at p*scale_page_stride + h*scale_head_stride + r of
+ * k_scale (or v_scale; NULL for MK_KV_BF16). k, v and the strides in bytes
+ * are multiples of 8 elements, for mk_pages_attend also of 16 bytes.
+ * page_size is a power of two; head_dim a multiple of 8, at most 256. Rows of
+ * different (page, head, row) must not overlap. */
+typedef struct mk_pages {
+    void *k, *v;
+    float *k_scale, *v_scale;
+    int64_t page_stride, head_stride, row_stride;
+    int64_t scale_page_stride, scale_head_stride;
+    int32_t format, n_pages, n_kv_heads, page_size, head_dim, reserved;
+} mk_pages;
+
+/* The pages of a batch: position j of sequence b is row j % page_size of page
+ * table[b*stride + j / page_size] (device int32), for j below
+ * pages_per_seq * page_size. */
+typedef struct mk_page_table {
+    const int32_t* table;
+    int64_t stride;
+    int32_t batch, pages_per_seq;
+} mk_page_table;
+
+/* Rows outside a cache (device memory): element i of kv head h of token t of
+ * sequence b at b*seq_stride + t*token_stride + h*head_stride + i, of type
+ * `dtype`. */
+typedef struct mk_rows {
+    void* data;
+    int64_t seq_stride, token_stride, head_stride;
+    int32_t dtype, reserved;
+} mk_rows;
+
+/* mk_kv_write for a caller's pages, quantising on the way: tokens t in
+ * [0, counts[b]) (counts: device int32 [batch]; NULL: all n) of sequence b go
+ * to positions positions[b] + t (positions: device int32 [batch]). For the
+ * 8-bit formats a row's scale is max|x| / 448 (E4M3) or max|x| / 127 (INT8),
+ * at least 2^-126, its codes x / scale rounded to nearest, ties to even; the
+ * quotients are correctly rounded 32-bit ones. A row with a NaN or an infinity
+ * gets a NaN scale and zero codes: it reads back as NaN throughout. Rows past
+ * counts[b], and every other row of the cache, stay as they are. The positions
+ * a call writes must be distinct rows of the cache (two sequences sharing a
+ * page write neither of their shared positions). */
+int mk_pages_write(const mk_pages* pages, const mk_page_table* table, const int32_t* positions, const int32_t* counts,
+                   int32_t n, const mk_rows* k, const mk_rows* v, int32_t* status, void* stream);
+
+/* The way back: rows t in [0, counts[b]) of `k` and `v` become code x scale
+ * of positions positions[b] + t, rounded to their type. Rows past counts[b]
+ * and rows of positions or pages out of range stay as they are. */
+int mk_pages_read(const mk_pages* pages, const mk_page_table* table, const int32_t* positions, const int32_t* counts,
+                  int32_t n, const mk_rows* k, const mk_rows* v, int32_t* status, void* stream);
+
+/* The pages of one layer of a model's KV cache (GQA models: MK_KV_BF16 pages
+ * of 64 positions) and its block table, for the operators of this section:
+ * what the decode step wrote can be read, attended to or written by them.
+ * Valid until the cache is freed; mk_kv_set_block_table changes the table in
+ * place. Errors: INVALID_ARG; UNSUPPORTED for MLA (its rows are a latent and
+ * a rope part, not K and V). */
+int mk_kv_view(const mk_kv* kv, int32_t layer, mk_pages* pages, mk_page_table* table);
+
+/* Attention of the last n_tokens positions of every sequence over its pages.
+ * lens[b] counts the cached positions of sequence b, the new ones included
+ * (write them first): token t sits at p = lens[b] - n_tokens + t and sees the
+ * positions j with starts[b] <= j <= p. With x = scale q.k_j, capped to
+ * softcap * tanh(x / softcap) when softcap > 0, less slopes[h] * (p - j):
+ *   out = sum_j softmax(x)_j v_j,    lse = log sum_j exp(x_j).
+ * A token that sees nothing (a padded sequence of length 0, p < 0, a start
+ * past p) gets zeros and lse -infinity; values it does not see, NaN and
+ * infinities among them, do not reach its row. Query head h reads kv head
+ * h / (n_q_heads / n_kv_heads).
+ *
+ * shared_len > 0 says that the first shared_len positions of all sequences
+ * lie in the same pages (the first shared_len / page_size entries of every
+ * table row are those of row 0; a multiple of page_size): they are read once
+ * for the whole batch, as one product over all its queries. Sequences of
+ * length 0 may be among them; every other one must be at least shared_len
+ * long, shorter ones see the part they have. */
+typedef struct mk_attention {
+    const mk_pages* pages;
+    const mk_page_table* table;
+    const int32_t* lens;   /* device [batch] */
+    const int32_t* starts; /* device [batch], or NULL: 0 (first visible position: a document's start, left padding) */
+    const float* slopes;   /* device [n_q_heads], or NULL: no bias */
+    const mk_rows* q;      /* [batch][n_tokens][n_q_heads], MK_DT_BF16 or MK_DT_F16 */
+    const mk_rows* out;    /* the same shape and type, written */
+    float* lse;            /* device [batch][n_tokens][n_q_heads], or NULL */
+    int32_t* status;       /* device, or NULL */
+    int32_t n_tokens, n_q_heads;
+    float scale, softcap;
+    int32_t shared_len, reserved;
+} mk_attention;
+
+/* Bytes of device workspace mk_pages_attend needs for a call of these shapes
+ * (they do not depend on lens). The workspace belongs to one call until the
+ * call has run: calls that may overlap on the GPU (other streams, captured
+ * graphs replayed side by side) take one each. Its contents need no
+ * initialisation. */
+int mk_pages_attend_workspace(const mk_attention* args, int64_t* bytes);
+
+/* Errors: INVALID_ARG (NULL, shapes, alignment, a workspace too small or not
+ * 256-byte aligned), UNSUPPORTED (head_dim other than 64, 128 or 256). A length beyond the
+ * table or a page out of range is reported through `status`; what lies there
+ * counts as rows of zeros, or beyond the table as not visible. */
+int mk_pages_attend(const mk_attention* args, void* workspace, int64_t workspace_bytes, void* stream);
+
+/* Draws one token a row from logits. With w_i = exp((x_i - max x) / T), in 32
+ * bits, tokens ranked by (x descending, index ascending) and sums in 64 bits:
+ *   top-k  keeps ranks 0 .. k-1 (k <= 0 or k >= vocab: every token);
+ *   top-p  then keeps the ranks with less than p times top-k's mass before
+ *          them (p >= 1: all of them; the first rank always stays);
+ *   min-p  then keeps weights of at least min_p (the largest weight is 1; the
+ *          first rank always stays);
+ * and the token is the first kept one, in index order, whose running sum of
+ * kept weights exceeds u times their total. T <= 0 takes the largest logit
+ * (lowest index). -infinity masks a token: it is never kept. A row with a NaN
+ * or +infinity, or with no token unmasked, has no distribution: token -1. */
+typedef struct mk_sampling {
+    const void* logits;       /* device [rows][row_stride], `dtype` (mk_dtype) */
+    int64_t row_stride;       /* elements */
+    const float* u;           /* device [rows]: the random numbers, in [0, 1) */
+    const float* temperature; /* device [rows], or NULL: 1 */
+    const int32_t* top_k;     /* device [rows], or NULL: no limit */
+    const float* top_p;       /* device [rows], or NULL: 1 */
+    const float* min_p;       /* device [rows], or NULL: 0 */
+    int32_t* tokens;          /* device [rows], written */
+    float* probs;             /* device [rows] or NULL: the token's share of the kept mass (0 for token -1) */
+    int32_t* kept;            /* device [rows] or NULL: how many tokens were kept */
+    int32_t rows, vocab, dtype, reserved;
+} mk_sampling;
+
+/* Errors: INVALID_ARG (NULL, sizes, alignment), UNSUPPORTED (vocab above
+ * 360448). Deterministic: the same inputs give the same tokens. */
+int mk_sample(const mk_sampling* args, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

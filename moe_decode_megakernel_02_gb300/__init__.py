@@ -27,7 +27,8 @@ EXPORTS = ("mk_load_weights", "mk_load_synthetic", "mk_alloc_kv", "mk_kv_set_blo
            "mk_kv_write", "mk_kv_read", "mk_decode_step", "mk_decode_step_unfused", "mk_decode_step_noalloc",
            "mk_step_status",
            "mk_debug_routing", "mk_debug_scratch_read", "mk_last_argmax", "mk_model_info", "mk_trace_read", "mk_free",
-           "mk_last_error")
+           "mk_last_error",
+           "mk_pages_write", "mk_pages_read", "mk_pages_attend", "mk_pages_attend_workspace", "mk_kv_view", "mk_sample")
 TRACE_CAP = 8192
 
 
@@ -36,9 +37,11 @@ def build_cmds() -> list:
     synthetic loader, which links the input generator module) and for a
     second build of the same sources with a 2-slot ring (MK_NSLOT=2)."""
     os.makedirs(_BUILD, exist_ok=True)
-    srcs = [os.path.join(_HERE, "csrc", "mk_host.cu"), os.path.join(_HERE, "csrc", "mk_synth.cu"),
-            os.path.join(_ROOT, "synth", "synth_cuda.cu"), os.path.join(_ROOT, "synth", "synth_host.c")]
-    base = ["nvcc", "-gencode", "arch=compute_103a,code=sm_103a", "-O3", "-lineinfo", "-std=c++17",
+    srcs = [os.path.join(_HERE, "csrc", f) for f in (
+        "mk_host.cu", "mk_synth.cu", "mk_pages.cu", "mk_sample.cu", "mk_attend.cu", "mk_attend_d64.cu",
+        "mk_attend_d128.cu", "mk_attend_d256.cu")]
+    srcs += [os.path.join(_ROOT, "synth", "synth_cuda.cu"), os.path.join(_ROOT, "synth", "synth_host.c")]
+    base = ["nvcc", "--threads", "0", "-gencode", "arch=compute_103a,code=sm_103a", "-O3", "-lineinfo", "-std=c++17",
             "-Xcompiler", "-fPIC", "-shared", "-lpthread"]
     return [base + srcs + ["-o", os.path.join(_BUILD, "libmk.so")],
             base + ["-DMK_NSLOT=2"] + srcs + ["-o", LIB_NSLOT2]]
@@ -62,6 +65,48 @@ class Info(ctypes.Structure):
     _fields_ = [("weight_bytes", ctypes.c_int64), ("scratch_bytes", ctypes.c_int64)] + [
         (n, ctypes.c_int32) for n in ("grid_ctas", "threads_per_cta", "smem_bytes", "ring_slots", "slot_bytes",
                                       "sm_count")]
+
+
+# mk_kv_format and mk_dtype
+KV_BF16, KV_E4M3, KV_INT8 = 0, 1, 2
+DT_F32, DT_BF16, DT_F16 = 0, 1, 2
+
+
+class PagesStruct(ctypes.Structure):
+    """mk_pages"""
+    _fields_ = [(n, ctypes.c_void_p) for n in ("k", "v", "k_scale", "v_scale")] + [
+        (n, ctypes.c_int64) for n in ("page_stride", "head_stride", "row_stride", "scale_page_stride",
+                                      "scale_head_stride")] + [
+        (n, ctypes.c_int32) for n in ("format", "n_pages", "n_kv_heads", "page_size", "head_dim", "reserved")]
+
+
+class TableStruct(ctypes.Structure):
+    """mk_page_table"""
+    _fields_ = [("table", ctypes.c_void_p), ("stride", ctypes.c_int64), ("batch", ctypes.c_int32),
+                ("pages_per_seq", ctypes.c_int32)]
+
+
+class RowsStruct(ctypes.Structure):
+    """mk_rows"""
+    _fields_ = [("data", ctypes.c_void_p), ("seq_stride", ctypes.c_int64), ("token_stride", ctypes.c_int64),
+                ("head_stride", ctypes.c_int64), ("dtype", ctypes.c_int32), ("reserved", ctypes.c_int32)]
+
+
+class AttentionStruct(ctypes.Structure):
+    """mk_attention"""
+    _fields_ = [("pages", ctypes.POINTER(PagesStruct)), ("table", ctypes.POINTER(TableStruct))] + [
+        (n, ctypes.c_void_p) for n in ("lens", "starts", "slopes")] + [
+        ("q", ctypes.POINTER(RowsStruct)), ("out", ctypes.POINTER(RowsStruct)), ("lse", ctypes.c_void_p),
+        ("status", ctypes.c_void_p), ("n_tokens", ctypes.c_int32), ("n_q_heads", ctypes.c_int32),
+        ("scale", ctypes.c_float), ("softcap", ctypes.c_float), ("shared_len", ctypes.c_int32),
+        ("reserved", ctypes.c_int32)]
+
+
+class SamplingStruct(ctypes.Structure):
+    """mk_sampling"""
+    _fields_ = [("logits", ctypes.c_void_p), ("row_stride", ctypes.c_int64)] + [
+        (n, ctypes.c_void_p) for n in ("u", "temperature", "top_k", "top_p", "min_p", "tokens", "probs", "kept")] + [
+        (n, ctypes.c_int32) for n in ("rows", "vocab", "dtype", "reserved")]
 
 
 class MKError(RuntimeError):
@@ -101,10 +146,17 @@ def lib():
         L.mk_free.argtypes = [P]
         L.mk_free.restype = None
         L.mk_last_error.restype = ctypes.c_char_p
+        L.mk_pages_write.argtypes = [P, P, P, P, I32, P, P, P, P]
+        L.mk_pages_read.argtypes = [P, P, P, P, I32, P, P, P, P]
+        L.mk_pages_attend.argtypes = [P, P, ctypes.c_int64, P]
+        L.mk_pages_attend_workspace.argtypes = [P, ctypes.POINTER(ctypes.c_int64)]
+        L.mk_kv_view.argtypes = [P, I32, P, P]
+        L.mk_sample.argtypes = [P, P]
         for f in ("mk_load_weights", "mk_load_synthetic", "mk_alloc_kv", "mk_kv_set_block_table", "mk_kv_write",
                   "mk_kv_read", "mk_decode_step", "mk_decode_step_unfused", "mk_decode_step_noalloc", "mk_step_status",
                   "mk_debug_routing",
-                  "mk_debug_scratch_read", "mk_last_argmax", "mk_model_info", "mk_trace_read"):
+                  "mk_debug_scratch_read", "mk_last_argmax", "mk_model_info", "mk_trace_read", "mk_pages_write",
+                  "mk_pages_read", "mk_pages_attend", "mk_pages_attend_workspace", "mk_kv_view", "mk_sample"):
             getattr(L, f).restype = ctypes.c_int
         _lib = L
     return _lib
@@ -261,6 +313,12 @@ class KVCache:
         out = np.empty((n, row), dtype=np.uint16)
         _check(lib().mk_kv_read(self.h, layer, seq, pos0, n, out.ctypes.data, _stream(stream)))
         return out
+
+    def pages(self, layer):
+        """The layer's pages as a `pages.Pages` over the cache's own memory, with its block table as `.table`
+        (mk_kv_view; GQA models)."""
+        from . import pages
+        return pages.of_cache(self, layer)
 
     def close(self):
         if getattr(self, "h", None):

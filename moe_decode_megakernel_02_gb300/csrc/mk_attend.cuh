@@ -1,0 +1,1089 @@
+// mk_attend.cuh -- attention of a few new tokens a sequence over paged K and
+// V (mk_pages_attend).
+//
+// For one query row (a token and a query head) and the positions j it sees,
+//   x_j = cap(scale q.k_j) - slope (p - j),  m = max x_j,
+//   out = sum_j e^(x_j - m) v_j / sum_j e^(x_j - m),
+// in one pass: a running maximum, the sum and the output rescaled when the
+// maximum rises. Rows of one kv head (n_tokens x query heads of the group) are
+// the M of two chains of m16n8k16 tensor-core products, positions the N of
+// the first and the K of the second.
+//
+// Two shapes of the same loop over 64- or 128-position tiles (cp.async ring in
+// shared memory):
+//   FEW   up to 32 rows an item: the four warps split a tile's positions and
+//         hold the same rows; their maxima, sums and outputs meet at the end.
+//         Bound by the cache's bytes.
+//   MANY  64 rows an item: the four warps split the rows and all read the
+//         whole tile: large verify blocks, and the shared prefix, where the
+//         rows of all sequences stand against one copy of K and V. Bound by
+//         the tensor cores.
+//
+// Work is cut by tiles, not by sequences: the tiles of all items (sequence,
+// kv head, row block) are numbered in one line and every CTA takes an equal
+// stretch of it, whatever the lengths are; lengths are read on the device, so
+// a captured graph keeps working as they grow. An item that lies within one
+// CTA is finished by it; pieces of an item leave (output, maximum, sum) in the
+// workspace and a second launch joins them.
+//
+// Rounding. Scores and sums are 32-bit. bf16 pages: queries are exact in bf16
+// (16-bit floats: hi + lo parts), probabilities go in as hi + lo bf16 parts,
+// so a product keeps 16 bits. 8-bit pages: codes are exact in fp16; a query
+// row is scaled by a power of two into fp16 (exact but for values 2^-24 below
+// the row's largest); the K scale multiplies the score, the V scale the
+// probability, which goes in as one fp16 (11 bits), scaled by 2^15 over the
+// largest V scale so far: products below 2^-29 of the largest possible one
+// fall under fp16's normal range and keep steps of 2^-39 of it.
+#pragma once
+#include "mk_ops.cuh"
+
+namespace mkop {
+
+struct AttendP {
+    const uint8_t *k, *v;
+    const float *ks, *vs;
+    long long page_b, head_b, row_b;  // bytes
+    long long sc_page, sc_head;       // floats
+    const int* table;
+    long long table_s;
+    int pps, ps_shift, n_pages;
+    const int *lens, *starts;
+    const float* slopes;
+    const uint16_t* q;
+    long long qb, qt, qh;
+    uint16_t* out;
+    long long ob, ot, oh;
+    float* lse;
+    int* status;
+    int B, T, H, G, f16;
+    float scale, cap;
+    int shared;      // positions in shared pages: the shared launch covers [0, shared), the other one the rest
+    int is_shared;   // this is the shared launch (one virtual sequence, rows of the whole batch)
+    int RB;          // row blocks of an item
+    int rows_item;   // rows of one (sequence, kv head): T * G, or B * T * G
+    int keep_items;  // finished items go to the workspace too (a shared part joins them)
+    int min_units;   // a CTA's least stretch of tiles
+    int slot_rows;   // rows of a slot: slot_rows * D outputs, then (maximum, sum) pairs
+    int slot_floats;
+    float* slots;    // two of each CTA (its first and its last piece), then one of each item
+    long long* base;  // [B + 1]: first unit of each sequence, written for the joining launch
+};
+
+struct JoinP {
+    AttendP own, shared;
+    int own_grid, shared_grid;  // CTAs; shared_grid 0: no shared part
+    int own_rows, shared_rows;  // rows of a row block
+    int shared_units;           // tiles of a shared item
+};
+
+constexpr int AT = 128;  // threads of an attention CTA
+constexpr float LOG2E = 1.4426950408889634f, LN2 = 0.6931471805599453f;
+
+// units (tiles) of each CTA when `total` are shared out over `grid`
+__host__ __device__ __forceinline__ long long units_each(long long total, int grid, int min_units) {
+    const long long e = (total + grid - 1) / grid;
+    return e < min_units ? min_units : e;
+}
+
+// the positions of sequence b that a launch covers, [lo, hi)
+__device__ __forceinline__ void cover(const AttendP& p, int b, int& lo, int& hi) {
+    if (p.is_shared) {
+        lo = 0;
+        hi = p.shared;
+        return;
+    }
+    const int cap = p.pps << p.ps_shift;
+    lo = max(p.starts ? p.starts[b] : 0, p.shared);
+    hi = min(p.lens[b], cap);
+}
+template <int TILE>
+__device__ __forceinline__ int cover_units(const AttendP& p, int b) {
+    int lo, hi;
+    cover(p, b, lo, hi);
+    return hi > lo ? (hi + TILE - 1) / TILE - lo / TILE : 0;
+}
+
+__device__ __forceinline__ uint32_t sm32(const void* p) { return (uint32_t)__cvta_generic_to_shared(p); }
+__device__ __forceinline__ void cp16(uint32_t dst, const void* src, bool ok) {
+    const int n = ok ? 16 : 0;  // 0: the 16 bytes are filled with zeros, nothing is read
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
+}
+__device__ __forceinline__ void cp4(uint32_t dst, const void* src, bool ok) {
+    const int n = ok ? 4 : 0;
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
+}
+__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+__device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t a) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(a));
+}
+__device__ __forceinline__ void ldsm4t(uint32_t (&r)[4], uint32_t a) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(a));
+}
+template <bool F16>
+__device__ __forceinline__ void mma(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    if constexpr (F16)
+        asm volatile(
+            "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+            : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+            : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+    else
+        asm volatile(
+            "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+            : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+            : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// Two codes as two fp16 values, both exact. `pair` holds them in its low bytes.
+template <int FMT>
+__device__ __forceinline__ uint32_t e4m3_pair(uint32_t pair) {
+    const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)pair, __NV_E4M3);
+    return (uint32_t)h.x | (uint32_t)h.y << 16;
+}
+// signed bytes plus 128 set into the mantissa of 1024 give 1152 + code
+__device__ __forceinline__ uint32_t int8_half2(uint32_t w) {
+    __half2 h = *reinterpret_cast<__half2*>(&w);
+    const uint32_t c = 0x64806480u;  // 1152, 1152
+    h = __hsub2(h, *reinterpret_cast<const __half2*>(&c));
+    return *reinterpret_cast<uint32_t*>(&h);
+}
+
+// ROWB bytes of a row in shared memory: 16-byte pieces stored at piece ^ f(row),
+// so that eight consecutive rows' pieces lie in different banks
+template <int ROWB>
+__device__ __forceinline__ uint32_t piece(uint32_t base, int row, int c) {
+    const int x = ROWB >= 128 ? (row & 7) : ((row >> 1) & 3);
+    return base + row * ROWB + ((c ^ x) << 4);
+}
+
+template <int D, int FMT, bool SPLITQ, bool MANY, int MT>
+struct Shape {
+    static constexpr bool F8 = FMT != MK_KV_BF16;
+    static constexpr int EB = F8 ? 1 : 2;                  // bytes of a cached value
+    static constexpr int ROWB = D * EB;                    // bytes of a cached row
+    static constexpr int SL = F8 && !MANY && D < 256 ? 32 : 16;  // positions a warp takes at once
+    static constexpr int TILE = MANY ? 64 : 4 * SL;        // positions of a tile
+    static constexpr int ROWS = MANY ? 64 * MT : 16 * MT;  // query rows of an item
+    static constexpr int TILE_B = TILE * ROWB;             // bytes of K (or V) of a tile
+    static constexpr int STAGE_B = 2 * TILE_B + (F8 ? 2 * TILE * 4 : 0);
+    static constexpr int Q_B = ROWS * D * 2 * (SPLITQ ? 2 : 1);
+    // two CTAs an SM, one where a row takes 512 bytes
+    static constexpr int BUDGET = (D == 256 && !F8) ? 226 * 1024 : 113 * 1024;
+    static constexpr int FIT = (BUDGET - Q_B - 4096) / STAGE_B;
+    static constexpr int STAGES = FIT > 4 ? 4 : FIT;
+    static constexpr int RING_B = STAGES * STAGE_B;
+    static constexpr int SMEM = RING_B + Q_B + 4096;
+    // the warps' outputs meet in the ring's memory (FEW)
+    static_assert(MANY || 4 * ROWS * D * 4 <= RING_B, "ring too small for the merge");
+    static_assert(STAGES >= 2, "ring");
+};
+
+// per-row facts and the page numbers of the tiles being fetched
+template <int ROWS, int TILE>
+struct Misc {
+    float slope2[ROWS];  // slope * log2 e
+    float qscale[ROWS];  // 8-bit pages: the power of two taken out of the query
+    int lo[ROWS], hi[ROWS], at[ROWS];
+    int page[2][TILE];
+    long long scan[AT / 32 + 2];
+    long long found_base;
+    int found_b;
+};
+
+template <int D, int FMT, bool SPLITQ, bool MANY, int MT>
+__global__ void __launch_bounds__(AT) attend_kernel(const __grid_constant__ AttendP p) {
+    using S = Shape<D, FMT, SPLITQ, MANY, MT>;
+    constexpr bool F8 = S::F8;
+    constexpr int ROWB = S::ROWB, TILE = S::TILE, SL = S::SL, ROWS = S::ROWS, NT = D / 8;
+    using M = Misc<ROWS, TILE>;
+    static_assert(sizeof(M) <= 4096, "misc area");
+    extern __shared__ __align__(128) uint8_t smem[];
+    const uint32_t ring = sm32(smem), qs = ring + S::RING_B;
+    uint8_t* const qmem = smem + S::RING_B;
+    M& ms = *reinterpret_cast<M*>(smem + S::RING_B + S::Q_B);
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+
+    // ---- this CTA's stretch of units
+    const int items = p.H * p.RB;  // items of one (virtual) sequence
+    const int nb = p.is_shared ? 1 : p.B;
+    long long total, my_first = 0;
+    {
+        // each thread counts a stretch of sequences; sums before it by shuffles
+        const int each = (nb + AT - 1) / AT, b0 = min(nb, tid * each), b1 = min(nb, b0 + each);
+        long long mine = 0;
+        for (int b = b0; b < b1; ++b) {
+            mine += (long long)cover_units<TILE>(p, b) * items;
+            if (p.status && !p.is_shared && blockIdx.x == 0 && p.lens[b] > (p.pps << p.ps_shift))
+                *p.status = MK_ERR_INVALID_ARG;
+        }
+        long long inc = mine;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const long long a = __shfl_up_sync(0xffffffffu, inc, o);
+            if (lane >= o) inc += a;
+        }
+        if (lane == 31) ms.scan[warp] = inc;
+        __syncthreads();
+        long long before = inc - mine;
+        total = 0;
+#pragma unroll
+        for (int w = 0; w < AT / 32; ++w) {
+            if (w < warp) before += ms.scan[w];
+            total += ms.scan[w];
+        }
+        if (blockIdx.x == 0 && !p.is_shared) {
+            long long at = before;
+            for (int b = b0; b < b1; ++b) {
+                p.base[b] = at;
+                at += (long long)cover_units<TILE>(p, b) * items;
+            }
+            if (tid == 0) p.base[p.B] = total;
+        }
+        const long long per = units_each(total, gridDim.x, p.min_units);
+        my_first = per * blockIdx.x;
+        if (my_first >= total) {
+            asm volatile("griddepcontrol.wait;" ::: "memory");
+            return;
+        }
+        if (my_first >= before && my_first < before + mine) {
+            long long at = before;
+            for (int b = b0; b < b1; ++b) {
+                const long long n = (long long)cover_units<TILE>(p, b) * items;
+                if (my_first < at + n) {
+                    ms.found_b = b;
+                    ms.found_base = at;
+                    break;
+                }
+                at += n;
+            }
+        }
+        __syncthreads();
+    }
+    int b = ms.found_b;
+    long long base_b = ms.found_base;
+    const long long per = units_each(total, gridDim.x, p.min_units);
+    const long long my_end = min(total, my_first + per);
+    const float scale2 = p.scale * LOG2E;
+
+    for (long long u = my_first; u < my_end;) {
+        // ---- the item: sequence b, kv head h, row block rb; its tiles [t0, t0 + take)
+        int n_b = cover_units<TILE>(p, b);
+        while (b < nb && u >= base_b + (long long)n_b * items) {
+            base_b += (long long)n_b * items;
+            n_b = ++b < nb ? cover_units<TILE>(p, b) : 0;
+        }
+        if (n_b == 0) break;  // only if the lengths changed under the launch
+        const int item = (int)((u - base_b) / n_b), off = (int)((u - base_b) % n_b);
+        const int h = item / p.RB, rb = item - h * p.RB;
+        const int take = (int)min((long long)(n_b - off), my_end - u);
+        int clo, chi;
+        cover(p, b, clo, chi);
+        const int t0 = clo / TILE + off;
+        const int row0 = (p.is_shared ? 0 : b * p.rows_item) + rb * ROWS;
+        const int nrows = min(ROWS, p.rows_item - rb * ROWS);
+        const long long u_first = u;
+        u += take;
+
+        __syncthreads();  // the previous item is done with every shared area
+        for (int r = tid; r < ROWS; r += AT) {
+            int lo = 0, hi = 0, at = 0;
+            float sl = 0.f;
+            if (r < nrows) {
+                const int bt = (row0 + r) / p.G, g = (row0 + r) - bt * p.G;
+                const int rbq = bt / p.T, t = bt - rbq * p.T;
+                const int len = p.lens[rbq];
+                at = len - p.T + t;
+                lo = max(p.starts ? p.starts[rbq] : 0, clo);
+                hi = min(min(at + 1, p.is_shared ? len : chi), chi);
+                if (p.slopes) sl = p.slopes[h * p.G + g] * LOG2E;
+            }
+            ms.lo[r] = lo;
+            ms.hi[r] = hi;
+            ms.at[r] = at;
+            ms.slope2[r] = sl;
+        }
+        // ---- queries into shared memory, a warp a row
+        for (int r = warp; r < ROWS; r += 4) {
+            constexpr int E = D / 32;  // consecutive values of a lane
+            float x[E];
+#pragma unroll
+            for (int i = 0; i < E; ++i) x[i] = 0.f;
+            if (r < nrows) {
+                const int bt = (row0 + r) / p.G, g = (row0 + r) - bt * p.G;
+                const int rbq = bt / p.T, t = bt - rbq * p.T;
+                const uint16_t* src = p.q + rbq * p.qb + t * p.qt + (h * p.G + g) * p.qh + lane * E;
+#pragma unroll
+                for (int i = 0; i < E; ++i)
+                    x[i] = p.f16 ? __half2float(__ushort_as_half(src[i])) : bf2f(src[i]);
+            }
+            if constexpr (F8) {
+                float a = 0.f;
+#pragma unroll
+                for (int i = 0; i < E; ++i) a = fmaxf(a, fabsf(x[i]));
+#pragma unroll
+                for (int o = 16; o; o >>= 1) a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, o));
+                // 2^e <= a < 2^(e+1); a row of zeros, infinities or NaN is left as it is
+                const unsigned ex = __float_as_uint(a) >> 23;
+                const unsigned e = ex == 0 || ex == 255 ? 127u : min(ex, 253u);
+                if (lane == 0) ms.qscale[r] = __uint_as_float(e << 23);
+                const float inv = __uint_as_float((254u - e) << 23);
+#pragma unroll
+                for (int i = 0; i < E; ++i) x[i] *= inv;
+            }
+#pragma unroll
+            for (int i = 0; i < E; i += 2) {
+                const int d = lane * E + i;
+                // 8-bit pages: a lane's four consecutive codes feed slots
+                // {2l, 2l+1, 2l+8, 2l+9} of a 16-wide product step
+                const int c = F8 ? (d & ~15) + ((d >> 1) & 1) * 8 + ((d >> 2) & 3) * 2 : d;
+                uint8_t* dst = qmem + r * (D * 2) + ((((c >> 3) ^ (r & 7))) << 4) + (c & 7) * 2;
+                if constexpr (F8) {
+                    *reinterpret_cast<uint32_t*>(dst) = pack_f16(x[i], x[i + 1]);
+                } else {
+                    const uint32_t hi = pack_bf16(x[i], x[i + 1]);
+                    *reinterpret_cast<uint32_t*>(dst) = hi;
+                    if constexpr (SPLITQ)
+                        *reinterpret_cast<uint32_t*>(dst + ROWS * D * 2) =
+                            pack_bf16(x[i] - bf2f(hi & 0xffffu), x[i + 1] - bf2f(hi >> 16));
+                }
+            }
+        }
+
+        // ---- fetching: page numbers one tile ahead of the copies
+        const uint8_t* const kh = p.k + h * p.head_b;
+        const uint8_t* const vh = p.v + h * p.head_b;
+        const int* const trow = p.table + (p.is_shared ? 0 : b) * p.table_s;
+        auto page_of = [&](int tile, int i) {  // -1: not this item's, or no such page
+            const int pos = (t0 + tile) * TILE + i;
+            if (tile >= take || pos < clo || pos >= chi) return -1;
+            const int pg = trow[pos >> p.ps_shift];
+            if ((unsigned)pg < (unsigned)p.n_pages) return pg;
+            if (p.status) *p.status = MK_ERR_INVALID_ARG;
+            return -1;
+        };
+        auto fetch = [&](int tile) {
+            if (tile < take) {
+                const uint32_t st = ring + (tile % S::STAGES) * S::STAGE_B;
+                constexpr int CH = ROWB / 16;  // pieces of a row
+                const int* pg = ms.page[tile & 1];
+                const int mask = (1 << p.ps_shift) - 1;
+#pragma unroll
+                for (int i = tid; i < TILE * CH; i += AT) {
+                    const int r = i / CH, c = i % CH;
+                    const int page = pg[r];
+                    const bool ok = page >= 0;
+                    const long long o = ok ? page * p.page_b + (((t0 + tile) * TILE + r) & mask) * p.row_b + c * 16 : 0;
+                    cp16(piece<ROWB>(st, r, c), kh + o, ok);
+                    cp16(piece<ROWB>(st + S::TILE_B, r, c), vh + o, ok);
+                }
+                if constexpr (F8) {
+                    for (int r = tid; r < TILE; r += AT) {
+                        const int page = pg[r];
+                        const bool ok = page >= 0;
+                        const long long o =
+                            ok ? page * p.sc_page + h * p.sc_head + (((t0 + tile) * TILE + r) & mask) : 0;
+                        cp4(st + 2 * S::TILE_B + r * 4, p.ks + o, ok);
+                        cp4(st + 2 * S::TILE_B + (TILE + r) * 4, p.vs + o, ok);
+                    }
+                }
+            }
+            cp_commit();
+        };
+        for (int t = 0; t < S::STAGES - 1; ++t) {
+            if (tid < TILE) ms.page[t & 1][tid] = page_of(t, tid);
+            __syncthreads();
+            fetch(t);
+            // the buffer is rewritten two tiles later, past the next barrier
+        }
+        if (tid < TILE) ms.page[(S::STAGES - 1) & 1][tid] = page_of(S::STAGES - 1, tid);
+
+        // ---- the warp's rows
+        const int wrow = MANY ? warp * 16 * MT : 0;
+        // the range every row sees, and the range some row sees (rows that see something)
+        int lo_max = 0, lo_min = INT_MAX, hi_min = INT_MAX, hi_max = 0;
+        for (int i = lane; i < 16 * MT; i += 32) {
+            const int lo = ms.lo[wrow + i], hi = ms.hi[wrow + i];
+            if (wrow + i < nrows && lo < hi) {
+                lo_max = max(lo_max, lo), lo_min = min(lo_min, lo);
+                hi_min = min(hi_min, hi), hi_max = max(hi_max, hi);
+            }
+        }
+#pragma unroll
+        for (int o = 16; o; o >>= 1) {
+            lo_max = max(lo_max, __shfl_xor_sync(0xffffffffu, lo_max, o));
+            lo_min = min(lo_min, __shfl_xor_sync(0xffffffffu, lo_min, o));
+            hi_min = min(hi_min, __shfl_xor_sync(0xffffffffu, hi_min, o));
+            hi_max = max(hi_max, __shfl_xor_sync(0xffffffffu, hi_max, o));
+        }
+
+        float o[MT][NT][4], m[MT][2], l[MT][2];
+        float vunit = 0.f;  // 8-bit pages: outputs are in units of this power of two / 2^15
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt) {
+#pragma unroll
+            for (int i = 0; i < NT; ++i)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) o[mt][i][e] = 0.f;
+            m[mt][0] = m[mt][1] = -INFINITY;
+            l[mt][0] = l[mt][1] = 0.f;
+        }
+
+        for (int tile = 0; tile < take; ++tile) {
+            cp_wait<S::STAGES - 2>();
+            __syncthreads();
+            fetch(tile + S::STAGES - 1);
+            int next_page = -1;
+            if (tid < TILE) next_page = page_of(tile + S::STAGES, tid);
+
+            const uint32_t st = ring + (tile % S::STAGES) * S::STAGE_B;
+#pragma unroll 1
+            for (int s0 = MANY ? 0 : warp * SL; s0 < (MANY ? TILE : warp * SL + SL); s0 += SL) {
+                const int j0 = (t0 + tile) * TILE + s0;
+                if (j0 + SL <= lo_min || j0 >= hi_max) continue;  // no row sees any of it
+                const bool all_see = j0 >= lo_max && j0 + SL <= hi_min;
+                float x[MT][SL / 8][4];
+#pragma unroll
+                for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+                    for (int i = 0; i < SL / 8; ++i)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) x[mt][i][e] = 0.f;
+
+                // ---- scores
+                auto q_frag = [&](uint32_t(&a)[4], int mt, int step, int part) {
+                    const int r = wrow + mt * 16 + (lane & 15), c = step * 2 + (lane >> 4);
+                    ldsm4(a, qs + part * (ROWS * D * 2) + r * (D * 2) + ((c ^ (r & 7)) << 4));
+                };
+                if constexpr (!F8) {
+#pragma unroll
+                    for (int step = 0; step < D / 16; ++step) {
+                        uint32_t a[MT][4], al[MT][4];
+#pragma unroll
+                        for (int mt = 0; mt < MT; ++mt) {
+                            q_frag(a[mt], mt, step, 0);
+                            if constexpr (SPLITQ) q_frag(al[mt], mt, step, 1);
+                        }
+#pragma unroll
+                        for (int s = 0; s < SL / 16; ++s) {
+                            uint32_t kb[4];
+                            ldsm4(kb, piece<ROWB>(st, s0 + s * 16 + (lane >> 4) * 8 + (lane & 7),
+                                                  step * 2 + ((lane >> 3) & 1)));
+#pragma unroll
+                            for (int mt = 0; mt < MT; ++mt) {
+                                mma<false>(x[mt][2 * s], a[mt], kb[0], kb[1]);
+                                mma<false>(x[mt][2 * s + 1], a[mt], kb[2], kb[3]);
+                                if constexpr (SPLITQ) {
+                                    mma<false>(x[mt][2 * s], al[mt], kb[0], kb[1]);
+                                    mma<false>(x[mt][2 * s + 1], al[mt], kb[2], kb[3]);
+                                }
+                            }
+                        }
+                    }
+                } else {
+#pragma unroll
+                    for (int step = 0; step < D / 16; step += 2) {
+                        uint32_t a[MT][2][4];
+#pragma unroll
+                        for (int mt = 0; mt < MT; ++mt) {
+                            q_frag(a[mt][0], mt, step, 0);
+                            q_frag(a[mt][1], mt, step + 1, 0);
+                        }
+#pragma unroll
+                        for (int s = 0; s < SL / 16; ++s) {
+                            uint32_t kb[4];  // positions 0-7: pieces step, step+1; positions 8-15: the same
+                            ldsm4(kb, piece<ROWB>(st, s0 + s * 16 + (lane >> 4) * 8 + (lane & 7),
+                                                  step + ((lane >> 3) & 1)));
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) {
+                                uint32_t b0, b1;
+                                if constexpr (FMT == MK_KV_E4M3) {
+                                    b0 = e4m3_pair<FMT>(kb[i] & 0xffffu);
+                                    b1 = e4m3_pair<FMT>(kb[i] >> 16);
+                                } else {
+                                    const uint32_t w = kb[i] ^ 0x80808080u;
+                                    b0 = int8_half2(__byte_perm(w, 0x64646464u, 0x4140));
+                                    b1 = int8_half2(__byte_perm(w, 0x64646464u, 0x4342));
+                                }
+#pragma unroll
+                                for (int mt = 0; mt < MT; ++mt) mma<true>(x[mt][2 * s + (i >> 1)], a[mt][i & 1], b0, b1);
+                            }
+                        }
+                    }
+                }
+
+                // ---- 8-bit pages: scales of this thread's columns
+                float vsc[SL / 8][2];
+                float grow = 1.f;
+                if constexpr (F8) {
+                    const float* ksm = reinterpret_cast<const float*>(
+                        smem + (tile % S::STAGES) * S::STAGE_B + 2 * S::TILE_B);
+                    float big = 0.f;
+#pragma unroll
+                    for (int i = 0; i < SL / 8; ++i) {
+                        const int c = s0 + i * 8 + (lane & 3) * 2;
+                        const float2 kk = *reinterpret_cast<const float2*>(ksm + c);
+                        const float2 vv = *reinterpret_cast<const float2*>(ksm + TILE + c);
+#pragma unroll
+                        for (int mt = 0; mt < MT; ++mt) {
+                            x[mt][i][0] *= kk.x, x[mt][i][1] *= kk.y;
+                            x[mt][i][2] *= kk.x, x[mt][i][3] *= kk.y;
+                        }
+                        vsc[i][0] = vv.x, vsc[i][1] = vv.y;
+                        big = fmaxf(big, fmaxf(vv.x, vv.y));
+                    }
+                    big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 1));
+                    big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 2));
+                    if (big > vunit) {  // the same in all lanes: every row has the same columns
+                        // above `big`, and far enough from 0 for 2^15 over it
+                        const unsigned e = min((__float_as_uint(big) >> 23) + 1, 250u);
+                        const float nu = __uint_as_float(max(e, 27u) << 23);
+                        grow = vunit / nu;
+                        vunit = nu;
+                    }
+                    const float inv = vunit > 0.f ? 32768.f / vunit : 0.f;
+#pragma unroll
+                    for (int i = 0; i < SL / 8; ++i) vsc[i][0] *= inv, vsc[i][1] *= inv;
+                }
+
+                // ---- softmax: x becomes the probabilities
+                uint32_t seen[MT];  // bit (i*4+e): the value is visible to its row (used where some are not)
+#pragma unroll
+                for (int mt = 0; mt < MT; ++mt) {
+                    seen[mt] = 0xffffffffu;
+#pragma unroll
+                    for (int hf = 0; hf < 2; ++hf) {
+                        const int r = wrow + mt * 16 + (lane >> 2) + hf * 8;
+                        const float qsc = F8 ? ms.qscale[r] : 1.f;
+                        float top = -INFINITY;
+                        if (p.cap > 0.f || p.slopes) {
+                            const float sl2 = ms.slope2[r];
+                            const int at = ms.at[r];
+#pragma unroll
+                            for (int i = 0; i < SL / 8; ++i)
+#pragma unroll
+                                for (int e = 0; e < 2; ++e) {
+                                    float y = x[mt][i][hf * 2 + e] * qsc * p.scale;
+                                    if (p.cap > 0.f) {
+                                        // tanh z = 1 - 2 / (e^2z + 1): the error stays near 2^-23 of 1
+                                        const float z = y / p.cap;
+                                        const float t = 1.f - __fdividef(2.f, ex2(fminf(2.f * LOG2E * z, 80.f)) + 1.f);
+                                        y = p.cap * (y != y ? y : t);
+                                    }
+                                    const int j = j0 + i * 8 + (lane & 3) * 2 + e;
+                                    x[mt][i][hf * 2 + e] = y * LOG2E - sl2 * (float)(at - j);
+                                }
+                        } else {
+                            const float f = qsc * scale2;
+#pragma unroll
+                            for (int i = 0; i < SL / 8; ++i) {
+                                x[mt][i][hf * 2] *= f;
+                                x[mt][i][hf * 2 + 1] *= f;
+                            }
+                        }
+                        if (!all_see) {
+                            const int lo = ms.lo[r], hi = ms.hi[r];
+#pragma unroll
+                            for (int i = 0; i < SL / 8; ++i)
+#pragma unroll
+                                for (int e = 0; e < 2; ++e) {
+                                    const int j = j0 + i * 8 + (lane & 3) * 2 + e;
+                                    if (j < lo || j >= hi) {
+                                        x[mt][i][hf * 2 + e] = -INFINITY;
+                                        seen[mt] &= ~(1u << (i * 4 + hf * 2 + e));
+                                    }
+                                }
+                        }
+#pragma unroll
+                        for (int i = 0; i < SL / 8; ++i) top = fmaxf(top, fmaxf(x[mt][i][hf * 2], x[mt][i][hf * 2 + 1]));
+                        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+                        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+                        const float mn = fmaxf(m[mt][hf], top);
+                        const float ref = mn == -INFINITY ? 0.f : mn;
+                        const float keep = ex2(m[mt][hf] - ref);
+                        m[mt][hf] = mn;
+                        float sum = 0.f;
+#pragma unroll
+                        for (int i = 0; i < SL / 8; ++i)
+#pragma unroll
+                            for (int e = 0; e < 2; ++e) {
+                                const float pr = ex2(x[mt][i][hf * 2 + e] - ref);
+                                sum += pr;
+                                if constexpr (F8)  // a masked row's scale may be anything
+                                    x[mt][i][hf * 2 + e] =
+                                        seen[mt] >> (i * 4 + hf * 2 + e) & 1u ? pr * vsc[i][e] : 0.f;
+                                else
+                                    x[mt][i][hf * 2 + e] = pr;
+                            }
+                        l[mt][hf] = l[mt][hf] * keep + sum;
+                        const float f = F8 ? keep * grow : keep;
+                        if (__any_sync(0xffffffffu, f != 1.f)) {
+#pragma unroll
+                            for (int i = 0; i < NT; ++i) {
+                                o[mt][i][hf * 2] *= f;
+                                o[mt][i][hf * 2 + 1] *= f;
+                            }
+                        }
+                    }
+                }
+
+                // ---- values some row does not see must not reach it, and 0 x NaN would: look for
+                // non-finite ones where rows see different parts
+                const uint32_t vt = st + S::TILE_B;
+                bool odd = false;
+                if (!all_see && FMT != MK_KV_INT8) {
+                    for (int i = lane; i < SL * (ROWB / 16); i += 32) {
+                        uint32_t w[4];
+                        asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
+                                     : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
+                                     : "r"(vt + (s0 * ROWB) + i * 16));
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            if constexpr (FMT == MK_KV_BF16) {
+                                odd |= (w[e] & 0x7f80u) == 0x7f80u || (w[e] & 0x7f800000u) == 0x7f800000u;
+                            } else {
+                                // a code is NaN when its low seven bits are all set
+                                odd |= (((w[e] & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u) != 0;
+                            }
+                        }
+                    }
+                    odd = __any_sync(0xffffffffu, odd);
+                }
+                if (odd) {
+                    // such values go to the rows that see them one by one; below they count as zeros
+                    for (int j = 0; j < SL; ++j) {
+#pragma unroll
+                        for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+                            for (int hf = 0; hf < 2; ++hf) {
+                                float pv = 0.f;
+                                unsigned vis = 0;
+#pragma unroll
+                                for (int i = 0; i < SL / 8; ++i)
+#pragma unroll
+                                    for (int e = 0; e < 2; ++e)
+                                        if (i * 8 + e == (j & ~6)) {
+                                            pv = x[mt][i][hf * 2 + e];
+                                            vis = seen[mt] >> (i * 4 + hf * 2 + e) & 1u;
+                                        }
+                                const int from = (lane & ~3) | ((j & 7) >> 1);
+                                pv = __shfl_sync(0xffffffffu, pv, from);
+                                vis = __shfl_sync(0xffffffffu, vis, from);
+                                if (!vis) continue;
+#pragma unroll
+                                for (int i = 0; i < NT; ++i)
+#pragma unroll
+                                    for (int e = 0; e < 2; ++e) {
+                                        const int d = F8 ? (i >> 1) * 16 + (lane & 3) * 4 + 2 * e + (i & 1)
+                                                         : i * 8 + (lane & 3) * 2 + e;
+                                        const uint32_t a = piece<ROWB>(vt, s0 + j, d * S::EB / 16) + (d * S::EB & 15);
+                                        if constexpr (F8) {
+                                            uint32_t c;
+                                            asm volatile("ld.shared.u8 %0, [%1];" : "=r"(c) : "r"(a));
+                                            if ((c & 0x7fu) == 0x7fu) o[mt][i][hf * 2 + e] = __uint_as_float(0x7fffffffu);
+                                        } else {
+                                            uint16_t c;
+                                            asm volatile("ld.shared.u16 %0, [%1];" : "=h"(c) : "r"(a));
+                                            if ((c & 0x7f80u) == 0x7f80u) o[mt][i][hf * 2 + e] += pv * bf2f(c);
+                                        }
+                                    }
+                            }
+                    }
+                }
+
+                // ---- outputs
+#pragma unroll
+                for (int s = 0; s < SL / 16; ++s) {
+                    uint32_t a[MT][4], al[MT][4];
+#pragma unroll
+                    for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const float y0 = x[mt][2 * s + (i >> 1)][(i & 1) * 2];
+                            const float y1 = x[mt][2 * s + (i >> 1)][(i & 1) * 2 + 1];
+                            if constexpr (F8) {
+                                a[mt][i] = pack_f16(y0, y1);
+                            } else {
+                                a[mt][i] = pack_bf16(y0, y1);
+                                al[mt][i] = pack_bf16(y0 - bf2f(a[mt][i] & 0xffffu), y1 - bf2f(a[mt][i] >> 16));
+                            }
+                        }
+                    if constexpr (!F8) {
+#pragma unroll
+                        for (int dt = 0; dt < D / 16; ++dt) {
+                            uint32_t vb[4];
+                            ldsm4t(vb, piece<ROWB>(vt, s0 + s * 16 + (lane & 15), dt * 2 + (lane >> 4)));
+                            if (odd) {
+#pragma unroll
+                                for (int i = 0; i < 4; ++i) {
+                                    if ((vb[i] & 0x7f80u) == 0x7f80u) vb[i] &= 0xffff0000u;
+                                    if ((vb[i] & 0x7f800000u) == 0x7f800000u) vb[i] &= 0xffffu;
+                                }
+                            }
+#pragma unroll
+                            for (int mt = 0; mt < MT; ++mt) {
+                                mma<false>(o[mt][2 * dt], a[mt], vb[0], vb[1]);
+                                mma<false>(o[mt][2 * dt + 1], a[mt], vb[2], vb[3]);
+                                mma<false>(o[mt][2 * dt], al[mt], vb[0], vb[1]);
+                                mma<false>(o[mt][2 * dt + 1], al[mt], vb[2], vb[3]);
+                            }
+                        }
+                    } else {
+#pragma unroll
+                        for (int dt = 0; dt < D / 16; dt += 2) {
+                            // transposing byte pairs: a register holds values 2n, 2n+1 of two
+                            // positions; the even ones are one product's columns, the odd ones another's
+                            uint32_t vb[4];
+                            ldsm4t(vb, piece<ROWB>(vt, s0 + s * 16 + (lane & 15), dt + (lane >> 4)));
+#pragma unroll
+                            for (int c = 0; c < 2; ++c) {
+                                uint32_t be[2], bo[2];
+#pragma unroll
+                                for (int i = 0; i < 2; ++i) {
+                                    uint32_t w = vb[2 * c + i];
+                                    if constexpr (FMT == MK_KV_E4M3) {
+                                        if (odd) {
+                                            // NaN codes to zero
+                                            const uint32_t f = ((w & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u;
+                                            w &= ~((f >> 7) * 0xffu);
+                                        }
+                                        w = __byte_perm(w, 0, 0x3120);
+                                        be[i] = e4m3_pair<FMT>(w & 0xffffu);
+                                        bo[i] = e4m3_pair<FMT>(w >> 16);
+                                    } else {
+                                        w ^= 0x80808080u;
+                                        be[i] = int8_half2(__byte_perm(w, 0x64646464u, 0x4240));
+                                        bo[i] = int8_half2(__byte_perm(w, 0x64646464u, 0x4341));
+                                    }
+                                }
+#pragma unroll
+                                for (int mt = 0; mt < MT; ++mt) {
+                                    mma<true>(o[mt][2 * (dt + c)], a[mt], be[0], be[1]);
+                                    mma<true>(o[mt][2 * (dt + c) + 1], a[mt], bo[0], bo[1]);
+                                }
+                            }
+                        }
+                    }
+                }
+            }
+            if (tid < TILE) ms.page[(tile + S::STAGES) & 1][tid] = next_page;
+        }
+
+        // ---- the item's (or piece's) result
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+            for (int hf = 0; hf < 2; ++hf) {
+                l[mt][hf] += __shfl_xor_sync(0xffffffffu, l[mt][hf], 1);
+                l[mt][hf] += __shfl_xor_sync(0xffffffffu, l[mt][hf], 2);
+                if constexpr (F8) {
+                    const float f = vunit * (1.f / 32768.f);
+#pragma unroll
+                    for (int i = 0; i < NT; ++i) {
+                        o[mt][i][hf * 2] *= f;
+                        o[mt][i][hf * 2 + 1] *= f;
+                    }
+                }
+            }
+        const bool whole = take == n_b;
+        float* slot = nullptr;
+        if (whole && p.keep_items)
+            slot = p.slots + (2ll * gridDim.x + (long long)b * items + item) * p.slot_floats;
+        else if (!whole)
+            slot = p.slots + (2ll * blockIdx.x + (u_first == my_first ? 0 : 1)) * p.slot_floats;
+        // (m, l) of slot row r at slot + slot_rows * D + 2 r
+        auto put = [&](int r, int d, float y0, float y1, float y2, float y3, float mm, float ll, bool first) {
+            // four values of row r from column d on. A row that sees nothing was
+            // not masked where all others see everything: it is dropped here.
+            if (ms.lo[r] >= ms.hi[r]) mm = -INFINITY, ll = 0.f;
+            if (slot) {
+                *reinterpret_cast<float4*>(slot + (long long)r * D + d) = make_float4(y0, y1, y2, y3);
+                if (first) *reinterpret_cast<float2*>(slot + (long long)p.slot_rows * D + 2 * r) = make_float2(mm, ll);
+                return;
+            }
+            const int bt = (row0 + r) / p.G, g = (row0 + r) - bt * p.G;
+            const int rbq = bt / p.T, t = bt - rbq * p.T, hq = h * p.G + g;
+            const bool none = ll == 0.f;
+            const float inv = none ? 0.f : 1.f / ll;
+            const float z[4] = {none ? 0.f : y0 * inv, none ? 0.f : y1 * inv, none ? 0.f : y2 * inv,
+                                none ? 0.f : y3 * inv};
+            uint16_t* dst = p.out + rbq * p.ob + t * p.ot + hq * p.oh + d;
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                dst[i] = p.f16 ? __half_as_ushort(__float2half_rn(z[i])) : __bfloat16_as_ushort(__float2bfloat16_rn(z[i]));
+            if (first && p.lse)
+                p.lse[((long long)rbq * p.T + t) * (p.H * p.G) + hq] = none ? -INFINITY : (mm + log2f(ll)) * LN2;
+        };
+        cp_wait<0>();
+        __syncthreads();  // the ring is free
+        {
+            // Outputs pass through shared memory: rows by row, four columns a
+            // thread. FEW: four warps' parts of the same rows are joined on the way.
+            constexpr int PARTS = MANY ? 1 : 4;
+            constexpr int RW = 16 * MT;  // rows of a warp
+            float* om = reinterpret_cast<float*>(smem);
+            if constexpr (!MANY) {
+                float* oml = reinterpret_cast<float*>(qmem);  // the queries are done with
+#pragma unroll
+                for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+                    for (int hf = 0; hf < 2; ++hf) {
+                        const int r = mt * 16 + (lane >> 2) + hf * 8;
+                        float* dst = om + (warp * RW + r) * D;
+#pragma unroll
+                        for (int i = 0; i < NT; ++i)
+#pragma unroll
+                            for (int e = 0; e < 2; ++e) {
+                                const int d = F8 ? (i >> 1) * 16 + (lane & 3) * 4 + 2 * e + (i & 1)
+                                                 : i * 8 + (lane & 3) * 2 + e;
+                                dst[d] = o[mt][i][hf * 2 + e];
+                            }
+                        if ((lane & 3) == 0) {
+                            oml[(warp * RW + r) * 2] = m[mt][hf];
+                            oml[(warp * RW + r) * 2 + 1] = l[mt][hf];
+                        }
+                    }
+                __syncthreads();
+                for (int i = tid; i < nrows * (D / 4); i += AT) {
+                    const int r = i / (D / 4), d = (i % (D / 4)) * 4;
+                    float mm = -INFINITY, ll = 0.f;
+#pragma unroll
+                    for (int w = 0; w < 4; ++w) mm = fmaxf(mm, oml[(w * RW + r) * 2]);
+                    const float ref = mm == -INFINITY ? 0.f : mm;
+                    float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+                    for (int w = 0; w < 4; ++w) {
+                        const float f = ex2(oml[(w * RW + r) * 2] - ref);
+                        ll += oml[(w * RW + r) * 2 + 1] * f;
+                        const float4 z = *reinterpret_cast<const float4*>(om + (w * RW + r) * D + d);
+                        y.x += z.x * f, y.y += z.y * f, y.z += z.z * f, y.w += z.w * f;
+                    }
+                    put(r, d, y.x, y.y, y.z, y.w, mm, ll, d == 0);
+                }
+            } else {
+                // each warp owns its rows: straight from registers
+#pragma unroll
+                for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+                    for (int hf = 0; hf < 2; ++hf) {
+                        const int r = wrow + mt * 16 + (lane >> 2) + hf * 8;
+                        const bool ok = r < nrows;
+                        // a quad's values of 16 columns, regrouped so that each lane has four in a row
+#pragma unroll
+                        for (int dt = 0; dt < D / 16; ++dt) {
+                            float y[4];
+                            if constexpr (F8) {
+                                y[0] = o[mt][2 * dt][hf * 2], y[1] = o[mt][2 * dt + 1][hf * 2];
+                                y[2] = o[mt][2 * dt][hf * 2 + 1], y[3] = o[mt][2 * dt + 1][hf * 2 + 1];
+                            } else {
+                                // lanes 0,1 of a quad take columns 0-7 of the 16, lanes 2,3 columns 8-15
+                                const float a0 = o[mt][2 * dt][hf * 2], a1 = o[mt][2 * dt][hf * 2 + 1];
+                                const float b0 = o[mt][2 * dt + 1][hf * 2], b1 = o[mt][2 * dt + 1][hf * 2 + 1];
+                                const int q4 = lane & 3, src = (lane & ~3) | ((q4 & 1) * 2);
+                                const float a0l = __shfl_sync(0xffffffffu, a0, src), a1l = __shfl_sync(0xffffffffu, a1, src);
+                                const float a0h = __shfl_sync(0xffffffffu, a0, src + 1), a1h = __shfl_sync(0xffffffffu, a1, src + 1);
+                                const float b0l = __shfl_sync(0xffffffffu, b0, src), b1l = __shfl_sync(0xffffffffu, b1, src);
+                                const float b0h = __shfl_sync(0xffffffffu, b0, src + 1), b1h = __shfl_sync(0xffffffffu, b1, src + 1);
+                                const bool second = q4 >= 2;
+                                y[0] = second ? b0l : a0l, y[1] = second ? b1l : a1l;
+                                y[2] = second ? b0h : a0h, y[3] = second ? b1h : a1h;
+                            }
+                            const int d = dt * 16 + (lane & 3) * 4;
+                            if (ok) put(r, d, y[0], y[1], y[2], y[3], m[mt][hf], l[mt][hf], d == 0);
+                        }
+                    }
+            }
+        }
+    }
+    // This launch may have begun before the shared one ended; the joining
+    // launch waits for this one alone, so this one ends after the shared one.
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+
+// Joins the pieces of one output row: a block a row, a warp every fourth
+// piece. Rows whose only piece went straight to the output are left alone;
+// rows without any piece get their zeros here. Reads the pieces from L2: a few
+// microseconds of latency.
+template <int D>
+__global__ void __launch_bounds__(AT) join_kernel(const __grid_constant__ JoinP jp) {
+    constexpr int E = D / 32;
+    __shared__ float om[4][D];
+    __shared__ float2 oml[4];
+    const AttendP& p = jp.own;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, Hq = p.H * p.G;
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const int bt = blockIdx.x / Hq, hq = blockIdx.x - bt * Hq;
+    const int b = bt / p.T, t = bt - b * p.T, h = hq / p.G, g = hq - h * p.G;
+
+    // pieces of a launch: CTAs c0 .. c1, the row's place in a slot
+    struct Part {
+        const float* slots;
+        long long c0, c1, per, first, whole_slot;
+        int row, rows, floats, n;
+    };
+    auto part = [&](const AttendP& a, int grid, int rows_blk, long long base, long long total, int n_b, int vb, int r) {
+        Part x;
+        const int rb = r / rows_blk, item = h * a.RB + rb;
+        x.n = n_b;
+        x.per = units_each(total, grid, a.min_units);
+        x.first = base + (long long)item * n_b;
+        x.c0 = x.first / x.per;
+        x.c1 = n_b ? (x.first + n_b - 1) / x.per : x.c0 - 1;
+        x.whole_slot = 2ll * grid + (long long)vb * a.H * a.RB + item;
+        x.row = r - rb * rows_blk;
+        x.rows = a.slot_rows;
+        x.floats = a.slot_floats;
+        x.slots = a.slots;
+        return x;
+    };
+    const int items = p.H * p.RB;
+    const long long base = p.base[b];
+    const Part own = part(p, jp.own_grid, jp.own_rows, base, p.base[p.B], (int)((p.base[b + 1] - base) / items), b,
+                          t * p.G + g);
+    const bool with_shared = jp.shared_grid > 0;
+    if (own.n && own.c0 == own.c1 && !p.keep_items) return;
+
+    float m = -INFINITY, l = 0.f, o[E];
+#pragma unroll
+    for (int i = 0; i < E; ++i) o[i] = 0.f;
+    auto add = [&](const Part& x) {
+#pragma unroll 4
+        for (long long c = x.c0 + warp; c <= x.c1; c += 4) {
+            const long long slot = x.c0 == x.c1 ? x.whole_slot : 2 * c + (x.first <= c * x.per ? 0 : 1);
+            const float* s = x.slots + slot * x.floats;
+            const float2 ml = *reinterpret_cast<const float2*>(s + (long long)x.rows * D + 2 * x.row);
+            float y[E];
+            const float* src = s + (long long)x.row * D + lane * E;
+#pragma unroll
+            for (int i = 0; i < E; i += 2) {
+                const float2 z = *reinterpret_cast<const float2*>(src + i);
+                y[i] = z.x, y[i + 1] = z.y;
+            }
+            const float mn = fmaxf(m, ml.x), ref = mn == -INFINITY ? 0.f : mn;
+            const float f = ex2(m - ref), e = ex2(ml.x - ref);
+            m = mn;
+            l = l * f + ml.y * e;
+            // a piece in which the row saw nothing adds nothing
+#pragma unroll
+            for (int i = 0; i < E; ++i) o[i] = o[i] * f + (ml.x == -INFINITY ? 0.f : y[i] * e);
+        }
+    };
+    if (own.n) add(own);
+    if (with_shared) {
+        const AttendP& a = jp.shared;
+        add(part(a, jp.shared_grid, jp.shared_rows, 0, (long long)jp.shared_units * a.H * a.RB, jp.shared_units, 0,
+                 bt * p.G + g));
+    }
+#pragma unroll
+    for (int i = 0; i < E; ++i) om[warp][lane * E + i] = o[i];
+    if (lane == 0) oml[warp] = make_float2(m, l);
+    __syncthreads();
+    float mm = -INFINITY, ll = 0.f, w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) mm = fmaxf(mm, oml[i].x);
+    const float ref = mm == -INFINITY ? 0.f : mm;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        w[i] = ex2(oml[i].x - ref);
+        ll += oml[i].y * w[i];
+    }
+    const bool none = ll == 0.f;
+    uint16_t* dst = p.out + b * p.ob + t * p.ot + hq * p.oh;
+    for (int d = threadIdx.x; d < D; d += AT) {
+        const float y = om[0][d] * w[0] + om[1][d] * w[1] + om[2][d] * w[2] + om[3][d] * w[3];
+        const float z = none ? 0.f : y / ll;
+        dst[d] = p.f16 ? __half_as_ushort(__float2half_rn(z)) : __bfloat16_as_ushort(__float2bfloat16_rn(z));
+    }
+    if (threadIdx.x == 0 && p.lse)
+        p.lse[((long long)b * p.T + t) * Hq + hq] = none ? -INFINITY : (mm + log2f(ll)) * LN2;
+}
+
+// Which kernel a call takes: format, whether queries need a lo part, rows.
+struct Kind {
+    int format;
+    bool splitq, many;
+    int mt;
+};
+struct KindInfo {
+    int tile, rows, ctas;  // positions of a tile, rows of an item, CTAs an SM
+};
+
+// A kernel by its template arguments, with what the host has to know of it.
+template <int D, int FMT, bool SPLITQ, bool MANY, int MT>
+int attend_run(const AttendP* p, KindInfo* info, int grid, bool after, cudaStream_t s) {
+    using S = Shape<D, FMT, SPLITQ, MANY, MT>;
+    auto kern = attend_kernel<D, FMT, SPLITQ, MANY, MT>;
+    if (info) {
+        info->tile = S::TILE;
+        info->rows = S::ROWS;
+        cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, S::SMEM);
+        if (e == cudaSuccess) e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&info->ctas, kern, AT, S::SMEM);
+        return cuda_status(e, "mk_pages_attend");
+    }
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)grid);
+    cfg.blockDim = dim3(AT);
+    cfg.dynamicSmemBytes = S::SMEM;
+    cfg.stream = s;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = after ? 1 : 0;
+    return cuda_status(cudaLaunchKernelEx(&cfg, kern, *p), "mk_pages_attend");
+}
+
+template <int D, int FMT, bool SPLITQ>
+int attend_pick(const Kind& k, const AttendP* p, KindInfo* info, int grid, bool after, cudaStream_t s) {
+    if (k.many) return attend_run<D, FMT, SPLITQ, true, 1>(p, info, grid, after, s);
+    if constexpr (D <= 128) {
+        if (k.mt == 2) return attend_run<D, FMT, SPLITQ, false, 2>(p, info, grid, after, s);
+    }
+    return attend_run<D, FMT, SPLITQ, false, 1>(p, info, grid, after, s);
+}
+
+// With `info`: what the host has to know of the kernel (and its one-time
+// attributes on the current device); else the launch, which may begin before
+// the previous one of the stream ends when `after` is set.
+template <int D>
+int attend_d(const Kind& k, const AttendP* p, KindInfo* info, int grid, bool after, cudaStream_t s) {
+    if (k.format == MK_KV_E4M3) return attend_pick<D, MK_KV_E4M3, false>(k, p, info, grid, after, s);
+    if (k.format == MK_KV_INT8) return attend_pick<D, MK_KV_INT8, false>(k, p, info, grid, after, s);
+    if (k.splitq) return attend_pick<D, MK_KV_BF16, true>(k, p, info, grid, after, s);
+    return attend_pick<D, MK_KV_BF16, false>(k, p, info, grid, after, s);
+}
+template <int D>
+int join_d(const JoinP& j, unsigned rows, cudaStream_t s) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(rows);
+    cfg.blockDim = dim3(AT);
+    cfg.stream = s;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    return cuda_status(cudaLaunchKernelEx(&cfg, join_kernel<D>, j), "mk_pages_attend");
+}
+
+// one translation unit a head_dim
+typedef int (*AttendFn)(const Kind&, const AttendP*, KindInfo*, int, bool, cudaStream_t);
+int attend_64(const Kind&, const AttendP*, KindInfo*, int, bool, cudaStream_t);
+int attend_128(const Kind&, const AttendP*, KindInfo*, int, bool, cudaStream_t);
+int attend_256(const Kind&, const AttendP*, KindInfo*, int, bool, cudaStream_t);
+int join_64(const JoinP&, unsigned, cudaStream_t);
+int join_128(const JoinP&, unsigned, cudaStream_t);
+int join_256(const JoinP&, unsigned, cudaStream_t);
+
+}  // namespace mkop

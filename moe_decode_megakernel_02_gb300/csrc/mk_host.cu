@@ -1066,6 +1066,28 @@ int mk_kv_write(mk_kv* kv, int32_t layer, int32_t seq, int32_t pos0, int32_t n, 
     return kv_copy(kv, layer, seq, pos0, n, const_cast<void*>(rows), stream, 1);
 }
 
+int mk_kv_view(const mk_kv* kv, int32_t layer, mk_pages* pages, mk_page_table* table) {
+    if (!kv || kv->magic != KV_MAGIC || !pages || !table) return fail(MK_ERR_INVALID_ARG, "bad kv, pages or table");
+    const Dims D = dims_of(kv->m->cfg);
+    if (layer < 0 || layer >= D.L) return fail(MK_ERR_INVALID_ARG, "layer %d out of range", layer);
+    if (!D.gqa) return fail(MK_ERR_UNSUPPORTED, "kv view: MLA pages hold a latent and a rope part, not K and V");
+    // a page is [Hkv][K rows | V rows][PAGE][hd]
+    const int64_t plane = (int64_t)mk::PAGE * D.hd;
+    *pages = mk_pages{};
+    pages->k = kv->pool + (size_t)layer * kv->layer_elems;
+    pages->v = (uint16_t*)pages->k + plane;
+    pages->page_stride = (int64_t)kv->page_elems;
+    pages->head_stride = 2 * plane;
+    pages->row_stride = D.hd;
+    pages->format = MK_KV_BF16;
+    pages->n_pages = kv->batch * kv->pps;
+    pages->n_kv_heads = D.Hkv;
+    pages->page_size = mk::PAGE;
+    pages->head_dim = D.hd;
+    *table = mk_page_table{kv->btab, kv->pps, kv->batch, kv->pps};
+    return MK_OK;
+}
+
 int mk_kv_read(const mk_kv* kv, int32_t layer, int32_t seq, int32_t pos0, int32_t n, void* rows, void* stream) {
     return kv_copy(kv, layer, seq, pos0, n, rows, stream, 0);
 }

@@ -1,0 +1,199 @@
+"""Paged KV caches of the caller: rows in (quantised on the way), rows out, and attention over the pages.
+
+Binding of mk_pages_write, mk_pages_read and mk_pages_attend (include/mk.h).
+The cache, its block table and everything else are the caller's own tensors;
+a `Pages` only describes them. Calls run on the current stream (or `stream`)
+of the cache's device and may be captured into a CUDA graph.
+
+    k = torch.empty(n_pages, n_kv_heads, page_size, head_dim, dtype=torch.float8_e4m3fn, device="cuda")
+    cache = Pages(k, torch.empty_like(k), k_scale, v_scale)   # scales: float32 [n_pages, n_kv_heads, page_size]
+    cache.write(table, positions, k_new, v_new)               # [batch, tokens, n_kv_heads, head_dim]
+    out = cache.attend(table, lens, q)                        # [batch, tokens, n_q_heads, head_dim]
+
+Position j of sequence b is row j % page_size of page table[b, j // page_size].
+"""
+from __future__ import annotations
+
+import ctypes
+import math
+
+import torch
+
+from . import (DT_BF16, DT_F16, DT_F32, KV_BF16, KV_E4M3, KV_INT8, AttentionStruct, PagesStruct, RowsStruct,
+               TableStruct, _check, lib)
+
+_FORMAT = {torch.bfloat16: KV_BF16, torch.float8_e4m3fn: KV_E4M3, torch.int8: KV_INT8}
+_DTYPE = {torch.float32: DT_F32, torch.bfloat16: DT_BF16, torch.float16: DT_F16}
+_byref = ctypes.byref
+
+
+def _launch(device, stream, call):
+    """call(stream handle) with `device` current and torch's allocations on that stream."""
+    index = device.index
+    if stream is None and index == torch.cuda.current_device():
+        return call(torch._C._cuda_getCurrentRawStream(index))
+    with torch.cuda.device(index):
+        if stream is None:
+            return call(torch.cuda.current_stream().cuda_stream)
+        if not isinstance(stream, torch.cuda.Stream):
+            stream = torch.cuda.ExternalStream(int(stream)) if stream else torch.cuda.default_stream()
+        if stream.device.index != index:
+            raise ValueError(f"stream of device {stream.device.index}, tensors on device {index}")
+        with torch.cuda.stream(stream):
+            return call(stream.cuda_stream)
+
+
+def _ptr(x, name, shape, dtype, device):
+    """data_ptr of an optional contiguous argument after its checks."""
+    if x is None:
+        return None
+    if x.dtype != dtype or x.shape != shape or x.device != device or not x.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)} on {device}, got "
+                         f"{x.dtype} {tuple(x.shape)} on {x.device}")
+    return x.data_ptr()
+
+
+def _rows(x, name, device, shape=None):
+    dt = _DTYPE.get(x.dtype)
+    if dt is None or x.dim() != 4 or x.device != device or (x.stride(3) != 1 and x.shape[3] > 1):
+        raise ValueError(f"{name} must be a float32, bfloat16 or float16 tensor [batch, tokens, heads, head_dim] on "
+                         f"{device} whose last dimension is contiguous, got {x.dtype} {tuple(x.shape)} strides "
+                         f"{x.stride()} on {x.device}")
+    if shape is not None and x.shape != shape:
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(x.shape)}")
+    s = x.stride()
+    return RowsStruct(x.data_ptr(), s[0], s[1], s[2], dt, 0)
+
+
+class Pages:
+    """K and V pages: two tensors [n_pages, n_kv_heads, page_size, head_dim] of the same strides (bfloat16,
+    float8_e4m3fn or int8, last dimension contiguous) and, for the 8-bit types, two float32 scale tensors
+    [n_pages, n_kv_heads, page_size]."""
+
+    def __init__(self, k, v, k_scale=None, v_scale=None):
+        fmt = _FORMAT.get(k.dtype)
+        if fmt is None or v.dtype != k.dtype:
+            raise ValueError(f"k and v must both be bfloat16, float8_e4m3fn or int8, got {k.dtype} and {v.dtype}")
+        if k.dim() != 4 or v.shape != k.shape or v.stride() != k.stride() or k.stride(3) != 1:
+            raise ValueError("k and v must be [n_pages, n_kv_heads, page_size, head_dim] with the same strides and a "
+                             "contiguous last dimension")
+        if not k.is_cuda or v.device != k.device:
+            raise ValueError("k and v must be CUDA tensors of one device")
+        if (k_scale is None) != (fmt == KV_BF16) or (v_scale is None) != (fmt == KV_BF16):
+            raise ValueError("8-bit pages need k_scale and v_scale, bfloat16 pages have none")
+        ss = (0, 0)
+        if k_scale is not None:
+            for s in (k_scale, v_scale):
+                if s.dtype != torch.float32 or s.shape != k.shape[:3] or s.device != k.device or s.stride(2) != 1:
+                    raise ValueError("scales must be float32 [n_pages, n_kv_heads, page_size] on the pages' device "
+                                     "with a contiguous last dimension")
+            if k_scale.stride() != v_scale.stride():
+                raise ValueError("k_scale and v_scale must have the same strides")
+            ss = k_scale.stride()
+        self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
+        self.device = k.device
+        st = k.stride()
+        self._s = PagesStruct(k.data_ptr(), v.data_ptr(), k_scale.data_ptr() if k_scale is not None else None,
+                              v_scale.data_ptr() if v_scale is not None else None, st[0], st[1], st[2], ss[0], ss[1],
+                              fmt, k.shape[0], k.shape[1], k.shape[2], k.shape[3], 0)
+
+    def _table(self, table):
+        if table.dtype != torch.int32 or table.dim() != 2 or table.device != self.device or table.stride(1) != 1:
+            raise ValueError(f"table must be an int32 tensor [batch, pages per sequence] on {self.device} with a "
+                             f"contiguous last dimension, got {table.dtype} {tuple(table.shape)} on {table.device}")
+        return TableStruct(table.data_ptr(), table.stride(0), table.shape[0], table.shape[1])
+
+    def _copy(self, fn, table, positions, k, v, counts, status, stream):
+        dev, t = self.device, self._table(table)
+        B = (t.batch,)
+        rk, rv = _rows(k, "k", dev), _rows(v, "v", dev, k.shape)
+        s = self._s
+        if k.shape[0] != t.batch or k.shape[2] != s.n_kv_heads or k.shape[3] != s.head_dim:
+            raise ValueError(f"k and v must be [{t.batch}, tokens, {s.n_kv_heads}, {s.head_dim}], got {tuple(k.shape)}")
+        if positions is None:
+            raise ValueError("positions is required")
+        pos = _ptr(positions, "positions", B, torch.int32, dev)
+        cnt = _ptr(counts, "counts", B, torch.int32, dev)
+        st = _ptr(status, "status", (1,), torch.int32, dev)
+        if t.batch == 0 or k.shape[1] == 0:
+            return
+        _launch(dev, stream, lambda h: _check(fn(_byref(s), _byref(t), pos, cnt, k.shape[1], _byref(rk), _byref(rv),
+                                                 st, h)))
+
+    def write(self, table, positions, k, v, counts=None, status=None, stream=None):
+        """Rows t < counts[b] (all, without counts) of k and v, [batch, tokens, n_kv_heads, head_dim], to positions
+        positions[b] + t: 8-bit pages get codes and a scale a row. positions, counts: int32 [batch]. A position or
+        page out of range is skipped and sets status[0] (int32 [1]) to MK_ERR_INVALID_ARG."""
+        self._copy(lib().mk_pages_write, table, positions, k, v, counts, status, stream)
+
+    def read(self, table, positions, k, v, counts=None, status=None, stream=None):
+        """Fills rows t < counts[b] of k and v, [batch, tokens, n_kv_heads, head_dim], from positions
+        positions[b] + t, as code x scale rounded to their type; other rows stay as they are. Returns (k, v)."""
+        self._copy(lib().mk_pages_read, table, positions, k, v, counts, status, stream)
+        return k, v
+
+    def attend(self, table, lens, q, scale=None, softcap=0.0, slopes=None, starts=None, shared_len=0, out=None,
+               return_lse=False, status=None, stream=None):
+        """Attention of q, [batch, tokens, n_q_heads, head_dim] (bfloat16 or float16): the queries of the last
+        `tokens` of the lens[b] cached positions, each over what lies before it and itself.
+
+        lens, starts: int32 [batch] (starts: the first visible position); scale: 1/sqrt(head_dim) by default;
+        softcap > 0: scores become softcap * tanh(score / softcap); slopes: float32 [n_q_heads], scores lose
+        slope * distance; shared_len: the first positions of all sequences lie in the same pages (whole pages) and
+        are read once. A token that sees nothing gets zeros (lse -inf). Returns out, or (out, lse) with lse float32
+        [batch, tokens, n_q_heads]. The workspace comes from torch's allocator, on the call's stream."""
+        dev, t, s = self.device, self._table(table), self._s
+        rq = _rows(q, "q", dev)
+        B, T, Hq, D = q.shape
+        if B != t.batch or D != s.head_dim or Hq < 1 or Hq % s.n_kv_heads:
+            raise ValueError(f"q must be [{t.batch}, tokens, a multiple of {s.n_kv_heads}, {s.head_dim}], got "
+                             f"{tuple(q.shape)}")
+        if lens is None:
+            raise ValueError("lens is required")
+        n = _ptr(lens, "lens", (B,), torch.int32, dev)
+        first = _ptr(starts, "starts", (B,), torch.int32, dev)
+        sl = _ptr(slopes, "slopes", (Hq,), torch.float32, dev)
+        st = _ptr(status, "status", (1,), torch.int32, dev)
+        if out is not None and out.dtype != q.dtype:
+            raise ValueError(f"out must have q's type {q.dtype}, got {out.dtype}")
+        if scale is None:
+            scale = 1.0 / math.sqrt(D)
+
+        def call(h):
+            o = torch.empty((B, T, Hq, D), dtype=q.dtype, device=dev) if out is None else out
+            ro = _rows(o, "out", dev, q.shape)
+            lse = torch.empty((B, T, Hq), dtype=torch.float32, device=dev) if return_lse else None
+            if B and T:
+                a = AttentionStruct(ctypes.pointer(s), ctypes.pointer(t), n, first, sl, ctypes.pointer(rq),
+                                    ctypes.pointer(ro), None if lse is None else lse.data_ptr(), st, T, Hq, scale,
+                                    softcap, shared_len, 0)
+                need = ctypes.c_int64()
+                _check(lib().mk_pages_attend_workspace(_byref(a), _byref(need)))
+                w = torch.empty((need.value,), dtype=torch.uint8, device=dev)
+                _check(lib().mk_pages_attend(_byref(a), w.data_ptr(), need.value, h))
+            return (o, lse) if return_lse else o
+
+        return _launch(dev, stream, call)
+
+
+class _Memory:
+    """Device memory of the library as torch sees it (keeps its owner alive)."""
+
+    def __init__(self, owner, ptr, shape, strides, typestr):
+        self.owner = owner
+        self.__cuda_array_interface__ = {"shape": shape, "strides": strides, "typestr": typestr, "data": (ptr, False),
+                                         "version": 3, "stream": None}
+
+
+def of_cache(kv, layer) -> Pages:
+    """The pages of one layer of a model's KVCache (no copy); `.table` is its block table, int32 [batch, pages]."""
+    s, t = PagesStruct(), TableStruct()
+    _check(lib().mk_kv_view(kv.h, layer, _byref(s), _byref(t)))
+    shape = (s.n_pages, s.n_kv_heads, s.page_size, s.head_dim)
+    strides = (2 * s.page_stride, 2 * s.head_stride, 2 * s.row_stride, 2)
+    # bfloat16 has no type string there: taken as 16-bit integers, then seen as bfloat16
+    k, v = (torch.as_tensor(_Memory(kv, p, shape, strides, "<i2"), device="cuda").view(torch.bfloat16)
+            for p in (s.k, s.v))
+    out = Pages(k, v)
+    out.table = torch.as_tensor(_Memory(kv, t.table, (t.batch, t.pages_per_seq), None, "<i4"), device="cuda")
+    return out
