@@ -5,15 +5,17 @@
 //   x_j = cap(scale q.k_j) - slope (p - j),  m = max x_j,
 //   out = sum_j e^(x_j - m) v_j / sum_j e^(x_j - m),
 // in one pass: a running maximum, the sum and the output rescaled when the
-// maximum rises. Rows of one kv head (n_tokens x query heads of the group) are
-// the M of two chains of m16n8k16 tensor-core products, positions the N of
-// the first and the K of the second.
+// maximum rises. Both products run transposed on the tensor cores
+// (m16n8k16): 16 positions by 8 rows of scores, then 16 values by 8 rows of
+// output, so that a decode step's 1 to 8 query heads of a kv head fill the
+// 8-wide side, K and V fragments are each used once per 8 rows, and a thread
+// keeps the same two rows from the scores to the output.
 //
-// Two shapes of the same loop over 64- or 128-position tiles (cp.async ring in
-// shared memory):
-//   FEW   up to 32 rows an item: the four warps split a tile's positions and
-//         hold the same rows; their maxima, sums and outputs meet at the end.
-//         Bound by the cache's bytes.
+// Two shapes of the same loop over 64-position tiles (cp.async ring in shared
+// memory):
+//   FEW   up to 8, 16 or 32 rows an item: the four warps split a tile's
+//         positions and hold the same rows; their maxima, sums and outputs
+//         meet at the end. Bound by the cache's bytes.
 //   MANY  64 rows an item: the four warps split the rows and all read the
 //         whole tile: large verify blocks, and the shared prefix, where the
 //         rows of all sequences stand against one copy of K and V. Bound by
@@ -31,9 +33,10 @@
 // so a product keeps 16 bits. 8-bit pages: codes are exact in fp16; a query
 // row is scaled by a power of two into fp16 (exact but for values 2^-24 below
 // the row's largest); the K scale multiplies the score, the V scale the
-// probability, which goes in as one fp16 (11 bits), scaled by 2^15 over the
-// largest V scale so far: products below 2^-29 of the largest possible one
-// fall under fp16's normal range and keep steps of 2^-39 of it.
+// probability, which goes in as one fp16 (11 bits; hi + lo parts for fp16
+// outputs, whose own rounding is as fine), scaled by 2^15 over the largest V
+// scale so far: products below 2^-29 of the largest possible one fall under
+// fp16's normal range and keep steps of 2^-39 of it.
 #pragma once
 #include "mk_ops.cuh"
 
@@ -140,24 +143,44 @@ __device__ __forceinline__ void mma(float (&d)[4], const uint32_t (&a)[4], uint3
             : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
             : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
+// an 8 x 8 matrix of 16-bit values over the warp, transposed
+__device__ __forceinline__ uint32_t transpose8(uint32_t x) {
+    uint32_t y;
+    asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+    return y;
+}
 __device__ __forceinline__ float ex2(float x) {
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
 }
-
-// Two codes as two fp16 values, both exact. `pair` holds them in its low bytes.
-template <int FMT>
-__device__ __forceinline__ uint32_t e4m3_pair(uint32_t pair) {
-    const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)pair, __NV_E4M3);
-    return (uint32_t)h.x | (uint32_t)h.y << 16;
+__device__ __forceinline__ float rcp(float x) {
+    float y;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
 }
-// signed bytes plus 128 set into the mantissa of 1024 give 1152 + code
+
+// Four E4M3 codes as two registers of two fp16 values, exact.
+__device__ __forceinline__ void e4m3_quad(uint32_t w, uint32_t& lo, uint32_t& hi) {
+    asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, a;\n\tcvt.rn.f16x2.e4m3x2 %1, b;\n\t}"
+        : "=r"(lo), "=r"(hi)
+        : "r"(w));
+}
+// signed bytes plus 128, set into the mantissa of 1024, give 1152 + code
 __device__ __forceinline__ uint32_t int8_half2(uint32_t w) {
-    __half2 h = *reinterpret_cast<__half2*>(&w);
     const uint32_t c = 0x64806480u;  // 1152, 1152
-    h = __hsub2(h, *reinterpret_cast<const __half2*>(&c));
-    return *reinterpret_cast<uint32_t*>(&h);
+    const __half2 h = __hsub2(*reinterpret_cast<const __half2*>(&w), *reinterpret_cast<const __half2*>(&c));
+    return *reinterpret_cast<const uint32_t*>(&h);
+}
+template <int FMT>
+__device__ __forceinline__ void code_quad(uint32_t w, uint32_t& lo, uint32_t& hi) {
+    if constexpr (FMT == MK_KV_E4M3) {
+        e4m3_quad(w, lo, hi);
+    } else {
+        w ^= 0x80808080u;
+        lo = int8_half2(__byte_perm(w, 0x64646464u, 0x4140));
+        hi = int8_half2(__byte_perm(w, 0x64646464u, 0x4342));
+    }
 }
 
 // ROWB bytes of a row in shared memory: 16-byte pieces stored at piece ^ f(row),
@@ -168,47 +191,53 @@ __device__ __forceinline__ uint32_t piece(uint32_t base, int row, int c) {
     return base + row * ROWB + ((c ^ x) << 4);
 }
 
-template <int D, int FMT, bool SPLITQ, bool MANY, int MT>
+// RN: groups of 8 query rows a warp holds.
+template <int D, int FMT, bool SPLITQ, bool MANY, int RN>
 struct Shape {
     static constexpr bool F8 = FMT != MK_KV_BF16;
-    static constexpr int EB = F8 ? 1 : 2;                  // bytes of a cached value
-    static constexpr int ROWB = D * EB;                    // bytes of a cached row
-    static constexpr int SL = F8 && !MANY && D < 256 ? 32 : 16;  // positions a warp takes at once
-    static constexpr int TILE = MANY ? 64 : 4 * SL;        // positions of a tile
-    static constexpr int ROWS = MANY ? 64 * MT : 16 * MT;  // query rows of an item
-    static constexpr int TILE_B = TILE * ROWB;             // bytes of K (or V) of a tile
+    static constexpr int EB = F8 ? 1 : 2;                   // bytes of a cached value
+    static constexpr int ROWB = D * EB;                     // bytes of a cached row
+    static constexpr int SL = 16;                           // positions a warp takes at once
+    static constexpr int TILE = 64;                         // positions of a tile
+    static constexpr int ROWS = MANY ? 4 * 8 * RN : 8 * RN; // query rows of an item
+    static constexpr int TILE_B = TILE * ROWB;              // bytes of K (or V) of a tile
     static constexpr int STAGE_B = 2 * TILE_B + (F8 ? 2 * TILE * 4 : 0);
     static constexpr int Q_B = ROWS * D * 2 * (SPLITQ ? 2 : 1);
-    // two CTAs an SM, one where a row takes 512 bytes
-    static constexpr int BUDGET = (D == 256 && !F8) ? 226 * 1024 : 113 * 1024;
-    static constexpr int FIT = (BUDGET - Q_B - 4096) / STAGE_B;
-    static constexpr int STAGES = FIT > 4 ? 4 : FIT;
+    static constexpr int MISC_B = 3072;
+    static constexpr int OREGS = RN * D / 4;                // registers of the output
+    static constexpr bool QREG = RN * D / 8 * (SPLITQ ? 2 : 1) <= 32;  // the queries stay in registers too
+    // CTAs an SM: what the registers allow, and at least two stages of the ring
+    static constexpr int WANT = OREGS <= 32 ? 4 : RN < 4 && OREGS <= 64 ? 3 : 2;
+    static constexpr int fit(int ctas) { return (227 * 1024 / ctas - 1024 - Q_B - MISC_B) / STAGE_B; }
+    static constexpr int CTAS = fit(WANT) >= 3 ? WANT : fit(3) >= 3 && WANT > 3 ? 3 : fit(2) >= 2 ? 2 : 1;
+    static constexpr int STAGES = fit(CTAS) > 4 ? 4 : fit(CTAS);
     static constexpr int RING_B = STAGES * STAGE_B;
-    static constexpr int SMEM = RING_B + Q_B + 4096;
+    static constexpr int SMEM = RING_B + Q_B + MISC_B;
     // the warps' outputs meet in the ring's memory (FEW)
     static_assert(MANY || 4 * ROWS * D * 4 <= RING_B, "ring too small for the merge");
-    static_assert(STAGES >= 2, "ring");
+    static_assert(STAGES >= 2 && SMEM <= 227 * 1024, "ring");
 };
 
-// per-row facts and the page numbers of the tiles being fetched
+// per-row facts, and where the rows of the tiles being fetched lie
 template <int ROWS, int TILE>
 struct Misc {
+    long long off[2][TILE];  // bytes after the head's first row; -1: no such row, zeros
+    long long scan[AT / 32];
+    long long found_base;
     float slope2[ROWS];  // slope * log2 e
     float qscale[ROWS];  // 8-bit pages: the power of two taken out of the query
     int lo[ROWS], hi[ROWS], at[ROWS];
-    int page[2][TILE];
-    long long scan[AT / 32 + 2];
-    long long found_base;
     int found_b;
 };
 
-template <int D, int FMT, bool SPLITQ, bool MANY, int MT>
-__global__ void __launch_bounds__(AT) attend_kernel(const __grid_constant__ AttendP p) {
-    using S = Shape<D, FMT, SPLITQ, MANY, MT>;
+template <int D, int FMT, bool SPLITQ, bool MANY, int RN>
+__global__ void __launch_bounds__(AT, Shape<D, FMT, SPLITQ, MANY, RN>::CTAS)
+    attend_kernel(const __grid_constant__ AttendP p) {
+    using S = Shape<D, FMT, SPLITQ, MANY, RN>;
     constexpr bool F8 = S::F8;
-    constexpr int ROWB = S::ROWB, TILE = S::TILE, SL = S::SL, ROWS = S::ROWS, NT = D / 8;
+    constexpr int ROWB = S::ROWB, TILE = S::TILE, SL = S::SL, ROWS = S::ROWS, DT = D / 16;
     using M = Misc<ROWS, TILE>;
-    static_assert(sizeof(M) <= 4096, "misc area");
+    static_assert(sizeof(M) <= S::MISC_B, "misc area");
     extern __shared__ __align__(128) uint8_t smem[];
     const uint32_t ring = sm32(smem), qs = ring + S::RING_B;
     uint8_t* const qmem = smem + S::RING_B;
@@ -273,9 +302,8 @@ __global__ void __launch_bounds__(AT) attend_kernel(const __grid_constant__ Atte
     }
     int b = ms.found_b;
     long long base_b = ms.found_base;
-    const long long per = units_each(total, gridDim.x, p.min_units);
-    const long long my_end = min(total, my_first + per);
-    const float scale2 = p.scale * LOG2E;
+    const long long my_end = min(total, my_first + units_each(total, gridDim.x, p.min_units));
+    const int g8 = lane >> 2, q4 = lane & 3;  // a fragment's row (or column) and pair
 
     for (long long u = my_first; u < my_end;) {
         // ---- the item: sequence b, kv head h, row block rb; its tiles [t0, t0 + take)
@@ -296,6 +324,56 @@ __global__ void __launch_bounds__(AT) attend_kernel(const __grid_constant__ Atte
         const long long u_first = u;
         u += take;
 
+        // ---- fetching: where a tile's rows lie is looked up one tile ahead of the copies, a thread a row
+        const uint8_t* const kh = p.k + h * p.head_b;
+        const uint8_t* const vh = p.v + h * p.head_b;
+        const int* const trow = p.table + (p.is_shared ? 0 : b) * p.table_s;
+        const int mask = (1 << p.ps_shift) - 1;
+        auto page_of = [&](int tile) {  // of position tid of the tile; -1: not this item's, or no such page
+            const int pos = (t0 + tile) * TILE + tid;
+            if (tid >= TILE || tile >= take || pos < clo || pos >= chi) return -1;
+            const int pg = trow[pos >> p.ps_shift];
+            if ((unsigned)pg < (unsigned)p.n_pages) return pg;
+            if (p.status) *p.status = MK_ERR_INVALID_ARG;
+            return -1;
+        };
+        long long sc_at = -1;  // 8-bit pages: where this thread's row of the tile fetched next has its scales
+        auto place = [&](int tile, int page) {
+            if (tid < TILE) {
+                const int r = ((t0 + tile) * TILE + tid) & mask;
+                ms.off[tile & 1][tid] = page < 0 ? -1 : page * p.page_b + r * p.row_b;
+                if constexpr (F8) sc_at = page < 0 ? -1 : page * p.sc_page + h * p.sc_head + r;
+            }
+        };
+        auto fetch = [&](int tile) {
+            if (tile < take) {
+                const uint32_t st = ring + (tile % S::STAGES) * S::STAGE_B;
+                constexpr int CH = ROWB / 16;  // pieces of a row
+                static_assert(AT % CH == 0, "a thread copies one column of pieces");
+                const long long* off = ms.off[tile & 1];
+                const int c = tid % CH;
+#pragma unroll
+                for (int r = tid / CH; r < TILE; r += AT / CH) {
+                    const long long o = off[r];
+                    const bool ok = o >= 0;
+                    const long long a = ok ? o + c * 16 : 0;
+                    const uint32_t to = piece<ROWB>(st, r, c);
+                    cp16(to, kh + a, ok);
+                    cp16(to + S::TILE_B, vh + a, ok);
+                }
+                if constexpr (F8) {
+                    if (tid < TILE) {
+                        const bool ok = sc_at >= 0;
+                        const long long a = ok ? sc_at : 0;
+                        cp4(st + 2 * S::TILE_B + tid * 4, p.ks + a, ok);
+                        cp4(st + 2 * S::TILE_B + (TILE + tid) * 4, p.vs + a, ok);
+                    }
+                }
+            }
+            cp_commit();
+        };
+
+        const int first_page = page_of(0);
         __syncthreads();  // the previous item is done with every shared area
         for (int r = tid; r < ROWS; r += AT) {
             int lo = 0, hi = 0, at = 0;
@@ -313,6 +391,13 @@ __global__ void __launch_bounds__(AT) attend_kernel(const __grid_constant__ Atte
             ms.hi[r] = hi;
             ms.at[r] = at;
             ms.slope2[r] = sl;
+        }
+        place(0, first_page);
+        for (int t = 0; t < S::STAGES - 1; ++t) {
+            const int next = page_of(t + 1);
+            __syncthreads();
+            fetch(t);
+            place(t + 1, next);
         }
         // ---- queries into shared memory, a warp a row
         for (int r = warp; r < ROWS; r += 4) {
@@ -360,287 +445,209 @@ __global__ void __launch_bounds__(AT) attend_kernel(const __grid_constant__ Atte
                 }
             }
         }
+        __syncthreads();
 
-        // ---- fetching: page numbers one tile ahead of the copies
-        const uint8_t* const kh = p.k + h * p.head_b;
-        const uint8_t* const vh = p.v + h * p.head_b;
-        const int* const trow = p.table + (p.is_shared ? 0 : b) * p.table_s;
-        auto page_of = [&](int tile, int i) {  // -1: not this item's, or no such page
-            const int pos = (t0 + tile) * TILE + i;
-            if (tile >= take || pos < clo || pos >= chi) return -1;
-            const int pg = trow[pos >> p.ps_shift];
-            if ((unsigned)pg < (unsigned)p.n_pages) return pg;
-            if (p.status) *p.status = MK_ERR_INVALID_ARG;
-            return -1;
-        };
-        auto fetch = [&](int tile) {
-            if (tile < take) {
-                const uint32_t st = ring + (tile % S::STAGES) * S::STAGE_B;
-                constexpr int CH = ROWB / 16;  // pieces of a row
-                const int* pg = ms.page[tile & 1];
-                const int mask = (1 << p.ps_shift) - 1;
+        // ---- the warp's rows; a thread has rows 2 q4 and 2 q4 + 1 of each group of 8
+        const int wrow = MANY ? warp * 8 * RN : 0;
+        int rlo[RN][2], rhi[RN][2];
+        float f2[RN][2];  // score to exponent of 2 (without a cap: scale log2 e; with one: into tanh's exponential)
 #pragma unroll
-                for (int i = tid; i < TILE * CH; i += AT) {
-                    const int r = i / CH, c = i % CH;
-                    const int page = pg[r];
-                    const bool ok = page >= 0;
-                    const long long o = ok ? page * p.page_b + (((t0 + tile) * TILE + r) & mask) * p.row_b + c * 16 : 0;
-                    cp16(piece<ROWB>(st, r, c), kh + o, ok);
-                    cp16(piece<ROWB>(st + S::TILE_B, r, c), vh + o, ok);
-                }
-                if constexpr (F8) {
-                    for (int r = tid; r < TILE; r += AT) {
-                        const int page = pg[r];
-                        const bool ok = page >= 0;
-                        const long long o =
-                            ok ? page * p.sc_page + h * p.sc_head + (((t0 + tile) * TILE + r) & mask) : 0;
-                        cp4(st + 2 * S::TILE_B + r * 4, p.ks + o, ok);
-                        cp4(st + 2 * S::TILE_B + (TILE + r) * 4, p.vs + o, ok);
-                    }
-                }
+        for (int n = 0; n < RN; ++n)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const int r = wrow + n * 8 + q4 * 2 + e;
+                rlo[n][e] = ms.lo[r];
+                rhi[n][e] = ms.hi[r];
+                f2[n][e] = p.scale * LOG2E * (p.cap > 0.f ? 2.f / p.cap : 1.f) * (F8 ? ms.qscale[r] : 1.f);
             }
-            cp_commit();
-        };
-        for (int t = 0; t < S::STAGES - 1; ++t) {
-            if (tid < TILE) ms.page[t & 1][tid] = page_of(t, tid);
-            __syncthreads();
-            fetch(t);
-            // the buffer is rewritten two tiles later, past the next barrier
-        }
-        if (tid < TILE) ms.page[(S::STAGES - 1) & 1][tid] = page_of(S::STAGES - 1, tid);
-
-        // ---- the warp's rows
-        const int wrow = MANY ? warp * 16 * MT : 0;
         // the range every row sees, and the range some row sees (rows that see something)
         int lo_max = 0, lo_min = INT_MAX, hi_min = INT_MAX, hi_max = 0;
-        for (int i = lane; i < 16 * MT; i += 32) {
-            const int lo = ms.lo[wrow + i], hi = ms.hi[wrow + i];
-            if (wrow + i < nrows && lo < hi) {
-                lo_max = max(lo_max, lo), lo_min = min(lo_min, lo);
-                hi_min = min(hi_min, hi), hi_max = max(hi_max, hi);
-            }
-        }
 #pragma unroll
-        for (int o = 16; o; o >>= 1) {
+        for (int n = 0; n < RN; ++n)
+#pragma unroll
+            for (int e = 0; e < 2; ++e)
+                if (wrow + n * 8 + q4 * 2 + e < nrows && rlo[n][e] < rhi[n][e]) {
+                    lo_max = max(lo_max, rlo[n][e]), lo_min = min(lo_min, rlo[n][e]);
+                    hi_min = min(hi_min, rhi[n][e]), hi_max = max(hi_max, rhi[n][e]);
+                }
+#pragma unroll
+        for (int o = 1; o < 4; o <<= 1) {
             lo_max = max(lo_max, __shfl_xor_sync(0xffffffffu, lo_max, o));
             lo_min = min(lo_min, __shfl_xor_sync(0xffffffffu, lo_min, o));
             hi_min = min(hi_min, __shfl_xor_sync(0xffffffffu, hi_min, o));
             hi_max = max(hi_max, __shfl_xor_sync(0xffffffffu, hi_max, o));
         }
+        // queries as B fragments: columns are rows, steps along D
+        auto q_frag = [&](uint32_t(&q)[4], int n, int step, int part) {  // of steps `step` and `step + 1`
+            const int r = wrow + n * 8 + (lane & 7), c = step * 2 + (lane >> 3);
+            ldsm4(q, qs + part * (ROWS * D * 2) + r * (D * 2) + ((c ^ (r & 7)) << 4));
+        };
+        uint32_t qf[S::QREG ? RN : 1][S::QREG ? DT / 2 : 1][4], ql[S::QREG && SPLITQ ? RN : 1][S::QREG && SPLITQ ? DT / 2 : 1][4];
+        if constexpr (S::QREG) {
+#pragma unroll
+            for (int n = 0; n < RN; ++n)
+#pragma unroll
+                for (int i = 0; i < DT / 2; ++i) {
+                    q_frag(qf[n][i], n, 2 * i, 0);
+                    if constexpr (SPLITQ) q_frag(ql[n][i], n, 2 * i, 1);
+                }
+        }
 
-        float o[MT][NT][4], m[MT][2], l[MT][2];
-        float vunit = 0.f;  // 8-bit pages: outputs are in units of this power of two / 2^15
+        float o[RN][DT][4], m[RN][2], l[RN][2];
+        float vunit = 0.f, vinv = 0.f;  // 8-bit pages: outputs are in units of this power of two / 2^15, and 1 over that
 #pragma unroll
-        for (int mt = 0; mt < MT; ++mt) {
+        for (int n = 0; n < RN; ++n) {
 #pragma unroll
-            for (int i = 0; i < NT; ++i)
+            for (int i = 0; i < DT; ++i)
 #pragma unroll
-                for (int e = 0; e < 4; ++e) o[mt][i][e] = 0.f;
-            m[mt][0] = m[mt][1] = -INFINITY;
-            l[mt][0] = l[mt][1] = 0.f;
+                for (int e = 0; e < 4; ++e) o[n][i][e] = 0.f;
+            m[n][0] = m[n][1] = -INFINITY;
+            l[n][0] = l[n][1] = 0.f;
         }
 
         for (int tile = 0; tile < take; ++tile) {
             cp_wait<S::STAGES - 2>();
             __syncthreads();
             fetch(tile + S::STAGES - 1);
-            int next_page = -1;
-            if (tid < TILE) next_page = page_of(tile + S::STAGES, tid);
+            const int next_page = page_of(tile + S::STAGES);
 
-            const uint32_t st = ring + (tile % S::STAGES) * S::STAGE_B;
+            const uint32_t st = ring + (tile % S::STAGES) * S::STAGE_B, vt = st + S::TILE_B;
+            const float* const scales =
+                reinterpret_cast<const float*>(smem + (tile % S::STAGES) * S::STAGE_B + 2 * S::TILE_B);
 #pragma unroll 1
             for (int s0 = MANY ? 0 : warp * SL; s0 < (MANY ? TILE : warp * SL + SL); s0 += SL) {
                 const int j0 = (t0 + tile) * TILE + s0;
                 if (j0 + SL <= lo_min || j0 >= hi_max) continue;  // no row sees any of it
                 const bool all_see = j0 >= lo_max && j0 + SL <= hi_min;
-                float x[MT][SL / 8][4];
-#pragma unroll
-                for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-                    for (int i = 0; i < SL / 8; ++i)
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) x[mt][i][e] = 0.f;
 
-                // ---- scores
-                auto q_frag = [&](uint32_t(&a)[4], int mt, int step, int part) {
-                    const int r = wrow + mt * 16 + (lane & 15), c = step * 2 + (lane >> 4);
-                    ldsm4(a, qs + part * (ROWS * D * 2) + r * (D * 2) + ((c ^ (r & 7)) << 4));
-                };
-                if constexpr (!F8) {
+                // ---- scores, transposed: 16 positions by 8 rows a product.
+                // x[n][0..1]: position g8, rows 2 q4 and 2 q4 + 1; x[n][2..3]: position g8 + 8
+                float x[RN][4];
 #pragma unroll
-                    for (int step = 0; step < D / 16; ++step) {
-                        uint32_t a[MT][4], al[MT][4];
+                for (int n = 0; n < RN; ++n)
 #pragma unroll
-                        for (int mt = 0; mt < MT; ++mt) {
-                            q_frag(a[mt], mt, step, 0);
-                            if constexpr (SPLITQ) q_frag(al[mt], mt, step, 1);
-                        }
+                    for (int e = 0; e < 4; ++e) x[n][e] = 0.f;
 #pragma unroll
-                        for (int s = 0; s < SL / 16; ++s) {
-                            uint32_t kb[4];
-                            ldsm4(kb, piece<ROWB>(st, s0 + s * 16 + (lane >> 4) * 8 + (lane & 7),
-                                                  step * 2 + ((lane >> 3) & 1)));
+                for (int i = 0; i < DT / 2; ++i) {
+                    uint32_t a[2][4];
+                    if constexpr (!F8) {
 #pragma unroll
-                            for (int mt = 0; mt < MT; ++mt) {
-                                mma<false>(x[mt][2 * s], a[mt], kb[0], kb[1]);
-                                mma<false>(x[mt][2 * s + 1], a[mt], kb[2], kb[3]);
-                                if constexpr (SPLITQ) {
-                                    mma<false>(x[mt][2 * s], al[mt], kb[0], kb[1]);
-                                    mma<false>(x[mt][2 * s + 1], al[mt], kb[2], kb[3]);
-                                }
-                            }
+                        for (int c = 0; c < 2; ++c)
+                            ldsm4(a[c], piece<ROWB>(st, s0 + (lane & 15), (2 * i + c) * 2 + (lane >> 4)));
+                    } else {
+                        uint32_t w[4];
+                        ldsm4(w, piece<ROWB>(st, s0 + (lane & 15), 2 * i + (lane >> 4)));
+#pragma unroll
+                        for (int c = 0; c < 2; ++c) {
+                            code_quad<FMT>(w[2 * c], a[c][0], a[c][2]);
+                            code_quad<FMT>(w[2 * c + 1], a[c][1], a[c][3]);
                         }
                     }
-                } else {
 #pragma unroll
-                    for (int step = 0; step < D / 16; step += 2) {
-                        uint32_t a[MT][2][4];
-#pragma unroll
-                        for (int mt = 0; mt < MT; ++mt) {
-                            q_frag(a[mt][0], mt, step, 0);
-                            q_frag(a[mt][1], mt, step + 1, 0);
-                        }
-#pragma unroll
-                        for (int s = 0; s < SL / 16; ++s) {
-                            uint32_t kb[4];  // positions 0-7: pieces step, step+1; positions 8-15: the same
-                            ldsm4(kb, piece<ROWB>(st, s0 + s * 16 + (lane >> 4) * 8 + (lane & 7),
-                                                  step + ((lane >> 3) & 1)));
-#pragma unroll
-                            for (int i = 0; i < 4; ++i) {
-                                uint32_t b0, b1;
-                                if constexpr (FMT == MK_KV_E4M3) {
-                                    b0 = e4m3_pair<FMT>(kb[i] & 0xffffu);
-                                    b1 = e4m3_pair<FMT>(kb[i] >> 16);
-                                } else {
-                                    const uint32_t w = kb[i] ^ 0x80808080u;
-                                    b0 = int8_half2(__byte_perm(w, 0x64646464u, 0x4140));
-                                    b1 = int8_half2(__byte_perm(w, 0x64646464u, 0x4342));
-                                }
-#pragma unroll
-                                for (int mt = 0; mt < MT; ++mt) mma<true>(x[mt][2 * s + (i >> 1)], a[mt][i & 1], b0, b1);
+                    for (int n = 0; n < RN; ++n) {
+                        if constexpr (S::QREG) {
+                            mma<F8>(x[n], a[0], qf[n][i][0], qf[n][i][1]);
+                            mma<F8>(x[n], a[1], qf[n][i][2], qf[n][i][3]);
+                            if constexpr (SPLITQ) {
+                                mma<F8>(x[n], a[0], ql[n][i][0], ql[n][i][1]);
+                                mma<F8>(x[n], a[1], ql[n][i][2], ql[n][i][3]);
+                            }
+                        } else {
+                            uint32_t q[4];
+                            q_frag(q, n, 2 * i, 0);
+                            mma<F8>(x[n], a[0], q[0], q[1]);
+                            mma<F8>(x[n], a[1], q[2], q[3]);
+                            if constexpr (SPLITQ) {
+                                q_frag(q, n, 2 * i, 1);
+                                mma<F8>(x[n], a[0], q[0], q[1]);
+                                mma<F8>(x[n], a[1], q[2], q[3]);
                             }
                         }
                     }
                 }
 
-                // ---- 8-bit pages: scales of this thread's columns
-                float vsc[SL / 8][2];
-                float grow = 1.f;
+                // ---- 8-bit pages: scales of this thread's two positions
+                float vsc[2] = {1.f, 1.f}, grow = 1.f;
                 if constexpr (F8) {
-                    const float* ksm = reinterpret_cast<const float*>(
-                        smem + (tile % S::STAGES) * S::STAGE_B + 2 * S::TILE_B);
-                    float big = 0.f;
+                    const float k0 = scales[s0 + g8], k1 = scales[s0 + g8 + 8];
+                    vsc[0] = scales[TILE + s0 + g8], vsc[1] = scales[TILE + s0 + g8 + 8];
 #pragma unroll
-                    for (int i = 0; i < SL / 8; ++i) {
-                        const int c = s0 + i * 8 + (lane & 3) * 2;
-                        const float2 kk = *reinterpret_cast<const float2*>(ksm + c);
-                        const float2 vv = *reinterpret_cast<const float2*>(ksm + TILE + c);
-#pragma unroll
-                        for (int mt = 0; mt < MT; ++mt) {
-                            x[mt][i][0] *= kk.x, x[mt][i][1] *= kk.y;
-                            x[mt][i][2] *= kk.x, x[mt][i][3] *= kk.y;
-                        }
-                        vsc[i][0] = vv.x, vsc[i][1] = vv.y;
-                        big = fmaxf(big, fmaxf(vv.x, vv.y));
+                    for (int n = 0; n < RN; ++n) {
+                        x[n][0] *= k0, x[n][1] *= k0;
+                        x[n][2] *= k1, x[n][3] *= k1;
                     }
-                    big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 1));
-                    big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 2));
-                    if (big > vunit) {  // the same in all lanes: every row has the same columns
+                    float big = fmaxf(vsc[0], vsc[1]);
+                    if (__any_sync(0xffffffffu, big > vunit)) {
+#pragma unroll
+                        for (int s = 4; s < 32; s <<= 1) big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, s));
                         // above `big`, and far enough from 0 for 2^15 over it
                         const unsigned e = min((__float_as_uint(big) >> 23) + 1, 250u);
                         const float nu = __uint_as_float(max(e, 27u) << 23);
                         grow = vunit / nu;
                         vunit = nu;
+                        vinv = __uint_as_float((2u * 127u + 15u - max(e, 27u)) << 23);
                     }
-                    const float inv = vunit > 0.f ? 32768.f / vunit : 0.f;
-#pragma unroll
-                    for (int i = 0; i < SL / 8; ++i) vsc[i][0] *= inv, vsc[i][1] *= inv;
+                    vsc[0] *= vinv, vsc[1] *= vinv;
                 }
 
                 // ---- softmax: x becomes the probabilities
-                uint32_t seen[MT];  // bit (i*4+e): the value is visible to its row (used where some are not)
+                uint32_t seen = 0xffffffffu;  // bit n*4+e: the row sees the position
+                bool turn = false;
+                float f[RN][2];
 #pragma unroll
-                for (int mt = 0; mt < MT; ++mt) {
-                    seen[mt] = 0xffffffffu;
+                for (int n = 0; n < RN; ++n)
 #pragma unroll
-                    for (int hf = 0; hf < 2; ++hf) {
-                        const int r = wrow + mt * 16 + (lane >> 2) + hf * 8;
-                        const float qsc = F8 ? ms.qscale[r] : 1.f;
-                        float top = -INFINITY;
-                        if (p.cap > 0.f || p.slopes) {
-                            const float sl2 = ms.slope2[r];
-                            const int at = ms.at[r];
-#pragma unroll
-                            for (int i = 0; i < SL / 8; ++i)
-#pragma unroll
-                                for (int e = 0; e < 2; ++e) {
-                                    float y = x[mt][i][hf * 2 + e] * qsc * p.scale;
-                                    if (p.cap > 0.f) {
-                                        // tanh z = 1 - 2 / (e^2z + 1): the error stays near 2^-23 of 1
-                                        const float z = y / p.cap;
-                                        const float t = 1.f - __fdividef(2.f, ex2(fminf(2.f * LOG2E * z, 80.f)) + 1.f);
-                                        y = p.cap * (y != y ? y : t);
-                                    }
-                                    const int j = j0 + i * 8 + (lane & 3) * 2 + e;
-                                    x[mt][i][hf * 2 + e] = y * LOG2E - sl2 * (float)(at - j);
-                                }
-                        } else {
-                            const float f = qsc * scale2;
-#pragma unroll
-                            for (int i = 0; i < SL / 8; ++i) {
-                                x[mt][i][hf * 2] *= f;
-                                x[mt][i][hf * 2 + 1] *= f;
-                            }
+                    for (int e = 0; e < 2; ++e) {
+                        float y0 = x[n][e] * f2[n][e], y1 = x[n][2 + e] * f2[n][e];
+                        if (p.cap > 0.f) {
+                            // tanh z = 1 - 2 / (e^2z + 1): the error stays near 2^-23 of 1
+                            const float c2 = p.cap * LOG2E;
+                            y0 = c2 - 2.f * c2 * rcp(ex2(y0) + 1.f);
+                            y1 = c2 - 2.f * c2 * rcp(ex2(y1) + 1.f);
+                        }
+                        if (p.slopes) {
+                            const int r = wrow + n * 8 + q4 * 2 + e;
+                            const float sl = ms.slope2[r], far = (float)(ms.at[r] - j0 - g8);  // a whole number: exact
+                            y0 -= sl * far;
+                            y1 -= sl * (far - 8.f);
                         }
                         if (!all_see) {
-                            const int lo = ms.lo[r], hi = ms.hi[r];
-#pragma unroll
-                            for (int i = 0; i < SL / 8; ++i)
-#pragma unroll
-                                for (int e = 0; e < 2; ++e) {
-                                    const int j = j0 + i * 8 + (lane & 3) * 2 + e;
-                                    if (j < lo || j >= hi) {
-                                        x[mt][i][hf * 2 + e] = -INFINITY;
-                                        seen[mt] &= ~(1u << (i * 4 + hf * 2 + e));
-                                    }
-                                }
+                            const int j = j0 + g8;
+                            if (j < rlo[n][e] || j >= rhi[n][e]) y0 = -INFINITY, seen &= ~(1u << (n * 4 + e));
+                            if (j + 8 < rlo[n][e] || j + 8 >= rhi[n][e]) y1 = -INFINITY, seen &= ~(4u << (n * 4 + e));
                         }
+                        float top = fmaxf(y0, y1);
 #pragma unroll
-                        for (int i = 0; i < SL / 8; ++i) top = fmaxf(top, fmaxf(x[mt][i][hf * 2], x[mt][i][hf * 2 + 1]));
-                        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
-                        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-                        const float mn = fmaxf(m[mt][hf], top);
+                        for (int s = 4; s < 32; s <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, s));
+                        const float mn = fmaxf(m[n][e], top);
                         const float ref = mn == -INFINITY ? 0.f : mn;
-                        const float keep = ex2(m[mt][hf] - ref);
-                        m[mt][hf] = mn;
-                        float sum = 0.f;
-#pragma unroll
-                        for (int i = 0; i < SL / 8; ++i)
-#pragma unroll
-                            for (int e = 0; e < 2; ++e) {
-                                const float pr = ex2(x[mt][i][hf * 2 + e] - ref);
-                                sum += pr;
-                                if constexpr (F8)  // a masked row's scale may be anything
-                                    x[mt][i][hf * 2 + e] =
-                                        seen[mt] >> (i * 4 + hf * 2 + e) & 1u ? pr * vsc[i][e] : 0.f;
-                                else
-                                    x[mt][i][hf * 2 + e] = pr;
-                            }
-                        l[mt][hf] = l[mt][hf] * keep + sum;
-                        const float f = F8 ? keep * grow : keep;
-                        if (__any_sync(0xffffffffu, f != 1.f)) {
-#pragma unroll
-                            for (int i = 0; i < NT; ++i) {
-                                o[mt][i][hf * 2] *= f;
-                                o[mt][i][hf * 2 + 1] *= f;
+                        const float keep = ex2(m[n][e] - ref);
+                        m[n][e] = mn;
+                        const float p0 = ex2(y0 - ref), p1 = ex2(y1 - ref);
+                        l[n][e] = l[n][e] * keep + (p0 + p1);
+                        x[n][e] = p0, x[n][2 + e] = p1;
+                        if constexpr (F8) {
+                            x[n][e] *= vsc[0], x[n][2 + e] *= vsc[1];
+                            if (!all_see) {  // the scale of a row that is not seen may be anything
+                                if (!(seen >> (n * 4 + e) & 1u)) x[n][e] = 0.f;
+                                if (!(seen >> (n * 4 + e) & 4u)) x[n][2 + e] = 0.f;
                             }
                         }
+                        f[n][e] = keep * grow;
+                        turn |= f[n][e] != 1.f;
                     }
+                if (__any_sync(0xffffffffu, turn)) {
+#pragma unroll
+                    for (int n = 0; n < RN; ++n)
+#pragma unroll
+                        for (int i = 0; i < DT; ++i) {
+                            o[n][i][0] *= f[n][0], o[n][i][1] *= f[n][1];
+                            o[n][i][2] *= f[n][0], o[n][i][3] *= f[n][1];
+                        }
                 }
 
                 // ---- values some row does not see must not reach it, and 0 x NaN would: look for
                 // non-finite ones where rows see different parts
-                const uint32_t vt = st + S::TILE_B;
                 bool odd = false;
                 if (!all_see && FMT != MK_KV_INT8) {
                     for (int i = lane; i < SL * (ROWB / 16); i += 32) {
@@ -662,138 +669,114 @@ __global__ void __launch_bounds__(AT) attend_kernel(const __grid_constant__ Atte
                 }
                 if (odd) {
                     // such values go to the rows that see them one by one; below they count as zeros
+#pragma unroll 1
                     for (int j = 0; j < SL; ++j) {
 #pragma unroll
-                        for (int mt = 0; mt < MT; ++mt)
+                        for (int n = 0; n < RN; ++n) {
+                            float pv[2];
+                            unsigned vis = seen >> (n * 4 + (j >= 8 ? 2 : 0));
 #pragma unroll
-                            for (int hf = 0; hf < 2; ++hf) {
-                                float pv = 0.f;
-                                unsigned vis = 0;
+                            for (int e = 0; e < 2; ++e)
+                                pv[e] = __shfl_sync(0xffffffffu, j >= 8 ? x[n][2 + e] : x[n][e], ((j & 7) << 2) | q4);
+                            vis = __shfl_sync(0xffffffffu, vis, ((j & 7) << 2) | q4);
 #pragma unroll
-                                for (int i = 0; i < SL / 8; ++i)
+                            for (int i = 0; i < DT; ++i)
 #pragma unroll
-                                    for (int e = 0; e < 2; ++e)
-                                        if (i * 8 + e == (j & ~6)) {
-                                            pv = x[mt][i][hf * 2 + e];
-                                            vis = seen[mt] >> (i * 4 + hf * 2 + e) & 1u;
+                                for (int c = 0; c < 2; ++c) {
+                                    const int d = F8 ? i * 16 + 2 * g8 + c : i * 16 + g8 + 8 * c;
+                                    const uint32_t a = piece<ROWB>(vt, s0 + j, d * S::EB / 16) + (d * S::EB & 15);
+                                    if constexpr (F8) {
+                                        uint32_t v;
+                                        asm volatile("ld.shared.u8 %0, [%1];" : "=r"(v) : "r"(a));
+                                        if ((v & 0x7fu) == 0x7fu) {
+                                            if (vis & 1u) o[n][i][2 * c] = __uint_as_float(0x7fffffffu);
+                                            if (vis & 2u) o[n][i][2 * c + 1] = __uint_as_float(0x7fffffffu);
                                         }
-                                const int from = (lane & ~3) | ((j & 7) >> 1);
-                                pv = __shfl_sync(0xffffffffu, pv, from);
-                                vis = __shfl_sync(0xffffffffu, vis, from);
-                                if (!vis) continue;
-#pragma unroll
-                                for (int i = 0; i < NT; ++i)
-#pragma unroll
-                                    for (int e = 0; e < 2; ++e) {
-                                        const int d = F8 ? (i >> 1) * 16 + (lane & 3) * 4 + 2 * e + (i & 1)
-                                                         : i * 8 + (lane & 3) * 2 + e;
-                                        const uint32_t a = piece<ROWB>(vt, s0 + j, d * S::EB / 16) + (d * S::EB & 15);
-                                        if constexpr (F8) {
-                                            uint32_t c;
-                                            asm volatile("ld.shared.u8 %0, [%1];" : "=r"(c) : "r"(a));
-                                            if ((c & 0x7fu) == 0x7fu) o[mt][i][hf * 2 + e] = __uint_as_float(0x7fffffffu);
-                                        } else {
-                                            uint16_t c;
-                                            asm volatile("ld.shared.u16 %0, [%1];" : "=h"(c) : "r"(a));
-                                            if ((c & 0x7f80u) == 0x7f80u) o[mt][i][hf * 2 + e] += pv * bf2f(c);
+                                    } else {
+                                        uint16_t v;
+                                        asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(a));
+                                        if ((v & 0x7f80u) == 0x7f80u) {
+                                            if (vis & 1u) o[n][i][2 * c] += pv[0] * bf2f(v);
+                                            if (vis & 2u) o[n][i][2 * c + 1] += pv[1] * bf2f(v);
                                         }
                                     }
-                            }
+                                }
+                        }
                     }
                 }
 
-                // ---- outputs
+                // ---- outputs, transposed: 16 values by 8 rows a product. Probabilities become B fragments
+                // (16 positions by 8 rows) by transposing 8 x 8 pieces; lo: what the 16-bit hi part left
+                const bool with_lo = !F8 || p.f16;
+                uint32_t ph[RN][2], pl[RN][2];
 #pragma unroll
-                for (int s = 0; s < SL / 16; ++s) {
-                    uint32_t a[MT][4], al[MT][4];
+                for (int n = 0; n < RN; ++n)
 #pragma unroll
-                    for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            const float y0 = x[mt][2 * s + (i >> 1)][(i & 1) * 2];
-                            const float y1 = x[mt][2 * s + (i >> 1)][(i & 1) * 2 + 1];
-                            if constexpr (F8) {
-                                a[mt][i] = pack_f16(y0, y1);
-                            } else {
-                                a[mt][i] = pack_bf16(y0, y1);
-                                al[mt][i] = pack_bf16(y0 - bf2f(a[mt][i] & 0xffffu), y1 - bf2f(a[mt][i] >> 16));
+                    for (int c = 0; c < 2; ++c) {
+                        const float y0 = x[n][2 * c], y1 = x[n][2 * c + 1];
+                        uint32_t hi, lo = 0;
+                        if constexpr (F8) {
+                            hi = pack_f16(y0, y1);
+                            if (with_lo) {
+                                const float2 z = __half22float2(*reinterpret_cast<const __half2*>(&hi));
+                                lo = pack_f16(y0 - z.x, y1 - z.y);
                             }
+                        } else {
+                            hi = pack_bf16(y0, y1);
+                            lo = pack_bf16(y0 - bf2f(hi & 0xffffu), y1 - bf2f(hi >> 16));
                         }
+                        ph[n][c] = transpose8(hi);
+                        if (with_lo) pl[n][c] = transpose8(lo);
+                    }
+#pragma unroll
+                for (int dt = 0; dt < DT; dt += F8 ? 2 : 1) {
+                    uint32_t a[F8 ? 2 : 1][4];
                     if constexpr (!F8) {
+                        ldsm4t(a[0], piece<ROWB>(vt, s0 + (lane & 7) + (lane >> 4) * 8, dt * 2 + ((lane >> 3) & 1)));
+                        if (odd) {
 #pragma unroll
-                        for (int dt = 0; dt < D / 16; ++dt) {
-                            uint32_t vb[4];
-                            ldsm4t(vb, piece<ROWB>(vt, s0 + s * 16 + (lane & 15), dt * 2 + (lane >> 4)));
-                            if (odd) {
-#pragma unroll
-                                for (int i = 0; i < 4; ++i) {
-                                    if ((vb[i] & 0x7f80u) == 0x7f80u) vb[i] &= 0xffff0000u;
-                                    if ((vb[i] & 0x7f800000u) == 0x7f800000u) vb[i] &= 0xffffu;
-                                }
-                            }
-#pragma unroll
-                            for (int mt = 0; mt < MT; ++mt) {
-                                mma<false>(o[mt][2 * dt], a[mt], vb[0], vb[1]);
-                                mma<false>(o[mt][2 * dt + 1], a[mt], vb[2], vb[3]);
-                                mma<false>(o[mt][2 * dt], al[mt], vb[0], vb[1]);
-                                mma<false>(o[mt][2 * dt + 1], al[mt], vb[2], vb[3]);
+                            for (int i = 0; i < 4; ++i) {
+                                if ((a[0][i] & 0x7f80u) == 0x7f80u) a[0][i] &= 0xffff0000u;
+                                if ((a[0][i] & 0x7f800000u) == 0x7f800000u) a[0][i] &= 0xffffu;
                             }
                         }
                     } else {
+                        // transposing byte pairs: a register holds values 2 g8, 2 g8 + 1 of two positions;
+                        // the even ones are rows 0-7 of the product, the odd ones rows 8-15
+                        uint32_t w[4];
+                        ldsm4t(w, piece<ROWB>(vt, s0 + (lane & 15), dt + (lane >> 4)));
 #pragma unroll
-                        for (int dt = 0; dt < D / 16; dt += 2) {
-                            // transposing byte pairs: a register holds values 2n, 2n+1 of two
-                            // positions; the even ones are one product's columns, the odd ones another's
-                            uint32_t vb[4];
-                            ldsm4t(vb, piece<ROWB>(vt, s0 + s * 16 + (lane & 15), dt + (lane >> 4)));
-#pragma unroll
-                            for (int c = 0; c < 2; ++c) {
-                                uint32_t be[2], bo[2];
-#pragma unroll
-                                for (int i = 0; i < 2; ++i) {
-                                    uint32_t w = vb[2 * c + i];
-                                    if constexpr (FMT == MK_KV_E4M3) {
-                                        if (odd) {
-                                            // NaN codes to zero
-                                            const uint32_t f = ((w & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u;
-                                            w &= ~((f >> 7) * 0xffu);
-                                        }
-                                        w = __byte_perm(w, 0, 0x3120);
-                                        be[i] = e4m3_pair<FMT>(w & 0xffffu);
-                                        bo[i] = e4m3_pair<FMT>(w >> 16);
-                                    } else {
-                                        w ^= 0x80808080u;
-                                        be[i] = int8_half2(__byte_perm(w, 0x64646464u, 0x4240));
-                                        bo[i] = int8_half2(__byte_perm(w, 0x64646464u, 0x4341));
-                                    }
-                                }
-#pragma unroll
-                                for (int mt = 0; mt < MT; ++mt) {
-                                    mma<true>(o[mt][2 * (dt + c)], a[mt], be[0], be[1]);
-                                    mma<true>(o[mt][2 * (dt + c) + 1], a[mt], bo[0], bo[1]);
-                                }
+                        for (int c = 0; c < 4; ++c) {
+                            if (FMT == MK_KV_E4M3 && odd) {  // NaN codes to zero
+                                const uint32_t z = ((w[c] & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u;
+                                w[c] &= ~((z >> 7) * 0xffu);
                             }
+                            code_quad<FMT>(__byte_perm(w[c], 0, 0x3120), a[c >> 1][(c & 1) * 2], a[c >> 1][(c & 1) * 2 + 1]);
                         }
                     }
+#pragma unroll
+                    for (int c = 0; c < (F8 ? 2 : 1); ++c)
+#pragma unroll
+                        for (int n = 0; n < RN; ++n) {
+                            mma<F8>(o[n][dt + c], a[c], ph[n][0], ph[n][1]);
+                            if (with_lo) mma<F8>(o[n][dt + c], a[c], pl[n][0], pl[n][1]);
+                        }
                 }
             }
-            if (tid < TILE) ms.page[(tile + S::STAGES) & 1][tid] = next_page;
+            place(tile + S::STAGES, next_page);
         }
 
-        // ---- the item's (or piece's) result
+        // ---- the item's (or piece's) result: outputs pass through shared memory, a warp's rows by rows
 #pragma unroll
-        for (int mt = 0; mt < MT; ++mt)
+        for (int n = 0; n < RN; ++n)
 #pragma unroll
-            for (int hf = 0; hf < 2; ++hf) {
-                l[mt][hf] += __shfl_xor_sync(0xffffffffu, l[mt][hf], 1);
-                l[mt][hf] += __shfl_xor_sync(0xffffffffu, l[mt][hf], 2);
+            for (int e = 0; e < 2; ++e) {
+#pragma unroll
+                for (int s = 4; s < 32; s <<= 1) l[n][e] += __shfl_xor_sync(0xffffffffu, l[n][e], s);
                 if constexpr (F8) {
                     const float f = vunit * (1.f / 32768.f);
 #pragma unroll
-                    for (int i = 0; i < NT; ++i) {
-                        o[mt][i][hf * 2] *= f;
-                        o[mt][i][hf * 2 + 1] *= f;
-                    }
+                    for (int i = 0; i < DT; ++i) o[n][i][e] *= f, o[n][i][2 + e] *= f;
                 }
             }
         const bool whole = take == n_b;
@@ -803,12 +786,12 @@ __global__ void __launch_bounds__(AT) attend_kernel(const __grid_constant__ Atte
         else if (!whole)
             slot = p.slots + (2ll * blockIdx.x + (u_first == my_first ? 0 : 1)) * p.slot_floats;
         // (m, l) of slot row r at slot + slot_rows * D + 2 r
-        auto put = [&](int r, int d, float y0, float y1, float y2, float y3, float mm, float ll, bool first) {
+        auto put = [&](int r, int d, float4 y, float mm, float ll, bool first) {
             // four values of row r from column d on. A row that sees nothing was
             // not masked where all others see everything: it is dropped here.
             if (ms.lo[r] >= ms.hi[r]) mm = -INFINITY, ll = 0.f;
             if (slot) {
-                *reinterpret_cast<float4*>(slot + (long long)r * D + d) = make_float4(y0, y1, y2, y3);
+                *reinterpret_cast<float4*>(slot + (long long)r * D + d) = y;
                 if (first) *reinterpret_cast<float2*>(slot + (long long)p.slot_rows * D + 2 * r) = make_float2(mm, ll);
                 return;
             }
@@ -816,8 +799,8 @@ __global__ void __launch_bounds__(AT) attend_kernel(const __grid_constant__ Atte
             const int rbq = bt / p.T, t = bt - rbq * p.T, hq = h * p.G + g;
             const bool none = ll == 0.f;
             const float inv = none ? 0.f : 1.f / ll;
-            const float z[4] = {none ? 0.f : y0 * inv, none ? 0.f : y1 * inv, none ? 0.f : y2 * inv,
-                                none ? 0.f : y3 * inv};
+            const float z[4] = {none ? 0.f : y.x * inv, none ? 0.f : y.y * inv, none ? 0.f : y.z * inv,
+                                none ? 0.f : y.w * inv};
             uint16_t* dst = p.out + rbq * p.ob + t * p.ot + hq * p.oh + d;
 #pragma unroll
             for (int i = 0; i < 4; ++i)
@@ -828,32 +811,31 @@ __global__ void __launch_bounds__(AT) attend_kernel(const __grid_constant__ Atte
         cp_wait<0>();
         __syncthreads();  // the ring is free
         {
-            // Outputs pass through shared memory: rows by row, four columns a
-            // thread. FEW: four warps' parts of the same rows are joined on the way.
-            constexpr int PARTS = MANY ? 1 : 4;
-            constexpr int RW = 16 * MT;  // rows of a warp
+            constexpr int RW = 8 * RN;  // rows of a warp
+            // MANY: a warp's rows one group of 8 after another through the warp's own 8 rows of memory;
+            // FEW: all four warps' rows side by side
             float* om = reinterpret_cast<float*>(smem);
-            if constexpr (!MANY) {
-                float* oml = reinterpret_cast<float*>(qmem);  // the queries are done with
+            float* oml = reinterpret_cast<float*>(qmem);  // the queries are done with
+            auto store = [&](int n, int at_row) {
 #pragma unroll
-                for (int mt = 0; mt < MT; ++mt)
+                for (int i = 0; i < DT; ++i)
 #pragma unroll
-                    for (int hf = 0; hf < 2; ++hf) {
-                        const int r = mt * 16 + (lane >> 2) + hf * 8;
-                        float* dst = om + (warp * RW + r) * D;
-#pragma unroll
-                        for (int i = 0; i < NT; ++i)
-#pragma unroll
-                            for (int e = 0; e < 2; ++e) {
-                                const int d = F8 ? (i >> 1) * 16 + (lane & 3) * 4 + 2 * e + (i & 1)
-                                                 : i * 8 + (lane & 3) * 2 + e;
-                                dst[d] = o[mt][i][hf * 2 + e];
-                            }
-                        if ((lane & 3) == 0) {
-                            oml[(warp * RW + r) * 2] = m[mt][hf];
-                            oml[(warp * RW + r) * 2 + 1] = l[mt][hf];
-                        }
+                    for (int c = 0; c < 2; ++c) {
+                        const int d = F8 ? i * 16 + 2 * g8 + c : i * 16 + g8 + 8 * c;
+                        om[(at_row + q4 * 2) * D + d] = o[n][i][2 * c];
+                        om[(at_row + q4 * 2 + 1) * D + d] = o[n][i][2 * c + 1];
                     }
+                if (g8 == 0) {
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        oml[(at_row + q4 * 2 + e) * 2] = m[n][e];
+                        oml[(at_row + q4 * 2 + e) * 2 + 1] = l[n][e];
+                    }
+                }
+            };
+            if constexpr (!MANY) {
+#pragma unroll
+                for (int n = 0; n < RN; ++n) store(n, warp * RW + n * 8);
                 __syncthreads();
                 for (int i = tid; i < nrows * (D / 4); i += AT) {
                     const int r = i / (D / 4), d = (i % (D / 4)) * 4;
@@ -869,40 +851,21 @@ __global__ void __launch_bounds__(AT) attend_kernel(const __grid_constant__ Atte
                         const float4 z = *reinterpret_cast<const float4*>(om + (w * RW + r) * D + d);
                         y.x += z.x * f, y.y += z.y * f, y.z += z.z * f, y.w += z.w * f;
                     }
-                    put(r, d, y.x, y.y, y.z, y.w, mm, ll, d == 0);
+                    put(r, d, y, mm, ll, d == 0);
                 }
             } else {
-                // each warp owns its rows: straight from registers
 #pragma unroll
-                for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-                    for (int hf = 0; hf < 2; ++hf) {
-                        const int r = wrow + mt * 16 + (lane >> 2) + hf * 8;
-                        const bool ok = r < nrows;
-                        // a quad's values of 16 columns, regrouped so that each lane has four in a row
-#pragma unroll
-                        for (int dt = 0; dt < D / 16; ++dt) {
-                            float y[4];
-                            if constexpr (F8) {
-                                y[0] = o[mt][2 * dt][hf * 2], y[1] = o[mt][2 * dt + 1][hf * 2];
-                                y[2] = o[mt][2 * dt][hf * 2 + 1], y[3] = o[mt][2 * dt + 1][hf * 2 + 1];
-                            } else {
-                                // lanes 0,1 of a quad take columns 0-7 of the 16, lanes 2,3 columns 8-15
-                                const float a0 = o[mt][2 * dt][hf * 2], a1 = o[mt][2 * dt][hf * 2 + 1];
-                                const float b0 = o[mt][2 * dt + 1][hf * 2], b1 = o[mt][2 * dt + 1][hf * 2 + 1];
-                                const int q4 = lane & 3, src = (lane & ~3) | ((q4 & 1) * 2);
-                                const float a0l = __shfl_sync(0xffffffffu, a0, src), a1l = __shfl_sync(0xffffffffu, a1, src);
-                                const float a0h = __shfl_sync(0xffffffffu, a0, src + 1), a1h = __shfl_sync(0xffffffffu, a1, src + 1);
-                                const float b0l = __shfl_sync(0xffffffffu, b0, src), b1l = __shfl_sync(0xffffffffu, b1, src);
-                                const float b0h = __shfl_sync(0xffffffffu, b0, src + 1), b1h = __shfl_sync(0xffffffffu, b1, src + 1);
-                                const bool second = q4 >= 2;
-                                y[0] = second ? b0l : a0l, y[1] = second ? b1l : a1l;
-                                y[2] = second ? b0h : a0h, y[3] = second ? b1h : a1h;
-                            }
-                            const int d = dt * 16 + (lane & 3) * 4;
-                            if (ok) put(r, d, y[0], y[1], y[2], y[3], m[mt][hf], l[mt][hf], d == 0);
-                        }
+                for (int n = 0; n < RN; ++n) {
+                    store(n, warp * 8);
+                    __syncwarp();
+                    for (int i = lane; i < 8 * (D / 4); i += 32) {
+                        const int r = i / (D / 4), d = (i % (D / 4)) * 4, row = wrow + n * 8 + r;
+                        if (row < nrows)
+                            put(row, d, *reinterpret_cast<const float4*>(om + (warp * 8 + r) * D + d),
+                                oml[(warp * 8 + r) * 2], oml[(warp * 8 + r) * 2 + 1], d == 0);
                     }
+                    __syncwarp();
+                }
             }
         }
     }
@@ -1013,17 +976,17 @@ __global__ void __launch_bounds__(AT) join_kernel(const __grid_constant__ JoinP 
 struct Kind {
     int format;
     bool splitq, many;
-    int mt;
+    int rn;  // groups of 8 rows a warp holds
 };
 struct KindInfo {
     int tile, rows, ctas;  // positions of a tile, rows of an item, CTAs an SM
 };
 
 // A kernel by its template arguments, with what the host has to know of it.
-template <int D, int FMT, bool SPLITQ, bool MANY, int MT>
+template <int D, int FMT, bool SPLITQ, bool MANY, int RN>
 int attend_run(const AttendP* p, KindInfo* info, int grid, bool after, cudaStream_t s) {
-    using S = Shape<D, FMT, SPLITQ, MANY, MT>;
-    auto kern = attend_kernel<D, FMT, SPLITQ, MANY, MT>;
+    using S = Shape<D, FMT, SPLITQ, MANY, RN>;
+    auto kern = attend_kernel<D, FMT, SPLITQ, MANY, RN>;
     if (info) {
         info->tile = S::TILE;
         info->rows = S::ROWS;
@@ -1046,10 +1009,11 @@ int attend_run(const AttendP* p, KindInfo* info, int grid, bool after, cudaStrea
 
 template <int D, int FMT, bool SPLITQ>
 int attend_pick(const Kind& k, const AttendP* p, KindInfo* info, int grid, bool after, cudaStream_t s) {
-    if (k.many) return attend_run<D, FMT, SPLITQ, true, 1>(p, info, grid, after, s);
+    if (k.many) return attend_run<D, FMT, SPLITQ, true, 2>(p, info, grid, after, s);
     if constexpr (D <= 128) {
-        if (k.mt == 2) return attend_run<D, FMT, SPLITQ, false, 2>(p, info, grid, after, s);
+        if (k.rn == 4) return attend_run<D, FMT, SPLITQ, false, 4>(p, info, grid, after, s);
     }
+    if (k.rn == 2) return attend_run<D, FMT, SPLITQ, false, 2>(p, info, grid, after, s);
     return attend_run<D, FMT, SPLITQ, false, 1>(p, info, grid, after, s);
 }
 
