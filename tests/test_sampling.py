@@ -273,3 +273,28 @@ def test_sampled_decode_loop():
     assert loop.tokens()[0] == [int(t[0]) for t in loop.emitted]
     with pytest.raises(ValueError):
         sampling.SampledLoop(model, fresh(), first, [ctx] * B, cfg["vocab"], temperature=[1.0] * 3)
+
+
+@gpu
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_borders_that_fit_no_list(dtype):
+    """Long runs of equal and nearly equal logits, large k, and one thread's share of the row holding all that counts."""
+    V = 40000
+    g = torch.Generator(device="cuda").manual_seed(1)
+    x = torch.zeros((8, V), device="cuda")
+    x[1] = torch.randn(V, generator=g, device="cuda") * 1e-4        # all in one bin
+    x[2] = torch.randn(V, generator=g, device="cuda")
+    x[3] = torch.randint(0, 3, (V,), generator=g, device="cuda").float()
+    x[4, 20000:] = -math.inf
+    x[5] = torch.linspace(5, -5, V, device="cuda")                  # sorted: the largest lie side by side
+    x[6, ::4096] = 3.0                                              # the largest at one stride
+    x[7] = -torch.arange(V, device="cuda").float() / 7
+    x = x.to(dtype)
+    u = torch.rand(8, generator=g, device="cuda")
+    for k in (0, 3, 1500, 9999, 30000):
+        for p in (1.0, 0.5, 0.97):
+            check(x, u, floats(*[0.9] * 8), ints(*[k] * 8), floats(*[p] * 8), floats(0, 0, 0, 0.2, 0, 0, 0.01, 0.001))
+    # equal logits: exact counts and tokens
+    tok, _, kept = sampling.sample(x[:1].repeat(4, 1), floats(0, 0.5, 0.999999, 0.999999), top_k=ints(0, 9000, 9000, 9000),
+                                   top_p=floats(0.5, 1.0, 0.5, 1.0), return_details=True)
+    assert kept.tolist() == [20000, 9000, 4500, 9000] and tok.tolist() == [0, 4500, 4499, 8999]
