@@ -13,22 +13,25 @@
 // number, the distance of the token's ordered bit pattern from the row's
 // largest above its index. Nothing is sorted but short lists:
 //   top-k  the k-th largest of the threads' own maxima bounds the k-th logit
-//          from below (to a bin of 1/8 octave); the few tokens above go to a
-//          list in one CTA, which ranks them and does all the rest.
+//          from below (to one of 512 equal bins); the few tokens above go to
+//          a list in one CTA, which ranks them and does all the rest.
 //   top-p  one pass sums all weights; a token lighter than (1 - p) sum / V
-//          cannot be kept, the others fill a histogram of masses (1/8 octave);
-//          the bin where the mass reaches p goes to the list, which gives the
-//          last rank kept.
+//          cannot be kept, the others fill a histogram of masses, 512 bins
+//          between that bound and the largest logit. Tokens above the bin
+//          where the mass reaches p are kept, the bin's own go to a list,
+//          which gives the last rank kept.
 //   Where a list would not fit (long runs of nearly equal logits, a large k),
-//   the border is searched by histograms over 12, 12 and 8 bits of the
+//   the border is searched by histograms over 9, 9, 9 and 5 bits of the
 //   distance, and what is left at one exact value are ties, taken by index.
-// Then the kept weights are summed a warp a stretch of tokens, and the warp
-// whose stretch u falls into walks it.
+// The kept weights are summed a warp a stretch of tokens, and the warp whose
+// stretch u falls into walks it.
 //
 // A row is one thread-block cluster of C CTAs: each keeps its slice of the row
 // in shared memory as it came, so the logits are read from HBM once however
 // many passes follow; sums, histograms and lists meet through distributed
-// shared memory.
+// shared memory. A meeting (write to the others, cluster barrier) costs about
+// 2500 cycles, as much as a pass: a row takes 2 (no filter), 3 (top-k) or 4
+// (top-p) of them, and every CTA works out what it can by itself.
 #include <cooperative_groups.h>
 
 #include <type_traits>
@@ -42,8 +45,8 @@ namespace cg = cooperative_groups;
 
 constexpr int ST = 512;        // threads of a CTA
 constexpr int SW = ST / 32;
-constexpr int BINS = 4096;     // histogram bins (12 bits a level)
-constexpr int LIST = BINS;     // ranks a list holds
+constexpr int BINS = ST;       // histogram bins, one a thread
+constexpr int LIST = 1024;     // ranks a list holds: ordering more costs more than further histograms
 constexpr int MAXC = 8;        // CTAs of a cluster
 constexpr int MAX_SLICE_B = 180224;  // bytes of a slice of logits: 176 KB
 
@@ -61,19 +64,22 @@ struct SampleP {
     int V, slice;
 };
 
+// Written by one CTA for another only where it says so; each such place is
+// written once, or alternates, so that a late reader is never overtaken.
 struct Shared {
-    union {
-        u64 hist[BINS];     // masses, or counts
-        u64 list[LIST];     // ranks
-    };
+    unsigned limb[3][BINS], number[BINS];  // a histogram being filled: masses in 14-bit limbs, counts
+    u64 mass[2][BINS];                     // complete ones, read by the cluster
+    unsigned count[2][BINS];
+    u64 list[LIST];                        // ranks, from all CTAs
+    u64 part[2][MAXC];                     // totals of each CTA, from it
+    u64 sums[MAXC * SW];                   // kept mass of every warp's stretch, from its CTA
+    unsigned kept[MAXC];                   // kept tokens of each CTA, from it
+    unsigned top[MAXC], low[MAXC], low_max[MAXC], bad[MAXC];  // what each CTA saw, from it
     u64 warp_sum[SW];
-    u64 part[MAXC];         // a total of each CTA of the cluster, written by that CTA
-    u64 cross_before;       // a level's result, written by the CTA that has it
-    u64 last;               // the last rank kept
-    unsigned cross_bin;
-    unsigned top, argmax, bad;
-    unsigned kept[MAXC];
-    unsigned list_n;
+    u64 cross_before, last;
+    unsigned cross_bin, cross_count;
+    unsigned argmax, list_n;
+    unsigned my_top, my_low, my_low_max, my_bad, my_kept;
 };
 
 // order-preserving unsigned image of a float (no NaN; -0 equals +0)
@@ -123,6 +129,19 @@ __device__ __forceinline__ u64 fixed(float w) {
     return s.value();
 }
 
+// f t (0 <= f < 1) in whole numbers, rounded down, or up. Integers: 64-bit
+// floating point runs at 1/64 of the 32-bit rate here.
+__device__ __forceinline__ u64 part_of(float f, u64 t, bool up) {
+    const unsigned b = __float_as_uint(f), ex = b >> 23;
+    const unsigned man = ex ? (b & 0x7fffffu) | 0x800000u : b;
+    const int s = 150 - (int)(ex ? ex : 1u);  // f = man / 2^s, s >= 24
+    const u64 hi = __umul64hi(t, man), lo = t * man;
+    if (s >= 128) return up && (hi | lo);
+    const u64 q = s < 64 ? hi << (64 - s) | lo >> s : s == 64 ? hi : hi >> (s - 64);
+    const bool rest = s < 64 ? (lo << (64 - s)) != 0 : lo != 0 || (s > 64 && (hi << (128 - s)) != 0);
+    return q + (up && rest);
+}
+
 __device__ __forceinline__ u64 warp_incl(u64 v) {
     const int lane = threadIdx.x & 31;
 #pragma unroll
@@ -149,58 +168,51 @@ __device__ u64 block_excl(u64 v, u64* warp_sum, u64& total) {
     return before + inc - v;
 }
 
-// The cluster's sum of one number a thread, and the sum over the threads before
-// this one. The next call overwrites the parts: a cluster barrier lies between
-// any two.
-__device__ u64 cluster_sum(cg::cluster_group& cl, Shared& sh, int C, int rank, u64 v, u64& before) {
-    u64 mine;
-    before = block_excl(v, sh.warp_sum, mine);
-    if ((int)threadIdx.x < C) cl.map_shared_rank(sh.part, threadIdx.x)[rank] = mine;
-    cl.sync();
-    u64 total = 0;
-    for (int c = 0; c < C; ++c) {
-        if (c == rank) before += total;
-        total += sh.part[c];
-    }
-    return total;
+// A token's weight (below 2^43) into a bin: limbs of 14 bits, whose 32-bit
+// sums hold 2^18 tokens, so that no atomic's result is waited for.
+__device__ __forceinline__ void tally(Shared& sh, int bin, u64 w) {
+    const unsigned a = (unsigned)w & 0x3fffu, b = (unsigned)(w >> 14) & 0x3fffu, c = (unsigned)(w >> 28);
+    if (a) atomicAdd(&sh.limb[0][bin], a);
+    if (b) atomicAdd(&sh.limb[1][bin], b);
+    if (c) atomicAdd(&sh.limb[2][bin], c);
+    atomicAdd(&sh.number[bin], 1u);
 }
 
-// One level of the search over the cluster's histograms: the bin at which the
-// running sum, `before` in front of bin 0, reaches `target`; `before` becomes
-// the sum in front of that bin.
-__device__ unsigned find_bin(cg::cluster_group& cl, Shared& sh, int C, int rank, u64& before, u64 target) {
-    cl.sync();  // every CTA's histogram is complete
-    const int per = BINS / C, each = per / ST;  // bins of this CTA, of a thread
-    u64 mine = 0, bins[BINS / ST];
-    const int b0 = rank * per + threadIdx.x * each;
-#pragma unroll
-    for (int i = 0; i < BINS / ST; ++i) {
-        bins[i] = 0;
-        if (i < each)
-            for (int c = 0; c < C; ++c) bins[i] += cl.map_shared_rank(sh.hist, c)[b0 + i];
-        mine += bins[i];
-    }
-    u64 at;
-    cluster_sum(cl, sh, C, rank, mine, at);  // its barrier: histograms have been read
-    u64 run = before + at;
-#pragma unroll
-    for (int i = 0; i < BINS / ST; ++i) {
-        if (run < target && run + bins[i] >= target) {
-            for (int c = 0; c < C; ++c) {
-                *cl.map_shared_rank(&sh.cross_bin, c) = (unsigned)(b0 + i);
-                *cl.map_shared_rank(&sh.cross_before, c) = run;
-            }
-        }
-        run += bins[i];
-    }
-    cl.sync();  // the result is here
-    before = sh.cross_before;
-    return sh.cross_bin;
-}
-
-__device__ __forceinline__ void clear_hist(Shared& sh) {
-    for (int i = threadIdx.x; i < BINS; i += ST) sh.hist[i] = 0;
+struct Found {
+    int bin;         // -1: the total does not reach the target
+    u64 before;      // in front of the bin
+    unsigned count;  // tokens in it
+    u64 total;
+};
+// The bin of the cluster's histogram at which the running sum (of masses, or
+// of counts), `before` in front of bin 0, reaches the target; every CTA finds
+// it by itself from all CTAs' bins. `turn` alternates. The histogram is empty again.
+__device__ Found find_bin(cg::cluster_group& cl, Shared& sh, int C, int turn, bool by_count, u64 before, u64 target) {
+    const int t = threadIdx.x;
     __syncthreads();
+    sh.mass[turn][t] = ((u64)sh.limb[2][t] << 28) + ((u64)sh.limb[1][t] << 14) + sh.limb[0][t];
+    sh.count[turn][t] = sh.number[t];
+    sh.limb[0][t] = sh.limb[1][t] = sh.limb[2][t] = sh.number[t] = 0;
+    if (t == 0) sh.cross_bin = 0xffffffffu;
+    cl.sync();
+    u64 m = 0;
+    unsigned n = 0;
+#pragma unroll
+    for (int c = 0; c < MAXC; ++c)  // all at once: each is a round trip through the cluster
+        if (c < C) {
+            if (!by_count) m += cl.map_shared_rank(sh.mass[turn], c)[t];
+            n += cl.map_shared_rank(sh.count[turn], c)[t];
+        }
+    const u64 v = by_count ? n : m;
+    Found f;
+    const u64 run = before + block_excl(v, sh.warp_sum, f.total);
+    if (run < target && run + v >= target) sh.cross_bin = t, sh.cross_before = run, sh.cross_count = n;
+    __syncthreads();
+    f.bin = (int)sh.cross_bin;
+    f.before = sh.cross_before;
+    f.count = sh.cross_count;
+    __syncthreads();
+    return f;
 }
 
 // v[0 .. n) ascending; `n2` a power of two not below n, padded with ~0 here
@@ -239,7 +251,7 @@ __device__ void order_list(u64* v, int n) {
 
 // Bound: one read of the logits from HBM, then passes over shared memory of 4
 // to 25 operations a token (the largest: summing all weights). Small calls are
-// the latency of 5 to 12 cluster barriers.
+// the latency of the cluster's meetings.
 template <int DT>
 __global__ void __launch_bounds__(ST, 2) sample_kernel(const SampleP p) {
     typedef typename std::conditional<DT == MK_DT_F32, float, uint16_t>::type Raw;
@@ -272,14 +284,22 @@ __global__ void __launch_bounds__(ST, 2) sample_kernel(const SampleP p) {
         }
     };
 
-    // ---- the slice into shared memory; this thread's largest logit
-    if (tid == 0) sh.top = 0, sh.bad = 0, sh.argmax = 0xffffffffu, sh.list_n = 0;
+    // ---- the slice into shared memory; the largest and the least unmasked logit
+    if (tid == 0) {
+        sh.my_top = 0, sh.my_low = sh.my_low_max = 0xffffffffu, sh.my_bad = 0, sh.my_kept = 0;
+        sh.argmax = 0xffffffffu, sh.list_n = 0;
+    }
+    sh.limb[0][tid] = sh.limb[1][tid] = sh.limb[2][tid] = sh.number[tid] = 0;
     __syncthreads();
-    float big = -INFINITY;
+    float big = -INFINITY, small = INFINITY;
     bool bad = false;
+    auto look = [&](float x) {
+        big = fmaxf(big, x);
+        small = fminf(small, x == -INFINITY ? INFINITY : x);
+        bad |= !(x < INFINITY);  // NaN or +infinity
+    };
     {
         const Raw* src = (const Raw*)p.logits + row * p.row_stride + i0;
-        const Raw fill = DT == MK_DT_F32 ? (Raw)0 : DT == MK_DT_BF16 ? (Raw)0xff80 : (Raw)0xfc00;  // -infinity
         Raw* raw = reinterpret_cast<Raw*>(xs);
         const int whole = (uintptr_t)src % 16 == 0 ? n / E : 0;
 #pragma unroll 4
@@ -289,43 +309,78 @@ __global__ void __launch_bounds__(ST, 2) sample_kernel(const SampleP p) {
             float x[E];
             unpack(x, a);
 #pragma unroll
-            for (int e = 0; e < E; ++e) {
-                big = fmaxf(big, x[e]);
-                bad |= !(x[e] < INFINITY);  // NaN or +infinity
-            }
+            for (int e = 0; e < E; ++e) look(x[e]);
         }
         for (int i = whole * E + tid; i < nv * E; i += ST) {
-            if (i < n) {
-                const Raw a = src[i];
-                raw[i] = a;
-                float x;
-                if constexpr (DT == MK_DT_F32) x = a;
-                else x = value(a);
-                big = fmaxf(big, x);
-                bad |= !(x < INFINITY);
-            } else if constexpr (DT == MK_DT_F32) {
-                raw[i] = -INFINITY;  // the last vector's rest is masked
+            if constexpr (DT == MK_DT_F32) {
+                raw[i] = i < n ? src[i] : -INFINITY;  // the last vector's rest is masked
+                look(raw[i]);
             } else {
-                raw[i] = fill;
+                raw[i] = i < n ? src[i] : DT == MK_DT_BF16 ? (Raw)0xff80 : (Raw)0xfc00;
+                look(value(raw[i]));
             }
         }
     }
     {
-        unsigned k = key_of(big);
-#pragma unroll
-        for (int o = 16; o; o >>= 1) k = max(k, __shfl_xor_sync(0xffffffffu, k, o));
-        if (lane == 0) atomicMax(&sh.top, k);
-        if (bad) sh.bad = 1;
+        // the least of the threads' largest bounds top-k's search; threads without a token do not count
+        const unsigned k = key_of(big), masked_key = key_of(-INFINITY);
+        const unsigned a = __reduce_max_sync(0xffffffffu, k);
+        const unsigned b = __reduce_min_sync(0xffffffffu, small < INFINITY ? key_of(small) : 0xffffffffu);
+        const unsigned c = __reduce_min_sync(0xffffffffu, k > masked_key ? k : 0xffffffffu);
+        if (lane == 0) {
+            atomicMax(&sh.my_top, a);
+            atomicMin(&sh.my_low, b);
+            atomicMin(&sh.my_low_max, c);
+        }
+        if (bad) sh.my_bad = 1;
     }
-    cl.sync();
-    unsigned top = 0, any_bad = 0;
+    cl.sync();  // every CTA runs, and has its numbers
+    if (tid < C) {
+        sh.top[tid] = *cl.map_shared_rank(&sh.my_top, tid);
+        sh.low[tid] = *cl.map_shared_rank(&sh.my_low, tid);
+        sh.low_max[tid] = *cl.map_shared_rank(&sh.my_low_max, tid);
+        sh.bad[tid] = *cl.map_shared_rank(&sh.my_bad, tid);
+    }
+    __syncthreads();
+    unsigned top = 0, low_key = 0xffffffffu, low_max_key = 0xffffffffu, any_bad = 0;
     for (int c = 0; c < C; ++c) {
-        top = max(top, *cl.map_shared_rank(&sh.top, c));
-        any_bad |= *cl.map_shared_rank(&sh.bad, c);
+        top = max(top, sh.top[c]);
+        low_key = min(low_key, sh.low[c]);
+        low_max_key = min(low_max_key, sh.low_max[c]);
+        any_bad |= sh.bad[c];
     }
     const float m = value_of(top);
     const float T = p.temperature ? p.temperature[row] : 1.0f;
+    const float least = p.min_p ? p.min_p[row] : 0.0f;
     const bool none = any_bad || m == -INFINITY;  // a NaN, a +infinity, or nothing but masked tokens
+    if (none || !(T > 0.f) || !(least <= 1.f)) {
+        // nothing to draw from, or only the first rank: the lowest index of the largest logit
+        if (!none && sh.my_top == top) {
+            for (int v = tid; v < nv; v += ST) {
+                float x[E];
+                unpack(x, xs[v]);
+#pragma unroll
+                for (int e = 0; e < E; ++e)
+                    if (x[e] == m) atomicMin(cl.map_shared_rank(&sh.argmax, 0), (unsigned)(i0 + v * E + e));
+            }
+        }
+        cl.sync();
+        if (rank == 0 && tid == 0) {
+            p.tokens[row] = none ? -1 : (int)sh.argmax;
+            if (p.probs) p.probs[row] = none ? 0.f : 1.f;
+            if (p.kept) p.kept[row] = none ? 0 : 1;
+        }
+        return;
+    }
+    const Weight W = {m, T, __frcp_rn(T), T > 0x1p-60f && T < 0x1p60f};
+    const int k_in = p.top_k ? p.top_k[row] : 0;
+    const float p_in = p.top_p ? p.top_p[row] : 1.0f;
+    const bool by_k = k_in > 0 && k_in < p.V, by_p = p_in < 1.0f;
+    const float u = fminf(fmaxf(p.u[row], 0.f), 0x1.fffffep-1f);
+    const unsigned masked = top - key_of(-INFINITY);
+    auto mass_target = [&](u64 total) {  // the mass that ends top-p; at least 1: the first rank always stays
+        return max(1ull, part_of(fmaxf(p_in, 0.f), total, true));
+    };
 
     // a warp's stretch of the slice, in vectors
     const int v0 = (int)((long long)nv * warp / SW), v1 = (int)((long long)nv * (warp + 1) / SW);
@@ -337,304 +392,336 @@ __global__ void __launch_bounds__(ST, 2) sample_kernel(const SampleP p) {
             for (int e = 0; e < E; ++e) f(x[e], i0 + v * E + e);
         }
     };
-
-    // the lowest index of the largest logit: rank 0, which always stays
-    if (!none && sh.top == top) {
-        for (int v = tid; v < nv; v += ST) {
+    // equal bins from the largest logit down to `edge`; lower ones fall into the last
+    struct Linear {
+        float m, scale;
+        __device__ int operator()(float x) const { return (int)fminf((m - x) * scale, (float)(BINS - 1)); }
+    };
+    auto bins_down_to = [&](float edge) {
+        const float s = (float)BINS / (m - edge);
+        return Linear{m, s < 1e30f ? s : 0.f};  // no room between the two: one bin
+    };
+    // The ranks of tokens that `pick` takes, to the lists of CTAs [0, to). All warps call it; the number is in
+    // CTA 0's list_n after the next barrier (those that do not fit counted).
+    auto collect = [&](int to, auto pick) {
+        unsigned* count = cl.map_shared_rank(&sh.list_n, 0);
+        for (int v = v0; v < v1; v += 32) {
             float x[E];
-            unpack(x, xs[v]);
+            unsigned in = 0;
+            if (v + lane < v1) {
+                unpack(x, xs[v + lane]);
+#pragma unroll
+                for (int e = 0; e < E; ++e) in |= (unsigned)pick(x[e], i0 + (v + lane) * E + e) << e;
+            }
+            if (!__any_sync(0xffffffffu, in)) continue;
+            // one place for all of the warp's
+            const unsigned mine = __popc(in);
+            unsigned at = mine;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const unsigned a = __shfl_up_sync(0xffffffffu, at, o);
+                if (lane >= o) at += a;
+            }
+            unsigned base = 0;
+            if (lane == 31) base = atomicAdd(count, at);
+            at += __shfl_sync(0xffffffffu, base, 31) - mine;
 #pragma unroll
             for (int e = 0; e < E; ++e)
-                if (x[e] == m) atomicMin(&sh.argmax, (unsigned)(i0 + v * E + e));
+                if (in >> e & 1u) {
+                    const u64 r = (u64)(top - key_of(x[e])) << 32 | (unsigned)(i0 + (v + lane) * E + e);
+                    if (at < LIST)
+                        for (int c = 0; c < to; ++c) cl.map_shared_rank(sh.list, c)[at] = r;
+                    ++at;
+                }
         }
-    }
-    cl.sync();
-    unsigned argmax = 0xffffffffu;
-    for (int c = 0; c < C; ++c) argmax = min(argmax, *cl.map_shared_rank(&sh.argmax, c));
-    if (none || !(T > 0.f)) {
-        if (rank == 0 && tid == 0) {
-            p.tokens[row] = none ? -1 : (int)argmax;
-            if (p.probs) p.probs[row] = none ? 0.f : 1.f;
-            if (p.kept) p.kept[row] = none ? 0 : 1;
+    };
+    int turn = 0;
+    // The rank at which a running sum over ranks (of counts, or of masses of tokens up to `up_to`) reaches the
+    // target, by histograms over the bits of the distance, then by index among equal logits. All CTAs call it; the
+    // sum reaches the target.
+    auto search = [&](bool by_count, u64 target, u64 up_to) {
+        const float xk = value_of(top - (unsigned)(up_to >> 32));
+        const unsigned ik = (unsigned)up_to;
+        u64 before = 0;
+        unsigned prefix = 0;
+#pragma unroll 1
+        for (int l = 0; l < 4; ++l) {
+            const int lo = l == 3 ? 0 : 23 - 9 * l, up = l == 0 ? 32 : 32 - 9 * l;
+            each([&](float x, int i) {
+                const unsigned d = top - key_of(x);
+                if ((l == 0 || (d >> up) == prefix) && (x > xk || (x == xk && (unsigned)i <= ik)))
+                    tally(sh, (d >> lo) & ((1u << (up - lo)) - 1), by_count ? 0 : fixed(W(x)));
+            });
+            const Found f = find_bin(cl, sh, C, turn, by_count, before, target);
+            turn ^= 1;
+            prefix = prefix << (up - lo) | (unsigned)f.bin;
+            before = f.before;
         }
-        cl.sync();  // no CTA leaves while another reads its shared memory
-        return;
-    }
-    const Weight W = {m, T, __frcp_rn(T), T > 0x1p-60f && T < 0x1p60f};
-    const int k_in = p.top_k ? p.top_k[row] : 0;
-    const float p_in = p.top_p ? p.top_p[row] : 1.0f;
-    const float least = p.min_p ? p.min_p[row] : 0.0f;
-    const bool by_k = k_in > 0 && k_in < p.V, by_p = p_in < 1.0f;
-    const float u = fminf(fmaxf(p.u[row], 0.f), 0x1.fffffep-1f);
-    const unsigned masked = top - key_of(-INFINITY);
-    auto mass_target = [&](u64 total) {  // the mass that ends top-p; at least 1: the first rank always stays
-        return max(1ull, (u64)ceil(fmax((double)p_in, 0.0) * (double)total));
-    };
-    // the least logit at a distance of at most d
-    auto at_distance = [&](unsigned d) { return value_of(top - min(d, masked)); };
-    // Ranks of the unmasked tokens with low <= x < high, to the first CTA's list; returns how many there are
-    // (those that do not fit counted).
-    auto collect = [&](float low, float high) {
-        u64* list = cl.map_shared_rank(sh.list, 0);
-        unsigned* count = cl.map_shared_rank(&sh.list_n, 0);
-        each([&](float x, int i) {
-            if (x >= low && x < high && x > -INFINITY) {
-                const unsigned at = atomicAdd(count, 1u);
-                if (at < LIST) list[at] = (u64)(top - key_of(x)) << 32 | (unsigned)i;
-            }
-        });
-        cl.sync();
-        const unsigned got = *count;
-        cl.sync();  // read everywhere: the first CTA may go on, and leave
-        return got;
-    };
-    // The token at place `quota` (from 1) among those exactly at distance d, by index: its rank.
-    auto nth_tie = [&](unsigned d, u64 quota) {
-        const float x0 = value_of(top - d);
+        // equal logits: their first `want`, in index order
+        const float x0 = value_of(top - prefix);
+        const u64 w = by_count ? 1 : fixed(W(x0));
         unsigned c = 0;
         each([&](float x, int) { c += x == x0; });
         c = __reduce_add_sync(0xffffffffu, c);
-        u64 at;
-        const u64 all = cluster_sum(cl, sh, C, rank, lane == 0 ? c : 0, at);
-        // lanes past 0 come after their warp's count
+        u64 mine, all = 0, at = block_excl(lane == 0 ? c : 0, sh.warp_sum, mine);
+        if (tid < C) cl.map_shared_rank(sh.part[turn], tid)[rank] = mine;
+        cl.sync();
         at = __shfl_sync(0xffffffffu, at, 0);
-        const u64 want = min(quota, all);
+        for (int r = 0; r < C; ++r) {
+            if (r == rank) at += all;
+            all += sh.part[turn][r];
+        }
+        const u64 want = min((target - before + w - 1) / w, all);
         if (at < want && at + c >= want) {  // one warp of the cluster
             u64 seen = at;
             for (int v = v0; v < v1 && seen < want; v += 32) {
                 float x[E];
                 const bool in = v + lane < v1;
                 if (in) unpack(x, xs[v + lane]);
-                unsigned mine = 0;
+                unsigned some = 0;
 #pragma unroll
-                for (int e = 0; e < E; ++e) mine += in && x[e] == x0;
-                u64 before = seen + warp_incl(mine) - mine;
+                for (int e = 0; e < E; ++e) some += in && x[e] == x0;
+                u64 place = seen + warp_incl(some) - some;
 #pragma unroll
                 for (int e = 0; e < E; ++e)
-                    if (in && x[e] == x0 && ++before == want)
+                    if (in && x[e] == x0 && ++place == want)
                         for (int r = 0; r < C; ++r)
-                            *cl.map_shared_rank(&sh.last, r) = (u64)d << 32 | (unsigned)(i0 + (v + lane) * E + e);
-                seen += __reduce_add_sync(0xffffffffu, mine);
+                            *cl.map_shared_rank(&sh.last, r) = (u64)prefix << 32 | (unsigned)(i0 + (v + lane) * E + e);
+                seen += __reduce_add_sync(0xffffffffu, some);
             }
         }
         cl.sync();
-        return sh.last;
+        turn ^= 1;
+        return min(sh.last, up_to);
     };
 
     // kept: ranks up to `last` (and weights of at least min_p)
     u64 last = ((u64)masked << 32) - 1;  // masked tokens are never kept
-    bool listed = false;                 // rank 0's list holds all tokens top-k keeps, and maybe more
     if (by_k) {
-        const int holders = min(p.V, C * ST);
-        unsigned bin = masked >> 20;
-        u64 before = 0;
-        clear_hist(sh);
-        if (k_in <= holders / 4) {
-            // at least k tokens lie at or above the k-th largest of the threads' maxima
-            if (big > -INFINITY) atomicAdd(reinterpret_cast<unsigned*>(&sh.hist[(top - key_of(big)) >> 20]), 1u);
+        // at least k tokens lie at or above the k-th largest of the threads' maxima; a k beyond what those
+        // tell is sought among all tokens
+        const bool by_threads = k_in <= min(p.V, C * ST) / 4;
+        const float edge = value_of(by_threads ? low_max_key : low_key);
+        const Linear bin = bins_down_to(edge);
+        if (by_threads) {
+            if (big > -INFINITY) atomicAdd(&sh.number[bin(big)], 1u);
         } else {
             each([&](float x, int) {
-                if (x > -INFINITY) atomicAdd(reinterpret_cast<unsigned*>(&sh.hist[(top - key_of(x)) >> 20]), 1u);
+                if (x > -INFINITY) atomicAdd(&sh.number[bin(x)], 1u);
             });
         }
-        if (tid == 0) sh.cross_bin = masked >> 20;  // fewer than k: every unmasked token
-        bin = find_bin(cl, sh, C, rank, before, (u64)k_in);
-        const unsigned got = collect(at_distance(bin << 20 | 0xfffffu), INFINITY);
-        listed = got <= LIST;
-        if (!listed) {
-            // the k-th rank by three levels of counts
-            u64 ahead = 0;
-            unsigned prefix = 0;
-            bool found = true;
-#pragma unroll 1
-            for (int l = 0; l < 3 && found; ++l) {
-                const int lo = l == 0 ? 20 : l == 1 ? 8 : 0, up = l == 0 ? 32 : l == 1 ? 20 : 8;
-                clear_hist(sh);
-                each([&](float x, int) {
-                    const unsigned d = top - key_of(x);
-                    if (x > -INFINITY && (l == 0 || (d >> up) == prefix))
-                        atomicAdd(reinterpret_cast<unsigned*>(&sh.hist[(d >> lo) & ((1u << (up - lo)) - 1)]), 1u);
-                });
-                if (tid == 0) sh.cross_bin = 0xffffffffu;
-                const unsigned b = find_bin(cl, sh, C, rank, ahead, (u64)k_in);
-                found = b != 0xffffffffu;
-                prefix = prefix << (up - lo) | b;
-            }
-            if (found) last = nth_tie(prefix, (u64)k_in - ahead);
+        const Found f = find_bin(cl, sh, C, turn, true, 0, (u64)k_in);
+        turn ^= 1;
+        // With fewer than k of them, top-k may still bind: search(). A bin of all tokens is known to fit or not.
+        bool listed = f.bin >= 0 && (by_threads || f.before + f.count <= LIST);
+        bool binds = f.bin >= 0 || by_threads;
+        if (listed) {
+            collect(1, [&](float x, int) { return x >= edge && bin(x) <= f.bin; });
+            cl.sync();
+            listed = *cl.map_shared_rank(&sh.list_n, 0) <= LIST;
+        } else if (by_threads) {
+            // how many tokens are there at all
+            unsigned c = 0;
+            each([&](float x, int) { c += x > -INFINITY; });
+            u64 mine, all = 0;
+            block_excl(c, sh.warp_sum, mine);
+            if (tid < C) cl.map_shared_rank(sh.part[turn], tid)[rank] = mine;
+            cl.sync();
+            for (int r = 0; r < C; ++r) all += sh.part[turn][r];
+            turn ^= 1;
+            binds = all >= (u64)k_in;
         }
-    }
-
-    if (listed) {
-        // ---- rank 0 has every candidate: the other CTAs are done
-        if (rank == 0) {
-            int n_l = (int)sh.list_n;
-            order_list(sh.list, n_l);
-            n_l = min(n_l, k_in);
-            // running mass in rank order; top-p and min-p both keep a beginning
-            const int each_l = (n_l + ST - 1) / ST, a0 = min(n_l, tid * each_l), a1 = min(n_l, a0 + each_l);
-            u64 mass = 0, total;
-            for (int i = a0; i < a1; ++i) mass += fixed(W(value_of(top - (unsigned)(sh.list[i] >> 32))));
-            u64 run = block_excl(mass, sh.warp_sum, total);
-            const u64 target = by_p ? mass_target(total) : ~0ull;
-            unsigned keeps = 0;
-            for (int i = a0; i < a1; ++i) {
-                const float w = W(value_of(top - (unsigned)(sh.list[i] >> 32)));
-                if (i == 0 || (run < target && w >= least)) ++keeps;
-                run += fixed(w);
-            }
-            u64 n_k;
-            block_excl(keeps, sh.warp_sum, n_k);
-            // in index order now: (index, distance)
-            for (int i = tid; i < (int)n_k; i += ST) sh.list[i] = sh.list[i] << 32 | sh.list[i] >> 32;
-            __syncthreads();
-            order_list(sh.list, (int)n_k);
-            const int each_k = ((int)n_k + ST - 1) / ST, b0 = min((int)n_k, tid * each_k), b1 = min((int)n_k, b0 + each_k);
-            mass = 0;
-            for (int i = b0; i < b1; ++i) mass += fixed(W(value_of(top - (unsigned)sh.list[i])));
-            run = block_excl(mass, sh.warp_sum, total);
-            const u64 pick = (u64)((double)u * (double)total);
-            for (int i = b0; i < b1; ++i) {
-                const float w = W(value_of(top - (unsigned)sh.list[i]));
-                const u64 f = fixed(w);
-                if (run <= pick && run + f > pick) {
-                    p.tokens[row] = (int)(sh.list[i] >> 32);
-                    if (p.probs) p.probs[row] = (float)((double)w * 0x1p42 / (double)total);
+        if (listed) {
+            // ---- CTA 0 has every candidate
+            if (rank == 0) {
+                int n_l = (int)sh.list_n;
+                order_list(sh.list, n_l);
+                n_l = min(n_l, k_in);
+                // running mass in rank order; top-p and min-p both keep a beginning
+                const int each_l = (n_l + ST - 1) / ST, a0 = min(n_l, tid * each_l), a1 = min(n_l, a0 + each_l);
+                u64 mass = 0, total;
+                for (int i = a0; i < a1; ++i) mass += fixed(W(value_of(top - (unsigned)(sh.list[i] >> 32))));
+                u64 run = block_excl(mass, sh.warp_sum, total);
+                const u64 target = by_p ? mass_target(total) : ~0ull;
+                unsigned keeps = 0;
+                for (int i = a0; i < a1; ++i) {
+                    const float w = W(value_of(top - (unsigned)(sh.list[i] >> 32)));
+                    if (run < target && w >= least) ++keeps;
+                    run += fixed(w);
                 }
-                run += f;
+                u64 n_k;
+                block_excl(keeps, sh.warp_sum, n_k);
+                // in index order now: (index, distance)
+                for (int i = tid; i < (int)n_k; i += ST) sh.list[i] = sh.list[i] << 32 | sh.list[i] >> 32;
+                __syncthreads();
+                order_list(sh.list, (int)n_k);
+                const int each_k = ((int)n_k + ST - 1) / ST, b0 = min((int)n_k, tid * each_k),
+                          b1 = min((int)n_k, b0 + each_k);
+                mass = 0;
+                for (int i = b0; i < b1; ++i) mass += fixed(W(value_of(top - (unsigned)sh.list[i])));
+                run = block_excl(mass, sh.warp_sum, total);
+                const u64 pick = part_of(u, total, false);
+                for (int i = b0; i < b1; ++i) {
+                    const float w = W(value_of(top - (unsigned)sh.list[i]));
+                    const u64 f2 = fixed(w);
+                    if (run <= pick && run + f2 > pick) {
+                        p.tokens[row] = (int)(sh.list[i] >> 32);
+                        if (p.probs) p.probs[row] = (float)((double)w * 0x1p42 / (double)total);
+                    }
+                    run += f2;
+                }
+                if (tid == 0 && p.kept) p.kept[row] = (int)n_k;
             }
-            if (tid == 0 && p.kept) p.kept[row] = (int)n_k;
+            cl.sync();  // no CTA leaves while another reads its shared memory
+            return;
         }
-        return;
+        if (binds) last = search(true, (u64)k_in, last);
+        if (tid == 0) sh.list_n = 0;  // for top-p, after the barriers to come
     }
 
-    const float least_x = least > 0.f ? m + T * (logf(fminf(least, 1.f)) - 0.01f) : -INFINITY;  // below: lighter than min_p
+    const float least_x = least > 0.f ? m + T * (logf(least) - 0.01f) : -INFINITY;  // below: lighter than min_p
+    // kept tokens above a bound: `sure` by themselves, or up to `last`
+    float xc = value_of(top - (unsigned)(last >> 32));
+    unsigned ic = (unsigned)last;
+    auto up_to_last = [&](float x, int i) { return x > xc || (x == xc && (unsigned)i <= ic); };
+    Linear bin = {m, 0.f};
+    int border = -1;       // the bin whose tokens are in the list
+    unsigned listed = 0;   // how many
+    u64 before = 0, target = 0;
+    float low_x = -INFINITY;
     if (by_p) {
         // all of top-k's mass
-        const float xk = value_of(top - (unsigned)(last >> 32));
-        const unsigned ik = (unsigned)last;
         Sum s;
         each([&](float x, int i) {
-            if (x > xk || (x == xk && (unsigned)i <= ik)) s.add(W(x));
+            if (up_to_last(x, i)) s.add(W(x));
         });
-        u64 at, before = 0;
-        const u64 total = cluster_sum(cl, sh, C, rank, s.value(), at);
-        const u64 target = mass_target(total);
+        u64 mine, total = 0;
+        block_excl(s.value(), sh.warp_sum, mine);
+        if (tid < C) cl.map_shared_rank(sh.part[turn], tid)[rank] = mine;
+        cl.sync();
+        for (int c = 0; c < C; ++c) total += sh.part[turn][c];
+        turn ^= 1;
+        target = mass_target(total);
         // Tokens lighter than (1 - p) total / V weigh less than (1 - p) total together: at least p total lies
         // before them. Half of that bound, and a hundredth, leave room for roundings.
-        const double light = (1.0 - fmax((double)p_in, 0.0)) * (double)total * 0x1p-43 / (double)p.V;
-        const float low_x = light > 1e-30 ? m + T * (logf((float)light) - 0.01f) : -INFINITY;
-        clear_hist(sh);
+        const float light = (1.f - fmaxf(p_in, 0.f)) * (__ull2float_rn(total) * 0x1p-43f) / (float)p.V;
+        low_x = fmaxf(value_of(low_key), light > 1e-30f ? m + T * (logf(light) - 0.01f) : -INFINITY);
+        bin = bins_down_to(low_x);
         each([&](float x, int i) {
-            if (x >= low_x && (x > xk || (x == xk && (unsigned)i <= ik))) {
-                const u64 w = fixed(W(x));
-                if (w) atomicAdd(&sh.hist[(top - key_of(x)) >> 20], w);
-            }
+            if (x >= low_x && up_to_last(x, i)) tally(sh, bin(x), fixed(W(x)));
         });
-        unsigned prefix = find_bin(cl, sh, C, rank, before, target);
-        const float high = prefix ? at_distance((prefix << 20) - 1) : INFINITY, low = at_distance(prefix << 20 | 0xfffffu);
-        if (tid == 0) sh.list_n = 0;
-        cl.sync();
-        const unsigned got = collect(low, high);  // hist is free: find_bin's barriers are behind
-        if (got <= LIST) {
-            if (rank == 0) {
-                int n_l = (int)got;
-                order_list(sh.list, n_l);
-                const int each_l = (n_l + ST - 1) / ST, a0 = min(n_l, tid * each_l), a1 = min(n_l, a0 + each_l);
-                u64 mass = 0, all;
-                for (int i = a0; i < a1; ++i)
-                    if (sh.list[i] <= last) mass += fixed(W(value_of(top - (unsigned)(sh.list[i] >> 32))));
-                u64 run = before + block_excl(mass, sh.warp_sum, all);
-                for (int i = a0; i < a1; ++i) {
-                    if (sh.list[i] > last) break;
-                    const u64 f = fixed(W(value_of(top - (unsigned)(sh.list[i] >> 32))));
-                    // the last one with less than the target before it
-                    if (run < target && run + f >= target)
-                        for (int r = 0; r < C; ++r) *cl.map_shared_rank(&sh.last, r) = sh.list[i];
-                    run += f;
-                }
-            }
-            cl.sync();
-            last = sh.last;
+        const Found f = find_bin(cl, sh, C, turn, false, 0, target);
+        turn ^= 1;
+        if (f.count <= LIST) {
+            border = f.bin;
+            listed = f.count;
+            before = f.before;
         } else {
-            unsigned p2 = prefix;
-#pragma unroll 1
-            for (int l = 1; l < 3; ++l) {
-                const int lo = l == 1 ? 8 : 0, up = l == 1 ? 20 : 8;
-                clear_hist(sh);
-                each([&](float x, int i) {
-                    const unsigned d = top - key_of(x);
-                    if ((d >> up) == p2 && (x > xk || (x == xk && (unsigned)i <= ik))) {
-                        const u64 w = fixed(W(x));
-                        if (w) atomicAdd(&sh.hist[(d >> lo) & ((1u << (up - lo)) - 1)], w);
-                    }
-                });
-                p2 = p2 << (up - lo) | find_bin(cl, sh, C, rank, before, target);
-            }
-            // ties at the border: as many as have less than the target before
-            // them (their weight is not 0: the bin was found by its mass)
-            const u64 w = fixed(W(value_of(top - p2)));
-            last = min(last, nth_tie(p2, (target - before + w - 1) / w));
+            last = search(false, target, last);
+            xc = value_of(top - (unsigned)(last >> 32));
+            ic = (unsigned)last;
         }
     }
 
-    // ---- the draw: a warp sums its stretch, the one that u falls into walks it
-    const float xc = value_of(top - (unsigned)(last >> 32));
-    const unsigned ic = (unsigned)last;
-    auto weigh = [&](float x, int i, float& w) {
-        if (!(x > xc || (x == xc && (unsigned)i <= ic)) || (x < least_x && i != (int)argmax)) return false;
+    // ---- the draw: a warp sums its stretch's kept weights, all CTAs get all sums (and the list)
+    auto weigh = [&](float x, float& w) {
+        if (x < least_x) return false;
         w = W(x);
-        return w >= least || i == (int)argmax;
+        return w >= least;
     };
     Sum s;
     each([&](float x, int i) {
         float w;
-        if (weigh(x, i, w)) s.add(w);
+        if (up_to_last(x, i) && (border < 0 || (x >= low_x && bin(x) < border)) && weigh(x, w)) s.add(w);
     });
+    if (border >= 0)
+        collect(C, [&](float x, int i) { return x >= low_x && bin(x) == border && up_to_last(x, i); });
     u64 sum = s.value();
-    unsigned count = __reduce_add_sync(0xffffffffu, s.n);
+    const unsigned count = __reduce_add_sync(0xffffffffu, s.n);
 #pragma unroll
     for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-    u64 at, slice_kept;
-    block_excl(lane == 0 ? count : 0, sh.warp_sum, slice_kept);
-    if (tid < C) cl.map_shared_rank(sh.kept, tid)[rank] = (unsigned)slice_kept;
-    cl.sync();  // the parts of an earlier sum have been read
-    const u64 total = cluster_sum(cl, sh, C, rank, lane == 0 ? sum : 0, at);
-    at = __shfl_sync(0xffffffffu, at, 0);
-    // u total lies at or above the running sum of every token before the drawn one
-    const u64 pick = (u64)((double)u * (double)total);
-    if (at <= pick && at + sum > pick) {  // one warp of the cluster
-        const int per = (v1 - v0 + 31) / 32, a0 = min(v1, v0 + lane * per), a1 = min(v1, a0 + per);
-        Sum mine;
-        for (int v = a0; v < a1; ++v) {
-            float x[E], w;
-            unpack(x, xs[v]);
-#pragma unroll
-            for (int e = 0; e < E; ++e)
-                if (weigh(x[e], i0 + v * E + e, w)) mine.add(w);
+    if (lane < C) cl.map_shared_rank(sh.sums, lane)[rank * SW + warp] = sum;
+    if (lane == 0) atomicAdd(&sh.my_kept, count);
+    __syncthreads();
+    if (tid < C) cl.map_shared_rank(sh.kept, tid)[rank] = sh.my_kept;
+    cl.sync();
+    unsigned kept = 0;
+    for (int c = 0; c < C; ++c) kept += sh.kept[c];
+    if (border >= 0) {
+        // the border's tokens in rank order; those kept join their stretches
+        const int n_l = (int)listed;
+        order_list(sh.list, n_l);
+        const int each_l = (n_l + ST - 1) / ST, a0 = min(n_l, tid * each_l), a1 = min(n_l, a0 + each_l);
+        u64 mass = 0, all;
+        for (int i = a0; i < a1; ++i) mass += fixed(W(value_of(top - (unsigned)(sh.list[i] >> 32))));
+        u64 run = before + block_excl(mass, sh.warp_sum, all);
+        unsigned keeps = 0;
+        for (int i = a0; i < a1; ++i) {
+            const float x = value_of(top - (unsigned)(sh.list[i] >> 32));
+            const float w = W(x);
+            const u64 f = fixed(w);
+            if (run < target) {
+                if (run + f >= target || i == n_l - 1) sh.last = sh.list[i];  // the last rank kept
+                if (w >= least) {
+                    const int j = (int)(unsigned)sh.list[i], c = j / p.slice, v = (j - c * p.slice) / E;
+                    const int nvc = (min(p.V, (c + 1) * p.slice) - c * p.slice + E - 1) / E;
+                    // the warp whose stretch holds vector v of CTA c: floor(nvc w / SW) <= v
+                    int w8 = (int)(((long long)v * SW + SW - 1) / nvc);
+                    while ((int)((long long)nvc * w8 / SW) > v) --w8;
+                    while ((int)((long long)nvc * (w8 + 1) / SW) <= v) ++w8;
+                    atomicAdd(&sh.sums[c * SW + w8], f);
+                    ++keeps;
+                }
+            }
+            run += f;
         }
-        u64 run = mine.value();
-        run = at + warp_incl(run) - run;
-        if (run <= pick && run + mine.value() > pick) {
-            for (int v = a0; v < a1; ++v) {
-                float x[E], w;
-                unpack(x, xs[v]);
+        u64 n_k;
+        block_excl(keeps, sh.warp_sum, n_k);
+        kept += (unsigned)n_k;
+        last = sh.last;
+        xc = value_of(top - (unsigned)(last >> 32));
+        ic = (unsigned)last;
+    }
+    // running sums over all stretches of the row, in index order
+    u64 total;
+    u64 at = block_excl(tid < C * SW ? sh.sums[tid] : 0, sh.warp_sum, total);
+    // u total lies at or above the running sum of every token before the drawn one
+    const u64 pick = part_of(u, total, false);
+    if (tid < C * SW && at <= pick && at + sh.sums[tid] > pick) sh.cross_bin = tid, sh.cross_before = at;
+    __syncthreads();
+    if ((int)sh.cross_bin == rank * SW + warp) {  // one warp of the cluster
+        u64 seen = sh.cross_before;
+        for (int v = v0; v < v1 && seen <= pick; v += 32) {
+            const int i = i0 + (v + lane) * E;
+            float x[E], w;
+            Sum mine;
+            if (v + lane < v1) {
+                unpack(x, xs[v + lane]);
+#pragma unroll
+                for (int e = 0; e < E; ++e)
+                    if (up_to_last(x[e], i + e) && weigh(x[e], w)) mine.add(w);
+            }
+            const u64 f = mine.value(), incl = warp_incl(f);
+            u64 run = seen + incl - f;
+            seen += __shfl_sync(0xffffffffu, incl, 31);
+            if (run <= pick && run + f > pick) {  // one lane
+#pragma unroll 1
                 for (int e = 0; e < E; ++e) {
-                    if (!weigh(x[e], i0 + v * E + e, w)) continue;
-                    const u64 f = fixed(w);
-                    if (run <= pick && run + f > pick) {
-                        p.tokens[row] = i0 + v * E + e;
+                    float y;
+                    if constexpr (DT == MK_DT_F32) y = reinterpret_cast<const float*>(xs)[(v + lane) * E + e];
+                    else y = value(reinterpret_cast<const uint16_t*>(xs)[(v + lane) * E + e]);
+                    if (!up_to_last(y, i + e) || !weigh(y, w)) continue;
+                    const u64 g = fixed(w);
+                    if (run <= pick && run + g > pick) {
+                        p.tokens[row] = i + e;
                         if (p.probs) p.probs[row] = (float)((double)w * 0x1p42 / (double)total);
                     }
-                    run += f;
+                    run += g;
                 }
             }
         }
     }
-    if (rank == 0 && tid == 0 && p.kept) {
-        unsigned kept = 0;
-        for (int c = 0; c < C; ++c) kept += sh.kept[c];
-        p.kept[row] = (int)kept;
-    }
+    if (rank == 0 && tid == 0 && p.kept) p.kept[row] = (int)kept;
 }
 
 }  // namespace
