@@ -74,7 +74,7 @@ struct Shared {
     u64 part[2][MAXC];                     // totals of each CTA, from it
     u64 sums[MAXC * SW];                   // kept mass of every warp's stretch, from its CTA
     unsigned kept[MAXC];                   // kept tokens of each CTA, from it
-    unsigned top[MAXC], low[MAXC], low_max[MAXC], bad[MAXC];  // what each CTA saw, from it
+    unsigned top[MAXC], low_max[MAXC], bad[MAXC];  // what each CTA saw, from it
     u64 warp_sum[SW];
     u64 cross_before, last;
     unsigned cross_bin, cross_count;
@@ -93,14 +93,13 @@ __device__ __forceinline__ float value_of(unsigned key) {
 }
 
 struct Weight {
-    float m, T, r;
+    float m, T, r, low;
     bool plain;  // T far from the ends of the range: the quotient by remainder (Markstein 1990) is the divided one
+    // x = -infinity weighs 0 (where T is plain)
     __device__ __forceinline__ float operator()(float x) const {
-        const float d = x - m;
-        if (!plain) return expf(__fdiv_rn(d, T));
-        const float q = d * r;
-        // far below the smallest 32-bit number: also keeps overflowed quotients out of the remainder
-        if (q < -150.f) return 0.f;
+        if (!plain) return expf(__fdiv_rn(x - m, T));
+        // below -200 T the weight is 0 anyway; the bound keeps infinities out of the remainder
+        const float d = fmaxf(x - m, low), q = d * r;
         return expf(__fmaf_rn(__fmaf_rn(-q, T, d), r, q));
     }
 };
@@ -109,24 +108,23 @@ struct Weight {
 // adding 24 leaves w in steps of 2^-19 in the low bits of the sum, adding
 // 1.5 2^-19 what is left of it in steps of 2^-42.
 struct Sum {
-    unsigned hi = 0, lo = 0, n = 0;
+    unsigned hi = 0, lo = 0;
     __device__ __forceinline__ void add(float w) {
         const float a = w + 24.0f;
         const float b = (w - (a - 24.0f)) + 0x1.8p-19f;
         hi += __float_as_uint(a);
         lo += __float_as_uint(b);
-        ++n;
     }
-    __device__ __forceinline__ u64 value() const {
-        const unsigned h = hi - n * 0x41c00000u;       // the bits of 24
-        const int l = (int)(lo - n * 0x36400000u);     // and of 1.5 2^-19
+    __device__ __forceinline__ u64 value(unsigned n) const {  // of n weights
+        const unsigned h = hi - n * 0x41c00000u;    // the bits of 24
+        const int l = (int)(lo - n * 0x36400000u);  // and of 1.5 2^-19
         return ((u64)h << 23) + (u64)(long long)l;
     }
 };
 __device__ __forceinline__ u64 fixed(float w) {
     Sum s;
     s.add(w);
-    return s.value();
+    return s.value(1);
 }
 
 // f t (0 <= f < 1) in whole numbers, rounded down, or up. Integers: 64-bit
@@ -284,68 +282,69 @@ __global__ void __launch_bounds__(ST, 2) sample_kernel(const SampleP p) {
         }
     };
 
-    // ---- the slice into shared memory; the largest and the least unmasked logit
+    // ---- the slice into shared memory; the largest logit, a NaN if there is one
     if (tid == 0) {
         sh.my_top = 0, sh.my_low = sh.my_low_max = 0xffffffffu, sh.my_bad = 0, sh.my_kept = 0;
         sh.argmax = 0xffffffffu, sh.list_n = 0;
     }
     sh.limb[0][tid] = sh.limb[1][tid] = sh.limb[2][tid] = sh.number[tid] = 0;
     __syncthreads();
-    float big = -INFINITY, small = INFINITY;
-    bool bad = false;
-    auto look = [&](float x) {
-        big = fmaxf(big, x);
-        small = fminf(small, x == -INFINITY ? INFINITY : x);
-        bad |= !(x < INFINITY);  // NaN or +infinity
-    };
+    float big;
     {
         const Raw* src = (const Raw*)p.logits + row * p.row_stride + i0;
         Raw* raw = reinterpret_cast<Raw*>(xs);
         const int whole = (uintptr_t)src % 16 == 0 ? n / E : 0;
+        auto larger = [](uint32_t a, uint32_t b) {  // of one 32-bit logit, or of two 16-bit ones; NaN wins
+            uint32_t y;
+            if constexpr (DT == MK_DT_F32) asm("max.NaN.f32 %0, %1, %2;" : "=r"(y) : "r"(a), "r"(b));
+            else if constexpr (DT == MK_DT_BF16) asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(y) : "r"(a), "r"(b));
+            else asm("max.NaN.f16x2 %0, %1, %2;" : "=r"(y) : "r"(a), "r"(b));
+            return y;
+        };
+        const uint32_t masked_raw = DT == MK_DT_F32 ? 0xff800000u : DT == MK_DT_BF16 ? 0xff80ff80u : 0xfc00fc00u;
+        uint32_t best = masked_raw;
 #pragma unroll 4
         for (int i = tid; i < whole; i += ST) {
             const uint4 a = __ldcs(reinterpret_cast<const uint4*>(src) + i);
             xs[i] = a;
-            float x[E];
-            unpack(x, a);
-#pragma unroll
-            for (int e = 0; e < E; ++e) look(x[e]);
+            best = larger(best, larger(larger(a.x, a.y), larger(a.z, a.w)));
         }
         for (int i = whole * E + tid; i < nv * E; i += ST) {
-            if constexpr (DT == MK_DT_F32) {
-                raw[i] = i < n ? src[i] : -INFINITY;  // the last vector's rest is masked
-                look(raw[i]);
-            } else {
-                raw[i] = i < n ? src[i] : DT == MK_DT_BF16 ? (Raw)0xff80 : (Raw)0xfc00;
-                look(value(raw[i]));
-            }
+            Raw a;
+            if constexpr (DT == MK_DT_F32) a = i < n ? src[i] : -INFINITY;  // the last vector's rest is masked
+            else a = i < n ? src[i] : (Raw)masked_raw;
+            raw[i] = a;
+            if constexpr (DT == MK_DT_F32) best = larger(best, __float_as_uint(a));
+            else best = larger(best, (masked_raw & 0xffff0000u) | a);
+        }
+        if constexpr (DT == MK_DT_F32) {
+            big = __uint_as_float(best);
+        } else {
+            const float lo = value(best & 0xffffu), hi = value(best >> 16);
+            big = lo != lo || hi != hi ? __uint_as_float(0x7fffffffu) : fmaxf(lo, hi);
         }
     }
     {
         // the least of the threads' largest bounds top-k's search; threads without a token do not count
         const unsigned k = key_of(big), masked_key = key_of(-INFINITY);
         const unsigned a = __reduce_max_sync(0xffffffffu, k);
-        const unsigned b = __reduce_min_sync(0xffffffffu, small < INFINITY ? key_of(small) : 0xffffffffu);
         const unsigned c = __reduce_min_sync(0xffffffffu, k > masked_key ? k : 0xffffffffu);
         if (lane == 0) {
             atomicMax(&sh.my_top, a);
-            atomicMin(&sh.my_low, b);
             atomicMin(&sh.my_low_max, c);
         }
-        if (bad) sh.my_bad = 1;
+        if (!(big < INFINITY)) sh.my_bad = 1;  // NaN or +infinity
     }
     cl.sync();  // every CTA runs, and has its numbers
     if (tid < C) {
         sh.top[tid] = *cl.map_shared_rank(&sh.my_top, tid);
-        sh.low[tid] = *cl.map_shared_rank(&sh.my_low, tid);
         sh.low_max[tid] = *cl.map_shared_rank(&sh.my_low_max, tid);
         sh.bad[tid] = *cl.map_shared_rank(&sh.my_bad, tid);
     }
     __syncthreads();
-    unsigned top = 0, low_key = 0xffffffffu, low_max_key = 0xffffffffu, any_bad = 0;
+    unsigned top = 0, low_max_key = 0xffffffffu, any_bad = 0;
     for (int c = 0; c < C; ++c) {
         top = max(top, sh.top[c]);
-        low_key = min(low_key, sh.low[c]);
         low_max_key = min(low_max_key, sh.low_max[c]);
         any_bad |= sh.bad[c];
     }
@@ -372,7 +371,7 @@ __global__ void __launch_bounds__(ST, 2) sample_kernel(const SampleP p) {
         }
         return;
     }
-    const Weight W = {m, T, __frcp_rn(T), T > 0x1p-60f && T < 0x1p60f};
+    const Weight W = {m, T, __frcp_rn(T), -200.f * T, T > 0x1p-60f && T < 0x1p60f};
     const int k_in = p.top_k ? p.top_k[row] : 0;
     const float p_in = p.top_p ? p.top_p[row] : 1.0f;
     const bool by_k = k_in > 0 && k_in < p.V, by_p = p_in < 1.0f;
@@ -395,7 +394,11 @@ __global__ void __launch_bounds__(ST, 2) sample_kernel(const SampleP p) {
     // equal bins from the largest logit down to `edge`; lower ones fall into the last
     struct Linear {
         float m, scale;
-        __device__ int operator()(float x) const { return (int)fminf((m - x) * scale, (float)(BINS - 1)); }
+        __device__ float place(float x) const { return (m - x) * scale; }
+        __device__ int operator()(float x) const { return (int)fminf(place(x), (float)(BINS - 1)); }
+        // whether x lies above bin b, and in it, without a conversion
+        __device__ bool above(float x, int b) const { return place(x) < (float)b; }
+        __device__ bool in(float x, int b) const { return !(place(x) < (float)b) && (place(x) < (float)(b + 1) || b == BINS - 1); }
     };
     auto bins_down_to = [&](float edge) {
         const float s = (float)BINS / (m - edge);
@@ -436,6 +439,28 @@ __global__ void __launch_bounds__(ST, 2) sample_kernel(const SampleP p) {
         }
     };
     int turn = 0;
+    // sums and minima over all threads of the cluster
+    auto cluster_sum = [&](u64 v) {
+        u64 mine, all = 0;
+        block_excl(v, sh.warp_sum, mine);
+        if (tid < C) cl.map_shared_rank(sh.part[turn], tid)[rank] = mine;
+        cl.sync();
+        for (int c = 0; c < C; ++c) all += sh.part[turn][c];
+        turn ^= 1;
+        return all;
+    };
+    auto cluster_min = [&](unsigned v) {
+        v = __reduce_min_sync(0xffffffffu, v);
+        __syncthreads();
+        if (lane == 0) sh.warp_sum[warp] = v;
+        __syncthreads();
+        for (int w = 0; w < SW; ++w) v = min(v, (unsigned)sh.warp_sum[w]);
+        if (tid < C) cl.map_shared_rank(sh.part[turn], tid)[rank] = v;
+        cl.sync();
+        for (int c = 0; c < C; ++c) v = min(v, (unsigned)sh.part[turn][c]);
+        turn ^= 1;
+        return v;
+    };
     // The rank at which a running sum over ranks (of counts, or of masses of tokens up to `up_to`) reaches the
     // target, by histograms over the bits of the distance, then by index among equal logits. All CTAs call it; the
     // sum reaches the target.
@@ -501,7 +526,12 @@ __global__ void __launch_bounds__(ST, 2) sample_kernel(const SampleP p) {
         // at least k tokens lie at or above the k-th largest of the threads' maxima; a k beyond what those
         // tell is sought among all tokens
         const bool by_threads = k_in <= min(p.V, C * ST) / 4;
-        const float edge = value_of(by_threads ? low_max_key : low_key);
+        float edge = value_of(low_max_key);
+        if (!by_threads) {
+            float small = INFINITY;
+            each([&](float x, int) { small = fminf(small, x > -INFINITY ? x : INFINITY); });
+            edge = value_of(cluster_min(small < INFINITY ? key_of(small) : 0xffffffffu));
+        }
         const Linear bin = bins_down_to(edge);
         if (by_threads) {
             if (big > -INFINITY) atomicAdd(&sh.number[bin(big)], 1u);
@@ -516,20 +546,14 @@ __global__ void __launch_bounds__(ST, 2) sample_kernel(const SampleP p) {
         bool listed = f.bin >= 0 && (by_threads || f.before + f.count <= LIST);
         bool binds = f.bin >= 0 || by_threads;
         if (listed) {
-            collect(1, [&](float x, int) { return x >= edge && bin(x) <= f.bin; });
+            collect(1, [&](float x, int) { return x >= edge && (f.bin == BINS - 1 || bin.above(x, f.bin + 1)); });
             cl.sync();
             listed = *cl.map_shared_rank(&sh.list_n, 0) <= LIST;
         } else if (by_threads) {
             // how many tokens are there at all
             unsigned c = 0;
             each([&](float x, int) { c += x > -INFINITY; });
-            u64 mine, all = 0;
-            block_excl(c, sh.warp_sum, mine);
-            if (tid < C) cl.map_shared_rank(sh.part[turn], tid)[rank] = mine;
-            cl.sync();
-            for (int r = 0; r < C; ++r) all += sh.part[turn][r];
-            turn ^= 1;
-            binds = all >= (u64)k_in;
+            binds = cluster_sum(c) >= (u64)k_in;
         }
         if (listed) {
             // ---- CTA 0 has every candidate
@@ -580,7 +604,8 @@ __global__ void __launch_bounds__(ST, 2) sample_kernel(const SampleP p) {
     }
 
     const float least_x = least > 0.f ? m + T * (logf(least) - 0.01f) : -INFINITY;  // below: lighter than min_p
-    // kept tokens above a bound: `sure` by themselves, or up to `last`
+    // kept tokens end at `last`; a row that keeps all unmasked tokens needs no comparison, as masked ones weigh 0
+    bool all_ranks = last == ((u64)masked << 32) - 1 && W.plain;
     float xc = value_of(top - (unsigned)(last >> 32));
     unsigned ic = (unsigned)last;
     auto up_to_last = [&](float x, int i) { return x > xc || (x == xc && (unsigned)i <= ic); };
@@ -590,22 +615,37 @@ __global__ void __launch_bounds__(ST, 2) sample_kernel(const SampleP p) {
     u64 before = 0, target = 0;
     float low_x = -INFINITY;
     if (by_p) {
-        // all of top-k's mass
+        // all of top-k's mass, and the least logit
         Sum s;
-        each([&](float x, int i) {
-            if (up_to_last(x, i)) s.add(W(x));
-        });
-        u64 mine, total = 0;
-        block_excl(s.value(), sh.warp_sum, mine);
-        if (tid < C) cl.map_shared_rank(sh.part[turn], tid)[rank] = mine;
-        cl.sync();
-        for (int c = 0; c < C; ++c) total += sh.part[turn][c];
-        turn ^= 1;
+        unsigned number = 0;
+        float small = INFINITY;
+        if (all_ranks) {
+            each([&](float x, int) {
+                s.add(W(x));
+                ++number;
+                small = fminf(small, x > -INFINITY ? x : INFINITY);
+            });
+        } else {
+            each([&](float x, int i) {
+                if (up_to_last(x, i)) {
+                    s.add(W(x));
+                    ++number;
+                    small = fminf(small, x);
+                }
+            });
+        }
+        const unsigned low_key = __reduce_min_sync(0xffffffffu, small < INFINITY ? key_of(small) : 0xffffffffu);
+        if (lane == 0) atomicMin(&sh.my_low, low_key);
+        const u64 total = cluster_sum(s.value(number));  // its barriers are for my_low too
         target = mass_target(total);
         // Tokens lighter than (1 - p) total / V weigh less than (1 - p) total together: at least p total lies
         // before them. Half of that bound, and a hundredth, leave room for roundings.
         const float light = (1.f - fmaxf(p_in, 0.f)) * (__ull2float_rn(total) * 0x1p-43f) / (float)p.V;
-        low_x = fmaxf(value_of(low_key), light > 1e-30f ? m + T * (logf(light) - 0.01f) : -INFINITY);
+        unsigned low = 0xffffffffu;
+#pragma unroll
+        for (int c = 0; c < MAXC; ++c)
+            if (c < C) low = min(low, *cl.map_shared_rank(&sh.my_low, c));
+        low_x = fmaxf(value_of(low), light > 1e-30f ? m + T * (logf(light) - 0.01f) : -INFINITY);
         bin = bins_down_to(low_x);
         each([&](float x, int i) {
             if (x >= low_x && up_to_last(x, i)) tally(sh, bin(x), fixed(W(x)));
@@ -621,6 +661,7 @@ __global__ void __launch_bounds__(ST, 2) sample_kernel(const SampleP p) {
             xc = value_of(top - (unsigned)(last >> 32));
             ic = (unsigned)last;
         }
+        all_ranks = false;
     }
 
     // ---- the draw: a warp sums its stretch's kept weights, all CTAs get all sums (and the list)
@@ -630,14 +671,27 @@ __global__ void __launch_bounds__(ST, 2) sample_kernel(const SampleP p) {
         return w >= least;
     };
     Sum s;
-    each([&](float x, int i) {
-        float w;
-        if (up_to_last(x, i) && (border < 0 || (x >= low_x && bin(x) < border)) && weigh(x, w)) s.add(w);
-    });
+    unsigned added = 0, count = 0;  // weights in s, tokens kept
+    if (all_ranks && !(least > 0.f)) {
+        each([&](float x, int) {
+            s.add(W(x));
+            ++added;
+            count += x > -INFINITY;
+        });
+    } else {
+        each([&](float x, int i) {
+            float w;
+            if ((border < 0 ? up_to_last(x, i) : bin.above(x, border) && up_to_last(x, i)) && weigh(x, w)) {
+                s.add(w);
+                ++added;
+            }
+        });
+        count = added;
+    }
     if (border >= 0)
-        collect(C, [&](float x, int i) { return x >= low_x && bin(x) == border && up_to_last(x, i); });
-    u64 sum = s.value();
-    const unsigned count = __reduce_add_sync(0xffffffffu, s.n);
+        collect(C, [&](float x, int i) { return bin.in(x, border) && x >= low_x && up_to_last(x, i); });
+    u64 sum = s.value(added);
+    count = __reduce_add_sync(0xffffffffu, count);
 #pragma unroll
     for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
     if (lane < C) cl.map_shared_rank(sh.sums, lane)[rank * SW + warp] = sum;
@@ -695,13 +749,14 @@ __global__ void __launch_bounds__(ST, 2) sample_kernel(const SampleP p) {
             const int i = i0 + (v + lane) * E;
             float x[E], w;
             Sum mine;
+            unsigned some = 0;
             if (v + lane < v1) {
                 unpack(x, xs[v + lane]);
 #pragma unroll
                 for (int e = 0; e < E; ++e)
-                    if (up_to_last(x[e], i + e) && weigh(x[e], w)) mine.add(w);
+                    if (up_to_last(x[e], i + e) && weigh(x[e], w)) mine.add(w), ++some;
             }
-            const u64 f = mine.value(), incl = warp_incl(f);
+            const u64 f = mine.value(some), incl = warp_incl(f);
             u64 run = seen + incl - f;
             seen += __shfl_sync(0xffffffffu, incl, 31);
             if (run <= pick && run + f > pick) {  // one lane
