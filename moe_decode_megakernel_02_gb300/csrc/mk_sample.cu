@@ -46,7 +46,7 @@ namespace cg = cooperative_groups;
 constexpr int ST = 512;        // threads of a CTA
 constexpr int SW = ST / 32;
 constexpr int BINS = ST;       // histogram bins, one a thread
-constexpr int LIST = 1024;     // ranks a list holds: ordering more costs more than further histograms
+constexpr int LIST = 2 * ST;     // ranks a list holds: ordering more costs more than further histograms
 constexpr int MAXC = 8;        // CTAs of a cluster
 constexpr int MAX_SLICE_B = 180224;  // bytes of a slice of logits: 176 KB
 
@@ -67,8 +67,14 @@ struct SampleP {
 // Written by one CTA for another only where it says so; each such place is
 // written once, or alternates, so that a late reader is never overtaken.
 struct Shared {
-    unsigned limb[3][BINS], number[BINS];  // a histogram being filled: masses in 14-bit limbs, counts
-    u64 mass[2][BINS];                     // complete ones, read by the cluster
+    union {
+        struct {
+            unsigned limb[3][BINS], number[BINS];  // a histogram being filled: masses in 14-bit limbs, counts
+        };
+        u64 own[LIST];                     // ranks of this CTA's tokens
+    };
+    u64 mass[2][BINS];                     // complete histograms, read by the cluster; the next one's place is free
+                                           // until it is complete, and serves as the warps' queues
     unsigned count[2][BINS];
     u64 list[LIST];                        // ranks, from all CTAs
     u64 part[2][MAXC];                     // totals of each CTA, from it
@@ -77,8 +83,8 @@ struct Shared {
     unsigned top[MAXC], low_max[MAXC], bad[MAXC];  // what each CTA saw, from it
     u64 warp_sum[SW];
     u64 cross_before, last;
-    unsigned cross_bin, cross_count;
-    unsigned argmax, list_n;
+    unsigned cross_bin, cross_count, cross_ahead;
+    unsigned argmax, list_n, own_n, own_base;
     unsigned my_top, my_low, my_low_max, my_bad, my_kept;
 };
 
@@ -180,12 +186,13 @@ struct Found {
     int bin;         // -1: the total does not reach the target
     u64 before;      // in front of the bin
     unsigned count;  // tokens in it
+    unsigned ahead;  // those of them in the CTAs before this one
     u64 total;
 };
 // The bin of the cluster's histogram at which the running sum (of masses, or
 // of counts), `before` in front of bin 0, reaches the target; every CTA finds
 // it by itself from all CTAs' bins. `turn` alternates. The histogram is empty again.
-__device__ Found find_bin(cg::cluster_group& cl, Shared& sh, int C, int turn, bool by_count, u64 before, u64 target) {
+__device__ Found find_bin(cg::cluster_group& cl, Shared& sh, int C, int rank, int turn, bool by_count, u64 before, u64 target) {
     const int t = threadIdx.x;
     __syncthreads();
     sh.mass[turn][t] = ((u64)sh.limb[2][t] << 28) + ((u64)sh.limb[1][t] << 14) + sh.limb[0][t];
@@ -194,26 +201,28 @@ __device__ Found find_bin(cg::cluster_group& cl, Shared& sh, int C, int turn, bo
     if (t == 0) sh.cross_bin = 0xffffffffu;
     cl.sync();
     u64 m = 0;
-    unsigned n = 0;
+    unsigned n = 0, ahead = 0;
 #pragma unroll
     for (int c = 0; c < MAXC; ++c)  // all at once: each is a round trip through the cluster
         if (c < C) {
             if (!by_count) m += cl.map_shared_rank(sh.mass[turn], c)[t];
+            if (c == rank) ahead = n;
             n += cl.map_shared_rank(sh.count[turn], c)[t];
         }
     const u64 v = by_count ? n : m;
     Found f;
     const u64 run = before + block_excl(v, sh.warp_sum, f.total);
-    if (run < target && run + v >= target) sh.cross_bin = t, sh.cross_before = run, sh.cross_count = n;
+    if (run < target && run + v >= target) sh.cross_bin = t, sh.cross_before = run, sh.cross_count = n, sh.cross_ahead = ahead;
     __syncthreads();
     f.bin = (int)sh.cross_bin;
     f.before = sh.cross_before;
     f.count = sh.cross_count;
+    f.ahead = sh.cross_ahead;
     __syncthreads();
     return f;
 }
 
-// v[0 .. n) ascending; `n2` a power of two not below n, padded with ~0 here
+// v[0 .. n) ascending; `n2` a power of two not below n, within v, padded with ~0 here
 __device__ void sort_list(u64* v, int n, int n2) {
     for (int i = n + threadIdx.x; i < n2; i += ST) v[i] = ~0ull;
     __syncthreads();
@@ -227,24 +236,37 @@ __device__ void sort_list(u64* v, int n, int n2) {
             __syncthreads();
         }
 }
-// the same for up to ST numbers, all different: each thread finds its own one's place
-__device__ void rank_list(u64* v, int n) {
-    const int i = threadIdx.x;
-    const u64 x = i < n ? v[i] : ~0ull;
-    int at = 0;
-    for (int j = 0; j < n; ++j) at += v[j] < x;
+// the same for up to ST numbers, one a thread in a register: partners within a
+// warp meet by shuffles, the others through v
+__device__ void sort_one_each(u64* v, int n) {
+    const int t = threadIdx.x;
+    int n2 = 32;
+    while (n2 < n) n2 *= 2;
+    u64 x = t < n ? v[t] : ~0ull;
     __syncthreads();
-    if (i < n) v[at] = x;
+    for (int k = 2; k <= n2; k <<= 1)
+        for (int j = k >> 1; j; j >>= 1) {
+            u64 y;
+            if (j < 32) {
+                y = __shfl_xor_sync(0xffffffffu, x, j);
+            } else {
+                if (t < n2) v[t] = x;
+                __syncthreads();
+                y = t < n2 ? v[t ^ j] : 0;
+                __syncthreads();
+            }
+            // the lower place of an ascending pair takes the smaller one
+            const bool smaller = ((t & j) == 0) == ((t & k) == 0);
+            x = (x < y) == smaller ? x : y;
+        }
+    if (t < n) v[t] = x;
     __syncthreads();
 }
 __device__ void order_list(u64* v, int n) {
-    if (n <= ST) {
-        rank_list(v, n);
-    } else {
-        int n2 = 2 * ST;
-        while (n2 < n) n2 *= 2;
-        sort_list(v, n, n2);
-    }
+    if (n <= ST)
+        sort_one_each(v, n);
+    else
+        sort_list(v, n, 2 * ST);
 }
 
 // Bound: one read of the logits from HBM, then passes over shared memory of 4
@@ -282,10 +304,19 @@ __global__ void __launch_bounds__(ST, 2) sample_kernel(const SampleP p) {
         }
     };
 
+    auto larger = [](uint32_t a, uint32_t b) {  // of one 32-bit logit, or of two 16-bit ones; NaN wins
+        uint32_t y;
+        if constexpr (DT == MK_DT_F32) asm("max.NaN.f32 %0, %1, %2;" : "=r"(y) : "r"(a), "r"(b));
+        else if constexpr (DT == MK_DT_BF16) asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(y) : "r"(a), "r"(b));
+        else asm("max.NaN.f16x2 %0, %1, %2;" : "=r"(y) : "r"(a), "r"(b));
+        return y;
+    };
+    const uint32_t masked_raw = DT == MK_DT_F32 ? 0xff800000u : DT == MK_DT_BF16 ? 0xff80ff80u : 0xfc00fc00u;
+
     // ---- the slice into shared memory; the largest logit, a NaN if there is one
     if (tid == 0) {
         sh.my_top = 0, sh.my_low = sh.my_low_max = 0xffffffffu, sh.my_bad = 0, sh.my_kept = 0;
-        sh.argmax = 0xffffffffu, sh.list_n = 0;
+        sh.argmax = 0xffffffffu, sh.list_n = 0, sh.own_n = 0;
     }
     sh.limb[0][tid] = sh.limb[1][tid] = sh.limb[2][tid] = sh.number[tid] = 0;
     __syncthreads();
@@ -294,14 +325,6 @@ __global__ void __launch_bounds__(ST, 2) sample_kernel(const SampleP p) {
         const Raw* src = (const Raw*)p.logits + row * p.row_stride + i0;
         Raw* raw = reinterpret_cast<Raw*>(xs);
         const int whole = (uintptr_t)src % 16 == 0 ? n / E : 0;
-        auto larger = [](uint32_t a, uint32_t b) {  // of one 32-bit logit, or of two 16-bit ones; NaN wins
-            uint32_t y;
-            if constexpr (DT == MK_DT_F32) asm("max.NaN.f32 %0, %1, %2;" : "=r"(y) : "r"(a), "r"(b));
-            else if constexpr (DT == MK_DT_BF16) asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(y) : "r"(a), "r"(b));
-            else asm("max.NaN.f16x2 %0, %1, %2;" : "=r"(y) : "r"(a), "r"(b));
-            return y;
-        };
-        const uint32_t masked_raw = DT == MK_DT_F32 ? 0xff800000u : DT == MK_DT_BF16 ? 0xff80ff80u : 0xfc00fc00u;
         uint32_t best = masked_raw;
 #pragma unroll 4
         for (int i = tid; i < whole; i += ST) {
@@ -391,6 +414,38 @@ __global__ void __launch_bounds__(ST, 2) sample_kernel(const SampleP p) {
             for (int e = 0; e < E; ++e) f(x[e], i0 + v * E + e);
         }
     };
+    int turn = 0;  // of what alternates
+    // f(logit) for the tokens that `take(logit, index)` says, 32 of them at a time: they wait in a queue of the
+    // warp's, so that costly work runs on full warps
+    auto dense = [&](auto take, auto f) {
+        static_assert(sizeof(sh.mass[0]) >= SW * 64 * sizeof(float), "queues");
+        float* q = reinterpret_cast<float*>(sh.mass[turn]) + warp * 64;
+        int waiting = 0;
+        for (int v = v0; v < v1; v += 32) {
+            float x[E];
+            unpack(x, v + lane < v1 ? xs[v + lane] : make_uint4(masked_raw, masked_raw, masked_raw, masked_raw));
+#pragma unroll
+            for (int e = 0; e < E; ++e) {
+                const bool in = take(x[e], i0 + (v + lane) * E + e);
+                const unsigned who = __ballot_sync(0xffffffffu, in);
+                if (who) {
+                    if (in) q[waiting + __popc(who & ((1u << lane) - 1))] = x[e];
+                    waiting += __popc(who);
+                    __syncwarp();
+                    if (waiting >= 32) {
+                        f(q[lane]);
+                        waiting -= 32;
+                        const float rest = q[32 + lane];
+                        __syncwarp();
+                        if (lane < waiting) q[lane] = rest;
+                        __syncwarp();
+                    }
+                }
+            }
+        }
+        if (lane < waiting) f(q[lane]);
+        __syncwarp();
+    };
     // equal bins from the largest logit down to `edge`; lower ones fall into the last
     struct Linear {
         float m, scale;
@@ -404,41 +459,43 @@ __global__ void __launch_bounds__(ST, 2) sample_kernel(const SampleP p) {
         const float s = (float)BINS / (m - edge);
         return Linear{m, s < 1e30f ? s : 0.f};  // no room between the two: one bin
     };
-    // The ranks of tokens that `pick` takes, to the lists of CTAs [0, to). All warps call it; the number is in
-    // CTA 0's list_n after the next barrier (those that do not fit counted).
-    auto collect = [&](int to, auto pick) {
-        unsigned* count = cl.map_shared_rank(&sh.list_n, 0);
+    // The ranks of tokens of the lane's vector v + lane, elements `in`, to this CTA's own list. A list goes on to
+    // the cluster as a whole, as every trip there takes about a thousand cycles.
+    auto put = [&](int v, const float (&x)[E], unsigned in) {
+        if (!in) return;
+        unsigned at = atomicAdd(&sh.own_n, (unsigned)__popc(in));
+#pragma unroll
+        for (int e = 0; e < E; ++e)
+            if (in >> e & 1u) {
+                if (at < LIST) sh.own[at] = (u64)(top - key_of(x[e])) << 32 | (unsigned)(i0 + (v + lane) * E + e);
+                ++at;
+            }
+    };
+    // this CTA's list to the lists of CTAs [0, to), from place `base` on
+    auto deliver = [&](int to, unsigned base) {
+        const unsigned n_own = min(sh.own_n, (unsigned)LIST);
+        for (unsigned i = tid; i < n_own; i += ST)
+            if (base + i < LIST)
+                for (int c = 0; c < to; ++c) cl.map_shared_rank(sh.list, c)[base + i] = sh.own[i];
+    };
+    // all tokens from `edge` on that `pick` takes
+    auto collect = [&](float edge, auto pick) {
         for (int v = v0; v < v1; v += 32) {
             float x[E];
             unsigned in = 0;
-            if (v + lane < v1) {
-                unpack(x, xs[v + lane]);
+            uint4 a = make_uint4(masked_raw, masked_raw, masked_raw, masked_raw);
+            if (v + lane < v1) a = xs[v + lane];
+            const uint32_t best = larger(larger(a.x, a.y), larger(a.z, a.w));
+            bool some;
+            if constexpr (DT == MK_DT_F32) some = __uint_as_float(best) >= edge;
+            else some = fmaxf(value(best & 0xffffu), value(best >> 16)) >= edge;
+            if (!__any_sync(0xffffffffu, some)) continue;
+            unpack(x, a);
 #pragma unroll
-                for (int e = 0; e < E; ++e) in |= (unsigned)pick(x[e], i0 + (v + lane) * E + e) << e;
-            }
-            if (!__any_sync(0xffffffffu, in)) continue;
-            // one place for all of the warp's
-            const unsigned mine = __popc(in);
-            unsigned at = mine;
-#pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const unsigned a = __shfl_up_sync(0xffffffffu, at, o);
-                if (lane >= o) at += a;
-            }
-            unsigned base = 0;
-            if (lane == 31) base = atomicAdd(count, at);
-            at += __shfl_sync(0xffffffffu, base, 31) - mine;
-#pragma unroll
-            for (int e = 0; e < E; ++e)
-                if (in >> e & 1u) {
-                    const u64 r = (u64)(top - key_of(x[e])) << 32 | (unsigned)(i0 + (v + lane) * E + e);
-                    if (at < LIST)
-                        for (int c = 0; c < to; ++c) cl.map_shared_rank(sh.list, c)[at] = r;
-                    ++at;
-                }
+            for (int e = 0; e < E; ++e) in |= (unsigned)(x[e] >= edge && pick(x[e])) << e;
+            put(v, x, in);
         }
     };
-    int turn = 0;
     // sums and minima over all threads of the cluster
     auto cluster_sum = [&](u64 v) {
         u64 mine, all = 0;
@@ -477,7 +534,7 @@ __global__ void __launch_bounds__(ST, 2) sample_kernel(const SampleP p) {
                 if ((l == 0 || (d >> up) == prefix) && (x > xk || (x == xk && (unsigned)i <= ik)))
                     tally(sh, (d >> lo) & ((1u << (up - lo)) - 1), by_count ? 0 : fixed(W(x)));
             });
-            const Found f = find_bin(cl, sh, C, turn, by_count, before, target);
+            const Found f = find_bin(cl, sh, C, rank, turn, by_count, before, target);
             turn ^= 1;
             prefix = prefix << (up - lo) | (unsigned)f.bin;
             before = f.before;
@@ -540,13 +597,17 @@ __global__ void __launch_bounds__(ST, 2) sample_kernel(const SampleP p) {
                 if (x > -INFINITY) atomicAdd(&sh.number[bin(x)], 1u);
             });
         }
-        const Found f = find_bin(cl, sh, C, turn, true, 0, (u64)k_in);
+        const Found f = find_bin(cl, sh, C, rank, turn, true, 0, (u64)k_in);
         turn ^= 1;
         // With fewer than k of them, top-k may still bind: search(). A bin of all tokens is known to fit or not.
         bool listed = f.bin >= 0 && (by_threads || f.before + f.count <= LIST);
         bool binds = f.bin >= 0 || by_threads;
         if (listed) {
-            collect(1, [&](float x, int) { return x >= edge && (f.bin == BINS - 1 || bin.above(x, f.bin + 1)); });
+            collect(edge, [&](float x) { return f.bin == BINS - 1 || bin.above(x, f.bin + 1); });
+            __syncthreads();
+            if (tid == 0) sh.own_base = atomicAdd(cl.map_shared_rank(&sh.list_n, 0), sh.own_n);
+            __syncthreads();
+            deliver(1, sh.own_base);
             cl.sync();
             listed = *cl.map_shared_rank(&sh.list_n, 0) <= LIST;
         } else if (by_threads) {
@@ -599,8 +660,11 @@ __global__ void __launch_bounds__(ST, 2) sample_kernel(const SampleP p) {
             cl.sync();  // no CTA leaves while another reads its shared memory
             return;
         }
+        // the list's place is the histogram's
+        sh.limb[0][tid] = sh.limb[1][tid] = sh.limb[2][tid] = sh.number[tid] = 0;
+        __syncthreads();
+        if (tid == 0) sh.own_n = 0;
         if (binds) last = search(true, (u64)k_in, last);
-        if (tid == 0) sh.list_n = 0;  // for top-p, after the barriers to come
     }
 
     const float least_x = least > 0.f ? m + T * (logf(least) - 0.01f) : -INFINITY;  // below: lighter than min_p
@@ -612,6 +676,7 @@ __global__ void __launch_bounds__(ST, 2) sample_kernel(const SampleP p) {
     Linear bin = {m, 0.f};
     int border = -1;       // the bin whose tokens are in the list
     unsigned listed = 0;   // how many
+    unsigned ahead = 0;    // how many of them in the CTAs before this one
     u64 before = 0, target = 0;
     float low_x = -INFINITY;
     if (by_p) {
@@ -647,14 +712,14 @@ __global__ void __launch_bounds__(ST, 2) sample_kernel(const SampleP p) {
             if (c < C) low = min(low, *cl.map_shared_rank(&sh.my_low, c));
         low_x = fmaxf(value_of(low), light > 1e-30f ? m + T * (logf(light) - 0.01f) : -INFINITY);
         bin = bins_down_to(low_x);
-        each([&](float x, int i) {
-            if (x >= low_x && up_to_last(x, i)) tally(sh, bin(x), fixed(W(x)));
-        });
-        const Found f = find_bin(cl, sh, C, turn, false, 0, target);
+        dense([&](float x, int i) { return x >= low_x && up_to_last(x, i); },
+              [&](float x) { tally(sh, bin(x), fixed(W(x))); });
+        const Found f = find_bin(cl, sh, C, rank, turn, false, 0, target);
         turn ^= 1;
         if (f.count <= LIST) {
             border = f.bin;
             listed = f.count;
+            ahead = f.ahead;
             before = f.before;
         } else {
             last = search(false, target, last);
@@ -679,17 +744,29 @@ __global__ void __launch_bounds__(ST, 2) sample_kernel(const SampleP p) {
             count += x > -INFINITY;
         });
     } else {
-        each([&](float x, int i) {
-            float w;
-            if ((border < 0 ? up_to_last(x, i) : bin.above(x, border) && up_to_last(x, i)) && weigh(x, w)) {
-                s.add(w);
-                ++added;
-            }
-        });
+        dense([&](float x, int i) { return (border < 0 || bin.above(x, border)) && x >= least_x && up_to_last(x, i); },
+              [&](float x) {
+                  const float w = W(x);
+                  if (w >= least) {
+                      s.add(w);
+                      ++added;
+                  }
+              });
         count = added;
     }
-    if (border >= 0)
-        collect(C, [&](float x, int i) { return bin.in(x, border) && x >= low_x && up_to_last(x, i); });
+    if (border >= 0) {
+        for (int v = v0; v < v1; v += 32) {
+            float x[E];
+            unsigned in = 0;
+            if (v + lane < v1) {
+                unpack(x, xs[v + lane]);
+#pragma unroll
+                for (int e = 0; e < E; ++e)
+                    in |= (unsigned)(bin.in(x[e], border) && x[e] >= low_x && up_to_last(x[e], i0 + (v + lane) * E + e)) << e;
+            }
+            put(v, x, in);
+        }
+    }
     u64 sum = s.value(added);
     count = __reduce_add_sync(0xffffffffu, count);
 #pragma unroll
@@ -697,6 +774,7 @@ __global__ void __launch_bounds__(ST, 2) sample_kernel(const SampleP p) {
     if (lane < C) cl.map_shared_rank(sh.sums, lane)[rank * SW + warp] = sum;
     if (lane == 0) atomicAdd(&sh.my_kept, count);
     __syncthreads();
+    if (border >= 0) deliver(C, ahead);
     if (tid < C) cl.map_shared_rank(sh.kept, tid)[rank] = sh.my_kept;
     cl.sync();
     unsigned kept = 0;
@@ -743,35 +821,57 @@ __global__ void __launch_bounds__(ST, 2) sample_kernel(const SampleP p) {
     const u64 pick = part_of(u, total, false);
     if (tid < C * SW && at <= pick && at + sh.sums[tid] > pick) sh.cross_bin = tid, sh.cross_before = at;
     __syncthreads();
-    if ((int)sh.cross_bin == rank * SW + warp) {  // one warp of the cluster
-        u64 seen = sh.cross_before;
-        for (int v = v0; v < v1 && seen <= pick; v += 32) {
-            const int i = i0 + (v + lane) * E;
-            float x[E], w;
-            Sum mine;
-            unsigned some = 0;
-            if (v + lane < v1) {
-                unpack(x, xs[v + lane]);
+    if ((int)sh.cross_bin / SW == rank) {
+        // The stretch is this CTA's: its warps sum a part of it each, and the one that u falls into walks that.
+        const int w = (int)sh.cross_bin % SW;
+        const int s0 = (int)((long long)nv * w / SW), s1 = (int)((long long)nv * (w + 1) / SW);
+        const int a0 = s0 + (s1 - s0) * warp / SW, a1 = s0 + (s1 - s0) * (warp + 1) / SW;
+        auto weight_of = [&](const float (&x)[E], int v, Sum& mine, unsigned& some) {  // of the kept ones of vector v
+            float y;
 #pragma unroll
-                for (int e = 0; e < E; ++e)
-                    if (up_to_last(x[e], i + e) && weigh(x[e], w)) mine.add(w), ++some;
-            }
-            const u64 f = mine.value(some), incl = warp_incl(f);
-            u64 run = seen + incl - f;
-            seen += __shfl_sync(0xffffffffu, incl, 31);
-            if (run <= pick && run + f > pick) {  // one lane
+            for (int e = 0; e < E; ++e)
+                if (up_to_last(x[e], i0 + v * E + e) && weigh(x[e], y)) mine.add(y), ++some;
+        };
+        Sum part;
+        unsigned parts = 0;
+        for (int v = a0 + lane; v < a1; v += 32) {
+            float x[E];
+            unpack(x, xs[v]);
+            weight_of(x, v, part, parts);
+        }
+        u64 mine = part.value(parts), all;
+#pragma unroll
+        for (int o = 16; o; o >>= 1) mine += __shfl_xor_sync(0xffffffffu, mine, o);
+        u64 seen = block_excl(lane == 0 ? mine : 0, sh.warp_sum, all);
+        seen = sh.cross_before + __shfl_sync(0xffffffffu, seen, 0);
+        if (seen <= pick && seen + mine > pick) {  // one warp
+            for (int v = a0; v < a1 && seen <= pick; v += 32) {
+                const int i = i0 + (v + lane) * E;
+                float y;
+                Sum some;
+                unsigned number = 0;
+                if (v + lane < a1) {
+                    float x[E];
+                    unpack(x, xs[v + lane]);
+                    weight_of(x, v + lane, some, number);
+                }
+                const u64 f = some.value(number), incl = warp_incl(f);
+                u64 run = seen + incl - f;
+                seen += __shfl_sync(0xffffffffu, incl, 31);
+                if (run <= pick && run + f > pick) {  // one lane
 #pragma unroll 1
-                for (int e = 0; e < E; ++e) {
-                    float y;
-                    if constexpr (DT == MK_DT_F32) y = reinterpret_cast<const float*>(xs)[(v + lane) * E + e];
-                    else y = value(reinterpret_cast<const uint16_t*>(xs)[(v + lane) * E + e]);
-                    if (!up_to_last(y, i + e) || !weigh(y, w)) continue;
-                    const u64 g = fixed(w);
-                    if (run <= pick && run + g > pick) {
-                        p.tokens[row] = i + e;
-                        if (p.probs) p.probs[row] = (float)((double)w * 0x1p42 / (double)total);
+                    for (int e = 0; e < E; ++e) {
+                        float x;
+                        if constexpr (DT == MK_DT_F32) x = reinterpret_cast<const float*>(xs)[(v + lane) * E + e];
+                        else x = value(reinterpret_cast<const uint16_t*>(xs)[(v + lane) * E + e]);
+                        if (!up_to_last(x, i + e) || !weigh(x, y)) continue;
+                        const u64 g = fixed(y);
+                        if (run <= pick && run + g > pick) {
+                            p.tokens[row] = i + e;
+                            if (p.probs) p.probs[row] = (float)((double)y * 0x1p42 / (double)total);
+                        }
+                        run += g;
                     }
-                    run += g;
                 }
             }
         }
