@@ -12,11 +12,11 @@ constexpr int MAX_DEV = 32;
 
 // KindInfo of each kernel on each device, asked for once
 int kind_info(int dev, int d, const Kind& k, KindInfo& out) {
-    static KindInfo cache[MAX_DEV][3][4][6];
-    static bool have[MAX_DEV][3][4][6];
+    static KindInfo cache[MAX_DEV][3][5][6];
+    static bool have[MAX_DEV][3][5][6];
     static std::mutex lock;
     const int di = d == 64 ? 0 : d == 128 ? 1 : 2;
-    const int ri = k.many ? 3 : k.rn >> 1, fi = k.format * 2 + (k.splitq ? 1 : 0);
+    const int ri = log2_exact(k.rows) - 3, fi = k.format * 2 + (k.splitq ? 1 : 0);
     const AttendFn fn = d == 64 ? attend_64 : d == 128 ? attend_128 : attend_256;
     if (dev >= MAX_DEV) return fn(k, nullptr, &out, 0, false, nullptr);
     std::lock_guard<std::mutex> g(lock);
@@ -71,10 +71,9 @@ int make_plan(const mk_attention* a, Plan& pl) {
 
     const int rows = T * (Hq / H);
     const bool splitq = g.format == MK_KV_BF16 && a->q->dtype == MK_DT_F16;
-    // up to 16 rows (32 where their outputs fit the registers) the warps split
-    // the positions; more rows are split over the warps
-    pl.own_k = Kind{g.format, splitq, rows > (D <= 128 ? 32 : 16), rows <= 8 ? 1 : rows <= 16 ? 2 : 4};
-    if (pl.own_k.many) pl.own_k.rn = 2;
+    // the least row block that holds the rows, or the largest there is
+    auto block_of = [D](int64_t n) { return n <= 8 ? 8 : n <= 16 ? 16 : n <= 32 ? 32 : n <= 64 || D == 256 ? 64 : 128; };
+    pl.own_k = Kind{g.format, splitq, block_of(rows)};
     if (const int rc = kind_info(dev, D, pl.own_k, pl.own_i)) return rc;
     if (pl.own_i.ctas < 1) return fail(MK_ERR_UNSUPPORTED, "attend: the kernel does not fit this device");
     pl.own_rb = (rows + pl.own_i.rows - 1) / pl.own_i.rows;
@@ -95,7 +94,7 @@ int make_plan(const mk_attention* a, Plan& pl) {
     pl.sh_off = pl.bytes;
     if (a->shared_len) {
         const int64_t all = (int64_t)B * rows;
-        pl.sh_k = Kind{g.format, splitq, true, 2};
+        pl.sh_k = Kind{g.format, splitq, block_of(all)};
         if (const int rc = kind_info(dev, D, pl.sh_k, pl.sh_i)) return rc;
         if (pl.sh_i.ctas < 1) return fail(MK_ERR_UNSUPPORTED, "attend: the kernel does not fit this device");
         pl.sh_rb = (int)((all + pl.sh_i.rows - 1) / pl.sh_i.rows);

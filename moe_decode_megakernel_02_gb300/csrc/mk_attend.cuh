@@ -11,15 +11,15 @@
 // 8-wide side, K and V fragments are each used once per 8 rows, and a thread
 // keeps the same two rows from the scores to the output.
 //
-// Two shapes of the same loop over 64-position tiles (cp.async ring in shared
-// memory):
-//   FEW   up to 8, 16 or 32 rows an item: the four warps split a tile's
-//         positions and hold the same rows; their maxima, sums and outputs
-//         meet at the end. Bound by the cache's bytes.
-//   MANY  64 rows an item: the four warps split the rows and all read the
-//         whole tile: large verify blocks, and the shared prefix, where the
-//         rows of all sequences stand against one copy of K and V. Bound by
-//         the tensor cores.
+// One loop over 64-position tiles (cp.async ring in shared memory); a CTA's
+// warps split a tile's positions WP ways and the item's rows WR ways:
+//   4 x 1, 4 x 2  up to 8, 16 or 32 rows an item, the usual decode and verify
+//                 steps. Bound by the cache's bytes.
+//   2 x 4, 1 x 8  64 or 128 rows: large verify blocks, and the shared prefix,
+//                 where the rows of all sequences stand against one copy of K
+//                 and V. Bound by the tensor cores and what feeds them.
+// Warps of the same rows hold maxima, sums and outputs of their own positions,
+// which meet at the item's end.
 //
 // Work is cut by tiles, not by sequences: the tiles of all items (sequence,
 // kv head, row block) are numbered in one line and every CTA takes an equal
@@ -79,7 +79,7 @@ struct JoinP {
     int shared_units;           // tiles of a shared item
 };
 
-constexpr int AT = 128;  // threads of an attention CTA
+constexpr int JT = 128;  // threads of a joining CTA
 constexpr float LOG2E = 1.4426950408889634f, LN2 = 0.6931471805599453f;
 
 // units (tiles) of each CTA when `total` are shared out over `grid`
@@ -192,29 +192,30 @@ __device__ __forceinline__ uint32_t piece(uint32_t base, int row, int c) {
 }
 
 // RN: groups of 8 query rows a warp holds.
-template <int D, int FMT, bool SPLITQ, bool MANY, int RN>
+template <int D, int FMT, bool SPLITQ, int WP, int WR, int RN>
 struct Shape {
     static constexpr bool F8 = FMT != MK_KV_BF16;
     static constexpr int EB = F8 ? 1 : 2;                   // bytes of a cached value
     static constexpr int ROWB = D * EB;                     // bytes of a cached row
     static constexpr int SL = 16;                           // positions a warp takes at once
     static constexpr int TILE = 64;                         // positions of a tile
-    static constexpr int ROWS = MANY ? 4 * 8 * RN : 8 * RN; // query rows of an item
+    static constexpr int NT = 32 * WP * WR;                 // threads
+    static constexpr int ROWS = WR * 8 * RN;                // query rows of an item
     static constexpr int TILE_B = TILE * ROWB;              // bytes of K (or V) of a tile
     static constexpr int STAGE_B = 2 * TILE_B + (F8 ? 2 * TILE * 4 : 0);
     static constexpr int Q_B = ROWS * D * 2 * (SPLITQ ? 2 : 1);
-    static constexpr int MISC_B = 3072;
+    static constexpr int MISC_B = 4096;
     static constexpr int OREGS = RN * D / 4;                // registers of the output
-    static constexpr bool QREG = RN * D / 8 * (SPLITQ ? 2 : 1) <= 32;  // the queries stay in registers too
+    static constexpr bool QREG = RN * D / 8 * (SPLITQ ? 2 : 1) <= 16 || (NT == 128 && RN * D / 8 * (SPLITQ ? 2 : 1) <= 32);
     // CTAs an SM: what the registers allow, and at least two stages of the ring
-    static constexpr int WANT = OREGS <= 32 ? 4 : RN < 4 && OREGS <= 64 ? 3 : 2;
+    static constexpr int WANT = (OREGS <= 32 ? 4 : OREGS <= 64 ? 4 : 2) * 128 / NT;
     static constexpr int fit(int ctas) { return (227 * 1024 / ctas - 1024 - Q_B - MISC_B) / STAGE_B; }
-    static constexpr int CTAS = fit(WANT) >= 3 ? WANT : fit(3) >= 3 && WANT > 3 ? 3 : fit(2) >= 2 ? 2 : 1;
+    static constexpr int CTAS = WANT > 3 && fit(WANT) >= 3 ? WANT : WANT >= 3 && fit(3) >= 3 ? 3 : WANT >= 2 && fit(2) >= 2 ? 2 : 1;
     static constexpr int STAGES = fit(CTAS) > 4 ? 4 : fit(CTAS);
     static constexpr int RING_B = STAGES * STAGE_B;
     static constexpr int SMEM = RING_B + Q_B + MISC_B;
-    // the warps' outputs meet in the ring's memory (FEW)
-    static_assert(MANY || 4 * ROWS * D * 4 <= RING_B, "ring too small for the merge");
+    // the warps' outputs meet in the ring's memory
+    static_assert(WP == 1 || WP * ROWS * D * 4 <= RING_B, "ring too small for the merge");
     static_assert(STAGES >= 2 && SMEM <= 227 * 1024, "ring");
 };
 
@@ -222,7 +223,7 @@ struct Shape {
 template <int ROWS, int TILE>
 struct Misc {
     long long off[2][TILE];  // bytes after the head's first row; -1: no such row, zeros
-    long long scan[AT / 32];
+    long long scan[8];
     long long found_base;
     float slope2[ROWS];  // slope * log2 e
     float qscale[ROWS];  // 8-bit pages: the power of two taken out of the query
@@ -230,10 +231,11 @@ struct Misc {
     int found_b;
 };
 
-template <int D, int FMT, bool SPLITQ, bool MANY, int RN>
-__global__ void __launch_bounds__(AT, Shape<D, FMT, SPLITQ, MANY, RN>::CTAS)
+template <int D, int FMT, bool SPLITQ, int WP, int WR, int RN>
+__global__ void __launch_bounds__(32 * WP * WR, Shape<D, FMT, SPLITQ, WP, WR, RN>::CTAS)
     attend_kernel(const __grid_constant__ AttendP p) {
-    using S = Shape<D, FMT, SPLITQ, MANY, RN>;
+    using S = Shape<D, FMT, SPLITQ, WP, WR, RN>;
+    constexpr int AT = S::NT;
     constexpr bool F8 = S::F8;
     constexpr int ROWB = S::ROWB, TILE = S::TILE, SL = S::SL, ROWS = S::ROWS, DT = D / 16;
     using M = Misc<ROWS, TILE>;
@@ -400,7 +402,7 @@ __global__ void __launch_bounds__(AT, Shape<D, FMT, SPLITQ, MANY, RN>::CTAS)
             place(t + 1, next);
         }
         // ---- queries into shared memory, a warp a row
-        for (int r = warp; r < ROWS; r += 4) {
+        for (int r = warp; r < ROWS; r += AT / 32) {
             constexpr int E = D / 32;  // consecutive values of a lane
             float x[E];
 #pragma unroll
@@ -448,7 +450,7 @@ __global__ void __launch_bounds__(AT, Shape<D, FMT, SPLITQ, MANY, RN>::CTAS)
         __syncthreads();
 
         // ---- the warp's rows; a thread has rows 2 q4 and 2 q4 + 1 of each group of 8
-        const int wrow = MANY ? warp * 8 * RN : 0;
+        const int wrow = warp % WR * 8 * RN;
         int rlo[RN][2], rhi[RN][2];
         float f2[RN][2];  // score to exponent of 2 (without a cap: scale log2 e; with one: into tanh's exponential)
 #pragma unroll
@@ -515,7 +517,7 @@ __global__ void __launch_bounds__(AT, Shape<D, FMT, SPLITQ, MANY, RN>::CTAS)
             const float* const scales =
                 reinterpret_cast<const float*>(smem + (tile % S::STAGES) * S::STAGE_B + 2 * S::TILE_B);
 #pragma unroll 1
-            for (int s0 = MANY ? 0 : warp * SL; s0 < (MANY ? TILE : warp * SL + SL); s0 += SL) {
+            for (int s0 = warp / WR * (TILE / WP), s1 = s0 + TILE / WP; s0 < s1; s0 += SL) {
                 const int j0 = (t0 + tile) * TILE + s0;
                 if (j0 + SL <= lo_min || j0 >= hi_max) continue;  // no row sees any of it
                 const bool all_see = j0 >= lo_max && j0 + SL <= hi_min;
@@ -811,9 +813,8 @@ __global__ void __launch_bounds__(AT, Shape<D, FMT, SPLITQ, MANY, RN>::CTAS)
         cp_wait<0>();
         __syncthreads();  // the ring is free
         {
-            constexpr int RW = 8 * RN;  // rows of a warp
-            // MANY: a warp's rows one group of 8 after another through the warp's own 8 rows of memory;
-            // FEW: all four warps' rows side by side
+            // WP = 1: a warp's rows one group of 8 after another through the warp's own 8 rows of memory;
+            // else the parts of all rows side by side
             float* om = reinterpret_cast<float*>(smem);
             float* oml = reinterpret_cast<float*>(qmem);  // the queries are done with
             auto store = [&](int n, int at_row) {
@@ -833,22 +834,22 @@ __global__ void __launch_bounds__(AT, Shape<D, FMT, SPLITQ, MANY, RN>::CTAS)
                     }
                 }
             };
-            if constexpr (!MANY) {
+            if constexpr (WP > 1) {
 #pragma unroll
-                for (int n = 0; n < RN; ++n) store(n, warp * RW + n * 8);
+                for (int n = 0; n < RN; ++n) store(n, warp / WR * ROWS + wrow + n * 8);
                 __syncthreads();
                 for (int i = tid; i < nrows * (D / 4); i += AT) {
                     const int r = i / (D / 4), d = (i % (D / 4)) * 4;
                     float mm = -INFINITY, ll = 0.f;
 #pragma unroll
-                    for (int w = 0; w < 4; ++w) mm = fmaxf(mm, oml[(w * RW + r) * 2]);
+                    for (int w = 0; w < WP; ++w) mm = fmaxf(mm, oml[(w * ROWS + r) * 2]);
                     const float ref = mm == -INFINITY ? 0.f : mm;
                     float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-                    for (int w = 0; w < 4; ++w) {
-                        const float f = ex2(oml[(w * RW + r) * 2] - ref);
-                        ll += oml[(w * RW + r) * 2 + 1] * f;
-                        const float4 z = *reinterpret_cast<const float4*>(om + (w * RW + r) * D + d);
+                    for (int w = 0; w < WP; ++w) {
+                        const float f = ex2(oml[(w * ROWS + r) * 2] - ref);
+                        ll += oml[(w * ROWS + r) * 2 + 1] * f;
+                        const float4 z = *reinterpret_cast<const float4*>(om + (w * ROWS + r) * D + d);
                         y.x += z.x * f, y.y += z.y * f, y.z += z.z * f, y.w += z.w * f;
                     }
                     put(r, d, y, mm, ll, d == 0);
@@ -879,7 +880,7 @@ __global__ void __launch_bounds__(AT, Shape<D, FMT, SPLITQ, MANY, RN>::CTAS)
 // rows without any piece get their zeros here. Reads the pieces from L2: a few
 // microseconds of latency.
 template <int D>
-__global__ void __launch_bounds__(AT) join_kernel(const __grid_constant__ JoinP jp) {
+__global__ void __launch_bounds__(JT) join_kernel(const __grid_constant__ JoinP jp) {
     constexpr int E = D / 32;
     __shared__ float om[4][D];
     __shared__ float2 oml[4];
@@ -963,7 +964,7 @@ __global__ void __launch_bounds__(AT) join_kernel(const __grid_constant__ JoinP 
     }
     const bool none = ll == 0.f;
     uint16_t* dst = p.out + b * p.ob + t * p.ot + hq * p.oh;
-    for (int d = threadIdx.x; d < D; d += AT) {
+    for (int d = threadIdx.x; d < D; d += JT) {
         const float y = om[0][d] * w[0] + om[1][d] * w[1] + om[2][d] * w[2] + om[3][d] * w[3];
         const float z = none ? 0.f : y / ll;
         dst[d] = p.f16 ? __half_as_ushort(__float2half_rn(z)) : __bfloat16_as_ushort(__float2bfloat16_rn(z));
@@ -975,28 +976,28 @@ __global__ void __launch_bounds__(AT) join_kernel(const __grid_constant__ JoinP 
 // Which kernel a call takes: format, whether queries need a lo part, rows.
 struct Kind {
     int format;
-    bool splitq, many;
-    int rn;  // groups of 8 rows a warp holds
+    bool splitq;
+    int rows;  // of an item: 8, 16, 32, 64 or, below 256 wide heads, 128
 };
 struct KindInfo {
     int tile, rows, ctas;  // positions of a tile, rows of an item, CTAs an SM
 };
 
 // A kernel by its template arguments, with what the host has to know of it.
-template <int D, int FMT, bool SPLITQ, bool MANY, int RN>
+template <int D, int FMT, bool SPLITQ, int WP, int WR, int RN>
 int attend_run(const AttendP* p, KindInfo* info, int grid, bool after, cudaStream_t s) {
-    using S = Shape<D, FMT, SPLITQ, MANY, RN>;
-    auto kern = attend_kernel<D, FMT, SPLITQ, MANY, RN>;
+    using S = Shape<D, FMT, SPLITQ, WP, WR, RN>;
+    auto kern = attend_kernel<D, FMT, SPLITQ, WP, WR, RN>;
     if (info) {
         info->tile = S::TILE;
         info->rows = S::ROWS;
         cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, S::SMEM);
-        if (e == cudaSuccess) e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&info->ctas, kern, AT, S::SMEM);
+        if (e == cudaSuccess) e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&info->ctas, kern, S::NT, S::SMEM);
         return cuda_status(e, "mk_pages_attend");
     }
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)grid);
-    cfg.blockDim = dim3(AT);
+    cfg.blockDim = dim3(S::NT);
     cfg.dynamicSmemBytes = S::SMEM;
     cfg.stream = s;
     cudaLaunchAttribute at[1];
@@ -1009,12 +1010,13 @@ int attend_run(const AttendP* p, KindInfo* info, int grid, bool after, cudaStrea
 
 template <int D, int FMT, bool SPLITQ>
 int attend_pick(const Kind& k, const AttendP* p, KindInfo* info, int grid, bool after, cudaStream_t s) {
-    if (k.many) return attend_run<D, FMT, SPLITQ, true, 2>(p, info, grid, after, s);
-    if constexpr (D <= 128) {
-        if (k.rn == 4) return attend_run<D, FMT, SPLITQ, false, 4>(p, info, grid, after, s);
+    if (k.rows == 8) return attend_run<D, FMT, SPLITQ, 4, 1, 1>(p, info, grid, after, s);
+    if (k.rows == 16) return attend_run<D, FMT, SPLITQ, 4, 1, 2>(p, info, grid, after, s);
+    if (k.rows == 32) return attend_run<D, FMT, SPLITQ, 4, 2, 2>(p, info, grid, after, s);
+    if constexpr (D < 256) {  // 128 rows of 256 leave no room for the ring
+        if (k.rows == 128) return attend_run<D, FMT, SPLITQ, 1, 8, 2>(p, info, grid, after, s);
     }
-    if (k.rn == 2) return attend_run<D, FMT, SPLITQ, false, 2>(p, info, grid, after, s);
-    return attend_run<D, FMT, SPLITQ, false, 1>(p, info, grid, after, s);
+    return attend_run<D, FMT, SPLITQ, 2, 4, 2>(p, info, grid, after, s);
 }
 
 // With `info`: what the host has to know of the kernel (and its one-time
@@ -1031,7 +1033,7 @@ template <int D>
 int join_d(const JoinP& j, unsigned rows, cudaStream_t s) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(rows);
-    cfg.blockDim = dim3(AT);
+    cfg.blockDim = dim3(JT);
     cfg.stream = s;
     cudaLaunchAttribute at[1];
     at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
