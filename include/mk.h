@@ -441,9 +441,9 @@ int mk_kv_view(const mk_kv* kv, int32_t layer, mk_pages* pages, mk_page_table* t
  * shared_len > 0 says that the first shared_len positions of all sequences
  * lie in the same pages (the first shared_len / page_size entries of every
  * table row are those of row 0; a multiple of page_size): they are read once
- * for the whole batch, as one product over all its queries. Sequences of
- * length 0 may be among them; every other one must be at least shared_len
- * long, shorter ones see the part they have. */
+ * for the whole batch, as one product over all its queries. Sequences whose
+ * tokens do not all see all of them (length 0, a later start, a length that
+ * ends inside) are read on their own, through their own table row. */
 typedef struct mk_attention {
     const mk_pages* pages;
     const mk_page_table* table;

@@ -28,8 +28,22 @@ int kind_info(int dev, int d, const Kind& k, KindInfo& out) {
     return MK_OK;
 }
 
+// the shared launch's own kernel, where there is one: up to 32 rows are bound
+// by the cache's bytes and leave most of its 128 rows empty
+int prefix_info(int dev, int d, int format, KindInfo& out) {
+    static bool have[MAX_DEV][2][3];
+    static std::mutex lock;
+    out = KindInfo{64, 128, 1};
+    std::lock_guard<std::mutex> g(lock);
+    if (dev < MAX_DEV && have[dev][d == 128][format]) return MK_OK;
+    const int rc = prefix_run(d, format, nullptr, 0, nullptr);
+    if (dev < MAX_DEV && !rc) have[dev][d == 128][format] = true;
+    return rc;
+}
+
 struct Plan {
     Kind own_k, sh_k;
+    bool prefix;
     KindInfo own_i, sh_i;
     int own_grid, sh_grid;  // sh_grid 0: nothing shared
     int own_rb, sh_rb;
@@ -82,7 +96,7 @@ int make_plan(const mk_attention* a, Plan& pl) {
     const int min_units = 2;
     const int64_t items = (int64_t)B * H * pl.own_rb;
     if (items > INT32_MAX / 4) return fail(MK_ERR_UNSUPPORTED, "attend: too many queries in one call");
-    const int64_t most = items * ((cap - a->shared_len + pl.own_i.tile - 1) / pl.own_i.tile + 1);
+    const int64_t most = items * ((cap + pl.own_i.tile - 1) / pl.own_i.tile + 1);
     int64_t grid = (int64_t)sms * pl.own_i.ctas;
     if (grid > (most + min_units - 1) / min_units) grid = (most + min_units - 1) / min_units;
     pl.own_grid = (int)grid;
@@ -95,7 +109,9 @@ int make_plan(const mk_attention* a, Plan& pl) {
     if (a->shared_len) {
         const int64_t all = (int64_t)B * rows;
         pl.sh_k = Kind{g.format, splitq, block_of(all)};
-        if (const int rc = kind_info(dev, D, pl.sh_k, pl.sh_i)) return rc;
+        pl.prefix = D <= 128 && a->q->dtype == MK_DT_BF16 && all > 32;
+        if (const int rc = pl.prefix ? prefix_info(dev, D, g.format, pl.sh_i) : kind_info(dev, D, pl.sh_k, pl.sh_i))
+            return rc;
         if (pl.sh_i.ctas < 1) return fail(MK_ERR_UNSUPPORTED, "attend: the kernel does not fit this device");
         pl.sh_rb = (int)((all + pl.sh_i.rows - 1) / pl.sh_i.rows);
         pl.sh_slot_rows = (int)(all < pl.sh_i.rows ? all : pl.sh_i.rows);
@@ -156,7 +172,9 @@ extern "C" int mk_pages_attend(const mk_attention* a, void* workspace, int64_t w
         q.slot_rows = pl.sh_slot_rows, q.slot_floats = pl.sh_floats, q.slots = (float*)(ws + pl.sh_off);
         j.shared = q, j.shared_grid = pl.sh_grid, j.shared_rows = pl.sh_i.rows;
         j.shared_units = (a->shared_len + pl.sh_i.tile - 1) / pl.sh_i.tile;
-        if (const int rc = fn(pl.sh_k, &q, nullptr, pl.sh_grid, false, s)) return rc;
+        if (const int rc = pl.prefix ? prefix_run(D, g.format, &q, pl.sh_grid, s)
+                                     : fn(pl.sh_k, &q, nullptr, pl.sh_grid, false, s))
+            return rc;
     }
     if (const int rc = fn(pl.own_k, &p, nullptr, pl.own_grid, pl.sh_grid > 0, s)) return rc;
     const unsigned rows = (unsigned)((int64_t)p.B * p.T * a->n_q_heads);

@@ -88,6 +88,13 @@ __host__ __device__ __forceinline__ long long units_each(long long total, int gr
     return e < min_units ? min_units : e;
 }
 
+// Whether all of sequence b's tokens see all of the shared positions: it takes
+// part in the shared launch. Others (padding, documents that start inside,
+// lengths that end inside) are read on their own, so that the shared launch
+// has no row that sees a part.
+__device__ __forceinline__ bool shares(const AttendP& p, int b) {
+    return p.shared > 0 && (long long)p.lens[b] - p.T + 1 >= p.shared && (!p.starts || p.starts[b] <= 0);
+}
 // the positions of sequence b that a launch covers, [lo, hi)
 __device__ __forceinline__ void cover(const AttendP& p, int b, int& lo, int& hi) {
     if (p.is_shared) {
@@ -95,9 +102,8 @@ __device__ __forceinline__ void cover(const AttendP& p, int b, int& lo, int& hi)
         hi = p.shared;
         return;
     }
-    const int cap = p.pps << p.ps_shift;
-    lo = max(p.starts ? p.starts[b] : 0, p.shared);
-    hi = min(p.lens[b], cap);
+    lo = shares(p, b) ? p.shared : max(p.starts ? p.starts[b] : 0, 0);
+    hi = min(p.lens[b], p.pps << p.ps_shift);
 }
 template <int TILE>
 __device__ __forceinline__ int cover_units(const AttendP& p, int b) {
@@ -385,8 +391,8 @@ __global__ void __launch_bounds__(32 * WP * WR, Shape<D, FMT, SPLITQ, WP, WR, RN
                 const int rbq = bt / p.T, t = bt - rbq * p.T;
                 const int len = p.lens[rbq];
                 at = len - p.T + t;
-                lo = max(p.starts ? p.starts[rbq] : 0, clo);
-                hi = min(min(at + 1, p.is_shared ? len : chi), chi);
+                lo = clo;
+                hi = p.is_shared ? (shares(p, rbq) ? chi : 0) : min(at + 1, chi);
                 if (p.slopes) sl = p.slopes[h * p.G + g] * LOG2E;
             }
             ms.lo[r] = lo;
@@ -1048,6 +1054,9 @@ typedef int (*AttendFn)(const Kind&, const AttendP*, KindInfo*, int, bool, cudaS
 int attend_64(const Kind&, const AttendP*, KindInfo*, int, bool, cudaStream_t);
 int attend_128(const Kind&, const AttendP*, KindInfo*, int, bool, cudaStream_t);
 int attend_256(const Kind&, const AttendP*, KindInfo*, int, bool, cudaStream_t);
+// the shared launch on the tensor memory (mk_prefix.cuh; head_dim 64 and 128,
+// bf16 queries): 128 rows an item, one CTA an SM. p NULL: one-time attributes.
+int prefix_run(int head_dim, int format, const AttendP* p, int grid, cudaStream_t s);
 int join_64(const JoinP&, unsigned, cudaStream_t);
 int join_128(const JoinP&, unsigned, cudaStream_t);
 int join_256(const JoinP&, unsigned, cudaStream_t);

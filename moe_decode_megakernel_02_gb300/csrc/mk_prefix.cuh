@@ -1,0 +1,584 @@
+// mk_prefix.cuh -- attention of a whole batch over positions that all its
+// sequences share, on the fifth-generation tensor cores.
+//
+// The rows of a kv head (every sequence's tokens and query heads of the group)
+// stand against one copy of K and V, 128 rows a CTA, 64 positions a tile:
+//   S = Q K^T   128 x 64, both operands in shared memory, S in tensor memory;
+//   P = 2^(x - m) per row, one thread a row (tensor memory gives a thread its
+//       row, so that no value crosses threads);
+//   O += P V    P as the tensor-memory operand, V from shared memory as it
+//       lies there (rows are the product's K: the transposed form), O in
+//       tensor memory for the item's whole stretch of tiles.
+// P goes in as bf16 hi + lo parts (16 bits of each probability) in two chains
+// of products. O is rescaled only when a row's maximum has risen by more than
+// 2^8 since its reference: until then probabilities up to 2^8 and their sum are
+// as exact as ones below 1.
+//
+// Warps 0-3: softmax, a row a thread; 4-7: loads (cp.async, or codes through
+// registers for 8-bit pages: E4M3 and INT8 codes are exact in bf16, the K
+// scale multiplies the score, the V scale the probability); 8: one thread
+// issues the products, S of the next tile before P V of this one, so that the
+// tensor cores work while the softmax does. All waits are on mbarriers with a
+// limit; a wait that runs out raises a flag that every role sees, and the CTA
+// leaves after freeing its tensor memory (MK_ERR_TIMEOUT in `status`).
+//
+// Bound by the softmax: 8192 exponentials a tile at 16 a cycle are 512 cycles,
+// the three products 768 at the bf16 rate. Work is cut as in mk_attend.cuh;
+// every piece goes to the workspace for the joining launch.
+#pragma once
+#include "mk_attend.cuh"
+
+namespace mkop {
+
+template <int D, int FMT>
+struct PrefixShape {
+    static constexpr bool F8 = FMT != MK_KV_BF16;
+    static constexpr int ROWS = 128, TILE = 64;
+    static constexpr int PANELS = D / 64;          // 128-byte wide panels of a row
+    static constexpr int Q_B = PANELS * ROWS * 128;
+    static constexpr int KV_B = PANELS * TILE * 128;  // K (or V) of a tile
+    static constexpr int STAGE_B = 2 * KV_B;
+    static constexpr int SCALE_B = 2 * TILE * 4;   // of a stage: K scales, V scales (8-bit pages)
+    static constexpr int STAGES = D == 128 ? 5 : 8;
+    static constexpr int SC_OFF = Q_B + STAGES * STAGE_B;
+    static constexpr int MISC_OFF = SC_OFF + STAGES * SCALE_B;
+    static constexpr int SMEM = MISC_OFF + 2048 + 1024;  // and room to align to 1024
+    static constexpr int NT = 288;
+    // tensor memory columns: S twice, P (hi, lo) twice, O
+    static constexpr int T_S = 0, T_P = 2 * TILE, T_O = T_P + 2 * TILE, T_ALL = 512;
+    static_assert(T_O + D <= T_ALL && SMEM <= 227 * 1024, "");
+};
+
+struct PrefixMisc {
+    unsigned long long kv_full[8], pv_done[8], s_full[2], s_free[2], p_ready[2], q_ready, drained;
+    unsigned tmem, abort;
+    long long off[2][64];  // where a tile's rows lie (bytes), -1: zeros
+};
+
+__device__ __forceinline__ void bar_init(unsigned long long* b, unsigned n) {
+    asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(sm32(b)), "r"(n) : "memory");
+}
+__device__ __forceinline__ void bar_arrive(unsigned long long* b) {
+    asm volatile("{\n\t.reg .b64 t;\n\tmbarrier.arrive.shared::cta.b64 t, [%0];\n\t}" ::"r"(sm32(b)) : "memory");
+}
+__device__ __forceinline__ bool bar_try(unsigned long long* b, unsigned parity) {
+    unsigned ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(sm32(b)), "r"(parity)
+        : "memory");
+    return ok;
+}
+constexpr long long PREFIX_WAIT_NS = 2000000000ll;  // no wait of a healthy launch comes near it
+__device__ __forceinline__ long long now_ns() {
+    long long t;
+    asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t));
+    return t;
+}
+// Waits for the phase of `parity` to end; false when it took too long, or
+// another role gave up.
+__device__ __forceinline__ bool bar_wait(unsigned long long* b, unsigned parity, volatile unsigned* abort) {
+    if (bar_try(b, parity)) return true;
+    const long long t0 = now_ns();
+    while (!bar_try(b, parity)) {
+        if (*abort) return false;
+        if (now_ns() - t0 > PREFIX_WAIT_NS) {
+            *abort = 1;
+            return false;
+        }
+    }
+    return true;
+}
+// the same for a whole warp, which goes on or gives up together
+__device__ __forceinline__ bool warp_wait(unsigned long long* b, unsigned parity, volatile unsigned* abort) {
+    return __all_sync(0xffffffffu, bar_wait(b, parity, abort));
+}
+
+// Shared-memory matrix descriptors: start address, leading and stride offsets
+// in 16-byte units, version 1, 128-byte swizzle.
+__device__ __forceinline__ uint64_t smem_desc(uint32_t addr, uint32_t lead, uint32_t stride) {
+    return (uint64_t)((addr & 0x3ffffu) >> 4) | (uint64_t)(lead >> 4) << 16 | (uint64_t)(stride >> 4) << 32 |
+           (uint64_t)1 << 46 | (uint64_t)2 << 61;
+}
+// bf16 x bf16 -> fp32, M rows, N columns; `b_rows`: B's rows are its K (MN-major)
+__host__ __device__ constexpr uint32_t mma_desc(int m, int n, bool b_rows) {
+    return 1u << 4 | 1u << 7 | 1u << 10 | (b_rows ? 1u << 16 : 0u) | (uint32_t)(n >> 3) << 17 | (uint32_t)(m >> 4) << 24;
+}
+__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t desc, bool add) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(desc), "r"((uint32_t)add)
+        : "memory");
+}
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t desc, bool add) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+        "r"(a), "l"(b), "r"(desc), "r"((uint32_t)add)
+        : "memory");
+}
+__device__ __forceinline__ void mma_commit(unsigned long long* b) {
+    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(sm32(b))
+                 : "memory");
+}
+__device__ __forceinline__ void tm_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void tm_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void tm_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+__device__ __forceinline__ void tm_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+// 32 columns of this thread's row
+__device__ __forceinline__ void tm_ld32(uint32_t (&r)[32], uint32_t a) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
+        "%15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
+          "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
+          "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+        : "r"(a));
+}
+__device__ __forceinline__ void tm_st32(uint32_t a, const uint32_t (&r)[32]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
+        "%15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};" ::"r"(a),
+        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+        "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]),
+        "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]),
+        "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+        : "memory");
+}
+
+// 16-byte piece c (of D/8) of row r in a 128-byte-swizzled operand of `rows` rows
+__device__ __forceinline__ uint32_t panel_at(uint32_t base, int rows, int r, int c) {
+    return base + (c >> 3) * rows * 128 + r * 128 + (((c & 7) ^ (r & 7)) << 4);
+}
+
+// Four codes as two bf16 pairs, exact. E4M3: sign, exponent and mantissa moved
+// to their bf16 places, times 2^(127 - 7), which also makes its subnormals
+// right; NaN codes (all seven low bits set) would come out as 480. INT8: code
+// + 128 as the mantissa of 2^23, minus 2^23 + 128.
+template <int FMT>
+__device__ __forceinline__ void codes_bf16(uint32_t w, uint32_t& lo, uint32_t& hi) {
+    if constexpr (FMT == MK_KV_E4M3) {
+        const uint32_t a = __byte_perm(w, 0, 0x1404), b = __byte_perm(w, 0, 0x3424);  // codes in the high bytes
+        const uint32_t x = (a & 0x80008000u) | (a >> 4 & 0x07f007f0u), y = (b & 0x80008000u) | (b >> 4 & 0x07f007f0u);
+        const uint32_t s = 0x7b807b80u;  // 2^120
+        const __nv_bfloat162 f = *reinterpret_cast<const __nv_bfloat162*>(&s);
+        const __nv_bfloat162 p = __hmul2(*reinterpret_cast<const __nv_bfloat162*>(&x), f);
+        const __nv_bfloat162 q = __hmul2(*reinterpret_cast<const __nv_bfloat162*>(&y), f);
+        lo = *reinterpret_cast<const uint32_t*>(&p);
+        hi = *reinterpret_cast<const uint32_t*>(&q);
+        if ((((w & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u) != 0) {
+            if ((w & 0x7fu) == 0x7fu) lo = (lo & 0xffff0000u) | 0x7fffu;
+            if ((w & 0x7f00u) == 0x7f00u) lo = (lo & 0xffffu) | 0x7fff0000u;
+            if ((w & 0x7f0000u) == 0x7f0000u) hi = (hi & 0xffff0000u) | 0x7fffu;
+            if ((w & 0x7f000000u) == 0x7f000000u) hi = (hi & 0xffffu) | 0x7fff0000u;
+        }
+    } else {
+        w ^= 0x80808080u;
+        auto whole = [&](unsigned sel) { return __uint_as_float(__byte_perm(w, 0x4b000000u, sel)) - 8388736.0f; };
+        lo = pack_bf16(whole(0x7440), whole(0x7441));
+        hi = pack_bf16(whole(0x7442), whole(0x7443));
+    }
+}
+
+template <int D, int FMT>
+__global__ void __launch_bounds__(288, 1) prefix_kernel(const __grid_constant__ AttendP p) {
+    using S = PrefixShape<D, FMT>;
+    constexpr bool F8 = S::F8;
+    constexpr int TILE = S::TILE, ROWS = S::ROWS;
+    extern __shared__ uint8_t raw_smem[];
+    uint8_t* const smem = raw_smem + ((1024u - (sm32(raw_smem) & 1023u)) & 1023u);
+    const uint32_t qs = sm32(smem), ring = qs + S::Q_B;
+    float* const scales = reinterpret_cast<float*>(smem + S::SC_OFF);
+    PrefixMisc& ms = *reinterpret_cast<PrefixMisc*>(smem + S::MISC_OFF);
+    static_assert(sizeof(PrefixMisc) <= 2048, "");
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    volatile unsigned* const abort = &ms.abort;
+
+    const int items = p.H * p.RB, n_t = (p.shared + TILE - 1) / TILE;
+    const long long total = (long long)items * n_t, per = units_each(total, gridDim.x, p.min_units);
+    const long long first = per * blockIdx.x, end = min(total, first + per);
+    if (first >= end) return;
+
+    if (tid == 0) {
+        for (int i = 0; i < S::STAGES; ++i) {
+            bar_init(&ms.kv_full[i], 128);
+            bar_init(&ms.pv_done[i], 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            bar_init(&ms.s_full[i], 1);
+            bar_init(&ms.s_free[i], 128);
+            bar_init(&ms.p_ready[i], 128);
+        }
+        bar_init(&ms.q_ready, 128);
+        bar_init(&ms.drained, 1);
+        ms.abort = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    if (warp == 8) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(sm32(&ms.tmem)),
+                     "n"(S::T_ALL)
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    }
+    tm_before();
+    __syncthreads();
+    tm_after();
+    const uint32_t tm = ms.tmem;
+
+    // Tiles are counted over all pieces (c): tile c uses stage c % STAGES, S and P buffer c & 1.
+    if (warp < 4) {
+        // ================ softmax, a row a thread ================
+        const uint32_t my = tm + ((uint32_t)(warp * 32) << 16);
+        long long c = 0;
+        unsigned piece_no = 0;
+        for (long long u = first; u < end; ++piece_no) {
+            const int item = (int)(u / n_t), off = (int)(u % n_t), take = (int)min((long long)(n_t - off), end - u);
+            const int h = item / p.RB, rb = item - h * p.RB;
+            const long long row = (long long)rb * ROWS + tid;
+            const bool real = row < p.rows_item;
+            const int bt = real ? (int)(row / p.G) : 0, g = real ? (int)(row - (long long)bt * p.G) : 0;
+            const int b = bt / p.T, t = bt - b * p.T;
+            const bool live = real && shares(p, b);
+            // the row's query; every product that read the last one has ended (its S came)
+            {
+                const uint16_t* src = p.q + b * p.qb + t * p.qt + (long long)(h * p.G + g) * p.qh;
+                const bool wide = ((uintptr_t)src & 15) == 0;
+#pragma unroll
+                for (int i = 0; i < D / 8; ++i) {
+                    uint4 x = make_uint4(0, 0, 0, 0);
+                    if (live) {
+                        if (wide) {
+                            x = *reinterpret_cast<const uint4*>(src + 8 * i);
+                        } else {
+                            uint32_t w[4];
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) w[e] = src[8 * i + 2 * e] | (uint32_t)src[8 * i + 2 * e + 1] << 16;
+                            x = make_uint4(w[0], w[1], w[2], w[3]);
+                        }
+                    }
+                    *reinterpret_cast<uint4*>(smem + (panel_at(qs, ROWS, tid, i) - qs)) = x;
+                }
+                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                bar_arrive(&ms.q_ready);
+            }
+            const float scale2 = p.scale * LOG2E, cap2 = p.cap * LOG2E, in2 = p.cap > 0.f ? p.scale * 2.f * LOG2E / p.cap : 0.f;
+            const float slope2 = p.slopes ? p.slopes[h * p.G + g] * LOG2E : 0.f;
+            const int at = live ? p.lens[b] - p.T + t : 0;
+            float m = -INFINITY, l = 0.f;
+            bool ok = true;
+            for (int i = 0; i < take && ok; ++i, ++c) {
+                const int buf = (int)(c & 1), stage = (int)(c % S::STAGES);
+                const int j0 = (off + i) * TILE;
+                if (!(ok = warp_wait(&ms.s_full[buf], (unsigned)(c >> 1) & 1u, abort))) break;
+                tm_after();
+                uint32_t s0[32], s1[32];
+                tm_ld32(s0, my + S::T_S + buf * TILE);
+                tm_ld32(s1, my + S::T_S + buf * TILE + 32);
+                tm_wait_ld();
+                tm_before();
+                bar_arrive(&ms.s_free[buf]);
+                const float* ksc = scales + stage * 2 * TILE;
+                // the scales come with the tile
+                if (F8 && !(ok = warp_wait(&ms.kv_full[stage], (unsigned)(c / S::STAGES) & 1u, abort))) break;
+                if constexpr (F8) {
+#pragma unroll
+                    for (int j = 0; j < 32; j += 4) {
+                        const float4 a = *reinterpret_cast<const float4*>(ksc + j);
+                        const float4 e = *reinterpret_cast<const float4*>(ksc + 32 + j);
+                        s0[j] = __float_as_uint(__uint_as_float(s0[j]) * a.x), s0[j + 1] = __float_as_uint(__uint_as_float(s0[j + 1]) * a.y);
+                        s0[j + 2] = __float_as_uint(__uint_as_float(s0[j + 2]) * a.z), s0[j + 3] = __float_as_uint(__uint_as_float(s0[j + 3]) * a.w);
+                        s1[j] = __float_as_uint(__uint_as_float(s1[j]) * e.x), s1[j + 1] = __float_as_uint(__uint_as_float(s1[j + 1]) * e.y);
+                        s1[j + 2] = __float_as_uint(__uint_as_float(s1[j + 2]) * e.z), s1[j + 3] = __float_as_uint(__uint_as_float(s1[j + 3]) * e.w);
+                    }
+                }
+                auto shape = [&](uint32_t& v, int j) {
+                    float x = __uint_as_float(v);
+                    x = p.cap > 0.f ? cap2 - 2.f * cap2 * rcp(ex2(x * in2) + 1.f) : x * scale2;
+                    if (p.slopes) x -= slope2 * (float)(at - j0 - j);
+                    v = __float_as_uint(x);
+                };
+                if (p.cap > 0.f || p.slopes) {
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) shape(s0[j], j), shape(s1[j], 32 + j);
+                } else {
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) {
+                        s0[j] = __float_as_uint(__uint_as_float(s0[j]) * scale2);
+                        s1[j] = __float_as_uint(__uint_as_float(s1[j]) * scale2);
+                    }
+                }
+                if (j0 + TILE > p.shared) {
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) {
+                        if (j0 + j >= p.shared) s0[j] = 0xff800000u;
+                        if (j0 + 32 + j >= p.shared) s1[j] = 0xff800000u;
+                    }
+                }
+                float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+                for (int j = 0; j < 32; ++j) top[j & 3] = fmaxf(top[j & 3], fmaxf(__uint_as_float(s0[j]), __uint_as_float(s1[j])));
+                const float mx = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
+                // the reference: the first tile's maximum, or a new one past 2^8 of the old
+                const bool rise = i == 0 || mx > m + 8.f;
+                if (i == 0) {
+                    m = mx;
+                } else if (__any_sync(0xffffffffu, rise)) {
+                    const float mn = rise ? mx : m;
+                    const float f = ex2((m == -INFINITY ? (mn == -INFINITY ? 0.f : -INFINITY) : m) - (mn == -INFINITY ? 0.f : mn));
+                    m = mn;
+                    l *= f;
+                    // every product so far is in O
+                    if (!(ok = warp_wait(&ms.pv_done[(c - 1) % S::STAGES], (unsigned)((c - 1) / S::STAGES) & 1u, abort))) break;
+                    tm_after();
+#pragma unroll 1
+                    for (int d = 0; d < D; d += 32) {
+                        uint32_t o[32];
+                        tm_ld32(o, my + S::T_O + d);
+                        tm_wait_ld();
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+                        tm_st32(my + S::T_O + d, o);
+                    }
+                    tm_wait_st();
+                }
+                const float ref = m == -INFINITY ? 0.f : m;
+                float sum[4] = {0.f, 0.f, 0.f, 0.f};
+                uint32_t hi[32], lo[32];
+                auto pair = [&](uint32_t a, uint32_t b2, float va, float vb, uint32_t& ph, uint32_t& pl, float& s) {
+                    float x = ex2(__uint_as_float(a) - ref), y = ex2(__uint_as_float(b2) - ref);
+                    s += x + y;
+                    if constexpr (F8) x *= va, y *= vb;
+                    ph = pack_bf16(x, y);
+                    pl = pack_bf16(x - bf2f(ph & 0xffffu), y - __uint_as_float(ph & 0xffff0000u));
+                };
+#pragma unroll
+                for (int j = 0; j < 16; j += 2) {
+                    float4 va = make_float4(1.f, 1.f, 1.f, 1.f), vb = va;
+                    if constexpr (F8) {
+                        va = *reinterpret_cast<const float4*>(ksc + TILE + 2 * j);
+                        vb = *reinterpret_cast<const float4*>(ksc + TILE + 32 + 2 * j);
+                    }
+                    pair(s0[2 * j], s0[2 * j + 1], va.x, va.y, hi[j], lo[j], sum[0]);
+                    pair(s0[2 * j + 2], s0[2 * j + 3], va.z, va.w, hi[j + 1], lo[j + 1], sum[1]);
+                    pair(s1[2 * j], s1[2 * j + 1], vb.x, vb.y, hi[16 + j], lo[16 + j], sum[2]);
+                    pair(s1[2 * j + 2], s1[2 * j + 3], vb.z, vb.w, hi[17 + j], lo[17 + j], sum[3]);
+                }
+                l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+                // the P buffer is free when the product two tiles ago has read it
+                if (c >= 2 && !(ok = warp_wait(&ms.pv_done[(c - 2) % S::STAGES], (unsigned)((c - 2) / S::STAGES) & 1u, abort))) break;
+                tm_after();
+                tm_st32(my + S::T_P + buf * TILE, hi);
+                tm_st32(my + S::T_P + buf * TILE + 32, lo);
+                tm_wait_st();
+                tm_before();
+                bar_arrive(&ms.p_ready[buf]);
+            }
+            if (!ok) break;
+            // ---- the piece: O out of tensor memory
+            if (!warp_wait(&ms.pv_done[(c - 1) % S::STAGES], (unsigned)((c - 1) / S::STAGES) & 1u, abort)) break;
+            tm_after();
+            const bool whole = take == n_t;
+            float* slot = p.slots + (whole ? 2ll * gridDim.x + item : 2ll * blockIdx.x + (u == first ? 0 : 1)) * p.slot_floats;
+#pragma unroll 1
+            for (int d = 0; d < D; d += 32) {
+                uint32_t o[32];
+                tm_ld32(o, my + S::T_O + d);
+                tm_wait_ld();
+                if (real) {
+#pragma unroll
+                    for (int e = 0; e < 32; e += 4)
+                        *reinterpret_cast<uint4*>(slot + (long long)tid * D + d + e) = make_uint4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+                }
+            }
+            tm_before();
+            if (real)
+                *reinterpret_cast<float2*>(slot + (long long)p.slot_rows * D + 2 * tid) =
+                    live ? make_float2(m, l) : make_float2(-INFINITY, 0.f);
+            u += take;
+        }
+    } else if (warp < 8) {
+        // ================ loads ================
+        const int t = tid - 128;
+        const int mask = (1 << p.ps_shift) - 1;
+        constexpr int CH = D * (F8 ? 1 : 2) / 16;  // 16-byte pieces of a cached row
+        constexpr int EACH = TILE * CH / 128;      // pieces of K (and of V) a thread copies
+        constexpr int LAG = F8 ? 1 : S::STAGES - 2;  // tiles in flight
+        const int cc = t % CH;
+        const long long tiles = end - first;
+        auto arrived = [&](long long c) {  // this thread's part of tile c lies in shared memory
+            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+            bar_arrive(&ms.kv_full[c % S::STAGES]);
+        };
+        auto look = [&](long long c) {  // where row t of tile c lies, and its scales
+            if (t < TILE && c < tiles) {
+                const int pos = (int)((first + c) % n_t) * TILE + t;
+                int page = -1;
+                if (pos < p.shared) {
+                    page = p.table[pos >> p.ps_shift];
+                    if ((unsigned)page >= (unsigned)p.n_pages) {
+                        page = -1;
+                        if (p.status) *p.status = MK_ERR_INVALID_ARG;
+                    }
+                }
+                return page;
+            }
+            return -1;
+        };
+        auto note = [&](long long c, int page) {
+            if (t < TILE && c < tiles) {
+                const int r = ((int)((first + c) % n_t) * TILE + t) & mask;
+                ms.off[c & 1][t] = page < 0 ? -1 : page * p.page_b + r * p.row_b;
+            }
+        };
+        int page = look(0);
+        note(0, page);
+        asm volatile("bar.sync 1, 128;" ::: "memory");
+        bool ok = true;
+        for (long long c = 0; c < tiles; ++c) {
+            const int stage = (int)(c % S::STAGES);
+            const int h = (int)((first + c) / n_t) / p.RB;
+            const uint8_t* const kh = p.k + h * p.head_b;
+            const uint8_t* const vh = p.v + h * p.head_b;
+            const uint32_t st = ring + stage * S::STAGE_B;
+            float sk = 0.f, sv = 0.f;
+            if constexpr (F8) {
+                if (t < TILE && page >= 0) {
+                    const int r = ((int)((first + c) % n_t) * TILE + t) & mask;
+                    const long long o = page * p.sc_page + h * p.sc_head + r;
+                    sk = p.ks[o], sv = p.vs[o];
+                }
+            }
+            const int next = look(c + 1);
+            // a thread that gave up keeps the loop's barriers
+            auto free_stage = [&] {
+                if (ok && c >= S::STAGES) ok = bar_wait(&ms.pv_done[stage], (unsigned)(c / S::STAGES - 1) & 1u, abort);
+            };
+            if constexpr (!F8) {
+                free_stage();
+                if (ok) {
+#pragma unroll
+                    for (int i = 0; i < EACH; ++i) {
+                        const int r = t / CH + i * (128 / CH);
+                        const long long o = ms.off[c & 1][r];
+                        const bool in = o >= 0;
+                        const long long a = in ? o + cc * 16 : 0;
+                        cp16(panel_at(st, TILE, r, cc), kh + a, in);
+                        cp16(panel_at(st + S::KV_B, TILE, r, cc), vh + a, in);
+                    }
+                }
+                cp_commit();
+                if (ok && c >= LAG) {
+                    cp_wait<LAG>();
+                    arrived(c - LAG);
+                }
+            } else {
+                uint4 k[EACH], v[EACH];
+#pragma unroll
+                for (int i = 0; i < EACH; ++i) {
+                    const int r = t / CH + i * (128 / CH);
+                    const long long o = ms.off[c & 1][r];
+                    k[i] = v[i] = make_uint4(0, 0, 0, 0);
+                    if (o >= 0) {
+                        k[i] = __ldg(reinterpret_cast<const uint4*>(kh + o + cc * 16));
+                        v[i] = __ldg(reinterpret_cast<const uint4*>(vh + o + cc * 16));
+                    }
+                }
+                free_stage();
+                auto put = [&](uint32_t base, int r, const uint4& w) {
+                    uint4 a, b;
+                    codes_bf16<FMT>(w.x, a.x, a.y);
+                    codes_bf16<FMT>(w.y, a.z, a.w);
+                    codes_bf16<FMT>(w.z, b.x, b.y);
+                    codes_bf16<FMT>(w.w, b.z, b.w);
+                    *reinterpret_cast<uint4*>(smem + (panel_at(base, TILE, r, 2 * cc) - qs)) = a;
+                    *reinterpret_cast<uint4*>(smem + (panel_at(base, TILE, r, 2 * cc + 1) - qs)) = b;
+                };
+                if (ok) {
+#pragma unroll
+                    for (int i = 0; i < EACH; ++i) {
+                        const int r = t / CH + i * (128 / CH);
+                        put(st, r, k[i]);
+                        put(st + S::KV_B, r, v[i]);
+                    }
+                    if (t < TILE) {
+                        scales[stage * 2 * TILE + t] = sk;
+                        scales[stage * 2 * TILE + TILE + t] = sv;
+                    }
+                    arrived(c);
+                }
+            }
+            note(c + 1, next);
+            page = next;
+            asm volatile("bar.sync 1, 128;" ::: "memory");
+        }
+        if constexpr (!F8) {
+            cp_wait<0>();
+            if (ok)
+                for (long long c = max(0ll, tiles - LAG); c < tiles; ++c) arrived(c);
+        }
+    } else if (lane == 0) {
+        // ================ products ================
+        // (the other lanes wait below)
+        constexpr uint32_t QK = mma_desc(ROWS, TILE, false), PV = mma_desc(ROWS, D, true);
+        auto scores = [&](long long c) {  // S of tile c
+            const uint32_t k = ring + (uint32_t)(c % S::STAGES) * S::STAGE_B;
+#pragma unroll
+            for (int i = 0; i < D / 16; ++i) {
+                const uint32_t in = (uint32_t)(i & 3) * 32;
+                mma_ss(tm + S::T_S + (uint32_t)(c & 1) * TILE, smem_desc(qs + (i >> 2) * ROWS * 128 + in, 16, 1024),
+                       smem_desc(k + (i >> 2) * TILE * 128 + in, 16, 1024), QK, i > 0);
+            }
+            mma_commit(&ms.s_full[c & 1]);
+        };
+        long long c = 0;
+        unsigned piece_no = 0;
+        bool ok = true;
+        for (long long u = first; u < end && ok; ++piece_no) {
+            const int off = (int)(u % n_t), take = (int)min((long long)(n_t - off), end - u);
+            if (!(ok = bar_wait(&ms.q_ready, piece_no & 1u, abort))) break;
+            for (int i = -1; i < take && ok; ++i) {
+                if (i + 1 < take) {
+                    const long long n = c + i + 1;
+                    // K and V are here; the softmax has read what the S buffer held two tiles ago
+                    ok = bar_wait(&ms.kv_full[n % S::STAGES], (unsigned)(n / S::STAGES) & 1u, abort) &&
+                         (n < 2 || bar_wait(&ms.s_free[n & 1], (unsigned)((n >> 1) - 1) & 1u, abort));
+                    if (!ok) break;
+                    tm_after();
+                    scores(n);
+                }
+                if (i < 0) continue;
+                const long long n = c + i;
+                if (!(ok = bar_wait(&ms.p_ready[n & 1], (unsigned)(n >> 1) & 1u, abort))) break;
+                tm_after();
+                const uint32_t v = ring + (uint32_t)(n % S::STAGES) * S::STAGE_B + S::KV_B;
+                const uint32_t pa = tm + S::T_P + (uint32_t)(n & 1) * TILE;
+#pragma unroll
+                for (int part = 0; part < 2; ++part)
+#pragma unroll
+                    for (int k = 0; k < TILE / 16; ++k)
+                        mma_ts(tm + S::T_O, pa + part * 32 + k * 8, smem_desc(v + k * 2048, TILE * 128, 1024), PV,
+                               i > 0 || part > 0 || k > 0);
+                mma_commit(&ms.pv_done[n % S::STAGES]);
+            }
+            c += take;
+            u += take;
+        }
+        // the last products end before the tensor memory goes, also when a role gave up
+        mma_commit(&ms.drained);
+        const long long t0 = now_ns();
+        while (!bar_try(&ms.drained, 0) && now_ns() - t0 < PREFIX_WAIT_NS) {
+        }
+    }
+    __syncwarp();
+    tm_before();
+    __syncthreads();
+    tm_after();
+    if (tid == 0 && ms.abort && p.status) *p.status = MK_ERR_TIMEOUT;
+    if (warp == 8)
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tm), "n"(S::T_ALL) : "memory");
+}
+
+}  // namespace mkop

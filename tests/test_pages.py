@@ -621,3 +621,52 @@ def test_a_models_own_cache_is_read_in_place():
         cache.write(view.table, ints(0, 0), k, v)
         out8, lse8 = cache.attend(view.table, ints(ctx + 1, ctx + 1), q, return_lse=True)
         check(cache, view.table, ints(ctx + 1, ctx + 1), q, out8, lse8, 1 / math.sqrt(D))
+
+
+@gpu
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("B,T,Hq,H,ps,shared", [(40, 1, 2, 2, 64, 64), (17, 2, 8, 2, 32, 1984), (70, 1, 12, 3, 16, 6160)])
+def test_long_shared_prefixes(fmt, D, B, T, Hq, H, ps, shared):
+    """One tile, several turns of the ring, several pieces a CTA; scores that keep rising, so that maxima move late."""
+    lens = [shared + T - 1 + (7 * b) % 40 for b in range(B)]
+    lens[B // 2] = 0
+    lens[B // 3] = shared // 2  # ends inside: read on its own
+    cache, table, n, q = build(fmt, torch.bfloat16, B, T, Hq, H, D, ps, lens, shared=shared)
+    rise = torch.linspace(0.1, 2.5, shared // ps, device="cuda")
+    pg = table[0, :shared // ps].long()
+    if fmt == torch.bfloat16:
+        cache.k[pg] = (cache.k[pg].float() * rise[:, None, None, None]).to(fmt)
+    else:
+        cache.k_scale[pg] *= rise[:, None, None]
+        cache.v_scale[pg] *= rise.flip(0)[:, None, None]
+    scale = 1 / math.sqrt(D)
+    status = ints(0)
+    for kw in (dict(), dict(softcap=15.0, slopes=torch.linspace(0.001, 0.02, Hq, device="cuda"))):
+        out, lse = cache.attend(table, n, q, shared_len=shared, return_lse=True, status=status, **kw)
+        check(cache, table, n, q, out, lse, scale, **kw)
+        assert torch.equal(out, cache.attend(table, n, q, shared_len=shared, **kw))
+    assert int(status) == 0
+
+
+@gpu
+def test_non_finite_values_in_a_shared_prefix_stay_with_who_sees_them():
+    B, Hq, H, D, ps, shared = 40, 4, 2, 128, 64, 192
+    lens = [shared + 5 + b for b in range(B)]
+    lens[3], lens[7] = 100, 0  # ends inside the prefix; padded
+    for fmt in FORMATS:
+        cache, table, n, q = build(fmt, torch.bfloat16, B, 1, Hq, H, D, ps, lens, shared=shared)
+        clean = cache.attend(table, n, q, shared_len=shared)
+        pg = int(table[0, 2])  # positions 128 .. 191
+        if fmt == torch.bfloat16:
+            cache.v[pg, :, 9, 40] = math.nan
+        elif fmt == torch.int8:
+            cache.v_scale[pg, :, 9] = math.nan
+        else:
+            cache.v.view(torch.uint8)[pg, :, 9, 40] = 0xFF
+        out = cache.attend(table, n, q, shared_len=shared)
+        assert torch.equal(out[3], clean[3]) and bool((out[7] == 0).all())
+        others = [b for b in range(B) if b not in (3, 7)]
+        assert bool(torch.isnan(out[others][..., 40]).all())
+        if fmt != torch.int8:
+            assert bool(torch.isfinite(out[others][..., :40]).all())
