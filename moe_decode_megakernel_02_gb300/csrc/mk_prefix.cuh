@@ -14,10 +14,10 @@
 // 2^8 since its reference: until then probabilities up to 2^8 and their sum are
 // as exact as ones below 1.
 //
-// Warps 0-3: softmax, a row a thread; 4-7: loads (cp.async, or codes through
-// registers for 8-bit pages: E4M3 and INT8 codes are exact in bf16, the K
-// scale multiplies the score, the V scale the probability); 8: one thread
-// issues the products, S of the next tile before P V of this one, so that the
+// Warps 0-3: softmax, a row a thread; 4-7: loads (bf16 pages: one thread, by
+// tensor maps; 8-bit pages: codes through registers, as E4M3 and INT8 codes are
+// exact in bf16; the K scale multiplies the score, the V scale the
+// probability); 8: one thread issues the products, S of the next tile before P V of this one, so that the
 // tensor cores work while the softmax does. All waits are on mbarriers with a
 // limit; a wait that runs out raises a flag that every role sees, and the CTA
 // leaves after freeing its tensor memory (MK_ERR_TIMEOUT in `status`).
@@ -26,6 +26,8 @@
 // the three products 768 at the bf16 rate. Work is cut as in mk_attend.cuh;
 // every piece goes to the workspace for the joining launch.
 #pragma once
+#include <cuda.h>
+
 #include "mk_attend.cuh"
 
 namespace mkop {
@@ -100,6 +102,10 @@ __device__ __forceinline__ bool warp_wait(unsigned long long* b, unsigned parity
 __device__ __forceinline__ uint64_t smem_desc(uint32_t addr, uint32_t lead, uint32_t stride) {
     return (uint64_t)((addr & 0x3ffffu) >> 4) | (uint64_t)(lead >> 4) << 16 | (uint64_t)(stride >> 4) << 32 |
            (uint64_t)1 << 46 | (uint64_t)2 << 61;
+}
+// the same further on in the same operand
+__device__ __forceinline__ uint64_t desc_on(uint64_t d, uint32_t bytes) {
+    return (d & 0xffffffff00000000ull) | ((uint32_t)d + (bytes >> 4));
 }
 // bf16 x bf16 -> fp32, M rows, N columns; `b_rows`: B's rows are its K (MN-major)
 __host__ __device__ constexpr uint32_t mma_desc(int m, int n, bool b_rows) {
@@ -183,8 +189,26 @@ __device__ __forceinline__ void codes_bf16(uint32_t w, uint32_t& lo, uint32_t& h
     }
 }
 
+// K and V as tensors [page][kv head][row][value] (bf16 pages)
+struct PrefixMaps {
+    CUtensorMap k, v;
+};
+__device__ __forceinline__ void tma_rows(uint32_t dst, const CUtensorMap* map, int x, int row, int head, int page,
+                                         unsigned long long* bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, "
+        "%5}], [%6];" ::"r"(dst),
+        "l"(map), "r"(x), "r"(row), "r"(head), "r"(page), "r"(sm32(bar))
+        : "memory");
+}
+__device__ __forceinline__ void bar_expect(unsigned long long* b, unsigned bytes) {
+    asm volatile("{\n\t.reg .b64 t;\n\tmbarrier.arrive.expect_tx.shared::cta.b64 t, [%0], %1;\n\t}" ::"r"(sm32(b)),
+                 "r"(bytes)
+                 : "memory");
+}
+
 template <int D, int FMT>
-__global__ void __launch_bounds__(288, 1) prefix_kernel(const __grid_constant__ AttendP p) {
+__global__ void __launch_bounds__(288, 1) prefix_kernel(const __grid_constant__ AttendP p, const __grid_constant__ PrefixMaps maps) {
     using S = PrefixShape<D, FMT>;
     constexpr bool F8 = S::F8;
     constexpr int TILE = S::TILE, ROWS = S::ROWS;
@@ -204,7 +228,7 @@ __global__ void __launch_bounds__(288, 1) prefix_kernel(const __grid_constant__ 
 
     if (tid == 0) {
         for (int i = 0; i < S::STAGES; ++i) {
-            bar_init(&ms.kv_full[i], 128);
+            bar_init(&ms.kv_full[i], F8 ? 128 : 1);
             bar_init(&ms.pv_done[i], 1);
         }
         for (int i = 0; i < 2; ++i) {
@@ -399,13 +423,64 @@ __global__ void __launch_bounds__(288, 1) prefix_kernel(const __grid_constant__ 
                     live ? make_float2(m, l) : make_float2(-INFINITY, 0.f);
             u += take;
         }
+    } else if (!F8 && warp < 8) {
+        // ================ loads by tensor maps: one warp ================
+        if (warp == 4) {
+            // A tile is `parts` boxes of up to 64 rows of one page. The lanes hold the pages of the next 32 boxes,
+            // and of the 32 after them.
+            const int rows = min(TILE, 1 << p.ps_shift), parts = TILE / rows, mask = (1 << p.ps_shift) - 1;
+            const long long tiles = end - first, boxes = tiles * parts;
+            auto page_of = [&](long long i) {  // of box i; one that does not exist reads as zeros
+                if (i >= boxes) return p.n_pages;
+                const int pos = (int)((first + i / parts) % n_t) * TILE + (int)(i % parts) * rows;
+                if (pos >= p.shared) return p.n_pages;
+                const int page = p.table[pos >> p.ps_shift];
+                if ((unsigned)page < (unsigned)p.n_pages) return page;
+                if (p.status) *p.status = MK_ERR_INVALID_ARG;
+                return p.n_pages;
+            };
+            int now = page_of(lane), next = page_of(32 + lane);
+            bool ok = true;
+            long long box = 0;
+            for (long long c = 0; c < tiles && ok; ++c) {
+                const int stage = (int)(c % S::STAGES);
+                const int h = (int)((first + c) / n_t) / p.RB, j0 = (int)((first + c) % n_t) * TILE;
+                const uint32_t st = ring + stage * S::STAGE_B;
+                if (c >= S::STAGES) ok = warp_wait(&ms.pv_done[stage], (unsigned)(c / S::STAGES - 1) & 1u, abort);
+                if (!ok) break;
+                if (lane == 0) bar_expect(&ms.kv_full[stage], S::STAGE_B);
+                for (int i = 0; i < parts; ++i, ++box) {
+                    const int page = __shfl_sync(0xffffffffu, now, (int)(box & 31));
+                    if (lane == 0) {
+                        const int row = (j0 + i * rows) & mask;
+#pragma unroll
+                        for (int x = 0; x < S::PANELS; ++x) {
+                            const uint32_t to = st + x * TILE * 128 + i * rows * 128;
+                            tma_rows(to, &maps.k, x * 64, row, h, page, &ms.kv_full[stage]);
+                            tma_rows(to + S::KV_B, &maps.v, x * 64, row, h, page, &ms.kv_full[stage]);
+                        }
+                    }
+                    if ((box & 31) == 31) {
+                        now = next;
+                        next = page_of(box + 33 + lane);
+                    }
+                }
+            }
+            // a launch that gave up still waits for its copies on the way
+            if (!ok) {
+                const long long t0 = now_ns();
+                const long long to = box / parts;  // tiles sent
+                for (long long c = max(0ll, to - S::STAGES); c < to; ++c)
+                    while (!bar_try(&ms.kv_full[c % S::STAGES], (unsigned)(c / S::STAGES) & 1u) && now_ns() - t0 < PREFIX_WAIT_NS) {
+                    }
+            }
+        }
     } else if (warp < 8) {
-        // ================ loads ================
+        // ================ loads of codes ================
         const int t = tid - 128;
         const int mask = (1 << p.ps_shift) - 1;
         constexpr int CH = D * (F8 ? 1 : 2) / 16;  // 16-byte pieces of a cached row
         constexpr int EACH = TILE * CH / 128;      // pieces of K (and of V) a thread copies
-        constexpr int LAG = F8 ? 1 : S::STAGES - 2;  // tiles in flight
         const int cc = t % CH;
         const long long tiles = end - first;
         auto arrived = [&](long long c) {  // this thread's part of tile c lies in shared memory
@@ -433,60 +508,44 @@ __global__ void __launch_bounds__(288, 1) prefix_kernel(const __grid_constant__ 
                 ms.off[c & 1][t] = page < 0 ? -1 : page * p.page_b + r * p.row_b;
             }
         };
-        int page = look(0);
+        // pages two tiles ahead of their use, 8-bit codes and scales one: each is a trip to memory
+        int page = look(0), next = look(1);
         note(0, page);
         asm volatile("bar.sync 1, 128;" ::: "memory");
-        bool ok = true;
-        for (long long c = 0; c < tiles; ++c) {
-            const int stage = (int)(c % S::STAGES);
-            const int h = (int)((first + c) / n_t) / p.RB;
-            const uint8_t* const kh = p.k + h * p.head_b;
-            const uint8_t* const vh = p.v + h * p.head_b;
-            const uint32_t st = ring + stage * S::STAGE_B;
-            float sk = 0.f, sv = 0.f;
+        uint4 k[F8 ? EACH : 1], v[F8 ? EACH : 1];
+        float sk = 0.f, sv = 0.f;
+        auto codes = [&](long long c, int pg) {  // of tile c, to registers
             if constexpr (F8) {
-                if (t < TILE && page >= 0) {
-                    const int r = ((int)((first + c) % n_t) * TILE + t) & mask;
-                    const long long o = page * p.sc_page + h * p.sc_head + r;
-                    sk = p.ks[o], sv = p.vs[o];
-                }
-            }
-            const int next = look(c + 1);
-            // a thread that gave up keeps the loop's barriers
-            auto free_stage = [&] {
-                if (ok && c >= S::STAGES) ok = bar_wait(&ms.pv_done[stage], (unsigned)(c / S::STAGES - 1) & 1u, abort);
-            };
-            if constexpr (!F8) {
-                free_stage();
-                if (ok) {
-#pragma unroll
-                    for (int i = 0; i < EACH; ++i) {
-                        const int r = t / CH + i * (128 / CH);
-                        const long long o = ms.off[c & 1][r];
-                        const bool in = o >= 0;
-                        const long long a = in ? o + cc * 16 : 0;
-                        cp16(panel_at(st, TILE, r, cc), kh + a, in);
-                        cp16(panel_at(st + S::KV_B, TILE, r, cc), vh + a, in);
-                    }
-                }
-                cp_commit();
-                if (ok && c >= LAG) {
-                    cp_wait<LAG>();
-                    arrived(c - LAG);
-                }
-            } else {
-                uint4 k[EACH], v[EACH];
+                if (c >= tiles) return;
+                const int h = (int)((first + c) / n_t) / p.RB;
+                const uint8_t* const kh = p.k + h * p.head_b;
+                const uint8_t* const vh = p.v + h * p.head_b;
 #pragma unroll
                 for (int i = 0; i < EACH; ++i) {
-                    const int r = t / CH + i * (128 / CH);
-                    const long long o = ms.off[c & 1][r];
+                    const long long o = ms.off[c & 1][t / CH + i * (128 / CH)];
                     k[i] = v[i] = make_uint4(0, 0, 0, 0);
                     if (o >= 0) {
                         k[i] = __ldg(reinterpret_cast<const uint4*>(kh + o + cc * 16));
                         v[i] = __ldg(reinterpret_cast<const uint4*>(vh + o + cc * 16));
                     }
                 }
-                free_stage();
+                sk = sv = 0.f;
+                if (t < TILE && pg >= 0) {
+                    const int r = ((int)((first + c) % n_t) * TILE + t) & mask;
+                    const long long o = pg * p.sc_page + h * p.sc_head + r;
+                    sk = __ldg(p.ks + o), sv = __ldg(p.vs + o);
+                }
+            }
+        };
+        codes(0, page);
+        bool ok = true;
+        for (long long c = 0; c < tiles; ++c) {
+            const int stage = (int)(c % S::STAGES);
+            const uint32_t st = ring + stage * S::STAGE_B;
+            const int after = look(c + 2);
+            // a thread that gave up keeps the loop's barriers
+            if (ok && c >= S::STAGES) ok = bar_wait(&ms.pv_done[stage], (unsigned)(c / S::STAGES - 1) & 1u, abort);
+            if constexpr (F8) {
                 auto put = [&](uint32_t base, int r, const uint4& w) {
                     uint4 a, b;
                     codes_bf16<FMT>(w.x, a.x, a.y);
@@ -509,28 +568,25 @@ __global__ void __launch_bounds__(288, 1) prefix_kernel(const __grid_constant__ 
                     }
                     arrived(c);
                 }
+                note(c + 1, next);
+                asm volatile("bar.sync 1, 128;" ::: "memory");
+                codes(c + 1, next);
             }
-            note(c + 1, next);
             page = next;
-            asm volatile("bar.sync 1, 128;" ::: "memory");
-        }
-        if constexpr (!F8) {
-            cp_wait<0>();
-            if (ok)
-                for (long long c = max(0ll, tiles - LAG); c < tiles; ++c) arrived(c);
+            next = after;
         }
     } else if (lane == 0) {
         // ================ products ================
         // (the other lanes wait below)
         constexpr uint32_t QK = mma_desc(ROWS, TILE, false), PV = mma_desc(ROWS, D, true);
+        const uint64_t q = smem_desc(qs, 16, 1024);
         auto scores = [&](long long c) {  // S of tile c
-            const uint32_t k = ring + (uint32_t)(c % S::STAGES) * S::STAGE_B;
+            const uint64_t k = smem_desc(ring + (uint32_t)(c % S::STAGES) * S::STAGE_B, 16, 1024);
+            const uint32_t d = tm + S::T_S + (uint32_t)(c & 1) * TILE;
 #pragma unroll
-            for (int i = 0; i < D / 16; ++i) {
-                const uint32_t in = (uint32_t)(i & 3) * 32;
-                mma_ss(tm + S::T_S + (uint32_t)(c & 1) * TILE, smem_desc(qs + (i >> 2) * ROWS * 128 + in, 16, 1024),
-                       smem_desc(k + (i >> 2) * TILE * 128 + in, 16, 1024), QK, i > 0);
-            }
+            for (int i = 0; i < D / 16; ++i)
+                mma_ss(d, desc_on(q, (i >> 2) * ROWS * 128 + (i & 3) * 32),
+                       desc_on(k, (i >> 2) * TILE * 128 + (i & 3) * 32), QK, i > 0);
             mma_commit(&ms.s_full[c & 1]);
         };
         long long c = 0;
@@ -553,14 +609,13 @@ __global__ void __launch_bounds__(288, 1) prefix_kernel(const __grid_constant__ 
                 const long long n = c + i;
                 if (!(ok = bar_wait(&ms.p_ready[n & 1], (unsigned)(n >> 1) & 1u, abort))) break;
                 tm_after();
-                const uint32_t v = ring + (uint32_t)(n % S::STAGES) * S::STAGE_B + S::KV_B;
+                const uint64_t v = smem_desc(ring + (uint32_t)(n % S::STAGES) * S::STAGE_B + S::KV_B, TILE * 128, 1024);
                 const uint32_t pa = tm + S::T_P + (uint32_t)(n & 1) * TILE;
 #pragma unroll
                 for (int part = 0; part < 2; ++part)
 #pragma unroll
                     for (int k = 0; k < TILE / 16; ++k)
-                        mma_ts(tm + S::T_O, pa + part * 32 + k * 8, smem_desc(v + k * 2048, TILE * 128, 1024), PV,
-                               i > 0 || part > 0 || k > 0);
+                        mma_ts(tm + S::T_O, pa + part * 32 + k * 8, desc_on(v, k * 2048), PV, i > 0 || part > 0 || k > 0);
                 mma_commit(&ms.pv_done[n % S::STAGES]);
             }
             c += take;

@@ -670,3 +670,26 @@ def test_non_finite_values_in_a_shared_prefix_stay_with_who_sees_them():
         assert bool(torch.isnan(out[others][..., 40]).all())
         if fmt != torch.int8:
             assert bool(torch.isfinite(out[others][..., :40]).all())
+
+
+@gpu
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("order", ["token", "interleaved", "shifted"])
+def test_shared_prefixes_in_other_layouts(fmt, order):
+    """Heads inside tokens, K and V in one buffer, rows wider than a head: the same result as dense pages."""
+    B, Hq, H, D, ps, shared = 40, 8, 2, 128, 16, 144
+    cache, table, n, q = build(fmt, torch.bfloat16, B, 1, Hq, H, D, ps, [shared + 3 + b for b in range(B)], shared=shared)
+    want = cache.attend(table, n, q, shared_len=shared)
+    N, raw = cache.k.shape[0], torch.uint8 if fmt != torch.bfloat16 else fmt
+    if order == "token":
+        k, v = (torch.zeros((N, ps, H, D), dtype=raw, device="cuda").permute(0, 2, 1, 3) for _ in range(2))
+    elif order == "interleaved":
+        buf = torch.zeros((H, N, ps, 2, D), dtype=raw, device="cuda")
+        k, v = (buf[:, :, :, i].permute(1, 0, 2, 3) for i in (0, 1))
+    else:
+        buf = torch.zeros((2, N, H, ps, D + 16), dtype=raw, device="cuda")
+        k, v = (buf[i, ..., 16:] for i in (0, 1))
+    k.copy_(cache.k.view(raw))
+    v.copy_(cache.v.view(raw))
+    other = pages.Pages(k.view(fmt), v.view(fmt), cache.k_scale, cache.v_scale)
+    assert torch.equal(other.attend(table, n, q, shared_len=shared), want)
