@@ -97,6 +97,23 @@ __device__ __forceinline__ bool warp_wait(unsigned long long* b, unsigned parity
     return __all_sync(0xffffffffu, bar_wait(b, parity, abort));
 }
 
+// A role's place in the line of tiles: the ring's stage and its turn, the
+// buffer pair and its turn (without divisions).
+template <int STAGES>
+struct Place {
+    int stage = 0;
+    unsigned turn = 0, c = 0;
+    __device__ __forceinline__ void next() {
+        ++c;
+        if (++stage == STAGES) stage = 0, ++turn;
+    }
+    __device__ __forceinline__ int buf() const { return (int)(c & 1u); }
+    __device__ __forceinline__ unsigned full() const { return turn & 1u; }          // parity of the stage's phase of this tile
+    __device__ __forceinline__ unsigned free() const { return (turn - 1) & 1u; }    // of the tile before it in the stage
+    __device__ __forceinline__ unsigned pair() const { return c >> 1 & 1u; }        // of the buffer's phase of this tile
+    __device__ __forceinline__ unsigned pair_free() const { return ((c >> 1) - 1) & 1u; }
+};
+
 // Shared-memory matrix descriptors: start address, leading and stride offsets
 // in 16-byte units, version 1, 128-byte swizzle.
 __device__ __forceinline__ uint64_t smem_desc(uint32_t addr, uint32_t lead, uint32_t stride) {
@@ -124,6 +141,13 @@ __device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint3
         "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
         "r"(a), "l"(b), "r"(desc), "r"((uint32_t)add)
         : "memory");
+}
+// one lane of a converged warp; the compiler then knows that a single thread
+// runs the branch and keeps the products' operands in uniform registers
+__device__ __forceinline__ bool elect_one() {
+    uint32_t p;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
+    return p != 0;
 }
 __device__ __forceinline__ void mma_commit(unsigned long long* b) {
     asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(sm32(b))
@@ -252,13 +276,12 @@ __global__ void __launch_bounds__(288, 1) prefix_kernel(const __grid_constant__ 
     tm_after();
     const uint32_t tm = ms.tmem;
 
-    // Tiles are counted over all pieces (c): tile c uses stage c % STAGES, S and P buffer c & 1.
+    // Tiles are counted over all pieces: tile c uses stage c % STAGES, S and P buffer c & 1.
     if (warp < 4) {
         // ================ softmax, a row a thread ================
         const uint32_t my = tm + ((uint32_t)(warp * 32) << 16);
-        long long c = 0;
-        unsigned piece_no = 0;
-        for (long long u = first; u < end; ++piece_no) {
+        Place<S::STAGES> at_c, back1, back2;  // this tile, and the ones one and two before it
+        for (long long u = first; u < end;) {
             const int item = (int)(u / n_t), off = (int)(u % n_t), take = (int)min((long long)(n_t - off), end - u);
             const int h = item / p.RB, rb = item - h * p.RB;
             const long long row = (long long)rb * ROWS + tid;
@@ -293,10 +316,10 @@ __global__ void __launch_bounds__(288, 1) prefix_kernel(const __grid_constant__ 
             const int at = live ? p.lens[b] - p.T + t : 0;
             float m = -INFINITY, l = 0.f;
             bool ok = true;
-            for (int i = 0; i < take && ok; ++i, ++c) {
-                const int buf = (int)(c & 1), stage = (int)(c % S::STAGES);
+            for (int i = 0; i < take; ++i) {
+                const int buf = at_c.buf(), stage = at_c.stage;
                 const int j0 = (off + i) * TILE;
-                if (!(ok = warp_wait(&ms.s_full[buf], (unsigned)(c >> 1) & 1u, abort))) break;
+                if (!(ok = warp_wait(&ms.s_full[buf], at_c.pair(), abort))) break;
                 tm_after();
                 uint32_t s0[32], s1[32];
                 tm_ld32(s0, my + S::T_S + buf * TILE);
@@ -306,7 +329,7 @@ __global__ void __launch_bounds__(288, 1) prefix_kernel(const __grid_constant__ 
                 bar_arrive(&ms.s_free[buf]);
                 const float* ksc = scales + stage * 2 * TILE;
                 // the scales come with the tile
-                if (F8 && !(ok = warp_wait(&ms.kv_full[stage], (unsigned)(c / S::STAGES) & 1u, abort))) break;
+                if (F8 && !(ok = warp_wait(&ms.kv_full[stage], at_c.full(), abort))) break;
                 if constexpr (F8) {
 #pragma unroll
                     for (int j = 0; j < 32; j += 4) {
@@ -355,7 +378,7 @@ __global__ void __launch_bounds__(288, 1) prefix_kernel(const __grid_constant__ 
                     m = mn;
                     l *= f;
                     // every product so far is in O
-                    if (!(ok = warp_wait(&ms.pv_done[(c - 1) % S::STAGES], (unsigned)((c - 1) / S::STAGES) & 1u, abort))) break;
+                    if (!(ok = warp_wait(&ms.pv_done[back1.stage], back1.full(), abort))) break;
                     tm_after();
 #pragma unroll 1
                     for (int d = 0; d < D; d += 32) {
@@ -392,17 +415,20 @@ __global__ void __launch_bounds__(288, 1) prefix_kernel(const __grid_constant__ 
                 }
                 l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
                 // the P buffer is free when the product two tiles ago has read it
-                if (c >= 2 && !(ok = warp_wait(&ms.pv_done[(c - 2) % S::STAGES], (unsigned)((c - 2) / S::STAGES) & 1u, abort))) break;
+                if (at_c.c >= 2 && !(ok = warp_wait(&ms.pv_done[back2.stage], back2.full(), abort))) break;
                 tm_after();
                 tm_st32(my + S::T_P + buf * TILE, hi);
                 tm_st32(my + S::T_P + buf * TILE + 32, lo);
                 tm_wait_st();
                 tm_before();
                 bar_arrive(&ms.p_ready[buf]);
+                back2 = back1;
+                back1 = at_c;
+                at_c.next();
             }
             if (!ok) break;
             // ---- the piece: O out of tensor memory
-            if (!warp_wait(&ms.pv_done[(c - 1) % S::STAGES], (unsigned)((c - 1) / S::STAGES) & 1u, abort)) break;
+            if (!warp_wait(&ms.pv_done[back1.stage], back1.full(), abort)) break;
             tm_after();
             const bool whole = take == n_t;
             float* slot = p.slots + (whole ? 2ll * gridDim.x + item : 2ll * blockIdx.x + (u == first ? 0 : 1)) * p.slot_floats;
@@ -442,12 +468,13 @@ __global__ void __launch_bounds__(288, 1) prefix_kernel(const __grid_constant__ 
             int now = page_of(lane), next = page_of(32 + lane);
             bool ok = true;
             long long box = 0;
-            for (long long c = 0; c < tiles && ok; ++c) {
-                const int stage = (int)(c % S::STAGES);
-                const int h = (int)((first + c) / n_t) / p.RB, j0 = (int)((first + c) % n_t) * TILE;
+            Place<S::STAGES> pl;
+            int item = (int)(first / n_t), tile = (int)(first % n_t);
+            for (long long c = 0; c < tiles; ++c, pl.next()) {
+                const int stage = pl.stage, h = item / p.RB, j0 = tile * TILE;
+                if (++tile == n_t) tile = 0, ++item;
                 const uint32_t st = ring + stage * S::STAGE_B;
-                if (c >= S::STAGES) ok = warp_wait(&ms.pv_done[stage], (unsigned)(c / S::STAGES - 1) & 1u, abort);
-                if (!ok) break;
+                if (c >= S::STAGES && !(ok = warp_wait(&ms.pv_done[stage], pl.free(), abort))) break;
                 if (lane == 0) bar_expect(&ms.kv_full[stage], S::STAGE_B);
                 for (int i = 0; i < parts; ++i, ++box) {
                     const int page = __shfl_sync(0xffffffffu, now, (int)(box & 31));
@@ -483,10 +510,6 @@ __global__ void __launch_bounds__(288, 1) prefix_kernel(const __grid_constant__ 
         constexpr int EACH = TILE * CH / 128;      // pieces of K (and of V) a thread copies
         const int cc = t % CH;
         const long long tiles = end - first;
-        auto arrived = [&](long long c) {  // this thread's part of tile c lies in shared memory
-            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-            bar_arrive(&ms.kv_full[c % S::STAGES]);
-        };
         auto look = [&](long long c) {  // where row t of tile c lies, and its scales
             if (t < TILE && c < tiles) {
                 const int pos = (int)((first + c) % n_t) * TILE + t;
@@ -539,12 +562,13 @@ __global__ void __launch_bounds__(288, 1) prefix_kernel(const __grid_constant__ 
         };
         codes(0, page);
         bool ok = true;
-        for (long long c = 0; c < tiles; ++c) {
-            const int stage = (int)(c % S::STAGES);
+        Place<S::STAGES> pl;
+        for (long long c = 0; c < tiles; ++c, pl.next()) {
+            const int stage = pl.stage;
             const uint32_t st = ring + stage * S::STAGE_B;
             const int after = look(c + 2);
             // a thread that gave up keeps the loop's barriers
-            if (ok && c >= S::STAGES) ok = bar_wait(&ms.pv_done[stage], (unsigned)(c / S::STAGES - 1) & 1u, abort);
+            if (ok && c >= S::STAGES) ok = bar_wait(&ms.pv_done[stage], pl.free(), abort);
             if constexpr (F8) {
                 auto put = [&](uint32_t base, int r, const uint4& w) {
                     uint4 a, b;
@@ -566,7 +590,9 @@ __global__ void __launch_bounds__(288, 1) prefix_kernel(const __grid_constant__ 
                         scales[stage * 2 * TILE + t] = sk;
                         scales[stage * 2 * TILE + TILE + t] = sv;
                     }
-                    arrived(c);
+                    // this thread's part of the tile lies in shared memory
+                    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                    bar_arrive(&ms.kv_full[stage]);
                 }
                 note(c + 1, next);
                 asm volatile("bar.sync 1, 128;" ::: "memory");
@@ -575,54 +601,57 @@ __global__ void __launch_bounds__(288, 1) prefix_kernel(const __grid_constant__ 
             page = next;
             next = after;
         }
-    } else if (lane == 0) {
-        // ================ products ================
-        // (the other lanes wait below)
+    } else {
+        // ================ products: a warp in step, one lane issues ================
         constexpr uint32_t QK = mma_desc(ROWS, TILE, false), PV = mma_desc(ROWS, D, true);
+        const uint32_t tmu = __shfl_sync(0xffffffffu, tm, 0);
         const uint64_t q = smem_desc(qs, 16, 1024);
-        auto scores = [&](long long c) {  // S of tile c
-            const uint64_t k = smem_desc(ring + (uint32_t)(c % S::STAGES) * S::STAGE_B, 16, 1024);
-            const uint32_t d = tm + S::T_S + (uint32_t)(c & 1) * TILE;
-#pragma unroll
-            for (int i = 0; i < D / 16; ++i)
-                mma_ss(d, desc_on(q, (i >> 2) * ROWS * 128 + (i & 3) * 32),
-                       desc_on(k, (i >> 2) * TILE * 128 + (i & 3) * 32), QK, i > 0);
-            mma_commit(&ms.s_full[c & 1]);
-        };
-        long long c = 0;
+        const uint64_t k0 = smem_desc(ring, 16, 1024), v0 = smem_desc(ring + S::KV_B, TILE * 128, 1024);
+        Place<S::STAGES> ahead, at_c;  // the tile whose scores come next, and whose output
         unsigned piece_no = 0;
         bool ok = true;
         for (long long u = first; u < end && ok; ++piece_no) {
             const int off = (int)(u % n_t), take = (int)min((long long)(n_t - off), end - u);
-            if (!(ok = bar_wait(&ms.q_ready, piece_no & 1u, abort))) break;
-            for (int i = -1; i < take && ok; ++i) {
+            if (!(ok = warp_wait(&ms.q_ready, piece_no & 1u, abort))) break;
+            for (int i = -1; i < take; ++i) {
                 if (i + 1 < take) {
-                    const long long n = c + i + 1;
                     // K and V are here; the softmax has read what the S buffer held two tiles ago
-                    ok = bar_wait(&ms.kv_full[n % S::STAGES], (unsigned)(n / S::STAGES) & 1u, abort) &&
-                         (n < 2 || bar_wait(&ms.s_free[n & 1], (unsigned)((n >> 1) - 1) & 1u, abort));
+                    ok = warp_wait(&ms.kv_full[ahead.stage], ahead.full(), abort) &&
+                         (ahead.c < 2 || warp_wait(&ms.s_free[ahead.buf()], ahead.pair_free(), abort));
                     if (!ok) break;
                     tm_after();
-                    scores(n);
+                    if (elect_one()) {
+                        const uint64_t k = desc_on(k0, ahead.stage * S::STAGE_B);
+                        const uint32_t d = tmu + S::T_S + ahead.buf() * TILE;
+#pragma unroll
+                        for (int j = 0; j < D / 16; ++j)
+                            mma_ss(d, desc_on(q, (j >> 2) * ROWS * 128 + (j & 3) * 32),
+                                   desc_on(k, (j >> 2) * TILE * 128 + (j & 3) * 32), QK, j > 0);
+                        mma_commit(&ms.s_full[ahead.buf()]);
+                    }
+                    __syncwarp();
+                    ahead.next();
                 }
                 if (i < 0) continue;
-                const long long n = c + i;
-                if (!(ok = bar_wait(&ms.p_ready[n & 1], (unsigned)(n >> 1) & 1u, abort))) break;
+                if (!(ok = warp_wait(&ms.p_ready[at_c.buf()], at_c.pair(), abort))) break;
                 tm_after();
-                const uint64_t v = smem_desc(ring + (uint32_t)(n % S::STAGES) * S::STAGE_B + S::KV_B, TILE * 128, 1024);
-                const uint32_t pa = tm + S::T_P + (uint32_t)(n & 1) * TILE;
+                if (elect_one()) {
+                    const uint64_t v = desc_on(v0, at_c.stage * S::STAGE_B);
+                    const uint32_t pa = tmu + S::T_P + at_c.buf() * TILE;
 #pragma unroll
-                for (int part = 0; part < 2; ++part)
+                    for (int part = 0; part < 2; ++part)
 #pragma unroll
-                    for (int k = 0; k < TILE / 16; ++k)
-                        mma_ts(tm + S::T_O, pa + part * 32 + k * 8, desc_on(v, k * 2048), PV, i > 0 || part > 0 || k > 0);
-                mma_commit(&ms.pv_done[n % S::STAGES]);
+                        for (int j = 0; j < TILE / 16; ++j)
+                            mma_ts(tmu + S::T_O, pa + part * 32 + j * 8, desc_on(v, j * 2048), PV, i > 0 || part > 0 || j > 0);
+                    mma_commit(&ms.pv_done[at_c.stage]);
+                }
+                __syncwarp();
+                at_c.next();
             }
-            c += take;
             u += take;
         }
         // the last products end before the tensor memory goes, also when a role gave up
-        mma_commit(&ms.drained);
+        if (elect_one()) mma_commit(&ms.drained);
         const long long t0 = now_ns();
         while (!bar_try(&ms.drained, 0) && now_ns() - t0 < PREFIX_WAIT_NS) {
         }
