@@ -463,7 +463,7 @@ typedef struct mk_attention {
  * (they do not depend on lens). The workspace belongs to one call until the
  * call has run: calls that may overlap on the GPU (other streams, captured
  * graphs replayed side by side) take one each. Its contents need no
- * initialisation. */
+ * initialisation. Small calls need none (0 bytes). */
 int mk_pages_attend_workspace(const mk_attention* args, int64_t* bytes);
 
 /* Errors: INVALID_ARG (NULL, shapes, alignment, a workspace too small or not

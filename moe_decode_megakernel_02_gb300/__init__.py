@@ -149,7 +149,7 @@ def lib():
         L.mk_pages_write.argtypes = [P, P, P, P, I32, P, P, P, P]
         L.mk_pages_read.argtypes = [P, P, P, P, I32, P, P, P, P]
         L.mk_pages_attend.argtypes = [P, P, ctypes.c_int64, P]
-        L.mk_pages_attend_workspace.argtypes = [P, ctypes.POINTER(ctypes.c_int64)]
+        L.mk_pages_attend_workspace.argtypes = [P, P]
         L.mk_kv_view.argtypes = [P, I32, P, P]
         L.mk_sample.argtypes = [P, P]
         for f in ("mk_load_weights", "mk_load_synthetic", "mk_alloc_kv", "mk_kv_set_block_table", "mk_kv_write",

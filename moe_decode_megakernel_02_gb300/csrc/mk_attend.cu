@@ -9,6 +9,7 @@ namespace {
 using namespace mkop;
 
 constexpr int MAX_DEV = 32;
+constexpr int CLUSTER_TILES = 12;
 
 // KindInfo of each kernel on each device, asked for once
 int kind_info(int dev, int d, const Kind& k, KindInfo& out) {
@@ -43,6 +44,7 @@ int prefix_info(int dev, int d, int format, KindInfo& out) {
 
 struct Plan {
     Kind own_k, sh_k;
+    int cluster;  // > 0: small call, an item a cluster
     bool prefix;
     KindInfo own_i, sh_i;
     int own_grid, sh_grid;  // sh_grid 0: nothing shared
@@ -95,7 +97,21 @@ int make_plan(const mk_attention* a, Plan& pl) {
     pl.own_floats = slot_floats(pl.own_slot_rows, D);
     const int min_units = 2;
     const int64_t items = (int64_t)B * H * pl.own_rb;
-    if (items > INT32_MAX / 4) return fail(MK_ERR_UNSUPPORTED, "attend: too many queries in one call");
+    if (items > INT32_MAX / 16) return fail(MK_ERR_UNSUPPORTED, "attend: too many queries in one call");
+    // Small calls: up to CLUSTER_TILES tiles a CTA, all items' clusters resident at once (or nearly)
+    pl.cluster = 0;
+    if (!a->shared_len && pl.own_k.rows <= 32) {
+        const int64_t tiles = (cap + pl.own_i.tile - 1) / pl.own_i.tile;
+        int c = 1;
+        while (c < 8 && tiles > 4 * c && items * c * 2 <= (int64_t)sms * pl.own_i.ctas) c *= 2;
+        if (tiles <= CLUSTER_TILES * c && items * c <= (int64_t)sms * pl.own_i.ctas * 2) {
+            pl.cluster = c;
+            pl.own_grid = (int)(items * c);
+            pl.sh_grid = 0;
+            pl.base_off = pl.own_off = pl.sh_off = pl.bytes = 0;
+            return MK_OK;
+        }
+    }
     const int64_t most = items * ((cap + pl.own_i.tile - 1) / pl.own_i.tile + 1);
     int64_t grid = (int64_t)sms * pl.own_i.ctas;
     if (grid > (most + min_units - 1) / min_units) grid = (most + min_units - 1) / min_units;
@@ -141,7 +157,7 @@ extern "C" int mk_pages_attend_workspace(const mk_attention* args, int64_t* byte
 extern "C" int mk_pages_attend(const mk_attention* a, void* workspace, int64_t workspace_bytes, void* stream) {
     Plan pl;
     if (const int rc = make_plan(a, pl)) return rc;
-    if (!workspace || (uintptr_t)workspace % 256 || workspace_bytes < pl.bytes)
+    if (pl.bytes && (!workspace || (uintptr_t)workspace % 256 || workspace_bytes < pl.bytes))
         return fail(MK_ERR_INVALID_ARG, "attend: the workspace needs %lld bytes, 256-byte aligned", (long long)pl.bytes);
     const mk_pages& g = *a->pages;
     const int eb = code_bytes(g.format), D = g.head_dim;
@@ -178,7 +194,9 @@ extern "C" int mk_pages_attend(const mk_attention* a, void* workspace, int64_t w
                                      : fn(pl.sh_k, &q, nullptr, pl.sh_grid, false, s))
             return rc;
     }
+    p.cluster = pl.cluster;
     if (const int rc = fn(pl.own_k, &p, nullptr, pl.own_grid, pl.sh_grid > 0, s)) return rc;
+    if (pl.cluster) return MK_OK;
     const unsigned rows = (unsigned)((int64_t)p.B * p.T * a->n_q_heads);
     return D == 64 ? join_64(j, rows, s) : D == 128 ? join_128(j, rows, s) : join_256(j, rows, s);
 }

@@ -26,7 +26,9 @@
 // stretch of it, whatever the lengths are; lengths are read on the device, so
 // a captured graph keeps working as they grow. An item that lies within one
 // CTA is finished by it; pieces of an item leave (output, maximum, sum) in the
-// workspace and a second launch joins them.
+// workspace and a second launch joins them. Small calls, whose time is the
+// latency of launches, give every item a cluster of 1 to 8 CTAs instead, which
+// join through distributed shared memory: one launch, no workspace.
 //
 // Rounding. Scores and sums are 32-bit. bf16 pages: queries are exact in bf16
 // (16-bit floats: hi + lo parts), probabilities go in as hi + lo bf16 parts,
@@ -38,6 +40,8 @@
 // scale so far: products below 2^-29 of the largest possible one fall under
 // fp16's normal range and keep steps of 2^-39 of it.
 #pragma once
+#include <cooperative_groups.h>
+
 #include "mk_ops.cuh"
 
 namespace mkop {
@@ -61,6 +65,7 @@ struct AttendP {
     int B, T, H, G, f16;
     float scale, cap;
     int shared;      // positions in shared pages: the shared launch covers [0, shared), the other one the rest
+    int cluster;     // > 0: one item a cluster of so many CTAs, no pieces in the workspace
     int is_shared;   // this is the shared launch (one virtual sequence, rows of the whole batch)
     int RB;          // row blocks of an item
     int rows_item;   // rows of one (sequence, kv head): T * G, or B * T * G
@@ -216,12 +221,12 @@ struct Shape {
     // CTAs an SM: what the registers allow, and at least two stages of the ring
     static constexpr int WANT = (OREGS <= 32 ? 4 : OREGS <= 64 ? 4 : 2) * 128 / NT;
     static constexpr int fit(int ctas) { return (227 * 1024 / ctas - 1024 - Q_B - MISC_B) / STAGE_B; }
-    static constexpr int CTAS = WANT > 3 && fit(WANT) >= 3 ? WANT : WANT >= 3 && fit(3) >= 3 ? 3 : WANT >= 2 && fit(2) >= 2 ? 2 : 1;
+    static constexpr int CTAS = WANT > 3 && fit(WANT) >= 3 ? WANT : WANT >= 3 && fit(3) >= 2 ? 3 : WANT >= 2 && fit(2) >= 2 ? 2 : 1;
     static constexpr int STAGES = fit(CTAS) > 4 ? 4 : fit(CTAS);
     static constexpr int RING_B = STAGES * STAGE_B;
     static constexpr int SMEM = RING_B + Q_B + MISC_B;
     // the warps' outputs meet in the ring's memory
-    static_assert(WP == 1 || WP * ROWS * D * 4 <= RING_B, "ring too small for the merge");
+    static_assert(WP == 1 || (WP * ROWS * D * 4 <= RING_B && (WP + 1) * ROWS * 8 <= Q_B), "too small for the merge");
     static_assert(STAGES >= 2 && SMEM <= 227 * 1024, "ring");
 };
 
@@ -237,11 +242,64 @@ struct Misc {
     int found_b;
 };
 
-template <int D, int FMT, bool SPLITQ, int WP, int WR, int RN>
+// four values of a finished row (of the kv head's rows) from column d on, divided and written
+__device__ __forceinline__ void emit(const AttendP& p, int row, int h, int d, const float4& y, float mm, float ll) {
+    const int bt = row / p.G, g = row - bt * p.G;
+    const int b = bt / p.T, t = bt - b * p.T, hq = h * p.G + g;
+    const bool none = ll == 0.f;
+    const float inv = none ? 0.f : 1.f / ll;
+    const float z[4] = {none ? 0.f : y.x * inv, none ? 0.f : y.y * inv, none ? 0.f : y.z * inv, none ? 0.f : y.w * inv};
+    uint16_t* dst = p.out + b * p.ob + t * p.ot + hq * p.oh + d;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        dst[i] = p.f16 ? __half_as_ushort(__float2half_rn(z[i])) : __bfloat16_as_ushort(__float2bfloat16_rn(z[i]));
+    if (d == 0 && p.lse)
+        p.lse[((long long)b * p.T + t) * (p.H * p.G) + hq] = none ? -INFINITY : (mm + log2f(ll)) * LN2;
+}
+
+// Joins an item over its cluster: every CTA has its part of all rows in om and
+// (maximum, sum) in ml; each joins its share of the values.
+template <int D, int ROWS, int AT>
+__device__ __forceinline__ void cluster_join(const AttendP& p, float* om, float* ml, const int* lo, const int* hi, int row0,
+                                          int h, int nrows, int rank) {
+    namespace cg = cooperative_groups;
+    cg::cluster_group cl = cg::this_cluster();
+    cl.sync();
+    for (int i = rank * AT + (int)threadIdx.x; i < nrows * (D / 4); i += p.cluster * AT) {
+        const int r = i / (D / 4), d = (i % (D / 4)) * 4;
+        float4 z[8];
+        float2 a[8];
+#pragma unroll
+        for (int c = 0; c < 8; ++c)  // all at once: each is a round trip through the cluster
+            if (c < p.cluster) {
+                z[c] = *reinterpret_cast<const float4*>(cl.map_shared_rank(om, c) + r * D + d);
+                a[c] = *reinterpret_cast<const float2*>(cl.map_shared_rank(ml, c) + 2 * r);
+            }
+        float mm = -INFINITY, ll = 0.f;
+#pragma unroll
+        for (int c = 0; c < 8; ++c)
+            if (c < p.cluster) mm = fmaxf(mm, a[c].x);
+        const float ref = mm == -INFINITY ? 0.f : mm;
+        float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int c = 0; c < 8; ++c)
+            if (c < p.cluster) {
+                const float f = ex2(a[c].x - ref);
+                ll += a[c].y * f;
+                y.x += z[c].x * f, y.y += z[c].y * f, y.z += z[c].z * f, y.w += z[c].w * f;
+            }
+        emit(p, row0 + r, h, d, y, mm, lo[r] < hi[r] ? ll : 0.f);
+    }
+    cl.sync();  // no CTA leaves while another reads its shared memory
+}
+
+// CL: an item a cluster (small calls)
+template <int D, int FMT, bool SPLITQ, int WP, int WR, int RN, bool CL>
 __global__ void __launch_bounds__(32 * WP * WR, Shape<D, FMT, SPLITQ, WP, WR, RN>::CTAS)
     attend_kernel(const __grid_constant__ AttendP p) {
     using S = Shape<D, FMT, SPLITQ, WP, WR, RN>;
     constexpr int AT = S::NT;
+    const int cluster = CL ? p.cluster : 0;
     constexpr bool F8 = S::F8;
     constexpr int ROWB = S::ROWB, TILE = S::TILE, SL = S::SL, ROWS = S::ROWS, DT = D / 16;
     using M = Misc<ROWS, TILE>;
@@ -255,8 +313,12 @@ __global__ void __launch_bounds__(32 * WP * WR, Shape<D, FMT, SPLITQ, WP, WR, RN
     // ---- this CTA's stretch of units
     const int items = p.H * p.RB;  // items of one (virtual) sequence
     const int nb = p.is_shared ? 1 : p.B;
-    long long total, my_first = 0;
-    {
+    long long total = 0, my_first = 0;
+    if (CL) {
+        if (p.status && blockIdx.x == 0)
+            for (int b = tid; b < p.B; b += AT)
+                if (p.lens[b] > (p.pps << p.ps_shift)) *p.status = MK_ERR_INVALID_ARG;
+    } else {
         // each thread counts a stretch of sequences; sums before it by shuffles
         const int each = (nb + AT - 1) / AT, b0 = min(nb, tid * each), b1 = min(nb, b0 + each);
         long long mine = 0;
@@ -308,29 +370,37 @@ __global__ void __launch_bounds__(32 * WP * WR, Shape<D, FMT, SPLITQ, WP, WR, RN
         }
         __syncthreads();
     }
-    int b = ms.found_b;
-    long long base_b = ms.found_base;
-    const long long my_end = min(total, my_first + units_each(total, gridDim.x, p.min_units));
+    // a cluster's item, and this CTA's place in it
+    const int c_item = CL ? blockIdx.x / cluster : 0, c_rank = CL ? blockIdx.x - c_item * cluster : 0;
+    int b = CL ? c_item / items : ms.found_b;
+    long long base_b = CL ? 0 : ms.found_base;
+    const long long my_end = CL ? 1 : min(total, my_first + units_each(total, gridDim.x, p.min_units));
     const int g8 = lane >> 2, q4 = lane & 3;  // a fragment's row (or column) and pair
 
     for (long long u = my_first; u < my_end;) {
         // ---- the item: sequence b, kv head h, row block rb; its tiles [t0, t0 + take)
-        int n_b = cover_units<TILE>(p, b);
-        while (b < nb && u >= base_b + (long long)n_b * items) {
-            base_b += (long long)n_b * items;
-            n_b = ++b < nb ? cover_units<TILE>(p, b) : 0;
+        int n_b = cover_units<TILE>(p, b), item, off, take;
+        if (CL) {
+            item = c_item - b * items;
+            off = n_b * c_rank / cluster;
+            take = n_b * (c_rank + 1) / cluster - off;
+        } else {
+            while (b < nb && u >= base_b + (long long)n_b * items) {
+                base_b += (long long)n_b * items;
+                n_b = ++b < nb ? cover_units<TILE>(p, b) : 0;
+            }
+            if (n_b == 0) break;  // only if the lengths changed under the launch
+            item = (int)((u - base_b) / n_b), off = (int)((u - base_b) % n_b);
+            take = (int)min((long long)(n_b - off), my_end - u);
         }
-        if (n_b == 0) break;  // only if the lengths changed under the launch
-        const int item = (int)((u - base_b) / n_b), off = (int)((u - base_b) % n_b);
         const int h = item / p.RB, rb = item - h * p.RB;
-        const int take = (int)min((long long)(n_b - off), my_end - u);
         int clo, chi;
         cover(p, b, clo, chi);
         const int t0 = clo / TILE + off;
         const int row0 = (p.is_shared ? 0 : b * p.rows_item) + rb * ROWS;
         const int nrows = min(ROWS, p.rows_item - rb * ROWS);
         const long long u_first = u;
-        u += take;
+        u += CL ? 1 : take;
 
         // ---- fetching: where a tile's rows lie is looked up one tile ahead of the copies, a thread a row
         const uint8_t* const kh = p.k + h * p.head_b;
@@ -787,7 +857,7 @@ __global__ void __launch_bounds__(32 * WP * WR, Shape<D, FMT, SPLITQ, WP, WR, RN
                     for (int i = 0; i < DT; ++i) o[n][i][e] *= f, o[n][i][2 + e] *= f;
                 }
             }
-        const bool whole = take == n_b;
+        const bool whole = take == n_b || CL;
         float* slot = nullptr;
         if (whole && p.keep_items)
             slot = p.slots + (2ll * gridDim.x + (long long)b * items + item) * p.slot_floats;
@@ -803,18 +873,7 @@ __global__ void __launch_bounds__(32 * WP * WR, Shape<D, FMT, SPLITQ, WP, WR, RN
                 if (first) *reinterpret_cast<float2*>(slot + (long long)p.slot_rows * D + 2 * r) = make_float2(mm, ll);
                 return;
             }
-            const int bt = (row0 + r) / p.G, g = (row0 + r) - bt * p.G;
-            const int rbq = bt / p.T, t = bt - rbq * p.T, hq = h * p.G + g;
-            const bool none = ll == 0.f;
-            const float inv = none ? 0.f : 1.f / ll;
-            const float z[4] = {none ? 0.f : y.x * inv, none ? 0.f : y.y * inv, none ? 0.f : y.z * inv,
-                                none ? 0.f : y.w * inv};
-            uint16_t* dst = p.out + rbq * p.ob + t * p.ot + hq * p.oh + d;
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-                dst[i] = p.f16 ? __half_as_ushort(__float2half_rn(z[i])) : __bfloat16_as_ushort(__float2bfloat16_rn(z[i]));
-            if (first && p.lse)
-                p.lse[((long long)rbq * p.T + t) * (p.H * p.G) + hq] = none ? -INFINITY : (mm + log2f(ll)) * LN2;
+            emit(p, row0 + r, h, d, y, mm, ll);
         };
         cp_wait<0>();
         __syncthreads();  // the ring is free
@@ -858,8 +917,15 @@ __global__ void __launch_bounds__(32 * WP * WR, Shape<D, FMT, SPLITQ, WP, WR, RN
                         const float4 z = *reinterpret_cast<const float4*>(om + (w * ROWS + r) * D + d);
                         y.x += z.x * f, y.y += z.y * f, y.z += z.z * f, y.w += z.w * f;
                     }
-                    put(r, d, y, mm, ll, d == 0);
+                    if (CL && cluster > 1) {  // to where only this thread has read
+                        *reinterpret_cast<float4*>(om + r * D + d) = y;
+                        if (d == 0) *reinterpret_cast<float2*>(oml + WP * ROWS * 2 + 2 * r) = make_float2(mm, ll);
+                    } else {
+                        put(r, d, y, mm, ll, d == 0);
+                    }
                 }
+                if (CL && cluster > 1)
+                    cluster_join<D, ROWS, AT>(p, om, oml + WP * ROWS * 2, ms.lo, ms.hi, row0, h, nrows, c_rank);
             } else {
 #pragma unroll
                 for (int n = 0; n < RN; ++n) {
@@ -990,10 +1056,10 @@ struct KindInfo {
 };
 
 // A kernel by its template arguments, with what the host has to know of it.
-template <int D, int FMT, bool SPLITQ, int WP, int WR, int RN>
+template <int D, int FMT, bool SPLITQ, int WP, int WR, int RN, bool CL>
 int attend_run(const AttendP* p, KindInfo* info, int grid, bool after, cudaStream_t s) {
     using S = Shape<D, FMT, SPLITQ, WP, WR, RN>;
-    auto kern = attend_kernel<D, FMT, SPLITQ, WP, WR, RN>;
+    auto kern = attend_kernel<D, FMT, SPLITQ, WP, WR, RN, CL>;
     if (info) {
         info->tile = S::TILE;
         info->rows = S::ROWS;
@@ -1007,22 +1073,36 @@ int attend_run(const AttendP* p, KindInfo* info, int grid, bool after, cudaStrea
     cfg.dynamicSmemBytes = S::SMEM;
     cfg.stream = s;
     cudaLaunchAttribute at[1];
-    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    at[0].val.programmaticStreamSerializationAllowed = 1;
+    if (p->cluster > 1) {
+        at[0].id = cudaLaunchAttributeClusterDimension;
+        at[0].val.clusterDim.x = p->cluster;
+        at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+    } else {
+        at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        at[0].val.programmaticStreamSerializationAllowed = 1;
+    }
     cfg.attrs = at;
-    cfg.numAttrs = after ? 1 : 0;
+    cfg.numAttrs = after || p->cluster > 1 ? 1 : 0;
     return cuda_status(cudaLaunchKernelEx(&cfg, kern, *p), "mk_pages_attend");
 }
 
 template <int D, int FMT, bool SPLITQ>
 int attend_pick(const Kind& k, const AttendP* p, KindInfo* info, int grid, bool after, cudaStream_t s) {
-    if (k.rows == 8) return attend_run<D, FMT, SPLITQ, 4, 1, 1>(p, info, grid, after, s);
-    if (k.rows == 16) return attend_run<D, FMT, SPLITQ, 4, 1, 2>(p, info, grid, after, s);
-    if (k.rows == 32) return attend_run<D, FMT, SPLITQ, 4, 2, 2>(p, info, grid, after, s);
+    // the kernel's attributes are the same with and without clusters, but are set for each
+    auto go = [&](auto run, auto run_cl) {
+        if (info) {
+            if (const int rc = run_cl(nullptr, info, 0, false, nullptr)) return rc;
+            return run(nullptr, info, 0, false, nullptr);
+        }
+        return p->cluster ? run_cl(p, nullptr, grid, after, s) : run(p, nullptr, grid, after, s);
+    };
+    if (k.rows == 8) return go(attend_run<D, FMT, SPLITQ, 4, 1, 1, false>, attend_run<D, FMT, SPLITQ, 4, 1, 1, true>);
+    if (k.rows == 16) return go(attend_run<D, FMT, SPLITQ, 4, 1, 2, false>, attend_run<D, FMT, SPLITQ, 4, 1, 2, true>);
+    if (k.rows == 32) return go(attend_run<D, FMT, SPLITQ, 4, 2, 2, false>, attend_run<D, FMT, SPLITQ, 4, 2, 2, true>);
     if constexpr (D < 256) {  // 128 rows of 256 leave no room for the ring
-        if (k.rows == 128) return attend_run<D, FMT, SPLITQ, 1, 8, 2>(p, info, grid, after, s);
+        if (k.rows == 128) return attend_run<D, FMT, SPLITQ, 1, 8, 2, false>(p, info, grid, after, s);
     }
-    return attend_run<D, FMT, SPLITQ, 2, 4, 2>(p, info, grid, after, s);
+    return attend_run<D, FMT, SPLITQ, 2, 4, 2, false>(p, info, grid, after, s);
 }
 
 // With `info`: what the host has to know of the kernel (and its one-time

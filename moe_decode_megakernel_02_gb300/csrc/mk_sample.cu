@@ -34,6 +34,7 @@
 // (top-p) of them, and every CTA works out what it can by itself.
 #include <cooperative_groups.h>
 
+#include <atomic>
 #include <type_traits>
 
 #include "mk_ops.cuh"
@@ -907,7 +908,16 @@ extern "C" int mk_sample(const mk_sampling* a, void* stream) {
                 : a->dtype == MK_DT_BF16 ? sample_kernel<MK_DT_BF16>
                                          : sample_kernel<MK_DT_F16>;
     const size_t smem = (sizeof(Shared) + 15) / 16 * 16 + (size_t)p.slice * e;
-    cudaError_t err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    int dev = 0;
+    cudaError_t err = cudaGetDevice(&dev);
+    // the kernel's shared-memory limit, raised once on each device
+    constexpr int MAX_DEV = 32;
+    static std::atomic<bool> raised[MAX_DEV][3];
+    if (err == cudaSuccess && (dev >= MAX_DEV || !raised[dev][a->dtype].load())) {
+        err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                   (int)((sizeof(Shared) + 15) / 16 * 16 + MAX_SLICE_B));
+        if (err == cudaSuccess && dev < MAX_DEV) raised[dev][a->dtype] = true;
+    }
     if (err != cudaSuccess) return cuda_status(err, "mk_sample");
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)a->rows * C);

@@ -16,53 +16,69 @@ from __future__ import annotations
 
 import ctypes
 import math
+import struct
 
 import torch
 
-from . import (DT_BF16, DT_F16, DT_F32, KV_BF16, KV_E4M3, KV_INT8, AttentionStruct, PagesStruct, RowsStruct,
-               TableStruct, _check, lib)
+from . import (DT_BF16, DT_F16, DT_F32, KV_BF16, KV_E4M3, KV_INT8, AttentionStruct, PagesStruct, TableStruct, _check,
+               lib)
 
 _FORMAT = {torch.bfloat16: KV_BF16, torch.float8_e4m3fn: KV_E4M3, torch.int8: KV_INT8}
 _DTYPE = {torch.float32: DT_F32, torch.bfloat16: DT_BF16, torch.float16: DT_F16}
 _byref = ctypes.byref
+_ONE = torch.Size((1,))
 
 
-def _launch(device, stream, call):
-    """call(stream handle) with `device` current and torch's allocations on that stream."""
+def _launch(device, stream, call, args):
+    """call(stream handle, *args) with `device` current and torch's allocations on that stream."""
     index = device.index
     if stream is None and index == torch.cuda.current_device():
-        return call(torch._C._cuda_getCurrentRawStream(index))
+        return call(torch._C._cuda_getCurrentRawStream(index), *args)
     with torch.cuda.device(index):
         if stream is None:
-            return call(torch.cuda.current_stream().cuda_stream)
+            return call(torch.cuda.current_stream().cuda_stream, *args)
         if not isinstance(stream, torch.cuda.Stream):
             stream = torch.cuda.ExternalStream(int(stream)) if stream else torch.cuda.default_stream()
         if stream.device.index != index:
             raise ValueError(f"stream of device {stream.device.index}, tensors on device {index}")
         with torch.cuda.stream(stream):
-            return call(stream.cuda_stream)
+            return call(stream.cuda_stream, *args)
+
+
+def _copy_call(h, fn, pages, packed, pos, cnt, n, st):
+    buf = ctypes.create_string_buffer(packed, len(packed))
+    at = ctypes.addressof(buf)
+    rc = fn(pages, at, pos, cnt, n, at + 24, at + 64, st, h)
+    if rc:
+        _check(rc)
 
 
 def _ptr(x, name, shape, dtype, device):
     """data_ptr of an optional contiguous argument after its checks."""
     if x is None:
-        return None
-    if x.dtype != dtype or x.shape != shape or x.device != device or not x.is_contiguous():
+        return 0
+    if x.dtype is not dtype or x.shape != shape or x.device != device or not x.is_contiguous():
         raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)} on {device}, got "
                          f"{x.dtype} {tuple(x.shape)} on {x.device}")
     return x.data_ptr()
 
 
-def _rows(x, name, device, shape=None):
+def _rows(x, name, device):
+    """The fields of an mk_rows."""
     dt = _DTYPE.get(x.dtype)
-    if dt is None or x.dim() != 4 or x.device != device or (x.stride(3) != 1 and x.shape[3] > 1):
+    if dt is None or x.dim() != 4 or x.device != device:
         raise ValueError(f"{name} must be a float32, bfloat16 or float16 tensor [batch, tokens, heads, head_dim] on "
-                         f"{device} whose last dimension is contiguous, got {x.dtype} {tuple(x.shape)} strides "
-                         f"{x.stride()} on {x.device}")
-    if shape is not None and x.shape != shape:
-        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(x.shape)}")
+                         f"{device}, got {x.dtype} {tuple(x.shape)} on {x.device}")
     s = x.stride()
-    return RowsStruct(x.data_ptr(), s[0], s[1], s[2], dt, 0)
+    if s[3] != 1 and x.shape[3] > 1:
+        raise ValueError(f"{name}'s last dimension must be contiguous, got strides {s}")
+    return x.data_ptr(), s[0], s[1], s[2], dt, 0
+
+
+# A call's structures side by side in one buffer: (mk_attention,) mk_page_table, mk_rows, mk_rows
+_COPY = struct.Struct("Pqii Pqqqii Pqqqii")
+_ATTEND = struct.Struct("PP PPP PP PP ii ff ii Pqii Pqqqii Pqqqii")
+assert _COPY.size == 24 + 2 * 40 and _ATTEND.size == 96 + _COPY.size and ctypes.sizeof(AttentionStruct) == 96
 
 
 class Pages:
@@ -93,32 +109,35 @@ class Pages:
         self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
         self.device = k.device
         st = k.stride()
+        self._heads = (k.shape[1], k.shape[3])
+        self._need = {}  # workspace bytes by shapes
         self._s = PagesStruct(k.data_ptr(), v.data_ptr(), k_scale.data_ptr() if k_scale is not None else None,
                               v_scale.data_ptr() if v_scale is not None else None, st[0], st[1], st[2], ss[0], ss[1],
                               fmt, k.shape[0], k.shape[1], k.shape[2], k.shape[3], 0)
+        self._at = ctypes.addressof(self._s)
 
     def _table(self, table):
         if table.dtype != torch.int32 or table.dim() != 2 or table.device != self.device or table.stride(1) != 1:
             raise ValueError(f"table must be an int32 tensor [batch, pages per sequence] on {self.device} with a "
                              f"contiguous last dimension, got {table.dtype} {tuple(table.shape)} on {table.device}")
-        return TableStruct(table.data_ptr(), table.stride(0), table.shape[0], table.shape[1])
+        return table.data_ptr(), table.stride(0), table.shape[0], table.shape[1]
 
     def _copy(self, fn, table, positions, k, v, counts, status, stream):
         dev, t = self.device, self._table(table)
-        B = (t.batch,)
-        rk, rv = _rows(k, "k", dev), _rows(v, "v", dev, k.shape)
-        s = self._s
-        if k.shape[0] != t.batch or k.shape[2] != s.n_kv_heads or k.shape[3] != s.head_dim:
-            raise ValueError(f"k and v must be [{t.batch}, tokens, {s.n_kv_heads}, {s.head_dim}], got {tuple(k.shape)}")
+        rk, rv = _rows(k, "k", dev), _rows(v, "v", dev)
+        shape = k.shape
+        if shape[0] != t[2] or shape[2:] != self._heads or v.shape != shape:
+            raise ValueError(f"k and v must be [{t[2]}, tokens, {self._heads[0]}, {self._heads[1]}], got {tuple(shape)} "
+                             f"and {tuple(v.shape)}")
         if positions is None:
             raise ValueError("positions is required")
-        pos = _ptr(positions, "positions", B, torch.int32, dev)
-        cnt = _ptr(counts, "counts", B, torch.int32, dev)
-        st = _ptr(status, "status", (1,), torch.int32, dev)
-        if t.batch == 0 or k.shape[1] == 0:
+        pos = _ptr(positions, "positions", shape[:1], torch.int32, dev)
+        cnt = _ptr(counts, "counts", shape[:1], torch.int32, dev)
+        st = _ptr(status, "status", _ONE, torch.int32, dev)
+        n = shape[1]
+        if shape[0] == 0 or n == 0:
             return
-        _launch(dev, stream, lambda h: _check(fn(_byref(s), _byref(t), pos, cnt, k.shape[1], _byref(rk), _byref(rv),
-                                                 st, h)))
+        _launch(dev, stream, _copy_call, (fn, self._at, _COPY.pack(*t, *rk, *rv), pos, cnt, n, st))
 
     def write(self, table, positions, k, v, counts=None, status=None, stream=None):
         """Rows t < counts[b] (all, without counts) of k and v, [batch, tokens, n_kv_heads, head_dim], to positions
@@ -142,38 +161,58 @@ class Pages:
         slope * distance; shared_len: the first positions of all sequences lie in the same pages (whole pages) and
         are read once. A token that sees nothing gets zeros (lse -inf). Returns out, or (out, lse) with lse float32
         [batch, tokens, n_q_heads]. The workspace comes from torch's allocator, on the call's stream."""
-        dev, t, s = self.device, self._table(table), self._s
+        dev, t = self.device, self._table(table)
         rq = _rows(q, "q", dev)
-        B, T, Hq, D = q.shape
-        if B != t.batch or D != s.head_dim or Hq < 1 or Hq % s.n_kv_heads:
-            raise ValueError(f"q must be [{t.batch}, tokens, a multiple of {s.n_kv_heads}, {s.head_dim}], got "
-                             f"{tuple(q.shape)}")
+        shape = q.shape
+        B, T, Hq, D = shape
+        H = self._heads[0]
+        if B != t[2] or D != self._heads[1] or Hq < 1 or Hq % H:
+            raise ValueError(f"q must be [{t[2]}, tokens, a multiple of {H}, {self._heads[1]}], got {tuple(shape)}")
         if lens is None:
             raise ValueError("lens is required")
-        n = _ptr(lens, "lens", (B,), torch.int32, dev)
-        first = _ptr(starts, "starts", (B,), torch.int32, dev)
-        sl = _ptr(slopes, "slopes", (Hq,), torch.float32, dev)
-        st = _ptr(status, "status", (1,), torch.int32, dev)
-        if out is not None and out.dtype != q.dtype:
-            raise ValueError(f"out must have q's type {q.dtype}, got {out.dtype}")
+        batch = shape[:1]
+        n = _ptr(lens, "lens", batch, torch.int32, dev)
+        first = _ptr(starts, "starts", batch, torch.int32, dev)
+        sl = _ptr(slopes, "slopes", shape[2:3], torch.float32, dev)
+        st = _ptr(status, "status", _ONE, torch.int32, dev)
+        if out is not None and (out.dtype is not q.dtype or out.shape != shape):
+            raise ValueError(f"out must have q's type and shape, {q.dtype} {tuple(shape)}")
         if scale is None:
             scale = 1.0 / math.sqrt(D)
+        return _launch(dev, stream, self._attend, (t, rq, q, n, first, sl, st, out, scale, softcap, shared_len,
+                                                   return_lse))
 
-        def call(h):
-            o = torch.empty((B, T, Hq, D), dtype=q.dtype, device=dev) if out is None else out
-            ro = _rows(o, "out", dev, q.shape)
-            lse = torch.empty((B, T, Hq), dtype=torch.float32, device=dev) if return_lse else None
-            if B and T:
-                a = AttentionStruct(ctypes.pointer(s), ctypes.pointer(t), n, first, sl, ctypes.pointer(rq),
-                                    ctypes.pointer(ro), None if lse is None else lse.data_ptr(), st, T, Hq, scale,
-                                    softcap, shared_len, 0)
-                need = ctypes.c_int64()
-                _check(lib().mk_pages_attend_workspace(_byref(a), _byref(need)))
-                w = torch.empty((need.value,), dtype=torch.uint8, device=dev)
-                _check(lib().mk_pages_attend(_byref(a), w.data_ptr(), need.value, h))
-            return (o, lse) if return_lse else o
-
-        return _launch(dev, stream, call)
+    def _attend(self, h, t, rq, q, n, first, sl, st, out, scale, softcap, shared_len, return_lse):
+        dev, shape = self.device, q.shape
+        B, T, Hq, D = shape
+        if out is None:
+            out = torch.empty(shape, dtype=q.dtype, device=dev)
+            ro = (out.data_ptr(), T * Hq * D, Hq * D, D, rq[4], 0)
+        else:
+            ro = _rows(out, "out", dev)
+        lse = torch.empty((B, T, Hq), dtype=torch.float32, device=dev) if return_lse else None
+        if B and T:
+            buf = ctypes.create_string_buffer(_ATTEND.size)
+            at = ctypes.addressof(buf)
+            try:
+                _ATTEND.pack_into(buf, 0, self._at, at + 96, n, first, sl, at + 120, at + 160,
+                                  lse.data_ptr() if return_lse else 0, st, T, Hq, scale, softcap, shared_len, 0, *t, *rq,
+                                  *ro)
+            except (struct.error, OverflowError) as e:
+                raise ValueError(f"scale, softcap and shared_len must be numbers in range: {e}") from None
+            L = lib()
+            # the workspace's size depends on shapes alone
+            key = (B, T, Hq, t[3], shared_len, rq[4])
+            need = self._need.get(key)
+            if need is None:
+                c = ctypes.c_int64()
+                _check(L.mk_pages_attend_workspace(at, _byref(c)))
+                need = self._need[key] = c.value
+            w = torch.empty((need,), dtype=torch.uint8, device=dev) if need else None
+            rc = L.mk_pages_attend(at, w.data_ptr() if need else 0, need, h)
+            if rc:
+                _check(rc)
+        return (out, lse) if return_lse else out
 
 
 class _Memory:

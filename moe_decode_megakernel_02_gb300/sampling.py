@@ -6,11 +6,15 @@ token a sequence and step, every step on the device.
 from __future__ import annotations
 
 import ctypes
+import struct
 
 import torch
 
 from . import SamplingStruct, _check, lib
 from .pages import _DTYPE, _launch, _ptr
+
+_SAMPLING = struct.Struct("Pq PPPPP PPP iiii")
+assert _SAMPLING.size == ctypes.sizeof(SamplingStruct)
 
 
 def sample(logits, u, temperature=None, top_k=None, top_p=None, min_p=None, out=None, return_details=False,
@@ -27,26 +31,28 @@ def sample(logits, u, temperature=None, top_k=None, top_p=None, min_p=None, out=
         raise ValueError("logits must be a float32, bfloat16 or float16 CUDA tensor [rows, vocab] with contiguous rows, "
                          f"got {logits.dtype} {tuple(logits.shape)} strides {logits.stride()} on {logits.device}")
     R, V = logits.shape
-    dev, n = logits.device, (R,)
+    dev, n = logits.device, logits.shape[:1]
     if u is None:
         raise ValueError("u is required")
     args = (_ptr(u, "u", n, torch.float32, dev), _ptr(temperature, "temperature", n, torch.float32, dev),
             _ptr(top_k, "top_k", n, torch.int32, dev), _ptr(top_p, "top_p", n, torch.float32, dev),
             _ptr(min_p, "min_p", n, torch.float32, dev))
     _ptr(out, "out", n, torch.int32, dev)
+    return _launch(dev, stream, _sample, (logits, args, out, return_details, n, R, V, dt))
 
-    def call(h):
-        tokens = torch.empty(n, dtype=torch.int32, device=dev) if out is None else out
-        probs = torch.empty(n, dtype=torch.float32, device=dev) if return_details else None
-        kept = torch.empty(n, dtype=torch.int32, device=dev) if return_details else None
-        if R:
-            a = SamplingStruct(logits.data_ptr(), logits.stride(0), *args, tokens.data_ptr(),
-                               probs.data_ptr() if return_details else None,
-                               kept.data_ptr() if return_details else None, R, V, dt, 0)
-            _check(lib().mk_sample(ctypes.byref(a), h))
-        return (tokens, probs, kept) if return_details else tokens
 
-    return _launch(dev, stream, call)
+def _sample(h, logits, args, out, details, n, R, V, dt):
+    dev = logits.device
+    tokens = torch.empty(n, dtype=torch.int32, device=dev) if out is None else out
+    probs = torch.empty(n, dtype=torch.float32, device=dev) if details else None
+    kept = torch.empty(n, dtype=torch.int32, device=dev) if details else None
+    if R:
+        a = _SAMPLING.pack(logits.data_ptr(), logits.stride(0), *args, tokens.data_ptr(),
+                           probs.data_ptr() if details else 0, kept.data_ptr() if details else 0, R, V, dt, 0)
+        rc = lib().mk_sample(a, h)
+        if rc:
+            _check(rc)
+    return (tokens, probs, kept) if details else tokens
 
 
 class SampledLoop:
