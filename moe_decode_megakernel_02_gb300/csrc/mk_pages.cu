@@ -1,5 +1,7 @@
 // mk_pages.cu -- rows into a paged cache and back (mk_pages_write,
 // mk_pages_read): 8-bit codes with one fp32 scale a row, or bf16.
+#include <type_traits>
+
 #include "mk_ops.cuh"
 
 namespace mkop {
@@ -43,48 +45,85 @@ struct CopyP {
     const int *positions, *counts;
     uint8_t *xk, *xv;                                  // the rows outside the cache
     long long kb, kt, kh, vb, vt, vh;                  // their strides, elements
-    int pps, ps_shift, n_pages, H, D, n;
-    unsigned rows;  // B * n * H
+    int pps, ps_shift, n_pages, H, n;
+    int lanes, lanes_shift;  // threads of a row: head_dim / 8, and the power of two they are spaced by
+    int units, toks;         // of a token: H rows' threads; tokens of a block
+    unsigned magic;          // unit / units by the high word of a product
+    int chunks;              // blocks of a sequence
     int* status;
 };
 
-constexpr int CT = 256;
+constexpr int CT = 256;    // threads of a block
+constexpr int AHEAD = 4;   // pieces of K and of V a thread has in flight
+constexpr int TOKS = 64;   // most tokens of a block
 
-// eight values of a row outside the cache, as fp32. VEC: 8 elements' bytes
-// aligned. The fp32 values of 16-bit types are exact.
+// Eight values of a row outside the cache, as they lie there. VEC: 16-byte
+// aligned.
 template <int DT, bool VEC>
-__device__ __forceinline__ void load8(float (&x)[8], const uint8_t* base, long long at) {
-    if constexpr (DT == MK_DT_F32) {
-        const float* p = reinterpret_cast<const float*>(base) + at;
-        if constexpr (VEC) {
-            const float4 a = __ldcs(reinterpret_cast<const float4*>(p)), b = __ldcs(reinterpret_cast<const float4*>(p) + 1);
-            x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w, x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
-        } else {
+struct Values8 {
+    static constexpr int W = DT == MK_DT_F32 ? 8 : 4;  // 32-bit words
+    uint32_t w[W];
+    __device__ __forceinline__ void zero() {
 #pragma unroll
-            for (int i = 0; i < 8; ++i) x[i] = p[i];
-        }
-    } else {
-        const uint16_t* p = reinterpret_cast<const uint16_t*>(base) + at;
-        uint32_t w[4];
+        for (int i = 0; i < W; ++i) w[i] = 0;
+    }
+    __device__ __forceinline__ void load(const uint8_t* base, long long at) {
         if constexpr (VEC) {
-            const uint4 a = __ldcs(reinterpret_cast<const uint4*>(p));
-            w[0] = a.x, w[1] = a.y, w[2] = a.z, w[3] = a.w;
+            const uint4* p = reinterpret_cast<const uint4*>(base + at * (DT == MK_DT_F32 ? 4 : 2));
+#pragma unroll
+            for (int i = 0; i < W / 4; ++i) {
+                const uint4 a = __ldcs(p + i);
+                w[4 * i] = a.x, w[4 * i + 1] = a.y, w[4 * i + 2] = a.z, w[4 * i + 3] = a.w;
+            }
+        } else if constexpr (DT == MK_DT_F32) {
+            const uint32_t* p = reinterpret_cast<const uint32_t*>(base) + at;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) w[i] = p[i];
         } else {
+            const uint16_t* p = reinterpret_cast<const uint16_t*>(base) + at;
 #pragma unroll
             for (int i = 0; i < 4; ++i) w[i] = p[2 * i] | (uint32_t)p[2 * i + 1] << 16;
         }
+    }
+    // 16-bit types are exact in 32 bits
+    __device__ __forceinline__ void floats(float (&x)[8]) const {
+        if constexpr (DT == MK_DT_F32) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            if constexpr (DT == MK_DT_BF16) {
-                x[2 * i] = __uint_as_float(w[i] << 16);
-                x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
-            } else {
-                const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
-                x[2 * i] = f.x;
-                x[2 * i + 1] = f.y;
+            for (int i = 0; i < 8; ++i) x[i] = __uint_as_float(w[i]);
+        } else {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                if constexpr (DT == MK_DT_BF16) {
+                    x[2 * i] = __uint_as_float(w[i] << 16);
+                    x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+                } else {
+                    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
+                    x[2 * i] = f.x;
+                    x[2 * i + 1] = f.y;
+                }
             }
         }
     }
+    // The largest magnitude's bits (16-bit types: in 16 bits): as numbers, so
+    // that infinities and then NaN win.
+    __device__ __forceinline__ uint32_t largest() const {
+        if constexpr (DT == MK_DT_F32) {
+            uint32_t m = 0;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) m = max(m, w[i] & 0x7fffffffu);
+            return m;
+        } else {
+            const uint32_t m = __vmaxu2(__vmaxu2(w[0] & 0x7fff7fffu, w[1] & 0x7fff7fffu),
+                                        __vmaxu2(w[2] & 0x7fff7fffu, w[3] & 0x7fff7fffu));
+            return max(m & 0xffffu, m >> 16);
+        }
+    }
+};
+template <int DT>
+__device__ __forceinline__ float magnitude(uint32_t bits) {
+    if constexpr (DT == MK_DT_F32) return __uint_as_float(bits);
+    else if constexpr (DT == MK_DT_BF16) return __uint_as_float(bits << 16);
+    else return __half2float(__ushort_as_half((unsigned short)bits));
 }
 
 template <int DT, bool VEC>
@@ -122,176 +161,249 @@ __device__ __forceinline__ void store8(uint8_t* base, long long at, const float 
 // correctly rounded reciprocal (Markstein, "Computation of elementary
 // functions on the IBM RISC System/6000 processor", 1990). Three operations a
 // value. Scales so small that a remainder could be subnormal take the division.
-__device__ __forceinline__ float quotient(float x, float s, float r, bool tiny) {
-    if (tiny) return __fdiv_rn(x, s);
+__device__ __forceinline__ float quotient(float x, float s, float r) {
     const float q = x * r;
     return __fmaf_rn(__fmaf_rn(-q, s, x), r, q);
+}
+// largest / Q in the same way; r = 1 / Q
+__device__ __forceinline__ float scale_of(float largest, float q, float r) {
+    return largest < 0x1p-80f ? fmaxf(__fdiv_rn(largest, q), 0x1p-126f) : quotient(largest, q, r);
 }
 
 template <int FMT>
 __device__ __forceinline__ uint2 encode8(const float (&x)[8], float scale) {
-    const float r = __frcp_rn(scale);
-    const bool tiny = scale < 0x1p-80f;
+    float q[8];
+    if (scale < 0x1p-80f) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) q[i] = __fdiv_rn(x[i], scale);
+    } else {
+        const float r = __frcp_rn(scale);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) q[i] = quotient(x[i], scale, r);
+    }
     uint32_t w[2];
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
         if constexpr (FMT == MK_KV_E4M3) {
-            float q[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) q[i] = quotient(x[4 * h + i], scale, r, tiny);
-            const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(q[0], q[1]), __NV_SATFINITE, __NV_E4M3);
-            const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(q[2], q[3]), __NV_SATFINITE, __NV_E4M3);
+            const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(q[4 * h], q[4 * h + 1]), __NV_SATFINITE, __NV_E4M3);
+            const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(q[4 * h + 2], q[4 * h + 3]), __NV_SATFINITE, __NV_E4M3);
             w[h] = lo | hi << 16;
         } else {
             // adding 1.5 * 2^23 leaves the value rounded to an integer (ties
             // to even) in the low mantissa bits, as two's complement
             uint32_t c[4];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) c[i] = __float_as_uint(quotient(x[4 * h + i], scale, r, tiny) + 12582912.0f);
+            for (int i = 0; i < 4; ++i) c[i] = __float_as_uint(q[4 * h + i] + 12582912.0f);
             w[h] = __byte_perm(__byte_perm(c[0], c[1], 0x0040), __byte_perm(c[2], c[3], 0x0040), 0x5410);
         }
     }
     return make_uint2(w[0], w[1]);
 }
 
-// One thread: 8 values of a row, of K and of V; `lanes` = head_dim / 8 threads
-// of a warp hold a row, the row's largest magnitude by shuffles among them.
-// Magnitudes are compared as the bits of |x|, so a NaN wins and is seen. Bound
-// by HBM (reads 2-4 bytes a value, writes 1 + 4/head_dim): K and V together
-// keep two 16-byte loads a thread in flight. Measured times: at the launch.
-template <int FMT, int DT, bool VEC>
-__global__ void __launch_bounds__(CT) write_kernel(const CopyP p, int lanes, int lanes_shift) {
-    const unsigned gid = blockIdx.x * CT + threadIdx.x;
-    const unsigned row = gid >> lanes_shift;
-    const int c = (int)(gid & ((1u << lanes_shift) - 1));
-    bool live = row < p.rows && c < lanes;
-    float xk[8], xv[8];
-    long long at = 0, sat = 0;
-    if (live) {
-        const unsigned bt = row / (unsigned)p.H;
-        const int h = (int)(row - bt * p.H);
-        const int b = (int)(bt / (unsigned)p.n), t = (int)(bt - (unsigned)b * p.n);
-        if (p.counts && t >= p.counts[b]) {
-            live = false;
-        } else {
-            const long long pos = (long long)p.positions[b] + t;
-            const long long col = pos >> p.ps_shift;
+// A block's tokens: where each one's rows lie in the cache, -1 where they are
+// to be left alone (past the count, or no such place).
+struct Tokens {
+    long long at[TOKS], scale[TOKS];
+};
+__device__ __forceinline__ void find_tokens(const CopyP& p, Tokens& tk, int b, int t0) {
+    for (int i = threadIdx.x; i < p.toks; i += CT) {
+        const int t = t0 + i;
+        long long at = -1, scale = -1;
+        if (t < p.n && (!p.counts || t < p.counts[b])) {
+            const long long pos = (long long)p.positions[b] + t, col = pos >> p.ps_shift;
             const int page = pos >= 0 && col < p.pps ? p.table[b * p.table_s + col] : -1;
-            if ((unsigned)page >= (unsigned)p.n_pages) {
-                if (p.status) *p.status = MK_ERR_INVALID_ARG;
-                live = false;
-            } else {
+            if ((unsigned)page < (unsigned)p.n_pages) {
                 const int r = (int)(pos & ((1 << p.ps_shift) - 1));
-                at = page * p.page_s + h * p.head_s + r * p.row_s + 8 * c;
-                sat = page * p.sc_page + h * p.sc_head + r;
-                load8<DT, VEC>(xk, p.xk, b * p.kb + t * p.kt + h * p.kh + 8 * c);
-                load8<DT, VEC>(xv, p.xv, b * p.vb + t * p.vt + h * p.vh + 8 * c);
+                at = page * p.page_s + r * p.row_s;
+                scale = page * p.sc_page + r;
+            } else if (p.status) {
+                *p.status = MK_ERR_INVALID_ARG;
             }
         }
+        tk.at[i] = at;
+        tk.scale[i] = scale;
     }
-    if constexpr (FMT == MK_KV_BF16) {
-        if (!live) return;
-        store8<MK_DT_BF16, true>(p.k, at, xk);
-        store8<MK_DT_BF16, true>(p.v, at, xv);
-    } else {
-        uint32_t mk = 0, mv = 0;
-        if (live) {
+}
+// Unit u of a block: 8 values (piece c) of the row of kv head h of token `tok`.
+__device__ __forceinline__ void unit_of(const CopyP& p, int u, int& tok, int& h, int& c) {
+    tok = p.units == 1 ? u : p.toks > 1 ? (int)__umulhi((unsigned)u, p.magic) : 0;
+    const int rest = u - tok * p.units;  // (a token of one unit: the magic number does not fit 32 bits)
+    h = rest >> p.lanes_shift;
+    c = rest & ((1 << p.lanes_shift) - 1);
+}
+
+// One thread: 8 values of a row, of K and of V, AHEAD rows at a time; head_dim
+// / 8 threads of a warp hold a row and find its largest magnitude by shuffles.
+// Magnitudes are compared as the bits of |x|, so a NaN wins and is seen. The
+// rows are fetched before the block knows where they go, so that the two trips
+// to memory overlap. Bound by HBM: reads 2 or 4 bytes a value, writes 1 +
+// 4 / head_dim.
+template <int FMT, int DT, bool VEC>
+__global__ void __launch_bounds__(CT) write_kernel(const __grid_constant__ CopyP p) {
+    __shared__ Tokens tk;
+    const int b = blockIdx.x / p.chunks, t0 = (blockIdx.x - b * p.chunks) * p.toks;
+    const int limit = p.counts ? min(p.counts[b], p.n) : p.n;
+    if (t0 >= limit) return;
+    const int all = min(p.toks, limit - t0) * p.units;
+#pragma unroll 1
+    for (int u0 = 0; u0 < all; u0 += CT * AHEAD) {
+        Values8<DT, VEC> k[AHEAD], v[AHEAD];
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                mk = max(mk, __float_as_uint(xk[i]) & 0x7fffffffu);
-                mv = max(mv, __float_as_uint(xv[i]) & 0x7fffffffu);
+        for (int i = 0; i < AHEAD; ++i) {
+            if (u0 + i * CT >= all) break;
+            int tok, h, c;
+            unit_of(p, u0 + i * CT + threadIdx.x, tok, h, c);
+            if (u0 + i * CT + (int)threadIdx.x < all && c < p.lanes) {
+                k[i].load(p.xk, b * p.kb + (t0 + tok) * p.kt + h * p.kh + 8 * c);
+                v[i].load(p.xv, b * p.vb + (t0 + tok) * p.vt + h * p.vh + 8 * c);
+            } else {
+                k[i].zero();
+                v[i].zero();
             }
         }
-        for (int o = (1 << lanes_shift) >> 1; o; o >>= 1) {
-            mk = max(mk, __shfl_xor_sync(0xffffffffu, mk, o));
-            mv = max(mv, __shfl_xor_sync(0xffffffffu, mv, o));
+        if (u0 == 0) {
+            find_tokens(p, tk, b, t0);
+            __syncthreads();
         }
-        if (!live) return;
-        constexpr float QMAX = FMT == MK_KV_E4M3 ? 448.0f : 127.0f;
-        // the upper bound keeps code x scale finite for the largest 32-bit inputs
-        constexpr float SMAX = FMT == MK_KV_E4M3 ? 0x1.249248p+119f : 0x1.020406p+121f;
-        const float sk = fminf(fmaxf(__fdiv_rn(__uint_as_float(mk), QMAX), 0x1p-126f), SMAX);
-        const float sv = fminf(fmaxf(__fdiv_rn(__uint_as_float(mv), QMAX), 0x1p-126f), SMAX);
-        const bool bad_k = mk >= 0x7f800000u, bad_v = mv >= 0x7f800000u;
-        const uint2 ck = bad_k ? make_uint2(0, 0) : encode8<FMT>(xk, sk);
-        const uint2 cv = bad_v ? make_uint2(0, 0) : encode8<FMT>(xv, sv);
-        *reinterpret_cast<uint2*>(p.k + at) = ck;
-        *reinterpret_cast<uint2*>(p.v + at) = cv;
-        if (c == 0) {
-            p.ks[sat] = bad_k ? __uint_as_float(0x7fffffffu) : sk;
-            p.vs[sat] = bad_v ? __uint_as_float(0x7fffffffu) : sv;
+#pragma unroll
+        for (int i = 0; i < AHEAD; ++i) {
+            if (u0 + i * CT >= all) break;
+            int tok, h, c;
+            const int u = u0 + i * CT + threadIdx.x;
+            unit_of(p, u, tok, h, c);
+            const long long row = u < all && c < p.lanes ? tk.at[tok] : -1;
+            const long long at = row + h * p.head_s + 8 * c;
+            float x[8], y[8];
+            k[i].floats(x);
+            v[i].floats(y);
+            if constexpr (FMT == MK_KV_BF16) {
+                if (row >= 0) {
+                    store8<MK_DT_BF16, true>(p.k, at, x);
+                    store8<MK_DT_BF16, true>(p.v, at, y);
+                }
+            } else {
+                uint32_t mk = k[i].largest(), mv = v[i].largest();
+                if constexpr (DT == MK_DT_F32) {
+                    for (int o = (1 << p.lanes_shift) >> 1; o; o >>= 1) {
+                        mk = max(mk, __shfl_xor_sync(0xffffffffu, mk, o));
+                        mv = max(mv, __shfl_xor_sync(0xffffffffu, mv, o));
+                    }
+                } else {  // both in one word
+                    uint32_t m = mk | mv << 16;
+                    for (int o = (1 << p.lanes_shift) >> 1; o; o >>= 1) m = __vmaxu2(m, __shfl_xor_sync(0xffffffffu, m, o));
+                    mk = m & 0xffffu;
+                    mv = m >> 16;
+                }
+                constexpr float QMAX = FMT == MK_KV_E4M3 ? 448.0f : 127.0f, QINV = 1.0f / QMAX;
+                // the upper bound keeps code x scale finite for the largest 32-bit inputs
+                constexpr float SMAX = FMT == MK_KV_E4M3 ? 0x1.249248p+119f : 0x1.020406p+121f;
+                const float ak = magnitude<DT>(mk), av = magnitude<DT>(mv);
+                const bool bad_k = !(ak < INFINITY), bad_v = !(av < INFINITY);
+                const float sk = fminf(scale_of(ak, QMAX, QINV), SMAX), sv = fminf(scale_of(av, QMAX, QINV), SMAX);
+                if (row >= 0) {
+                    *reinterpret_cast<uint2*>(p.k + at) = bad_k ? make_uint2(0, 0) : encode8<FMT>(x, sk);
+                    *reinterpret_cast<uint2*>(p.v + at) = bad_v ? make_uint2(0, 0) : encode8<FMT>(y, sv);
+                    if (c == 0) {
+                        p.ks[tk.scale[tok] + h * p.sc_head] = bad_k ? __uint_as_float(0x7fffffffu) : sk;
+                        p.vs[tk.scale[tok] + h * p.sc_head] = bad_v ? __uint_as_float(0x7fffffffu) : sv;
+                    }
+                }
+            }
         }
     }
 }
 
+// 8 cached values as they lie there: codes, or bf16
 template <int FMT>
-__device__ __forceinline__ void decode8(float (&x)[8], const uint8_t* base, long long at, float scale) {
-    if constexpr (FMT == MK_KV_BF16) {
-        load8<MK_DT_BF16, true>(x, base, at);
-    } else {
-        const uint2 w = __ldcs(reinterpret_cast<const uint2*>(base + at));
+struct Raw8 {
+    typename std::conditional<FMT == MK_KV_BF16, uint4, uint2>::type w;
+    __device__ __forceinline__ void load(const uint8_t* base, long long at) {
+        if constexpr (FMT == MK_KV_BF16) w = __ldcs(reinterpret_cast<const uint4*>(base + 2 * at));
+        else w = __ldcs(reinterpret_cast<const uint2*>(base + at));
+    }
+    __device__ __forceinline__ void decode(float (&x)[8], float scale) const {
+        if constexpr (FMT == MK_KV_BF16) {
+            const uint32_t v[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const uint32_t byte = ((i < 4 ? w.x : w.y) >> (8 * (i & 3))) & 0xffu;
-            if constexpr (FMT == MK_KV_E4M3)
-                x[i] = __half2float(__half(__nv_cvt_fp8_to_halfraw((__nv_fp8_storage_t)byte, __NV_E4M3))) * scale;
-            else
-                x[i] = (float)(int8_t)byte * scale;
+            for (int i = 0; i < 4; ++i) {
+                x[2 * i] = __uint_as_float(v[i] << 16);
+                x[2 * i + 1] = __uint_as_float(v[i] & 0xffff0000u);
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const uint32_t byte = ((i < 4 ? w.x : w.y) >> (8 * (i & 3))) & 0xffu;
+                if constexpr (FMT == MK_KV_E4M3)
+                    x[i] = __half2float(__half(__nv_cvt_fp8_to_halfraw((__nv_fp8_storage_t)byte, __NV_E4M3))) * scale;
+                else
+                    x[i] = (float)(int8_t)byte * scale;
+            }
         }
     }
-}
+};
 
 // The write's way back, the same threads for the same values; bound by HBM.
 template <int FMT, int DT, bool VEC>
-__global__ void __launch_bounds__(CT) read_kernel(const CopyP p, int lanes, int lanes_shift) {
-    const unsigned gid = blockIdx.x * CT + threadIdx.x;
-    const unsigned row = gid >> lanes_shift;
-    const int c = (int)(gid & ((1u << lanes_shift) - 1));
-    if (row >= p.rows || c >= lanes) return;
-    const unsigned bt = row / (unsigned)p.H;
-    const int h = (int)(row - bt * p.H);
-    const int b = (int)(bt / (unsigned)p.n), t = (int)(bt - (unsigned)b * p.n);
-    if (p.counts && t >= p.counts[b]) return;
-    const long long pos = (long long)p.positions[b] + t;
-    const long long col = pos >> p.ps_shift;
-    const int page = pos >= 0 && col < p.pps ? p.table[b * p.table_s + col] : -1;
-    if ((unsigned)page >= (unsigned)p.n_pages) {
-        if (p.status) *p.status = MK_ERR_INVALID_ARG;
-        return;
+__global__ void __launch_bounds__(CT) read_kernel(const __grid_constant__ CopyP p) {
+    __shared__ Tokens tk;
+    const int b = blockIdx.x / p.chunks, t0 = (blockIdx.x - b * p.chunks) * p.toks;
+    const int limit = p.counts ? min(p.counts[b], p.n) : p.n;
+    if (t0 >= limit) return;
+    const int all = min(p.toks, limit - t0) * p.units;
+    find_tokens(p, tk, b, t0);
+    __syncthreads();
+#pragma unroll 1
+    for (int u0 = 0; u0 < all; u0 += CT * AHEAD) {
+        Raw8<FMT> k[AHEAD], v[AHEAD];
+        float sk[AHEAD], sv[AHEAD];
+#pragma unroll
+        for (int i = 0; i < AHEAD; ++i) {
+            int tok, h, c;
+            const int u = u0 + i * CT + threadIdx.x;
+            unit_of(p, u, tok, h, c);
+            const long long row = u < all && c < p.lanes ? tk.at[tok] : -1;
+            sk[i] = sv[i] = 1.f;
+            if (row >= 0) {
+                k[i].load(p.k, row + h * p.head_s + 8 * c);
+                v[i].load(p.v, row + h * p.head_s + 8 * c);
+                if constexpr (FMT != MK_KV_BF16) {
+                    sk[i] = p.ks[tk.scale[tok] + h * p.sc_head];
+                    sv[i] = p.vs[tk.scale[tok] + h * p.sc_head];
+                }
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < AHEAD; ++i) {
+            int tok, h, c;
+            const int u = u0 + i * CT + threadIdx.x;
+            unit_of(p, u, tok, h, c);
+            if (u < all && c < p.lanes && tk.at[tok] >= 0) {
+                float x[8];
+                k[i].decode(x, sk[i]);
+                store8<DT, VEC>(p.xk, b * p.kb + (t0 + tok) * p.kt + h * p.kh + 8 * c, x);
+                v[i].decode(x, sv[i]);
+                store8<DT, VEC>(p.xv, b * p.vb + (t0 + tok) * p.vt + h * p.vh + 8 * c, x);
+            }
+        }
     }
-    const int r = (int)(pos & ((1 << p.ps_shift) - 1));
-    const long long at = page * p.page_s + h * p.head_s + r * p.row_s + 8 * c;
-    const long long sat = page * p.sc_page + h * p.sc_head + r;
-    float xk[8], xv[8];
-    decode8<FMT>(xk, p.k, at, FMT == MK_KV_BF16 ? 1.f : p.ks[sat]);
-    decode8<FMT>(xv, p.v, at, FMT == MK_KV_BF16 ? 1.f : p.vs[sat]);
-    store8<DT, VEC>(p.xk, b * p.kb + t * p.kt + h * p.kh + 8 * c, xk);
-    store8<DT, VEC>(p.xv, b * p.vb + t * p.vt + h * p.vh + 8 * c, xv);
 }
 
 template <bool WRITE, int FMT, int DT>
-void launch3(const CopyP& p, bool vec, int lanes, int shift, unsigned blocks, cudaStream_t s) {
+void launch3(const CopyP& p, bool vec, unsigned blocks, cudaStream_t s) {
     if constexpr (WRITE) {
-        if (vec)
-            write_kernel<FMT, DT, true><<<blocks, CT, 0, s>>>(p, lanes, shift);
-        else
-            write_kernel<FMT, DT, false><<<blocks, CT, 0, s>>>(p, lanes, shift);
+        if (vec) write_kernel<FMT, DT, true><<<blocks, CT, 0, s>>>(p);
+        else write_kernel<FMT, DT, false><<<blocks, CT, 0, s>>>(p);
     } else {
-        if (vec)
-            read_kernel<FMT, DT, true><<<blocks, CT, 0, s>>>(p, lanes, shift);
-        else
-            read_kernel<FMT, DT, false><<<blocks, CT, 0, s>>>(p, lanes, shift);
+        if (vec) read_kernel<FMT, DT, true><<<blocks, CT, 0, s>>>(p);
+        else read_kernel<FMT, DT, false><<<blocks, CT, 0, s>>>(p);
     }
 }
 
 template <bool WRITE, int FMT>
-void launch2(const CopyP& p, int dt, bool vec, int lanes, int shift, unsigned blocks, cudaStream_t s) {
-    if (dt == MK_DT_F32)
-        launch3<WRITE, FMT, MK_DT_F32>(p, vec, lanes, shift, blocks, s);
-    else if (dt == MK_DT_BF16)
-        launch3<WRITE, FMT, MK_DT_BF16>(p, vec, lanes, shift, blocks, s);
-    else
-        launch3<WRITE, FMT, MK_DT_F16>(p, vec, lanes, shift, blocks, s);
+void launch2(const CopyP& p, int dt, bool vec, unsigned blocks, cudaStream_t s) {
+    if (dt == MK_DT_F32) launch3<WRITE, FMT, MK_DT_F32>(p, vec, blocks, s);
+    else if (dt == MK_DT_BF16) launch3<WRITE, FMT, MK_DT_BF16>(p, vec, blocks, s);
+    else launch3<WRITE, FMT, MK_DT_F16>(p, vec, blocks, s);
 }
 
 int check_rows(const mk_rows* r, const char* name) {
@@ -318,11 +430,6 @@ int copy(const mk_pages* g, const mk_page_table* t, const int32_t* positions, co
     if (const int rc = check_rows(v, "v")) return rc;
     if (k->dtype != v->dtype) return fail(MK_ERR_INVALID_ARG, "pages: k and v rows must have one type");
     if (n == 0) return MK_OK;
-    const long long rows = (long long)t->batch * n * g->n_kv_heads;
-    const int lanes = g->head_dim / 8;
-    int shift = 0;
-    while ((1 << shift) < lanes) ++shift;
-    if (rows << shift > UINT32_MAX - CT) return fail(MK_ERR_UNSUPPORTED, "pages: too many rows in one call");
     CopyP p;
     p.k = (uint8_t*)g->k, p.v = (uint8_t*)g->v, p.ks = g->k_scale, p.vs = g->v_scale;
     p.page_s = g->page_stride, p.head_s = g->head_stride, p.row_s = g->row_stride;
@@ -331,17 +438,28 @@ int copy(const mk_pages* g, const mk_page_table* t, const int32_t* positions, co
     p.positions = positions, p.counts = counts;
     p.xk = (uint8_t*)k->data, p.kb = k->seq_stride, p.kt = k->token_stride, p.kh = k->head_stride;
     p.xv = (uint8_t*)v->data, p.vb = v->seq_stride, p.vt = v->token_stride, p.vh = v->head_stride;
-    p.ps_shift = log2_exact(g->page_size), p.n_pages = g->n_pages, p.H = g->n_kv_heads, p.D = g->head_dim, p.n = n;
-    p.rows = (unsigned)rows, p.status = status;
+    p.ps_shift = log2_exact(g->page_size), p.n_pages = g->n_pages, p.H = g->n_kv_heads, p.n = n;
+    p.status = status;
+    p.lanes = g->head_dim / 8, p.lanes_shift = 0;
+    while ((1 << p.lanes_shift) < p.lanes) ++p.lanes_shift;
+    p.units = p.H << p.lanes_shift;
+    // a block's tokens keep its threads busy twice over, or are all there are
+    int toks = 2 * CT * AHEAD / p.units;
+    p.toks = toks < 1 ? 1 : toks > TOKS ? TOKS : toks;
+    if (p.toks > n) p.toks = n;
+    p.magic = (unsigned)(0x100000000ull / p.units + 1);  // exact for the units of a block: below 2^16
+    p.chunks = (n + p.toks - 1) / p.toks;
+    const int64_t blocks64 = (int64_t)t->batch * p.chunks;
+    if (blocks64 > INT32_MAX) return fail(MK_ERR_UNSUPPORTED, "pages: too many rows in one call");
+    const unsigned blocks = (unsigned)blocks64;
     const bool vec = rows_vec(k) && rows_vec(v);
-    const unsigned blocks = (unsigned)(((rows << shift) + CT - 1) / CT);
     cudaStream_t s = (cudaStream_t)stream;
     if (g->format == MK_KV_BF16)
-        launch2<WRITE, MK_KV_BF16>(p, k->dtype, vec, lanes, shift, blocks, s);
+        launch2<WRITE, MK_KV_BF16>(p, k->dtype, vec, blocks, s);
     else if (g->format == MK_KV_E4M3)
-        launch2<WRITE, MK_KV_E4M3>(p, k->dtype, vec, lanes, shift, blocks, s);
+        launch2<WRITE, MK_KV_E4M3>(p, k->dtype, vec, blocks, s);
     else
-        launch2<WRITE, MK_KV_INT8>(p, k->dtype, vec, lanes, shift, blocks, s);
+        launch2<WRITE, MK_KV_INT8>(p, k->dtype, vec, blocks, s);
     return cuda_status(cudaGetLastError(), WRITE ? "mk_pages_write" : "mk_pages_read");
 }
 
