@@ -46,7 +46,7 @@ struct CopyP {
     uint8_t *xk, *xv;                                  // the rows outside the cache
     long long kb, kt, kh, vb, vt, vh;                  // their strides, elements
     int pps, ps_shift, n_pages, H, n;
-    int lanes, lanes_shift;  // threads of a row: head_dim / 8, and the power of two they are spaced by
+    int lanes, lanes_shift;  // threads of a row (8 or 16 values each), and the power of two they are spaced by
     int units, toks;         // of a token: H rows' threads; tokens of a block
     unsigned magic;          // unit / units by the high word of a product
     int chunks;              // blocks of a sequence
@@ -54,8 +54,18 @@ struct CopyP {
 };
 
 constexpr int CT = 256;    // threads of a block
-constexpr int AHEAD = 4;   // pieces of K and of V a thread has in flight
+constexpr int AHEAD = 4;   // rows of K and of V a reading thread has in flight
 constexpr int TOKS = 64;   // most tokens of a block
+
+// the larger of magnitudes (of one 32-bit number, or of two 16-bit ones); NaN wins
+template <int DT>
+__device__ __forceinline__ uint32_t larger(uint32_t a, uint32_t b) {
+    if constexpr (DT == MK_DT_F32) return max(a, b);
+    uint32_t y;
+    if constexpr (DT == MK_DT_BF16) asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(y) : "r"(a), "r"(b));
+    else asm("max.NaN.f16x2 %0, %1, %2;" : "=r"(y) : "r"(a), "r"(b));
+    return y;
+}
 
 // Eight values of a row outside the cache, as they lie there. VEC: 16-byte
 // aligned.
@@ -104,19 +114,13 @@ struct Values8 {
             }
         }
     }
-    // The largest magnitude's bits (16-bit types: in 16 bits): as numbers, so
-    // that infinities and then NaN win.
+    // the largest magnitude's bits; 16-bit types: of the even and of the odd values, side by side
     __device__ __forceinline__ uint32_t largest() const {
-        if constexpr (DT == MK_DT_F32) {
-            uint32_t m = 0;
+        constexpr uint32_t ABS = DT == MK_DT_F32 ? 0x7fffffffu : 0x7fff7fffu;
+        uint32_t m = w[0] & ABS;
 #pragma unroll
-            for (int i = 0; i < 8; ++i) m = max(m, w[i] & 0x7fffffffu);
-            return m;
-        } else {
-            const uint32_t m = __vmaxu2(__vmaxu2(w[0] & 0x7fff7fffu, w[1] & 0x7fff7fffu),
-                                        __vmaxu2(w[2] & 0x7fff7fffu, w[3] & 0x7fff7fffu));
-            return max(m & 0xffffu, m >> 16);
-        }
+        for (int i = 1; i < W; ++i) m = larger<DT>(m, w[i] & ABS);
+        return m;
     }
 };
 template <int DT>
@@ -232,33 +236,40 @@ __device__ __forceinline__ void unit_of(const CopyP& p, int u, int& tok, int& h,
     c = rest & ((1 << p.lanes_shift) - 1);
 }
 
-// One thread: 8 values of a row, of K and of V, AHEAD rows at a time; head_dim
-// / 8 threads of a warp hold a row and find its largest magnitude by shuffles.
-// Magnitudes are compared as the bits of |x|, so a NaN wins and is seen. The
-// rows are fetched before the block knows where they go, so that the two trips
-// to memory overlap. Bound by HBM: reads 2 or 4 bytes a value, writes 1 +
-// 4 / head_dim.
-template <int FMT, int DT, bool VEC>
-__global__ void __launch_bounds__(CT) write_kernel(const __grid_constant__ CopyP p) {
+// One thread: 8 G values of a row, of K and of V, WAHEAD rows at a time; the
+// threads of a row lie in one warp and find its largest magnitude by shuffles,
+// K's and V's together where they fit one word. The rows are fetched before the
+// block knows where they go, so that the two trips to memory overlap. Reads 2
+// or 4 bytes a value, writes 1 + 4 / head_dim; bound by instructions (about 9 a
+// value, 3 of them the quotient), so a thread takes 16 values where rows allow.
+template <int FMT, int DT, bool VEC, int G>
+__global__ void __launch_bounds__(CT, 3) write_kernel(const __grid_constant__ CopyP p) {
+    constexpr int WAHEAD = G == 2 ? 1 : 2;
     __shared__ Tokens tk;
     const int b = blockIdx.x / p.chunks, t0 = (blockIdx.x - b * p.chunks) * p.toks;
     const int limit = p.counts ? min(p.counts[b], p.n) : p.n;
     if (t0 >= limit) return;
     const int all = min(p.toks, limit - t0) * p.units;
+    const uint8_t* const xk = p.xk + (b * p.kb + t0 * p.kt) * (DT == MK_DT_F32 ? 4 : 2);
+    const uint8_t* const xv = p.xv + (b * p.vb + t0 * p.vt) * (DT == MK_DT_F32 ? 4 : 2);
 #pragma unroll 1
-    for (int u0 = 0; u0 < all; u0 += CT * AHEAD) {
-        Values8<DT, VEC> k[AHEAD], v[AHEAD];
+    for (int u0 = 0; u0 < all; u0 += CT * WAHEAD) {
+        Values8<DT, VEC> k[WAHEAD][G], v[WAHEAD][G];
 #pragma unroll
-        for (int i = 0; i < AHEAD; ++i) {
+        for (int i = 0; i < WAHEAD; ++i) {
             if (u0 + i * CT >= all) break;
             int tok, h, c;
             unit_of(p, u0 + i * CT + threadIdx.x, tok, h, c);
-            if (u0 + i * CT + (int)threadIdx.x < all && c < p.lanes) {
-                k[i].load(p.xk, b * p.kb + (t0 + tok) * p.kt + h * p.kh + 8 * c);
-                v[i].load(p.xv, b * p.vb + (t0 + tok) * p.vt + h * p.vh + 8 * c);
-            } else {
-                k[i].zero();
-                v[i].zero();
+            const bool in = u0 + i * CT + (int)threadIdx.x < all && c < p.lanes;
+#pragma unroll
+            for (int g = 0; g < G; ++g) {
+                if (in) {
+                    k[i][g].load(xk, tok * p.kt + h * p.kh + 8 * (G * c + g));
+                    v[i][g].load(xv, tok * p.vt + h * p.vh + 8 * (G * c + g));
+                } else {
+                    k[i][g].zero();
+                    v[i][g].zero();
+                }
             }
         }
         if (u0 == 0) {
@@ -266,48 +277,67 @@ __global__ void __launch_bounds__(CT) write_kernel(const __grid_constant__ CopyP
             __syncthreads();
         }
 #pragma unroll
-        for (int i = 0; i < AHEAD; ++i) {
+        for (int i = 0; i < WAHEAD; ++i) {
             if (u0 + i * CT >= all) break;
             int tok, h, c;
             const int u = u0 + i * CT + threadIdx.x;
             unit_of(p, u, tok, h, c);
             const long long row = u < all && c < p.lanes ? tk.at[tok] : -1;
-            const long long at = row + h * p.head_s + 8 * c;
-            float x[8], y[8];
-            k[i].floats(x);
-            v[i].floats(y);
+            const long long at = row + h * p.head_s + 8 * G * c;
             if constexpr (FMT == MK_KV_BF16) {
                 if (row >= 0) {
-                    store8<MK_DT_BF16, true>(p.k, at, x);
-                    store8<MK_DT_BF16, true>(p.v, at, y);
+#pragma unroll
+                    for (int g = 0; g < G; ++g) {
+                        float x[8];
+                        k[i][g].floats(x);
+                        store8<MK_DT_BF16, true>(p.k, at + 8 * g, x);
+                        v[i][g].floats(x);
+                        store8<MK_DT_BF16, true>(p.v, at + 8 * g, x);
+                    }
                 }
             } else {
-                uint32_t mk = k[i].largest(), mv = v[i].largest();
+                uint32_t mk = k[i][0].largest(), mv = v[i][0].largest();
+#pragma unroll
+                for (int g = 1; g < G; ++g) {
+                    mk = larger<DT>(mk, k[i][g].largest());
+                    mv = larger<DT>(mv, v[i][g].largest());
+                }
                 if constexpr (DT == MK_DT_F32) {
                     for (int o = (1 << p.lanes_shift) >> 1; o; o >>= 1) {
-                        mk = max(mk, __shfl_xor_sync(0xffffffffu, mk, o));
-                        mv = max(mv, __shfl_xor_sync(0xffffffffu, mv, o));
+                        mk = larger<DT>(mk, __shfl_xor_sync(0xffffffffu, mk, o));
+                        mv = larger<DT>(mv, __shfl_xor_sync(0xffffffffu, mv, o));
                     }
                 } else {  // both in one word
-                    uint32_t m = mk | mv << 16;
-                    for (int o = (1 << p.lanes_shift) >> 1; o; o >>= 1) m = __vmaxu2(m, __shfl_xor_sync(0xffffffffu, m, o));
+                    uint32_t m = larger<DT>(__byte_perm(mk, mv, 0x5410), __byte_perm(mk, mv, 0x7632));
+                    for (int o = (1 << p.lanes_shift) >> 1; o; o >>= 1)
+                        m = larger<DT>(m, __shfl_xor_sync(0xffffffffu, m, o));
                     mk = m & 0xffffu;
                     mv = m >> 16;
                 }
                 constexpr float QMAX = FMT == MK_KV_E4M3 ? 448.0f : 127.0f, QINV = 1.0f / QMAX;
                 // the upper bound keeps code x scale finite for the largest 32-bit inputs
                 constexpr float SMAX = FMT == MK_KV_E4M3 ? 0x1.249248p+119f : 0x1.020406p+121f;
-                const float ak = magnitude<DT>(mk), av = magnitude<DT>(mv);
-                const bool bad_k = !(ak < INFINITY), bad_v = !(av < INFINITY);
-                const float sk = fminf(scale_of(ak, QMAX, QINV), SMAX), sv = fminf(scale_of(av, QMAX, QINV), SMAX);
-                if (row >= 0) {
-                    *reinterpret_cast<uint2*>(p.k + at) = bad_k ? make_uint2(0, 0) : encode8<FMT>(x, sk);
-                    *reinterpret_cast<uint2*>(p.v + at) = bad_v ? make_uint2(0, 0) : encode8<FMT>(y, sv);
-                    if (c == 0) {
-                        p.ks[tk.scale[tok] + h * p.sc_head] = bad_k ? __uint_as_float(0x7fffffffu) : sk;
-                        p.vs[tk.scale[tok] + h * p.sc_head] = bad_v ? __uint_as_float(0x7fffffffu) : sv;
+                if (row < 0) continue;
+                auto out = [&](const Values8<DT, VEC>(&x)[G], uint32_t bits, uint8_t* codes, float* scales) {
+                    const float a = magnitude<DT>(bits);
+                    const bool bad = !(a < INFINITY);
+                    const float s = fminf(scale_of(a, QMAX, QINV), SMAX);
+                    uint2 w[G];
+#pragma unroll
+                    for (int g = 0; g < G; ++g) {
+                        float y[8];
+                        x[g].floats(y);
+                        w[g] = encode8<FMT>(y, s);
+                        if (bad) w[g] = make_uint2(0, 0);
                     }
-                }
+                    if constexpr (G == 2)
+                        *reinterpret_cast<uint4*>(codes + at) = make_uint4(w[0].x, w[0].y, w[1].x, w[1].y);
+                    else
+                        *reinterpret_cast<uint2*>(codes + at) = w[0];
+                    if (c == 0) scales[tk.scale[tok] + h * p.sc_head] = bad ? __uint_as_float(0x7fffffffu) : s;
+                };
+                out(k[i], mk, p.k, p.ks);
+                out(v[i], mv, p.v, p.vs);
             }
         }
     }
@@ -389,10 +419,11 @@ __global__ void __launch_bounds__(CT) read_kernel(const __grid_constant__ CopyP 
 }
 
 template <bool WRITE, int FMT, int DT>
-void launch3(const CopyP& p, bool vec, unsigned blocks, cudaStream_t s) {
+void launch3(const CopyP& p, bool vec, bool wide, unsigned blocks, cudaStream_t s) {
     if constexpr (WRITE) {
-        if (vec) write_kernel<FMT, DT, true><<<blocks, CT, 0, s>>>(p);
-        else write_kernel<FMT, DT, false><<<blocks, CT, 0, s>>>(p);
+        if (vec && wide) write_kernel<FMT, DT, true, 2><<<blocks, CT, 0, s>>>(p);
+        else if (vec) write_kernel<FMT, DT, true, 1><<<blocks, CT, 0, s>>>(p);
+        else write_kernel<FMT, DT, false, 1><<<blocks, CT, 0, s>>>(p);
     } else {
         if (vec) read_kernel<FMT, DT, true><<<blocks, CT, 0, s>>>(p);
         else read_kernel<FMT, DT, false><<<blocks, CT, 0, s>>>(p);
@@ -400,10 +431,10 @@ void launch3(const CopyP& p, bool vec, unsigned blocks, cudaStream_t s) {
 }
 
 template <bool WRITE, int FMT>
-void launch2(const CopyP& p, int dt, bool vec, unsigned blocks, cudaStream_t s) {
-    if (dt == MK_DT_F32) launch3<WRITE, FMT, MK_DT_F32>(p, vec, blocks, s);
-    else if (dt == MK_DT_BF16) launch3<WRITE, FMT, MK_DT_BF16>(p, vec, blocks, s);
-    else launch3<WRITE, FMT, MK_DT_F16>(p, vec, blocks, s);
+void launch2(const CopyP& p, int dt, bool vec, bool wide, unsigned blocks, cudaStream_t s) {
+    if (dt == MK_DT_F32) launch3<WRITE, FMT, MK_DT_F32>(p, vec, wide, blocks, s);
+    else if (dt == MK_DT_BF16) launch3<WRITE, FMT, MK_DT_BF16>(p, vec, wide, blocks, s);
+    else launch3<WRITE, FMT, MK_DT_F16>(p, vec, wide, blocks, s);
 }
 
 int check_rows(const mk_rows* r, const char* name) {
@@ -440,7 +471,11 @@ int copy(const mk_pages* g, const mk_page_table* t, const int32_t* positions, co
     p.xv = (uint8_t*)v->data, p.vb = v->seq_stride, p.vt = v->token_stride, p.vh = v->head_stride;
     p.ps_shift = log2_exact(g->page_size), p.n_pages = g->n_pages, p.H = g->n_kv_heads, p.n = n;
     p.status = status;
-    p.lanes = g->head_dim / 8, p.lanes_shift = 0;
+    const bool vec = rows_vec(k) && rows_vec(v);
+    // 16 values a thread: 16-byte stores of codes
+    const bool wide = WRITE && vec && g->head_dim % 16 == 0 && g->page_stride % 16 == 0 && g->head_stride % 16 == 0 &&
+                      g->row_stride % 16 == 0 && (uintptr_t)g->k % 16 == 0 && (uintptr_t)g->v % 16 == 0;
+    p.lanes = g->head_dim / (wide ? 16 : 8), p.lanes_shift = 0;
     while ((1 << p.lanes_shift) < p.lanes) ++p.lanes_shift;
     p.units = p.H << p.lanes_shift;
     // a block's tokens keep its threads busy twice over, or are all there are
@@ -452,14 +487,13 @@ int copy(const mk_pages* g, const mk_page_table* t, const int32_t* positions, co
     const int64_t blocks64 = (int64_t)t->batch * p.chunks;
     if (blocks64 > INT32_MAX) return fail(MK_ERR_UNSUPPORTED, "pages: too many rows in one call");
     const unsigned blocks = (unsigned)blocks64;
-    const bool vec = rows_vec(k) && rows_vec(v);
     cudaStream_t s = (cudaStream_t)stream;
     if (g->format == MK_KV_BF16)
-        launch2<WRITE, MK_KV_BF16>(p, k->dtype, vec, blocks, s);
+        launch2<WRITE, MK_KV_BF16>(p, k->dtype, vec, wide, blocks, s);
     else if (g->format == MK_KV_E4M3)
-        launch2<WRITE, MK_KV_E4M3>(p, k->dtype, vec, blocks, s);
+        launch2<WRITE, MK_KV_E4M3>(p, k->dtype, vec, wide, blocks, s);
     else
-        launch2<WRITE, MK_KV_INT8>(p, k->dtype, vec, blocks, s);
+        launch2<WRITE, MK_KV_INT8>(p, k->dtype, vec, wide, blocks, s);
     return cuda_status(cudaGetLastError(), WRITE ? "mk_pages_write" : "mk_pages_read");
 }
 
