@@ -14,16 +14,20 @@
 // 2^8 since its reference: until then probabilities up to 2^8 and their sum are
 // as exact as ones below 1.
 //
-// Warps 0-3: softmax, a row a thread; 4-7: loads (bf16 pages: one thread, by
-// tensor maps; 8-bit pages: codes through registers, as E4M3 and INT8 codes are
-// exact in bf16; the K scale multiplies the score, the V scale the
-// probability); 8: one thread issues the products, S of the next tile before P V of this one, so that the
+// Two groups of four warps: softmax, a row a thread, of the even and of the odd
+// tiles; each group keeps its own maxima, sums and output, which meet at the
+// piece's end. Then loads (bf16 pages: one warp, by tensor maps; 8-bit pages:
+// four warps, codes through registers, as E4M3 and INT8 codes are exact in
+// bf16; the K scale multiplies the score, the V scale the probability) and one
+// warp whose elected thread issues the products, S of the next tile before P V of this one, so that the
 // tensor cores work while the softmax does. All waits are on mbarriers with a
 // limit; a wait that runs out raises a flag that every role sees, and the CTA
 // leaves after freeing its tensor memory (MK_ERR_TIMEOUT in `status`).
 //
-// Bound by the softmax: 8192 exponentials a tile at 16 a cycle are 512 cycles,
-// the three products 768 at the bf16 rate. Work is cut as in mk_attend.cuh;
+// Bound by the products: Q K^T of 128 x 64 takes 48 cycles a 16-wide step (its
+// operands' shared-memory reads), the two chains of P V 64 each, 875 cycles a
+// tile of 128-wide heads (measured with nothing else running); 8192
+// exponentials at 16 a cycle are 512. Work is cut as in mk_attend.cuh;
 // every piece goes to the workspace for the joining launch.
 #pragma once
 #include <cuda.h>
@@ -44,17 +48,19 @@ struct PrefixShape {
     static constexpr int STAGES = D == 128 ? 5 : 8;
     static constexpr int SC_OFF = Q_B + STAGES * STAGE_B;
     static constexpr int MISC_OFF = SC_OFF + STAGES * SCALE_B;
-    static constexpr int SMEM = MISC_OFF + 2048 + 1024;  // and room to align to 1024
-    static constexpr int NT = 288;
-    // tensor memory columns: S twice, P (hi, lo) twice, O
+    static constexpr int MISC_B = 4096;
+    static constexpr int SMEM = MISC_OFF + MISC_B + 1024;  // and room to align to 1024
+    static constexpr int LOADERS = F8 ? 4 : 1, NT = 32 * (8 + LOADERS + 1);  // warps: softmax, loads, products
+    // tensor memory columns of the two groups: S, P (hi, lo), O
     static constexpr int T_S = 0, T_P = 2 * TILE, T_O = T_P + 2 * TILE, T_ALL = 512;
-    static_assert(T_O + D <= T_ALL && SMEM <= 227 * 1024, "");
+    static_assert(T_O + 2 * D <= T_ALL && SMEM <= 227 * 1024, "");
 };
 
 struct PrefixMisc {
     unsigned long long kv_full[8], pv_done[8], s_full[2], s_free[2], p_ready[2], q_ready, drained;
     unsigned tmem, abort;
     long long off[2][64];  // where a tile's rows lie (bytes), -1: zeros
+    float2 stat[2][128];   // (maximum, sum) of each group's rows
 };
 
 __device__ __forceinline__ void bar_init(unsigned long long* b, unsigned n) {
@@ -81,11 +87,13 @@ __device__ __forceinline__ long long now_ns() {
 // Waits for the phase of `parity` to end; false when it took too long, or
 // another role gave up.
 __device__ __forceinline__ bool bar_wait(unsigned long long* b, unsigned parity, volatile unsigned* abort) {
-    if (bar_try(b, parity)) return true;
-    const long long t0 = now_ns();
-    while (!bar_try(b, parity)) {
+    long long t0 = 0;
+    for (unsigned n = 0; !bar_try(b, parity); ++n) {
+        if ((n & 63u) != 63u) continue;  // the timer is slow to read
         if (*abort) return false;
-        if (now_ns() - t0 > PREFIX_WAIT_NS) {
+        const long long t = now_ns();
+        if (!t0) t0 = t;
+        if (t - t0 > PREFIX_WAIT_NS) {
             *abort = 1;
             return false;
         }
@@ -232,7 +240,7 @@ __device__ __forceinline__ void bar_expect(unsigned long long* b, unsigned bytes
 }
 
 template <int D, int FMT>
-__global__ void __launch_bounds__(288, 1) prefix_kernel(const __grid_constant__ AttendP p, const __grid_constant__ PrefixMaps maps) {
+__global__ void __launch_bounds__(PrefixShape<D, FMT>::NT, 1) prefix_kernel(const __grid_constant__ AttendP p, const __grid_constant__ PrefixMaps maps) {
     using S = PrefixShape<D, FMT>;
     constexpr bool F8 = S::F8;
     constexpr int TILE = S::TILE, ROWS = S::ROWS;
@@ -241,7 +249,7 @@ __global__ void __launch_bounds__(288, 1) prefix_kernel(const __grid_constant__ 
     const uint32_t qs = sm32(smem), ring = qs + S::Q_B;
     float* const scales = reinterpret_cast<float*>(smem + S::SC_OFF);
     PrefixMisc& ms = *reinterpret_cast<PrefixMisc*>(smem + S::MISC_OFF);
-    static_assert(sizeof(PrefixMisc) <= 2048, "");
+    static_assert(sizeof(PrefixMisc) <= S::MISC_B, "");
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     volatile unsigned* const abort = &ms.abort;
 
@@ -260,12 +268,13 @@ __global__ void __launch_bounds__(288, 1) prefix_kernel(const __grid_constant__ 
             bar_init(&ms.s_free[i], 128);
             bar_init(&ms.p_ready[i], 128);
         }
-        bar_init(&ms.q_ready, 128);
+        bar_init(&ms.q_ready, 256);
         bar_init(&ms.drained, 1);
         ms.abort = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
-    if (warp == 8) {
+    constexpr int MMA_WARP = 8 + S::LOADERS;
+    if (warp == MMA_WARP) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(sm32(&ms.tmem)),
                      "n"(S::T_ALL)
                      : "memory");
@@ -277,24 +286,30 @@ __global__ void __launch_bounds__(288, 1) prefix_kernel(const __grid_constant__ 
     const uint32_t tm = ms.tmem;
 
     // Tiles are counted over all pieces: tile c uses stage c % STAGES, S and P buffer c & 1.
-    if (warp < 4) {
+    if (warp < 8) {
         // ================ softmax, a row a thread ================
-        const uint32_t my = tm + ((uint32_t)(warp * 32) << 16);
-        Place<S::STAGES> at_c, back1, back2;  // this tile, and the ones one and two before it
+        const int wg = warp >> 2, lrow = tid & 127;
+        const uint32_t my = tm + ((uint32_t)((warp & 3) * 32) << 16);
+        const uint32_t my_s = my + S::T_S + wg * TILE, my_p = my + S::T_P + wg * TILE, my_o = my + S::T_O + wg * D;
+        Place<S::STAGES> at_c, back;  // the group's tile, and its last one
+        int parity = 0;               // of the tile that comes next, over both groups
+        if (wg) at_c.next();
+        bool ok = true;
         for (long long u = first; u < end;) {
             const int item = (int)(u / n_t), off = (int)(u % n_t), take = (int)min((long long)(n_t - off), end - u);
             const int h = item / p.RB, rb = item - h * p.RB;
-            const long long row = (long long)rb * ROWS + tid;
+            const long long row = (long long)rb * ROWS + lrow;
             const bool real = row < p.rows_item;
             const int bt = real ? (int)(row / p.G) : 0, g = real ? (int)(row - (long long)bt * p.G) : 0;
             const int b = bt / p.T, t = bt - b * p.T;
             const bool live = real && shares(p, b);
-            // the row's query; every product that read the last one has ended (its S came)
+            // half of the row's query; every product that read the last one has ended (all scores came)
             {
                 const uint16_t* src = p.q + b * p.qb + t * p.qt + (long long)(h * p.G + g) * p.qh;
                 const bool wide = ((uintptr_t)src & 15) == 0;
 #pragma unroll
-                for (int i = 0; i < D / 8; ++i) {
+                for (int j = 0; j < D / 16; ++j) {
+                    const int i = wg * (D / 16) + j;
                     uint4 x = make_uint4(0, 0, 0, 0);
                     if (live) {
                         if (wide) {
@@ -306,7 +321,7 @@ __global__ void __launch_bounds__(288, 1) prefix_kernel(const __grid_constant__ 
                             x = make_uint4(w[0], w[1], w[2], w[3]);
                         }
                     }
-                    *reinterpret_cast<uint4*>(smem + (panel_at(qs, ROWS, tid, i) - qs)) = x;
+                    *reinterpret_cast<uint4*>(smem + (panel_at(qs, ROWS, lrow, i) - qs)) = x;
                 }
                 asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                 bar_arrive(&ms.q_ready);
@@ -315,18 +330,18 @@ __global__ void __launch_bounds__(288, 1) prefix_kernel(const __grid_constant__ 
             const float slope2 = p.slopes ? p.slopes[h * p.G + g] * LOG2E : 0.f;
             const int at = live ? p.lens[b] - p.T + t : 0;
             float m = -INFINITY, l = 0.f;
-            bool ok = true;
-            for (int i = 0; i < take; ++i) {
-                const int buf = at_c.buf(), stage = at_c.stage;
+            bool fresh = true;  // no tile of this piece yet
+            for (int i = (parity ^ wg) & 1; i < take && ok; i += 2) {
+                const int stage = at_c.stage;
                 const int j0 = (off + i) * TILE;
-                if (!(ok = warp_wait(&ms.s_full[buf], at_c.pair(), abort))) break;
+                if (!(ok = warp_wait(&ms.s_full[wg], at_c.pair(), abort))) break;
                 tm_after();
                 uint32_t s0[32], s1[32];
-                tm_ld32(s0, my + S::T_S + buf * TILE);
-                tm_ld32(s1, my + S::T_S + buf * TILE + 32);
+                tm_ld32(s0, my_s);
+                tm_ld32(s1, my_s + 32);
                 tm_wait_ld();
                 tm_before();
-                bar_arrive(&ms.s_free[buf]);
+                bar_arrive(&ms.s_free[wg]);
                 const float* ksc = scales + stage * 2 * TILE;
                 // the scales come with the tile
                 if (F8 && !(ok = warp_wait(&ms.kv_full[stage], at_c.full(), abort))) break;
@@ -369,8 +384,8 @@ __global__ void __launch_bounds__(288, 1) prefix_kernel(const __grid_constant__ 
                 for (int j = 0; j < 32; ++j) top[j & 3] = fmaxf(top[j & 3], fmaxf(__uint_as_float(s0[j]), __uint_as_float(s1[j])));
                 const float mx = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
                 // the reference: the first tile's maximum, or a new one past 2^8 of the old
-                const bool rise = i == 0 || mx > m + 8.f;
-                if (i == 0) {
+                const bool rise = mx > m + 8.f;
+                if (fresh) {
                     m = mx;
                 } else if (__any_sync(0xffffffffu, rise)) {
                     const float mn = rise ? mx : m;
@@ -378,16 +393,16 @@ __global__ void __launch_bounds__(288, 1) prefix_kernel(const __grid_constant__ 
                     m = mn;
                     l *= f;
                     // every product so far is in O
-                    if (!(ok = warp_wait(&ms.pv_done[back1.stage], back1.full(), abort))) break;
+                    if (!(ok = warp_wait(&ms.pv_done[back.stage], back.full(), abort))) break;
                     tm_after();
 #pragma unroll 1
                     for (int d = 0; d < D; d += 32) {
                         uint32_t o[32];
-                        tm_ld32(o, my + S::T_O + d);
+                        tm_ld32(o, my_o + d);
                         tm_wait_ld();
 #pragma unroll
                         for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
-                        tm_st32(my + S::T_O + d, o);
+                        tm_st32(my_o + d, o);
                     }
                     tm_wait_st();
                 }
@@ -414,44 +429,61 @@ __global__ void __launch_bounds__(288, 1) prefix_kernel(const __grid_constant__ 
                     pair(s1[2 * j + 2], s1[2 * j + 3], vb.z, vb.w, hi[17 + j], lo[17 + j], sum[3]);
                 }
                 l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
-                // the P buffer is free when the product two tiles ago has read it
-                if (at_c.c >= 2 && !(ok = warp_wait(&ms.pv_done[back2.stage], back2.full(), abort))) break;
+                // the P buffer is free when the group's last product has read it
+                if (at_c.c >= 2 && !(ok = warp_wait(&ms.pv_done[back.stage], back.full(), abort))) break;
                 tm_after();
-                tm_st32(my + S::T_P + buf * TILE, hi);
-                tm_st32(my + S::T_P + buf * TILE + 32, lo);
+                tm_st32(my_p, hi);
+                tm_st32(my_p + 32, lo);
                 tm_wait_st();
                 tm_before();
-                bar_arrive(&ms.p_ready[buf]);
-                back2 = back1;
-                back1 = at_c;
+                bar_arrive(&ms.p_ready[wg]);
+                fresh = false;
+                back = at_c;
+                at_c.next();
                 at_c.next();
             }
-            if (!ok) break;
-            // ---- the piece: O out of tensor memory
-            if (!warp_wait(&ms.pv_done[back1.stage], back1.full(), abort)) break;
+            parity ^= take & 1;
+            // ---- the piece: both groups' outputs join out of tensor memory, half of the columns by each
+            // (a group that gave up keeps the barriers)
+            if (ok && !fresh) ok = warp_wait(&ms.pv_done[back.stage], back.full(), abort);
+            ms.stat[wg][lrow] = make_float2(m, l);
+            tm_before();
+            asm volatile("bar.sync 2, 256;" ::: "memory");
             tm_after();
+            const float2 s0 = ms.stat[0][lrow], s1 = ms.stat[1][lrow];
+            const float mm = fmaxf(s0.x, s1.x), mr = mm == -INFINITY ? 0.f : mm;
+            const float f0 = ex2(s0.x - mr), f1 = ex2(s1.x - mr), ll = s0.y * f0 + s1.y * f1;
+            // a group without a tile (or without a finite score) has nothing in its output
+            const bool has0 = s0.x != -INFINITY, has1 = s1.x != -INFINITY;
             const bool whole = take == n_t;
             float* slot = p.slots + (whole ? 2ll * gridDim.x + item : 2ll * blockIdx.x + (u == first ? 0 : 1)) * p.slot_floats;
 #pragma unroll 1
-            for (int d = 0; d < D; d += 32) {
-                uint32_t o[32];
-                tm_ld32(o, my + S::T_O + d);
+            for (int d = wg * (D / 2); d < (wg + 1) * (D / 2); d += 32) {
+                uint32_t x[32], y[32];
+                tm_ld32(x, my + S::T_O + d);
+                tm_ld32(y, my + S::T_O + D + d);
                 tm_wait_ld();
                 if (real) {
 #pragma unroll
-                    for (int e = 0; e < 32; e += 4)
-                        *reinterpret_cast<uint4*>(slot + (long long)tid * D + d + e) = make_uint4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+                    for (int e = 0; e < 32; e += 4) {
+                        float z[4];
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            z[i] = (has0 ? __uint_as_float(x[e + i]) * f0 : 0.f) + (has1 ? __uint_as_float(y[e + i]) * f1 : 0.f);
+                        *reinterpret_cast<float4*>(slot + (long long)lrow * D + d + e) = make_float4(z[0], z[1], z[2], z[3]);
+                    }
                 }
             }
             tm_before();
-            if (real)
-                *reinterpret_cast<float2*>(slot + (long long)p.slot_rows * D + 2 * tid) =
-                    live ? make_float2(m, l) : make_float2(-INFINITY, 0.f);
+            if (real && wg == 0)
+                *reinterpret_cast<float2*>(slot + (long long)p.slot_rows * D + 2 * lrow) =
+                    live ? make_float2(mm, ll) : make_float2(-INFINITY, 0.f);
+            asm volatile("bar.sync 2, 256;" ::: "memory");  // the outputs have been read
             u += take;
         }
-    } else if (!F8 && warp < 8) {
+    } else if (!F8 && warp < MMA_WARP) {
         // ================ loads by tensor maps: one warp ================
-        if (warp == 4) {
+        {
             // A tile is `parts` boxes of up to 64 rows of one page. The lanes hold the pages of the next 32 boxes,
             // and of the 32 after them.
             const int rows = min(TILE, 1 << p.ps_shift), parts = TILE / rows, mask = (1 << p.ps_shift) - 1;
@@ -502,9 +534,9 @@ __global__ void __launch_bounds__(288, 1) prefix_kernel(const __grid_constant__ 
                     }
             }
         }
-    } else if (warp < 8) {
+    } else if (warp < MMA_WARP) {
         // ================ loads of codes ================
-        const int t = tid - 128;
+        const int t = tid - 256;
         const int mask = (1 << p.ps_shift) - 1;
         constexpr int CH = D * (F8 ? 1 : 2) / 16;  // 16-byte pieces of a cached row
         constexpr int EACH = TILE * CH / 128;      // pieces of K (and of V) a thread copies
@@ -642,7 +674,8 @@ __global__ void __launch_bounds__(288, 1) prefix_kernel(const __grid_constant__ 
                     for (int part = 0; part < 2; ++part)
 #pragma unroll
                         for (int j = 0; j < TILE / 16; ++j)
-                            mma_ts(tmu + S::T_O, pa + part * 32 + j * 8, desc_on(v, j * 2048), PV, i > 0 || part > 0 || j > 0);
+                            mma_ts(tmu + S::T_O + at_c.buf() * D, pa + part * 32 + j * 8, desc_on(v, j * 2048), PV,
+                                   i > 1 || part > 0 || j > 0);
                     mma_commit(&ms.pv_done[at_c.stage]);
                 }
                 __syncwarp();
@@ -661,7 +694,7 @@ __global__ void __launch_bounds__(288, 1) prefix_kernel(const __grid_constant__ 
     __syncthreads();
     tm_after();
     if (tid == 0 && ms.abort && p.status) *p.status = MK_ERR_TIMEOUT;
-    if (warp == 8)
+    if (warp == MMA_WARP)
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tm), "n"(S::T_ALL) : "memory");
 }
 
