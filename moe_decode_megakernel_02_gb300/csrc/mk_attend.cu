@@ -127,7 +127,8 @@ int make_plan(const mk_attention* a, Plan& pl) {
         pl.sh_k = Kind{g.format, splitq, block_of(all)};
         // (its tensor maps want distinct rows, 8 or more of them a page)
         pl.prefix = D <= 128 && a->q->dtype == MK_DT_BF16 && all > 32 && g.page_size >= 8 && g.row_stride > 0 &&
-                    g.head_stride > 0 && g.page_stride > 0;
+                    g.head_stride > 0 && g.page_stride > 0 &&
+                    (int64_t)H * (all / 128 + 1) * (a->shared_len / 64 + 1) < INT32_MAX / 2;
         if (const int rc = pl.prefix ? prefix_info(dev, D, g.format, pl.sh_i) : kind_info(dev, D, pl.sh_k, pl.sh_i))
             return rc;
         if (pl.sh_i.ctas < 1) return fail(MK_ERR_UNSUPPORTED, "attend: the kernel does not fit this device");

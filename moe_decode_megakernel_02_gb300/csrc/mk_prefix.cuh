@@ -17,9 +17,9 @@
 // Two groups of four warps: softmax, a row a thread, of the even and of the odd
 // tiles; each group keeps its own maxima, sums and output, which meet at the
 // piece's end. Then loads (bf16 pages: one warp, by tensor maps; 8-bit pages:
-// four warps, codes through registers, as E4M3 and INT8 codes are exact in
-// bf16; the K scale multiplies the score, the V scale the probability) and one
-// warp whose elected thread issues the products, S of the next tile before P V of this one, so that the
+// four warps, which turn staged codes into bf16 -- E4M3 and INT8 codes are
+// exact in it; the K scale multiplies the score, the V scale the probability)
+// and two warps, an elected thread of which issues Q K^T, and P V, S of the next tile before P V of this one, so that the
 // tensor cores work while the softmax does. All waits are on mbarriers with a
 // limit; a wait that runs out raises a flag that every role sees, and the CTA
 // leaves after freeing its tensor memory (MK_ERR_TIMEOUT in `status`).
@@ -45,12 +45,14 @@ struct PrefixShape {
     static constexpr int KV_B = PANELS * TILE * 128;  // K (or V) of a tile
     static constexpr int STAGE_B = 2 * KV_B;
     static constexpr int SCALE_B = 2 * TILE * 4;   // of a stage: K scales, V scales (8-bit pages)
-    static constexpr int STAGES = D == 128 ? 5 : 8;
+    static constexpr int STAGES = D == 128 ? (F8 ? 3 : 5) : (F8 ? 6 : 8);
+    static constexpr int RAW_B = 2 * TILE * D + SCALE_B, RAWS = 3;  // staged codes and scales of a tile
     static constexpr int SC_OFF = Q_B + STAGES * STAGE_B;
-    static constexpr int MISC_OFF = SC_OFF + STAGES * SCALE_B;
+    static constexpr int RAW_OFF = SC_OFF + STAGES * SCALE_B;
+    static constexpr int MISC_OFF = RAW_OFF + (F8 ? RAWS * RAW_B : 0);
     static constexpr int MISC_B = 4096;
     static constexpr int SMEM = MISC_OFF + MISC_B + 1024;  // and room to align to 1024
-    static constexpr int LOADERS = F8 ? 4 : 1, NT = 32 * (8 + LOADERS + 1);  // warps: softmax, loads, products
+    static constexpr int LOADERS = F8 ? 4 : 1, NT = 32 * (8 + LOADERS + 2);  // warps: softmax, loads, products
     // tensor memory columns of the two groups: S, P (hi, lo), O
     static constexpr int T_S = 0, T_P = 2 * TILE, T_O = T_P + 2 * TILE, T_ALL = 512;
     static_assert(T_O + 2 * D <= T_ALL && SMEM <= 227 * 1024, "");
@@ -253,9 +255,10 @@ __global__ void __launch_bounds__(PrefixShape<D, FMT>::NT, 1) prefix_kernel(cons
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     volatile unsigned* const abort = &ms.abort;
 
-    const int items = p.H * p.RB, n_t = (p.shared + TILE - 1) / TILE;
-    const long long total = (long long)items * n_t, per = units_each(total, gridDim.x, p.min_units);
-    const long long first = per * blockIdx.x, end = min(total, first + per);
+    // (the host sees to it that the tiles of all items fit 32 bits)
+    const int n_t = (p.shared + TILE - 1) / TILE, total = p.H * p.RB * n_t;
+    const int per = (int)units_each(total, gridDim.x, p.min_units);
+    const int first = per * blockIdx.x, end = min(total, first + per);
     if (first >= end) return;
 
     if (tid == 0) {
@@ -269,7 +272,7 @@ __global__ void __launch_bounds__(PrefixShape<D, FMT>::NT, 1) prefix_kernel(cons
             bar_init(&ms.p_ready[i], 128);
         }
         bar_init(&ms.q_ready, 256);
-        bar_init(&ms.drained, 1);
+        bar_init(&ms.drained, 2);
         ms.abort = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
@@ -295,12 +298,12 @@ __global__ void __launch_bounds__(PrefixShape<D, FMT>::NT, 1) prefix_kernel(cons
         int parity = 0;               // of the tile that comes next, over both groups
         if (wg) at_c.next();
         bool ok = true;
-        for (long long u = first; u < end;) {
-            const int item = (int)(u / n_t), off = (int)(u % n_t), take = (int)min((long long)(n_t - off), end - u);
+        for (int u = first; u < end;) {
+            const int item = u / n_t, off = u - item * n_t, take = min(n_t - off, end - u);
             const int h = item / p.RB, rb = item - h * p.RB;
-            const long long row = (long long)rb * ROWS + lrow;
+            const int row = rb * ROWS + lrow;
             const bool real = row < p.rows_item;
-            const int bt = real ? (int)(row / p.G) : 0, g = real ? (int)(row - (long long)bt * p.G) : 0;
+            const int bt = real ? row / p.G : 0, g = real ? row - bt * p.G : 0;
             const int b = bt / p.T, t = bt - b * p.T;
             const bool live = real && shares(p, b);
             // half of the row's query; every product that read the last one has ended (all scores came)
@@ -487,10 +490,10 @@ __global__ void __launch_bounds__(PrefixShape<D, FMT>::NT, 1) prefix_kernel(cons
             // A tile is `parts` boxes of up to 64 rows of one page. The lanes hold the pages of the next 32 boxes,
             // and of the 32 after them.
             const int rows = min(TILE, 1 << p.ps_shift), parts = TILE / rows, mask = (1 << p.ps_shift) - 1;
-            const long long tiles = end - first, boxes = tiles * parts;
-            auto page_of = [&](long long i) {  // of box i; one that does not exist reads as zeros
-                if (i >= boxes) return p.n_pages;
-                const int pos = (int)((first + i / parts) % n_t) * TILE + (int)(i % parts) * rows;
+            const int tiles = end - first, pshift = __ffs(parts) - 1;
+            auto page_of = [&](int i) {  // of box i; one that does not exist reads as zeros
+                if (i >> pshift >= tiles) return p.n_pages;
+                const int pos = (first + (i >> pshift)) % n_t * TILE + (i & (parts - 1)) * rows;
                 if (pos >= p.shared) return p.n_pages;
                 const int page = p.table[pos >> p.ps_shift];
                 if ((unsigned)page < (unsigned)p.n_pages) return page;
@@ -499,17 +502,17 @@ __global__ void __launch_bounds__(PrefixShape<D, FMT>::NT, 1) prefix_kernel(cons
             };
             int now = page_of(lane), next = page_of(32 + lane);
             bool ok = true;
-            long long box = 0;
+            int box = 0;
             Place<S::STAGES> pl;
-            int item = (int)(first / n_t), tile = (int)(first % n_t);
-            for (long long c = 0; c < tiles; ++c, pl.next()) {
+            int item = first / n_t, tile = first - item * n_t;
+            for (int c = 0; c < tiles; ++c, pl.next()) {
                 const int stage = pl.stage, h = item / p.RB, j0 = tile * TILE;
                 if (++tile == n_t) tile = 0, ++item;
                 const uint32_t st = ring + stage * S::STAGE_B;
                 if (c >= S::STAGES && !(ok = warp_wait(&ms.pv_done[stage], pl.free(), abort))) break;
                 if (lane == 0) bar_expect(&ms.kv_full[stage], S::STAGE_B);
                 for (int i = 0; i < parts; ++i, ++box) {
-                    const int page = __shfl_sync(0xffffffffu, now, (int)(box & 31));
+                    const int page = __shfl_sync(0xffffffffu, now, box & 31);
                     if (lane == 0) {
                         const int row = (j0 + i * rows) & mask;
 #pragma unroll
@@ -528,8 +531,8 @@ __global__ void __launch_bounds__(PrefixShape<D, FMT>::NT, 1) prefix_kernel(cons
             // a launch that gave up still waits for its copies on the way
             if (!ok) {
                 const long long t0 = now_ns();
-                const long long to = box / parts;  // tiles sent
-                for (long long c = max(0ll, to - S::STAGES); c < to; ++c)
+                const int to = box >> pshift;  // tiles sent
+                for (int c = max(0, to - S::STAGES); c < to; ++c)
                     while (!bar_try(&ms.kv_full[c % S::STAGES], (unsigned)(c / S::STAGES) & 1u) && now_ns() - t0 < PREFIX_WAIT_NS) {
                     }
             }
@@ -541,67 +544,72 @@ __global__ void __launch_bounds__(PrefixShape<D, FMT>::NT, 1) prefix_kernel(cons
         constexpr int CH = D * (F8 ? 1 : 2) / 16;  // 16-byte pieces of a cached row
         constexpr int EACH = TILE * CH / 128;      // pieces of K (and of V) a thread copies
         const int cc = t % CH;
-        const long long tiles = end - first;
-        auto look = [&](long long c) {  // where row t of tile c lies, and its scales
-            if (t < TILE && c < tiles) {
-                const int pos = (int)((first + c) % n_t) * TILE + t;
-                int page = -1;
-                if (pos < p.shared) {
-                    page = p.table[pos >> p.ps_shift];
-                    if ((unsigned)page >= (unsigned)p.n_pages) {
-                        page = -1;
-                        if (p.status) *p.status = MK_ERR_INVALID_ARG;
-                    }
-                }
-                return page;
-            }
+        const int tiles = end - first;
+        const uint32_t raw0 = qs + S::RAW_OFF;
+        // Row t of a tile: its page, looked up two tiles ahead of the copies, which are two ahead of their use. A
+        // thread turns what it copied itself, so only the rows' places pass between threads.
+        auto look = [&](int c) {
+            if (t >= TILE || c >= tiles) return -1;
+            const int pos = (first + c) % n_t * TILE + t;
+            if (pos >= p.shared) return -1;
+            const int page = p.table[pos >> p.ps_shift];
+            if ((unsigned)page < (unsigned)p.n_pages) return page;
+            if (p.status) *p.status = MK_ERR_INVALID_ARG;
             return -1;
         };
-        auto note = [&](long long c, int page) {
+        auto note = [&](int c, int page) {
             if (t < TILE && c < tiles) {
-                const int r = ((int)((first + c) % n_t) * TILE + t) & mask;
+                const int r = ((first + c) % n_t * TILE + t) & mask;
                 ms.off[c & 1][t] = page < 0 ? -1 : page * p.page_b + r * p.row_b;
             }
         };
-        // pages two tiles ahead of their use, 8-bit codes and scales one: each is a trip to memory
-        int page = look(0), next = look(1);
-        note(0, page);
-        asm volatile("bar.sync 1, 128;" ::: "memory");
-        uint4 k[F8 ? EACH : 1], v[F8 ? EACH : 1];
-        float sk = 0.f, sv = 0.f;
-        auto codes = [&](long long c, int pg) {  // of tile c, to registers
-            if constexpr (F8) {
-                if (c >= tiles) return;
-                const int h = (int)((first + c) / n_t) / p.RB;
+        auto copy = [&](int c, int page) {
+            if (c < tiles) {
+                const int h = (first + c) / n_t / p.RB;
                 const uint8_t* const kh = p.k + h * p.head_b;
                 const uint8_t* const vh = p.v + h * p.head_b;
+                const uint32_t to = raw0 + c % S::RAWS * S::RAW_B;
 #pragma unroll
                 for (int i = 0; i < EACH; ++i) {
-                    const long long o = ms.off[c & 1][t / CH + i * (128 / CH)];
-                    k[i] = v[i] = make_uint4(0, 0, 0, 0);
-                    if (o >= 0) {
-                        k[i] = __ldg(reinterpret_cast<const uint4*>(kh + o + cc * 16));
-                        v[i] = __ldg(reinterpret_cast<const uint4*>(vh + o + cc * 16));
-                    }
+                    const int r = t / CH + i * (128 / CH);
+                    const long long o = ms.off[c & 1][r];
+                    const bool in = o >= 0;
+                    const long long a = in ? o + cc * 16 : 0;
+                    cp16(to + (i * 128 + t) * 16, kh + a, in);
+                    cp16(to + TILE * D + (i * 128 + t) * 16, vh + a, in);
                 }
-                sk = sv = 0.f;
-                if (t < TILE && pg >= 0) {
-                    const int r = ((int)((first + c) % n_t) * TILE + t) & mask;
-                    const long long o = pg * p.sc_page + h * p.sc_head + r;
-                    sk = __ldg(p.ks + o), sv = __ldg(p.vs + o);
+                if (t < TILE) {
+                    const int r = ((first + c) % n_t * TILE + t) & mask;
+                    const long long o = page < 0 ? 0 : page * p.sc_page + h * p.sc_head + r;
+                    cp4(to + 2 * TILE * D + t * 4, p.ks + o, page >= 0);
+                    cp4(to + 2 * TILE * D + (TILE + t) * 4, p.vs + o, page >= 0);
                 }
             }
+            cp_commit();
         };
-        codes(0, page);
-        bool ok = true;
+        auto here = [] { asm volatile("bar.sync 1, 128;" ::: "memory"); };
+        int page0 = look(0), page1 = look(1), page2 = look(2);
+        note(0, page0);
+        note(1, page1);
+        here();
+        copy(0, page0);
+        copy(1, page1);
+        here();
         Place<S::STAGES> pl;
-        for (long long c = 0; c < tiles; ++c, pl.next()) {
+        bool ok = true;
+        for (int c = 0; c < tiles; ++c, pl.next()) {
             const int stage = pl.stage;
             const uint32_t st = ring + stage * S::STAGE_B;
-            const int after = look(c + 2);
+            const int page3 = look(c + 3);
+            note(c + 2, page2);  // over the places of tile c, which were read two barriers ago
+            here();
+            copy(c + 2, page2);
+            page2 = page3;
             // a thread that gave up keeps the loop's barriers
             if (ok && c >= S::STAGES) ok = bar_wait(&ms.pv_done[stage], pl.free(), abort);
-            if constexpr (F8) {
+            cp_wait<2>();
+            if (ok) {
+                const uint8_t* const raw = smem + S::RAW_OFF + c % S::RAWS * S::RAW_B;
                 auto put = [&](uint32_t base, int r, const uint4& w) {
                     uint4 a, b;
                     codes_bf16<FMT>(w.x, a.x, a.y);
@@ -611,77 +619,80 @@ __global__ void __launch_bounds__(PrefixShape<D, FMT>::NT, 1) prefix_kernel(cons
                     *reinterpret_cast<uint4*>(smem + (panel_at(base, TILE, r, 2 * cc) - qs)) = a;
                     *reinterpret_cast<uint4*>(smem + (panel_at(base, TILE, r, 2 * cc + 1) - qs)) = b;
                 };
-                if (ok) {
 #pragma unroll
-                    for (int i = 0; i < EACH; ++i) {
-                        const int r = t / CH + i * (128 / CH);
-                        put(st, r, k[i]);
-                        put(st + S::KV_B, r, v[i]);
-                    }
-                    if (t < TILE) {
-                        scales[stage * 2 * TILE + t] = sk;
-                        scales[stage * 2 * TILE + TILE + t] = sv;
-                    }
-                    // this thread's part of the tile lies in shared memory
-                    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-                    bar_arrive(&ms.kv_full[stage]);
+                for (int i = 0; i < EACH; ++i) {
+                    const int r = t / CH + i * (128 / CH);
+                    put(st, r, *reinterpret_cast<const uint4*>(raw + (i * 128 + t) * 16));
+                    put(st + S::KV_B, r, *reinterpret_cast<const uint4*>(raw + TILE * D + (i * 128 + t) * 16));
                 }
-                note(c + 1, next);
-                asm volatile("bar.sync 1, 128;" ::: "memory");
-                codes(c + 1, next);
+                if (t < TILE) {
+                    const float* sc = reinterpret_cast<const float*>(raw + 2 * TILE * D);
+                    scales[stage * 2 * TILE + t] = sc[t];
+                    scales[stage * 2 * TILE + TILE + t] = sc[TILE + t];
+                }
+                // this thread's part of the tile lies in shared memory
+                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                bar_arrive(&ms.kv_full[stage]);
             }
-            page = next;
-            next = after;
         }
+        cp_wait<0>();
     } else {
-        // ================ products: a warp in step, one lane issues ================
-        constexpr uint32_t QK = mma_desc(ROWS, TILE, false), PV = mma_desc(ROWS, D, true);
+        // ================ products: two warps in step, one lane of each issues ================
         const uint32_t tmu = __shfl_sync(0xffffffffu, tm, 0);
-        const uint64_t q = smem_desc(qs, 16, 1024);
-        const uint64_t k0 = smem_desc(ring, 16, 1024), v0 = smem_desc(ring + S::KV_B, TILE * 128, 1024);
-        Place<S::STAGES> ahead, at_c;  // the tile whose scores come next, and whose output
+        Place<S::STAGES> at_c;
         unsigned piece_no = 0;
         bool ok = true;
-        for (long long u = first; u < end && ok; ++piece_no) {
-            const int off = (int)(u % n_t), take = (int)min((long long)(n_t - off), end - u);
-            if (!(ok = warp_wait(&ms.q_ready, piece_no & 1u, abort))) break;
-            for (int i = -1; i < take; ++i) {
-                if (i + 1 < take) {
-                    // K and V are here; the softmax has read what the S buffer held two tiles ago
-                    ok = warp_wait(&ms.kv_full[ahead.stage], ahead.full(), abort) &&
-                         (ahead.c < 2 || warp_wait(&ms.s_free[ahead.buf()], ahead.pair_free(), abort));
+        if (warp == MMA_WARP) {
+            constexpr uint32_t QK = mma_desc(ROWS, TILE, false);
+            const uint64_t q = smem_desc(qs, 16, 1024), k0 = smem_desc(ring, 16, 1024);
+            for (int u = first; u < end && ok; ++piece_no) {
+                const int off = u % n_t, take = min(n_t - off, end - u);
+                u += take;
+                ok = warp_wait(&ms.q_ready, piece_no & 1u, abort);
+                for (int i = 0; i < take && ok; ++i) {
+                    // K is here; the softmax has read what the S buffer held two tiles ago
+                    ok = warp_wait(&ms.kv_full[at_c.stage], at_c.full(), abort) &&
+                         (at_c.c < 2 || warp_wait(&ms.s_free[at_c.buf()], at_c.pair_free(), abort));
                     if (!ok) break;
                     tm_after();
                     if (elect_one()) {
-                        const uint64_t k = desc_on(k0, ahead.stage * S::STAGE_B);
-                        const uint32_t d = tmu + S::T_S + ahead.buf() * TILE;
+                        const uint64_t k = desc_on(k0, at_c.stage * S::STAGE_B);
+                        const uint32_t d = tmu + S::T_S + at_c.buf() * TILE;
 #pragma unroll
                         for (int j = 0; j < D / 16; ++j)
                             mma_ss(d, desc_on(q, (j >> 2) * ROWS * 128 + (j & 3) * 32),
                                    desc_on(k, (j >> 2) * TILE * 128 + (j & 3) * 32), QK, j > 0);
-                        mma_commit(&ms.s_full[ahead.buf()]);
+                        mma_commit(&ms.s_full[at_c.buf()]);
                     }
                     __syncwarp();
-                    ahead.next();
+                    at_c.next();
                 }
-                if (i < 0) continue;
-                if (!(ok = warp_wait(&ms.p_ready[at_c.buf()], at_c.pair(), abort))) break;
-                tm_after();
-                if (elect_one()) {
-                    const uint64_t v = desc_on(v0, at_c.stage * S::STAGE_B);
-                    const uint32_t pa = tmu + S::T_P + at_c.buf() * TILE;
-#pragma unroll
-                    for (int part = 0; part < 2; ++part)
-#pragma unroll
-                        for (int j = 0; j < TILE / 16; ++j)
-                            mma_ts(tmu + S::T_O + at_c.buf() * D, pa + part * 32 + j * 8, desc_on(v, j * 2048), PV,
-                                   i > 1 || part > 0 || j > 0);
-                    mma_commit(&ms.pv_done[at_c.stage]);
-                }
-                __syncwarp();
-                at_c.next();
             }
-            u += take;
+        } else {
+            constexpr uint32_t PV = mma_desc(ROWS, D, true);
+            const uint64_t v0 = smem_desc(ring + S::KV_B, TILE * 128, 1024);
+            for (int u = first; u < end && ok;) {
+                const int off = u % n_t, take = min(n_t - off, end - u);
+                u += take;
+                for (int i = 0; i < take; ++i) {
+                    // the probabilities are here, and so V (their scores came from the same stage)
+                    if (!(ok = warp_wait(&ms.p_ready[at_c.buf()], at_c.pair(), abort))) break;
+                    tm_after();
+                    if (elect_one()) {
+                        const uint64_t v = desc_on(v0, at_c.stage * S::STAGE_B);
+                        const uint32_t pa = tmu + S::T_P + at_c.buf() * TILE, d = tmu + S::T_O + at_c.buf() * D;
+                        // the first tile of each group's piece overwrites
+#pragma unroll
+                        for (int part = 0; part < 2; ++part)
+#pragma unroll
+                            for (int j = 0; j < TILE / 16; ++j)
+                                mma_ts(d, pa + part * 32 + j * 8, desc_on(v, j * 2048), PV, i > 1 || part > 0 || j > 0);
+                        mma_commit(&ms.pv_done[at_c.stage]);
+                    }
+                    __syncwarp();
+                    at_c.next();
+                }
+            }
         }
         // the last products end before the tensor memory goes, also when a role gave up
         if (elect_one()) mma_commit(&ms.drained);
