@@ -113,11 +113,12 @@ int make_plan(const mk_attention* a, Plan& pl) {
         }
     }
     const int64_t most = items * ((cap + pl.own_i.tile - 1) / pl.own_i.tile + 1);
+    if (most > (1 << 30)) return fail(MK_ERR_UNSUPPORTED, "attend: too many positions in one call");
     int64_t grid = (int64_t)sms * pl.own_i.ctas;
     if (grid > (most + min_units - 1) / min_units) grid = (most + min_units - 1) / min_units;
     pl.own_grid = (int)grid;
     pl.base_off = 0;
-    pl.own_off = up256((int64_t)(B + 1) * 8);
+    pl.own_off = up256((int64_t)(B + 1) * 4);
     const int64_t own_slots = 2 * grid + (a->shared_len ? items : 0);
     pl.bytes = up256(pl.own_off + own_slots * pl.own_floats * 4);
     pl.sh_grid = 0;
@@ -127,8 +128,7 @@ int make_plan(const mk_attention* a, Plan& pl) {
         pl.sh_k = Kind{g.format, splitq, block_of(all)};
         // (its tensor maps want distinct rows, 8 or more of them a page)
         pl.prefix = D <= 128 && a->q->dtype == MK_DT_BF16 && all > 32 && g.page_size >= 8 && g.row_stride > 0 &&
-                    g.head_stride > 0 && g.page_stride > 0 &&
-                    (int64_t)H * (all / 128 + 1) * (a->shared_len / 64 + 1) < INT32_MAX / 2;
+                    g.head_stride > 0 && g.page_stride > 0;
         if (const int rc = pl.prefix ? prefix_info(dev, D, g.format, pl.sh_i) : kind_info(dev, D, pl.sh_k, pl.sh_i))
             return rc;
         if (pl.sh_i.ctas < 1) return fail(MK_ERR_UNSUPPORTED, "attend: the kernel does not fit this device");
@@ -137,6 +137,7 @@ int make_plan(const mk_attention* a, Plan& pl) {
         pl.sh_floats = slot_floats(pl.sh_slot_rows, D);
         const int64_t sh_items = (int64_t)H * pl.sh_rb;
         const int64_t units = sh_items * ((a->shared_len + pl.sh_i.tile - 1) / pl.sh_i.tile);
+        if (units > (1 << 30)) return fail(MK_ERR_UNSUPPORTED, "attend: too many positions in one call");
         int64_t sg = (int64_t)sms * pl.sh_i.ctas;
         if (sg > (units + min_units - 1) / min_units) sg = (units + min_units - 1) / min_units;
         pl.sh_grid = (int)sg;
@@ -179,7 +180,7 @@ extern "C" int mk_pages_attend(const mk_attention* a, void* workspace, int64_t w
     p.min_units = 2;
     p.RB = pl.own_rb, p.rows_item = p.T * p.G, p.keep_items = a->shared_len > 0;
     p.slot_rows = pl.own_slot_rows, p.slot_floats = pl.own_floats;
-    p.slots = (float*)(ws + pl.own_off), p.base = (long long*)(ws + pl.base_off);
+    p.slots = (float*)(ws + pl.own_off), p.base = (int*)(ws + pl.base_off);
     JoinP j = {};
     j.own = p, j.own_grid = pl.own_grid, j.own_rows = pl.own_i.rows;
     const AttendFn fn = D == 64 ? attend_64 : D == 128 ? attend_128 : attend_256;

@@ -74,7 +74,7 @@ struct AttendP {
     int slot_rows;   // rows of a slot: slot_rows * D outputs, then (maximum, sum) pairs
     int slot_floats;
     float* slots;    // two of each CTA (its first and its last piece), then one of each item
-    long long* base;  // [B + 1]: first unit of each sequence, written for the joining launch
+    int* base;       // [B + 1]: first unit of each sequence, written for the joining launch
 };
 
 struct JoinP {
@@ -88,8 +88,9 @@ constexpr int JT = 128;  // threads of a joining CTA
 constexpr float LOG2E = 1.4426950408889634f, LN2 = 0.6931471805599453f;
 
 // units (tiles) of each CTA when `total` are shared out over `grid`
-__host__ __device__ __forceinline__ long long units_each(long long total, int grid, int min_units) {
-    const long long e = (total + grid - 1) / grid;
+// (the host keeps totals below 2^30)
+__host__ __device__ __forceinline__ int units_each(int total, int grid, int min_units) {
+    const int e = (total + grid - 1) / grid;
     return e < min_units ? min_units : e;
 }
 
@@ -234,8 +235,8 @@ struct Shape {
 template <int ROWS, int TILE>
 struct Misc {
     long long off[2][TILE];  // bytes after the head's first row; -1: no such row, zeros
-    long long scan[8];
-    long long found_base;
+    int scan[8];
+    int found_base;
     float slope2[ROWS];  // slope * log2 e
     float qscale[ROWS];  // 8-bit pages: the power of two taken out of the query
     int lo[ROWS], hi[ROWS], at[ROWS];
@@ -313,7 +314,7 @@ __global__ void __launch_bounds__(32 * WP * WR, Shape<D, FMT, SPLITQ, WP, WR, RN
     // ---- this CTA's stretch of units
     const int items = p.H * p.RB;  // items of one (virtual) sequence
     const int nb = p.is_shared ? 1 : p.B;
-    long long total = 0, my_first = 0;
+    int total = 0, my_first = 0;
     if (CL) {
         if (p.status && blockIdx.x == 0)
             for (int b = tid; b < p.B; b += AT)
@@ -321,21 +322,21 @@ __global__ void __launch_bounds__(32 * WP * WR, Shape<D, FMT, SPLITQ, WP, WR, RN
     } else {
         // each thread counts a stretch of sequences; sums before it by shuffles
         const int each = (nb + AT - 1) / AT, b0 = min(nb, tid * each), b1 = min(nb, b0 + each);
-        long long mine = 0;
+        int mine = 0;
         for (int b = b0; b < b1; ++b) {
-            mine += (long long)cover_units<TILE>(p, b) * items;
+            mine += cover_units<TILE>(p, b) * items;
             if (p.status && !p.is_shared && blockIdx.x == 0 && p.lens[b] > (p.pps << p.ps_shift))
                 *p.status = MK_ERR_INVALID_ARG;
         }
-        long long inc = mine;
+        int inc = mine;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
-            const long long a = __shfl_up_sync(0xffffffffu, inc, o);
+            const int a = __shfl_up_sync(0xffffffffu, inc, o);
             if (lane >= o) inc += a;
         }
         if (lane == 31) ms.scan[warp] = inc;
         __syncthreads();
-        long long before = inc - mine;
+        int before = inc - mine;
         total = 0;
 #pragma unroll
         for (int w = 0; w < AT / 32; ++w) {
@@ -343,23 +344,23 @@ __global__ void __launch_bounds__(32 * WP * WR, Shape<D, FMT, SPLITQ, WP, WR, RN
             total += ms.scan[w];
         }
         if (blockIdx.x == 0 && !p.is_shared) {
-            long long at = before;
+            int at = before;
             for (int b = b0; b < b1; ++b) {
                 p.base[b] = at;
-                at += (long long)cover_units<TILE>(p, b) * items;
+                at += cover_units<TILE>(p, b) * items;
             }
             if (tid == 0) p.base[p.B] = total;
         }
-        const long long per = units_each(total, gridDim.x, p.min_units);
+        const int per = units_each(total, gridDim.x, p.min_units);
         my_first = per * blockIdx.x;
         if (my_first >= total) {
             asm volatile("griddepcontrol.wait;" ::: "memory");
             return;
         }
         if (my_first >= before && my_first < before + mine) {
-            long long at = before;
+            int at = before;
             for (int b = b0; b < b1; ++b) {
-                const long long n = (long long)cover_units<TILE>(p, b) * items;
+                const int n = cover_units<TILE>(p, b) * items;
                 if (my_first < at + n) {
                     ms.found_b = b;
                     ms.found_base = at;
@@ -373,11 +374,11 @@ __global__ void __launch_bounds__(32 * WP * WR, Shape<D, FMT, SPLITQ, WP, WR, RN
     // a cluster's item, and this CTA's place in it
     const int c_item = CL ? blockIdx.x / cluster : 0, c_rank = CL ? blockIdx.x - c_item * cluster : 0;
     int b = CL ? c_item / items : ms.found_b;
-    long long base_b = CL ? 0 : ms.found_base;
-    const long long my_end = CL ? 1 : min(total, my_first + units_each(total, gridDim.x, p.min_units));
+    int base_b = CL ? 0 : ms.found_base;
+    const int my_end = CL ? 1 : min(total, my_first + units_each(total, gridDim.x, p.min_units));
     const int g8 = lane >> 2, q4 = lane & 3;  // a fragment's row (or column) and pair
 
-    for (long long u = my_first; u < my_end;) {
+    for (int u = my_first; u < my_end;) {
         // ---- the item: sequence b, kv head h, row block rb; its tiles [t0, t0 + take)
         int n_b = cover_units<TILE>(p, b), item, off, take;
         if (CL) {
@@ -385,13 +386,13 @@ __global__ void __launch_bounds__(32 * WP * WR, Shape<D, FMT, SPLITQ, WP, WR, RN
             off = n_b * c_rank / cluster;
             take = n_b * (c_rank + 1) / cluster - off;
         } else {
-            while (b < nb && u >= base_b + (long long)n_b * items) {
-                base_b += (long long)n_b * items;
+            while (b < nb && u >= base_b + n_b * items) {
+                base_b += n_b * items;
                 n_b = ++b < nb ? cover_units<TILE>(p, b) : 0;
             }
             if (n_b == 0) break;  // only if the lengths changed under the launch
-            item = (int)((u - base_b) / n_b), off = (int)((u - base_b) % n_b);
-            take = (int)min((long long)(n_b - off), my_end - u);
+            item = (u - base_b) / n_b, off = u - base_b - item * n_b;
+            take = min(n_b - off, my_end - u);
         }
         const int h = item / p.RB, rb = item - h * p.RB;
         int clo, chi;
@@ -399,7 +400,7 @@ __global__ void __launch_bounds__(32 * WP * WR, Shape<D, FMT, SPLITQ, WP, WR, RN
         const int t0 = clo / TILE + off;
         const int row0 = (p.is_shared ? 0 : b * p.rows_item) + rb * ROWS;
         const int nrows = min(ROWS, p.rows_item - rb * ROWS);
-        const long long u_first = u;
+        const int u_first = u;
         u += CL ? 1 : take;
 
         // ---- fetching: where a tile's rows lie is looked up one tile ahead of the copies, a thread a row
@@ -965,15 +966,15 @@ __global__ void __launch_bounds__(JT) join_kernel(const __grid_constant__ JoinP 
     // pieces of a launch: CTAs c0 .. c1, the row's place in a slot
     struct Part {
         const float* slots;
-        long long c0, c1, per, first, whole_slot;
-        int row, rows, floats, n;
+        long long whole_slot;
+        int c0, c1, per, first, row, rows, floats, n;
     };
-    auto part = [&](const AttendP& a, int grid, int rows_blk, long long base, long long total, int n_b, int vb, int r) {
+    auto part = [&](const AttendP& a, int grid, int rows_blk, int base, int total, int n_b, int vb, int r) {
         Part x;
         const int rb = r / rows_blk, item = h * a.RB + rb;
         x.n = n_b;
         x.per = units_each(total, grid, a.min_units);
-        x.first = base + (long long)item * n_b;
+        x.first = base + item * n_b;
         x.c0 = x.first / x.per;
         x.c1 = n_b ? (x.first + n_b - 1) / x.per : x.c0 - 1;
         x.whole_slot = 2ll * grid + (long long)vb * a.H * a.RB + item;
@@ -984,8 +985,8 @@ __global__ void __launch_bounds__(JT) join_kernel(const __grid_constant__ JoinP 
         return x;
     };
     const int items = p.H * p.RB;
-    const long long base = p.base[b];
-    const Part own = part(p, jp.own_grid, jp.own_rows, base, p.base[p.B], (int)((p.base[b + 1] - base) / items), b,
+    const int base = p.base[b];
+    const Part own = part(p, jp.own_grid, jp.own_rows, base, p.base[p.B], (p.base[b + 1] - base) / items, b,
                           t * p.G + g);
     const bool with_shared = jp.shared_grid > 0;
     if (own.n && own.c0 == own.c1 && !p.keep_items) return;
@@ -995,7 +996,7 @@ __global__ void __launch_bounds__(JT) join_kernel(const __grid_constant__ JoinP 
     for (int i = 0; i < E; ++i) o[i] = 0.f;
     auto add = [&](const Part& x) {
 #pragma unroll 4
-        for (long long c = x.c0 + warp; c <= x.c1; c += 4) {
+        for (int c = x.c0 + warp; c <= x.c1; c += 4) {
             const long long slot = x.c0 == x.c1 ? x.whole_slot : 2 * c + (x.first <= c * x.per ? 0 : 1);
             const float* s = x.slots + slot * x.floats;
             const float2 ml = *reinterpret_cast<const float2*>(s + (long long)x.rows * D + 2 * x.row);
@@ -1018,7 +1019,7 @@ __global__ void __launch_bounds__(JT) join_kernel(const __grid_constant__ JoinP 
     if (own.n) add(own);
     if (with_shared) {
         const AttendP& a = jp.shared;
-        add(part(a, jp.shared_grid, jp.shared_rows, 0, (long long)jp.shared_units * a.H * a.RB, jp.shared_units, 0,
+        add(part(a, jp.shared_grid, jp.shared_rows, 0, jp.shared_units * a.H * a.RB, jp.shared_units, 0,
                  bt * p.G + g));
     }
 #pragma unroll

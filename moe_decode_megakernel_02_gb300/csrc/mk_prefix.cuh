@@ -194,32 +194,27 @@ __device__ __forceinline__ uint32_t panel_at(uint32_t base, int rows, int r, int
     return base + (c >> 3) * rows * 128 + r * 128 + (((c & 7) ^ (r & 7)) << 4);
 }
 
-// Four codes as two bf16 pairs, exact. E4M3: sign, exponent and mantissa moved
-// to their bf16 places, times 2^(127 - 7), which also makes its subnormals
-// right; NaN codes (all seven low bits set) would come out as 480. INT8: code
-// + 128 as the mantissa of 2^23, minus 2^23 + 128.
+// Four codes as two bf16 pairs, exact. E4M3: through fp16 and fp32. INT8: the
+// low seven bits as the mantissa of 128 (whose bf16 step is 1), less 128, or
+// less 256 where the sign bit is set.
 template <int FMT>
 __device__ __forceinline__ void codes_bf16(uint32_t w, uint32_t& lo, uint32_t& hi) {
     if constexpr (FMT == MK_KV_E4M3) {
-        const uint32_t a = __byte_perm(w, 0, 0x1404), b = __byte_perm(w, 0, 0x3424);  // codes in the high bytes
-        const uint32_t x = (a & 0x80008000u) | (a >> 4 & 0x07f007f0u), y = (b & 0x80008000u) | (b >> 4 & 0x07f007f0u);
-        const uint32_t s = 0x7b807b80u;  // 2^120
-        const __nv_bfloat162 f = *reinterpret_cast<const __nv_bfloat162*>(&s);
-        const __nv_bfloat162 p = __hmul2(*reinterpret_cast<const __nv_bfloat162*>(&x), f);
-        const __nv_bfloat162 q = __hmul2(*reinterpret_cast<const __nv_bfloat162*>(&y), f);
-        lo = *reinterpret_cast<const uint32_t*>(&p);
-        hi = *reinterpret_cast<const uint32_t*>(&q);
-        if ((((w & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u) != 0) {
-            if ((w & 0x7fu) == 0x7fu) lo = (lo & 0xffff0000u) | 0x7fffu;
-            if ((w & 0x7f00u) == 0x7f00u) lo = (lo & 0xffffu) | 0x7fff0000u;
-            if ((w & 0x7f0000u) == 0x7f0000u) hi = (hi & 0xffff0000u) | 0x7fffu;
-            if ((w & 0x7f000000u) == 0x7f000000u) hi = (hi & 0xffffu) | 0x7fff0000u;
-        }
+        uint32_t a, b;
+        e4m3_quad(w, a, b);
+        const float2 x = __half22float2(*reinterpret_cast<const __half2*>(&a));
+        const float2 y = __half22float2(*reinterpret_cast<const __half2*>(&b));
+        lo = pack_bf16(x.x, x.y);
+        hi = pack_bf16(y.x, y.y);
     } else {
-        w ^= 0x80808080u;
-        auto whole = [&](unsigned sel) { return __uint_as_float(__byte_perm(w, 0x4b000000u, sel)) - 8388736.0f; };
-        lo = pack_bf16(whole(0x7440), whole(0x7441));
-        hi = pack_bf16(whole(0x7442), whole(0x7443));
+        auto pair = [](uint32_t v) {
+            const uint32_t x = v & 0xff7fff7fu, c = v & 0xff80ff80u;
+            const __nv_bfloat162 r =
+                __hsub2(*reinterpret_cast<const __nv_bfloat162*>(&x), *reinterpret_cast<const __nv_bfloat162*>(&c));
+            return *reinterpret_cast<const uint32_t*>(&r);
+        };
+        lo = pair(__byte_perm(w, 0x43434343u, 0x4140));
+        hi = pair(__byte_perm(w, 0x43434343u, 0x4342));
     }
 }
 
@@ -305,27 +300,29 @@ __global__ void __launch_bounds__(PrefixShape<D, FMT>::NT, 1) prefix_kernel(cons
             const bool real = row < p.rows_item;
             const int bt = real ? row / p.G : 0, g = real ? row - bt * p.G : 0;
             const int b = bt / p.T, t = bt - b * p.T;
-            const bool live = real && shares(p, b);
-            // half of the row's query; every product that read the last one has ended (all scores came)
+            // half of the row's query, fetched while the length is; every product that read the last one has
+            // ended (all scores came)
+            bool live;
             {
-                const uint16_t* src = p.q + b * p.qb + t * p.qt + (long long)(h * p.G + g) * p.qh;
-                const bool wide = ((uintptr_t)src & 15) == 0;
+                const uint16_t* src = p.q + b * p.qb + t * p.qt + (long long)(h * p.G + g) * p.qh + wg * (D / 2);
+                uint4 x[D / 16];
+                if (((uintptr_t)src & 15) == 0) {
 #pragma unroll
-                for (int j = 0; j < D / 16; ++j) {
-                    const int i = wg * (D / 16) + j;
-                    uint4 x = make_uint4(0, 0, 0, 0);
-                    if (live) {
-                        if (wide) {
-                            x = *reinterpret_cast<const uint4*>(src + 8 * i);
-                        } else {
-                            uint32_t w[4];
+                    for (int j = 0; j < D / 16; ++j) x[j] = reinterpret_cast<const uint4*>(src)[j];
+                } else {
 #pragma unroll
-                            for (int e = 0; e < 4; ++e) w[e] = src[8 * i + 2 * e] | (uint32_t)src[8 * i + 2 * e + 1] << 16;
-                            x = make_uint4(w[0], w[1], w[2], w[3]);
-                        }
+                    for (int j = 0; j < D / 16; ++j) {
+                        uint32_t w[4];
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) w[e] = src[8 * j + 2 * e] | (uint32_t)src[8 * j + 2 * e + 1] << 16;
+                        x[j] = make_uint4(w[0], w[1], w[2], w[3]);
                     }
-                    *reinterpret_cast<uint4*>(smem + (panel_at(qs, ROWS, lrow, i) - qs)) = x;
                 }
+                live = real && shares(p, b);
+#pragma unroll
+                for (int j = 0; j < D / 16; ++j)
+                    *reinterpret_cast<uint4*>(smem + (panel_at(qs, ROWS, lrow, wg * (D / 16) + j) - qs)) =
+                        live ? x[j] : make_uint4(0, 0, 0, 0);
                 asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                 bar_arrive(&ms.q_ready);
             }
