@@ -611,6 +611,11 @@ __global__ void __launch_bounds__(ST, 2) sample_kernel(const SampleP p) {
             deliver(1, sh.own_base);
             cl.sync();
             listed = *cl.map_shared_rank(&sh.list_n, 0) <= LIST;
+            if (listed && rank != 0) {
+                // CTA 0 has every candidate and goes on alone; it ends after all others have read its count
+                asm volatile("barrier.cluster.arrive;" ::: "memory");
+                return;
+            }
         } else if (by_threads) {
             // how many tokens are there at all
             unsigned c = 0;
@@ -618,8 +623,7 @@ __global__ void __launch_bounds__(ST, 2) sample_kernel(const SampleP p) {
             binds = cluster_sum(c) >= (u64)k_in;
         }
         if (listed) {
-            // ---- CTA 0 has every candidate
-            if (rank == 0) {
+            {
                 int n_l = (int)sh.list_n;
                 order_list(sh.list, n_l);
                 n_l = min(n_l, k_in);
@@ -658,7 +662,7 @@ __global__ void __launch_bounds__(ST, 2) sample_kernel(const SampleP p) {
                 }
                 if (tid == 0 && p.kept) p.kept[row] = (int)n_k;
             }
-            cl.sync();  // no CTA leaves while another reads its shared memory
+            asm volatile("barrier.cluster.arrive;\n\tbarrier.cluster.wait;" ::: "memory");
             return;
         }
         // the list's place is the histogram's
@@ -671,6 +675,7 @@ __global__ void __launch_bounds__(ST, 2) sample_kernel(const SampleP p) {
     const float least_x = least > 0.f ? m + T * (logf(least) - 0.01f) : -INFINITY;  // below: lighter than min_p
     // kept tokens end at `last`; a row that keeps all unmasked tokens needs no comparison, as masked ones weigh 0
     bool all_ranks = last == ((u64)masked << 32) - 1 && W.plain;
+    const bool plain_ranks = all_ranks;
     float xc = value_of(top - (unsigned)(last >> 32));
     unsigned ic = (unsigned)last;
     auto up_to_last = [&](float x, int i) { return x > xc || (x == xc && (unsigned)i <= ic); };
@@ -744,6 +749,13 @@ __global__ void __launch_bounds__(ST, 2) sample_kernel(const SampleP p) {
             ++added;
             count += x > -INFINITY;
         });
+    } else if (border >= 0 && plain_ranks && !(least > 0.f)) {
+        dense([&](float x, int) { return bin.above(x, border); },
+              [&](float x) {
+                  s.add(W(x));
+                  ++added;
+              });
+        count = added;
     } else {
         dense([&](float x, int i) { return (border < 0 || bin.above(x, border)) && x >= least_x && up_to_last(x, i); },
               [&](float x) {
@@ -761,9 +773,14 @@ __global__ void __launch_bounds__(ST, 2) sample_kernel(const SampleP p) {
             unsigned in = 0;
             if (v + lane < v1) {
                 unpack(x, xs[v + lane]);
+                if (plain_ranks) {
 #pragma unroll
-                for (int e = 0; e < E; ++e)
-                    in |= (unsigned)(bin.in(x[e], border) && x[e] >= low_x && up_to_last(x[e], i0 + (v + lane) * E + e)) << e;
+                    for (int e = 0; e < E; ++e) in |= (unsigned)(x[e] >= low_x && bin.in(x[e], border)) << e;
+                } else {
+#pragma unroll
+                    for (int e = 0; e < E; ++e)
+                        in |= (unsigned)(x[e] >= low_x && bin.in(x[e], border) && up_to_last(x[e], i0 + (v + lane) * E + e)) << e;
+                }
             }
             put(v, x, in);
         }
