@@ -39,7 +39,7 @@ def build_cmds() -> list:
     os.makedirs(_BUILD, exist_ok=True)
     srcs = [os.path.join(_HERE, "csrc", f) for f in (
         "mk_host.cu", "mk_synth.cu", "mk_pages.cu", "mk_sample.cu", "mk_attend.cu", "mk_attend_d64.cu",
-        "mk_attend_d128.cu", "mk_attend_d256.cu", "mk_prefix.cu")]
+        "mk_attend_d128.cu", "mk_attend_d256.cu", "mk_prefix.cu", "mk_prefix_f16.cu")]
     srcs += [os.path.join(_ROOT, "synth", "synth_cuda.cu"), os.path.join(_ROOT, "synth", "synth_host.c")]
     base = ["nvcc", "--threads", "0", "-gencode", "arch=compute_103a,code=sm_103a", "-O3", "-lineinfo", "-std=c++17",
             "-Xcompiler", "-fPIC", "-shared", "-lpthread"]

@@ -10,6 +10,15 @@ using namespace mkop;
 
 constexpr int MAX_DEV = 32;
 constexpr int CLUSTER_TILES = 12;
+// Wide calls: from so many rows x tiles an SM on, the tiles that a sequence's
+// tokens all see whole go to the tensor memory's kernel, the rest and the join
+// being worth some 10 us. Measured without and with it, 16 query heads on 4 kv
+// heads of 128, bf16: 8 sequences of 8192 positions, 28 rows 37 and 43 us, 128
+// rows 88 and 75; 16 sequences of 16384, 28 rows 118 and 107, 56 rows 190 and
+// 121; 256 tokens at 16384 217 and 90. 8-bit pages: 128 rows 96 and 87, 256
+// tokens 242 and 134, but 28 rows at 65536 191 and 265: their conversion costs
+// the same for fewer rows.
+constexpr int64_t WIDE_WORK = 2000;
 
 // KindInfo of each kernel on each device, asked for once
 int kind_info(int dev, int d, const Kind& k, KindInfo& out) {
@@ -29,28 +38,27 @@ int kind_info(int dev, int d, const Kind& k, KindInfo& out) {
     return MK_OK;
 }
 
-// the shared launch's own kernel, where there is one: up to 32 rows are bound
-// by the cache's bytes and leave most of its 128 rows empty
-int prefix_info(int dev, int d, int format, KindInfo& out) {
-    static bool have[MAX_DEV][2][3];
+// one-time attributes of the kernels of mk_prefix.cuh
+int prefix_info(int dev, int d, int format, bool f16, KindInfo& out) {
+    static bool have[MAX_DEV][2][3][2];
     static std::mutex lock;
     out = KindInfo{64, 128, 1};
     std::lock_guard<std::mutex> g(lock);
-    if (dev < MAX_DEV && have[dev][d == 128][format]) return MK_OK;
-    const int rc = prefix_run(d, format, nullptr, 0, nullptr);
-    if (dev < MAX_DEV && !rc) have[dev][d == 128][format] = true;
+    if (dev < MAX_DEV && have[dev][d == 128][format][f16]) return MK_OK;
+    const int rc = (f16 ? prefix_f16 : prefix_bf16)(d, format, nullptr, 0, nullptr);
+    if (dev < MAX_DEV && !rc) have[dev][d == 128][format][f16] = true;
     return rc;
 }
 
 struct Plan {
     Kind own_k, sh_k;
     int cluster;  // > 0: small call, an item a cluster
-    bool prefix;
+    bool prefix, wide;
     KindInfo own_i, sh_i;
     int own_grid, sh_grid;  // sh_grid 0: nothing shared
     int own_rb, sh_rb;
     int own_slot_rows, sh_slot_rows, own_floats, sh_floats;
-    int64_t base_off, own_off, sh_off, bytes;
+    int64_t base_off, sh_base_off, own_off, sh_off, bytes;
 };
 
 int64_t up256(int64_t n) { return (n + 255) / 256 * 256; }
@@ -100,6 +108,7 @@ int make_plan(const mk_attention* a, Plan& pl) {
     if (items > INT32_MAX / 16) return fail(MK_ERR_UNSUPPORTED, "attend: too many queries in one call");
     // Small calls: up to CLUSTER_TILES tiles a CTA, all items' clusters resident at once (or nearly)
     pl.cluster = 0;
+    pl.wide = false;
     if (!a->shared_len && pl.own_k.rows <= 32) {
         const int64_t tiles = (cap + pl.own_i.tile - 1) / pl.own_i.tile;
         int c = 1;
@@ -117,26 +126,32 @@ int make_plan(const mk_attention* a, Plan& pl) {
     int64_t grid = (int64_t)sms * pl.own_i.ctas;
     if (grid > (most + min_units - 1) / min_units) grid = (most + min_units - 1) / min_units;
     pl.own_grid = (int)grid;
+    // what the kernels of mk_prefix.cuh read (their tensor maps want distinct rows, 8 or more of them a page)
+    const bool fits = D <= 128 && g.page_size >= 8 && g.row_stride > 0 && g.head_stride > 0 && g.page_stride > 0;
+    if (!a->shared_len && fits && rows > (g.format == MK_KV_BF16 ? 16 : 32)) {
+        const int64_t tiles = (int64_t)B * H * ((rows + 127) / 128) * (cap / 64);
+        pl.wide = tiles * (rows < 128 ? rows : 128) >= WIDE_WORK * sms;
+    }
     pl.base_off = 0;
-    pl.own_off = up256((int64_t)(B + 1) * 4);
-    const int64_t own_slots = 2 * grid + (a->shared_len ? items : 0);
+    pl.sh_base_off = up256((int64_t)(B + 1) * 4);
+    pl.own_off = 2 * pl.sh_base_off;
+    const int64_t own_slots = 2 * grid + (a->shared_len || pl.wide ? items : 0);
     pl.bytes = up256(pl.own_off + own_slots * pl.own_floats * 4);
     pl.sh_grid = 0;
     pl.sh_off = pl.bytes;
-    if (a->shared_len) {
-        const int64_t all = (int64_t)B * rows;
+    if (a->shared_len || pl.wide) {
+        const int64_t all = pl.wide ? rows : (int64_t)B * rows;
         pl.sh_k = Kind{g.format, splitq, block_of(all)};
-        // (its tensor maps want distinct rows, 8 or more of them a page)
-        pl.prefix = D <= 128 && a->q->dtype == MK_DT_BF16 && all > 32 && g.page_size >= 8 && g.row_stride > 0 &&
-                    g.head_stride > 0 && g.page_stride > 0;
-        if (const int rc = pl.prefix ? prefix_info(dev, D, g.format, pl.sh_i) : kind_info(dev, D, pl.sh_k, pl.sh_i))
+        // (up to 32 shared rows are bound by the cache's bytes and would leave most of its 128 rows empty)
+        pl.prefix = pl.wide || (fits && all > 32);
+        if (const int rc = pl.prefix ? prefix_info(dev, D, g.format, a->q->dtype == MK_DT_F16, pl.sh_i) : kind_info(dev, D, pl.sh_k, pl.sh_i))
             return rc;
         if (pl.sh_i.ctas < 1) return fail(MK_ERR_UNSUPPORTED, "attend: the kernel does not fit this device");
         pl.sh_rb = (int)((all + pl.sh_i.rows - 1) / pl.sh_i.rows);
         pl.sh_slot_rows = (int)(all < pl.sh_i.rows ? all : pl.sh_i.rows);
         pl.sh_floats = slot_floats(pl.sh_slot_rows, D);
-        const int64_t sh_items = (int64_t)H * pl.sh_rb;
-        const int64_t units = sh_items * ((a->shared_len + pl.sh_i.tile - 1) / pl.sh_i.tile);
+        const int64_t sh_items = (int64_t)H * pl.sh_rb * (pl.wide ? B : 1);
+        const int64_t units = sh_items * (((pl.wide ? cap : a->shared_len) + pl.sh_i.tile - 1) / pl.sh_i.tile);
         if (units > (1 << 30)) return fail(MK_ERR_UNSUPPORTED, "attend: too many positions in one call");
         int64_t sg = (int64_t)sms * pl.sh_i.ctas;
         if (sg > (units + min_units - 1) / min_units) sg = (units + min_units - 1) / min_units;
@@ -178,7 +193,7 @@ extern "C" int mk_pages_attend(const mk_attention* a, void* workspace, int64_t w
     p.f16 = a->q->dtype == MK_DT_F16;
     p.scale = a->scale, p.cap = a->softcap, p.shared = a->shared_len;
     p.min_units = 2;
-    p.RB = pl.own_rb, p.rows_item = p.T * p.G, p.keep_items = a->shared_len > 0;
+    p.RB = pl.own_rb, p.rows_item = p.T * p.G, p.keep_items = a->shared_len > 0 || pl.wide, p.wide = pl.wide;
     p.slot_rows = pl.own_slot_rows, p.slot_floats = pl.own_floats;
     p.slots = (float*)(ws + pl.own_off), p.base = (int*)(ws + pl.base_off);
     JoinP j = {};
@@ -187,12 +202,13 @@ extern "C" int mk_pages_attend(const mk_attention* a, void* workspace, int64_t w
     cudaStream_t s = (cudaStream_t)stream;
     if (pl.sh_grid) {
         AttendP q = p;
-        q.is_shared = 1;
-        q.RB = pl.sh_rb, q.rows_item = p.B * p.T * p.G;
+        q.is_shared = !pl.wide;
+        q.RB = pl.sh_rb, q.rows_item = pl.wide ? p.T * p.G : p.B * p.T * p.G;
+        q.base = (int*)(ws + pl.sh_base_off);
         q.slot_rows = pl.sh_slot_rows, q.slot_floats = pl.sh_floats, q.slots = (float*)(ws + pl.sh_off);
         j.shared = q, j.shared_grid = pl.sh_grid, j.shared_rows = pl.sh_i.rows;
         j.shared_units = (a->shared_len + pl.sh_i.tile - 1) / pl.sh_i.tile;
-        if (const int rc = pl.prefix ? prefix_run(D, g.format, &q, pl.sh_grid, s)
+        if (const int rc = pl.prefix ? (p.f16 ? prefix_f16 : prefix_bf16)(D, g.format, &q, pl.sh_grid, s)
                                      : fn(pl.sh_k, &q, nullptr, pl.sh_grid, false, s))
             return rc;
     }

@@ -67,6 +67,7 @@ struct AttendP {
     int shared;      // positions in shared pages: the shared launch covers [0, shared), the other one the rest
     int cluster;     // > 0: one item a cluster of so many CTAs, no pieces in the workspace
     int is_shared;   // this is the shared launch (one virtual sequence, rows of the whole batch)
+    int wide;        // the tiles that all of a sequence's rows see whole have a launch of their own (mk_prefix.cuh)
     int RB;          // row blocks of an item
     int rows_item;   // rows of one (sequence, kv head): T * G, or B * T * G
     int keep_items;  // finished items go to the workspace too (a shared part joins them)
@@ -101,6 +102,13 @@ __host__ __device__ __forceinline__ int units_each(int total, int grid, int min_
 __device__ __forceinline__ bool shares(const AttendP& p, int b) {
     return p.shared > 0 && (long long)p.lens[b] - p.T + 1 >= p.shared && (!p.starts || p.starts[b] <= 0);
 }
+// Wide calls: the tiles [g0, g1) of 64 positions of sequence b that all of its tokens see whole
+__device__ __forceinline__ void whole_tiles(const AttendP& p, int b, int& g0, int& g1) {
+    const unsigned lo = p.starts ? max(p.starts[b], 0) : 0;
+    const long long hi = min((long long)p.lens[b] - p.T + 1, (long long)p.pps << p.ps_shift);
+    g0 = (int)((lo + 63u) / 64u);
+    g1 = max(g0, hi < 0 ? 0 : (int)(hi / 64));
+}
 // the positions of sequence b that a launch covers, [lo, hi)
 __device__ __forceinline__ void cover(const AttendP& p, int b, int& lo, int& hi) {
     if (p.is_shared) {
@@ -115,7 +123,14 @@ template <int TILE>
 __device__ __forceinline__ int cover_units(const AttendP& p, int b) {
     int lo, hi;
     cover(p, b, lo, hi);
-    return hi > lo ? (hi + TILE - 1) / TILE - lo / TILE : 0;
+    if (hi <= lo) return 0;
+    int n = (hi + TILE - 1) / TILE - lo / TILE;
+    if (p.wide) {
+        int g0, g1;
+        whole_tiles(p, b, g0, g1);
+        n -= g1 - g0;
+    }
+    return n;
 }
 
 __device__ __forceinline__ uint32_t sm32(const void* p) { return (uint32_t)__cvta_generic_to_shared(p); }
@@ -320,6 +335,7 @@ __global__ void __launch_bounds__(32 * WP * WR, Shape<D, FMT, SPLITQ, WP, WR, RN
             for (int b = tid; b < p.B; b += AT)
                 if (p.lens[b] > (p.pps << p.ps_shift)) *p.status = MK_ERR_INVALID_ARG;
     } else {
+        asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
         // each thread counts a stretch of sequences; sums before it by shuffles
         const int each = (nb + AT - 1) / AT, b0 = min(nb, tid * each), b1 = min(nb, b0 + each);
         int mine = 0;
@@ -359,6 +375,8 @@ __global__ void __launch_bounds__(32 * WP * WR, Shape<D, FMT, SPLITQ, WP, WR, RN
         }
         if (my_first >= before && my_first < before + mine) {
             int at = before;
+            ms.found_b = b0;
+            ms.found_base = before;
             for (int b = b0; b < b1; ++b) {
                 const int n = cover_units<TILE>(p, b) * items;
                 if (my_first < at + n) {
@@ -397,7 +415,14 @@ __global__ void __launch_bounds__(32 * WP * WR, Shape<D, FMT, SPLITQ, WP, WR, RN
         const int h = item / p.RB, rb = item - h * p.RB;
         int clo, chi;
         cover(p, b, clo, chi);
-        const int t0 = clo / TILE + off;
+        int gap0 = INT_MAX, gap = 0;  // wide calls: tiles from gap0 on lie `gap` further
+        if (!CL && p.wide) {
+            whole_tiles(p, b, gap0, gap);
+            gap -= gap0;
+            gap0 -= clo / TILE + off;
+        }
+        const int t_first = clo / TILE + off;
+        auto t_at = [&](int tile) { return t_first + tile + (!CL && tile >= gap0 ? gap : 0); };
         const int row0 = (p.is_shared ? 0 : b * p.rows_item) + rb * ROWS;
         const int nrows = min(ROWS, p.rows_item - rb * ROWS);
         const int u_first = u;
@@ -409,7 +434,7 @@ __global__ void __launch_bounds__(32 * WP * WR, Shape<D, FMT, SPLITQ, WP, WR, RN
         const int* const trow = p.table + (p.is_shared ? 0 : b) * p.table_s;
         const int mask = (1 << p.ps_shift) - 1;
         auto page_of = [&](int tile) {  // of position tid of the tile; -1: not this item's, or no such page
-            const int pos = (t0 + tile) * TILE + tid;
+            const int pos = t_at(tile) * TILE + tid;
             if (tid >= TILE || tile >= take || pos < clo || pos >= chi) return -1;
             const int pg = trow[pos >> p.ps_shift];
             if ((unsigned)pg < (unsigned)p.n_pages) return pg;
@@ -419,7 +444,7 @@ __global__ void __launch_bounds__(32 * WP * WR, Shape<D, FMT, SPLITQ, WP, WR, RN
         long long sc_at = -1;  // 8-bit pages: where this thread's row of the tile fetched next has its scales
         auto place = [&](int tile, int page) {
             if (tid < TILE) {
-                const int r = ((t0 + tile) * TILE + tid) & mask;
+                const int r = (t_at(tile) * TILE + tid) & mask;
                 ms.off[tile & 1][tid] = page < 0 ? -1 : page * p.page_b + r * p.row_b;
                 if constexpr (F8) sc_at = page < 0 ? -1 : page * p.sc_page + h * p.sc_head + r;
             }
@@ -590,12 +615,13 @@ __global__ void __launch_bounds__(32 * WP * WR, Shape<D, FMT, SPLITQ, WP, WR, RN
             fetch(tile + S::STAGES - 1);
             const int next_page = page_of(tile + S::STAGES);
 
+            const int tile_at = t_at(tile) * TILE;
             const uint32_t st = ring + (tile % S::STAGES) * S::STAGE_B, vt = st + S::TILE_B;
             const float* const scales =
                 reinterpret_cast<const float*>(smem + (tile % S::STAGES) * S::STAGE_B + 2 * S::TILE_B);
 #pragma unroll 1
             for (int s0 = warp / WR * (TILE / WP), s1 = s0 + TILE / WP; s0 < s1; s0 += SL) {
-                const int j0 = (t0 + tile) * TILE + s0;
+                const int j0 = tile_at + s0;
                 if (j0 + SL <= lo_min || j0 >= hi_max) continue;  // no row sees any of it
                 const bool all_see = j0 >= lo_max && j0 + SL <= hi_min;
 
@@ -1019,8 +1045,11 @@ __global__ void __launch_bounds__(JT) join_kernel(const __grid_constant__ JoinP 
     if (own.n) add(own);
     if (with_shared) {
         const AttendP& a = jp.shared;
-        add(part(a, jp.shared_grid, jp.shared_rows, 0, jp.shared_units * a.H * a.RB, jp.shared_units, 0,
-                 bt * p.G + g));
+        if (!a.wide)
+            add(part(a, jp.shared_grid, jp.shared_rows, 0, jp.shared_units * a.H * a.RB, jp.shared_units, 0,
+                     bt * p.G + g));
+        else if (const int n = (a.base[b + 1] - a.base[b]) / (a.H * a.RB))
+            add(part(a, jp.shared_grid, jp.shared_rows, a.base[b], a.base[a.B], n, b, t * p.G + g));
     }
 #pragma unroll
     for (int i = 0; i < E; ++i) om[warp][lane * E + i] = o[i];
@@ -1135,9 +1164,10 @@ typedef int (*AttendFn)(const Kind&, const AttendP*, KindInfo*, int, bool, cudaS
 int attend_64(const Kind&, const AttendP*, KindInfo*, int, bool, cudaStream_t);
 int attend_128(const Kind&, const AttendP*, KindInfo*, int, bool, cudaStream_t);
 int attend_256(const Kind&, const AttendP*, KindInfo*, int, bool, cudaStream_t);
-// the shared launch on the tensor memory (mk_prefix.cuh; head_dim 64 and 128,
-// bf16 queries): 128 rows an item, one CTA an SM. p NULL: one-time attributes.
-int prefix_run(int head_dim, int format, const AttendP* p, int grid, cudaStream_t s);
+// the launch on the tensor memory (mk_prefix.cuh; head_dim 64 and 128): 128
+// rows an item, one CTA an SM. p NULL: one-time attributes.
+int prefix_bf16(int head_dim, int format, const AttendP* p, int grid, cudaStream_t s);
+int prefix_f16(int head_dim, int format, const AttendP* p, int grid, cudaStream_t s);
 int join_64(const JoinP&, unsigned, cudaStream_t);
 int join_128(const JoinP&, unsigned, cudaStream_t);
 int join_256(const JoinP&, unsigned, cudaStream_t);

@@ -36,16 +36,17 @@
 
 namespace mkop {
 
-template <int D, int FMT>
+// SPLITQ: fp16 queries, as two bf16 parts (their 11 bits and range fit them)
+template <int D, int FMT, bool SPLITQ>
 struct PrefixShape {
     static constexpr bool F8 = FMT != MK_KV_BF16;
     static constexpr int ROWS = 128, TILE = 64;
     static constexpr int PANELS = D / 64;          // 128-byte wide panels of a row
-    static constexpr int Q_B = PANELS * ROWS * 128;
+    static constexpr int Q_PART = PANELS * ROWS * 128, Q_B = Q_PART * (SPLITQ ? 2 : 1);
     static constexpr int KV_B = PANELS * TILE * 128;  // K (or V) of a tile
     static constexpr int STAGE_B = 2 * KV_B;
     static constexpr int SCALE_B = 2 * TILE * 4;   // of a stage: K scales, V scales (8-bit pages)
-    static constexpr int STAGES = D == 128 ? (F8 ? 3 : 5) : (F8 ? 6 : 8);
+    static constexpr int STAGES = D == 128 ? (F8 ? 3 : SPLITQ ? 4 : 5) : (F8 ? 6 : 8);
     static constexpr int RAW_B = 2 * TILE * D + SCALE_B, RAWS = 3;  // staged codes and scales of a tile
     static constexpr int SC_OFF = Q_B + STAGES * STAGE_B;
     static constexpr int RAW_OFF = SC_OFF + STAGES * SCALE_B;
@@ -61,6 +62,7 @@ struct PrefixShape {
 struct PrefixMisc {
     unsigned long long kv_full[8], pv_done[8], s_full[2], s_free[2], p_ready[2], q_ready, drained;
     unsigned tmem, abort;
+    int scan[16], found_b, found_base;
     long long off[2][64];  // where a tile's rows lie (bytes), -1: zeros
     float2 stat[2][128];   // (maximum, sum) of each group's rows
 };
@@ -122,6 +124,49 @@ struct Place {
     __device__ __forceinline__ unsigned free() const { return (turn - 1) & 1u; }    // of the tile before it in the stage
     __device__ __forceinline__ unsigned pair() const { return c >> 1 & 1u; }        // of the buffer's phase of this tile
     __device__ __forceinline__ unsigned pair_free() const { return ((c >> 1) - 1) & 1u; }
+};
+
+// A role's place in the line of items and their tiles. Shared launch: one
+// sequence, whose items all have n tiles. Wide calls: the tiles that a
+// sequence's rows see whole, sequence after sequence.
+struct Walk {
+    int b, item, tile, n, t0;  // sequence, item of it, tile of the item, tiles of the item, the first one's number
+    __device__ __forceinline__ void count(const AttendP& p) {
+        if (p.wide) {
+            int g1;
+            whole_tiles(p, b, t0, g1);
+            n = g1 - t0;
+        } else {
+            t0 = 0;
+            n = (p.shared + 63) / 64;
+        }
+    }
+    // to tile u of the line; tiles of sequence b begin at `base`
+    __device__ __forceinline__ void start(const AttendP& p, int u, int seq, int base) {
+        b = seq;
+        count(p);
+        n = max(n, 1);
+        item = min((u - base) / n, p.H * p.RB - 1);
+        tile = u - base - item * n;
+    }
+    // k tiles on; behind the last item is one without an end
+    __device__ __forceinline__ void on(const AttendP& p, int k) {
+        tile += k;
+        while (tile >= n) {
+            tile -= n;
+            if (++item < p.H * p.RB) continue;
+            item = 0;
+            do {
+                if (p.wide && b + 1 < p.B) {
+                    ++b;
+                    count(p);
+                } else {
+                    n = INT_MAX;
+                }
+            } while (n == 0);
+        }
+    }
+    __device__ __forceinline__ int at() const { return (t0 + tile) * 64; }
 };
 
 // Shared-memory matrix descriptors: start address, leading and stride offsets
@@ -236,9 +281,10 @@ __device__ __forceinline__ void bar_expect(unsigned long long* b, unsigned bytes
                  : "memory");
 }
 
-template <int D, int FMT>
-__global__ void __launch_bounds__(PrefixShape<D, FMT>::NT, 1) prefix_kernel(const __grid_constant__ AttendP p, const __grid_constant__ PrefixMaps maps) {
-    using S = PrefixShape<D, FMT>;
+template <int D, int FMT, bool SPLITQ>
+__global__ void __launch_bounds__(PrefixShape<D, FMT, SPLITQ>::NT, 1)
+    prefix_kernel(const __grid_constant__ AttendP p, const __grid_constant__ PrefixMaps maps) {
+    using S = PrefixShape<D, FMT, SPLITQ>;
     constexpr bool F8 = S::F8;
     constexpr int TILE = S::TILE, ROWS = S::ROWS;
     extern __shared__ uint8_t raw_smem[];
@@ -250,11 +296,67 @@ __global__ void __launch_bounds__(PrefixShape<D, FMT>::NT, 1) prefix_kernel(cons
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     volatile unsigned* const abort = &ms.abort;
 
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     // (the host sees to it that the tiles of all items fit 32 bits)
-    const int n_t = (p.shared + TILE - 1) / TILE, total = p.H * p.RB * n_t;
+    const int items = p.H * p.RB, limit = p.wide ? p.pps << p.ps_shift : p.shared;  // items of a sequence; positions
+    int total, mine = 0, before = 0;
+    const int each = (p.B + S::NT - 1) / S::NT, b0 = min(p.B, tid * each), b1 = min(p.B, b0 + each);
+    auto tiles_of = [&](int b) {
+        int g0, g1;
+        whole_tiles(p, b, g0, g1);
+        return (g1 - g0) * items;
+    };
+    if (p.wide) {
+        // each thread counts a stretch of sequences; sums before it by shuffles
+        for (int b = b0; b < b1; ++b) mine += tiles_of(b);
+        int inc = mine;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int a = __shfl_up_sync(0xffffffffu, inc, o);
+            if (lane >= o) inc += a;
+        }
+        if (lane == 31) ms.scan[warp] = inc;
+        __syncthreads();
+        before = inc - mine;
+        total = 0;
+#pragma unroll
+        for (int w = 0; w < S::NT / 32; ++w) {
+            if (w < warp) before += ms.scan[w];
+            total += ms.scan[w];
+        }
+        if (blockIdx.x == 0) {  // for the joining launch
+            int at = before;
+            for (int b = b0; b < b1; ++b) {
+                p.base[b] = at;
+                at += tiles_of(b);
+            }
+            if (tid == 0) p.base[p.B] = total;
+        }
+    } else {
+        total = items * ((p.shared + TILE - 1) / TILE);
+    }
     const int per = (int)units_each(total, gridDim.x, p.min_units);
     const int first = per * blockIdx.x, end = min(total, first + per);
     if (first >= end) return;
+    if (p.wide) {
+        if (first >= before && first < before + mine) {
+            ms.found_b = b0;
+            ms.found_base = before;
+            for (int b = b0, at = before; b < b1; ++b) {
+                const int n = tiles_of(b);
+                if (first < at + n) {
+                    ms.found_b = b;
+                    ms.found_base = at;
+                    break;
+                }
+                at += n;
+            }
+        }
+    } else if (tid == 0) {
+        ms.found_b = ms.found_base = 0;
+    }
+    // warps of a group that have rows at all
+    const int act = p.RB > 1 ? 4 : (p.rows_item + 31) / 32;
 
     if (tid == 0) {
         for (int i = 0; i < S::STAGES; ++i) {
@@ -263,10 +365,10 @@ __global__ void __launch_bounds__(PrefixShape<D, FMT>::NT, 1) prefix_kernel(cons
         }
         for (int i = 0; i < 2; ++i) {
             bar_init(&ms.s_full[i], 1);
-            bar_init(&ms.s_free[i], 128);
-            bar_init(&ms.p_ready[i], 128);
+            bar_init(&ms.s_free[i], 32 * act);
+            bar_init(&ms.p_ready[i], 32 * act);
         }
-        bar_init(&ms.q_ready, 256);
+        bar_init(&ms.q_ready, 64 * act);
         bar_init(&ms.drained, 2);
         ms.abort = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -282,9 +384,13 @@ __global__ void __launch_bounds__(PrefixShape<D, FMT>::NT, 1) prefix_kernel(cons
     __syncthreads();
     tm_after();
     const uint32_t tm = ms.tmem;
+    Walk w;
+    w.start(p, first, ms.found_b, ms.found_base);
 
     // Tiles are counted over all pieces: tile c uses stage c % STAGES, S and P buffer c & 1.
-    if (warp < 8) {
+    if (warp < 8 && (warp & 3) >= act) {
+        // rows that no item has: nothing of them is read
+    } else if (warp < 8) {
         // ================ softmax, a row a thread ================
         const int wg = warp >> 2, lrow = tid & 127;
         const uint32_t my = tm + ((uint32_t)((warp & 3) * 32) << 16);
@@ -294,12 +400,12 @@ __global__ void __launch_bounds__(PrefixShape<D, FMT>::NT, 1) prefix_kernel(cons
         if (wg) at_c.next();
         bool ok = true;
         for (int u = first; u < end;) {
-            const int item = u / n_t, off = u - item * n_t, take = min(n_t - off, end - u);
-            const int h = item / p.RB, rb = item - h * p.RB;
+            const int take = min(w.n - w.tile, end - u);
+            const int h = w.item / p.RB, rb = w.item - h * p.RB;
             const int row = rb * ROWS + lrow;
             const bool real = row < p.rows_item;
             const int bt = real ? row / p.G : 0, g = real ? row - bt * p.G : 0;
-            const int b = bt / p.T, t = bt - b * p.T;
+            const int b = p.wide ? w.b : bt / p.T, t = p.wide ? bt : bt - b * p.T;
             // half of the row's query, fetched while the length is; every product that read the last one has
             // ended (all scores came)
             bool live;
@@ -318,11 +424,23 @@ __global__ void __launch_bounds__(PrefixShape<D, FMT>::NT, 1) prefix_kernel(cons
                         x[j] = make_uint4(w[0], w[1], w[2], w[3]);
                     }
                 }
-                live = real && shares(p, b);
+                live = real && (p.wide || shares(p, b));
 #pragma unroll
-                for (int j = 0; j < D / 16; ++j)
-                    *reinterpret_cast<uint4*>(smem + (panel_at(qs, ROWS, lrow, wg * (D / 16) + j) - qs)) =
-                        live ? x[j] : make_uint4(0, 0, 0, 0);
+                for (int j = 0; j < D / 16; ++j) {
+                    uint4 hi = live ? x[j] : make_uint4(0, 0, 0, 0);
+                    const uint32_t to = panel_at(0, ROWS, lrow, wg * (D / 16) + j);
+                    if constexpr (SPLITQ) {
+                        uint4 lo;
+                        auto split = [](uint32_t& v, uint32_t& rest) {
+                            const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&v));
+                            v = pack_bf16(f.x, f.y);
+                            rest = pack_bf16(f.x - bf2f(v & 0xffffu), f.y - __uint_as_float(v & 0xffff0000u));
+                        };
+                        split(hi.x, lo.x), split(hi.y, lo.y), split(hi.z, lo.z), split(hi.w, lo.w);
+                        *reinterpret_cast<uint4*>(smem + S::Q_PART + to) = lo;
+                    }
+                    *reinterpret_cast<uint4*>(smem + to) = hi;
+                }
                 asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                 bar_arrive(&ms.q_ready);
             }
@@ -333,7 +451,7 @@ __global__ void __launch_bounds__(PrefixShape<D, FMT>::NT, 1) prefix_kernel(cons
             bool fresh = true;  // no tile of this piece yet
             for (int i = (parity ^ wg) & 1; i < take && ok; i += 2) {
                 const int stage = at_c.stage;
-                const int j0 = (off + i) * TILE;
+                const int j0 = w.at() + i * TILE;
                 if (!(ok = warp_wait(&ms.s_full[wg], at_c.pair(), abort))) break;
                 tm_after();
                 uint32_t s0[32], s1[32];
@@ -372,11 +490,11 @@ __global__ void __launch_bounds__(PrefixShape<D, FMT>::NT, 1) prefix_kernel(cons
                         s1[j] = __float_as_uint(__uint_as_float(s1[j]) * scale2);
                     }
                 }
-                if (j0 + TILE > p.shared) {
+                if (j0 > limit - TILE) {
 #pragma unroll
                     for (int j = 0; j < 32; ++j) {
-                        if (j0 + j >= p.shared) s0[j] = 0xff800000u;
-                        if (j0 + 32 + j >= p.shared) s1[j] = 0xff800000u;
+                        if (j0 + j >= limit) s0[j] = 0xff800000u;
+                        if (j0 + 32 + j >= limit) s1[j] = 0xff800000u;
                     }
                 }
                 float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
@@ -448,15 +566,15 @@ __global__ void __launch_bounds__(PrefixShape<D, FMT>::NT, 1) prefix_kernel(cons
             if (ok && !fresh) ok = warp_wait(&ms.pv_done[back.stage], back.full(), abort);
             ms.stat[wg][lrow] = make_float2(m, l);
             tm_before();
-            asm volatile("bar.sync 2, 256;" ::: "memory");
+            asm volatile("bar.sync 2, %0;" ::"r"(64 * act) : "memory");
             tm_after();
             const float2 s0 = ms.stat[0][lrow], s1 = ms.stat[1][lrow];
             const float mm = fmaxf(s0.x, s1.x), mr = mm == -INFINITY ? 0.f : mm;
             const float f0 = ex2(s0.x - mr), f1 = ex2(s1.x - mr), ll = s0.y * f0 + s1.y * f1;
             // a group without a tile (or without a finite score) has nothing in its output
             const bool has0 = s0.x != -INFINITY, has1 = s1.x != -INFINITY;
-            const bool whole = take == n_t;
-            float* slot = p.slots + (whole ? 2ll * gridDim.x + item : 2ll * blockIdx.x + (u == first ? 0 : 1)) * p.slot_floats;
+            const bool whole = take == w.n;
+            float* slot = p.slots + (whole ? 2ll * gridDim.x + (p.wide ? (long long)w.b * items : 0) + w.item : 2ll * blockIdx.x + (u == first ? 0 : 1)) * p.slot_floats;
 #pragma unroll 1
             for (int d = wg * (D / 2); d < (wg + 1) * (D / 2); d += 32) {
                 uint32_t x[32], y[32];
@@ -478,8 +596,9 @@ __global__ void __launch_bounds__(PrefixShape<D, FMT>::NT, 1) prefix_kernel(cons
             if (real && wg == 0)
                 *reinterpret_cast<float2*>(slot + (long long)p.slot_rows * D + 2 * lrow) =
                     live ? make_float2(mm, ll) : make_float2(-INFINITY, 0.f);
-            asm volatile("bar.sync 2, 256;" ::: "memory");  // the outputs have been read
+            asm volatile("bar.sync 2, %0;" ::"r"(64 * act) : "memory");  // the outputs have been read
             u += take;
+            w.on(p, take);
         }
     } else if (!F8 && warp < MMA_WARP) {
         // ================ loads by tensor maps: one warp ================
@@ -488,23 +607,32 @@ __global__ void __launch_bounds__(PrefixShape<D, FMT>::NT, 1) prefix_kernel(cons
             // and of the 32 after them.
             const int rows = min(TILE, 1 << p.ps_shift), parts = TILE / rows, mask = (1 << p.ps_shift) - 1;
             const int tiles = end - first, pshift = __ffs(parts) - 1;
-            auto page_of = [&](int i) {  // of box i; one that does not exist reads as zeros
-                if (i >> pshift >= tiles) return p.n_pages;
-                const int pos = (first + (i >> pshift)) % n_t * TILE + (i & (parts - 1)) * rows;
-                if (pos >= p.shared) return p.n_pages;
-                const int page = p.table[pos >> p.ps_shift];
-                if ((unsigned)page < (unsigned)p.n_pages) return page;
-                if (p.status) *p.status = MK_ERR_INVALID_ARG;
-                return p.n_pages;
+            Walk ahead = w;
+            int ahead_c = lane >> pshift;
+            ahead.on(p, ahead_c);
+            auto page_next = [&] {  // of this lane's box of the next 32; one that does not exist reads as zeros
+                int page = p.n_pages;
+                if (ahead_c < tiles) {
+                    const int pos = ahead.at() + (lane & (parts - 1)) * rows;
+                    if ((unsigned)pos < (unsigned)limit) {
+                        page = p.table[ahead.b * p.table_s + (pos >> p.ps_shift)];
+                        if ((unsigned)page >= (unsigned)p.n_pages) {
+                            page = p.n_pages;
+                            if (p.status) *p.status = MK_ERR_INVALID_ARG;
+                        }
+                    }
+                    ahead_c += 32 >> pshift;
+                    ahead.on(p, 32 >> pshift);
+                }
+                return page;
             };
-            int now = page_of(lane), next = page_of(32 + lane);
+            int now = page_next(), next = page_next();
             bool ok = true;
             int box = 0;
             Place<S::STAGES> pl;
-            int item = first / n_t, tile = first - item * n_t;
             for (int c = 0; c < tiles; ++c, pl.next()) {
-                const int stage = pl.stage, h = item / p.RB, j0 = tile * TILE;
-                if (++tile == n_t) tile = 0, ++item;
+                const int stage = pl.stage, h = w.item / p.RB, j0 = w.at();
+                w.on(p, 1);
                 const uint32_t st = ring + stage * S::STAGE_B;
                 if (c >= S::STAGES && !(ok = warp_wait(&ms.pv_done[stage], pl.free(), abort))) break;
                 if (lane == 0) bar_expect(&ms.kv_full[stage], S::STAGE_B);
@@ -521,7 +649,7 @@ __global__ void __launch_bounds__(PrefixShape<D, FMT>::NT, 1) prefix_kernel(cons
                     }
                     if ((box & 31) == 31) {
                         now = next;
-                        next = page_of(box + 33 + lane);
+                        next = page_next();
                     }
                 }
             }
@@ -545,24 +673,31 @@ __global__ void __launch_bounds__(PrefixShape<D, FMT>::NT, 1) prefix_kernel(cons
         const uint32_t raw0 = qs + S::RAW_OFF;
         // Row t of a tile: its page, looked up two tiles ahead of the copies, which are two ahead of their use. A
         // thread turns what it copied itself, so only the rows' places pass between threads.
-        auto look = [&](int c) {
-            if (t >= TILE || c >= tiles) return -1;
-            const int pos = (first + c) % n_t * TILE + t;
-            if (pos >= p.shared) return -1;
-            const int page = p.table[pos >> p.ps_shift];
-            if ((unsigned)page < (unsigned)p.n_pages) return page;
-            if (p.status) *p.status = MK_ERR_INVALID_ARG;
-            return -1;
+        struct At {
+            int page, r, h;  // of row t: its page (-1: none) and row there; the tile's kv head
         };
-        auto note = [&](int c, int page) {
-            if (t < TILE && c < tiles) {
-                const int r = ((first + c) % n_t * TILE + t) & mask;
-                ms.off[c & 1][t] = page < 0 ? -1 : page * p.page_b + r * p.row_b;
+        auto look = [&](int c) {  // tiles in their order
+            At x = {-1, 0, 0};
+            if (c >= tiles) return x;
+            const int pos = w.at() + t;
+            x.r = pos & mask;
+            x.h = w.item / p.RB;
+            if (t < TILE && (unsigned)pos < (unsigned)limit) {
+                x.page = p.table[w.b * p.table_s + (pos >> p.ps_shift)];
+                if ((unsigned)x.page >= (unsigned)p.n_pages) {
+                    x.page = -1;
+                    if (p.status) *p.status = MK_ERR_INVALID_ARG;
+                }
             }
+            w.on(p, 1);
+            return x;
         };
-        auto copy = [&](int c, int page) {
+        auto note = [&](int c, const At& x) {
+            if (t < TILE && c < tiles) ms.off[c & 1][t] = x.page < 0 ? -1 : x.page * p.page_b + x.r * p.row_b;
+        };
+        auto copy = [&](int c, const At& x) {
             if (c < tiles) {
-                const int h = (first + c) / n_t / p.RB;
+                const int h = x.h;
                 const uint8_t* const kh = p.k + h * p.head_b;
                 const uint8_t* const vh = p.v + h * p.head_b;
                 const uint32_t to = raw0 + c % S::RAWS * S::RAW_B;
@@ -576,32 +711,32 @@ __global__ void __launch_bounds__(PrefixShape<D, FMT>::NT, 1) prefix_kernel(cons
                     cp16(to + TILE * D + (i * 128 + t) * 16, vh + a, in);
                 }
                 if (t < TILE) {
-                    const int r = ((first + c) % n_t * TILE + t) & mask;
-                    const long long o = page < 0 ? 0 : page * p.sc_page + h * p.sc_head + r;
-                    cp4(to + 2 * TILE * D + t * 4, p.ks + o, page >= 0);
-                    cp4(to + 2 * TILE * D + (TILE + t) * 4, p.vs + o, page >= 0);
+                    const long long o = x.page < 0 ? 0 : x.page * p.sc_page + h * p.sc_head + x.r;
+                    cp4(to + 2 * TILE * D + t * 4, p.ks + o, x.page >= 0);
+                    cp4(to + 2 * TILE * D + (TILE + t) * 4, p.vs + o, x.page >= 0);
                 }
             }
             cp_commit();
         };
         auto here = [] { asm volatile("bar.sync 1, 128;" ::: "memory"); };
-        int page0 = look(0), page1 = look(1), page2 = look(2);
-        note(0, page0);
-        note(1, page1);
+        const At at0 = look(0), at1 = look(1);
+        At at2 = look(2);
+        note(0, at0);
+        note(1, at1);
         here();
-        copy(0, page0);
-        copy(1, page1);
+        copy(0, at0);
+        copy(1, at1);
         here();
         Place<S::STAGES> pl;
         bool ok = true;
         for (int c = 0; c < tiles; ++c, pl.next()) {
             const int stage = pl.stage;
             const uint32_t st = ring + stage * S::STAGE_B;
-            const int page3 = look(c + 3);
-            note(c + 2, page2);  // over the places of tile c, which were read two barriers ago
+            const At at3 = look(c + 3);
+            note(c + 2, at2);  // over the places of tile c, which were read two barriers ago
             here();
-            copy(c + 2, page2);
-            page2 = page3;
+            copy(c + 2, at2);
+            at2 = at3;
             // a thread that gave up keeps the loop's barriers
             if (ok && c >= S::STAGES) ok = bar_wait(&ms.pv_done[stage], pl.free(), abort);
             cp_wait<2>();
@@ -643,8 +778,9 @@ __global__ void __launch_bounds__(PrefixShape<D, FMT>::NT, 1) prefix_kernel(cons
             constexpr uint32_t QK = mma_desc(ROWS, TILE, false);
             const uint64_t q = smem_desc(qs, 16, 1024), k0 = smem_desc(ring, 16, 1024);
             for (int u = first; u < end && ok; ++piece_no) {
-                const int off = u % n_t, take = min(n_t - off, end - u);
+                const int take = min(w.n - w.tile, end - u);
                 u += take;
+                w.on(p, take);
                 ok = warp_wait(&ms.q_ready, piece_no & 1u, abort);
                 for (int i = 0; i < take && ok; ++i) {
                     // K is here; the softmax has read what the S buffer held two tiles ago
@@ -656,9 +792,11 @@ __global__ void __launch_bounds__(PrefixShape<D, FMT>::NT, 1) prefix_kernel(cons
                         const uint64_t k = desc_on(k0, at_c.stage * S::STAGE_B);
                         const uint32_t d = tmu + S::T_S + at_c.buf() * TILE;
 #pragma unroll
-                        for (int j = 0; j < D / 16; ++j)
-                            mma_ss(d, desc_on(q, (j >> 2) * ROWS * 128 + (j & 3) * 32),
-                                   desc_on(k, (j >> 2) * TILE * 128 + (j & 3) * 32), QK, j > 0);
+                        for (int part = 0; part < (SPLITQ ? 2 : 1); ++part)
+#pragma unroll
+                            for (int j = 0; j < D / 16; ++j)
+                                mma_ss(d, desc_on(q, part * S::Q_PART + (j >> 2) * ROWS * 128 + (j & 3) * 32),
+                                       desc_on(k, (j >> 2) * TILE * 128 + (j & 3) * 32), QK, part > 0 || j > 0);
                         mma_commit(&ms.s_full[at_c.buf()]);
                     }
                     __syncwarp();
@@ -669,8 +807,9 @@ __global__ void __launch_bounds__(PrefixShape<D, FMT>::NT, 1) prefix_kernel(cons
             constexpr uint32_t PV = mma_desc(ROWS, D, true);
             const uint64_t v0 = smem_desc(ring + S::KV_B, TILE * 128, 1024);
             for (int u = first; u < end && ok;) {
-                const int off = u % n_t, take = min(n_t - off, end - u);
+                const int take = min(w.n - w.tile, end - u);
                 u += take;
+                w.on(p, take);
                 for (int i = 0; i < take; ++i) {
                     // the probabilities are here, and so V (their scores came from the same stage)
                     if (!(ok = warp_wait(&ms.p_ready[at_c.buf()], at_c.pair(), abort))) break;
@@ -704,6 +843,54 @@ __global__ void __launch_bounds__(PrefixShape<D, FMT>::NT, 1) prefix_kernel(cons
     if (tid == 0 && ms.abort && p.status) *p.status = MK_ERR_TIMEOUT;
     if (warp == MMA_WARP)
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tm), "n"(S::T_ALL) : "memory");
+}
+
+// ---- launches (p NULL: one-time attributes)
+
+// K or V as a 4-D tensor; a box is up to 64 rows of a page by 64 values, in
+// the 128-byte swizzled order the products read
+inline int map_of(const AttendP& p, const void* base, int head_dim, CUtensorMap* out) {
+    typedef CUresult (*Encode)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*, const cuuint64_t*,
+                               const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
+                               CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+    static const Encode encode = [] {
+        void* f = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &q) != cudaSuccess ||
+            q != cudaDriverEntryPointSuccess)
+            return (Encode) nullptr;
+        return (Encode)f;
+    }();
+    if (!encode) return fail(MK_ERR_CUDA, "attend: the driver has no cuTensorMapEncodeTiled");
+    const cuuint32_t rows = 1u << p.ps_shift;
+    const cuuint64_t dims[4] = {(cuuint64_t)head_dim, rows, (cuuint64_t)p.H, (cuuint64_t)p.n_pages};
+    const cuuint64_t strides[3] = {(cuuint64_t)p.row_b, (cuuint64_t)p.head_b, (cuuint64_t)p.page_b};
+    const cuuint32_t box[4] = {64, rows < 64 ? rows : 64, 1, 1}, one[4] = {1, 1, 1, 1};
+    const CUresult r = encode(out, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(base), dims, strides, box, one,
+                              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                              CU_TENSOR_MAP_L2_PROMOTION_L2_128B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    if (r != CUDA_SUCCESS) return fail(MK_ERR_CUDA, "attend: cuTensorMapEncodeTiled failed (%d)", (int)r);
+    return MK_OK;
+}
+
+template <int D, int FMT, bool SPLITQ>
+int prefix_go(const AttendP* p, int grid, cudaStream_t s) {
+    using S = PrefixShape<D, FMT, SPLITQ>;
+    auto kern = prefix_kernel<D, FMT, SPLITQ>;
+    if (!p) return cuda_status(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, S::SMEM), "mk_pages_attend");
+    PrefixMaps maps = {};
+    if constexpr (FMT == MK_KV_BF16) {
+        if (const int rc = map_of(*p, p->k, D, &maps.k)) return rc;
+        if (const int rc = map_of(*p, p->v, D, &maps.v)) return rc;
+    }
+    kern<<<grid, S::NT, S::SMEM, s>>>(*p, maps);
+    return cuda_status(cudaGetLastError(), "mk_pages_attend");
+}
+template <int D, bool SPLITQ>
+int prefix_pick(int format, const AttendP* p, int grid, cudaStream_t s) {
+    if (format == MK_KV_E4M3) return prefix_go<D, MK_KV_E4M3, SPLITQ>(p, grid, s);
+    if (format == MK_KV_INT8) return prefix_go<D, MK_KV_INT8, SPLITQ>(p, grid, s);
+    return prefix_go<D, MK_KV_BF16, SPLITQ>(p, grid, s);
 }
 
 }  // namespace mkop

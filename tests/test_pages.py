@@ -693,3 +693,105 @@ def test_shared_prefixes_in_other_layouts(fmt, order):
     v.copy_(cache.v.view(raw))
     other = pages.Pages(k.view(fmt), v.view(fmt), cache.k_scale, cache.v_scale)
     assert torch.equal(other.attend(table, n, q, shared_len=shared), want)
+
+
+# ---------------------------------------------------------------- wide calls: many rows a kv head and long tables
+
+def widen(table, Hq, H, T, ps):
+    """More columns, of no page, up to the capacity from which whole tiles have a launch of their own."""
+    rows = T * Hq // H
+    tiles = 2000 * 160 // (table.shape[0] * H * -(-rows // 128) * min(rows, 128)) + 1
+    return torch.nn.functional.pad(table, (0, max(0, tiles * 64 // ps - table.shape[1])), value=-1).contiguous()
+
+
+@gpu
+@pytest.mark.parametrize("qdtype", [torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("B,T,Hq,H,D,ps,lens", [
+    (1, 17, 2, 1, 64, 64, [4096]),                       # whole tiles alone but for the last tokens
+    (4, 1, 80, 2, 128, 16, [1024, 0, 64, 3000]),         # one token of 40 heads: a length of whole tiles has no rest
+    (3, 10, 16, 4, 128, 32, [73, 2050, 10]),             # a whole tile not seen by all tokens
+    (2, 66, 4, 2, 128, 64, [900, 1500]),                 # 132 rows: a second row block of four
+    (90, 33, 1, 1, 64, 8, [34 + 13 * b for b in range(90)]),
+    (2, 300, 4, 2, 64, 64, [1900, 200]),                 # fewer positions than tokens
+])
+def test_wide_calls_match_the_definition(qdtype, fmt, B, T, Hq, H, D, ps, lens):
+    cache, table, n, q = build(fmt, qdtype, B, T, Hq, H, D, ps, lens)
+    table = widen(table, Hq, H, T, ps)
+    scale = 1 / math.sqrt(D)
+    status = ints(0)
+    for kw in (dict(), dict(softcap=15.0, slopes=torch.linspace(0.001, 0.02, Hq, device="cuda"),
+                            starts=ints(*[(61 * b * b) % (lens[b] + 9) for b in range(B)]))):
+        out, lse = cache.attend(table, n, q, return_lse=True, status=status, **kw)
+        check(cache, table, n, q, out, lse, scale, **kw)
+        assert torch.equal(out, cache.attend(table, n, q, **kw))
+    assert int(status) == 0
+
+
+@gpu
+@pytest.mark.parametrize("fmt", FORMATS)
+def test_wide_calls_keep_what_a_row_does_not_see_out(fmt):
+    B, T, Hq, H, D, ps = 3, 10, 16, 4, 128, 16
+    lens, first = [2000, 333, 700], ints(130, 0, 64)
+    cache, table, n, q = build(fmt, torch.bfloat16, B, T, Hq, H, D, ps, lens)
+    table = widen(table, Hq, H, T, ps)
+    clean, clse = cache.attend(table, n, q, starts=first, return_lse=True)
+    seen = torch.zeros((cache.k.shape[0], ps), dtype=torch.bool, device="cuda")
+    for b in range(B):
+        j = torch.arange(int(first[b]), lens[b], device="cuda")
+        seen[table[b, j // ps].long(), j % ps] = True
+    hide = (~seen)[:, None, :].expand(-1, H, -1)
+    if fmt == torch.bfloat16:
+        cache.k[hide], cache.v[hide] = math.nan, math.inf
+    else:
+        cache.k_scale[hide], cache.v_scale[hide] = math.nan, math.inf
+        if fmt == torch.float8_e4m3fn:
+            cache.v.view(torch.uint8)[hide] = 0x7F
+    out, lse = cache.attend(table, n, q, starts=first, return_lse=True)
+    assert torch.equal(out, clean) and torch.equal(lse, clse)
+    # a value that every row of one head sees
+    pg, r = int(table[0, 500 // ps]), 500 % ps
+    if fmt == torch.bfloat16:
+        cache.v[pg, 1, r, 40] = math.nan
+    elif fmt == torch.int8:
+        cache.v_scale[pg, 1, r] = math.nan
+    else:
+        cache.v.view(torch.uint8)[pg, 1, r, 40] = 0xFF
+    out = cache.attend(table, n, q, starts=first)
+    assert bool(torch.isnan(out[0, :, 4:8, 40]).all())
+    keep = torch.ones_like(out, dtype=torch.bool)
+    keep[0, :, 4:8] = False
+    assert torch.equal(out[keep], clean[keep])
+
+
+@gpu
+def test_wide_calls_report_bad_pages_and_lengths():
+    B, T, Hq, H, ps = 2, 10, 16, 4, 64
+    cache, table, n, q = build(torch.int8, torch.bfloat16, B, T, Hq, H, 128, ps, [1000, 900])
+    table = widen(table, Hq, H, T, ps)
+    want = cache.attend(table, n, q)
+    status = ints(0)
+    bad = table.clone()
+    bad[1, 3] = cache.k.shape[0]
+    out = cache.attend(bad, n, q, status=status)
+    assert int(status) == mk.ERR_INVALID_ARG and torch.equal(out[0], want[0])
+    status.zero_()
+    out, lse = cache.attend(table, ints(1000, table.shape[1] * ps + 1), q, return_lse=True, status=status)  # past the table
+    assert int(status) == mk.ERR_INVALID_ARG
+    # work is cut by the tiles of all sequences, so the other one's sums are grouped in another way: the same bound
+    # holds for it, not the same bits
+    check(cache, table[:1], n[:1], q[:1], out[:1], lse[:1], 1 / math.sqrt(128))
+
+
+@gpu
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("D", [64, 128])
+def test_a_shared_prefix_with_fp16_queries(fmt, D):
+    B, T, Hq, H, ps, shared = 19, 2, 8, 2, 32, 1984
+    lens = [shared + T - 1 + (7 * b) % 40 for b in range(B)]
+    lens[5], lens[6] = 0, 700
+    cache, table, n, q = build(fmt, torch.float16, B, T, Hq, H, D, ps, lens, shared=shared)
+    q[1] = 2.0 ** -20  # under fp16's normal range
+    for kw in (dict(), dict(softcap=15.0, slopes=torch.linspace(0.001, 0.02, Hq, device="cuda"))):
+        out, lse = cache.attend(table, n, q, shared_len=shared, return_lse=True, **kw)
+        check(cache, table, n, q, out, lse, 1 / math.sqrt(D), **kw)
