@@ -346,7 +346,7 @@ const char* mk_last_error(void);
 /* ---------------------------------------------------------------------------
  * Operators on paged caches and logits. They run beside the decode step, on
  * memory the caller owns: no model handle, no allocation, no state kept
- * between calls. All of them are asynchronous on `stream`, may be captured
+ * between calls; what they compute has no gradient. All of them are asynchronous on `stream`, may be captured
  * into a CUDA graph, and check on the host what the host can see (NULL
  * pointers, shapes, alignment: MK_ERR_INVALID_ARG; shapes no kernel exists
  * for: MK_ERR_UNSUPPORTED). What only the device can see (positions and page
@@ -372,8 +372,8 @@ enum mk_dtype { MK_DT_F32 = 0, MK_DT_BF16 = 1, MK_DT_F16 = 2 };
  * v); its scale is at p*scale_page_stride + h*scale_head_stride + r of
  * k_scale (or v_scale; NULL for MK_KV_BF16). k, v and the strides in bytes
  * are multiples of 8 elements, for mk_pages_attend also of 16 bytes.
- * page_size is a power of two; head_dim a multiple of 8, at most 256. Rows of
- * different (page, head, row) must not overlap. */
+ * page_size is a power of two; head_dim a multiple of 8, at most 256; at most
+ * 1024 kv heads. Rows of different (page, head, row) must not overlap. */
 typedef struct mk_pages {
     void *k, *v;
     float *k_scale, *v_scale;
@@ -439,11 +439,12 @@ int mk_kv_view(const mk_kv* kv, int32_t layer, mk_pages* pages, mk_page_table* t
  * h / (n_q_heads / n_kv_heads).
  *
  * shared_len > 0 says that the first shared_len positions of all sequences
- * lie in the same pages (the first shared_len / page_size entries of every
- * table row are those of row 0; a multiple of page_size): they are read once
- * for the whole batch, as one product over all its queries. Sequences whose
- * tokens do not all see all of them (length 0, a later start, a length that
- * ends inside) are read on their own, through their own table row. */
+ * lie in the same pages (a multiple of page_size: the first shared_len /
+ * page_size entries of their table rows are the same): they are read once for
+ * the whole batch, as one product over all its queries. Sequences whose tokens
+ * do not all see all of them (length 0, a later start, a length that ends
+ * inside) do not take part: they are read on their own, through their own
+ * table row. */
 typedef struct mk_attention {
     const mk_pages* pages;
     const mk_page_table* table;
@@ -467,9 +468,11 @@ typedef struct mk_attention {
 int mk_pages_attend_workspace(const mk_attention* args, int64_t* bytes);
 
 /* Errors: INVALID_ARG (NULL, shapes, alignment, a workspace too small or not
- * 256-byte aligned), UNSUPPORTED (head_dim other than 64, 128 or 256). A length beyond the
- * table or a page out of range is reported through `status`; what lies there
- * counts as rows of zeros, or beyond the table as not visible. */
+ * 256-byte aligned), UNSUPPORTED (head_dim other than 64, 128 or 256). A length
+ * beyond the table or a page out of range is reported through `status`; what
+ * lies there counts as rows of zeros, or beyond the table as not visible. A
+ * wait inside a kernel that runs out (2 s; no healthy call comes near) stores
+ * MK_ERR_TIMEOUT there, and the output is not to be used. */
 int mk_pages_attend(const mk_attention* args, void* workspace, int64_t workspace_bytes, void* stream);
 
 /* Draws one token a row from logits. With w_i = exp((x_i - max x) / T), in 32

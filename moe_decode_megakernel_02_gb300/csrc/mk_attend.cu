@@ -82,6 +82,8 @@ int make_plan(const mk_attention* a, Plan& pl) {
         return fail(MK_ERR_INVALID_ARG, "attend: q must be bf16 or fp16, out of the same type");
     if ((uintptr_t)a->q->data % 2 || (uintptr_t)a->out->data % 2)
         return fail(MK_ERR_INVALID_ARG, "attend: q or out not aligned to its type");
+    if (off_by4(a->lens, a->starts, a->slopes, a->lse, a->status))
+        return fail(MK_ERR_INVALID_ARG, "attend: lens, starts, slopes, lse or status not aligned to 4 bytes");
     if (!(a->scale == a->scale) || !(a->softcap >= 0.f) || a->softcap > 1e30f)
         return fail(MK_ERR_INVALID_ARG, "attend: scale or softcap");
     const int64_t cap = (int64_t)t.pages_per_seq * g.page_size;

@@ -109,6 +109,20 @@ __device__ __forceinline__ void whole_tiles(const AttendP& p, int b, int& g0, in
     g0 = (int)((lo + 63u) / 64u);
     g1 = max(g0, hi < 0 ? 0 : (int)(hi / 64));
 }
+// The shared launch: the first sequence that takes part (its table row leads to
+// the pages; a padded one's may hold anything), INT_MAX when none does. A whole
+// CTA asks, of `threads` threads; `at` is shared memory.
+__device__ __forceinline__ int first_sharing(const AttendP& p, int threads, int* at) {
+    if (threadIdx.x == 0) *at = INT_MAX;
+    __syncthreads();
+    for (int b = threadIdx.x; b < p.B; b += threads)
+        if (shares(p, b)) {
+            atomicMin(at, b);
+            break;
+        }
+    __syncthreads();
+    return *at;
+}
 // the positions of sequence b that a launch covers, [lo, hi)
 __device__ __forceinline__ void cover(const AttendP& p, int b, int& lo, int& hi) {
     if (p.is_shared) {
@@ -251,7 +265,7 @@ template <int ROWS, int TILE>
 struct Misc {
     long long off[2][TILE];  // bytes after the head's first row; -1: no such row, zeros
     int scan[8];
-    int found_base;
+    int found_base, found_row;
     float slope2[ROWS];  // slope * log2 e
     float qscale[ROWS];  // 8-bit pages: the power of two taken out of the query
     int lo[ROWS], hi[ROWS], at[ROWS];
@@ -315,7 +329,7 @@ __global__ void __launch_bounds__(32 * WP * WR, Shape<D, FMT, SPLITQ, WP, WR, RN
     attend_kernel(const __grid_constant__ AttendP p) {
     using S = Shape<D, FMT, SPLITQ, WP, WR, RN>;
     constexpr int AT = S::NT;
-    const int cluster = CL ? p.cluster : 0;
+    const int cluster = CL ? p.cluster : 1;
     constexpr bool F8 = S::F8;
     constexpr int ROWB = S::ROWB, TILE = S::TILE, SL = S::SL, ROWS = S::ROWS, DT = D / 16;
     using M = Misc<ROWS, TILE>;
@@ -335,7 +349,6 @@ __global__ void __launch_bounds__(32 * WP * WR, Shape<D, FMT, SPLITQ, WP, WR, RN
             for (int b = tid; b < p.B; b += AT)
                 if (p.lens[b] > (p.pps << p.ps_shift)) *p.status = MK_ERR_INVALID_ARG;
     } else {
-        asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
         // each thread counts a stretch of sequences; sums before it by shuffles
         const int each = (nb + AT - 1) / AT, b0 = min(nb, tid * each), b1 = min(nb, b0 + each);
         int mine = 0;
@@ -389,6 +402,8 @@ __global__ void __launch_bounds__(32 * WP * WR, Shape<D, FMT, SPLITQ, WP, WR, RN
         }
         __syncthreads();
     }
+    // the sequence whose table row a shared launch reads; no page is looked up when no sequence takes part
+    const int row_seq = !CL && p.is_shared ? first_sharing(p, AT, &ms.found_row) : 0;
     // a cluster's item, and this CTA's place in it
     const int c_item = CL ? blockIdx.x / cluster : 0, c_rank = CL ? blockIdx.x - c_item * cluster : 0;
     int b = CL ? c_item / items : ms.found_b;
@@ -431,11 +446,11 @@ __global__ void __launch_bounds__(32 * WP * WR, Shape<D, FMT, SPLITQ, WP, WR, RN
         // ---- fetching: where a tile's rows lie is looked up one tile ahead of the copies, a thread a row
         const uint8_t* const kh = p.k + h * p.head_b;
         const uint8_t* const vh = p.v + h * p.head_b;
-        const int* const trow = p.table + (p.is_shared ? 0 : b) * p.table_s;
+        const int* const trow = p.table + (p.is_shared ? (row_seq == INT_MAX ? 0 : row_seq) : b) * p.table_s;
         const int mask = (1 << p.ps_shift) - 1;
         auto page_of = [&](int tile) {  // of position tid of the tile; -1: not this item's, or no such page
             const int pos = t_at(tile) * TILE + tid;
-            if (tid >= TILE || tile >= take || pos < clo || pos >= chi) return -1;
+            if (tid >= TILE || tile >= take || pos < clo || pos >= chi || row_seq == INT_MAX) return -1;
             const int pg = trow[pos >> p.ps_shift];
             if ((unsigned)pg < (unsigned)p.n_pages) return pg;
             if (p.status) *p.status = MK_ERR_INVALID_ARG;

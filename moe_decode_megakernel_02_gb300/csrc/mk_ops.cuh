@@ -33,6 +33,12 @@ inline int dtype_bytes(int dt) { return dt == MK_DT_F32 ? 4 : (dt == MK_DT_BF16 
 inline int code_bytes(int format) { return format == MK_KV_BF16 ? 2 : 1; }
 inline int log2_exact(int n) { return n > 0 && (n & (n - 1)) == 0 ? __builtin_ctz((unsigned)n) : -1; }
 
+// whether any of some pointers to 32-bit values is off its alignment
+template <typename... P>
+inline bool off_by4(const P*... p) {
+    return ((((uintptr_t)p % 4) | ...)) != 0;
+}
+
 // what every operator on pages asks of its cache and table
 int check_pages(const mk_pages* p, const mk_page_table* t);
 

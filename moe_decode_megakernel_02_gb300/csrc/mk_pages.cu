@@ -14,12 +14,15 @@ int check_pages(const mk_pages* p, const mk_page_table* t) {
         return fail(MK_ERR_INVALID_ARG, "pages: 8-bit formats need k_scale and v_scale, bf16 pages have none");
     if (p->n_pages < 1 || p->n_kv_heads < 1 || p->head_dim < 1 || t->batch < 1 || t->pages_per_seq < 1 || t->stride < 0)
         return fail(MK_ERR_INVALID_ARG, "pages: non-positive dimension");
-    if (p->n_kv_heads > 65535 || t->batch > (1 << 20)) return fail(MK_ERR_UNSUPPORTED, "pages: too many heads or sequences");
+    // (1024 heads of 32 lanes: what the copies' division by a multiplication is exact for)
+    if (p->n_kv_heads > 1024 || t->batch > (1 << 20)) return fail(MK_ERR_UNSUPPORTED, "pages: too many heads or sequences");
     if (p->head_dim % 8 || p->head_dim > 256)
         return fail(MK_ERR_UNSUPPORTED, "pages: head_dim must be a multiple of 8, at most 256");
     if (log2_exact(p->page_size) < 0) return fail(MK_ERR_UNSUPPORTED, "pages: page_size must be a power of two");
     if ((int64_t)t->pages_per_seq * p->page_size > (1 << 30))
         return fail(MK_ERR_UNSUPPORTED, "pages: a sequence has at most 2^30 positions");
+    if (off_by4(t->table, p->k_scale, p->v_scale))
+        return fail(MK_ERR_INVALID_ARG, "pages: table or scales not aligned to 4 bytes");
     const int e = code_bytes(p->format);
     if ((uintptr_t)p->k % (8 * e) || (uintptr_t)p->v % (8 * e) || p->page_stride % 8 || p->head_stride % 8 ||
         p->row_stride % 8)
@@ -456,6 +459,8 @@ int copy(const mk_pages* g, const mk_page_table* t, const int32_t* positions, co
          const mk_rows* k, const mk_rows* v, int32_t* status, void* stream) {
     if (const int rc = check_pages(g, t)) return rc;
     if (!positions) return fail(MK_ERR_INVALID_ARG, "pages: positions is NULL");
+    if (off_by4(positions, counts, status))
+        return fail(MK_ERR_INVALID_ARG, "pages: positions, counts or status not aligned to 4 bytes");
     if (n < 0) return fail(MK_ERR_INVALID_ARG, "pages: negative token count");
     if (const int rc = check_rows(k, "k")) return rc;
     if (const int rc = check_rows(v, "v")) return rc;

@@ -298,7 +298,8 @@ __global__ void __launch_bounds__(PrefixShape<D, FMT, SPLITQ>::NT, 1)
 
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     // (the host sees to it that the tiles of all items fit 32 bits)
-    const int items = p.H * p.RB, limit = p.wide ? p.pps << p.ps_shift : p.shared;  // items of a sequence; positions
+    const int items = p.H * p.RB;  // of a sequence
+    int limit = p.wide ? p.pps << p.ps_shift : p.shared;  // positions
     int total, mine = 0, before = 0;
     const int each = (p.B + S::NT - 1) / S::NT, b0 = min(p.B, tid * each), b1 = min(p.B, b0 + each);
     auto tiles_of = [&](int b) {
@@ -352,8 +353,10 @@ __global__ void __launch_bounds__(PrefixShape<D, FMT, SPLITQ>::NT, 1)
                 at += n;
             }
         }
-    } else if (tid == 0) {
-        ms.found_b = ms.found_base = 0;
+    } else {
+        const int b = first_sharing(p, S::NT, &ms.scan[0]);
+        if (b == INT_MAX) limit = 0;  // no sequence takes part, and no page is looked up
+        if (tid == 0) ms.found_b = b == INT_MAX ? 0 : b, ms.found_base = 0;
     }
     // warps of a group that have rows at all
     const int act = p.RB > 1 ? 4 : (p.rows_item + 31) / 32;

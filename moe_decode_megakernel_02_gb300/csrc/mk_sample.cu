@@ -907,6 +907,8 @@ extern "C" int mk_sample(const mk_sampling* a, void* stream) {
     if (a->rows == 0) return MK_OK;
     if (!a->logits || !a->u || !a->tokens) return fail(MK_ERR_INVALID_ARG, "sample: logits, u or tokens is NULL");
     if ((uintptr_t)a->logits % e) return fail(MK_ERR_INVALID_ARG, "sample: logits not aligned to their type");
+    if (off_by4(a->u, a->temperature, a->top_k, a->top_p, a->min_p, a->tokens, a->probs, a->kept))
+        return fail(MK_ERR_INVALID_ARG, "sample: a 32-bit array is not aligned to 4 bytes");
     constexpr int most = MAXC * (MAX_SLICE_B / 4);
     if (a->vocab > most) return fail(MK_ERR_UNSUPPORTED, "sample: vocab above %d", most);
     if (a->rows > INT32_MAX / MAXC) return fail(MK_ERR_UNSUPPORTED, "sample: too many rows");

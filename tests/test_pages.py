@@ -795,3 +795,134 @@ def test_a_shared_prefix_with_fp16_queries(fmt, D):
     for kw in (dict(), dict(softcap=15.0, slopes=torch.linspace(0.001, 0.02, Hq, device="cuda"))):
         out, lse = cache.attend(table, n, q, shared_len=shared, return_lse=True, **kw)
         check(cache, table, n, q, out, lse, 1 / math.sqrt(D), **kw)
+
+
+# ---------------------------------------------------------------- calls at their limits
+
+@pytest.mark.parametrize("over,code", [
+    (dict(t__table=4098), mk.ERR_INVALID_ARG), (dict(p__n_kv_heads=1025), mk.ERR_UNSUPPORTED),
+    (dict(p__format=mk.KV_INT8, p__k_scale=4097, p__v_scale=4096), mk.ERR_INVALID_ARG),
+])
+def test_unaligned_tables_and_too_many_heads_are_refused(over, code):
+    p, t, r, a = _structs(**over)
+    a["n_q_heads"] = p.n_kv_heads
+    ref, L = ctypes.byref, mk.lib()
+    for f in (L.mk_pages_write, L.mk_pages_read):
+        assert f(ref(p), ref(t), 4096, None, 1, ref(r), ref(r), None, None) == code
+    att = mk.AttentionStruct(pages=ctypes.pointer(p), table=ctypes.pointer(t), q=ctypes.pointer(r), out=ctypes.pointer(r),
+                             **a)
+    assert L.mk_pages_attend(ref(att), 4096, 1 << 30, None) == code
+
+
+def test_unaligned_positions_and_lengths_are_refused():
+    p, t, r, a = _structs()
+    ref, L = ctypes.byref, mk.lib()
+    for args in ((4097, None, None), (4096, 4098, None), (4096, None, 4099)):
+        pos, cnt, st = args
+        assert L.mk_pages_write(ref(p), ref(t), pos, cnt, 1, ref(r), ref(r), st, None) == mk.ERR_INVALID_ARG
+    for name in ("lens", "starts", "slopes", "lse", "status"):
+        b = dict(a, **{name: 4098})
+        att = mk.AttentionStruct(pages=ctypes.pointer(p), table=ctypes.pointer(t), q=ctypes.pointer(r),
+                                 out=ctypes.pointer(r), **b)
+        assert L.mk_pages_attend(ref(att), 4096, 1 << 30, None) == mk.ERR_INVALID_ARG
+
+
+@gpu
+@pytest.mark.parametrize("D,qdtype", [(128, torch.bfloat16), (64, torch.float16), (256, torch.bfloat16)])
+def test_a_padded_sequence_leads_to_no_shared_page(D, qdtype):
+    """The first sequences' table rows hold no pages: the others' shared positions are found all the same."""
+    B, Hq, H, ps, shared = 36, 4, 2, 16, 320
+    lens = [0, 0] + [shared + 3 + b for b in range(B - 2)]
+    cache, table, n, q = build(torch.int8, qdtype, B, 1, Hq, H, D, ps, lens, shared=shared)
+    table[:2] = -1
+    status = ints(0)
+    out, lse = cache.attend(table, n, q, shared_len=shared, return_lse=True, status=status)
+    check(cache, table, n, q, out, lse, 1 / math.sqrt(D))
+    # nobody takes part: nothing shared is read
+    n.zero_()
+    out, lse = cache.attend(torch.full_like(table, -1), n, q, shared_len=shared, return_lse=True, status=status)
+    assert bool((out == 0).all()) and bool((lse == -math.inf).all()) and int(status) == 0
+
+
+@gpu
+@pytest.mark.parametrize("kind", ["shared", "wide", "small"])
+def test_captured_calls_of_every_kind(kind):
+    """Each choice of kernels in two graphs, replayed side by side, with lengths that change after the capture."""
+    if kind == "shared":
+        B, T, Hq, H, ps, shared = 20, 1, 8, 2, 32, 640
+        lens = [shared + 5 * b + 1 for b in range(B)]
+    elif kind == "wide":
+        B, T, Hq, H, ps, shared, lens = 3, 10, 16, 4, 64, 0, [500, 2000, 64]
+    else:
+        B, T, Hq, H, ps, shared, lens = 2, 1, 8, 2, 64, 0, [900, 1500]
+    cache, table, n, q = build(torch.float8_e4m3fn, torch.bfloat16, B, T, Hq, H, 128, ps, lens, shared=shared)
+    if kind == "wide":
+        table = widen(table, Hq, H, T, ps)
+    cache.attend(table, n, q, shared_len=shared)
+    q2, n1, n2, side = torch.randn_like(q), n.clone(), n.clone(), torch.cuda.Stream()
+    graphs, outs = [], []
+    for nn, qq in ((n1, q), (n2, q2)):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            outs.append(cache.attend(table, nn, qq, shared_len=shared))
+        graphs.append(g)
+    n1.copy_(n.flip(0).clamp(max=max(lens)))
+    n2[B // 2] = 0
+    torch.cuda.synchronize()
+    for _ in range(5):
+        graphs[0].replay()
+        with torch.cuda.stream(side):
+            graphs[1].replay()
+    torch.cuda.synchronize()
+    assert torch.equal(outs[0], cache.attend(table, n1, q, shared_len=shared))
+    assert torch.equal(outs[1], cache.attend(table, n2, q2, shared_len=shared))
+
+
+@gpu
+def test_output_in_place_of_the_queries():
+    for B, T, Hq, H, lens, shared in ((2, 1, 8, 2, [900, 1500], 0), (1, 1, 8, 2, [40000], 0), (20, 1, 8, 2, [700] * 20, 640)):
+        cache, table, n, q = build(torch.bfloat16, torch.bfloat16, B, T, Hq, H, 64, 64, lens, shared=shared)
+        want = cache.attend(table, n, q, shared_len=shared)
+        assert cache.attend(table, n, q, shared_len=shared, out=q) is q
+        assert torch.equal(q, want)
+
+
+@gpu
+@pytest.mark.parametrize("fmt", FORMATS)
+def test_a_prompt_then_steps_then_tokens(fmt):
+    """The operators as a decode loop runs them: a prompt written and attended to in chunks, then steps whose queries
+    come from what the cache gave back, tokens drawn from their outputs; every step against 64 bits."""
+    from moe_decode_megakernel_02_gb300 import sampling
+    B, Hq, H, D, ps, V = 3, 8, 2, 64, 16, 512
+    g = torch.Generator(device="cuda").manual_seed(11)
+    rand = lambda *s: torch.randn(s, generator=g, device="cuda")  # noqa: E731
+    cache = make_cache(fmt, B * 8, H, ps, D, fill=False)
+    table = torch.randperm(B * 8, generator=g, device="cuda").to(torch.int32).view(B, 8)
+    head, prompt = rand(Hq * D, V), ints(50, 33, 1)
+    at = ints(0, 0, 0)
+    for t0 in range(0, 50, 20):  # chunks of 20 tokens; sequences end in different ones
+        T = min(20, 50 - t0)
+        counts = (prompt - t0).clamp(0, T).to(torch.int32)
+        x, y = rand(B, T, H, D).bfloat16(), rand(B, T, H, D).bfloat16()
+        cache.write(table, at, x, y, counts=counts)
+        at = at + counts
+        q = rand(B, T, Hq, D).bfloat16()
+        out, lse = cache.attend(table, at, q, return_lse=True)
+        check(cache, table, at, q, out, lse, 1 / math.sqrt(D))
+    assert at.tolist() == prompt.tolist()
+    tokens = torch.zeros(B, dtype=torch.int32, device="cuda")
+    for _ in range(4):
+        k, v = (torch.zeros((B, 1, H, D), dtype=torch.float32, device="cuda") for _ in range(2))
+        cache.read(table, at - 1, k, v)
+        x = k + 0.01 * tokens.view(B, 1, 1, 1)
+        cache.write(table, at, x, v)
+        at = at + 1
+        q = x.repeat_interleave(Hq // H, 2).bfloat16()
+        out, lse = cache.attend(table, at, q, return_lse=True)
+        check(cache, table, at, q, out, lse, 1 / math.sqrt(D))
+        logits = out.view(B, Hq * D).float() @ head
+        tokens = sampling.sample(logits, torch.rand(B, generator=g, device="cuda"), top_k=ints(1, 20, 0),
+                                 temperature=torch.full((B,), 0.7, device="cuda"))
+        assert int(tokens[0]) == int(logits[0].argmax()) and bool(((tokens >= 0) & (tokens < V)).all())
+        top = logits[1].sort(descending=True).indices[:20]
+        assert int(tokens[1]) in top.tolist()

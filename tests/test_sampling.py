@@ -298,3 +298,38 @@ def test_borders_that_fit_no_list(dtype):
     tok, _, kept = sampling.sample(x[:1].repeat(4, 1), floats(0, 0.5, 0.999999, 0.999999), top_k=ints(0, 9000, 9000, 9000),
                                    top_p=floats(0.5, 1.0, 0.5, 1.0), return_details=True)
     assert kept.tolist() == [20000, 9000, 4500, 9000] and tok.tolist() == [0, 4500, 4499, 8999]
+
+
+@pytest.mark.parametrize("name", ["u", "temperature", "top_k", "top_p", "min_p", "tokens", "probs", "kept"])
+def test_unaligned_arrays_are_refused(name):
+    assert mk.lib().mk_sample(ctypes.byref(_struct(**{name: 4098})), None) == mk.ERR_INVALID_ARG
+
+
+@gpu
+def test_two_calls_at_once_and_replayed():
+    """Every kind of filter in graphs replayed side by side, on rows that change after the capture."""
+    R, V = 12, 30000
+    x = torch.randn((R, V), device="cuda") * 2
+    y, u = torch.randn_like(x), torch.rand(R, device="cuda")
+    kinds = (dict(), dict(top_k=ints(*[30] * R)), dict(top_p=floats(*[0.9] * R)),
+             dict(top_k=ints(*[900] * R), top_p=floats(*[0.95] * R), min_p=floats(*[0.001] * R)),
+             dict(temperature=floats(*[0.0] * R)))
+    graphs, outs = [], []
+    for src in (x, y):
+        for kw in kinds:
+            g = torch.cuda.CUDAGraph()
+            with torch.cuda.graph(g):
+                outs.append(sampling.sample(src, u, return_details=True, **kw))
+            graphs.append(g)
+    x.copy_(torch.randn_like(x))
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for _ in range(3):
+        for i in range(len(kinds)):
+            graphs[i].replay()
+            with torch.cuda.stream(side):
+                graphs[len(kinds) + i].replay()
+    torch.cuda.synchronize()
+    want = [sampling.sample(src, u, return_details=True, **kw) for src in (x, y) for kw in kinds]
+    for got, w in zip(outs, want):
+        assert all(torch.equal(a, b) for a, b in zip(got, w))
