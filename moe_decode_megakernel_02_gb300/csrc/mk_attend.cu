@@ -9,7 +9,15 @@ namespace {
 using namespace mkop;
 
 constexpr int MAX_DEV = 32;
-constexpr int CLUSTER_TILES = 12;
+// Small calls: an item is one cluster's while that leaves a CTA at most so many
+// tiles. One launch in place of two, and no workspace: 6 us less of the host's
+// time, and for 8 sequences of 1024 positions (4 kv heads of 128) 10.6 us in
+// place of 13.3 on the device, of 4096 16.6 in place of 17.8. One sequence,
+// whose 4 clusters leave most of the device idle: 1024 positions 9.4 and 9.5,
+// 4096 (8 tiles) 14.1 and 11.1, which the host's time outweighs, 6144 18.6 and
+// 12.4, which it does not. Clusters of 16 take one sequence of 4096 to 11.4,
+// but cost the others 1 to 3 us (and are not portable).
+constexpr int CLUSTER_TILES = 8;
 // Wide calls: from so many rows x tiles an SM on, the tiles that a sequence's
 // tokens all see whole go to the tensor memory's kernel, the rest and the join
 // being worth some 10 us. Measured without and with it, 16 query heads on 4 kv
@@ -108,13 +116,13 @@ int make_plan(const mk_attention* a, Plan& pl) {
     const int min_units = 2;
     const int64_t items = (int64_t)B * H * pl.own_rb;
     if (items > INT32_MAX / 16) return fail(MK_ERR_UNSUPPORTED, "attend: too many queries in one call");
-    // Small calls: up to CLUSTER_TILES tiles a CTA, all items' clusters resident at once (or nearly)
+    // (all items' clusters are resident at once, or nearly)
     pl.cluster = 0;
     pl.wide = false;
     if (!a->shared_len && pl.own_k.rows <= 32) {
         const int64_t tiles = (cap + pl.own_i.tile - 1) / pl.own_i.tile;
         int c = 1;
-        while (c < 8 && tiles > 4 * c && items * c * 2 <= (int64_t)sms * pl.own_i.ctas) c *= 2;
+        while (c < MAX_CLUSTER && tiles > 4 * c && items * c * 2 <= (int64_t)sms * pl.own_i.ctas) c *= 2;
         if (tiles <= CLUSTER_TILES * c && items * c <= (int64_t)sms * pl.own_i.ctas * 2) {
             pl.cluster = c;
             pl.own_grid = (int)(items * c);
@@ -144,8 +152,10 @@ int make_plan(const mk_attention* a, Plan& pl) {
     if (a->shared_len || pl.wide) {
         const int64_t all = pl.wide ? rows : (int64_t)B * rows;
         pl.sh_k = Kind{g.format, splitq, block_of(all)};
-        // (up to 32 shared rows are bound by the cache's bytes and would leave most of its 128 rows empty)
-        pl.prefix = pl.wide || (fits && all > 32);
+        // 8-bit pages: their conversion costs the same for few rows. A prefix of 16384 positions in 8 heads of 128,
+        // without and with it: INT8 8 rows 31 and 44 us, 16 rows 40 and 44, 32 rows 53 and 49; bf16 4 rows 34 and
+        // 34, 16 rows 44 and 38, 32 rows 55 and 42.
+        pl.prefix = pl.wide || (fits && (g.format == MK_KV_BF16 || all > 16));
         if (const int rc = pl.prefix ? prefix_info(dev, D, g.format, a->q->dtype == MK_DT_F16, pl.sh_i) : kind_info(dev, D, pl.sh_k, pl.sh_i))
             return rc;
         if (pl.sh_i.ctas < 1) return fail(MK_ERR_UNSUPPORTED, "attend: the kernel does not fit this device");

@@ -85,6 +85,7 @@ struct JoinP {
     int shared_units;           // tiles of a shared item
 };
 
+constexpr int MAX_CLUSTER = 8;
 constexpr int JT = 128;  // threads of a joining CTA
 constexpr float LOG2E = 1.4426950408889634f, LN2 = 0.6931471805599453f;
 
@@ -297,22 +298,22 @@ __device__ __forceinline__ void cluster_join(const AttendP& p, float* om, float*
     cl.sync();
     for (int i = rank * AT + (int)threadIdx.x; i < nrows * (D / 4); i += p.cluster * AT) {
         const int r = i / (D / 4), d = (i % (D / 4)) * 4;
-        float4 z[8];
-        float2 a[8];
+        float4 z[MAX_CLUSTER];
+        float2 a[MAX_CLUSTER];
 #pragma unroll
-        for (int c = 0; c < 8; ++c)  // all at once: each is a round trip through the cluster
+        for (int c = 0; c < MAX_CLUSTER; ++c)  // all at once: each is a round trip through the cluster
             if (c < p.cluster) {
                 z[c] = *reinterpret_cast<const float4*>(cl.map_shared_rank(om, c) + r * D + d);
                 a[c] = *reinterpret_cast<const float2*>(cl.map_shared_rank(ml, c) + 2 * r);
             }
         float mm = -INFINITY, ll = 0.f;
 #pragma unroll
-        for (int c = 0; c < 8; ++c)
+        for (int c = 0; c < MAX_CLUSTER; ++c)
             if (c < p.cluster) mm = fmaxf(mm, a[c].x);
         const float ref = mm == -INFINITY ? 0.f : mm;
         float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-        for (int c = 0; c < 8; ++c)
+        for (int c = 0; c < MAX_CLUSTER; ++c)
             if (c < p.cluster) {
                 const float f = ex2(a[c].x - ref);
                 ll += a[c].y * f;
