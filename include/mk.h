@@ -373,7 +373,7 @@ enum mk_dtype { MK_DT_F32 = 0, MK_DT_BF16 = 1, MK_DT_F16 = 2 };
  * k_scale (or v_scale; NULL for MK_KV_BF16). k, v and the strides in bytes
  * are multiples of 8 elements, for mk_pages_attend also of 16 bytes.
  * page_size is a power of two; head_dim a multiple of 8, at most 256; at most
- * 1024 kv heads. Rows of different (page, head, row) must not overlap. */
+ * 65535 kv heads. Rows of different (page, head, row) must not overlap. */
 typedef struct mk_pages {
     void *k, *v;
     float *k_scale, *v_scale;

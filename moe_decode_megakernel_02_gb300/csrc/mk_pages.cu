@@ -14,8 +14,7 @@ int check_pages(const mk_pages* p, const mk_page_table* t) {
         return fail(MK_ERR_INVALID_ARG, "pages: 8-bit formats need k_scale and v_scale, bf16 pages have none");
     if (p->n_pages < 1 || p->n_kv_heads < 1 || p->head_dim < 1 || t->batch < 1 || t->pages_per_seq < 1 || t->stride < 0)
         return fail(MK_ERR_INVALID_ARG, "pages: non-positive dimension");
-    // (1024 heads of 32 lanes: what the copies' division by a multiplication is exact for)
-    if (p->n_kv_heads > 1024 || t->batch > (1 << 20)) return fail(MK_ERR_UNSUPPORTED, "pages: too many heads or sequences");
+    if (p->n_kv_heads > 65535 || t->batch > (1 << 20)) return fail(MK_ERR_UNSUPPORTED, "pages: too many heads or sequences");
     if (p->head_dim % 8 || p->head_dim > 256)
         return fail(MK_ERR_UNSUPPORTED, "pages: head_dim must be a multiple of 8, at most 256");
     if (log2_exact(p->page_size) < 0) return fail(MK_ERR_UNSUPPORTED, "pages: page_size must be a power of two");

@@ -800,7 +800,7 @@ def test_a_shared_prefix_with_fp16_queries(fmt, D):
 # ---------------------------------------------------------------- calls at their limits
 
 @pytest.mark.parametrize("over,code", [
-    (dict(t__table=4098), mk.ERR_INVALID_ARG), (dict(p__n_kv_heads=1025), mk.ERR_UNSUPPORTED),
+    (dict(t__table=4098), mk.ERR_INVALID_ARG), (dict(p__n_kv_heads=65536), mk.ERR_UNSUPPORTED),
     (dict(p__format=mk.KV_INT8, p__k_scale=4097, p__v_scale=4096), mk.ERR_INVALID_ARG),
 ])
 def test_unaligned_tables_and_too_many_heads_are_refused(over, code):
