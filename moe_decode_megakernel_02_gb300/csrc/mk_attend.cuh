@@ -15,9 +15,11 @@
 // warps split a tile's positions WP ways and the item's rows WR ways:
 //   4 x 1, 4 x 2  up to 8, 16 or 32 rows an item, the usual decode and verify
 //                 steps. Bound by the cache's bytes.
-//   2 x 4, 1 x 8  64 or 128 rows: large verify blocks, and the shared prefix,
-//                 where the rows of all sequences stand against one copy of K
-//                 and V. Bound by the tensor cores and what feeds them.
+//   2 x 4, 1 x 8  64 or 128 rows: chunks of prompts, and a shared prefix, where
+//                 the rows of all sequences stand against one copy of K and V;
+//                 only where mk_prefix.cuh has no kernel, or for tiles that not
+//                 every row sees whole. Bound by the tensor cores and what feeds
+//                 them.
 // Warps of the same rows hold maxima, sums and outputs of their own positions,
 // which meet at the item's end.
 //
@@ -29,6 +31,14 @@
 // workspace and a second launch joins them. Small calls, whose time is the
 // latency of launches, give every item a cluster of 1 to 8 CTAs instead, which
 // join through distributed shared memory: one launch, no workspace.
+//
+// Measured, 128-wide heads, 40 query heads on 8: 64 sequences of up to 32768
+// positions, E4M3, 484 us (5.8 TB/s, 87 % of what a copy reaches); 32 such in
+// bf16 389 us (7.0 TB/s); 64 sequences of up to 1024, bf16, 44 us (57 %: the
+// start, the join and the ends of pieces are 10 us of it). 16 query heads on 4:
+// one sequence of 4096 14 us, all latency; 8 sequences of 8192 with 7 new
+// tokens each (28 rows), E4M3 and capped scores, 37 us (12 %): issue and
+// latency of the conversions, exponentials and shuffles of 4 times the rows.
 //
 // Rounding. Scores and sums are 32-bit. bf16 pages: queries are exact in bf16
 // (16-bit floats: hi + lo parts), probabilities go in as hi + lo bf16 parts,
@@ -992,8 +1002,9 @@ __global__ void __launch_bounds__(32 * WP * WR, Shape<D, FMT, SPLITQ, WP, WR, RN
 
 // Joins the pieces of one output row: a block a row, a warp every fourth
 // piece. Rows whose only piece went straight to the output are left alone;
-// rows without any piece get their zeros here. Reads the pieces from L2: a few
-// microseconds of latency.
+// rows without any piece get their zeros here. Reads the pieces from L2: 3 us
+// (16 rows) to 6 us (896 rows) of latency, most of it the launch, the lookup of
+// the row's pieces and one trip to L2 each.
 template <int D>
 __global__ void __launch_bounds__(JT) join_kernel(const __grid_constant__ JoinP jp) {
     constexpr int E = D / 32;

@@ -1,8 +1,11 @@
-// mk_prefix.cuh -- attention of a whole batch over positions that all its
-// sequences share, on the fifth-generation tensor cores.
+// mk_prefix.cuh -- attention over positions that all rows of an item see, on
+// the fifth-generation tensor cores: a prefix that the sequences of a batch
+// share (rows of the whole batch), or, in calls with many rows a sequence, the
+// tiles that all of its tokens see whole. Everything that is masked for some
+// row stays with mk_attend.cuh, so that no row here sees a part of a tile.
 //
-// The rows of a kv head (every sequence's tokens and query heads of the group)
-// stand against one copy of K and V, 128 rows a CTA, 64 positions a tile:
+// The rows of a kv head (tokens and query heads of the group) stand against
+// one copy of K and V, 128 rows a CTA, 64 positions a tile:
 //   S = Q K^T   128 x 64, both operands in shared memory, S in tensor memory;
 //   P = 2^(x - m) per row, one thread a row (tensor memory gives a thread its
 //       row, so that no value crosses threads);
@@ -19,16 +22,25 @@
 // piece's end. Then loads (bf16 pages: one warp, by tensor maps; 8-bit pages:
 // four warps, which turn staged codes into bf16 -- E4M3 and INT8 codes are
 // exact in it; the K scale multiplies the score, the V scale the probability)
-// and two warps, an elected thread of which issues Q K^T, and P V, S of the next tile before P V of this one, so that the
-// tensor cores work while the softmax does. All waits are on mbarriers with a
-// limit; a wait that runs out raises a flag that every role sees, and the CTA
-// leaves after freeing its tensor memory (MK_ERR_TIMEOUT in `status`).
+// and two warps, an elected thread of each issuing Q K^T and P V; S of the next
+// tile comes before P V of this one, so that the tensor cores work while the
+// softmax does. fp16 queries are two bf16 parts, one more chain of Q K^T. All
+// waits are on mbarriers with a limit; a wait that runs out raises a flag that
+// every role sees, and the CTA leaves after freeing its tensor memory
+// (MK_ERR_TIMEOUT in `status`).
 //
 // Bound by the products: Q K^T of 128 x 64 takes 48 cycles a 16-wide step (its
 // operands' shared-memory reads), the two chains of P V 64 each, 875 cycles a
 // tile of 128-wide heads (measured with nothing else running); 8192
-// exponentials at 16 a cycle are 512. Work is cut as in mk_attend.cuh;
-// every piece goes to the workspace for the joining launch.
+// exponentials at 16 a cycle are 512. 8-bit pages: bound by the four warps that
+// convert, about 2300 cycles a tile. Work is cut as in mk_attend.cuh; every
+// piece goes to the workspace for the joining launch.
+//
+// Measured, 64 sequences on 16384 shared positions, 40 query heads on 8 of 128,
+// bf16: 43 us for this launch (0.75 PFLOP/s with both parts of P counted, 39 %
+// of a large product's rate), 88 us for the call with up to 1024 positions of each
+// sequence's own; INT8 116 us, fp16 queries 94 us. 256 tokens at 16384 positions
+// of one sequence, 16 query heads on 4: 90 us.
 #pragma once
 #include <cuda.h>
 

@@ -32,6 +32,13 @@
 // shared memory. A meeting (write to the others, cluster barrier) costs about
 // 2500 cycles, as much as a pass: a row takes 2 (no filter), 3 (top-k) or 4
 // (top-p) of them, and every CTA works out what it can by itself.
+//
+// Measured: one fp32 row of 32000 with all filters 9.7 us, the latency of its
+// passes and meetings; 32 fp32 rows of 64000 with top-p 31 us; 256 bf16 rows
+// of 151936, each with its own settings, 125 us (0.62 TB/s, 9 % of a copy's
+// rate): bound by instructions, most of all the exponentials and sums of the
+// 50 % of tokens that top-p's bound (1 - p) sum / V leaves in a normal row, in
+// two passes (34,000 and 27,000 of a row's 75,000 cycles).
 #include <cooperative_groups.h>
 
 #include <atomic>
@@ -918,7 +925,10 @@ extern "C" int mk_sample(const mk_sampling* a, void* stream) {
     p.tokens = a->tokens, p.probs = a->probs, p.kept = a->kept;
     p.V = a->vocab;
     // a slice of 2048 tokens keeps a CTA's threads busy with 4 each; where the
-    // rows fill the device anyway, larger slices that still leave two CTAs an SM
+    // rows fill the device anyway, larger slices that still leave two CTAs an SM:
+    // 256 bf16 rows of 151936 take 133 us so, 159 with 8 CTAs a row and 160 with
+    // slices that leave one CTA an SM; 200 fp32 rows of 8000 take 25 and, with
+    // 4 CTAs a row, 39
     int C = MAXC;
     while (C > 1 && a->vocab <= 2048 * (C / 2)) C /= 2;
     while (C > 1 && a->rows * (C / 2) >= 304 && ((int64_t)a->vocab * e + C / 2 - 1) / (C / 2) <= 78 * 1024) C /= 2;

@@ -3,7 +3,8 @@
 Binding of mk_pages_write, mk_pages_read and mk_pages_attend (include/mk.h).
 The cache, its block table and everything else are the caller's own tensors;
 a `Pages` only describes them. Calls run on the current stream (or `stream`)
-of the cache's device and may be captured into a CUDA graph.
+of the cache's device and may be captured into a CUDA graph; they record no
+gradients.
 
     k = torch.empty(n_pages, n_kv_heads, page_size, head_dim, dtype=torch.float8_e4m3fn, device="cuda")
     cache = Pages(k, torch.empty_like(k), k_scale, v_scale)   # scales: float32 [n_pages, n_kv_heads, page_size]
