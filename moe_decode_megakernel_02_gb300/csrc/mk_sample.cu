@@ -35,10 +35,12 @@
 //
 // Measured: one fp32 row of 32000 with all filters 9.7 us, the latency of its
 // passes and meetings; 32 fp32 rows of 64000 with top-p 31 us; 256 bf16 rows
-// of 151936, each with its own settings, 125 us (0.62 TB/s, 9 % of a copy's
-// rate): bound by instructions, most of all the exponentials and sums of the
-// 50 % of tokens that top-p's bound (1 - p) sum / V leaves in a normal row, in
-// two passes (34,000 and 27,000 of a row's 75,000 cycles).
+// of 151936, each with its own settings, 99 us (0.78 TB/s, 12 % of a copy's
+// rate), with top-p on most rows 207. Bound by top-p's two passes over the half
+// of a normal row's tokens that its bound (1 - p) sum / V leaves (34,000 and
+// 27,000 of a row's 75,000 cycles: four shared-memory atomics and an exponential
+// a token), and by the meetings, in which a CTA's warps wait (a scheduler issues
+// in 44 % of its cycles).
 #include <cooperative_groups.h>
 
 #include <atomic>
@@ -70,6 +72,7 @@ struct SampleP {
     float* probs;
     int* kept;
     int V, slice;
+    int rows, order;  // order: the costly rows go first
 };
 
 // Written by one CTA for another only where it says so; each such place is
@@ -93,6 +96,7 @@ struct Shared {
     u64 cross_before, last;
     unsigned cross_bin, cross_count, cross_ahead;
     unsigned argmax, list_n, own_n, own_base;
+    int row;
     unsigned my_top, my_low, my_low_max, my_bad, my_kept;
 };
 
@@ -277,6 +281,34 @@ __device__ void order_list(u64* v, int n) {
         sort_list(v, n, 2 * ST);
 }
 
+// Row number i of the order in which rows are taken: those that need top-p's
+// pass over the whole row first, each kind by index, so that none of them (2.5
+// times the others' time) begins when the rest is done. Every CTA works it out
+// by itself, from all rows' settings.
+__device__ int row_in_order(const SampleP& p, Shared& sh, int i) {
+    auto costly = [&](int r) {
+        const float T = p.temperature ? p.temperature[r] : 1.0f;
+        const int k = p.top_k ? p.top_k[r] : 0;
+        return T > 0.0f && p.top_p[r] < 1.0f && (k <= 0 || k > LIST);
+    };
+    int n = 0;
+    for (int r0 = 0; r0 < p.rows; r0 += ST) n += __syncthreads_count(r0 + (int)threadIdx.x < p.rows && costly(r0 + (int)threadIdx.x));
+    const bool want = i < n;
+    int left = want ? i : i - n;  // rows of the kind before the one looked for
+    if (threadIdx.x == 0) sh.row = i;
+    for (int r0 = 0; r0 < p.rows; r0 += ST) {
+        const int r = r0 + (int)threadIdx.x;
+        const bool one = r < p.rows && costly(r) == want;
+        u64 all;
+        const u64 before = block_excl(one, sh.warp_sum, all);
+        if (one && before == (u64)left) sh.row = r;
+        if ((u64)left < all) break;
+        left -= (int)all;
+    }
+    __syncthreads();
+    return sh.row;
+}
+
 // Bound: one read of the logits from HBM, then passes over shared memory of 4
 // to 25 operations a token (the largest: summing all weights). Small calls are
 // the latency of the cluster's meetings.
@@ -289,7 +321,7 @@ __global__ void __launch_bounds__(ST, 2) sample_kernel(const SampleP p) {
     uint4* const xs = reinterpret_cast<uint4*>(smem + (sizeof(Shared) + 15) / 16 * 16);
     cg::cluster_group cl = cg::this_cluster();
     const int C = (int)cl.num_blocks(), rank = (int)cl.block_rank();
-    const long long row = blockIdx.x / C;
+    const long long row = p.order ? row_in_order(p, sh, blockIdx.x / C) : blockIdx.x / C;
     const int i0 = min(p.V, rank * p.slice), n = min(p.V, i0 + p.slice) - i0;
     const int nv = (n + E - 1) / E;  // vectors of the slice
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -933,6 +965,13 @@ extern "C" int mk_sample(const mk_sampling* a, void* stream) {
     while (C > 1 && a->vocab <= 2048 * (C / 2)) C /= 2;
     while (C > 1 && a->rows * (C / 2) >= 304 && ((int64_t)a->vocab * e + C / 2 - 1) / (C / 2) <= 78 * 1024) C /= 2;
     p.slice = ((a->vocab + C - 1) / C + 7) / 8 * 8;  // whole 16-byte vectors
+    // More rows than run at once: in the order of their cost. 256 bf16 rows of
+    // 151936, an eighth of them costly, take 99 us so and 125 in the order they
+    // come; where all cost the same 86 and 82, and 200 fp32 rows of 8000, whose
+    // slices of 16 KB are quickly done, 27 and 25. With more waves of rows the
+    // last one counts for less.
+    p.rows = a->rows;
+    p.order = a->top_p && (int64_t)a->rows * C > 304 && a->rows <= 4 * ST && p.slice * e >= 32768;
     auto kern = a->dtype == MK_DT_F32    ? sample_kernel<MK_DT_F32>
                 : a->dtype == MK_DT_BF16 ? sample_kernel<MK_DT_BF16>
                                          : sample_kernel<MK_DT_F16>;

@@ -333,3 +333,22 @@ def test_two_calls_at_once_and_replayed():
     want = [sampling.sample(src, u, return_details=True, **kw) for src in (x, y) for kw in kinds]
     for got, w in zip(outs, want):
         assert all(torch.equal(a, b) for a, b in zip(got, w))
+
+
+@gpu
+@pytest.mark.parametrize("R", [330, 2048, 2049])
+def test_many_rows_give_what_few_do(R):
+    """More rows than run at once are taken in another order: every row's result is that of a call of its own size."""
+    V = 8200
+    g = torch.Generator(device="cuda").manual_seed(R)
+    x = torch.randn((R, V), generator=g, device="cuda") * 3
+    u = torch.rand((R,), generator=g, device="cuda")
+    T, k, p, least = settings(R, g)
+    cases = ((T, k, p, least), (None, None, p, None), (None, None, torch.ones_like(p), None))
+    for T, k, p, least in cases:
+        got = sampling.sample(x, u, temperature=T, top_k=k, top_p=p, min_p=least, return_details=True)
+        for r in range(0, R, 100):
+            cut = lambda v: None if v is None else v[r:r + 100]  # noqa: E731
+            want = sampling.sample(x[r:r + 100], cut(u), temperature=cut(T), top_k=cut(k), top_p=cut(p), min_p=cut(least),
+                                   return_details=True)
+            assert all(torch.equal(a[r:r + 100], b) for a, b in zip(got, want))
