@@ -22,9 +22,9 @@ constexpr int CLUSTER_TILES = 8;
 // tokens all see whole go to the tensor memory's kernel, the rest and the join
 // being worth some 10 us. Measured without and with it, 16 query heads on 4 kv
 // heads of 128, bf16: 8 sequences of 8192 positions, 28 rows 37 and 43 us, 128
-// rows 88 and 75; 16 sequences of 16384, 28 rows 118 and 107, 56 rows 190 and
-// 121; 256 tokens at 16384 217 and 90. 8-bit pages: 128 rows 96 and 87, 256
-// tokens 242 and 134, but 28 rows at 65536 191 and 265: their conversion costs
+// rows 88 and 71; 16 sequences of 16384, 28 rows 118 and 107, 56 rows 190 and
+// 117; 256 tokens at 16384 217 and 83. 8-bit pages: 128 rows 96 and 80, 256
+// tokens 242 and 125, but 28 rows at 65536 191 and 265: their conversion costs
 // the same for fewer rows.
 constexpr int64_t WIDE_WORK = 2000;
 
@@ -227,6 +227,8 @@ extern "C" int mk_pages_attend(const mk_attention* a, void* workspace, int64_t w
     p.cluster = pl.cluster;
     if (const int rc = fn(pl.own_k, &p, nullptr, pl.own_grid, pl.sh_grid > 0, s)) return rc;
     if (pl.cluster) return MK_OK;
-    const unsigned rows = (unsigned)((int64_t)p.B * p.T * a->n_q_heads);
-    return D == 64 ? join_64(j, rows, s) : D == 128 ? join_128(j, rows, s) : join_256(j, rows, s);
+    j.rows = (unsigned)((int64_t)p.B * p.T * a->n_q_heads);
+    j.pieces = pl.own_grid / (p.B * p.H * pl.own_rb) + 1;
+    if (pl.sh_grid) j.pieces += pl.sh_grid / (p.H * pl.sh_rb * (pl.wide ? p.B : 1)) + 1;
+    return D == 64 ? join_64(j, s) : D == 128 ? join_128(j, s) : join_256(j, s);
 }

@@ -33,8 +33,8 @@
 // join through distributed shared memory: one launch, no workspace.
 //
 // Measured, 128-wide heads, 40 query heads on 8: 64 sequences of up to 32768
-// positions, E4M3, 484 us (5.8 TB/s, 87 % of what a copy reaches); 32 such in
-// bf16 389 us (7.0 TB/s); 64 sequences of up to 1024, bf16, 44 us (57 %: the
+// positions, E4M3, 483 us (5.8 TB/s, 87 % of what a copy reaches); 32 such in
+// bf16 392 us (6.9 TB/s); 64 sequences of up to 1024, bf16, 43 us (59 %: the
 // start, the join and the ends of pieces are 10 us of it). 16 query heads on 4:
 // one sequence of 4096 14 us, all latency; 8 sequences of 8192 with 7 new
 // tokens each (28 rows), E4M3 and capped scores, 37 us (12 %): issue and
@@ -93,6 +93,8 @@ struct JoinP {
     int own_grid, shared_grid;  // CTAs; shared_grid 0: no shared part
     int own_rows, shared_rows;  // rows of a row block
     int shared_units;           // tiles of a shared item
+    unsigned rows;              // output rows
+    int pieces;                 // of a row, about
 };
 
 constexpr int MAX_CLUSTER = 8;
@@ -1000,20 +1002,23 @@ __global__ void __launch_bounds__(32 * WP * WR, Shape<D, FMT, SPLITQ, WP, WR, RN
     asm volatile("griddepcontrol.wait;" ::: "memory");
 }
 
-// Joins the pieces of one output row: a block a row, a warp every fourth
-// piece. Rows whose only piece went straight to the output are left alone;
+// Joins the pieces of one output row: a warp a row (W = 1), or four that take
+// every fourth piece each (W = 4: many pieces, whose trips to L2 would follow
+// one another). Rows whose only piece went straight to the output are left alone;
 // rows without any piece get their zeros here. Reads the pieces from L2: 3 us
 // (16 rows) to 6 us (896 rows) of latency, most of it the launch, the lookup of
 // the row's pieces and one trip to L2 each.
-template <int D>
+template <int D, int W>
 __global__ void __launch_bounds__(JT) join_kernel(const __grid_constant__ JoinP jp) {
-    constexpr int E = D / 32;
-    __shared__ float om[4][D];
-    __shared__ float2 oml[4];
+    constexpr int E = D / 32, AHEAD = W == 1 ? (D == 256 ? 4 : 8) : 4;
+    __shared__ float om[W][D];
+    __shared__ float2 oml[W];
     const AttendP& p = jp.own;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, Hq = p.H * p.G;
+    const int warp = W == 1 ? 0 : threadIdx.x >> 5, lane = threadIdx.x & 31, Hq = p.H * p.G;
+    const unsigned orow = W == 1 ? blockIdx.x * (JT / 32) + (threadIdx.x >> 5) : blockIdx.x;
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    const int bt = blockIdx.x / Hq, hq = blockIdx.x - bt * Hq;
+    if (orow >= jp.rows) return;
+    const int bt = orow / Hq, hq = orow - bt * Hq;
     const int b = bt / p.T, t = bt - b * p.T, h = hq / p.G, g = hq - h * p.G;
 
     // pieces of a launch: CTAs c0 .. c1, the row's place in a slot
@@ -1048,8 +1053,8 @@ __global__ void __launch_bounds__(JT) join_kernel(const __grid_constant__ JoinP 
 #pragma unroll
     for (int i = 0; i < E; ++i) o[i] = 0.f;
     auto add = [&](const Part& x) {
-#pragma unroll 4
-        for (int c = x.c0 + warp; c <= x.c1; c += 4) {
+#pragma unroll AHEAD
+        for (int c = x.c0 + warp; c <= x.c1; c += W) {
             const long long slot = x.c0 == x.c1 ? x.whole_slot : 2 * c + (x.first <= c * x.per ? 0 : 1);
             const float* s = x.slots + slot * x.floats;
             const float2 ml = *reinterpret_cast<const float2*>(s + (long long)x.rows * D + 2 * x.row);
@@ -1078,23 +1083,44 @@ __global__ void __launch_bounds__(JT) join_kernel(const __grid_constant__ JoinP 
         else if (const int n = (a.base[b + 1] - a.base[b]) / (a.H * a.RB))
             add(part(a, jp.shared_grid, jp.shared_rows, a.base[b], a.base[a.B], n, b, t * p.G + g));
     }
+    uint16_t* dst = p.out + b * p.ob + t * p.ot + hq * p.oh;
+    if constexpr (W == 1) {
+        const bool none = l == 0.f;
+        uint16_t z[E];
+#pragma unroll
+        for (int i = 0; i < E; ++i) {
+            const float y = none ? 0.f : o[i] / l;
+            z[i] = p.f16 ? __half_as_ushort(__float2half_rn(y)) : __bfloat16_as_ushort(__float2bfloat16_rn(y));
+        }
+        if (((uintptr_t)dst & 3) == 0) {
+#pragma unroll
+            for (int i = 0; i < E; i += 2)
+                *reinterpret_cast<uint32_t*>(dst + lane * E + i) = z[i] | (uint32_t)z[i + 1] << 16;
+        } else {
+#pragma unroll
+            for (int i = 0; i < E; ++i) dst[lane * E + i] = z[i];
+        }
+        if (lane == 0 && p.lse) p.lse[(long long)orow] = none ? -INFINITY : (m + log2f(l)) * LN2;
+        return;
+    }
 #pragma unroll
     for (int i = 0; i < E; ++i) om[warp][lane * E + i] = o[i];
     if (lane == 0) oml[warp] = make_float2(m, l);
     __syncthreads();
-    float mm = -INFINITY, ll = 0.f, w[4];
+    float mm = -INFINITY, ll = 0.f, w[W];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) mm = fmaxf(mm, oml[i].x);
+    for (int i = 0; i < W; ++i) mm = fmaxf(mm, oml[i].x);
     const float ref = mm == -INFINITY ? 0.f : mm;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < W; ++i) {
         w[i] = ex2(oml[i].x - ref);
         ll += oml[i].y * w[i];
     }
     const bool none = ll == 0.f;
-    uint16_t* dst = p.out + b * p.ob + t * p.ot + hq * p.oh;
     for (int d = threadIdx.x; d < D; d += JT) {
-        const float y = om[0][d] * w[0] + om[1][d] * w[1] + om[2][d] * w[2] + om[3][d] * w[3];
+        float y = 0.f;
+#pragma unroll
+        for (int i = 0; i < W; ++i) y += om[i][d] * w[i];
         const float z = none ? 0.f : y / ll;
         dst[d] = p.f16 ? __half_as_ushort(__float2half_rn(z)) : __bfloat16_as_ushort(__float2bfloat16_rn(z));
     }
@@ -1173,9 +1199,14 @@ int attend_d(const Kind& k, const AttendP* p, KindInfo* info, int grid, bool aft
     return attend_pick<D, MK_KV_BF16, false>(k, p, info, grid, after, s);
 }
 template <int D>
-int join_d(const JoinP& j, unsigned rows, cudaStream_t s) {
+int join_d(const JoinP& j, cudaStream_t s) {
+    // A warp a row where the pieces are few, or the rows so many that the instructions of four warps count more than
+    // trips to L2 in turn. Four and one, whole calls: 64 sequences of 1024 positions (40 query heads on 8, 2 pieces)
+    // 44.5 and 42.4 us, 256 tokens at 16384 (4096 rows, some 20 pieces) 90.9 and 85.1; 8 x 7 tokens at 8192 (896 rows,
+    // 15 pieces) 37.3 and 42.0, 16 x 4 at 4096 (1024 rows, 8 pieces) 31.3 and 33.2.
+    const bool one = j.pieces <= 4 || (j.rows >= 2048 && j.pieces <= 32);
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(rows);
+    cfg.gridDim = dim3(one ? (j.rows + JT / 32 - 1) / (JT / 32) : j.rows);
     cfg.blockDim = dim3(JT);
     cfg.stream = s;
     cudaLaunchAttribute at[1];
@@ -1183,7 +1214,8 @@ int join_d(const JoinP& j, unsigned rows, cudaStream_t s) {
     at[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = at;
     cfg.numAttrs = 1;
-    return cuda_status(cudaLaunchKernelEx(&cfg, join_kernel<D>, j), "mk_pages_attend");
+    return cuda_status(one ? cudaLaunchKernelEx(&cfg, join_kernel<D, 1>, j) : cudaLaunchKernelEx(&cfg, join_kernel<D, 4>, j),
+                       "mk_pages_attend");
 }
 
 // one translation unit a head_dim
@@ -1195,8 +1227,8 @@ int attend_256(const Kind&, const AttendP*, KindInfo*, int, bool, cudaStream_t);
 // rows an item, one CTA an SM. p NULL: one-time attributes.
 int prefix_bf16(int head_dim, int format, const AttendP* p, int grid, cudaStream_t s);
 int prefix_f16(int head_dim, int format, const AttendP* p, int grid, cudaStream_t s);
-int join_64(const JoinP&, unsigned, cudaStream_t);
-int join_128(const JoinP&, unsigned, cudaStream_t);
-int join_256(const JoinP&, unsigned, cudaStream_t);
+int join_64(const JoinP&, cudaStream_t);
+int join_128(const JoinP&, cudaStream_t);
+int join_256(const JoinP&, cudaStream_t);
 
 }  // namespace mkop

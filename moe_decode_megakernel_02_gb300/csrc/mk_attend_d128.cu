@@ -5,5 +5,5 @@ namespace mkop {
 int attend_128(const Kind& k, const AttendP* p, KindInfo* info, int grid, bool after, cudaStream_t s) {
     return attend_d<128>(k, p, info, grid, after, s);
 }
-int join_128(const JoinP& j, unsigned rows, cudaStream_t s) { return join_d<128>(j, rows, s); }
+int join_128(const JoinP& j, cudaStream_t s) { return join_d<128>(j, s); }
 }  // namespace mkop

@@ -5,5 +5,5 @@ namespace mkop {
 int attend_256(const Kind& k, const AttendP* p, KindInfo* info, int grid, bool after, cudaStream_t s) {
     return attend_d<256>(k, p, info, grid, after, s);
 }
-int join_256(const JoinP& j, unsigned rows, cudaStream_t s) { return join_d<256>(j, rows, s); }
+int join_256(const JoinP& j, cudaStream_t s) { return join_d<256>(j, s); }
 }  // namespace mkop

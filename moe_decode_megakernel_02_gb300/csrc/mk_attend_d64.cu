@@ -5,5 +5,5 @@ namespace mkop {
 int attend_64(const Kind& k, const AttendP* p, KindInfo* info, int grid, bool after, cudaStream_t s) {
     return attend_d<64>(k, p, info, grid, after, s);
 }
-int join_64(const JoinP& j, unsigned rows, cudaStream_t s) { return join_d<64>(j, rows, s); }
+int join_64(const JoinP& j, cudaStream_t s) { return join_d<64>(j, s); }
 }  // namespace mkop

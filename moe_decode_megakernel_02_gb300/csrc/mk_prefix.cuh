@@ -40,7 +40,7 @@
 // bf16: 43 us for this launch (0.75 PFLOP/s with both parts of P counted, 39 %
 // of a large product's rate), 88 us for the call with up to 1024 positions of each
 // sequence's own; INT8 116 us, fp16 queries 94 us. 256 tokens at 16384 positions
-// of one sequence, 16 query heads on 4: 90 us.
+// of one sequence, 16 query heads on 4: 83 us.
 #pragma once
 #include <cuda.h>
 
