@@ -142,8 +142,9 @@ class Pages:
 
     def write(self, table, positions, k, v, counts=None, status=None, stream=None):
         """Rows t < counts[b] (all, without counts) of k and v, [batch, tokens, n_kv_heads, head_dim], to positions
-        positions[b] + t: 8-bit pages get codes and a scale a row. positions, counts: int32 [batch]. A position or
-        page out of range is skipped and sets status[0] (int32 [1]) to MK_ERR_INVALID_ARG."""
+        positions[b] + t, which must be distinct rows of the cache: 8-bit pages get codes and a scale a row.
+        positions, counts: int32 [batch]. A position or page out of range is skipped and sets status[0] (int32 [1]) to
+        MK_ERR_INVALID_ARG."""
         self._copy(lib().mk_pages_write, table, positions, k, v, counts, status, stream)
 
     def read(self, table, positions, k, v, counts=None, status=None, stream=None):
