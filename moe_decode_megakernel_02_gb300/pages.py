@@ -47,7 +47,7 @@ def _launch(device, stream, call, args):
 
 
 def _copy_call(h, fn, pages, packed, pos, cnt, n, st):
-    buf = ctypes.create_string_buffer(packed, len(packed))
+    buf = _CopyBytes.from_buffer_copy(packed)
     at = ctypes.addressof(buf)
     rc = fn(pages, at, pos, cnt, n, at + 24, at + 64, st, h)
     if rc:
@@ -55,9 +55,7 @@ def _copy_call(h, fn, pages, packed, pos, cnt, n, st):
 
 
 def _ptr(x, name, shape, dtype, device):
-    """data_ptr of an optional contiguous argument after its checks."""
-    if x is None:
-        return 0
+    """data_ptr of a contiguous argument after its checks."""
     if x.dtype is not dtype or x.shape != shape or x.device != device or not x.is_contiguous():
         raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)} on {device}, got "
                          f"{x.dtype} {tuple(x.shape)} on {x.device}")
@@ -79,6 +77,7 @@ def _rows(x, name, device):
 # A call's structures side by side in one buffer: (mk_attention,) mk_page_table, mk_rows, mk_rows
 _COPY = struct.Struct("Pqii Pqqqii Pqqqii")
 _ATTEND = struct.Struct("PP PPP PP PP ii ff ii Pqii Pqqqii Pqqqii")
+_CopyBytes, _AttendBytes = ctypes.c_char * _COPY.size, ctypes.c_char * _ATTEND.size
 assert _COPY.size == 24 + 2 * 40 and _ATTEND.size == 96 + _COPY.size and ctypes.sizeof(AttentionStruct) == 96
 
 
@@ -118,10 +117,11 @@ class Pages:
         self._at = ctypes.addressof(self._s)
 
     def _table(self, table):
-        if table.dtype != torch.int32 or table.dim() != 2 or table.device != self.device or table.stride(1) != 1:
+        s, shape = table.stride(), table.shape
+        if table.dtype is not torch.int32 or len(s) != 2 or s[1] != 1 or table.device != self.device:
             raise ValueError(f"table must be an int32 tensor [batch, pages per sequence] on {self.device} with a "
                              f"contiguous last dimension, got {table.dtype} {tuple(table.shape)} on {table.device}")
-        return table.data_ptr(), table.stride(0), table.shape[0], table.shape[1]
+        return table.data_ptr(), s[0], shape[0], shape[1]
 
     def _copy(self, fn, table, positions, k, v, counts, status, stream):
         dev, t = self.device, self._table(table)
@@ -133,8 +133,8 @@ class Pages:
         if positions is None:
             raise ValueError("positions is required")
         pos = _ptr(positions, "positions", shape[:1], torch.int32, dev)
-        cnt = _ptr(counts, "counts", shape[:1], torch.int32, dev)
-        st = _ptr(status, "status", _ONE, torch.int32, dev)
+        cnt = 0 if counts is None else _ptr(counts, "counts", shape[:1], torch.int32, dev)
+        st = 0 if status is None else _ptr(status, "status", _ONE, torch.int32, dev)
         n = shape[1]
         if shape[0] == 0 or n == 0:
             return
@@ -174,9 +174,9 @@ class Pages:
             raise ValueError("lens is required")
         batch = shape[:1]
         n = _ptr(lens, "lens", batch, torch.int32, dev)
-        first = _ptr(starts, "starts", batch, torch.int32, dev)
-        sl = _ptr(slopes, "slopes", shape[2:3], torch.float32, dev)
-        st = _ptr(status, "status", _ONE, torch.int32, dev)
+        first = 0 if starts is None else _ptr(starts, "starts", batch, torch.int32, dev)
+        sl = 0 if slopes is None else _ptr(slopes, "slopes", shape[2:3], torch.float32, dev)
+        st = 0 if status is None else _ptr(status, "status", _ONE, torch.int32, dev)
         if out is not None and (out.dtype is not q.dtype or out.shape != shape):
             raise ValueError(f"out must have q's type and shape, {q.dtype} {tuple(shape)}")
         if scale is None:
@@ -192,9 +192,9 @@ class Pages:
             ro = (out.data_ptr(), T * Hq * D, Hq * D, D, rq[4], 0)
         else:
             ro = _rows(out, "out", dev)
-        lse = torch.empty((B, T, Hq), dtype=torch.float32, device=dev) if return_lse else None
+        lse = torch.empty(shape[:3], dtype=torch.float32, device=dev) if return_lse else None
         if B and T:
-            buf = ctypes.create_string_buffer(_ATTEND.size)
+            buf = _AttendBytes()
             at = ctypes.addressof(buf)
             try:
                 _ATTEND.pack_into(buf, 0, self._at, at + 96, n, first, sl, at + 120, at + 160,

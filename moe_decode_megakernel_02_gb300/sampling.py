@@ -34,10 +34,13 @@ def sample(logits, u, temperature=None, top_k=None, top_p=None, min_p=None, out=
     dev, n = logits.device, logits.shape[:1]
     if u is None:
         raise ValueError("u is required")
-    args = (_ptr(u, "u", n, torch.float32, dev), _ptr(temperature, "temperature", n, torch.float32, dev),
-            _ptr(top_k, "top_k", n, torch.int32, dev), _ptr(top_p, "top_p", n, torch.float32, dev),
-            _ptr(min_p, "min_p", n, torch.float32, dev))
-    _ptr(out, "out", n, torch.int32, dev)
+    args = (_ptr(u, "u", n, torch.float32, dev),
+            0 if temperature is None else _ptr(temperature, "temperature", n, torch.float32, dev),
+            0 if top_k is None else _ptr(top_k, "top_k", n, torch.int32, dev),
+            0 if top_p is None else _ptr(top_p, "top_p", n, torch.float32, dev),
+            0 if min_p is None else _ptr(min_p, "min_p", n, torch.float32, dev))
+    if out is not None:
+        _ptr(out, "out", n, torch.int32, dev)
     return _launch(dev, stream, _sample, (logits, args, out, return_details, n, R, V, dt))
 
 
