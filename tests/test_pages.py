@@ -926,3 +926,45 @@ def test_a_prompt_then_steps_then_tokens(fmt):
         assert int(tokens[0]) == int(logits[0].argmax()) and bool(((tokens >= 0) & (tokens < V)).all())
         top = logits[1].sort(descending=True).indices[:20]
         assert int(tokens[1]) in top.tolist()
+
+
+@gpu
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("ps", [1, 4, 8, 128, 1024])
+def test_page_sizes_of_shared_and_wide_calls(fmt, ps):
+    """Pages smaller and larger than a tile, and ones too small for the tensor maps."""
+    B, Hq, H, D = 5, 16, 2, 128
+    shared = max(ps, 192 // ps * ps)
+    lens = [shared + 40 * b + 1 for b in range(B)]
+    cache, table, n, q = build(fmt, torch.bfloat16, B, 1, Hq, H, D, ps, lens, shared=shared)
+    out, lse = cache.attend(table, n, q, shared_len=shared, return_lse=True)
+    check(cache, table, n, q, out, lse, 1 / math.sqrt(D))
+    T = 5  # 40 rows
+    cache, table, n, q = build(fmt, torch.bfloat16, B, T, Hq, H, D, ps, [50, 700, 5, 64, 1100])
+    table = widen(table, Hq, H, T, ps)
+    out, lse = cache.attend(table, n, q, return_lse=True)
+    check(cache, table, n, q, out, lse, 1 / math.sqrt(D))
+
+
+@gpu
+@pytest.mark.parametrize("fmt", FORMATS)
+def test_wide_and_shared_calls_past_32_bit_offsets(fmt):
+    """Pages whose bytes lie more than 2^32 after the cache's first."""
+    H, D, ps = 2, 128, 64
+    row = H * ps * D * (2 if fmt == torch.bfloat16 else 1)
+    n_pages = (1 << 32) // row + 40
+    k, v = (torch.zeros((n_pages, H, ps, D), dtype=torch.int8 if fmt == torch.float8_e4m3fn else fmt, device="cuda")
+            for _ in range(2))
+    ks, vs = (None, None) if fmt == torch.bfloat16 else (torch.ones((n_pages, H, ps), device="cuda") for _ in range(2))
+    cache = pages.Pages(k.view(fmt), v.view(fmt), ks, vs)
+    T, Hq, first = 5, 16, n_pages - 20
+    table = torch.arange(first, first + 16, dtype=torch.int32, device="cuda").view(1, 16)
+    x, y = (torch.randn((1, 16 * ps, H, D), device="cuda").bfloat16() for _ in range(2))
+    cache.write(table, ints(0), x, y)
+    small = pages.Pages(*(c[first:].contiguous() for c in (cache.k, cache.v)),
+                        *(c if c is None else c[first:].contiguous() for c in (ks, vs)))
+    q = torch.randn((1, T, Hq, D), device="cuda").bfloat16()
+    for t, kw in ((widen(table, Hq, H, T, ps), {}), (table, dict(shared_len=512))):
+        t0 = torch.where(t < 0, t, t - first)
+        a = cache.attend(t, ints(1000), q, **kw)
+        assert torch.equal(a, small.attend(t0, ints(1000), q, **kw)) and bool((a != 0).any())
