@@ -709,7 +709,7 @@ __global__ void __launch_bounds__(32 * WP * WR, Shape<D, FMT, SPLITQ, WP, WR, RN
                         x[n][0] *= k0, x[n][1] *= k0;
                         x[n][2] *= k1, x[n][3] *= k1;
                     }
-                    float big = fmaxf(vsc[0], vsc[1]);
+                    float big = fmaxf(fabsf(vsc[0]), fabsf(vsc[1]));  // a scale may have either sign
                     if (__any_sync(0xffffffffu, big > vunit)) {
 #pragma unroll
                         for (int s = 4; s < 32; s <<= 1) big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, s));
