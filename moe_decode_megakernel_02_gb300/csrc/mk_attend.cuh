@@ -626,7 +626,9 @@ __global__ void __launch_bounds__(32 * WP * WR, Shape<D, FMT, SPLITQ, WP, WR, RN
         }
 
         float o[RN][DT][4], m[RN][2], l[RN][2];
-        float vunit = 0.f, vinv = 0.f;  // 8-bit pages: outputs are in units of this power of two / 2^15, and 1 over that
+        // 8-bit pages: a row's output is in units of a power of two, not below any V scale that the row has seen, over
+        // 2^15; this is 1 over that. Each row has its own: a scale that only other rows see costs it no bits.
+        float vinv[RN][2];
 #pragma unroll
         for (int n = 0; n < RN; ++n) {
 #pragma unroll
@@ -635,6 +637,7 @@ __global__ void __launch_bounds__(32 * WP * WR, Shape<D, FMT, SPLITQ, WP, WR, RN
                 for (int e = 0; e < 4; ++e) o[n][i][e] = 0.f;
             m[n][0] = m[n][1] = -INFINITY;
             l[n][0] = l[n][1] = 0.f;
+            vinv[n][0] = vinv[n][1] = 0x1p115f;  // the least unit
         }
 
         for (int tile = 0; tile < take; ++tile) {
@@ -699,8 +702,10 @@ __global__ void __launch_bounds__(32 * WP * WR, Shape<D, FMT, SPLITQ, WP, WR, RN
                     }
                 }
 
-                // ---- 8-bit pages: scales of this thread's two positions
-                float vsc[2] = {1.f, 1.f}, grow = 1.f;
+                // ---- 8-bit pages: scales of this thread's two positions, and each row's unit
+                float vsc[2] = {1.f, 1.f}, grow[RN][2];
+#pragma unroll
+                for (int n = 0; n < RN; ++n) grow[n][0] = grow[n][1] = 1.f;
                 if constexpr (F8) {
                     const float k0 = scales[s0 + g8], k1 = scales[s0 + g8 + 8];
                     vsc[0] = scales[TILE + s0 + g8], vsc[1] = scales[TILE + s0 + g8 + 8];
@@ -709,18 +714,42 @@ __global__ void __launch_bounds__(32 * WP * WR, Shape<D, FMT, SPLITQ, WP, WR, RN
                         x[n][0] *= k0, x[n][1] *= k0;
                         x[n][2] *= k1, x[n][3] *= k1;
                     }
-                    float big = fmaxf(fabsf(vsc[0]), fabsf(vsc[1]));  // a scale may have either sign
-                    if (__any_sync(0xffffffffu, big > vunit)) {
+                    // the largest of the scales (of either sign) that a row sees, against its unit
+                    const float v0 = fabsf(vsc[0]), v1 = fabsf(vsc[1]);
+                    float big[RN][2];
+                    bool above = false;
 #pragma unroll
-                        for (int s = 4; s < 32; s <<= 1) big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, s));
-                        // above `big`, and far enough from 0 for 2^15 over it
-                        const unsigned e = min((__float_as_uint(big) >> 23) + 1, 250u);
-                        const float nu = __uint_as_float(max(e, 27u) << 23);
-                        grow = vunit / nu;
-                        vunit = nu;
-                        vinv = __uint_as_float((2u * 127u + 15u - max(e, 27u)) << 23);
+                    for (int n = 0; n < RN; ++n)
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) big[n][e] = fmaxf(v0, v1);
+                    if (!all_see) {
+                        const int j = j0 + g8;
+#pragma unroll
+                        for (int n = 0; n < RN; ++n)
+#pragma unroll
+                            for (int e = 0; e < 2; ++e)
+                                big[n][e] = fmaxf(j < rlo[n][e] || j >= rhi[n][e] ? 0.f : v0,
+                                                  j + 8 < rlo[n][e] || j + 8 >= rhi[n][e] ? 0.f : v1);
                     }
-                    vsc[0] *= vinv, vsc[1] *= vinv;
+#pragma unroll
+                    for (int n = 0; n < RN; ++n) above |= big[n][0] * vinv[n][0] > 32768.f || big[n][1] * vinv[n][1] > 32768.f;
+                    if (__any_sync(0xffffffffu, above)) {
+#pragma unroll
+                        for (int n = 0; n < RN; ++n)
+#pragma unroll
+                            for (int e = 0; e < 2; ++e) {
+                                float most = big[n][e];
+#pragma unroll
+                                for (int s = 4; s < 32; s <<= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, s));
+                                // a unit above `most`, and far enough from 0 for 2^15 over it
+                                const unsigned ex = min((__float_as_uint(most) >> 23) + 1, 250u);
+                                const float inv = __uint_as_float((2u * 127u + 15u - max(ex, 27u)) << 23);
+                                if (inv < vinv[n][e]) {
+                                    grow[n][e] = inv / vinv[n][e];
+                                    vinv[n][e] = inv;
+                                }
+                            }
+                    }
                 }
 
                 // ---- softmax: x becomes the probabilities
@@ -760,13 +789,13 @@ __global__ void __launch_bounds__(32 * WP * WR, Shape<D, FMT, SPLITQ, WP, WR, RN
                         l[n][e] = l[n][e] * keep + (p0 + p1);
                         x[n][e] = p0, x[n][2 + e] = p1;
                         if constexpr (F8) {
-                            x[n][e] *= vsc[0], x[n][2 + e] *= vsc[1];
+                            x[n][e] *= vsc[0] * vinv[n][e], x[n][2 + e] *= vsc[1] * vinv[n][e];
                             if (!all_see) {  // the scale of a row that is not seen may be anything
                                 if (!(seen >> (n * 4 + e) & 1u)) x[n][e] = 0.f;
                                 if (!(seen >> (n * 4 + e) & 4u)) x[n][2 + e] = 0.f;
                             }
                         }
-                        f[n][e] = keep * grow;
+                        f[n][e] = keep * grow[n][e];
                         turn |= f[n][e] != 1.f;
                     }
                 if (__any_sync(0xffffffffu, turn)) {
@@ -907,7 +936,7 @@ __global__ void __launch_bounds__(32 * WP * WR, Shape<D, FMT, SPLITQ, WP, WR, RN
 #pragma unroll
                 for (int s = 4; s < 32; s <<= 1) l[n][e] += __shfl_xor_sync(0xffffffffu, l[n][e], s);
                 if constexpr (F8) {
-                    const float f = vunit * (1.f / 32768.f);
+                    const float f = __uint_as_float((254u << 23) - __float_as_uint(vinv[n][e]));  // the unit
 #pragma unroll
                     for (int i = 0; i < DT; ++i) o[n][i][e] *= f, o[n][i][2 + e] *= f;
                 }

@@ -53,3 +53,23 @@ def test_scales_of_either_sign(fmt, kind, qdtype):
         out, lse = cache.attend(table, n, q, return_lse=True)
         dv = max(lens) * 2.0 ** -39 * tp.QMAX[fmt] * float(cache.v_scale.abs().max())
         close(cache, table, n, q, out, lse, 1 / math.sqrt(q.shape[-1]), dv + 2.0 ** -24)
+
+
+@gpu
+@pytest.mark.parametrize("fmt", FORMATS[1:])
+@pytest.mark.parametrize("kind", SHAPES)
+@pytest.mark.parametrize("scale", [math.inf, -math.inf, 1e30, 2.0 ** 40, math.nan])
+def test_the_scale_of_a_position_that_is_not_seen_changes_nothing(fmt, kind, scale):
+    """Only the last token sees the last position: the others' outputs stay, bit for bit, whatever its V scale."""
+    for qdtype in (torch.bfloat16, torch.float16):
+        cache, table, n, q, lens, ps = shape_of(kind, fmt, qdtype)
+        clean, clse = cache.attend(table, n, q, return_lse=True)
+        for b, L in enumerate(lens):
+            cache.v_scale[int(table[b, (L - 1) // ps]), :, (L - 1) % ps] = scale
+        out, lse = cache.attend(table, n, q, return_lse=True)
+        assert torch.equal(out[:, :-1], clean[:, :-1]) and torch.equal(lse, clse)
+        if not math.isfinite(scale):
+            assert not bool(torch.isfinite(out[:, -1]).any())
+        elif qdtype == torch.bfloat16:  # the last token sees it: its error is of that scale
+            dv = max(lens) * 2.0 ** -39 * tp.QMAX[fmt] * scale
+            close(cache, table, n, q[:, -1:], out[:, -1:], lse[:, -1:], 1 / math.sqrt(q.shape[-1]), dv)
