@@ -628,7 +628,7 @@ __global__ void __launch_bounds__(32 * WP * WR, Shape<D, FMT, SPLITQ, WP, WR, RN
         float o[RN][DT][4], m[RN][2], l[RN][2];
         // 8-bit pages: a row's output is in units of a power of two, not below any V scale that the row has seen, over
         // 2^15; this is 1 over that. Each row has its own: a scale that only other rows see costs it no bits.
-        float vinv[RN][2];
+        float vinv[RN][2], vtop = 0x1p115f;  // vtop: the largest of the thread's rows'
 #pragma unroll
         for (int n = 0; n < RN; ++n) {
 #pragma unroll
@@ -714,40 +714,28 @@ __global__ void __launch_bounds__(32 * WP * WR, Shape<D, FMT, SPLITQ, WP, WR, RN
                         x[n][0] *= k0, x[n][1] *= k0;
                         x[n][2] *= k1, x[n][3] *= k1;
                     }
-                    // the largest of the scales (of either sign) that a row sees, against its unit
+                    // scales (of either sign) above a row's unit
                     const float v0 = fabsf(vsc[0]), v1 = fabsf(vsc[1]);
-                    float big[RN][2];
-                    bool above = false;
-#pragma unroll
-                    for (int n = 0; n < RN; ++n)
-#pragma unroll
-                        for (int e = 0; e < 2; ++e) big[n][e] = fmaxf(v0, v1);
-                    if (!all_see) {
+                    if (__any_sync(0xffffffffu, fmaxf(v0, v1) * vtop > 32768.f)) {
                         const int j = j0 + g8;
-#pragma unroll
-                        for (int n = 0; n < RN; ++n)
-#pragma unroll
-                            for (int e = 0; e < 2; ++e)
-                                big[n][e] = fmaxf(j < rlo[n][e] || j >= rhi[n][e] ? 0.f : v0,
-                                                  j + 8 < rlo[n][e] || j + 8 >= rhi[n][e] ? 0.f : v1);
-                    }
-#pragma unroll
-                    for (int n = 0; n < RN; ++n) above |= big[n][0] * vinv[n][0] > 32768.f || big[n][1] * vinv[n][1] > 32768.f;
-                    if (__any_sync(0xffffffffu, above)) {
+                        vtop = 0.f;
 #pragma unroll
                         for (int n = 0; n < RN; ++n)
 #pragma unroll
                             for (int e = 0; e < 2; ++e) {
-                                float most = big[n][e];
+                                // the largest that the row sees
+                                float big = fmaxf(!all_see && (j < rlo[n][e] || j >= rhi[n][e]) ? 0.f : v0,
+                                                  !all_see && (j + 8 < rlo[n][e] || j + 8 >= rhi[n][e]) ? 0.f : v1);
 #pragma unroll
-                                for (int s = 4; s < 32; s <<= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, s));
-                                // a unit above `most`, and far enough from 0 for 2^15 over it
-                                const unsigned ex = min((__float_as_uint(most) >> 23) + 1, 250u);
+                                for (int s = 4; s < 32; s <<= 1) big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, s));
+                                // a unit above `big`, and far enough from 0 for 2^15 over it
+                                const unsigned ex = min((__float_as_uint(big) >> 23) + 1, 250u);
                                 const float inv = __uint_as_float((2u * 127u + 15u - max(ex, 27u)) << 23);
                                 if (inv < vinv[n][e]) {
                                     grow[n][e] = inv / vinv[n][e];
                                     vinv[n][e] = inv;
                                 }
+                                vtop = fmaxf(vtop, vinv[n][e]);
                             }
                     }
                 }
