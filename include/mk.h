@@ -431,7 +431,8 @@ int mk_kv_view(const mk_kv* kv, int32_t layer, mk_pages* pages, mk_page_table* t
  * lens[b] counts the cached positions of sequence b, the new ones included
  * (write them first): token t sits at p = lens[b] - n_tokens + t and sees the
  * positions j with starts[b] <= j <= p. With x = scale q.k_j, capped to
- * softcap * tanh(x / softcap) when softcap > 0, less slopes[h] * (p - j):
+ * softcap * tanh(x / softcap) when softcap > 0 (1e-30 to 1e30; its error is
+ * relative, 2^-20 of a score), less slopes[h] * (p - j):
  *   out = sum_j softmax(x)_j v_j,    lse = log sum_j exp(x_j).
  * A token that sees nothing (a padded sequence of length 0, p < 0, a start
  * past p) gets zeros and lse -infinity; values it does not see, NaN and

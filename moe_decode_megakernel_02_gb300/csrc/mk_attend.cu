@@ -92,8 +92,8 @@ int make_plan(const mk_attention* a, Plan& pl) {
         return fail(MK_ERR_INVALID_ARG, "attend: q or out not aligned to its type");
     if (off_by4(a->lens, a->starts, a->slopes, a->lse, a->status))
         return fail(MK_ERR_INVALID_ARG, "attend: lens, starts, slopes, lse or status not aligned to 4 bytes");
-    if (!(a->scale == a->scale) || !(a->softcap >= 0.f) || a->softcap > 1e30f)
-        return fail(MK_ERR_INVALID_ARG, "attend: scale or softcap");
+    if (!(a->scale == a->scale) || !(a->softcap == 0.f || (a->softcap >= 1e-30f && a->softcap <= 1e30f)))
+        return fail(MK_ERR_INVALID_ARG, "attend: scale is NaN, or softcap not 0 and outside 1e-30 .. 1e30");
     const int64_t cap = (int64_t)t.pages_per_seq * g.page_size;
     if (a->shared_len < 0 || a->shared_len % g.page_size || a->shared_len > cap)
         return fail(MK_ERR_INVALID_ARG, "attend: shared_len must be whole pages of the table");

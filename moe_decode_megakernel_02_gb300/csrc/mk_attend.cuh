@@ -214,6 +214,27 @@ __device__ __forceinline__ float rcp(float x) {
     return y;
 }
 
+// Capped scores as exponents of 2, cap log2(e) tanh z, from y = 2 z log2(e).
+// Below |z| = 1/2 y cap/2 times a polynomial in y^2 (Chebyshev interpolation of
+// tanh(sqrt t) / sqrt t on [0, 1/4]: 2^-26 off), so that the error is of the
+// score's size however large the cap is; from there on tanh z = 1 - 2 / (e^2z + 1),
+// whose 2.8 2^-23 of 1 is relative there too. Most scores lie below: a warp
+// whose scores all do skips the exponentials.
+constexpr float CAP_NEAR = 1.44f;  // |y| of |z| a little below 1/2
+__device__ __forceinline__ float cap_near(float y, float half_cap) {
+    const float w = y * y;
+    float p = 3.5657851e-6f;
+    p = __fmaf_rn(p, w, -9.1816237e-5f);
+    p = __fmaf_rn(p, w, 1.9223876e-3f);
+    p = __fmaf_rn(p, w, -4.0037432e-2f);
+    p = __fmaf_rn(p, w, 1.f);
+    return y * half_cap * p;
+}
+__device__ __forceinline__ float cap_any(float y, float cap) {
+    const float c2 = cap * LOG2E;
+    return fabsf(y) < CAP_NEAR ? cap_near(y, 0.5f * cap) : c2 - 2.f * c2 * rcp(ex2(y) + 1.f);
+}
+
 // Four E4M3 codes as two registers of two fp16 values, exact.
 __device__ __forceinline__ void e4m3_quad(uint32_t w, uint32_t& lo, uint32_t& hi) {
     asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, a;\n\tcvt.rn.f16x2.e4m3x2 %1, b;\n\t}"
@@ -740,6 +761,29 @@ __global__ void __launch_bounds__(32 * WP * WR, Shape<D, FMT, SPLITQ, WP, WR, RN
                     }
                 }
 
+                // ---- capped scores, as exponents of 2
+                if (p.cap > 0.f) {
+                    float far = 0.f;
+#pragma unroll
+                    for (int n = 0; n < RN; ++n)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            x[n][e] *= f2[n][e & 1];
+                            far = fmaxf(far, fabsf(x[n][e]));
+                        }
+                    if (__all_sync(0xffffffffu, far < CAP_NEAR)) {
+#pragma unroll
+                        for (int n = 0; n < RN; ++n)
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) x[n][e] = cap_near(x[n][e], 0.5f * p.cap);
+                    } else {
+#pragma unroll
+                        for (int n = 0; n < RN; ++n)
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) x[n][e] = cap_any(x[n][e], p.cap);
+                    }
+                }
+
                 // ---- softmax: x becomes the probabilities
                 uint32_t seen = 0xffffffffu;  // bit n*4+e: the row sees the position
                 bool turn = false;
@@ -748,13 +792,8 @@ __global__ void __launch_bounds__(32 * WP * WR, Shape<D, FMT, SPLITQ, WP, WR, RN
                 for (int n = 0; n < RN; ++n)
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
-                        float y0 = x[n][e] * f2[n][e], y1 = x[n][2 + e] * f2[n][e];
-                        if (p.cap > 0.f) {
-                            // tanh z = 1 - 2 / (e^2z + 1): the error stays near 2^-23 of 1
-                            const float c2 = p.cap * LOG2E;
-                            y0 = c2 - 2.f * c2 * rcp(ex2(y0) + 1.f);
-                            y1 = c2 - 2.f * c2 * rcp(ex2(y1) + 1.f);
-                        }
+                        float y0 = x[n][e], y1 = x[n][2 + e];
+                        if (!(p.cap > 0.f)) y0 *= f2[n][e], y1 *= f2[n][e];
                         if (p.slopes) {
                             const int r = wrow + n * 8 + q4 * 2 + e;
                             const float sl = ms.slope2[r], far = (float)(ms.at[r] - j0 - g8);  // a whole number: exact

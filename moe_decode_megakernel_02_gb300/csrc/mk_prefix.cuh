@@ -459,7 +459,8 @@ __global__ void __launch_bounds__(PrefixShape<D, FMT, SPLITQ>::NT, 1)
                 asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                 bar_arrive(&ms.q_ready);
             }
-            const float scale2 = p.scale * LOG2E, cap2 = p.cap * LOG2E, in2 = p.cap > 0.f ? p.scale * 2.f * LOG2E / p.cap : 0.f;
+            // score to exponent of 2, or to the cap's argument
+            const float scale2 = p.scale * LOG2E, in2 = p.cap > 0.f ? scale2 * (2.f / p.cap) : scale2;
             const float slope2 = p.slopes ? p.slopes[h * p.G + g] * LOG2E : 0.f;
             const int at = live ? p.lens[b] - p.T + t : 0;
             float m = -INFINITY, l = 0.f;
@@ -489,15 +490,37 @@ __global__ void __launch_bounds__(PrefixShape<D, FMT, SPLITQ>::NT, 1)
                         s1[j + 2] = __float_as_uint(__uint_as_float(s1[j + 2]) * e.z), s1[j + 3] = __float_as_uint(__uint_as_float(s1[j + 3]) * e.w);
                     }
                 }
-                auto shape = [&](uint32_t& v, int j) {
-                    float x = __uint_as_float(v);
-                    x = p.cap > 0.f ? cap2 - 2.f * cap2 * rcp(ex2(x * in2) + 1.f) : x * scale2;
-                    if (p.slopes) x -= slope2 * (float)(at - j0 - j);
-                    v = __float_as_uint(x);
-                };
                 if (p.cap > 0.f || p.slopes) {
 #pragma unroll
-                    for (int j = 0; j < 32; ++j) shape(s0[j], j), shape(s1[j], 32 + j);
+                    for (int j = 0; j < 32; ++j) {
+                        s0[j] = __float_as_uint(__uint_as_float(s0[j]) * in2);
+                        s1[j] = __float_as_uint(__uint_as_float(s1[j]) * in2);
+                    }
+                    if (p.cap > 0.f) {
+                        float far = 0.f;
+#pragma unroll
+                        for (int j = 0; j < 32; ++j) far = fmaxf(far, fmaxf(fabsf(__uint_as_float(s0[j])), fabsf(__uint_as_float(s1[j]))));
+                        if (__all_sync(0xffffffffu, far < CAP_NEAR)) {
+#pragma unroll
+                            for (int j = 0; j < 32; ++j) {
+                                s0[j] = __float_as_uint(cap_near(__uint_as_float(s0[j]), 0.5f * p.cap));
+                                s1[j] = __float_as_uint(cap_near(__uint_as_float(s1[j]), 0.5f * p.cap));
+                            }
+                        } else {
+#pragma unroll
+                            for (int j = 0; j < 32; ++j) {
+                                s0[j] = __float_as_uint(cap_any(__uint_as_float(s0[j]), p.cap));
+                                s1[j] = __float_as_uint(cap_any(__uint_as_float(s1[j]), p.cap));
+                            }
+                        }
+                    }
+                    if (p.slopes) {
+#pragma unroll
+                        for (int j = 0; j < 32; ++j) {
+                            s0[j] = __float_as_uint(__uint_as_float(s0[j]) - slope2 * (float)(at - j0 - j));
+                            s1[j] = __float_as_uint(__uint_as_float(s1[j]) - slope2 * (float)(at - j0 - 32 - j));
+                        }
+                    }
                 } else {
 #pragma unroll
                     for (int j = 0; j < 32; ++j) {

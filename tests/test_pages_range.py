@@ -1,22 +1,29 @@
 """Attention over pages at the ends of its values' range: scales, caps and infinities.
 
-The references are those of test_pages.py, in 64 bits.
+The references are those of test_pages.py, in 64 bits. A score's products are summed in 32 bits, at most about
+(D + 8) 2^-24 of sum |q k| scale off; the cap's error is relative to the capped score. For |z| >= 1/2, z the score over
+the cap, tanh z = 1 - 2 / (e^2z + 1): the exponent's roundings (3 2^-24 of z, times sech^2 z, at most 0.67 2^-23 of 1),
+the exponential's 2^-22 (0.79 2^-23), the reciprocal's 2^-23 of at most 0.27, twice (0.54 2^-23), and the roundings of
+the sums (0.77 2^-23) make 2.8 2^-23 of the cap, 6 2^-23 of a tanh that is at least 0.46; below, a polynomial and its
+7 roundings stay under 2^-20 as well, which the bounds here take with the cap's own two roundings.
 """
+import ctypes
 import math
 
 import pytest
 import torch
 
+import moe_decode_megakernel_02_gb300 as mk
 import test_pages as tp
 from test_pages import FORMATS, build, gpu, reference, widen
 
 
-def close(cache, table, lens, q, out, lse, scale, dv, **kw):
-    """Against 64 bits: dv is an absolute error of outputs."""
+def close(cache, table, lens, q, out, lse, scale, dv, rel=0.0, **kw):
+    """Against 64 bits: rel is the cap's error, of a score's size; dv an absolute error of outputs."""
     ref, rlse, mag, reach = reference(cache, table, lens, q, scale, **kw)
-    D = q.shape[-1]
+    D, cap = q.shape[-1], kw.get("softcap", 0.0)
     far = float(kw["slopes"].abs().max()) * float(lens.max()) if kw.get("slopes") is not None else 0.0
-    dx = (D + 8) * 2.0 ** -24 * (reach + far + 1) + 2.0 ** -20
+    dx = (D + 8) * 2.0 ** -24 * (reach + far + 1) + rel * (reach.clamp(max=cap) if cap else 0.0) + 2.0 ** -20
     weight = 2 * dx + (2.0 ** -16 if cache.k.dtype == torch.bfloat16 else 2.0 ** -11)
     eps = torch.finfo(q.dtype).eps / 2
     bound = weight[..., None] * mag + eps * (ref.abs() + weight[..., None] * mag) + dv
@@ -73,3 +80,33 @@ def test_the_scale_of_a_position_that_is_not_seen_changes_nothing(fmt, kind, sca
         elif qdtype == torch.bfloat16:  # the last token sees it: its error is of that scale
             dv = max(lens) * 2.0 ** -39 * tp.QMAX[fmt] * scale
             close(cache, table, n, q[:, -1:], out[:, -1:], lse[:, -1:], 1 / math.sqrt(q.shape[-1]), dv)
+
+
+@gpu
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("kind", list(SHAPES) + ["shared"])
+@pytest.mark.parametrize("cap", [3.0, 50.0, 1e3, 1e5, 1e8, 1e30])
+def test_caps_of_any_size(fmt, kind, cap):
+    """Scores up to some 30, far below and far above the cap: the error is of the score's size, not of the cap's."""
+    shared = 0
+    if kind == "shared":
+        B, T, Hq, H, D, ps, shared = 20, 1, 8, 2, 128, 16, 320
+        lens = [shared + 3 + 5 * b for b in range(B)]
+        cache, table, n, q = build(fmt, torch.bfloat16, B, T, Hq, H, D, ps, lens, shared=shared)
+    else:
+        cache, table, n, q, lens, ps = shape_of(kind, fmt, torch.bfloat16)
+    D = q.shape[-1]
+    for scale, slopes in ((3 / math.sqrt(D), None), (0.02 / math.sqrt(D), torch.full((q.shape[2],), 0.01, device="cuda"))):
+        kw = dict(softcap=cap, slopes=slopes)
+        out, lse = cache.attend(table, n, q, scale=scale, shared_len=shared, return_lse=True, **kw)
+        dv = 2.0 ** -24 if fmt == torch.bfloat16 else max(lens) * 2.0 ** -39 * tp.QMAX[fmt] * float(cache.v_scale.max())
+        close(cache, table, n, q, out, lse, scale, dv, rel=2.0 ** -20, **kw)
+
+
+@pytest.mark.parametrize("cap", [1e-31, 1e31, -1.0, math.nan, math.inf])
+def test_caps_out_of_range_are_refused(cap):
+    p, t, r, a = tp._structs(a__softcap=cap)
+    att = mk.AttentionStruct(pages=ctypes.pointer(p), table=ctypes.pointer(t), q=ctypes.pointer(r), out=ctypes.pointer(r),
+                             **a)
+    n = ctypes.c_int64()
+    assert mk.lib().mk_pages_attend_workspace(ctypes.byref(att), ctypes.byref(n)) == mk.ERR_INVALID_ARG
