@@ -265,7 +265,11 @@ int mk_decode_step_noalloc(mk_model* m, mk_kv* kv, const int32_t* tokens, const 
  *                 stages that read it wait until the wait limit (MK_WAIT_NS)
  *                 and the step reports MK_ERR_TIMEOUT through mk_step_status;
  *   "corrupt_guard" (debug mode, below) mk_step_status overwrites one scratch
- *                 guard before checking them and reports MK_ERR_STATE.
+ *                 guard before checking them and reports MK_ERR_STATE;
+ *   "skip_attend_signal" the launch of mk_pages_attend that reads a shared
+ *                 prefix (or the whole tiles of many rows) on the tensor
+ *                 memory leaves out one of its roles' signals: another waits
+ *                 until the wait limit, and `status` gets MK_ERR_TIMEOUT.
  * Each host failure sets mk_last_error() to a message naming MK_FAULT.
  *
  * Debug mode: with MK_DEBUG=1 when the model is loaded, every CTA writes a
@@ -472,9 +476,10 @@ int mk_pages_attend_workspace(const mk_attention* args, int64_t* bytes);
  * 256-byte aligned), UNSUPPORTED (head_dim other than 64, 128 or 256). A length
  * beyond the table or a page out of range is reported through `status`; what
  * lies there counts as rows of zeros, or beyond the table as not visible. A
- * wait inside a kernel that runs out (2 s; no healthy call comes near) stores
- * MK_ERR_TIMEOUT there, and the output is not to be used. Arguments in device
- * memory, lens above all, must not change while the call runs. */
+ * wait inside a kernel that runs out (MK_WAIT_NS, read by the call, up to 4 s;
+ * default 2 s, no healthy call comes near) stores MK_ERR_TIMEOUT there, and the
+ * output is not to be used. Arguments in device memory, lens above all, must
+ * not change while the call runs. */
 int mk_pages_attend(const mk_attention* args, void* workspace, int64_t workspace_bytes, void* stream);
 
 /* Draws one token a row from logits. With w_i = exp((x_i - max x) / T), in 32

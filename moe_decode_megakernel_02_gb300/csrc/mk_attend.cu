@@ -213,6 +213,8 @@ extern "C" int mk_pages_attend(const mk_attention* a, void* workspace, int64_t w
     const AttendFn fn = D == 64 ? attend_64 : D == 128 ? attend_128 : attend_256;
     cudaStream_t s = (cudaStream_t)stream;
     if (pl.sh_grid) {
+        const long long ns = mk_wait_ns_();
+        p.wait_ns = (unsigned)(ns < 4000000000ll ? ns : 4000000000ll), p.skip_signal = mk_fault_("skip_attend_signal");
         AttendP q = p;
         q.is_shared = !pl.wide;
         q.RB = pl.sh_rb, q.rows_item = pl.wide ? p.T * p.G : p.B * p.T * p.G;

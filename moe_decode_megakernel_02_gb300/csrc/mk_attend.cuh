@@ -86,6 +86,8 @@ struct AttendP {
     int slot_floats;
     float* slots;    // two of each CTA (its first and its last piece), then one of each item
     int* base;       // [B + 1]: first unit of each sequence, written for the joining launch
+    unsigned wait_ns;  // limit of the waits in mk_prefix.cuh, below 4 s
+    int skip_signal;   // for tests: one of their signals is left out
 };
 
 struct JoinP {

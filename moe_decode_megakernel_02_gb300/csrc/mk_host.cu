@@ -422,6 +422,8 @@ __attribute__((visibility("hidden"))) int mk_set_error_(int code, const char* ms
     g_err = msg;
     return code;
 }
+__attribute__((visibility("hidden"))) long long mk_wait_ns_(void) { return wait_ns(); }
+__attribute__((visibility("hidden"))) int mk_fault_(const char* what) { return fault(what); }
 __attribute__((visibility("hidden"))) int mk_fault_oom_(void) {
     return fault("oom") ? fail(MK_ERR_OOM, "allocation refused (injected by MK_FAULT=oom)") : MK_OK;
 }

@@ -12,8 +12,10 @@
 
 #include "../../include/mk.h"
 
-// the library's thread-local message (defined in mk_host.cu)
+// the library's thread-local message, its wait limit (MK_WAIT_NS) and injected failures (MK_FAULT), of mk_host.cu
 extern "C" __attribute__((visibility("hidden"))) int mk_set_error_(int code, const char* msg);
+extern "C" __attribute__((visibility("hidden"))) long long mk_wait_ns_(void);
+extern "C" __attribute__((visibility("hidden"))) int mk_fault_(const char* what);
 
 namespace mkop {
 

@@ -94,7 +94,12 @@ __device__ __forceinline__ bool bar_try(unsigned long long* b, unsigned parity) 
         : "memory");
     return ok;
 }
-constexpr long long PREFIX_WAIT_NS = 2000000000ll;  // no wait of a healthy launch comes near it
+// A CTA that gave up waits so long for what it has in flight (its roles' waits end at AttendP::wait_ns)
+constexpr long long DRAIN_NS = 2000000000ll;
+struct Limit {
+    volatile unsigned* abort;  // a role gave up
+    unsigned ns;
+};
 __device__ __forceinline__ long long now_ns() {
     long long t;
     asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t));
@@ -102,23 +107,24 @@ __device__ __forceinline__ long long now_ns() {
 }
 // Waits for the phase of `parity` to end; false when it took too long, or
 // another role gave up.
-__device__ __forceinline__ bool bar_wait(unsigned long long* b, unsigned parity, volatile unsigned* abort) {
-    long long t0 = 0;
+__device__ __forceinline__ bool bar_wait(unsigned long long* b, unsigned parity, const Limit& limit) {
+    unsigned t0 = 0;
     for (unsigned n = 0; !bar_try(b, parity); ++n) {
         if ((n & 63u) != 63u) continue;  // the timer is slow to read
-        if (*abort) return false;
-        const long long t = now_ns();
-        if (!t0) t0 = t;
-        if (t - t0 > PREFIX_WAIT_NS) {
-            *abort = 1;
+        if (*limit.abort) return false;
+        unsigned t;  // its low half comes round every 4.3 s
+        asm volatile("mov.u32 %0, %%globaltimer_lo;" : "=r"(t));
+        if (n == 63u) t0 = t;
+        if (t - t0 > limit.ns) {
+            *limit.abort = 1;
             return false;
         }
     }
     return true;
 }
 // the same for a whole warp, which goes on or gives up together
-__device__ __forceinline__ bool warp_wait(unsigned long long* b, unsigned parity, volatile unsigned* abort) {
-    return __all_sync(0xffffffffu, bar_wait(b, parity, abort));
+__device__ __forceinline__ bool warp_wait(unsigned long long* b, unsigned parity, const Limit& limit) {
+    return __all_sync(0xffffffffu, bar_wait(b, parity, limit));
 }
 
 // A role's place in the line of tiles: the ring's stage and its turn, the
@@ -306,7 +312,7 @@ __global__ void __launch_bounds__(PrefixShape<D, FMT, SPLITQ>::NT, 1)
     PrefixMisc& ms = *reinterpret_cast<PrefixMisc*>(smem + S::MISC_OFF);
     static_assert(sizeof(PrefixMisc) <= S::MISC_B, "");
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    volatile unsigned* const abort = &ms.abort;
+    const Limit wait_limit = {&ms.abort, p.wait_ns};
 
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     // (the host sees to it that the tiles of all items fit 32 bits)
@@ -401,6 +407,7 @@ __global__ void __launch_bounds__(PrefixShape<D, FMT, SPLITQ>::NT, 1)
     const uint32_t tm = ms.tmem;
     Walk w;
     w.start(p, first, ms.found_b, ms.found_base);
+    int sent = 0;  // tiles that the tensor maps' warp has asked for
 
     // Tiles are counted over all pieces: tile c uses stage c % STAGES, S and P buffer c & 1.
     if (warp < 8 && (warp & 3) >= act) {
@@ -468,7 +475,7 @@ __global__ void __launch_bounds__(PrefixShape<D, FMT, SPLITQ>::NT, 1)
             for (int i = (parity ^ wg) & 1; i < take && ok; i += 2) {
                 const int stage = at_c.stage;
                 const int j0 = w.at() + i * TILE;
-                if (!(ok = warp_wait(&ms.s_full[wg], at_c.pair(), abort))) break;
+                if (!(ok = warp_wait(&ms.s_full[wg], at_c.pair(), wait_limit))) break;
                 tm_after();
                 uint32_t s0[32], s1[32];
                 tm_ld32(s0, my_s);
@@ -478,7 +485,7 @@ __global__ void __launch_bounds__(PrefixShape<D, FMT, SPLITQ>::NT, 1)
                 bar_arrive(&ms.s_free[wg]);
                 const float* ksc = scales + stage * 2 * TILE;
                 // the scales come with the tile
-                if (F8 && !(ok = warp_wait(&ms.kv_full[stage], at_c.full(), abort))) break;
+                if (F8 && !(ok = warp_wait(&ms.kv_full[stage], at_c.full(), wait_limit))) break;
                 if constexpr (F8) {
 #pragma unroll
                     for (int j = 0; j < 32; j += 4) {
@@ -549,7 +556,7 @@ __global__ void __launch_bounds__(PrefixShape<D, FMT, SPLITQ>::NT, 1)
                     m = mn;
                     l *= f;
                     // every product so far is in O
-                    if (!(ok = warp_wait(&ms.pv_done[back.stage], back.full(), abort))) break;
+                    if (!(ok = warp_wait(&ms.pv_done[back.stage], back.full(), wait_limit))) break;
                     tm_after();
 #pragma unroll 1
                     for (int d = 0; d < D; d += 32) {
@@ -586,7 +593,7 @@ __global__ void __launch_bounds__(PrefixShape<D, FMT, SPLITQ>::NT, 1)
                 }
                 l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
                 // the P buffer is free when the group's last product has read it
-                if (at_c.c >= 2 && !(ok = warp_wait(&ms.pv_done[back.stage], back.full(), abort))) break;
+                if (at_c.c >= 2 && !(ok = warp_wait(&ms.pv_done[back.stage], back.full(), wait_limit))) break;
                 tm_after();
                 tm_st32(my_p, hi);
                 tm_st32(my_p + 32, lo);
@@ -601,7 +608,7 @@ __global__ void __launch_bounds__(PrefixShape<D, FMT, SPLITQ>::NT, 1)
             parity ^= take & 1;
             // ---- the piece: both groups' outputs join out of tensor memory, half of the columns by each
             // (a group that gave up keeps the barriers)
-            if (ok && !fresh) ok = warp_wait(&ms.pv_done[back.stage], back.full(), abort);
+            if (ok && !fresh) ok = warp_wait(&ms.pv_done[back.stage], back.full(), wait_limit);
             ms.stat[wg][lrow] = make_float2(m, l);
             tm_before();
             asm volatile("bar.sync 2, %0;" ::"r"(64 * act) : "memory");
@@ -665,15 +672,15 @@ __global__ void __launch_bounds__(PrefixShape<D, FMT, SPLITQ>::NT, 1)
                 return page;
             };
             int now = page_next(), next = page_next();
-            bool ok = true;
             int box = 0;
             Place<S::STAGES> pl;
             for (int c = 0; c < tiles; ++c, pl.next()) {
                 const int stage = pl.stage, h = w.item / p.RB, j0 = w.at();
                 w.on(p, 1);
                 const uint32_t st = ring + stage * S::STAGE_B;
-                if (c >= S::STAGES && !(ok = warp_wait(&ms.pv_done[stage], pl.free(), abort))) break;
+                if (c >= S::STAGES && !warp_wait(&ms.pv_done[stage], pl.free(), wait_limit)) break;
                 if (lane == 0) bar_expect(&ms.kv_full[stage], S::STAGE_B);
+                sent = c + 1;
                 for (int i = 0; i < parts; ++i, ++box) {
                     const int page = __shfl_sync(0xffffffffu, now, box & 31);
                     if (lane == 0) {
@@ -690,14 +697,6 @@ __global__ void __launch_bounds__(PrefixShape<D, FMT, SPLITQ>::NT, 1)
                         next = page_next();
                     }
                 }
-            }
-            // a launch that gave up still waits for its copies on the way
-            if (!ok) {
-                const long long t0 = now_ns();
-                const int to = box >> pshift;  // tiles sent
-                for (int c = max(0, to - S::STAGES); c < to; ++c)
-                    while (!bar_try(&ms.kv_full[c % S::STAGES], (unsigned)(c / S::STAGES) & 1u) && now_ns() - t0 < PREFIX_WAIT_NS) {
-                    }
             }
         }
     } else if (warp < MMA_WARP) {
@@ -776,7 +775,7 @@ __global__ void __launch_bounds__(PrefixShape<D, FMT, SPLITQ>::NT, 1)
             copy(c + 2, at2);
             at2 = at3;
             // a thread that gave up keeps the loop's barriers
-            if (ok && c >= S::STAGES) ok = bar_wait(&ms.pv_done[stage], pl.free(), abort);
+            if (ok && c >= S::STAGES) ok = bar_wait(&ms.pv_done[stage], pl.free(), wait_limit);
             cp_wait<2>();
             if (ok) {
                 const uint8_t* const raw = smem + S::RAW_OFF + c % S::RAWS * S::RAW_B;
@@ -819,11 +818,11 @@ __global__ void __launch_bounds__(PrefixShape<D, FMT, SPLITQ>::NT, 1)
                 const int take = min(w.n - w.tile, end - u);
                 u += take;
                 w.on(p, take);
-                ok = warp_wait(&ms.q_ready, piece_no & 1u, abort);
+                ok = warp_wait(&ms.q_ready, piece_no & 1u, wait_limit);
                 for (int i = 0; i < take && ok; ++i) {
                     // K is here; the softmax has read what the S buffer held two tiles ago
-                    ok = warp_wait(&ms.kv_full[at_c.stage], at_c.full(), abort) &&
-                         (at_c.c < 2 || warp_wait(&ms.s_free[at_c.buf()], at_c.pair_free(), abort));
+                    ok = warp_wait(&ms.kv_full[at_c.stage], at_c.full(), wait_limit) &&
+                         (at_c.c < 2 || warp_wait(&ms.s_free[at_c.buf()], at_c.pair_free(), wait_limit));
                     if (!ok) break;
                     tm_after();
                     if (elect_one()) {
@@ -850,7 +849,7 @@ __global__ void __launch_bounds__(PrefixShape<D, FMT, SPLITQ>::NT, 1)
                 w.on(p, take);
                 for (int i = 0; i < take; ++i) {
                     // the probabilities are here, and so V (their scores came from the same stage)
-                    if (!(ok = warp_wait(&ms.p_ready[at_c.buf()], at_c.pair(), abort))) break;
+                    if (!(ok = warp_wait(&ms.p_ready[at_c.buf()], at_c.pair(), wait_limit))) break;
                     tm_after();
                     if (elect_one()) {
                         const uint64_t v = desc_on(v0, at_c.stage * S::STAGE_B);
@@ -861,7 +860,7 @@ __global__ void __launch_bounds__(PrefixShape<D, FMT, SPLITQ>::NT, 1)
 #pragma unroll
                             for (int j = 0; j < TILE / 16; ++j)
                                 mma_ts(d, pa + part * 32 + j * 8, desc_on(v, j * 2048), PV, i > 1 || part > 0 || j > 0);
-                        mma_commit(&ms.pv_done[at_c.stage]);
+                        if (!p.skip_signal) mma_commit(&ms.pv_done[at_c.stage]);
                     }
                     __syncwarp();
                     at_c.next();
@@ -871,14 +870,24 @@ __global__ void __launch_bounds__(PrefixShape<D, FMT, SPLITQ>::NT, 1)
         // the last products end before the tensor memory goes, also when a role gave up
         if (elect_one()) mma_commit(&ms.drained);
         const long long t0 = now_ns();
-        while (!bar_try(&ms.drained, 0) && now_ns() - t0 < PREFIX_WAIT_NS) {
+        while (!bar_try(&ms.drained, 0) && now_ns() - t0 < DRAIN_NS) {
         }
     }
     __syncwarp();
     tm_before();
     __syncthreads();
     tm_after();
-    if (tid == 0 && ms.abort && p.status) *p.status = MK_ERR_TIMEOUT;
+    if (ms.abort) {
+        // Whichever role gave up, copies by the tensor maps may still be on their way into this CTA's memory: at most
+        // the ring's last tiles. (The loads of codes and the products have waited for theirs.)
+        if (!F8 && warp == 8) {
+            const long long t0 = now_ns();
+            for (int c = max(0, sent - S::STAGES); c < sent; ++c)
+                while (!bar_try(&ms.kv_full[c % S::STAGES], (unsigned)(c / S::STAGES) & 1u) && now_ns() - t0 < DRAIN_NS) {
+                }
+        }
+        if (tid == 0 && p.status) *p.status = MK_ERR_TIMEOUT;
+    }
     if (warp == MMA_WARP)
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tm), "n"(S::T_ALL) : "memory");
 }
