@@ -478,8 +478,8 @@ int mk_pages_attend_workspace(const mk_attention* args, int64_t* bytes);
  * lies there counts as rows of zeros, or beyond the table as not visible. A
  * wait inside a kernel that runs out (MK_WAIT_NS, read by the call, up to 4 s;
  * default 2 s, no healthy call comes near) stores MK_ERR_TIMEOUT there, and the
- * output is not to be used. Arguments in device memory, lens above all, must
- * not change while the call runs. */
+ * rows it concerns get NaN in `out` and `lse`. Arguments in device memory, lens
+ * above all, must not change while the call runs. */
 int mk_pages_attend(const mk_attention* args, void* workspace, int64_t workspace_bytes, void* stream);
 
 /* Draws one token a row from logits. With w_i = exp((x_i - max x) / T), in 32

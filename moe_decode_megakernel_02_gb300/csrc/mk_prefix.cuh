@@ -27,7 +27,7 @@
 // softmax does. fp16 queries are two bf16 parts, one more chain of Q K^T. All
 // waits are on mbarriers with a limit; a wait that runs out raises a flag that
 // every role sees, and the CTA leaves after freeing its tensor memory
-// (MK_ERR_TIMEOUT in `status`).
+// (MK_ERR_TIMEOUT in `status`, NaN in its rows).
 //
 // Bound by the products: Q K^T of 128 x 64 takes 48 cycles a 16-wide step (its
 // operands' shared-memory reads), the two chains of P V 64 each, 875 cycles a
@@ -609,13 +609,14 @@ __global__ void __launch_bounds__(PrefixShape<D, FMT, SPLITQ>::NT, 1)
             // ---- the piece: both groups' outputs join out of tensor memory, half of the columns by each
             // (a group that gave up keeps the barriers)
             if (ok && !fresh) ok = warp_wait(&ms.pv_done[back.stage], back.full(), wait_limit);
-            ms.stat[wg][lrow] = make_float2(m, l);
+            // what a group that gave up leaves is no number, in every row's output
+            ms.stat[wg][lrow] = make_float2(m, ok ? l : __uint_as_float(0x7fffffffu));
             tm_before();
             asm volatile("bar.sync 2, %0;" ::"r"(64 * act) : "memory");
             tm_after();
             const float2 s0 = ms.stat[0][lrow], s1 = ms.stat[1][lrow];
             const float mm = fmaxf(s0.x, s1.x), mr = mm == -INFINITY ? 0.f : mm;
-            const float f0 = ex2(s0.x - mr), f1 = ex2(s1.x - mr), ll = s0.y * f0 + s1.y * f1;
+            const float f0 = ex2(s0.x - mr), f1 = ex2(s1.x - mr), ll = s0.y * f0 + s1.y * f1;  // (0 x NaN stays NaN)
             // a group without a tile (or without a finite score) has nothing in its output
             const bool has0 = s0.x != -INFINITY, has1 = s1.x != -INFINITY;
             const bool whole = take == w.n;

@@ -37,3 +37,15 @@ def test_a_wait_that_runs_out_is_reported_and_the_next_call_is_right(fmt, kind, 
     status.zero_()
     out, lse = call(status)
     assert int(status) == 0 and torch.equal(out, want) and torch.equal(lse, wlse)
+
+
+@gpu
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("kind", ["short", "long", "wide"])
+def test_what_a_call_that_gave_up_leaves_is_no_number(fmt, kind, monkeypatch):
+    """A caller without a status sees it in the output: every row that the launch has a part in is NaN."""
+    cache, call = a_call(kind, fmt)
+    monkeypatch.setenv("MK_WAIT_NS", "20000000")
+    monkeypatch.setenv("MK_FAULT", "skip_attend_signal")
+    out, lse = call()
+    assert bool(torch.isnan(out).all()) and bool(torch.isnan(lse).all())
