@@ -316,7 +316,7 @@ class KVCache:
 
     def pages(self, layer):
         """The layer's pages as a `pages.Pages` over the cache's own memory, with its block table as `.table`
-        (mk_kv_view; GQA models)."""
+        (mk_kv_view; GQA models). They hold until the cache is closed."""
         from . import pages
         return pages.of_cache(self, layer)
 

@@ -226,15 +226,26 @@ class _Memory:
                                          "version": 3, "stream": None}
 
 
+def _device_of(owner, ptr):
+    """The device that holds the library's memory at ptr, the current one or another: torch copies what it is asked to
+    see on a device that does not hold it, so one byte tells."""
+    now = torch.cuda.current_device()
+    for i in [now] + [i for i in range(torch.cuda.device_count()) if i != now]:
+        if torch.as_tensor(_Memory(owner, ptr, (1,), None, "|u1"), device=f"cuda:{i}").data_ptr() == ptr:
+            return torch.device("cuda", i)
+    raise RuntimeError(f"no device holds the cache's memory at {ptr:#x}")
+
+
 def of_cache(kv, layer) -> Pages:
-    """The pages of one layer of a model's KVCache (no copy); `.table` is its block table, int32 [batch, pages]."""
+    """The pages of one layer of a model's KVCache (no copy); `.table` is its block table, int32 [batch, pages].
+    They hold until the cache is closed."""
     s, t = PagesStruct(), TableStruct()
     _check(lib().mk_kv_view(kv.h, layer, _byref(s), _byref(t)))
     shape = (s.n_pages, s.n_kv_heads, s.page_size, s.head_dim)
     strides = (2 * s.page_stride, 2 * s.head_stride, 2 * s.row_stride, 2)
     # bfloat16 has no type string there: taken as 16-bit integers, then seen as bfloat16
-    k, v = (torch.as_tensor(_Memory(kv, p, shape, strides, "<i2"), device="cuda").view(torch.bfloat16)
-            for p in (s.k, s.v))
+    dev = _device_of(kv, s.k)
+    k, v = (torch.as_tensor(_Memory(kv, p, shape, strides, "<i2"), device=dev).view(torch.bfloat16) for p in (s.k, s.v))
     out = Pages(k, v)
-    out.table = torch.as_tensor(_Memory(kv, t.table, (t.batch, t.pages_per_seq), None, "<i4"), device="cuda")
+    out.table = torch.as_tensor(_Memory(kv, t.table, (t.batch, t.pages_per_seq), None, "<i4"), device=dev)
     return out
