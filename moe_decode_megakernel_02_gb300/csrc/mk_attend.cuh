@@ -237,6 +237,15 @@ __device__ __forceinline__ float cap_any(float y, float cap) {
     return fabsf(y) < CAP_NEAR ? cap_near(y, 0.5f * cap) : c2 - 2.f * c2 * rcp(ex2(y) + 1.f);
 }
 
+// Two probabilities as bf16 parts: hi cut off, lo the rest, rounded (16 bits
+// together). Neither is negative and lo is never 0, so that an infinity in V,
+// times both, stays that infinity (0 x inf is NaN, and so is inf - inf).
+__device__ __forceinline__ void split_bf16(float x, float y, uint32_t& hi, uint32_t& lo) {
+    hi = __byte_perm(__float_as_uint(x), __float_as_uint(y), 0x7632);
+    lo = pack_bf16(x - __uint_as_float(__float_as_uint(x) & 0xffff0000u), y - __uint_as_float(__float_as_uint(y) & 0xffff0000u));
+    asm("max.u16x2 %0, %0, %1;" : "+r"(lo) : "r"(0x00010001u));  // 2^-133, the least one; NaN stays
+}
+
 // Four E4M3 codes as two registers of two fp16 values, exact.
 __device__ __forceinline__ void e4m3_quad(uint32_t w, uint32_t& lo, uint32_t& hi) {
     asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, a;\n\tcvt.rn.f16x2.e4m3x2 %1, b;\n\t}"
@@ -887,8 +896,8 @@ __global__ void __launch_bounds__(32 * WP * WR, Shape<D, FMT, SPLITQ, WP, WR, RN
                                         uint16_t v;
                                         asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(a));
                                         if ((v & 0x7f80u) == 0x7f80u) {
-                                            if (vis & 1u) o[n][i][2 * c] += pv[0] * bf2f(v);
-                                            if (vis & 2u) o[n][i][2 * c + 1] += pv[1] * bf2f(v);
+                                            if (vis & 1u) o[n][i][2 * c] += fmaxf(pv[0], 0x1p-126f) * bf2f(v);
+                                            if (vis & 2u) o[n][i][2 * c + 1] += fmaxf(pv[1], 0x1p-126f) * bf2f(v);
                                         }
                                     }
                                 }
@@ -913,8 +922,11 @@ __global__ void __launch_bounds__(32 * WP * WR, Shape<D, FMT, SPLITQ, WP, WR, RN
                                 lo = pack_f16(y0 - z.x, y1 - z.y);
                             }
                         } else {
-                            hi = pack_bf16(y0, y1);
-                            lo = pack_bf16(y0 - bf2f(hi & 0xffffu), y1 - bf2f(hi >> 16));
+                            split_bf16(y0, y1, hi, lo);
+                            if (!all_see) {  // nothing of what is not seen
+                                if (!(seen >> (n * 4 + 2 * c) & 1u)) lo &= 0xffff0000u;
+                                if (!(seen >> (n * 4 + 2 * c) & 2u)) lo &= 0xffffu;
+                            }
                         }
                         ph[n][c] = transpose8(hi);
                         if (with_lo) pl[n][c] = transpose8(lo);

@@ -575,9 +575,13 @@ __global__ void __launch_bounds__(PrefixShape<D, FMT, SPLITQ>::NT, 1)
                 auto pair = [&](uint32_t a, uint32_t b2, float va, float vb, uint32_t& ph, uint32_t& pl, float& s) {
                     float x = ex2(__uint_as_float(a) - ref), y = ex2(__uint_as_float(b2) - ref);
                     s += x + y;
-                    if constexpr (F8) x *= va, y *= vb;
-                    ph = pack_bf16(x, y);
-                    pl = pack_bf16(x - bf2f(ph & 0xffffu), y - __uint_as_float(ph & 0xffff0000u));
+                    if constexpr (F8) {
+                        x *= va, y *= vb;
+                        ph = pack_bf16(x, y);
+                        pl = pack_bf16(x - bf2f(ph & 0xffffu), y - __uint_as_float(ph & 0xffff0000u));
+                    } else {
+                        split_bf16(x, y, ph, pl);
+                    }
                 };
 #pragma unroll
                 for (int j = 0; j < 16; j += 2) {

@@ -110,3 +110,26 @@ def test_caps_out_of_range_are_refused(cap):
                              **a)
     n = ctypes.c_int64()
     assert mk.lib().mk_pages_attend_workspace(ctypes.byref(att), ctypes.byref(n)) == mk.ERR_INVALID_ARG
+
+
+@gpu
+@pytest.mark.parametrize("kind", list(SHAPES) + ["shared"])
+@pytest.mark.parametrize("qdtype", [torch.bfloat16, torch.float16])
+def test_infinite_values_in_whole_tiles_stay_infinite(kind, qdtype):
+    """Positions that every token sees, in tiles without a mask: an infinity times a weight is that infinity."""
+    shared = 0
+    if kind == "shared":
+        B, T, Hq, H, D, ps, shared = 20, 1, 8, 2, 128, 16, 320
+        lens = [shared + 3 + 5 * b for b in range(B)]
+        cache, table, n, q = build(torch.bfloat16, qdtype, B, T, Hq, H, D, ps, lens, shared=shared)
+    else:
+        cache, table, n, q, lens, ps = shape_of(kind, torch.bfloat16, qdtype)
+    for b, L in enumerate(lens):
+        for j, d, x in ((0, 5, math.inf), (1, 9, -math.inf), (17, 11, math.inf), (3, 11, -math.inf), (16, 33, math.inf)):
+            cache.v[int(table[b, j // ps]), :, j % ps, d] = x
+    out, lse = cache.attend(table, n, q, shared_len=shared, return_lse=True)
+    assert bool((out[..., 5] == math.inf).all()) and bool((out[..., 33] == math.inf).all())
+    assert bool((out[..., 9] == -math.inf).all()) and bool(torch.isnan(out[..., 11]).all())
+    rest = torch.ones(q.shape[-1], dtype=torch.bool, device="cuda")
+    rest[[5, 9, 11, 33]] = False
+    assert bool(torch.isfinite(out[..., rest]).all()) and bool(torch.isfinite(lse).all())
