@@ -71,6 +71,8 @@ class SampledLoop:
         B = len(first_tokens)
         if len(positions) != B or B < 1:
             raise ValueError("one position per sequence")
+        if int(vocab) != model.config.vocab:  # the step writes rows of the model's size
+            raise ValueError(f"vocab {vocab}, but the model's is {model.config.vocab}")
 
         def ints(v):
             return torch.as_tensor(v, dtype=torch.int32).to(device)
