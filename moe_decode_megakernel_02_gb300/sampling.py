@@ -10,7 +10,7 @@ import struct
 
 import torch
 
-from . import SamplingStruct, _check, lib
+from . import MKError, SamplingStruct, _check, lib
 from .pages import _DTYPE, _launch, _ptr
 
 _SAMPLING = struct.Struct("Pq PPPPP PPP iiii")
@@ -93,9 +93,12 @@ class SampledLoop:
         self.settings = dict(temperature=each(temperature, torch.float32), top_k=each(top_k, torch.int32),
                              top_p=each(top_p, torch.float32), min_p=each(min_p, torch.float32))
         self.emitted = []
+        self.failed = None  # the error of a step, from then on
 
     def step(self):
         """One decode step and one draw a sequence; returns the tokens (int32 [batch], on the device)."""
+        if self.failed:
+            raise self.failed
         self.model.decode_step(self.kv, self.tok, self.pos, self.logits)
         self.u.uniform_(generator=self.generator)
         drawn = sample(self.logits, self.u, **self.settings)
@@ -105,6 +108,14 @@ class SampledLoop:
         return drawn
 
     def tokens(self):
-        """The tokens drawn so far, [batch][steps], after checking the last step's device status."""
-        self.model.check()
+        """The tokens drawn so far, [batch][steps], after checking the steps' device status. After a failed step (a row
+        without a distribution, whose token -1 the next step refuses, or a position past the cache) it raises, and so
+        do later calls: what was drawn from there on came from old logits."""
+        if not self.failed:
+            try:
+                self.model.check()
+            except MKError as e:
+                self.failed = e
+        if self.failed:
+            raise self.failed
         return torch.stack(self.emitted, dim=1).cpu().tolist() if self.emitted else [[] for _ in range(self.B)]

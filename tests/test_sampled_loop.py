@@ -17,3 +17,17 @@ def test_a_vocabulary_that_is_not_the_models_is_refused(vocab):
     with pytest.raises(ValueError):
         sampling.SampledLoop(_model(), None, [1, 2], [0, 0], vocab, device="cpu")
     assert sampling.SampledLoop(_model(), None, [1, 2], [0, 0], 100, device="cpu").tokens() == [[], []]
+
+
+def test_a_failed_step_stays_failed():
+    """Reading the status clears it: tokens drawn after a failed step must not pass for good ones at the next call."""
+    codes = [mk.ERR_INVALID_ARG]
+
+    def check():
+        if codes:
+            raise mk.MKError(codes.pop(), "token id or position out of range for this step")
+
+    loop = sampling.SampledLoop(_model(check=check), None, [1], [0], 100, device="cpu")
+    for call in (loop.tokens, loop.tokens, loop.step):
+        with pytest.raises(mk.MKError):
+            call()
