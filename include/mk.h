@@ -397,7 +397,7 @@ typedef struct mk_page_table {
 
 /* Rows outside a cache (device memory): element i of kv head h of token t of
  * sequence b at b*seq_stride + t*token_stride + h*head_stride + i, of type
- * `dtype`. */
+ * `dtype`. Rows that a call writes must not overlap. */
 typedef struct mk_rows {
     void* data;
     int64_t seq_stride, token_stride, head_stride;

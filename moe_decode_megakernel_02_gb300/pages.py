@@ -4,7 +4,8 @@ Binding of mk_pages_write, mk_pages_read and mk_pages_attend (include/mk.h).
 The cache, its block table and everything else are the caller's own tensors;
 a `Pages` only describes them. Calls run on the current stream (or `stream`)
 of the cache's device and may be captured into a CUDA graph; they record no
-gradients.
+gradients. What a call on another stream than the tensors' own was given must
+live until that stream has run it.
 
     k = torch.empty(n_pages, n_kv_heads, page_size, head_dim, dtype=torch.float8_e4m3fn, device="cuda")
     cache = Pages(k, torch.empty_like(k), k_scale, v_scale)   # scales: float32 [n_pages, n_kv_heads, page_size]
@@ -72,6 +73,13 @@ def _rows(x, name, device):
     if s[3] != 1 and x.shape[3] > 1:
         raise ValueError(f"{name}'s last dimension must be contiguous, got strides {s}")
     return x.data_ptr(), s[0], s[1], s[2], dt, 0
+
+
+def _written(x, name):
+    """Refuses a tensor whose elements share memory by expansion: its rows would be written over one another."""
+    s = x.stride()
+    if 0 in s and any(n > 1 and not d for n, d in zip(x.shape, s)):
+        raise ValueError(f"{name} is written to, but its strides {s} put several elements in one place")
 
 
 # A call's structures side by side in one buffer: (mk_attention,) mk_page_table, mk_rows, mk_rows
@@ -150,6 +158,8 @@ class Pages:
     def read(self, table, positions, k, v, counts=None, status=None, stream=None):
         """Fills rows t < counts[b] of k and v, [batch, tokens, n_kv_heads, head_dim], from positions
         positions[b] + t, as code x scale rounded to their type; other rows stay as they are. Returns (k, v)."""
+        _written(k, "k")
+        _written(v, "v")
         self._copy(lib().mk_pages_read, table, positions, k, v, counts, status, stream)
         return k, v
 
@@ -177,8 +187,10 @@ class Pages:
         first = 0 if starts is None else _ptr(starts, "starts", batch, torch.int32, dev)
         sl = 0 if slopes is None else _ptr(slopes, "slopes", shape[2:3], torch.float32, dev)
         st = 0 if status is None else _ptr(status, "status", _ONE, torch.int32, dev)
-        if out is not None and (out.dtype is not q.dtype or out.shape != shape):
-            raise ValueError(f"out must have q's type and shape, {q.dtype} {tuple(shape)}")
+        if out is not None:
+            if out.dtype is not q.dtype or out.shape != shape:
+                raise ValueError(f"out must have q's type and shape, {q.dtype} {tuple(shape)}")
+            _written(out, "out")
         if scale is None:
             scale = 1.0 / math.sqrt(D)
         return _launch(dev, stream, self._attend, (t, rq, q, n, first, sl, st, out, scale, softcap, shared_len,
