@@ -936,6 +936,27 @@ __global__ void __launch_bounds__(ST, 2) sample_kernel(const SampleP p) {
     if (rank == 0 && tid == 0 && p.kept) p.kept[row] = (int)kept;
 }
 
+constexpr int MAX_DEV = 32;
+constexpr size_t RESERVED = 1024;  // shared memory that the system takes of every CTA
+struct Device {
+    int sms, smem;  // SMs, and the shared memory of each
+};
+// asked for once on each device
+cudaError_t device_facts(int dev, Device& out) {
+    static std::atomic<int> sms[MAX_DEV], smem[MAX_DEV];
+    if (dev < MAX_DEV && (out.smem = smem[dev].load(std::memory_order_acquire))) {
+        out.sms = sms[dev].load(std::memory_order_relaxed);
+        return cudaSuccess;
+    }
+    cudaError_t e = cudaDeviceGetAttribute(&out.sms, cudaDevAttrMultiProcessorCount, dev);
+    if (e == cudaSuccess) e = cudaDeviceGetAttribute(&out.smem, cudaDevAttrMaxSharedMemoryPerMultiprocessor, dev);
+    if (e == cudaSuccess && dev < MAX_DEV) {
+        sms[dev].store(out.sms, std::memory_order_relaxed);
+        smem[dev].store(out.smem, std::memory_order_release);
+    }
+    return e;
+}
+
 }  // namespace
 
 extern "C" int mk_sample(const mk_sampling* a, void* stream) {
@@ -957,31 +978,37 @@ extern "C" int mk_sample(const mk_sampling* a, void* stream) {
     p.tokens = a->tokens, p.probs = a->probs, p.kept = a->kept;
     p.V = a->vocab;
     // a slice of 2048 tokens keeps a CTA's threads busy with 4 each; where the
-    // rows fill the device anyway, larger slices that still leave two CTAs an SM:
-    // 256 bf16 rows of 151936 take 133 us so, 159 with 8 CTAs a row and 160 with
-    // slices that leave one CTA an SM; 200 fp32 rows of 8000 take 25 and, with
-    // 4 CTAs a row, 39
+    // rows fill the device anyway, larger slices that still leave two CTAs an SM.
+    // Measured before the rows had an order: 256 bf16 rows of 151936 133 us so,
+    // 159 with 8 CTAs a row and 160 with slices that leave one CTA an SM; 200
+    // fp32 rows of 8000 25 us and, with 4 CTAs a row, 39
     int C = MAXC;
     while (C > 1 && a->vocab <= 2048 * (C / 2)) C /= 2;
-    while (C > 1 && a->rows * (C / 2) >= 304 && ((int64_t)a->vocab * e + C / 2 - 1) / (C / 2) <= 78 * 1024) C /= 2;
-    p.slice = ((a->vocab + C - 1) / C + 7) / 8 * 8;  // whole 16-byte vectors
+    int dev = 0;
+    Device of;
+    cudaError_t err = cudaGetDevice(&dev);
+    if (err == cudaSuccess) err = device_facts(dev, of);
+    if (err != cudaSuccess) return cuda_status(err, "mk_sample");
+    auto slice_of = [&](int c) { return ((a->vocab + c - 1) / c + 7) / 8 * 8; };  // whole 16-byte vectors
+    auto smem_of = [&](int c) { return (sizeof(Shared) + 15) / 16 * 16 + (size_t)slice_of(c) * e; };
+    auto ctas_of = [&](int c) { return 2 * (smem_of(c) + RESERVED) <= (size_t)of.smem ? 2 : 1; };  // of an SM
+    while (C > 1 && (int64_t)a->rows * (C / 2) >= 2 * of.sms && ctas_of(C / 2) == 2) C /= 2;
+    p.slice = slice_of(C);
     // More rows than run at once: in the order of their cost. 256 bf16 rows of
     // 151936, an eighth of them costly, take 99 us so and 125 in the order they
-    // come; where all cost the same 86 and 82, and 200 fp32 rows of 8000, whose
-    // slices of 16 KB are quickly done, 27 and 25. With more waves of rows the
-    // last one counts for less.
+    // come, 30 fp32 rows of 300000, one CTA an SM, 97 and 111; where all cost the
+    // same 86 and 82 (195 and 192), and 200 fp32 rows of 8000, whose slices of
+    // 16 KB are quickly done, 27 and 25. With more waves of rows the last one
+    // counts for less.
     p.rows = a->rows;
-    p.order = a->top_p && (int64_t)a->rows * C > 304 && a->rows <= 4 * ST && p.slice * e >= 32768;
+    p.order = a->top_p && (int64_t)a->rows * C > of.sms * ctas_of(C) && a->rows <= 4 * ST && p.slice * e >= 32768;
     auto kern = a->dtype == MK_DT_F32    ? sample_kernel<MK_DT_F32>
                 : a->dtype == MK_DT_BF16 ? sample_kernel<MK_DT_BF16>
                                          : sample_kernel<MK_DT_F16>;
-    const size_t smem = (sizeof(Shared) + 15) / 16 * 16 + (size_t)p.slice * e;
-    int dev = 0;
-    cudaError_t err = cudaGetDevice(&dev);
+    const size_t smem = smem_of(C);
     // the kernel's shared-memory limit, raised once on each device
-    constexpr int MAX_DEV = 32;
     static std::atomic<bool> raised[MAX_DEV][3];
-    if (err == cudaSuccess && (dev >= MAX_DEV || !raised[dev][a->dtype].load())) {
+    if (dev >= MAX_DEV || !raised[dev][a->dtype].load()) {
         err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                    (int)((sizeof(Shared) + 15) / 16 * 16 + MAX_SLICE_B));
         if (err == cudaSuccess && dev < MAX_DEV) raised[dev][a->dtype] = true;
