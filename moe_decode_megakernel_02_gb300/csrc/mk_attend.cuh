@@ -294,7 +294,7 @@ struct Shape {
     static constexpr int OREGS = RN * D / 4;                // registers of the output
     static constexpr bool QREG = RN * D / 8 * (SPLITQ ? 2 : 1) <= 16 || (NT == 128 && RN * D / 8 * (SPLITQ ? 2 : 1) <= 32);
     // CTAs an SM: what the registers allow, and at least two stages of the ring
-    static constexpr int WANT = (OREGS <= 32 ? 4 : OREGS <= 64 ? 4 : 2) * 128 / NT;
+    static constexpr int WANT = (OREGS <= 64 ? 4 : 2) * 128 / NT;
     static constexpr int fit(int ctas) { return (227 * 1024 / ctas - 1024 - Q_B - MISC_B) / STAGE_B; }
     static constexpr int CTAS = WANT > 3 && fit(WANT) >= 3 ? WANT : WANT >= 3 && fit(3) >= 2 ? 3 : WANT >= 2 && fit(2) >= 2 ? 2 : 1;
     static constexpr int STAGES = fit(CTAS) > 4 ? 4 : fit(CTAS);

@@ -704,11 +704,11 @@ __global__ void __launch_bounds__(PrefixShape<D, FMT, SPLITQ>::NT, 1)
                 }
             }
         }
-    } else if (warp < MMA_WARP) {
+    } else if (F8 && warp < MMA_WARP) {
         // ================ loads of codes ================
         const int t = tid - 256;
         const int mask = (1 << p.ps_shift) - 1;
-        constexpr int CH = D * (F8 ? 1 : 2) / 16;  // 16-byte pieces of a cached row
+        constexpr int CH = D / 16;             // 16-byte pieces of a cached row
         constexpr int EACH = TILE * CH / 128;      // pieces of K (and of V) a thread copies
         const int cc = t % CH;
         const int tiles = end - first;
