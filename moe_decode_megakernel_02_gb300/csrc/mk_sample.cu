@@ -44,6 +44,7 @@
 #include <cooperative_groups.h>
 
 #include <atomic>
+#include <cfloat>
 #include <type_traits>
 
 #include "mk_ops.cuh"
@@ -115,7 +116,8 @@ struct Weight {
     bool plain;  // T far from the ends of the range: the quotient by remainder (Markstein 1990) is the divided one
     // x = -infinity weighs 0 (where T is plain)
     __device__ __forceinline__ float operator()(float x) const {
-        if (!plain) return expf(__fdiv_rn(x - m, T));
+        // (a difference beyond the range must not meet an infinite T)
+        if (!plain) return expf(__fdiv_rn(fmaxf(x - m, -FLT_MAX), T));
         // below -200 T the weight is 0 anyway; the bound keeps infinities out of the remainder
         const float d = fmaxf(x - m, low), q = d * r;
         return expf(__fmaf_rn(__fmaf_rn(-q, T, d), r, q));

@@ -1,4 +1,4 @@
-"""Sampling where rows outnumber the device because their slices leave room for one CTA an SM."""
+"""Sampling: rows that outnumber the device because their slices leave room for one CTA an SM; the largest temperature."""
 import pytest
 import torch
 
@@ -20,3 +20,24 @@ def test_rows_of_large_slices_give_what_they_give_alone(R, V, dtype):
         want = sampling.sample(x[cut], u[cut], temperature=T[cut], top_k=k[cut], top_p=p[cut], min_p=least[cut],
                                return_details=True)
         assert all(torch.equal(a[cut], b) for a, b in zip(got, want))
+
+
+@gpu
+@pytest.mark.parametrize("V", [3, 5000])
+@pytest.mark.parametrize("top_p", [None, 0.999999])
+def test_an_infinite_temperature_gives_every_unmasked_token_the_same_weight(V, top_p):
+    """Also where logits lie further apart than the largest number (masks of the type's lowest value)."""
+    inf, lowest = float("inf"), torch.finfo(torch.float32).min
+    x = torch.full((4, V), lowest, device="cuda")
+    x[:, ::2] = 3e38
+    x[3] = -inf
+    x[3, 1] = lowest
+    u = torch.tensor([0.0, 0.5, 0.9999999, 0.7], device="cuda")
+    kw = {} if top_p is None else dict(top_p=torch.full((4,), top_p, device="cuda"))
+    tok, prob, kept = sampling.sample(x, u, temperature=torch.full((4,), inf, device="cuda"), return_details=True, **kw)
+    assert tok[0] == 0 and tok[3] == 1
+    if top_p is None:
+        assert tok.tolist() == [0, V // 2, V - 1, 1] and kept.tolist() == [V, V, V, 1]
+        assert torch.equal(prob, 1 / kept.float())
+    else:  # at most the last rank falls away
+        assert all(V - 1 <= n <= V for n in kept[:3].tolist())
