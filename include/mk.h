@@ -439,8 +439,11 @@ int mk_kv_view(const mk_kv* kv, int32_t layer, mk_pages* pages, mk_page_table* t
  * relative, 2^-20 of a score), less slopes[h] * (p - j):
  *   out = sum_j softmax(x)_j v_j,    lse = log sum_j exp(x_j).
  * A token that sees nothing (a padded sequence of length 0, p < 0, a start
- * past p) gets zeros and lse -infinity; values it does not see, NaN and
- * infinities among them, do not reach its row. Query head h reads kv head
+ * past p) gets zeros and lse -infinity; values and scales it does not see, NaN
+ * and infinities among them, do not reach its row. What it sees is taken to be
+ * below 2^100 in magnitude (sums of larger values may overflow), keys finite;
+ * an infinity in a bf16 value stays one, a scale that is not finite leaves the
+ * row no finite number. Query head h reads kv head
  * h / (n_q_heads / n_kv_heads).
  *
  * shared_len > 0 says that the first shared_len positions of all sequences
@@ -469,7 +472,11 @@ typedef struct mk_attention {
  * (they do not depend on lens). The workspace belongs to one call until the
  * call has run: calls that may overlap on the GPU (other streams, captured
  * graphs replayed side by side) take one each. Its contents need no
- * initialisation. Small calls need none (0 bytes). */
+ * initialisation. Small calls need none (0 bytes); others some MB, and calls of
+ * many tokens over long tables or with a shared prefix up to two 32-bit copies
+ * of the output besides (4096 tokens with 32 heads of 128: over 130 MB a sequence).
+ * The choice of kernels, and so the time, goes by these shapes too: by the
+ * table's width, not by lens. Columns that no length reaches cost time. */
 int mk_pages_attend_workspace(const mk_attention* args, int64_t* bytes);
 
 /* Errors: INVALID_ARG (NULL, shapes, alignment, a workspace too small or not

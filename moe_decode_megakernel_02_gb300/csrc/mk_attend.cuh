@@ -33,22 +33,23 @@
 // join through distributed shared memory: one launch, no workspace.
 //
 // Measured, 128-wide heads, 40 query heads on 8: 64 sequences of up to 32768
-// positions, E4M3, 483 us (5.8 TB/s, 87 % of what a copy reaches); 32 such in
-// bf16 392 us (6.9 TB/s); 64 sequences of up to 1024, bf16, 43 us (59 %: the
+// positions, E4M3, 490 us (5.8 TB/s, 86 % of what a copy reaches); 32 such in
+// bf16 396 us (6.9 TB/s); 64 sequences of up to 1024, bf16, 43 us (58 %: the
 // start, the join and the ends of pieces are 10 us of it). 16 query heads on 4:
-// one sequence of 4096 14 us, all latency; 8 sequences of 8192 with 7 new
-// tokens each (28 rows), E4M3 and capped scores, 37 us (12 %): issue and
+// one sequence of 4096 14.5 us, all latency; 8 sequences of 8192 with 7 new
+// tokens each (28 rows), E4M3 and capped scores, 40 us (12 %): issue and
 // latency of the conversions, exponentials and shuffles of 4 times the rows.
 //
 // Rounding. Scores and sums are 32-bit. bf16 pages: queries are exact in bf16
-// (16-bit floats: hi + lo parts), probabilities go in as hi + lo bf16 parts,
-// so a product keeps 16 bits. 8-bit pages: codes are exact in fp16; a query
+// (16-bit floats: hi + lo parts), probabilities go in as hi + lo bf16 parts
+// (split_bf16), so a product keeps 16 bits. 8-bit pages: codes are exact in fp16; a query
 // row is scaled by a power of two into fp16 (exact but for values 2^-24 below
 // the row's largest); the K scale multiplies the score, the V scale the
 // probability, which goes in as one fp16 (11 bits; hi + lo parts for fp16
 // outputs, whose own rounding is as fine), scaled by 2^15 over the largest V
-// scale so far: products below 2^-29 of the largest possible one fall under
-// fp16's normal range and keep steps of 2^-39 of it.
+// scale that the row has seen so far: products below 2^-29 of the largest
+// possible one fall under fp16's normal range and keep steps of 2^-39 of it.
+// (A unit for each row costs 1 % of a long context's time and 5 % of 28 rows'.)
 #pragma once
 #include <cooperative_groups.h>
 

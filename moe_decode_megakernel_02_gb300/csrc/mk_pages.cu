@@ -7,8 +7,9 @@
 //
 // Measured, 8 kv heads of 128, 16 ragged prompts of up to 4096 tokens: bf16
 // rows into INT8 58 us (4.5 TB/s of reads and writes, 68 % of what a copy
-// reaches; the instructions of the quotients bound it), E4M3 back to bf16
-// 65.5 us (6.2 TB/s, 93 %). One new token of 8 sequences: 2.5 us, a launch.
+// reaches), E4M3 back to bf16 65.9 us (6.2 TB/s, 92 %). The same into bf16 pages
+// 62 us (83 %), and back 81 us (99 %). One new token of 8 sequences: 2.8 us, a
+// launch.
 #include <type_traits>
 
 #include "mk_ops.cuh"
@@ -251,9 +252,11 @@ __device__ __forceinline__ void unit_of(const CopyP& p, int u, int& tok, int& h,
 // threads of a row lie in one warp and find its largest magnitude by shuffles,
 // K's and V's together where they fit one word. The rows are fetched before the
 // block knows where they go, so that the two trips to memory overlap. Reads 2
-// or 4 bytes a value, writes 1 + 4 / head_dim; bound by instructions (about 9 a
-// value, 3 of them the quotient), so a thread takes 16 values where rows allow:
-// 58 us in place of 73 for the prompts above.
+// or 4 bytes a value, writes 1 + 4 / head_dim, with 15.5 instructions a value (3
+// of them the quotient); a thread takes 16 values where rows allow: 58 us in
+// place of 73 for the prompts above. Neither issue (2.35 instructions a cycle of
+// 4) nor HBM (45 %) is full there: 1326 blocks for the some 600 that run at once
+// are 2.2 waves that cost 3, and a thread has one row in flight.
 template <int FMT, int DT, bool VEC, int G>
 __global__ void __launch_bounds__(CT, 3) write_kernel(const __grid_constant__ CopyP p) {
     constexpr int WAHEAD = G == 2 ? 1 : 2;

@@ -29,18 +29,22 @@
 // every role sees, and the CTA leaves after freeing its tensor memory
 // (MK_ERR_TIMEOUT in `status`, NaN in its rows).
 //
-// Bound by the products: Q K^T of 128 x 64 takes 48 cycles a 16-wide step (its
-// operands' shared-memory reads), the two chains of P V 64 each, 875 cycles a
-// tile of 128-wide heads (measured with nothing else running); 8192
-// exponentials at 16 a cycle are 512. 8-bit pages: bound by the four warps that
-// convert, about 2300 cycles a tile. Work is cut as in mk_attend.cuh; every
-// piece goes to the workspace for the joining launch.
+// Bound by latency: a tile of 128-wide heads takes about 2000 cycles (54 tiles a
+// CTA in 106,000, bf16). Q K^T of 128 x 64 takes 48 cycles a 16-wide step (its
+// operands' shared-memory reads), the two chains of P V 64 each, 875 cycles of
+// products (the tensor pipe is busy 39 % of the time); the tile's 2980 warp
+// instructions are 745 issue slots of each scheduler, 8192 exponentials at 16 a
+// cycle 512. What is left is the chain from a tile's scores to its
+// probabilities, of which two warps a scheduler are on the way. 8-bit pages: the
+// four warps that convert, 3400 (E4M3) to 4100 (INT8) cycles a tile. Work is cut
+// as in mk_attend.cuh; every piece goes to the workspace for the joining launch.
 //
 // Measured, 64 sequences on 16384 shared positions, 40 query heads on 8 of 128,
-// bf16: 43 us for this launch (0.75 PFLOP/s with both parts of P counted, 39 %
-// of a large product's rate), 88 us for the call with up to 1024 positions of each
-// sequence's own; INT8 116 us, fp16 queries 94 us. 256 tokens at 16384 positions
-// of one sequence, 16 query heads on 4: 83 us.
+// bf16: 50 us for this launch by a profiler that runs launches one by one (0.65
+// PFLOP/s with both parts of P counted, 34 % of a large product's rate), 91 us
+// for the call with up to 1024 positions of each sequence's own; INT8 118 us,
+// fp16 queries 99 us. 256 tokens at 16384 positions of one sequence, 16 query
+// heads on 4: 84 us.
 #pragma once
 #include <cuda.h>
 

@@ -33,10 +33,11 @@
 // 2500 cycles, as much as a pass: a row takes 2 (no filter), 3 (top-k) or 4
 // (top-p) of them, and every CTA works out what it can by itself.
 //
-// Measured: one fp32 row of 32000 with all filters 9.7 us, the latency of its
+// Measured: one fp32 row of 32000 with all filters 10 us, the latency of its
 // passes and meetings; 32 fp32 rows of 64000 with top-p 31 us; 256 bf16 rows
-// of 151936, each with its own settings, 99 us (0.78 TB/s, 12 % of a copy's
-// rate), with top-p on most rows 207. Bound by top-p's two passes over the half
+// of 151936, each with its own settings, 100 us (0.78 TB/s, 12 % of a copy's
+// rate), with top-p on three rows of four 203 and on all 255, top-k alone 77,
+// min-p alone 70, no filter 79. Bound by top-p's two passes over the half
 // of a normal row's tokens that its bound (1 - p) sum / V leaves (34,000 and
 // 27,000 of a row's 75,000 cycles: four shared-memory atomics and an exponential
 // a token), and by the meetings, in which a CTA's warps wait (a scheduler issues
@@ -981,9 +982,10 @@ extern "C" int mk_sample(const mk_sampling* a, void* stream) {
     p.V = a->vocab;
     // a slice of 2048 tokens keeps a CTA's threads busy with 4 each; where the
     // rows fill the device anyway, larger slices that still leave two CTAs an SM.
-    // Measured before the rows had an order: 256 bf16 rows of 151936 133 us so,
-    // 159 with 8 CTAs a row and 160 with slices that leave one CTA an SM; 200
-    // fp32 rows of 8000 25 us and, with 4 CTAs a row, 39
+    // 256 bf16 rows of 151936, a quarter of them with top-p over the whole
+    // vocabulary, take 115 us so, 170 with 8 CTAs a row and 121 with slices that
+    // leave one CTA an SM; 512 fp32 rows of 64000 159, 271 and 162; 200 fp32 rows
+    // of 8000 31, 47 and 27
     int C = MAXC;
     while (C > 1 && a->vocab <= 2048 * (C / 2)) C /= 2;
     int dev = 0;
