@@ -442,8 +442,8 @@ int mk_kv_view(const mk_kv* kv, int32_t layer, mk_pages* pages, mk_page_table* t
  * past p) gets zeros and lse -infinity; values and scales it does not see, NaN
  * and infinities among them, do not reach its row. What it sees is taken to be
  * below 2^100 in magnitude (sums of larger values may overflow), keys finite;
- * an infinity in a bf16 value stays one, a scale that is not finite leaves the
- * row no finite number. Query head h reads kv head
+ * an infinity in a bf16 value stays one (where its weight is not 0 in 32 bits),
+ * a scale that is not finite leaves the row no finite number. Query head h reads kv head
  * h / (n_q_heads / n_kv_heads).
  *
  * shared_len > 0 says that the first shared_len positions of all sequences

@@ -239,8 +239,9 @@ __device__ __forceinline__ float cap_any(float y, float cap) {
 }
 
 // Two probabilities as bf16 parts: hi cut off, lo the rest, rounded (16 bits
-// together). Neither is negative and lo is never 0, so that an infinity in V,
-// times both, stays that infinity (0 x inf is NaN, and so is inf - inf).
+// together). Neither is negative, and lo is not 0, so that an infinity in V,
+// times both parts of a probability above 0, stays that infinity (0 x inf is
+// NaN, and so is inf - inf).
 __device__ __forceinline__ void split_bf16(float x, float y, uint32_t& hi, uint32_t& lo) {
     hi = __byte_perm(__float_as_uint(x), __float_as_uint(y), 0x7632);
     lo = pack_bf16(x - __uint_as_float(__float_as_uint(x) & 0xffff0000u), y - __uint_as_float(__float_as_uint(y) & 0xffff0000u));
