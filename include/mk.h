@@ -518,6 +518,168 @@ typedef struct mk_sampling {
  * 360448). Deterministic: the same inputs give the same tokens. */
 int mk_sample(const mk_sampling* args, void* stream);
 
+/* ---------------------------------------------------------------------------
+ * Rotary positions, latent caches and prompts: what a latent-attention model
+ * needs around its projections, on the caller's memory, under the same
+ * conventions as the operators above.
+ * ------------------------------------------------------------------------- */
+
+/* A rotation by positions. Values 0 .. n-1 (n even, 2 to 256) form n/2 pairs,
+ *  MK_ROTARY_HALF   (x[i], x[i + n/2]);
+ *  MK_ROTARY_PAIRS  (x[2i], x[2i + 1]),
+ * and pair i at position p turns by a = p inv_freq[i] radians:
+ *   (x, y) -> magnitude (x cos a - y sin a, x sin a + y cos a),
+ * with `inverse` by -a (for magnitude 1 the way back, and the gradient's).
+ * inv_freq holds 64-bit numbers (finite) in device memory, so that scaled
+ * frequencies of any recipe are the caller's to choose; angles keep 2^-60 of a
+ * turn a position however far it is, negative positions turn the other way. */
+enum mk_rotary_layout { MK_ROTARY_HALF = 0, MK_ROTARY_PAIRS = 1 };
+typedef struct mk_rotary {
+    const double* inv_freq; /* device [n / 2] */
+    int32_t n, layout;
+    float magnitude;
+    int32_t inverse;
+} mk_rotary;
+
+/* Rows x [batch][n_tokens][n_heads][head_dim] with values first .. first+n-1
+ * of every head turned, to `out` (the same shape and type). `out` may be x
+ * itself (the same pointer and strides: the other values are then neither
+ * read nor written) and must not overlap it otherwise. Computed in 32 bits,
+ * rounded once. */
+typedef struct mk_rotation {
+    const mk_rotary* rotary;
+    const int32_t* positions; /* device [batch]: token t of sequence b is at positions[b] + t; */
+    int64_t position_stride;  /* or, when not 0: at positions[b * position_stride + t] */
+    const mk_rows *x, *out;
+    int32_t batch, n_tokens, n_heads, head_dim, first, reserved;
+} mk_rotation;
+
+/* Errors: INVALID_ARG (NULL, shapes, alignment). */
+int mk_rotate(const mk_rotation* args, void* stream);
+
+/* One layer's latent cache: position r of page p has its latent (rank values,
+ * keys and values of all heads in one vector) at p*page_stride + r*row_stride
+ * elements after `latent`, and its rope part (rope_dim values, the rotated key
+ * all heads share) at p*rope_page_stride + r*rope_row_stride after `rope`.
+ * Both are of type `dtype` (MK_DT_BF16 or MK_DT_F16); the pointers and strides
+ * are multiples of 16 bytes. rank is a multiple of 8 up to 1024, rope_dim of 8
+ * up to 256, page_size a power of two. Rows of different (page, row) must not
+ * overlap. */
+typedef struct mk_latent_pages {
+    void *latent, *rope;
+    int64_t page_stride, row_stride, rope_page_stride, rope_row_stride;
+    int32_t dtype, n_pages, page_size, rank, rope_dim, reserved;
+} mk_latent_pages;
+
+/* Appends rows of a down-projection to a latent cache: tokens t in
+ * [0, counts[b]) (counts: device int32 [batch]; NULL: all n) of sequence b go
+ * to positions positions[b] + t. A row is `rank` latent values, then rope_dim
+ * rope values (rows->head_stride is not used). With `gain` (device [rank], of
+ * type gain_dtype) the latent is normalised,
+ *   c_i = x_i / sqrt(mean x^2 + eps) gain_i,
+ * without (NULL) it is kept; with `rotary` (n = rope_dim) the rope part turns
+ * by its position, without (NULL) it is kept. In 32 bits (magnitudes below
+ * 2^60), rounded once. Rows past counts[b], and every other row of the cache,
+ * stay as they are; positions or pages out of range as in mk_pages_write.
+ * Errors: INVALID_ARG; UNSUPPORTED (rank, rope_dim, page_size). */
+int mk_latent_write(const mk_latent_pages* pages, const mk_page_table* table, const int32_t* positions,
+                    const int32_t* counts, int32_t n, const mk_rows* rows, const void* gain, int32_t gain_dtype,
+                    float eps, const mk_rotary* rotary, int32_t* status, void* stream);
+
+/* The latent cache of one layer of an MLA model and its block table (pages of
+ * 64 positions), as mk_kv_view for a GQA model. Errors: INVALID_ARG;
+ * UNSUPPORTED for GQA. */
+int mk_kv_latent_view(const mk_kv* kv, int32_t layer, mk_latent_pages* pages, mk_page_table* table);
+
+/* Attention of the last n_tokens positions of every sequence over its latent
+ * cache, in the latent space (the absorbed form): with c_j and r_j the latent
+ * and the rope part of position j,
+ *   x_j = scale (q . c_j + q_rope . r_j),
+ *   out = sum_j softmax(x)_j c_j,    lse = log sum_j exp(x_j),
+ * where q is the head's query taken through the key up-projection and `out` is
+ * to be taken through the value up-projection. lens, starts, what a token sees
+ * and what a token that sees nothing gets are as in mk_attention; latents that
+ * a token does not see, NaN and infinities among them, do not reach its row.
+ * What it sees is finite, scores below 2^100 in magnitude. Sums are 32-bit; a
+ * probability goes into the second product rounded to the cache's type. */
+typedef struct mk_latent_attention {
+    const mk_latent_pages* pages;
+    const mk_page_table* table;
+    const int32_t* lens;   /* device [batch] */
+    const int32_t* starts; /* device [batch], or NULL: 0 */
+    const mk_rows* q;      /* [batch][n_tokens][n_heads][rank], of the cache's type */
+    const mk_rows* q_rope; /* [batch][n_tokens][n_heads][rope_dim], the same type */
+    const mk_rows* out;    /* [batch][n_tokens][n_heads][rank], the same type, written */
+    float* lse;            /* device [batch][n_tokens][n_heads], or NULL */
+    int32_t* status;       /* device, or NULL */
+    int32_t n_tokens, n_heads;
+    float scale;
+    int32_t reserved;
+} mk_latent_attention;
+
+/* Bytes of device workspace mk_latent_attend needs for a call of these shapes
+ * (they do not depend on lens; 0 is possible). As mk_pages_attend_workspace. */
+int mk_latent_attend_workspace(const mk_latent_attention* args, int64_t* bytes);
+
+/* Errors, reports through `status` and waits as in mk_pages_attend;
+ * UNSUPPORTED for a rank other than 256 or 512, or a rope_dim other than 64. */
+int mk_latent_attend(const mk_latent_attention* args, void* workspace, int64_t workspace_bytes, void* stream);
+
+/* Causal attention of prompts over expanded keys and values (no cache): a
+ * ragged batch, sequence b's queries being rows q_starts[b] .. q_starts[b+1]-1
+ * of q and out, its keys rows k_starts[b] .. k_starts[b+1]-1 of k, k_rope and
+ * v. Its queries are the last of its positions: query i of n over m keys sees
+ * keys 0 .. m - n + i (the m - n before the first one are its context, such
+ * as earlier chunks). Per head,
+ *   x_j = scale (q[0 .. nope_dim-1] . k_j + q[nope_dim ..] . k_rope_j),
+ *   out = sum_j softmax(x)_j v_j,    lse = log sum_j exp(x_j);
+ * a query that sees nothing (n > m) gets zeros and lse -infinity. k_rope is
+ * shared by the heads. Keys and values behind a query's own do not reach its
+ * row; what it sees is finite, scores below 2^100. All pointers are multiples
+ * of 16 bytes, so are the strides. Rows of no sequence stay as they are. */
+typedef struct mk_prompt_attention {
+    const int32_t *q_starts, *k_starts; /* device [batch + 1], ascending */
+    const void *q, *k, *k_rope, *v;     /* [n_tokens][n_heads][nope+rope], [n_keys][n_heads][nope], [n_keys][rope], */
+    void* out;                          /* [n_keys][n_heads][v_dim]; [n_tokens][n_heads][v_dim], written */
+    float* lse;                         /* device [n_tokens][n_heads], or NULL */
+    int32_t* status;                    /* device, or NULL */
+    int64_t q_token, q_head, k_token, k_head, rope_token, v_token, v_head, out_token, out_head; /* strides, elements */
+    int32_t batch, n_tokens, n_keys, n_heads, nope_dim, rope_dim, v_dim, dtype;
+    float scale;
+    int32_t reserved;
+} mk_prompt_attention;
+
+/* Errors: INVALID_ARG; UNSUPPORTED (dims other than nope 128, rope 64, v 128).
+ * Bounds that descend or leave the rows are reported through `status` (as
+ * MK_ERR_INVALID_ARG) and the sequence is skipped. */
+int mk_prompt_attend(const mk_prompt_attention* args, void* stream);
+
+/* Log probabilities. With z = logits / temperature of a row and
+ * log p_i = z_i - log sum_j exp(z_j):
+ *   logprobs[r][g] = log p of token tokens[r][g] (NaN for an id outside the
+ *                    vocabulary; the same id may be given twice);
+ *   entropy[r]     = - sum_i p_i log p_i (a term of p = 0 counts 0);
+ *   top_ids[r], top_logprobs[r]: the `top` tokens of the largest logits, by
+ *                    (logit descending, id ascending), and their log p.
+ * -infinity masks a token (log p -infinity). A row with a NaN or +infinity,
+ * with no token unmasked, or whose temperature is not above 0, has no
+ * distribution: NaN, and ids -1. Sums are 32-bit. */
+typedef struct mk_logprob {
+    const void* logits;       /* device [rows][row_stride], `dtype` */
+    int64_t row_stride;       /* elements */
+    const float* temperature; /* device [rows], or NULL: 1 */
+    const int32_t* tokens;    /* device [rows][given]; NULL when given is 0 */
+    float* logprobs;          /* device [rows][given], written */
+    float* entropy;           /* device [rows], or NULL */
+    int32_t* top_ids;         /* device [rows][top], written; NULL when top is 0 */
+    float* top_logprobs;      /* device [rows][top], written */
+    int32_t rows, vocab, dtype, given, top, reserved;
+} mk_logprob;
+
+/* Errors: INVALID_ARG (NULL, sizes, alignment, top above vocab); UNSUPPORTED
+ * (top above 64). Deterministic. */
+int mk_logprobs(const mk_logprob* args, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -28,7 +28,9 @@ EXPORTS = ("mk_load_weights", "mk_load_synthetic", "mk_alloc_kv", "mk_kv_set_blo
            "mk_step_status",
            "mk_debug_routing", "mk_debug_scratch_read", "mk_last_argmax", "mk_model_info", "mk_trace_read", "mk_free",
            "mk_last_error",
-           "mk_pages_write", "mk_pages_read", "mk_pages_attend", "mk_pages_attend_workspace", "mk_kv_view", "mk_sample")
+           "mk_pages_write", "mk_pages_read", "mk_pages_attend", "mk_pages_attend_workspace", "mk_kv_view", "mk_sample",
+           "mk_rotate", "mk_latent_write", "mk_kv_latent_view", "mk_latent_attend", "mk_latent_attend_workspace",
+           "mk_prompt_attend", "mk_logprobs")
 TRACE_CAP = 8192
 
 
@@ -39,7 +41,8 @@ def build_cmds() -> list:
     os.makedirs(_BUILD, exist_ok=True)
     srcs = [os.path.join(_HERE, "csrc", f) for f in (
         "mk_host.cu", "mk_synth.cu", "mk_pages.cu", "mk_sample.cu", "mk_attend.cu", "mk_attend_d64.cu",
-        "mk_attend_d128.cu", "mk_attend_d256.cu", "mk_prefix.cu", "mk_prefix_f16.cu")]
+        "mk_attend_d128.cu", "mk_attend_d256.cu", "mk_prefix.cu", "mk_prefix_f16.cu", "mk_rotary.cu", "mk_latent.cu",
+        "mk_prompt.cu", "mk_logprobs.cu")]
     srcs += [os.path.join(_ROOT, "synth", "synth_cuda.cu"), os.path.join(_ROOT, "synth", "synth_host.c")]
     base = ["nvcc", "--threads", "0", "-gencode", "arch=compute_103a,code=sm_103a", "-O3", "-lineinfo", "-std=c++17",
             "-Xcompiler", "-fPIC", "-shared", "-lpthread"]
@@ -67,9 +70,10 @@ class Info(ctypes.Structure):
                                       "sm_count")]
 
 
-# mk_kv_format and mk_dtype
+# mk_kv_format, mk_dtype and mk_rotary_layout
 KV_BF16, KV_E4M3, KV_INT8 = 0, 1, 2
 DT_F32, DT_BF16, DT_F16 = 0, 1, 2
+ROTARY_HALF, ROTARY_PAIRS = 0, 1
 
 
 class PagesStruct(ctypes.Structure):
@@ -107,6 +111,54 @@ class SamplingStruct(ctypes.Structure):
     _fields_ = [("logits", ctypes.c_void_p), ("row_stride", ctypes.c_int64)] + [
         (n, ctypes.c_void_p) for n in ("u", "temperature", "top_k", "top_p", "min_p", "tokens", "probs", "kept")] + [
         (n, ctypes.c_int32) for n in ("rows", "vocab", "dtype", "reserved")]
+
+
+class RotaryStruct(ctypes.Structure):
+    """mk_rotary"""
+    _fields_ = [("inv_freq", ctypes.c_void_p), ("n", ctypes.c_int32), ("layout", ctypes.c_int32),
+                ("magnitude", ctypes.c_float), ("inverse", ctypes.c_int32)]
+
+
+class RotationStruct(ctypes.Structure):
+    """mk_rotation"""
+    _fields_ = [("rotary", ctypes.POINTER(RotaryStruct)), ("positions", ctypes.c_void_p),
+                ("position_stride", ctypes.c_int64), ("x", ctypes.POINTER(RowsStruct)),
+                ("out", ctypes.POINTER(RowsStruct))] + [
+        (n, ctypes.c_int32) for n in ("batch", "n_tokens", "n_heads", "head_dim", "first", "reserved")]
+
+
+class LatentPagesStruct(ctypes.Structure):
+    """mk_latent_pages"""
+    _fields_ = [(n, ctypes.c_void_p) for n in ("latent", "rope")] + [
+        (n, ctypes.c_int64) for n in ("page_stride", "row_stride", "rope_page_stride", "rope_row_stride")] + [
+        (n, ctypes.c_int32) for n in ("dtype", "n_pages", "page_size", "rank", "rope_dim", "reserved")]
+
+
+class LatentAttentionStruct(ctypes.Structure):
+    """mk_latent_attention"""
+    _fields_ = [("pages", ctypes.POINTER(LatentPagesStruct)), ("table", ctypes.POINTER(TableStruct))] + [
+        (n, ctypes.c_void_p) for n in ("lens", "starts")] + [
+        (n, ctypes.POINTER(RowsStruct)) for n in ("q", "q_rope", "out")] + [
+        (n, ctypes.c_void_p) for n in ("lse", "status")] + [
+        ("n_tokens", ctypes.c_int32), ("n_heads", ctypes.c_int32), ("scale", ctypes.c_float),
+        ("reserved", ctypes.c_int32)]
+
+
+class PromptAttentionStruct(ctypes.Structure):
+    """mk_prompt_attention"""
+    _fields_ = [(n, ctypes.c_void_p) for n in ("q_starts", "k_starts", "q", "k", "k_rope", "v", "out", "lse",
+                                               "status")] + [
+        (n, ctypes.c_int64) for n in ("q_token", "q_head", "k_token", "k_head", "rope_token", "v_token", "v_head",
+                                      "out_token", "out_head")] + [
+        (n, ctypes.c_int32) for n in ("batch", "n_tokens", "n_keys", "n_heads", "nope_dim", "rope_dim", "v_dim",
+                                      "dtype")] + [("scale", ctypes.c_float), ("reserved", ctypes.c_int32)]
+
+
+class LogprobStruct(ctypes.Structure):
+    """mk_logprob"""
+    _fields_ = [("logits", ctypes.c_void_p), ("row_stride", ctypes.c_int64)] + [
+        (n, ctypes.c_void_p) for n in ("temperature", "tokens", "logprobs", "entropy", "top_ids", "top_logprobs")] + [
+        (n, ctypes.c_int32) for n in ("rows", "vocab", "dtype", "given", "top", "reserved")]
 
 
 class MKError(RuntimeError):
@@ -152,11 +204,20 @@ def lib():
         L.mk_pages_attend_workspace.argtypes = [P, P]
         L.mk_kv_view.argtypes = [P, I32, P, P]
         L.mk_sample.argtypes = [P, P]
+        L.mk_rotate.argtypes = [P, P]
+        L.mk_latent_write.argtypes = [P, P, P, P, I32, P, P, I32, ctypes.c_float, P, P, P]
+        L.mk_kv_latent_view.argtypes = [P, I32, P, P]
+        L.mk_latent_attend.argtypes = [P, P, ctypes.c_int64, P]
+        L.mk_latent_attend_workspace.argtypes = [P, P]
+        L.mk_prompt_attend.argtypes = [P, P]
+        L.mk_logprobs.argtypes = [P, P]
         for f in ("mk_load_weights", "mk_load_synthetic", "mk_alloc_kv", "mk_kv_set_block_table", "mk_kv_write",
                   "mk_kv_read", "mk_decode_step", "mk_decode_step_unfused", "mk_decode_step_noalloc", "mk_step_status",
                   "mk_debug_routing",
                   "mk_debug_scratch_read", "mk_last_argmax", "mk_model_info", "mk_trace_read", "mk_pages_write",
-                  "mk_pages_read", "mk_pages_attend", "mk_pages_attend_workspace", "mk_kv_view", "mk_sample"):
+                  "mk_pages_read", "mk_pages_attend", "mk_pages_attend_workspace", "mk_kv_view", "mk_sample",
+                  "mk_rotate", "mk_latent_write", "mk_kv_latent_view", "mk_latent_attend",
+                  "mk_latent_attend_workspace", "mk_prompt_attend", "mk_logprobs"):
             getattr(L, f).restype = ctypes.c_int
         _lib = L
     return _lib
@@ -319,6 +380,12 @@ class KVCache:
         (mk_kv_view; GQA models). They hold until the cache is closed."""
         from . import pages
         return pages.of_cache(self, layer)
+
+    def latent_pages(self, layer):
+        """The layer's latent cache as a `latent.LatentPages` over the cache's own memory, with its block table as
+        `.table` (mk_kv_latent_view; MLA models). It holds until the cache is closed."""
+        from . import latent
+        return latent.of_cache(self, layer)
 
     def close(self):
         if getattr(self, "h", None):

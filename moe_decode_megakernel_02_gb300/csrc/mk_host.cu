@@ -1090,6 +1090,27 @@ int mk_kv_view(const mk_kv* kv, int32_t layer, mk_pages* pages, mk_page_table* t
     return MK_OK;
 }
 
+int mk_kv_latent_view(const mk_kv* kv, int32_t layer, mk_latent_pages* pages, mk_page_table* table) {
+    if (!kv || kv->magic != KV_MAGIC || !pages || !table) return fail(MK_ERR_INVALID_ARG, "bad kv, pages or table");
+    const Dims D = dims_of(kv->m->cfg);
+    if (layer < 0 || layer >= D.L) return fail(MK_ERR_INVALID_ARG, "layer %d out of range", layer);
+    if (D.gqa) return fail(MK_ERR_UNSUPPORTED, "kv latent view: GQA pages hold K and V");
+    // a page is [PAGE][latent], then [PAGE][rope]
+    *pages = mk_latent_pages{};
+    pages->latent = kv->pool + (size_t)layer * kv->layer_elems;
+    pages->rope = (uint16_t*)pages->latent + (size_t)mk::PAGE * D.kl;
+    pages->page_stride = pages->rope_page_stride = (int64_t)kv->page_elems;
+    pages->row_stride = D.kl;
+    pages->rope_row_stride = D.rd;
+    pages->dtype = MK_DT_BF16;
+    pages->n_pages = kv->batch * kv->pps;
+    pages->page_size = mk::PAGE;
+    pages->rank = D.kl;
+    pages->rope_dim = D.rd;
+    *table = mk_page_table{kv->btab, kv->pps, kv->batch, kv->pps};
+    return MK_OK;
+}
+
 int mk_kv_read(const mk_kv* kv, int32_t layer, int32_t seq, int32_t pos0, int32_t n, void* rows, void* stream) {
     return kv_copy(kv, layer, seq, pos0, n, rows, stream, 0);
 }

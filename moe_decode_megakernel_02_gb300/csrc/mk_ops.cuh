@@ -43,6 +43,10 @@ inline bool off_by4(const P*... p) {
 
 // what every operator on pages asks of its cache and table
 int check_pages(const mk_pages* p, const mk_page_table* t);
+int check_latent(const mk_latent_pages* p, const mk_page_table* t);
+int check_rows(const mk_rows* r, const char* name);
+// whether rows can be read 16 bytes at a time
+bool rows_vec(const mk_rows* r);
 
 __device__ __forceinline__ float bf2f(uint32_t h) { return __uint_as_float(h << 16); }
 __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {

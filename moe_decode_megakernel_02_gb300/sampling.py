@@ -1,7 +1,7 @@
-"""Tokens from logits: mk_sample (include/mk.h), and a decode loop that samples.
+"""Tokens from logits and their probabilities: mk_sample and mk_logprobs (include/mk.h), and a decode loop that samples.
 
-`sample` is the operator; `SampledLoop` runs a loaded model with it, one
-token a sequence and step, every step on the device.
+`sample` and `logprobs` are the operators; `SampledLoop` runs a loaded model
+with them, one token a sequence and step, every step on the device.
 """
 from __future__ import annotations
 
@@ -10,11 +10,12 @@ import struct
 
 import torch
 
-from . import MKError, SamplingStruct, _check, lib
+from . import LogprobStruct, MKError, SamplingStruct, _check, lib
 from .pages import _DTYPE, _launch, _ptr
 
 _SAMPLING = struct.Struct("Pq PPPPP PPP iiii")
-assert _SAMPLING.size == ctypes.sizeof(SamplingStruct)
+_LOGPROB = struct.Struct("Pq PPPPPP iiiiii")
+assert _SAMPLING.size == ctypes.sizeof(SamplingStruct) and _LOGPROB.size == ctypes.sizeof(LogprobStruct)
 
 
 def sample(logits, u, temperature=None, top_k=None, top_p=None, min_p=None, out=None, return_details=False,
@@ -58,16 +59,59 @@ def _sample(h, logits, args, out, details, n, R, V, dt):
     return (tokens, probs, kept) if details else tokens
 
 
+def logprobs(logits, tokens, top=0, temperature=None, stream=None):
+    """Log probabilities of given tokens under `logits` ([rows, vocab], float32, bfloat16 or float16), divided by
+    `temperature` (float32 [rows]) when given.
+
+    tokens: int32 [rows] or [rows, given], or None; top: how many of the most probable tokens to name (at most 64).
+    Returns (log probabilities, float32 shaped as tokens, or None; entropies, float32 [rows]; the top tokens, int32
+    [rows, top], by descending logit, the lower id first where logits are equal; their log probabilities, float32
+    [rows, top]). An id outside the vocabulary gets NaN. -inf masks a token; a row with a NaN, +inf, no unmasked token
+    or a temperature that is not above 0 gives NaN throughout, and ids -1."""
+    dt = _DTYPE.get(logits.dtype)
+    if dt is None or logits.dim() != 2 or not logits.is_cuda or (logits.stride(1) != 1 and logits.shape[1] > 1):
+        raise ValueError("logits must be a float32, bfloat16 or float16 CUDA tensor [rows, vocab] with contiguous rows, "
+                         f"got {logits.dtype} {tuple(logits.shape)} strides {logits.stride()} on {logits.device}")
+    dev, n = logits.device, logits.shape[:1]
+    given = 0
+    if tokens is not None:
+        if tokens.dim() not in (1, 2):
+            raise ValueError(f"tokens must be [rows] or [rows, given], got {tuple(tokens.shape)}")
+        _ptr(tokens, "tokens", n + tokens.shape[1:], torch.int32, dev)
+        given = tokens.shape[1] if tokens.dim() == 2 else 1
+    t = 0 if temperature is None else _ptr(temperature, "temperature", n, torch.float32, dev)
+    if not 0 <= top <= logits.shape[1]:
+        raise ValueError(f"top must be between 0 and the vocabulary's {logits.shape[1]}, got {top}")
+    return _launch(dev, stream, _logprobs, (logits, tokens, given, top, t, dt))
+
+
+def _logprobs(h, logits, tokens, given, top, t, dt):
+    dev, (R, V) = logits.device, logits.shape
+    out = None if tokens is None else torch.empty(tokens.shape, dtype=torch.float32, device=dev)
+    entropy = torch.empty((R,), dtype=torch.float32, device=dev)
+    ids = torch.empty((R, top), dtype=torch.int32, device=dev)
+    best = torch.empty((R, top), dtype=torch.float32, device=dev)
+    if R:
+        a = _LOGPROB.pack(logits.data_ptr(), logits.stride(0), t, tokens.data_ptr() if given else 0,
+                          out.data_ptr() if given else 0, entropy.data_ptr(), ids.data_ptr() if top else 0,
+                          best.data_ptr() if top else 0, R, V, dt, given, top, 0)
+        rc = lib().mk_logprobs(a, h)
+        if rc:
+            _check(rc)
+    return out, entropy, ids, best
+
+
 class SampledLoop:
     """Sampled decoding of `batch` sequences, one token each a step.
 
     model, kv: a loaded `Model` and its `KVCache`; first_tokens[b] is the last token known of sequence b, to be
     written at positions[b]. generator: a torch.Generator of the device (the random numbers), or None for torch's
     own. temperature, top_k, top_p, min_p: a number for all sequences, one a sequence, or None. The drawn tokens
-    feed the next step on the device; the host reads them when `tokens()` is called."""
+    feed the next step on the device; the host reads them when `tokens()` is called. logprobs: with a number, every
+    step also keeps its tokens' log probabilities under the model's own logits, and as many alternatives (0: none)."""
 
     def __init__(self, model, kv, first_tokens, positions, vocab, temperature=None, top_k=None, top_p=None, min_p=None,
-                 generator=None, device="cuda"):
+                 generator=None, device="cuda", logprobs=None):
         B = len(first_tokens)
         if len(positions) != B or B < 1:
             raise ValueError("one position per sequence")
@@ -92,7 +136,10 @@ class SampledLoop:
         self.u = torch.empty((B,), dtype=torch.float32, device=device)
         self.settings = dict(temperature=each(temperature, torch.float32), top_k=each(top_k, torch.int32),
                              top_p=each(top_p, torch.float32), min_p=each(min_p, torch.float32))
+        if logprobs is not None and not 0 <= logprobs <= min(64, int(vocab)):
+            raise ValueError(f"logprobs must be None or a number of alternatives up to {min(64, int(vocab))}, got {logprobs}")
         self.emitted = []
+        self.top, self.scored = logprobs, []
         self.failed = None  # the error of a step, from then on
 
     def step(self):
@@ -105,12 +152,30 @@ class SampledLoop:
         self.tok = drawn.reshape(self.B, 1)
         self.pos = self.pos + 1
         self.emitted.append(drawn)
+        if self.top is not None:
+            self.scored.append(logprobs(self.logits, drawn, top=self.top))
         return drawn
 
     def tokens(self):
         """The tokens drawn so far, [batch][steps], after checking the steps' device status. After a failed step (a row
         without a distribution, whose token -1 the next step refuses, or a position past the cache) it raises, and so
         do later calls: what was drawn from there on came from old logits."""
+        self._settle()
+        return torch.stack(self.emitted, dim=1).cpu().tolist() if self.emitted else [[] for _ in range(self.B)]
+
+    def logprobs(self):
+        """What the steps so far kept of their tokens' probabilities (a loop made with `logprobs`): (log probabilities
+        [batch, steps], entropies [batch, steps], alternatives [batch, steps, n], their log probabilities), tensors on
+        the host. Fails as `tokens()` does."""
+        if self.top is None:
+            raise ValueError("the loop was made without logprobs")
+        self._settle()
+        if not self.scored:
+            return (torch.empty((self.B, 0)), torch.empty((self.B, 0)),
+                    torch.empty((self.B, 0, self.top), dtype=torch.int32), torch.empty((self.B, 0, self.top)))
+        return tuple(torch.stack(x, dim=1).cpu() for x in zip(*self.scored))
+
+    def _settle(self):
         if not self.failed:
             try:
                 self.model.check()
@@ -118,4 +183,3 @@ class SampledLoop:
                 self.failed = e
         if self.failed:
             raise self.failed
-        return torch.stack(self.emitted, dim=1).cpu().tolist() if self.emitted else [[] for _ in range(self.B)]
