@@ -53,7 +53,7 @@
 #pragma once
 #include <cooperative_groups.h>
 
-#include "mk_ops.cuh"
+#include "mk_tensor.cuh"
 
 namespace mkop {
 
@@ -102,7 +102,6 @@ struct JoinP {
 
 constexpr int MAX_CLUSTER = 8;
 constexpr int JT = 128;  // threads of a joining CTA
-constexpr float LOG2E = 1.4426950408889634f, LN2 = 0.6931471805599453f;
 
 // units (tiles) of each CTA when `total` are shared out over `grid`
 // (the host keeps totals below 2^30)
@@ -163,7 +162,6 @@ __device__ __forceinline__ int cover_units(const AttendP& p, int b) {
     return n;
 }
 
-__device__ __forceinline__ uint32_t sm32(const void* p) { return (uint32_t)__cvta_generic_to_shared(p); }
 __device__ __forceinline__ void cp16(uint32_t dst, const void* src, bool ok) {
     const int n = ok ? 16 : 0;  // 0: the 16 bytes are filled with zeros, nothing is read
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
@@ -204,11 +202,6 @@ __device__ __forceinline__ void mma(float (&d)[4], const uint32_t (&a)[4], uint3
 __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
     uint32_t y;
     asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
-    return y;
-}
-__device__ __forceinline__ float ex2(float x) {
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
 }
 __device__ __forceinline__ float rcp(float x) {

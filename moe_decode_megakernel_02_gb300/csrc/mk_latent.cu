@@ -1,5 +1,42 @@
 // mk_latent.cu -- attention over a paged latent cache, in the latent space
 // (mk_latent_attend).
+//
+// For one query row (a token and a head) and the positions j it sees,
+//   x_j = scale (q . c_j + q_rope . r_j),  m = max x_j,
+//   out = sum_j e^(x_j - m) c_j / sum_j e^(x_j - m):
+// one vector a position is key and value of all heads, so the rows of all heads
+// (and of a few tokens) stand against one copy of it, up to 64 rows a CTA. A
+// tile of positions lies in shared memory once, in the 128-byte-swizzled order
+// of tensor maps, and feeds both products on the fifth-generation tensor cores:
+//   S  = Q C^T      64 rows x the tile's positions, over rank + 64 values;
+//   O' = C^T P^T    rank values x rows: the output transposed, C as the
+//                   operand whose rows are the sum's (as it lies there), so
+//                   that up to 64 rows of 512 outputs take 256 columns of
+//                   tensor memory and few rows cost few of them.
+//
+// Roles: four warps softmax (S comes as 16-row fragments, a quad of threads a
+// row; P goes back through shared memory, rounded to the cache's type: what it
+// loses, half a step of each weight, is of the output's own rounding), one warp
+// copies, one cleans (below), two issue S and O'. O' is rescaled only when some
+// row's maximum has risen by more than 2^8 since its reference.
+//
+// Tiles at the ends of what is seen: scores are masked, and since 0 x NaN is
+// NaN, a warp zeroes the rows of such a tile that no row of the block sees. A
+// position that only some rows see (a later token of the block) and that is not
+// finite is zeroed too, and rows that do see it get NaN.
+//
+// Work is cut by tiles of all (sequence, row block) items in one line, an equal
+// stretch a CTA; pieces of an item leave (output, maximum, sum) in the workspace
+// and a second launch joins them. All waits have a limit, after which the CTA
+// frees its tensor memory and leaves (MK_ERR_TIMEOUT in `status`, NaN in its
+// rows).
+//
+// Pages of fewer than 8 positions, or overlapping ones (a stride of 0), have no
+// tensor map: a block a row takes them, a position a warp at a time.
+#include <climits>
+#include <mutex>
+
+#include "mk_tensor.cuh"
 #include "mk_values.cuh"
 
 namespace {
@@ -20,6 +57,16 @@ struct LatentP {
     int* status;
     int pps, ps_shift, n_pages, B, T, H;
     float scale;
+    // the tensor cores' kernel
+    int nr;          // rows of a block, padded to 16
+    int rows_blk;    // rows of a block
+    int RB;          // row blocks of a sequence
+    int stages;      // tiles in flight
+    int min_units;   // a CTA's least stretch of tiles
+    float* slots;    // two of each CTA: its first and its last piece
+    int* base;       // [items + 1]: first tile of each item, for the joining launch
+    unsigned wait_ns;
+    int skip_signal;  // for tests: a role's signals are left out
 };
 
 constexpr int LT = 128;
@@ -101,6 +148,710 @@ __global__ void __launch_bounds__(LT) latent_rows(const __grid_constant__ Latent
     if (threadIdx.x == 0 && p.lse) p.lse[row] = ll == 0.f ? -INFINITY : mm + logf(ll);
 }
 
+
+// ---------------------------------------------------------------- tensor cores
+
+constexpr int NT = 256, SMEM_MOST = 227 * 1024;
+
+// A sequence's row block and the tiles its rows see.
+template <int TILE>
+struct Item {
+    int b, rb, row0, rows;  // rows of the block: row0 .. row0 + rows - 1, token-major
+    int lo, hi, common;     // positions: [lo, hi) are seen by some row, [lo, common) by all
+    int t0, n;              // first tile, tiles
+    __device__ __forceinline__ void set(const LatentP& p, int item) {
+        b = item / p.RB;
+        rb = item - b * p.RB;
+        row0 = rb * p.rows_blk;
+        rows = min(p.rows_blk, p.T * p.H - row0);
+        const long long cap = (long long)p.pps << p.ps_shift, behind = (long long)p.lens[b] - p.T + 1;
+        lo = max(p.starts ? p.starts[b] : 0, 0);
+        hi = (int)max(0ll, min(behind + (row0 + rows - 1) / p.H, cap));
+        common = (int)max(0ll, min(behind + row0 / p.H, cap));
+        t0 = lo / TILE;
+        n = hi > lo ? (hi + TILE - 1) / TILE - t0 : 0;
+    }
+};
+
+template <int TILE>
+struct Line {  // a role's place in the line of tiles
+    Item<TILE> it;
+    int item, tile;
+    __device__ __forceinline__ void start(const LatentP& p, int i, int t) {
+        item = i;
+        tile = t;
+        it.set(p, i);
+    }
+    // k tiles on; behind the last item is one without an end
+    __device__ __forceinline__ void on(const LatentP& p, int k) {
+        tile += k;
+        while (tile >= it.n) {
+            tile -= it.n;
+            if (++item >= p.B * p.RB) it.n = INT_MAX, it.hi = 0;
+            else it.set(p, item);
+        }
+    }
+    __device__ __forceinline__ int at() const { return (it.t0 + tile) * TILE; }
+};
+
+// a ring's stage, its turn, and the tile's number
+struct Spot {
+    int stage = 0;
+    unsigned turn = 0, c = 0;
+    __device__ __forceinline__ void next(int stages) {
+        ++c;
+        if (++stage == stages) stage = 0, ++turn;
+    }
+    __device__ __forceinline__ int buf() const { return (int)(c & 1u); }
+    __device__ __forceinline__ unsigned full() const { return turn & 1u; }
+    __device__ __forceinline__ unsigned free() const { return (turn - 1) & 1u; }
+    __device__ __forceinline__ unsigned pair() const { return c >> 1 & 1u; }
+    __device__ __forceinline__ unsigned pair_free() const { return ((c >> 1) - 1) & 1u; }
+};
+
+struct LatentMisc {
+    unsigned long long kv_full[12], v_ok[12], pv_done[12], s_full[2], s_free[2], p_ready[2], q_ready, drained;
+    unsigned tmem, abort;
+    int scan[NT / 32], found_item, found_base;
+    int bad[16];           // of a piece: the first position of it that is not finite and that only some rows see
+    float m[64], f[64];    // of a row: its maximum, its factor
+    float sum[64];
+};
+
+template <int MT, int TILE>
+struct LatentShape {
+    static constexpr int RANK = 128 * MT, KP = 2 * MT + 1;  // 128-byte panels of a position
+    static constexpr int STAGE_B = KP * TILE * 128;
+    static constexpr int MISC_B = 1984;
+    static constexpr int T_S = 0, T_O = 128, T_ALL = 512;
+    // shared memory: queries, the ring, probabilities, the rest; and room to align to 1024
+    static int stages(int nr) {
+        const int n = (SMEM_MOST - 1024 - MISC_B - KP * nr * 128 - nr * 128) / STAGE_B;
+        return n < 12 ? n : 12;
+    }
+    static int smem(int nr) { return 1024 + MISC_B + KP * nr * 128 + nr * 128 + stages(nr) * STAGE_B; }
+    static_assert(sizeof(LatentMisc) <= MISC_B, "");
+};
+
+struct LatentMaps {
+    CUtensorMap latent, rope;
+};
+
+template <bool F16>
+__device__ __forceinline__ uint32_t pack16(float lo, float hi) {
+    return F16 ? pack_f16(lo, hi) : pack_bf16(lo, hi);
+}
+template <bool F16>
+__device__ __forceinline__ void put16(uint8_t* out, long long at, float x) {
+    if constexpr (F16) reinterpret_cast<__half*>(out)[at] = __float2half_rn(x);
+    else reinterpret_cast<__nv_bfloat16*>(out)[at] = __float2bfloat16_rn(x);
+}
+// one 32-bit word with either 16-bit half not finite
+template <bool F16>
+__device__ __forceinline__ bool not_finite(uint32_t w) {
+    constexpr uint32_t E = F16 ? 0x7c00u : 0x7f80u;
+    return (w & E) == E || (w & (E << 16)) == E << 16;
+}
+
+template <int MT, int TILE, bool F16>
+__global__ void __launch_bounds__(NT, 1)
+    latent_kernel(const __grid_constant__ LatentP p, const __grid_constant__ LatentMaps maps) {
+    using S = LatentShape<MT, TILE>;
+    extern __shared__ uint8_t raw_smem[];
+    uint8_t* const smem = raw_smem + ((1024u - (sm32(raw_smem) & 1023u)) & 1023u);
+    const int nr = p.nr, q_b = S::KP * nr * 128, stages = p.stages;
+    const uint32_t qs = sm32(smem), ring = qs + q_b, ps = ring + stages * S::STAGE_B;
+    uint8_t* const psm = smem + q_b + stages * S::STAGE_B;
+    LatentMisc& ms = *reinterpret_cast<LatentMisc*>(psm + nr * 128);
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const Limit limit = {&ms.abort, p.wait_ns};
+
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    // the line: each thread counts a stretch of items; sums before it by shuffles
+    const int items = p.B * p.RB, each = (items + NT - 1) / NT, i0 = min(items, tid * each), i1 = min(items, i0 + each);
+    int mine = 0;
+    for (int i = i0; i < i1; ++i) {
+        Item<TILE> it;
+        it.set(p, i);
+        mine += it.n;
+    }
+    int inc = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int a = __shfl_up_sync(0xffffffffu, inc, o);
+        if (lane >= o) inc += a;
+    }
+    if (lane == 31) ms.scan[warp] = inc;
+    if (tid == 0) {
+        for (int i = 0; i < stages; ++i) {
+            bar_init(&ms.kv_full[i], 1);
+            bar_init(&ms.v_ok[i], 1);
+            bar_init(&ms.pv_done[i], 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            bar_init(&ms.s_full[i], 1);
+            bar_init(&ms.s_free[i], 128);
+            bar_init(&ms.p_ready[i], 128);
+        }
+        bar_init(&ms.q_ready, 128);
+        bar_init(&ms.drained, 2);
+        ms.abort = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    if (warp == 5) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(sm32(&ms.tmem)),
+                     "n"(S::T_ALL)
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    }
+    __syncthreads();
+    int before = inc - mine, total = 0;
+#pragma unroll
+    for (int w = 0; w < NT / 32; ++w) {
+        if (w < warp) before += ms.scan[w];
+        total += ms.scan[w];
+    }
+    const int per = max((total + (int)gridDim.x - 1) / (int)gridDim.x, p.min_units);
+    const int first = per * blockIdx.x, end = min(total, first + per);
+    if (blockIdx.x == 0 || (first >= before && first < before + mine)) {
+        int at = before;
+        for (int i = i0; i < i1; ++i) {
+            Item<TILE> it;
+            it.set(p, i);
+            if (blockIdx.x == 0) {
+                p.base[i] = at;  // for the joining launch
+                if (it.rb == 0 && p.status && (long long)p.lens[it.b] > (long long)p.pps << p.ps_shift)
+                    *p.status = MK_ERR_INVALID_ARG;
+            }
+            if (first >= at && first < at + it.n) ms.found_item = i, ms.found_base = at;
+            at += it.n;
+        }
+    }
+    if (blockIdx.x == 0 && tid == 0) p.base[items] = total;
+    tm_before();
+    __syncthreads();
+    tm_after();
+    const uint32_t tm = ms.tmem;
+    int sent = 0;  // tiles that the copying warp has asked for
+    if (first < end) {
+        Line<TILE> w;
+        w.start(p, ms.found_item, first - ms.found_base);
+        if (warp < 4) {
+            // ================ softmax, and the pieces' ends ================
+            const int r0 = 16 * warp + (lane >> 2);  // this thread's rows: r0 and r0 + 8
+            const bool act = 16 * warp < nr;
+            const uint32_t my = tm + ((uint32_t)(warp * 32) << 16);
+            const float scale2 = p.scale * LOG2E;
+            Spot at_c, back;
+            bool ok = true;
+            unsigned piece = 0;
+            for (int u = first; u < end; ++piece) {
+                const int take = min(w.it.n - w.tile, end - u);
+                const Item<TILE>& it = w.it;
+                // queries: every product that read the last ones has ended (all its scores came)
+                for (int i = tid; i < nr * (S::KP * 8); i += 128) {
+                    const int r = i / (S::KP * 8), c = i - r * (S::KP * 8), g = it.row0 + r;
+                    uint4 x = make_uint4(0, 0, 0, 0);
+                    if (r < it.rows) {
+                        const int t = g / p.H, h = g - t * p.H;
+                        const uint8_t* src =
+                            c < 16 * MT ? p.q + 2 * (it.b * p.qb + t * p.qt + h * p.qh + 8 * c)
+                                        : p.qr + 2 * (it.b * p.rb + t * p.rt + h * p.rh + 8 * (c - 16 * MT));
+                        if (((uintptr_t)src & 15) == 0) {
+                            x = *reinterpret_cast<const uint4*>(src);
+                        } else {
+                            const uint16_t* s2 = reinterpret_cast<const uint16_t*>(src);
+                            x = make_uint4(s2[0] | (uint32_t)s2[1] << 16, s2[2] | (uint32_t)s2[3] << 16,
+                                           s2[4] | (uint32_t)s2[5] << 16, s2[6] | (uint32_t)s2[7] << 16);
+                        }
+                    }
+                    *reinterpret_cast<uint4*>(smem + panel_at(0, nr, r, c)) = x;
+                }
+                fence_async();
+                bar_arrive(&ms.q_ready);
+                int last[2];
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    const int r = r0 + 8 * i;
+                    const long long x = (long long)p.lens[it.b] - p.T + (it.row0 + r) / p.H;
+                    last[i] = r < it.rows ? (int)max(-1ll, min(x, (long long)it.hi - 1)) : -1;
+                }
+                float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
+                for (int i = 0; i < take; ++i) {
+                    const int j0 = (it.t0 + w.tile + i) * TILE;
+                    float x[2][TILE / 4];  // of row r0 and r0 + 8: columns 8 k + 2 (lane % 4) + {0, 1}
+                    ok = ok && warp_wait(&ms.s_full[at_c.buf()], at_c.pair(), limit);
+                    tm_after();
+                    if (act) {
+#pragma unroll
+                        for (int h = 0; h < TILE / 32; ++h) {
+                            uint32_t s[16];
+                            tm_frag32(s, my + S::T_S + at_c.buf() * TILE + 32 * h);
+                            tm_wait_ld();
+#pragma unroll
+                            for (int k = 0; k < 4; ++k) {
+                                x[0][8 * h + 2 * k] = __uint_as_float(s[4 * k]) * scale2;
+                                x[0][8 * h + 2 * k + 1] = __uint_as_float(s[4 * k + 1]) * scale2;
+                                x[1][8 * h + 2 * k] = __uint_as_float(s[4 * k + 2]) * scale2;
+                                x[1][8 * h + 2 * k + 1] = __uint_as_float(s[4 * k + 3]) * scale2;
+                            }
+                        }
+                    }
+                    tm_before();
+                    bar_arrive(&ms.s_free[at_c.buf()]);
+                    float mx[2] = {-INFINITY, -INFINITY};
+                    bool rise = false;
+                    if (act) {
+                        if (j0 < it.lo || j0 + TILE > it.common) {
+#pragma unroll
+                            for (int k = 0; k < TILE / 4; ++k) {
+                                const int j = j0 + 8 * (k >> 1) + 2 * (lane & 3) + (k & 1);
+                                if (j < it.lo || j > last[0]) x[0][k] = -INFINITY;
+                                if (j < it.lo || j > last[1]) x[1][k] = -INFINITY;
+                            }
+                        }
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+                            float a = x[e][0], b = x[e][1];
+#pragma unroll
+                            for (int k = 2; k < TILE / 4; k += 2) a = fmaxf(a, x[e][k]), b = fmaxf(b, x[e][k + 1]);
+                            a = fmaxf(a, b);
+                            a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, 1));
+                            mx[e] = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, 2));
+                        }
+                        rise = mx[0] > m[0] + 8.f || mx[1] > m[1] + 8.f;
+                    }
+                    if (i == 0) {
+                        m[0] = mx[0], m[1] = mx[1];
+                    } else if (bar_any(1, 128, rise)) {
+                        // rows whose maximum rose: their outputs so far shrink
+                        if (act) {
+#pragma unroll
+                            for (int e = 0; e < 2; ++e) {
+                                const float mn = mx[e] > m[e] + 8.f ? mx[e] : m[e];
+                                const float f = m[e] == -INFINITY ? 1.f : ex2(m[e] - mn);  // (nothing so far: zeros)
+                                m[e] = mn;
+                                l[e] *= f;
+                                if ((lane & 3) == 0) ms.f[r0 + 8 * e] = f;
+                            }
+                        }
+                        // every product so far is in the output
+                        ok = ok && warp_wait(&ms.pv_done[back.stage], back.full(), limit);
+                        bar_named(1, 128);
+                        tm_after();
+#pragma unroll 1
+                        for (int mb = 0; mb < MT; ++mb)
+#pragma unroll 1
+                            for (int c = 0; c < nr; c += 16) {
+                                uint32_t o[16];
+                                tm_ld16(o, my + S::T_O + mb * nr + c);
+                                tm_wait_ld();
+#pragma unroll
+                                for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * ms.f[c + e]);
+                                tm_st16(my + S::T_O + mb * nr + c, o);
+                            }
+                        tm_wait_st();
+                        tm_before();
+                        bar_named(1, 128);
+                    }
+                    // the buffer is free when the product of the tile that it held last has read it
+                    if (TILE == 32) {
+                        if (at_c.c >= 2) {
+                            // (of the tile before the last one: its stage is the one before `back`)
+                            Spot two = back;
+                            if (two.stage == 0) two.stage = stages - 1, --two.turn;
+                            else --two.stage;
+                            ok = ok && warp_wait(&ms.pv_done[two.stage], two.full(), limit);
+                        }
+                    } else if (at_c.c >= 1) {
+                        ok = ok && warp_wait(&ms.pv_done[back.stage], back.full(), limit);
+                    }
+                    if (act) {
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+                            const float ref = m[e] == -INFINITY ? 0.f : m[e];
+                            const int r = r0 + 8 * e;
+                            uint8_t* const row = psm + r * 128 + 4 * (lane & 3);
+                            float s0 = 0.f, s1 = 0.f;
+#pragma unroll
+                            for (int k = 0; k < TILE / 8; ++k) {
+                                const float a = ex2(x[e][2 * k] - ref), b = ex2(x[e][2 * k + 1] - ref);
+                                s0 += a, s1 += b;
+                                const int c = (TILE == 32 ? at_c.buf() * 4 : 0) + k;
+                                *reinterpret_cast<uint32_t*>(row + ((c ^ (r & 7)) << 4)) = pack16<F16>(a, b);
+                            }
+                            l[e] += s0 + s1;
+                        }
+                    }
+                    fence_async();
+                    tm_before();
+                    bar_arrive(&ms.p_ready[at_c.buf()]);
+                    back = at_c;
+                    at_c.next(stages);
+                }
+                // ---- the piece: maxima and sums by row, then the output out of tensor memory
+                if (act) {
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        l[e] += __shfl_xor_sync(0xffffffffu, l[e], 1);
+                        l[e] += __shfl_xor_sync(0xffffffffu, l[e], 2);
+                    }
+                }
+                ok = ok && warp_wait(&ms.pv_done[back.stage], back.full(), limit);
+                if (act && (lane & 3) == 0) {
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        // what a CTA that gave up leaves is no number, nor what sees a latent that is none
+                        const bool none = !ok || last[e] >= ms.bad[piece & 15];
+                        ms.m[r0 + 8 * e] = m[e];
+                        ms.sum[r0 + 8 * e] = none ? __uint_as_float(0x7fffffffu) : l[e];
+                    }
+                }
+                tm_before();
+                bar_named(1, 128);
+                tm_after();
+                const bool whole = take == it.n;
+                float* const slot = p.slots + (2ll * blockIdx.x + (u == first ? 0 : 1)) * ((long long)nr * (S::RANK + 2));
+#pragma unroll 1
+                for (int c = 0; c < nr; c += 16) {
+                    if (c >= it.rows) break;
+#pragma unroll 1
+                    for (int mb = 0; mb < MT; ++mb) {
+                        uint32_t o[16];
+                        tm_ld16(o, my + S::T_O + mb * nr + c);
+                        tm_wait_ld();
+                        const int d = mb * 128 + warp * 32 + lane;
+#pragma unroll
+                        for (int e = 0; e < 16; ++e) {
+                            const int r = c + e, g = it.row0 + r;
+                            if (r >= it.rows) break;
+                            // (a row that saw nothing in a piece of several has weights of 0 and a finite output)
+                            if (whole) {
+                                const float l2 = ms.sum[r];
+                                const int t = g / p.H, h = g - t * p.H;
+                                put16<F16>(p.out, it.b * p.ob + t * p.ot + h * p.oh + d,
+                                           l2 == 0.f ? 0.f : __fdividef(__uint_as_float(o[e]), l2));
+                            } else {
+                                slot[(long long)r * S::RANK + d] = __uint_as_float(o[e]);
+                            }
+                        }
+                    }
+                }
+                if (tid < it.rows) {
+                    const float l2 = ms.sum[tid];
+                    if (!whole)
+                        *reinterpret_cast<float2*>(slot + (long long)nr * S::RANK + 2 * tid) = make_float2(ms.m[tid], l2);
+                    else if (p.lse)
+                        p.lse[(long long)it.b * p.T * p.H + it.row0 + tid] = l2 == 0.f ? -INFINITY : (ms.m[tid] + log2f(l2)) * LN2;
+                }
+                tm_before();
+                bar_named(1, 128);  // the outputs have been read
+                u += take;
+                w.on(p, take);
+            }
+        } else if (warp == 4) {
+            // ================ copies ================
+            // A tile is `parts` boxes of up to TILE rows of one page. The lanes hold the pages of the next 32 boxes, and
+            // of the 32 after them.
+            const int rows = min(TILE, 1 << p.ps_shift), parts = TILE / rows, mask = (1 << p.ps_shift) - 1;
+            const int tiles = end - first, pshift = __ffs(parts) - 1;
+            Line<TILE> ahead = w;
+            int ahead_c = lane >> pshift;
+            ahead.on(p, ahead_c);
+            auto page_next = [&] {  // of this lane's box of the next 32; one that nothing sees reads as zeros
+                int page = p.n_pages;
+                if (ahead_c < tiles) {
+                    const int pos = ahead.at() + (lane & (parts - 1)) * rows;
+                    if (pos < ahead.it.hi && pos + rows > ahead.it.lo) {
+                        page = p.table[ahead.it.b * p.table_s + (pos >> p.ps_shift)];
+                        if ((unsigned)page >= (unsigned)p.n_pages) {
+                            page = p.n_pages;
+                            if (p.status) *p.status = MK_ERR_INVALID_ARG;
+                        }
+                    }
+                    ahead_c += 32 >> pshift;
+                    ahead.on(p, 32 >> pshift);
+                }
+                return page;
+            };
+            int now = page_next(), next = page_next();
+            int box = 0;
+            Spot pl;
+            for (int c = 0; c < tiles; ++c, pl.next(stages)) {
+                const int j0 = w.at();
+                w.on(p, 1);
+                const uint32_t st = ring + pl.stage * S::STAGE_B;
+                unsigned long long* const bar = &ms.kv_full[pl.stage];
+                if (c >= stages && !warp_wait(&ms.pv_done[pl.stage], pl.free(), limit)) break;
+                if (lane == 0) bar_expect(bar, S::STAGE_B);
+                sent = c + 1;
+                for (int i = 0; i < parts; ++i, ++box) {
+                    const int page = __shfl_sync(0xffffffffu, now, box & 31);
+                    if (lane == 0) {
+                        const int row = (j0 + i * rows) & mask;
+#pragma unroll
+                        for (int x = 0; x < 2 * MT; ++x)
+                            tma_3d(st + x * TILE * 128 + i * rows * 128, &maps.latent, x * 64, row, page, bar);
+                        tma_3d(st + 2 * MT * TILE * 128 + i * rows * 128, &maps.rope, 0, row, page, bar);
+                    }
+                    if ((box & 31) == 31) {
+                        now = next;
+                        next = page_next();
+                    }
+                }
+            }
+        } else if (warp == 7) {
+            // ================ rows that must not reach the output ================
+            Spot pl;
+            unsigned piece = 0;
+            bool ok = true;
+            for (int u = first; u < end && ok; ++piece) {
+                const int take = min(w.it.n - w.tile, end - u);
+                const Item<TILE>& it = w.it;
+                int bad = INT_MAX;
+                for (int i = 0; i < take; ++i, pl.next(stages)) {
+                    const int j0 = (it.t0 + w.tile + i) * TILE;
+                    if (!(ok = warp_wait(&ms.kv_full[pl.stage], pl.full(), limit))) break;
+                    if (j0 < it.lo || j0 + TILE > it.common) {
+                        uint8_t* const st = smem + q_b + pl.stage * S::STAGE_B;
+                        for (int r = 0; r < TILE; ++r) {
+                            const int j = j0 + r;
+                            const bool hidden = j < it.lo || j >= it.hi;
+                            if (!hidden && j < it.common) continue;
+                            for (int c = lane; c < 16 * MT; c += 32) {  // (the order within a panel's row does not matter)
+                                uint4* const at = reinterpret_cast<uint4*>(st + (c >> 3) * TILE * 128 + r * 128 + (c & 7) * 16);
+                                if (hidden) {
+                                    *at = make_uint4(0, 0, 0, 0);
+                                } else {
+                                    const uint4 v = *at;
+                                    if (not_finite<F16>(v.x) || not_finite<F16>(v.y) || not_finite<F16>(v.z) || not_finite<F16>(v.w)) {
+                                        *at = make_uint4(0, 0, 0, 0);
+                                        bad = min(bad, j);
+                                    }
+                                }
+                            }
+                        }
+                        fence_async();
+                    }
+                    if (i == take - 1) {
+                        bad = __reduce_min_sync(0xffffffffu, bad);
+                        if (lane == 0) ms.bad[piece & 15] = bad;
+                    }
+                    __syncwarp();
+                    if (lane == 0) bar_arrive(&ms.v_ok[pl.stage]);
+                }
+                u += take;
+                w.on(p, take);
+            }
+        } else {
+            // ================ products: two warps, one lane of each issues ================
+            const uint32_t tmu = __shfl_sync(0xffffffffu, tm, 0);
+            Spot at_c;
+            unsigned piece = 0;
+            bool ok = true;
+            if (warp == 5) {
+                constexpr uint32_t QK = mma_desc(64, TILE, false, false, F16);
+                const uint64_t q = smem_desc(qs, 16, 1024), k0 = smem_desc(ring, 16, 1024);
+                for (int u = first; u < end && ok; ++piece) {
+                    const int take = min(w.it.n - w.tile, end - u);
+                    u += take;
+                    w.on(p, take);
+                    ok = warp_wait(&ms.q_ready, piece & 1u, limit);
+                    for (int i = 0; i < take && ok; ++i) {
+                        // the tile is here; the softmax has read what the S buffer held two tiles ago
+                        ok = warp_wait(&ms.kv_full[at_c.stage], at_c.full(), limit) &&
+                             (at_c.c < 2 || warp_wait(&ms.s_free[at_c.buf()], at_c.pair_free(), limit));
+                        if (!ok) break;
+                        tm_after();
+                        if (elect_one()) {
+                            const uint64_t k = desc_on(k0, at_c.stage * S::STAGE_B);
+                            const uint32_t d = tmu + S::T_S + at_c.buf() * TILE;
+#pragma unroll
+                            for (int j = 0; j < 4 * S::KP; ++j)
+                                mma_ss(d, desc_on(q, (j >> 2) * nr * 128 + (j & 3) * 32),
+                                       desc_on(k, (j >> 2) * TILE * 128 + (j & 3) * 32), QK, j > 0);
+                            mma_commit(&ms.s_full[at_c.buf()]);
+                        }
+                        __syncwarp();
+                        at_c.next(stages);
+                    }
+                }
+            } else {
+                const uint32_t PV = mma_desc(128, nr, false, true, F16);
+                const uint64_t v0 = smem_desc(ring, TILE * 128, 1024), p0 = smem_desc(ps, 16, 1024);
+                for (int u = first; u < end && ok; ++piece) {
+                    const int take = min(w.it.n - w.tile, end - u);
+                    u += take;
+                    w.on(p, take);
+                    for (int i = 0; i < take; ++i) {
+                        ok = warp_wait(&ms.p_ready[at_c.buf()], at_c.pair(), limit) &&
+                             warp_wait(&ms.v_ok[at_c.stage], at_c.full(), limit);
+                        if (!ok) break;
+                        tm_after();
+                        if (elect_one()) {
+                            const uint64_t v = desc_on(v0, at_c.stage * S::STAGE_B);
+                            const uint64_t pb = desc_on(p0, TILE == 32 ? at_c.buf() * 64 : 0);
+                            // the first tile of a piece overwrites
+#pragma unroll
+                            for (int mb = 0; mb < MT; ++mb)
+#pragma unroll
+                                for (int j = 0; j < TILE / 16; ++j)
+                                    mma_ss(tmu + S::T_O + mb * nr, desc_on(v, mb * 2 * TILE * 128 + j * 2048),
+                                           desc_on(pb, j * 32), PV, i > 0 || j > 0);
+                            if (!p.skip_signal) mma_commit(&ms.pv_done[at_c.stage]);
+                        }
+                        __syncwarp();
+                        at_c.next(stages);
+                    }
+                }
+            }
+            // the last products end before the tensor memory goes, also when a role gave up
+            if (elect_one()) mma_commit(&ms.drained);
+            const long long t0 = now_ns();
+            while (!bar_try(&ms.drained, 0) && now_ns() - t0 < DRAIN_NS) {
+            }
+        }
+    }
+    __syncwarp();
+    tm_before();
+    __syncthreads();
+    tm_after();
+    if (ms.abort) {
+        // copies may still be on their way into this CTA's memory: at most the ring's last tiles
+        if (warp == 4) {
+            const long long t0 = now_ns();
+            for (int c = max(0, sent - stages); c < sent; ++c)
+                while (!bar_try(&ms.kv_full[c % stages], (unsigned)(c / stages) & 1u) && now_ns() - t0 < DRAIN_NS) {
+                }
+        }
+        if (tid == 0 && p.status) *p.status = MK_ERR_TIMEOUT;
+        __syncthreads();
+    }
+    if (warp == 5)
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tm), "n"(S::T_ALL) : "memory");
+}
+
+// Joins the pieces of an output row, four warps taking every fourth one; rows without a piece get their zeros, rows whose
+// only piece went straight to the output are left alone.
+template <int RANK, bool F16>
+__global__ void __launch_bounds__(128) latent_join(const __grid_constant__ LatentP p, int main_grid) {
+    constexpr int E = RANK / 128;  // float4 of a lane
+    __shared__ float4 om[4][RANK / 4];
+    __shared__ float2 oml[4];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, rows = p.T * p.H;
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const int b = blockIdx.x / rows, g = blockIdx.x - b * rows, rb = g / p.rows_blk, r = g - rb * p.rows_blk;
+    const int items = p.B * p.RB, item = b * p.RB + rb, total = p.base[items];
+    const int t0 = p.base[item], n = p.base[item + 1] - t0;
+    const int per = max((total + main_grid - 1) / main_grid, p.min_units);
+    const int c0 = t0 / per, c1 = n ? (t0 + n - 1) / per : c0 - 1;
+    if (n && c0 == c1) return;
+    float m = -INFINITY, l = 0.f;
+    float4 o[E];
+#pragma unroll
+    for (int e = 0; e < E; ++e) o[e] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+    for (int c = c0 + warp; c <= c1; c += 4) {
+        // a CTA's first piece is the one that its stretch begins with
+        const float* s = p.slots + (2ll * c + (t0 <= c * per ? 0 : 1)) * ((long long)p.nr * (RANK + 2));
+        const float2 ml = *reinterpret_cast<const float2*>(s + (long long)p.nr * RANK + 2 * r);
+        float4 y[E];
+#pragma unroll
+        for (int e = 0; e < E; ++e) y[e] = *reinterpret_cast<const float4*>(s + (long long)r * RANK + 4 * (32 * e + lane));
+        const float mn = fmaxf(m, ml.x), ref = mn == -INFINITY ? 0.f : mn, f = ex2(m - ref), w = ex2(ml.x - ref);
+        m = mn;
+        l = l * f + ml.y * w;
+#pragma unroll
+        for (int e = 0; e < E; ++e) {
+            o[e].x = o[e].x * f + y[e].x * w, o[e].y = o[e].y * f + y[e].y * w;
+            o[e].z = o[e].z * f + y[e].z * w, o[e].w = o[e].w * f + y[e].w * w;
+        }
+    }
+#pragma unroll
+    for (int e = 0; e < E; ++e) om[warp][32 * e + lane] = o[e];
+    if (lane == 0) oml[warp] = make_float2(m, l);
+    __syncthreads();
+    float mm = -INFINITY, ll = 0.f, w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) mm = fmaxf(mm, oml[i].x);
+    const float ref = mm == -INFINITY ? 0.f : mm;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        w[i] = ex2(oml[i].x - ref);
+        ll += oml[i].y * w[i];
+    }
+    const int t = g / p.H, h = g - t * p.H;
+    const long long at = b * p.ob + t * p.ot + h * p.oh;
+    const float* const of = reinterpret_cast<const float*>(om);
+    for (int d = threadIdx.x; d < RANK; d += 128) {
+        float y = 0.f;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) y += of[i * RANK + d] * w[i];
+        put16<F16>(p.out, at + d, ll == 0.f ? 0.f : y / ll);
+    }
+    if (threadIdx.x == 0 && p.lse) p.lse[blockIdx.x] = ll == 0.f ? -INFINITY : (mm + log2f(ll)) * LN2;
+}
+
+// ---- host
+
+// latents or rope parts as a tensor [page][row][value]; a box is up to TILE rows of a page by 64 values, in the 128-byte
+// swizzled order the products read
+int map_of(const void* base, int width, int tile, const mk_latent_pages& g, int64_t page_s, int64_t row_s, CUtensorMap* out) {
+    const EncodeFn encode = encode_fn();
+    if (!encode) return fail(MK_ERR_CUDA, "latent attend: the driver has no cuTensorMapEncodeTiled");
+    const cuuint64_t dims[3] = {(cuuint64_t)width, (cuuint64_t)g.page_size, (cuuint64_t)g.n_pages};
+    const cuuint64_t strides[2] = {(cuuint64_t)row_s * 2, (cuuint64_t)page_s * 2};
+    const cuuint32_t box[3] = {64, (cuuint32_t)(g.page_size < tile ? g.page_size : tile), 1}, one[3] = {1, 1, 1};
+    const CUresult r = encode(out, g.dtype == MK_DT_F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3,
+                              const_cast<void*>(base), dims, strides, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                              CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
+                              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    if (r != CUDA_SUCCESS) return fail(MK_ERR_CUDA, "latent attend: cuTensorMapEncodeTiled failed (%d)", (int)r);
+    return MK_OK;
+}
+
+struct Plan {
+    bool rows;  // a block a row
+    int nr, rows_blk, RB, tile, grid, stages;
+    int64_t slots_off, bytes;
+};
+
+constexpr int MIN_UNITS = 4;  // positions a CTA takes at least: 4 tiles
+
+template <int MT, int TILE, bool F16>
+int run(const LatentP* p, const mk_latent_pages* g, int grid, cudaStream_t s) {
+    using S = LatentShape<MT, TILE>;
+    auto kern = latent_kernel<MT, TILE, F16>;
+    static std::mutex lock;
+    static bool have[32];
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return cuda_status(e, "mk_latent_attend");
+    {
+        std::lock_guard<std::mutex> hold(lock);
+        if (dev >= 32 || !have[dev]) {
+            e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_MOST);
+            if (e != cudaSuccess) return cuda_status(e, "mk_latent_attend");
+            if (dev < 32) have[dev] = true;
+        }
+    }
+    LatentMaps maps;
+    if (const int rc = map_of(g->latent, g->rank, TILE, *g, g->page_stride, g->row_stride, &maps.latent)) return rc;
+    if (const int rc = map_of(g->rope, 64, TILE, *g, g->rope_page_stride, g->rope_row_stride, &maps.rope)) return rc;
+    kern<<<grid, NT, S::smem(p->nr), s>>>(*p, maps);
+    if (const int rc = cuda_status(cudaGetLastError(), "mk_latent_attend")) return rc;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(p->B * p->T * p->H));
+    cfg.blockDim = dim3(128);
+    cfg.stream = s;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    return cuda_status(cudaLaunchKernelEx(&cfg, latent_join<128 * MT, F16>, *p, grid), "mk_latent_attend");
+}
+
 int check(const mk_latent_attention* a) {
     if (!a) return fail(MK_ERR_INVALID_ARG, "latent attend: NULL arguments");
     if (const int rc = check_latent(a->pages, a->table)) return rc;
@@ -121,17 +872,51 @@ int check(const mk_latent_attention* a) {
     return MK_OK;
 }
 
-}  // namespace
-
-extern "C" int mk_latent_attend_workspace(const mk_latent_attention* a, int64_t* bytes) {
+int make_plan(const mk_latent_attention* a, Plan& pl) {
     if (const int rc = check(a)) return rc;
-    if (!bytes) return fail(MK_ERR_INVALID_ARG, "latent attend: NULL bytes");
-    *bytes = 0;
+    const mk_latent_pages& g = *a->pages;
+    const mk_page_table& t = *a->table;
+    pl = {};
+    pl.rows = g.page_size < 8 || !g.page_stride || !g.row_stride || !g.rope_page_stride || !g.rope_row_stride;
+    if (pl.rows) return MK_OK;
+    int dev = 0, sms = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+    if (e != cudaSuccess) return cuda_status(e, "mk_latent_attend");
+    const int rows = a->n_tokens * a->n_heads;
+    pl.RB = (rows + 63) / 64;
+    pl.rows_blk = (rows + pl.RB - 1) / pl.RB;
+    pl.RB = (rows + pl.rows_blk - 1) / pl.rows_blk;
+    pl.nr = (pl.rows_blk + 15) / 16 * 16;
+    pl.tile = pl.nr <= 32 ? 32 : 64;
+    pl.stages = g.rank == 512 ? (pl.tile == 32 ? LatentShape<4, 32>::stages(pl.nr) : LatentShape<4, 64>::stages(pl.nr))
+                              : (pl.tile == 32 ? LatentShape<2, 32>::stages(pl.nr) : LatentShape<2, 64>::stages(pl.nr));
+    const int64_t items = (int64_t)t.batch * pl.RB, cap = (int64_t)t.pages_per_seq * g.page_size;
+    const int64_t most = items * ((cap + pl.tile - 1) / pl.tile + 1);
+    if (most > (1 << 30)) return fail(MK_ERR_UNSUPPORTED, "latent attend: too many positions in one call");
+    const int64_t want = (most + MIN_UNITS - 1) / MIN_UNITS;
+    pl.grid = (int)(want < sms ? want : sms);
+    pl.slots_off = ((items + 1) * 4 + 255) / 256 * 256;
+    pl.bytes = pl.slots_off + 2ll * pl.grid * pl.nr * (g.rank + 2) * 4;
+    pl.bytes = (pl.bytes + 255) / 256 * 256;
     return MK_OK;
 }
 
-extern "C" int mk_latent_attend(const mk_latent_attention* a, void*, int64_t, void* stream) {
-    if (const int rc = check(a)) return rc;
+}  // namespace
+
+extern "C" int mk_latent_attend_workspace(const mk_latent_attention* a, int64_t* bytes) {
+    Plan pl;
+    if (const int rc = make_plan(a, pl)) return rc;
+    if (!bytes) return fail(MK_ERR_INVALID_ARG, "latent attend: NULL bytes");
+    *bytes = pl.bytes;
+    return MK_OK;
+}
+
+extern "C" int mk_latent_attend(const mk_latent_attention* a, void* workspace, int64_t workspace_bytes, void* stream) {
+    Plan pl;
+    if (const int rc = make_plan(a, pl)) return rc;
+    if (pl.bytes && (!workspace || (uintptr_t)workspace % 256 || workspace_bytes < pl.bytes))
+        return fail(MK_ERR_INVALID_ARG, "latent attend: the workspace must be %lld bytes, aligned to 256", (long long)pl.bytes);
     const mk_latent_pages& g = *a->pages;
     const mk_page_table& t = *a->table;
     LatentP p = {};
@@ -144,9 +929,23 @@ extern "C" int mk_latent_attend(const mk_latent_attention* a, void*, int64_t, vo
     p.lse = a->lse, p.status = a->status;
     p.pps = t.pages_per_seq, p.ps_shift = log2_exact(g.page_size), p.n_pages = g.n_pages, p.B = t.batch;
     p.T = a->n_tokens, p.H = a->n_heads, p.scale = a->scale;
-    const int grid = p.B * p.T * p.H;
     cudaStream_t s = (cudaStream_t)stream;
-    if (g.dtype == MK_DT_F16) g.rank == 512 ? latent_rows<MK_DT_F16, 512, 64><<<grid, LT, 0, s>>>(p) : latent_rows<MK_DT_F16, 256, 64><<<grid, LT, 0, s>>>(p);
-    else g.rank == 512 ? latent_rows<MK_DT_BF16, 512, 64><<<grid, LT, 0, s>>>(p) : latent_rows<MK_DT_BF16, 256, 64><<<grid, LT, 0, s>>>(p);
-    return cuda_status(cudaGetLastError(), "mk_latent_attend");
+    const bool f16 = g.dtype == MK_DT_F16, wide = g.rank == 512;
+    if (pl.rows) {
+        const int grid = p.B * p.T * p.H;
+        if (f16) wide ? latent_rows<MK_DT_F16, 512, 64><<<grid, LT, 0, s>>>(p) : latent_rows<MK_DT_F16, 256, 64><<<grid, LT, 0, s>>>(p);
+        else wide ? latent_rows<MK_DT_BF16, 512, 64><<<grid, LT, 0, s>>>(p) : latent_rows<MK_DT_BF16, 256, 64><<<grid, LT, 0, s>>>(p);
+        return cuda_status(cudaGetLastError(), "mk_latent_attend");
+    }
+    p.nr = pl.nr, p.rows_blk = pl.rows_blk, p.RB = pl.RB, p.stages = pl.stages, p.min_units = MIN_UNITS;
+    p.base = (int*)workspace, p.slots = (float*)((uint8_t*)workspace + pl.slots_off);
+    const long long ns = mk_wait_ns_();
+    p.wait_ns = (unsigned)(ns < 4000000000ll ? ns : 4000000000ll);
+    p.skip_signal = mk_fault_("skip_attend_signal");
+    if (pl.tile == 32) {
+        if (wide) return f16 ? run<4, 32, true>(&p, &g, pl.grid, s) : run<4, 32, false>(&p, &g, pl.grid, s);
+        return f16 ? run<2, 32, true>(&p, &g, pl.grid, s) : run<2, 32, false>(&p, &g, pl.grid, s);
+    }
+    if (wide) return f16 ? run<4, 64, true>(&p, &g, pl.grid, s) : run<4, 64, false>(&p, &g, pl.grid, s);
+    return f16 ? run<2, 64, true>(&p, &g, pl.grid, s) : run<2, 64, false>(&p, &g, pl.grid, s);
 }

@@ -46,8 +46,6 @@
 // fp16 queries 99 us. 256 tokens at 16384 positions of one sequence, 16 query
 // heads on 4: 84 us.
 #pragma once
-#include <cuda.h>
-
 #include "mk_attend.cuh"
 
 namespace mkop {
@@ -81,71 +79,6 @@ struct PrefixMisc {
     int scan[16], found_b, found_base;
     long long off[2][64];  // where a tile's rows lie (bytes), -1: zeros
     float2 stat[2][128];   // (maximum, sum) of each group's rows
-};
-
-__device__ __forceinline__ void bar_init(unsigned long long* b, unsigned n) {
-    asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(sm32(b)), "r"(n) : "memory");
-}
-__device__ __forceinline__ void bar_arrive(unsigned long long* b) {
-    asm volatile("{\n\t.reg .b64 t;\n\tmbarrier.arrive.shared::cta.b64 t, [%0];\n\t}" ::"r"(sm32(b)) : "memory");
-}
-__device__ __forceinline__ bool bar_try(unsigned long long* b, unsigned parity) {
-    unsigned ok;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\tselp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(ok)
-        : "r"(sm32(b)), "r"(parity)
-        : "memory");
-    return ok;
-}
-// A CTA that gave up waits so long for what it has in flight (its roles' waits end at AttendP::wait_ns)
-constexpr long long DRAIN_NS = 2000000000ll;
-struct Limit {
-    volatile unsigned* abort;  // a role gave up
-    unsigned ns;
-};
-__device__ __forceinline__ long long now_ns() {
-    long long t;
-    asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t));
-    return t;
-}
-// Waits for the phase of `parity` to end; false when it took too long, or
-// another role gave up.
-__device__ __forceinline__ bool bar_wait(unsigned long long* b, unsigned parity, const Limit& limit) {
-    unsigned t0 = 0;
-    for (unsigned n = 0; !bar_try(b, parity); ++n) {
-        if ((n & 63u) != 63u) continue;  // the timer is slow to read
-        if (*limit.abort) return false;
-        unsigned t;  // its low half comes round every 4.3 s
-        asm volatile("mov.u32 %0, %%globaltimer_lo;" : "=r"(t));
-        if (n == 63u) t0 = t;
-        if (t - t0 > limit.ns) {
-            *limit.abort = 1;
-            return false;
-        }
-    }
-    return true;
-}
-// the same for a whole warp, which goes on or gives up together
-__device__ __forceinline__ bool warp_wait(unsigned long long* b, unsigned parity, const Limit& limit) {
-    return __all_sync(0xffffffffu, bar_wait(b, parity, limit));
-}
-
-// A role's place in the line of tiles: the ring's stage and its turn, the
-// buffer pair and its turn (without divisions).
-template <int STAGES>
-struct Place {
-    int stage = 0;
-    unsigned turn = 0, c = 0;
-    __device__ __forceinline__ void next() {
-        ++c;
-        if (++stage == STAGES) stage = 0, ++turn;
-    }
-    __device__ __forceinline__ int buf() const { return (int)(c & 1u); }
-    __device__ __forceinline__ unsigned full() const { return turn & 1u; }          // parity of the stage's phase of this tile
-    __device__ __forceinline__ unsigned free() const { return (turn - 1) & 1u; }    // of the tile before it in the stage
-    __device__ __forceinline__ unsigned pair() const { return c >> 1 & 1u; }        // of the buffer's phase of this tile
-    __device__ __forceinline__ unsigned pair_free() const { return ((c >> 1) - 1) & 1u; }
 };
 
 // A role's place in the line of items and their tiles. Shared launch: one
@@ -191,76 +124,6 @@ struct Walk {
     __device__ __forceinline__ int at() const { return (t0 + tile) * 64; }
 };
 
-// Shared-memory matrix descriptors: start address, leading and stride offsets
-// in 16-byte units, version 1, 128-byte swizzle.
-__device__ __forceinline__ uint64_t smem_desc(uint32_t addr, uint32_t lead, uint32_t stride) {
-    return (uint64_t)((addr & 0x3ffffu) >> 4) | (uint64_t)(lead >> 4) << 16 | (uint64_t)(stride >> 4) << 32 |
-           (uint64_t)1 << 46 | (uint64_t)2 << 61;
-}
-// the same further on in the same operand
-__device__ __forceinline__ uint64_t desc_on(uint64_t d, uint32_t bytes) {
-    return (d & 0xffffffff00000000ull) | ((uint32_t)d + (bytes >> 4));
-}
-// bf16 x bf16 -> fp32, M rows, N columns; `b_rows`: B's rows are its K (MN-major)
-__host__ __device__ constexpr uint32_t mma_desc(int m, int n, bool b_rows) {
-    return 1u << 4 | 1u << 7 | 1u << 10 | (b_rows ? 1u << 16 : 0u) | (uint32_t)(n >> 3) << 17 | (uint32_t)(m >> 4) << 24;
-}
-__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t desc, bool add) {
-    asm volatile(
-        "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-        "l"(a), "l"(b), "r"(desc), "r"((uint32_t)add)
-        : "memory");
-}
-__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t desc, bool add) {
-    asm volatile(
-        "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
-        "r"(a), "l"(b), "r"(desc), "r"((uint32_t)add)
-        : "memory");
-}
-// one lane of a converged warp; the compiler then knows that a single thread
-// runs the branch and keeps the products' operands in uniform registers
-__device__ __forceinline__ bool elect_one() {
-    uint32_t p;
-    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
-    return p != 0;
-}
-__device__ __forceinline__ void mma_commit(unsigned long long* b) {
-    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(sm32(b))
-                 : "memory");
-}
-__device__ __forceinline__ void tm_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
-__device__ __forceinline__ void tm_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
-__device__ __forceinline__ void tm_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
-__device__ __forceinline__ void tm_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
-// 32 columns of this thread's row
-__device__ __forceinline__ void tm_ld32(uint32_t (&r)[32], uint32_t a) {
-    asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
-        "%15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
-        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
-          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
-          "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
-          "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
-        : "r"(a));
-}
-__device__ __forceinline__ void tm_st32(uint32_t a, const uint32_t (&r)[32]) {
-    asm volatile(
-        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
-        "%15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};" ::"r"(a),
-        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
-        "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]),
-        "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]),
-        "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
-        : "memory");
-}
-
-// 16-byte piece c (of D/8) of row r in a 128-byte-swizzled operand of `rows` rows
-__device__ __forceinline__ uint32_t panel_at(uint32_t base, int rows, int r, int c) {
-    return base + (c >> 3) * rows * 128 + r * 128 + (((c & 7) ^ (r & 7)) << 4);
-}
-
 // Four codes as two bf16 pairs, exact. E4M3: through fp16 and fp32. INT8: the
 // low seven bits as the mantissa of 128 (whose bf16 step is 1), less 128, or
 // less 256 where the sign bit is set.
@@ -297,12 +160,6 @@ __device__ __forceinline__ void tma_rows(uint32_t dst, const CUtensorMap* map, i
         "l"(map), "r"(x), "r"(row), "r"(head), "r"(page), "r"(sm32(bar))
         : "memory");
 }
-__device__ __forceinline__ void bar_expect(unsigned long long* b, unsigned bytes) {
-    asm volatile("{\n\t.reg .b64 t;\n\tmbarrier.arrive.expect_tx.shared::cta.b64 t, [%0], %1;\n\t}" ::"r"(sm32(b)),
-                 "r"(bytes)
-                 : "memory");
-}
-
 template <int D, int FMT, bool SPLITQ>
 __global__ void __launch_bounds__(PrefixShape<D, FMT, SPLITQ>::NT, 1)
     prefix_kernel(const __grid_constant__ AttendP p, const __grid_constant__ PrefixMaps maps) {
@@ -906,17 +763,7 @@ __global__ void __launch_bounds__(PrefixShape<D, FMT, SPLITQ>::NT, 1)
 // K or V as a 4-D tensor; a box is up to 64 rows of a page by 64 values, in
 // the 128-byte swizzled order the products read
 inline int map_of(const AttendP& p, const void* base, int head_dim, CUtensorMap* out) {
-    typedef CUresult (*Encode)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*, const cuuint64_t*,
-                               const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
-                               CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-    static const Encode encode = [] {
-        void* f = nullptr;
-        cudaDriverEntryPointQueryResult q;
-        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &q) != cudaSuccess ||
-            q != cudaDriverEntryPointSuccess)
-            return (Encode) nullptr;
-        return (Encode)f;
-    }();
+    const EncodeFn encode = encode_fn();
     if (!encode) return fail(MK_ERR_CUDA, "attend: the driver has no cuTensorMapEncodeTiled");
     const cuuint32_t rows = 1u << p.ps_shift;
     const cuuint64_t dims[4] = {(cuuint64_t)head_dim, rows, (cuuint64_t)p.H, (cuuint64_t)p.n_pages};
