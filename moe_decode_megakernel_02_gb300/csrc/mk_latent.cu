@@ -67,6 +67,7 @@ struct LatentP {
     int* base;       // [items + 1]: first tile of each item, for the joining launch
     unsigned wait_ns;
     int skip_signal;  // for tests: a role's signals are left out
+    int q_vec;        // queries can be copied 16 bytes at a time
 };
 
 constexpr int LT = 128;
@@ -216,6 +217,7 @@ struct LatentMisc {
     int bad[16];           // of a piece: the first position of it that is not finite and that only some rows see
     float m[64], f[64];    // of a row: its maximum, its factor
     float sum[64];
+    long long to[64];
 };
 
 template <int MT, int TILE>
@@ -269,11 +271,12 @@ __global__ void __launch_bounds__(NT, 1)
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     // the line: each thread counts a stretch of items; sums before it by shuffles
     const int items = p.B * p.RB, each = (items + NT - 1) / NT, i0 = min(items, tid * each), i1 = min(items, i0 + each);
-    int mine = 0;
+    int mine = 0, own = 0;
     for (int i = i0; i < i1; ++i) {
         Item<TILE> it;
         it.set(p, i);
-        mine += it.n;
+        own = it.n;
+        mine += own;
     }
     int inc = mine;
 #pragma unroll
@@ -316,15 +319,17 @@ __global__ void __launch_bounds__(NT, 1)
     if (blockIdx.x == 0 || (first >= before && first < before + mine)) {
         int at = before;
         for (int i = i0; i < i1; ++i) {
-            Item<TILE> it;
-            it.set(p, i);
+            if (each > 1) {
+                Item<TILE> it;
+                it.set(p, i);
+                own = it.n;
+            }
             if (blockIdx.x == 0) {
                 p.base[i] = at;  // for the joining launch
-                if (it.rb == 0 && p.status && (long long)p.lens[it.b] > (long long)p.pps << p.ps_shift)
-                    *p.status = MK_ERR_INVALID_ARG;
+                if (p.status && (long long)p.lens[i / p.RB] > (long long)p.pps << p.ps_shift) *p.status = MK_ERR_INVALID_ARG;
             }
-            if (first >= at && first < at + it.n) ms.found_item = i, ms.found_base = at;
-            at += it.n;
+            if (first >= at && first < at + own) ms.found_item = i, ms.found_base = at;
+            at += own;
         }
     }
     if (blockIdx.x == 0 && tid == 0) p.base[items] = total;
@@ -348,25 +353,36 @@ __global__ void __launch_bounds__(NT, 1)
             for (int u = first; u < end; ++piece) {
                 const int take = min(w.it.n - w.tile, end - u);
                 const Item<TILE>& it = w.it;
-                // queries: every product that read the last ones has ended (all its scores came)
-                for (int i = tid; i < nr * (S::KP * 8); i += 128) {
-                    const int r = i / (S::KP * 8), c = i - r * (S::KP * 8), g = it.row0 + r;
-                    uint4 x = make_uint4(0, 0, 0, 0);
-                    if (r < it.rows) {
-                        const int t = g / p.H, h = g - t * p.H;
-                        const uint8_t* src =
-                            c < 16 * MT ? p.q + 2 * (it.b * p.qb + t * p.qt + h * p.qh + 8 * c)
-                                        : p.qr + 2 * (it.b * p.rb + t * p.rt + h * p.rh + 8 * (c - 16 * MT));
-                        if (((uintptr_t)src & 15) == 0) {
-                            x = *reinterpret_cast<const uint4*>(src);
-                        } else {
-                            const uint16_t* s2 = reinterpret_cast<const uint16_t*>(src);
-                            x = make_uint4(s2[0] | (uint32_t)s2[1] << 16, s2[2] | (uint32_t)s2[3] << 16,
-                                           s2[4] | (uint32_t)s2[5] << 16, s2[6] | (uint32_t)s2[7] << 16);
+                // queries, a row a warp: every product that read the last ones has ended (all its scores came)
+                for (int r = warp; r < nr; r += 4) {
+                    const int g = it.row0 + r, t = g / p.H, h = g - t * p.H;
+                    const uint8_t* const a = p.q + 2 * (it.b * p.qb + t * p.qt + h * p.qh);
+                    const uint8_t* const e = p.qr + 2 * (it.b * p.rb + t * p.rt + h * p.rh);
+                    const bool in = r < it.rows;
+                    if (p.q_vec) {
+#pragma unroll
+                        for (int c = lane; c < 8 * S::KP; c += 32)
+                            cp16(qs + panel_at(0, nr, r, c), in ? (c < 16 * MT ? a + 16 * c : e + 16 * (c - 16 * MT)) : p.q, in);
+                    } else {
+                        for (int c = lane; c < 8 * S::KP; c += 32) {
+                            uint32_t x[4] = {0, 0, 0, 0};
+                            if (in) {
+                                const uint16_t* const s2 =
+                                    reinterpret_cast<const uint16_t*>(c < 16 * MT ? a + 16 * c : e + 16 * (c - 16 * MT));
+#pragma unroll
+                                for (int i = 0; i < 4; ++i) x[i] = s2[2 * i] | (uint32_t)s2[2 * i + 1] << 16;
+                            }
+                            *reinterpret_cast<uint4*>(smem + panel_at(0, nr, r, c)) = make_uint4(x[0], x[1], x[2], x[3]);
                         }
                     }
-                    *reinterpret_cast<uint4*>(smem + panel_at(0, nr, r, c)) = x;
                 }
+                // where the rows' outputs go
+                if (tid < it.rows) {
+                    const int g = it.row0 + tid, t = g / p.H, h = g - t * p.H;
+                    ms.to[tid] = it.b * p.ob + t * p.ot + h * p.oh;
+                }
+                cp_commit();
+                cp_wait<0>();
                 fence_async();
                 bar_arrive(&ms.q_ready);
                 int last[2];
@@ -504,7 +520,9 @@ __global__ void __launch_bounds__(NT, 1)
                         // what a CTA that gave up leaves is no number, nor what sees a latent that is none
                         const bool none = !ok || last[e] >= ms.bad[piece & 15];
                         ms.m[r0 + 8 * e] = m[e];
-                        ms.sum[r0 + 8 * e] = none ? __uint_as_float(0x7fffffffu) : l[e];
+                        const float l2 = none ? __uint_as_float(0x7fffffffu) : l[e];
+                        ms.sum[r0 + 8 * e] = l2;
+                        ms.f[r0 + 8 * e] = l2 == 0.f ? 0.f : 1.f / l2;
                     }
                 }
                 tm_before();
@@ -513,27 +531,21 @@ __global__ void __launch_bounds__(NT, 1)
                 const bool whole = take == it.n;
                 float* const slot = p.slots + (2ll * blockIdx.x + (u == first ? 0 : 1)) * ((long long)nr * (S::RANK + 2));
 #pragma unroll 1
-                for (int c = 0; c < nr; c += 16) {
-                    if (c >= it.rows) break;
-#pragma unroll 1
+                for (int c = 0; c < it.rows; c += 16) {
+#pragma unroll 2
                     for (int mb = 0; mb < MT; ++mb) {
                         uint32_t o[16];
                         tm_ld16(o, my + S::T_O + mb * nr + c);
                         tm_wait_ld();
                         const int d = mb * 128 + warp * 32 + lane;
+                        if (whole) {
 #pragma unroll
-                        for (int e = 0; e < 16; ++e) {
-                            const int r = c + e, g = it.row0 + r;
-                            if (r >= it.rows) break;
-                            // (a row that saw nothing in a piece of several has weights of 0 and a finite output)
-                            if (whole) {
-                                const float l2 = ms.sum[r];
-                                const int t = g / p.H, h = g - t * p.H;
-                                put16<F16>(p.out, it.b * p.ob + t * p.ot + h * p.oh + d,
-                                           l2 == 0.f ? 0.f : __fdividef(__uint_as_float(o[e]), l2));
-                            } else {
-                                slot[(long long)r * S::RANK + d] = __uint_as_float(o[e]);
-                            }
+                            for (int e = 0; e < 16; ++e)
+                                if (c + e < it.rows) put16<F16>(p.out, ms.to[c + e] + d, __uint_as_float(o[e]) * ms.f[c + e]);
+                        } else {
+#pragma unroll
+                            for (int e = 0; e < 16; ++e)
+                                if (c + e < it.rows) slot[(c + e) * S::RANK + d] = __uint_as_float(o[e]);
                         }
                     }
                 }
@@ -574,7 +586,7 @@ __global__ void __launch_bounds__(NT, 1)
                 }
                 return page;
             };
-            int now = page_next(), next = page_next();
+            int now = page_next(), next = 0;
             int box = 0;
             Spot pl;
             for (int c = 0; c < tiles; ++c, pl.next(stages)) {
@@ -594,10 +606,8 @@ __global__ void __launch_bounds__(NT, 1)
                             tma_3d(st + x * TILE * 128 + i * rows * 128, &maps.latent, x * 64, row, page, bar);
                         tma_3d(st + 2 * MT * TILE * 128 + i * rows * 128, &maps.rope, 0, row, page, bar);
                     }
-                    if ((box & 31) == 31) {
-                        now = next;
-                        next = page_next();
-                    }
+                    if ((box & 31) == 0) next = page_next();
+                    if ((box & 31) == 31) now = next;
                 }
             }
         } else if (warp == 7) {
@@ -731,65 +741,51 @@ __global__ void __launch_bounds__(NT, 1)
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tm), "n"(S::T_ALL) : "memory");
 }
 
-// Joins the pieces of an output row, four warps taking every fourth one; rows without a piece get their zeros, rows whose
-// only piece went straight to the output are left alone.
+// Joins the pieces of an output row, a block 128 values of it: four warps take every fourth piece. Rows without a piece
+// get their zeros, rows whose only piece went straight to the output are left alone.
+constexpr int JT = 128;
 template <int RANK, bool F16>
-__global__ void __launch_bounds__(128) latent_join(const __grid_constant__ LatentP p, int main_grid) {
-    constexpr int E = RANK / 128;  // float4 of a lane
-    __shared__ float4 om[4][RANK / 4];
-    __shared__ float2 oml[4];
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, rows = p.T * p.H;
+__global__ void __launch_bounds__(JT) latent_join(const __grid_constant__ LatentP p, int main_grid) {
+    __shared__ float4 om[JT / 32][32];
+    __shared__ float2 oml[JT / 32];
+    constexpr int CH = RANK / 128;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, row = blockIdx.x / CH, d0 = (blockIdx.x - row * CH) * 128;
+    const int rows = p.T * p.H, b = row / rows, g = row - b * rows, rb = g / p.rows_blk, r = g - rb * p.rows_blk;
+    const int item = b * p.RB + rb, t = g / p.H, h = g - t * p.H;
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    const int b = blockIdx.x / rows, g = blockIdx.x - b * rows, rb = g / p.rows_blk, r = g - rb * p.rows_blk;
-    const int items = p.B * p.RB, item = b * p.RB + rb, total = p.base[items];
-    const int t0 = p.base[item], n = p.base[item + 1] - t0;
+    const int total = p.base[p.B * p.RB], t0 = p.base[item], n = p.base[item + 1] - t0;
     const int per = max((total + main_grid - 1) / main_grid, p.min_units);
     const int c0 = t0 / per, c1 = n ? (t0 + n - 1) / per : c0 - 1;
     if (n && c0 == c1) return;
+    const long long slot_f = (long long)p.nr * (RANK + 2);
     float m = -INFINITY, l = 0.f;
-    float4 o[E];
-#pragma unroll
-    for (int e = 0; e < E; ++e) o[e] = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-    for (int c = c0 + warp; c <= c1; c += 4) {
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 8
+    for (int c = c0 + warp; c <= c1; c += JT / 32) {
         // a CTA's first piece is the one that its stretch begins with
-        const float* s = p.slots + (2ll * c + (t0 <= c * per ? 0 : 1)) * ((long long)p.nr * (RANK + 2));
-        const float2 ml = *reinterpret_cast<const float2*>(s + (long long)p.nr * RANK + 2 * r);
-        float4 y[E];
-#pragma unroll
-        for (int e = 0; e < E; ++e) y[e] = *reinterpret_cast<const float4*>(s + (long long)r * RANK + 4 * (32 * e + lane));
+        const float* const s = p.slots + (2ll * c + (t0 <= c * per ? 0 : 1)) * slot_f;
+        const float2 ml = *reinterpret_cast<const float2*>(s + p.nr * RANK + 2 * r);
+        const float4 y = *reinterpret_cast<const float4*>(s + r * RANK + d0 + 4 * lane);
         const float mn = fmaxf(m, ml.x), ref = mn == -INFINITY ? 0.f : mn, f = ex2(m - ref), w = ex2(ml.x - ref);
         m = mn;
         l = l * f + ml.y * w;
-#pragma unroll
-        for (int e = 0; e < E; ++e) {
-            o[e].x = o[e].x * f + y[e].x * w, o[e].y = o[e].y * f + y[e].y * w;
-            o[e].z = o[e].z * f + y[e].z * w, o[e].w = o[e].w * f + y[e].w * w;
-        }
+        o.x = o.x * f + y.x * w, o.y = o.y * f + y.y * w, o.z = o.z * f + y.z * w, o.w = o.w * f + y.w * w;
     }
-#pragma unroll
-    for (int e = 0; e < E; ++e) om[warp][32 * e + lane] = o[e];
+    om[warp][lane] = o;
     if (lane == 0) oml[warp] = make_float2(m, l);
     __syncthreads();
-    float mm = -INFINITY, ll = 0.f, w[4];
+    float mm = -INFINITY, ll = 0.f, y = 0.f;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) mm = fmaxf(mm, oml[i].x);
+    for (int i = 0; i < JT / 32; ++i) mm = fmaxf(mm, oml[i].x);
     const float ref = mm == -INFINITY ? 0.f : mm;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        w[i] = ex2(oml[i].x - ref);
-        ll += oml[i].y * w[i];
+    for (int i = 0; i < JT / 32; ++i) {
+        const float w = ex2(oml[i].x - ref);
+        ll += oml[i].y * w;
+        y += reinterpret_cast<const float*>(om[i])[threadIdx.x] * w;
     }
-    const int t = g / p.H, h = g - t * p.H;
-    const long long at = b * p.ob + t * p.ot + h * p.oh;
-    const float* const of = reinterpret_cast<const float*>(om);
-    for (int d = threadIdx.x; d < RANK; d += 128) {
-        float y = 0.f;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) y += of[i * RANK + d] * w[i];
-        put16<F16>(p.out, at + d, ll == 0.f ? 0.f : y / ll);
-    }
-    if (threadIdx.x == 0 && p.lse) p.lse[blockIdx.x] = ll == 0.f ? -INFINITY : (mm + log2f(ll)) * LN2;
+    put16<F16>(p.out, b * p.ob + t * p.ot + h * p.oh + d0 + threadIdx.x, ll == 0.f ? 0.f : y / ll);
+    if (threadIdx.x == 0 && d0 == 0 && p.lse) p.lse[row] = ll == 0.f ? -INFINITY : (mm + log2f(ll)) * LN2;
 }
 
 // ---- host
@@ -841,8 +837,8 @@ int run(const LatentP* p, const mk_latent_pages* g, int grid, cudaStream_t s) {
     kern<<<grid, NT, S::smem(p->nr), s>>>(*p, maps);
     if (const int rc = cuda_status(cudaGetLastError(), "mk_latent_attend")) return rc;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)(p->B * p->T * p->H));
-    cfg.blockDim = dim3(128);
+    cfg.gridDim = dim3((unsigned)(p->B * p->T * p->H * MT));
+    cfg.blockDim = dim3(JT);
     cfg.stream = s;
     cudaLaunchAttribute at[1];
     at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -942,6 +938,7 @@ extern "C" int mk_latent_attend(const mk_latent_attention* a, void* workspace, i
     const long long ns = mk_wait_ns_();
     p.wait_ns = (unsigned)(ns < 4000000000ll ? ns : 4000000000ll);
     p.skip_signal = mk_fault_("skip_attend_signal");
+    p.q_vec = rows_vec(a->q) && rows_vec(a->q_rope);
     if (pl.tile == 32) {
         if (wide) return f16 ? run<4, 32, true>(&p, &g, pl.grid, s) : run<4, 32, false>(&p, &g, pl.grid, s);
         return f16 ? run<2, 32, true>(&p, &g, pl.grid, s) : run<2, 32, false>(&p, &g, pl.grid, s);
