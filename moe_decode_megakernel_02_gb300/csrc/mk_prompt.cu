@@ -1,94 +1,498 @@
 // mk_prompt.cu -- causal attention of prompts over expanded keys and values
 // (mk_prompt_attend).
-#include "mk_values.cuh"
+//
+// For one query row (a token and a head) and the keys j it sees,
+//   x_j = scale (q . k_j + q_rope . r_j),  m = max x_j,
+//   out = sum_j e^(x_j - m) v_j / sum_j e^(x_j - m),
+// in one pass over tiles of 128 keys on the fifth-generation tensor cores. A CTA
+// takes 256 queries of a sequence and head as two blocks of 128 rows against the
+// same tiles:
+//   S = Q K^T   128 x 128 over 192 values, both operands in shared memory by
+//               tensor maps, S in tensor memory;
+//   P = 2^(x - m), a row a thread, over the columns that S took, rounded to the
+//               values' type (what a weight loses, half a step, is of the
+//               output's own rounding);
+//   O += P V    P as the tensor-memory operand, V from shared memory as it lies
+//               there (its rows are the product's K), O in tensor memory.
+// While the tensor cores work for one block, the other's four softmax warps
+// turn its scores into probabilities: products go block 0's O, its next S,
+// block 1's O, its next S, in the order they are issued, so that a block's next S
+// overwrites its P after the product that read it. O is rescaled only when a row's
+// maximum has risen by more than 2^8 since its reference.
+//
+// Shared memory is full: queries 96 KB, a ring of five 16 KB panels of keys (64
+// values of 128 keys), one of three 16 KB halves of values (64 keys).
+//
+// At the end of what is seen scores are masked, and since 0 x NaN is NaN, two
+// warps clean the tiles there: values that no row of the CTA sees become zeros;
+// so do values that are not finite and that only some rows see, and rows that
+// do see them get NaN.
+//
+// Longest CTAs first: blocks of a sequence in falling order, all heads of one
+// after another, so that short ones fill the end. All waits have a limit.
+#include <climits>
+#include <mutex>
+
+#include "mk_tensor.cuh"
 
 namespace {
 
 using namespace mkop;
 
 constexpr int NOPE = 128, ROPE = 64, VD = 128;
+constexpr int ROWS = 128, TILE = 128, PAIR = 2 * ROWS;
+constexpr int PANELS = (NOPE + ROPE) / 64;      // 64 values wide
+constexpr int PANEL_B = TILE * 128;             // of keys, and of queries
+constexpr int Q_B = PANELS * PANEL_B;           // a block's queries
+constexpr int KS = 5, VS = 3;                   // ring slots: panels of keys, halves of values
+constexpr int VHALF_B = 64 * VD * 2;
+constexpr int K_OFF = 2 * Q_B, V_OFF = K_OFF + KS * PANEL_B, MISC_OFF = V_OFF + VS * VHALF_B;
+constexpr int NT = 384;                         // warps: softmax 2 x 4, copies, products, cleaning 2
+constexpr int T_S = 0, T_O = 2 * TILE, T_ALL = 512;  // tensor memory: S (and P) of both blocks, O of both
+static_assert(T_O + 2 * VD <= T_ALL && PANEL_B == VHALF_B, "");
+
+struct PromptMisc {
+    unsigned long long q_full[2], k_full[KS], k_free[KS], v_full[VS], v_ok[VS], v_free[VS], s_full[2], p_ready[2], o_done[2],
+        drained;
+    unsigned tmem, abort;
+    int scan[NT / 32], seq, pair, bad;
+};
+constexpr int SMEM = 1024 + MISC_OFF + 1024;
+static_assert(sizeof(PromptMisc) <= 1024 && SMEM <= 227 * 1024, "");
 
 struct PromptP {
     const int *q_starts, *k_starts;
-    const uint8_t *q, *k, *kr, *v;
     uint8_t* out;
     float* lse;
     int* status;
-    long long qt, qh, kt, kh, rt, vt, vh, ot, oh;  // elements
+    long long ot, oh;           // elements
     int B, n_q, n_k, H;
+    int q_heads, k_heads, v_heads;  // 0: all heads are one (a stride of 0)
     float scale;
+    unsigned wait_ns;
+    int skip_signal;            // for tests
+};
+struct PromptMaps {
+    CUtensorMap q, k, r, v;
 };
 
-constexpr int PT = 128;
+__device__ __forceinline__ void tma_2d(uint32_t dst, const CUtensorMap* map, int x, int y, unsigned long long* bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
+        "l"(map), "r"(x), "r"(y), "r"(sm32(bar))
+        : "memory");
+}
+template <bool F16>
+__device__ __forceinline__ uint32_t pack16(float lo, float hi) {
+    return F16 ? pack_f16(lo, hi) : pack_bf16(lo, hi);
+}
+// one 32-bit word with either 16-bit half not finite
+template <bool F16>
+__device__ __forceinline__ bool not_finite(uint32_t w) {
+    constexpr uint32_t E = F16 ? 0x7c00u : 0x7f80u;
+    return (w & E) == E || (w & (E << 16)) == E << 16;
+}
+// a ring slot and its turn
+template <int N>
+struct Slot {
+    int i = 0;
+    unsigned turn = 0;
+    __device__ __forceinline__ void next() {
+        if (++i == N) i = 0, ++turn;
+    }
+};
 
-// A block a query row, a key a warp at a time.
-template <int DT>
-__global__ void __launch_bounds__(PT) prompt_rows(const __grid_constant__ PromptP p) {
-    __shared__ float om[PT / 32][VD], ml[PT / 32][2];
-    const int row = blockIdx.x / p.H, h = blockIdx.x - row * p.H;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    int q0, q1, k0, k1, mine = -1;
-    for (int b = 0; b < p.B; ++b) {
-        q0 = p.q_starts[b], q1 = p.q_starts[b + 1], k0 = p.k_starts[b], k1 = p.k_starts[b + 1];
-        const bool good = 0 <= q0 && q0 <= q1 && q1 <= p.n_q && 0 <= k0 && k0 <= k1 && k1 <= p.n_k;
-        if (!good && blockIdx.x == 0 && p.status) *p.status = MK_ERR_INVALID_ARG;
-        if (good && q0 <= row && row < q1 && mine < 0) mine = b;
+// blocks of 256 queries of a sequence; 0 where its bounds are none
+__device__ __forceinline__ int pairs_of(const PromptP& p, int b) {
+    const int q0 = p.q_starts[b], q1 = p.q_starts[b + 1], k0 = p.k_starts[b], k1 = p.k_starts[b + 1];
+    if (q0 < 0 || q1 < q0 || q1 > p.n_q || k0 < 0 || k1 < k0 || k1 > p.n_k) return -1;
+    return (q1 - q0 + PAIR - 1) / PAIR;
+}
+
+template <bool F16>
+__global__ void __launch_bounds__(NT, 1)
+    prompt_kernel(const __grid_constant__ PromptP p, const __grid_constant__ PromptMaps maps) {
+    extern __shared__ uint8_t raw_smem[];
+    uint8_t* const smem = raw_smem + ((1024u - (sm32(raw_smem) & 1023u)) & 1023u);
+    const uint32_t qs = sm32(smem);
+    PromptMisc& ms = *reinterpret_cast<PromptMisc*>(smem + MISC_OFF);
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const Limit limit = {&ms.abort, p.wait_ns};
+
+    // the CTA's block: each thread counts a stretch of sequences; sums before it by shuffles
+    const int h = blockIdx.x % p.H, u = blockIdx.x / p.H;
+    const int each = (p.B + NT - 1) / NT, b0 = min(p.B, tid * each), b1 = min(p.B, b0 + each);
+    int mine = 0;
+    for (int b = b0; b < b1; ++b) {
+        const int n = pairs_of(p, b);
+        mine += max(n, 0);
+        if (n < 0 && blockIdx.x == 0 && p.status) *p.status = MK_ERR_INVALID_ARG;
     }
-    if (mine < 0) return;
-    q0 = p.q_starts[mine], q1 = p.q_starts[mine + 1], k0 = p.k_starts[mine], k1 = p.k_starts[mine + 1];
-    const int last = k1 - q1 + row;  // a row of k
-    float q[8] = {}, o[4] = {};
-    if (lane < (NOPE + ROPE) / 8) {
-        Values8<DT, true> x;
-        x.load(p.q, row * p.qt + h * p.qh + 8 * lane);
-        x.floats(q);
+    int inc = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int a = __shfl_up_sync(0xffffffffu, inc, o);
+        if (lane >= o) inc += a;
     }
-    float m = -INFINITY, l = 0.f;
-    for (int j = k0 + warp; j <= last; j += PT / 32) {
-        float s = 0.f, k[8] = {};
-        Values8<DT, true> x;
-        if (lane < NOPE / 8) {
-            x.load(p.k, j * p.kt + h * p.kh + 8 * lane);
-            x.floats(k);
-        } else if (lane < (NOPE + ROPE) / 8) {
-            x.load(p.kr, j * p.rt + 8 * lane - NOPE);
-            x.floats(k);
-        }
-#pragma unroll
-        for (int e = 0; e < 8; ++e) s += q[e] * k[e];
-#pragma unroll
-        for (int d = 16; d; d >>= 1) s += __shfl_xor_sync(0xffffffffu, s, d);
-        s *= p.scale;
-        const float mn = fmaxf(m, s), f = __expf(m - mn), w = __expf(s - mn);
-        m = mn;
-        l = l * f + w;
-        const uint2 v2 = *reinterpret_cast<const uint2*>(p.v + 2 * (j * p.vt + h * p.vh + 4 * lane));
-        float v[4];
-        if constexpr (DT == MK_DT_BF16) {
-            v[0] = bf2f(v2.x & 0xffffu), v[1] = bf2f(v2.x >> 16), v[2] = bf2f(v2.y & 0xffffu), v[3] = bf2f(v2.y >> 16);
-        } else {
-            const float2 a = __half22float2(*reinterpret_cast<const __half2*>(&v2.x)), c = __half22float2(*reinterpret_cast<const __half2*>(&v2.y));
-            v[0] = a.x, v[1] = a.y, v[2] = c.x, v[3] = c.y;
-        }
-#pragma unroll
-        for (int e = 0; e < 4; ++e) o[e] = o[e] * f + w * v[e];
-    }
-#pragma unroll
-    for (int e = 0; e < 4; ++e) om[warp][4 * lane + e] = o[e];
-    if (lane == 0) ml[warp][0] = m, ml[warp][1] = l;
+    if (lane == 31) ms.scan[warp] = inc;
+    if (tid == 0) ms.seq = -1;
     __syncthreads();
-    float mm = -INFINITY, ll = 0.f, y = 0.f;
-    for (int w = 0; w < PT / 32; ++w) mm = fmaxf(mm, ml[w][0]);
-    const float ref = mm == -INFINITY ? 0.f : mm;
-    for (int w = 0; w < PT / 32; ++w) {
-        ll += ml[w][1] * __expf(ml[w][0] - ref);
-        y += om[w][threadIdx.x] * __expf(ml[w][0] - ref);
+    int before = inc - mine;
+    for (int w = 0; w < warp; ++w) before += ms.scan[w];
+    if (u >= before && u < before + mine) {
+        for (int b = b0, at = before; b < b1; ++b) {
+            const int n = max(pairs_of(p, b), 0);
+            if (u < at + n) {
+                ms.seq = b;
+                ms.pair = n - 1 - (u - at);  // the longest first
+                break;
+            }
+            at += n;
+        }
     }
-    y = ll == 0.f ? 0.f : y / ll;
-    const long long at = row * p.ot + h * p.oh + threadIdx.x;
-    if constexpr (DT == MK_DT_F16) reinterpret_cast<__half*>(p.out)[at] = __float2half_rn(y);
-    else reinterpret_cast<__nv_bfloat16*>(p.out)[at] = __float2bfloat16_rn(y);
-    if (threadIdx.x == 0 && p.lse) p.lse[(long long)row * p.H + h] = ll == 0.f ? -INFINITY : mm + logf(ll);
+    if (tid == 0) {
+        for (int i = 0; i < 2; ++i) {
+            bar_init(&ms.q_full[i], 1);
+            bar_init(&ms.s_full[i], 1);
+            bar_init(&ms.p_ready[i], 128);
+            bar_init(&ms.o_done[i], 1);
+        }
+        for (int i = 0; i < KS; ++i) bar_init(&ms.k_full[i], 1), bar_init(&ms.k_free[i], 1);
+        for (int i = 0; i < VS; ++i) bar_init(&ms.v_full[i], 1), bar_init(&ms.v_ok[i], 2), bar_init(&ms.v_free[i], 1);
+        bar_init(&ms.drained, 1);
+        ms.abort = 0;
+        ms.bad = INT_MAX;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    __syncthreads();
+    if (ms.seq < 0) return;  // (the grid has room for a block more a sequence than there may be)
+    if (warp == 9) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(sm32(&ms.tmem)), "n"(T_ALL)
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    }
+    tm_before();
+    __syncthreads();
+    tm_after();
+    const uint32_t tm = ms.tmem;
+    const int b = ms.seq, q0 = p.q_starts[b], n = p.q_starts[b + 1] - q0, k0 = p.k_starts[b], m = p.k_starts[b + 1] - k0;
+    const int i0 = ms.pair * PAIR, behind = m - n;  // query i sees keys 0 .. behind + i
+    // tiles that block g's rows see
+    auto tiles_of = [&](int g) {
+        const int first = i0 + g * ROWS, last = min(first + ROWS, n) - 1;
+        return first < n && behind + last >= 0 ? (behind + last) / TILE + 1 : 0;
+    };
+    const int nt0 = tiles_of(0), nt1 = tiles_of(1), nt = max(nt0, nt1);
+    int sent_k = 0, sent_v = 0;  // panels and halves that the copying warp has asked for
+
+    if (warp < 8) {
+        // ================ softmax, a row a thread ================
+        const int g = warp >> 2, row = i0 + g * ROWS + (tid & 127), mine_nt = g ? nt1 : nt0;
+        const uint32_t my = tm + ((uint32_t)((warp & 3) * 32) << 16), my_s = my + T_S + g * TILE, my_o = my + T_O + g * VD;
+        const int last = behind + row, least = behind + i0 + g * ROWS;  // the row's last key, and the block's first row's
+        const bool neg = p.scale < 0.f;  // (then the smallest product counts: signs turned)
+        const float scale2 = fabsf(p.scale) * LOG2E;
+        const uint32_t flip = neg ? 0x80000000u : 0u;
+        float mx = -INFINITY, l = 0.f;
+        bool ok = true;
+        for (int j = 0; j < mine_nt; ++j) {
+            if (!(ok = warp_wait(&ms.s_full[g], j & 1, limit))) break;
+            tm_after();
+            const int j0 = j * TILE;
+            const bool edge = j0 + TILE - 1 > least;
+            float t0 = -INFINITY, t1 = -INFINITY;
+#pragma unroll
+            for (int c = 0; c < TILE; c += 32) {
+                uint32_t s[32];
+                tm_ld32(s, my_s + c);
+                tm_wait_ld();
+                if (edge) {
+#pragma unroll
+                    for (int e = 0; e < 32; ++e)
+                        if (j0 + c + e > last) s[e] = 0xff800000u ^ flip;
+                }
+                if (neg) {
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) s[e] ^= 0x80000000u;
+                }
+#pragma unroll
+                for (int e = 0; e < 32; e += 4) {
+                    t0 = fmaxf(t0, fmaxf(__uint_as_float(s[e]), __uint_as_float(s[e + 1])));
+                    t1 = fmaxf(t1, fmaxf(__uint_as_float(s[e + 2]), __uint_as_float(s[e + 3])));
+                }
+            }
+            // (a scale of 0 times a masked -infinity is no number)
+            const float top = fmaxf(t0, t1), tile_m = top == -INFINITY ? top : top * scale2;
+            const bool rise = tile_m > mx + 8.f;
+            if (j == 0) {
+                mx = tile_m;
+            } else if (__any_sync(0xffffffffu, rise)) {
+                const float mn = rise ? tile_m : mx, f = mx == -INFINITY ? 1.f : ex2(mx - mn);
+                mx = mn;
+                l *= f;
+                // the last product is in the output
+                if (!(ok = warp_wait(&ms.o_done[g], (j - 1) & 1, limit))) break;
+                tm_after();
+#pragma unroll 1
+                for (int d = 0; d < VD; d += 32) {
+                    uint32_t o[32];
+                    tm_ld32(o, my_o + d);
+                    tm_wait_ld();
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+                    tm_st32(my_o + d, o);
+                }
+                tm_wait_st();
+            }
+            const float ref = mx == -INFINITY ? 0.f : mx;
+            float sum[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int c = 0; c < TILE; c += 32) {
+                uint32_t s[32], x[16];
+                tm_ld32(s, my_s + c);
+                tm_wait_ld();
+                if (neg) {
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) s[e] ^= 0x80000000u;
+                }
+#pragma unroll
+                for (int e = 0; e < 32; e += 2) {
+                    float a = ex2(fmaf(__uint_as_float(s[e]), scale2, -ref)), d = ex2(fmaf(__uint_as_float(s[e + 1]), scale2, -ref));
+                    if (edge) {
+                        if (j0 + c + e > last) a = 0.f;
+                        if (j0 + c + e + 1 > last) d = 0.f;
+                    }
+                    sum[(e >> 1) & 3] += a + d;
+                    x[e >> 1] = pack16<F16>(a, d);
+                }
+                tm_st16(my_s + (c >> 1), x);  // over columns that have been read
+            }
+            l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+            tm_wait_st();
+            tm_before();
+            bar_arrive(&ms.p_ready[g]);
+        }
+        // ---- the block's end
+        if (ok && mine_nt) ok = warp_wait(&ms.o_done[g], (mine_nt - 1) & 1, limit);
+        tm_after();
+        // what a CTA that gave up leaves is no number, nor what sees a value that is none
+        if (!ok || last >= ms.bad) l = __uint_as_float(0x7fffffffu);
+        const float inv = l == 0.f ? 0.f : 1.f / l;
+        const bool real = row < n;
+        uint4* const to = reinterpret_cast<uint4*>(p.out + 2 * ((long long)(q0 + row) * p.ot + (long long)h * p.oh));
+#pragma unroll 1
+        for (int d = 0; d < VD; d += 32) {
+            uint32_t o[32];
+            tm_ld32(o, my_o + d);
+            tm_wait_ld();
+            if (real) {
+#pragma unroll
+                for (int e = 0; e < 32; e += 8) {
+                    uint32_t y[4];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        y[i] = l == 0.f ? 0u  // (nothing seen: what lies in the tensor memory may be anything)
+                                        : pack16<F16>(__uint_as_float(o[e + 2 * i]) * inv, __uint_as_float(o[e + 2 * i + 1]) * inv);
+                    to[(d + e) / 8] = make_uint4(y[0], y[1], y[2], y[3]);
+                }
+            }
+        }
+        if (real && p.lse) p.lse[(long long)(q0 + row) * p.H + h] = l == 0.f ? -INFINITY : (mx + log2f(l)) * LN2;
+    } else if (warp == 8) {
+        // ================ copies ================
+        Slot<KS> ks;
+        Slot<VS> vs;
+        bool ok = true;
+        for (int j = 0; j < nt && ok; ++j) {
+            const int key = k0 + j * TILE;
+            for (int c = 0; c < PANELS; ++c, ks.next()) {
+                if (!(ok = !ks.turn || warp_wait(&ms.k_free[ks.i], (ks.turn - 1) & 1, limit))) break;
+                ++sent_k;
+                if (lane == 0) {
+                    unsigned long long* const bar = &ms.k_full[ks.i];
+                    bar_expect(bar, PANEL_B);
+                    const uint32_t to = qs + K_OFF + ks.i * PANEL_B;
+                    if (c < NOPE / 64) tma_3d(to, &maps.k, 64 * c, p.k_heads ? h : 0, key, bar);
+                    else tma_2d(to, &maps.r, 0, key, bar);
+                }
+                if (j == 0 && c == 0) {  // queries: with the first keys
+                    for (int g = 0; g < 2; ++g) {
+                        if (lane || !(g ? nt1 : nt0)) continue;
+                        bar_expect(&ms.q_full[g], Q_B);
+                        for (int x = 0; x < PANELS; ++x)
+                            tma_3d(qs + g * Q_B + x * PANEL_B, &maps.q, 64 * x, p.q_heads ? h : 0, q0 + i0 + g * ROWS, &ms.q_full[g]);
+                    }
+                }
+            }
+            for (int c = 0; c < 2 && ok; ++c, vs.next()) {
+                if (!(ok = !vs.turn || warp_wait(&ms.v_free[vs.i], (vs.turn - 1) & 1, limit))) break;
+                ++sent_v;
+                if (lane == 0) {
+                    unsigned long long* const bar = &ms.v_full[vs.i];
+                    bar_expect(bar, VHALF_B);
+                    for (int x = 0; x < 2; ++x)
+                        tma_3d(qs + V_OFF + vs.i * VHALF_B + x * 8192, &maps.v, 64 * x, p.v_heads ? h : 0, key + 64 * c, bar);
+                }
+            }
+        }
+    } else if (warp >= 10) {
+        // ================ values that must not reach the output ================
+        Slot<VS> vs;
+        bool ok = true;
+        const int all = behind + i0, some = behind + min(i0 + PAIR, n) - 1;  // keys up to which all rows, and any row, see
+        for (int j = 0; j < 2 * nt && ok; ++j, vs.next()) {
+            if (!(ok = warp_wait(&ms.v_full[vs.i], vs.turn & 1, limit))) break;
+            const int j0 = 64 * j;
+            if (j0 + 63 > all) {
+                uint8_t* const at = smem + V_OFF + vs.i * VHALF_B;
+                int bad = INT_MAX;
+                for (int c = (warp - 10) * 32 + lane; c < VHALF_B / 16; c += 64) {
+                    const int key = j0 + ((c >> 3) & 63);
+                    if (key <= all) continue;
+                    uint4* const x = reinterpret_cast<uint4*>(at) + c;
+                    if (key > some) {
+                        *x = make_uint4(0, 0, 0, 0);
+                    } else {
+                        const uint4 v = *x;
+                        if (not_finite<F16>(v.x) || not_finite<F16>(v.y) || not_finite<F16>(v.z) || not_finite<F16>(v.w)) {
+                            *x = make_uint4(0, 0, 0, 0);
+                            bad = min(bad, key);
+                        }
+                    }
+                }
+                if (bad != INT_MAX) atomicMin(&ms.bad, bad);
+                fence_async();
+            }
+            __syncwarp();
+            if (lane == 0) bar_arrive(&ms.v_ok[vs.i]);
+        }
+    } else {
+        // ================ products, an elected lane issues ================
+        const uint32_t tmu = __shfl_sync(0xffffffffu, tm, 0);
+        constexpr uint32_t QK = mma_desc(ROWS, TILE, false, false, F16), PV = mma_desc(ROWS, VD, true, false, F16);
+        const uint64_t qd = smem_desc(qs, 16, 1024), kd = smem_desc(qs + K_OFF, 16, 1024), vd = smem_desc(qs + V_OFF, 8192, 1024);
+        bool ok = true;
+        // S of block g for tile j, whose keys' first panel is in slot `at`
+        auto scores = [&](int g, int j, Slot<KS> at, bool free) {
+            if (j == 0) ok = ok && warp_wait(&ms.q_full[g], 0, limit);
+            Slot<KS> s = at;
+            for (int c = 0; c < PANELS; ++c, s.next()) ok = ok && warp_wait(&ms.k_full[s.i], s.turn & 1, limit);
+            if (!ok) return;
+            tm_after();
+            if (elect_one()) {
+                s = at;
+#pragma unroll
+                for (int c = 0; c < PANELS; ++c, s.next()) {
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        mma_ss(tmu + T_S + g * TILE, desc_on(qd, g * Q_B + c * PANEL_B + k * 32),
+                               desc_on(kd, s.i * PANEL_B + k * 32), QK, c > 0 || k > 0);
+                    if (free) mma_commit(&ms.k_free[s.i]);
+                }
+                mma_commit(&ms.s_full[g]);
+            }
+            __syncwarp();
+        };
+        auto outputs = [&](int g, int j, Slot<VS> at, bool free) {
+            ok = ok && warp_wait(&ms.p_ready[g], j & 1, limit);
+            Slot<VS> s = at;
+            for (int c = 0; c < 2; ++c, s.next()) ok = ok && warp_wait(&ms.v_ok[s.i], s.turn & 1, limit);
+            if (!ok) return;
+            tm_after();
+            if (elect_one()) {
+                s = at;
+#pragma unroll
+                for (int c = 0; c < 2; ++c, s.next()) {
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        mma_ts(tmu + T_O + g * VD, tmu + T_S + g * TILE + (4 * c + k) * 8, desc_on(vd, s.i * VHALF_B + k * 2048),
+                               PV, j > 0 || c > 0 || k > 0);
+                    if (free) mma_commit(&ms.v_free[s.i]);
+                }
+                if (!p.skip_signal) mma_commit(&ms.o_done[g]);
+            }
+            __syncwarp();
+        };
+        Slot<KS> ks;
+        Slot<VS> vs;
+        if (nt0) scores(0, 0, ks, !nt1);
+        if (nt1) scores(1, 0, ks, true);
+        for (int c = 0; c < PANELS; ++c) ks.next();
+        for (int j = 0; j < nt && ok; ++j) {
+            // what is read last for the tile frees it
+            if (j < nt0) outputs(0, j, vs, j >= nt1);
+            if (j + 1 < nt0) scores(0, j + 1, ks, j + 1 >= nt1);
+            if (j < nt1) outputs(1, j, vs, true);
+            if (j + 1 < nt1) scores(1, j + 1, ks, true);
+            for (int c = 0; c < PANELS; ++c) ks.next();
+            vs.next(), vs.next();
+        }
+        // the last products end before the tensor memory goes, also when a role gave up
+        if (elect_one()) mma_commit(&ms.drained);
+        const long long t0 = now_ns();
+        while (!bar_try(&ms.drained, 0) && now_ns() - t0 < DRAIN_NS) {
+        }
+    }
+    __syncwarp();
+    tm_before();
+    __syncthreads();
+    tm_after();
+    if (ms.abort) {
+        // copies may still be on their way into this CTA's memory: the queries, at most the rings' last ones
+        if (warp == 8 && sent_k) {
+            const long long t0 = now_ns();
+            auto gone = [&](unsigned long long* bar, unsigned parity) {
+                while (!bar_try(bar, parity) && now_ns() - t0 < DRAIN_NS) {
+                }
+            };
+            if (nt0) gone(&ms.q_full[0], 0);
+            if (nt1) gone(&ms.q_full[1], 0);
+            for (int c = max(0, sent_k - KS); c < sent_k; ++c) gone(&ms.k_full[c % KS], (unsigned)(c / KS) & 1u);
+            for (int c = max(0, sent_v - VS); c < sent_v; ++c) gone(&ms.v_full[c % VS], (unsigned)(c / VS) & 1u);
+        }
+        if (tid == 0 && p.status) *p.status = MK_ERR_TIMEOUT;
+        __syncthreads();
+    }
+    if (warp == 9)
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tm), "n"(T_ALL) : "memory");
+}
+
+// [rows][heads][width] as a tensor, boxes of `box` rows by 64 values of one head (heads 0: one for all, a stride of 0)
+int map_of(const void* base, int dtype, int width, int heads, int rows, int64_t head_s, int64_t row_s, int box, CUtensorMap* out) {
+    const EncodeFn encode = encode_fn();
+    if (!encode) return fail(MK_ERR_CUDA, "prompt: the driver has no cuTensorMapEncodeTiled");
+    // one row or head: its stride is never used, but has to be one
+    const cuuint64_t rs = rows > 1 ? (cuuint64_t)row_s * 2 : 16, hs = heads > 1 ? (cuuint64_t)head_s * 2 : 16;
+    const bool flat = heads < 0;
+    const cuuint64_t dims[3] = {(cuuint64_t)width, flat ? (cuuint64_t)rows : (cuuint64_t)(heads ? heads : 1), (cuuint64_t)rows};
+    const cuuint64_t strides[2] = {flat ? rs : hs, rs};
+    const cuuint32_t boxes[3] = {64, flat ? (cuuint32_t)box : 1, (cuuint32_t)box}, one[3] = {1, 1, 1};
+    const CUresult r = encode(out, dtype == MK_DT_F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
+                              flat ? 2 : 3, const_cast<void*>(base), dims, strides, boxes, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                              CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
+                              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    if (r != CUDA_SUCCESS) return fail(MK_ERR_CUDA, "prompt: cuTensorMapEncodeTiled failed (%d)", (int)r);
+    return MK_OK;
+}
+
+template <bool F16>
+int run(const PromptP& p, const PromptMaps& maps, int grid, cudaStream_t s) {
+    auto kern = prompt_kernel<F16>;
+    static std::mutex lock;
+    static bool have[32];
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return cuda_status(e, "mk_prompt_attend");
+    {
+        std::lock_guard<std::mutex> hold(lock);
+        if (dev >= 32 || !have[dev]) {
+            e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM);
+            if (e != cudaSuccess) return cuda_status(e, "mk_prompt_attend");
+            if (dev < 32) have[dev] = true;
+        }
+    }
+    kern<<<grid, NT, SMEM, s>>>(p, maps);
+    return cuda_status(cudaGetLastError(), "mk_prompt_attend");
 }
 
 }  // namespace
@@ -112,15 +516,27 @@ extern "C" int mk_prompt_attend(const mk_prompt_attention* a, void* stream) {
         return fail(MK_ERR_INVALID_ARG, "prompt: negative stride");
     if (a->batch > (1 << 20) || (int64_t)a->n_tokens * a->n_heads > INT32_MAX / 16)
         return fail(MK_ERR_UNSUPPORTED, "prompt: too many sequences or queries in one call");
+    if ((a->n_tokens > 1 && (!a->q_token || !a->out_token)) || (a->n_keys > 1 && (!a->k_token || !a->rope_token || !a->v_token)) ||
+        (a->n_heads > 1 && !a->out_head))
+        return fail(MK_ERR_UNSUPPORTED, "prompt: tokens must not share their rows (a stride of 0), nor heads those of out");
+    const int64_t blocks = ((int64_t)a->n_tokens / PAIR + a->batch) * a->n_heads;
+    if (blocks > INT32_MAX) return fail(MK_ERR_UNSUPPORTED, "prompt: too many sequences or queries in one call");
     PromptP p = {};
     p.q_starts = a->q_starts, p.k_starts = a->k_starts;
-    p.q = (const uint8_t*)a->q, p.k = (const uint8_t*)a->k, p.kr = (const uint8_t*)a->k_rope, p.v = (const uint8_t*)a->v;
-    p.out = (uint8_t*)a->out, p.lse = a->lse, p.status = a->status;
-    p.qt = a->q_token, p.qh = a->q_head, p.kt = a->k_token, p.kh = a->k_head, p.rt = a->rope_token;
-    p.vt = a->v_token, p.vh = a->v_head, p.ot = a->out_token, p.oh = a->out_head;
+    p.out = (uint8_t*)a->out, p.lse = a->lse, p.status = a->status, p.ot = a->out_token, p.oh = a->out_head;
     p.B = a->batch, p.n_q = a->n_tokens, p.n_k = a->n_keys, p.H = a->n_heads, p.scale = a->scale;
-    const int grid = p.n_q * p.H;
-    if (a->dtype == MK_DT_F16) prompt_rows<MK_DT_F16><<<grid, PT, 0, (cudaStream_t)stream>>>(p);
-    else prompt_rows<MK_DT_BF16><<<grid, PT, 0, (cudaStream_t)stream>>>(p);
-    return cuda_status(cudaGetLastError(), "mk_prompt_attend");
+    p.q_heads = a->q_head != 0, p.k_heads = a->k_head != 0, p.v_heads = a->v_head != 0;
+    const long long ns = mk_wait_ns_();
+    p.wait_ns = (unsigned)(ns < 4000000000ll ? ns : 4000000000ll);
+    p.skip_signal = mk_fault_("skip_attend_signal");
+    const int H = a->n_heads, dt = a->dtype, M = a->n_keys;
+    PromptMaps maps = {};
+    if (const int rc = map_of(a->q, dt, NOPE + ROPE, p.q_heads ? H : 0, a->n_tokens, a->q_head, a->q_token, ROWS, &maps.q)) return rc;
+    if (M) {  // (without keys nothing is copied)
+        if (const int rc = map_of(a->k, dt, NOPE, p.k_heads ? H : 0, M, a->k_head, a->k_token, TILE, &maps.k)) return rc;
+        if (const int rc = map_of(a->k_rope, dt, ROPE, -1, M, 0, a->rope_token, TILE, &maps.r)) return rc;
+        if (const int rc = map_of(a->v, dt, VD, p.v_heads ? H : 0, M, a->v_head, a->v_token, 64, &maps.v)) return rc;
+    }
+    cudaStream_t s = (cudaStream_t)stream;
+    return dt == MK_DT_F16 ? run<true>(p, maps, (int)blocks, s) : run<false>(p, maps, (int)blocks, s);
 }
