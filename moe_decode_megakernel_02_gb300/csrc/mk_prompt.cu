@@ -32,6 +32,7 @@
 // after another, so that short ones fill the end. All waits have a limit.
 #include <climits>
 #include <mutex>
+#include <type_traits>
 
 #include "mk_tensor.cuh"
 
@@ -48,6 +49,9 @@ constexpr int KS = 5, VS = 3;                   // ring slots: panels of keys, h
 constexpr int VHALF_B = 64 * VD * 2;
 constexpr int K_OFF = 2 * Q_B, V_OFF = K_OFF + KS * PANEL_B, MISC_OFF = V_OFF + VS * VHALF_B;
 constexpr int NT = 384;                         // warps: softmax 2 x 4, copies, products, cleaning 2
+// registers of a softmax thread's row and of the others: of the launch's 384 x 168
+constexpr int REGS_SOFTMAX = 208, REGS_REST = 80;
+static_assert(256 * REGS_SOFTMAX + 128 * REGS_REST <= NT * 168, "");
 constexpr int T_S = 0, T_O = 2 * TILE, T_ALL = 512;  // tensor memory: S (and P) of both blocks, O of both
 static_assert(T_O + 2 * VD <= T_ALL && PANEL_B == VHALF_B, "");
 
@@ -187,42 +191,38 @@ __global__ void __launch_bounds__(NT, 1)
 
     if (warp < 8) {
         // ================ softmax, a row a thread ================
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(REGS_SOFTMAX));
         const int g = warp >> 2, row = i0 + g * ROWS + (tid & 127), mine_nt = g ? nt1 : nt0;
         const uint32_t my = tm + ((uint32_t)((warp & 3) * 32) << 16), my_s = my + T_S + g * TILE, my_o = my + T_O + g * VD;
         const int last = behind + row, least = behind + i0 + g * ROWS;  // the row's last key, and the block's first row's
         const bool neg = p.scale < 0.f;  // (then the smallest product counts: signs turned)
         const float scale2 = fabsf(p.scale) * LOG2E;
-        const uint32_t flip = neg ? 0x80000000u : 0u;
         float mx = -INFINITY, l = 0.f;
         bool ok = true;
-        for (int j = 0; j < mine_nt; ++j) {
-            if (!(ok = warp_wait(&ms.s_full[g], j & 1, limit))) break;
-            tm_after();
+        // one tile; EDGE: some row of the block does not see all of it
+        auto tile = [&](auto EDGE, int j) {
+            constexpr bool edge = decltype(EDGE)::value;
             const int j0 = j * TILE;
-            const bool edge = j0 + TILE - 1 > least;
-            float t0 = -INFINITY, t1 = -INFINITY;
+            uint32_t s[TILE];
 #pragma unroll
-            for (int c = 0; c < TILE; c += 32) {
-                uint32_t s[32];
-                tm_ld32(s, my_s + c);
-                tm_wait_ld();
-                if (edge) {
+            for (int c = 0; c < TILE; c += 32) tm_ld32(*reinterpret_cast<uint32_t(*)[32]>(s + c), my_s + c);
+            tm_wait_ld();
+            if (neg) {
 #pragma unroll
-                    for (int e = 0; e < 32; ++e)
-                        if (j0 + c + e > last) s[e] = 0xff800000u ^ flip;
-                }
-                if (neg) {
-#pragma unroll
-                    for (int e = 0; e < 32; ++e) s[e] ^= 0x80000000u;
-                }
-#pragma unroll
-                for (int e = 0; e < 32; e += 4) {
-                    t0 = fmaxf(t0, fmaxf(__uint_as_float(s[e]), __uint_as_float(s[e + 1])));
-                    t1 = fmaxf(t1, fmaxf(__uint_as_float(s[e + 2]), __uint_as_float(s[e + 3])));
-                }
+                for (int e = 0; e < TILE; ++e) s[e] ^= 0x80000000u;
             }
+            if constexpr (edge) {
+#pragma unroll
+                for (int e = 0; e < TILE; ++e)
+                    if (j0 + e > last) s[e] = 0xff800000u;
+            }
+            float t[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+            for (int e = 0; e < TILE; e += 8)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) t[i] = fmaxf(t[i], fmaxf(__uint_as_float(s[e + 2 * i]), __uint_as_float(s[e + 2 * i + 1])));
             // (a scale of 0 times a masked -infinity is no number)
-            const float top = fmaxf(t0, t1), tile_m = top == -INFINITY ? top : top * scale2;
+            const float top = fmaxf(fmaxf(t[0], t[1]), fmaxf(t[2], t[3])), tile_m = top == -INFINITY ? top : top * scale2;
             const bool rise = tile_m > mx + 8.f;
             if (j == 0) {
                 mx = tile_m;
@@ -231,16 +231,16 @@ __global__ void __launch_bounds__(NT, 1)
                 mx = mn;
                 l *= f;
                 // the last product is in the output
-                if (!(ok = warp_wait(&ms.o_done[g], (j - 1) & 1, limit))) break;
+                if (!(ok = warp_wait(&ms.o_done[g], (j - 1) & 1, limit))) return;
                 tm_after();
 #pragma unroll 1
-                for (int d = 0; d < VD; d += 32) {
-                    uint32_t o[32];
-                    tm_ld32(o, my_o + d);
+                for (int d = 0; d < VD; d += 16) {
+                    uint32_t o[16];
+                    tm_ld16(o, my_o + d);
                     tm_wait_ld();
 #pragma unroll
-                    for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
-                    tm_st32(my_o + d, o);
+                    for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+                    tm_st16(my_o + d, o);
                 }
                 tm_wait_st();
             }
@@ -248,27 +248,29 @@ __global__ void __launch_bounds__(NT, 1)
             float sum[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
             for (int c = 0; c < TILE; c += 32) {
-                uint32_t s[32], x[16];
-                tm_ld32(s, my_s + c);
-                tm_wait_ld();
-                if (neg) {
-#pragma unroll
-                    for (int e = 0; e < 32; ++e) s[e] ^= 0x80000000u;
-                }
+                uint32_t x[16];
 #pragma unroll
                 for (int e = 0; e < 32; e += 2) {
-                    float a = ex2(fmaf(__uint_as_float(s[e]), scale2, -ref)), d = ex2(fmaf(__uint_as_float(s[e + 1]), scale2, -ref));
-                    if (edge) {
+                    float a = ex2(fmaf(__uint_as_float(s[c + e]), scale2, -ref));
+                    float d = ex2(fmaf(__uint_as_float(s[c + e + 1]), scale2, -ref));
+                    if constexpr (edge) {  // (a scale of 0 again)
                         if (j0 + c + e > last) a = 0.f;
                         if (j0 + c + e + 1 > last) d = 0.f;
                     }
                     sum[(e >> 1) & 3] += a + d;
                     x[e >> 1] = pack16<F16>(a, d);
                 }
-                tm_st16(my_s + (c >> 1), x);  // over columns that have been read
+                tm_st16(my_s + (c >> 1), x);
             }
             l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
             tm_wait_st();
+        };
+        for (int j = 0; j < mine_nt; ++j) {
+            if (!(ok = warp_wait(&ms.s_full[g], j & 1, limit))) break;
+            tm_after();
+            if (j * TILE + TILE - 1 > least) tile(std::true_type(), j);
+            else tile(std::false_type(), j);
+            if (!ok) break;
             tm_before();
             bar_arrive(&ms.p_ready[g]);
         }
@@ -298,6 +300,10 @@ __global__ void __launch_bounds__(NT, 1)
             }
         }
         if (real && p.lse) p.lse[(long long)(q0 + row) * p.H + h] = l == 0.f ? -INFINITY : (mx + log2f(l)) * LN2;
+    } else {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(REGS_REST));
+    }
+    if (warp < 8) {
     } else if (warp == 8) {
         // ================ copies ================
         Slot<KS> ks;
