@@ -15,16 +15,17 @@
 //   O += P V    P as the tensor-memory operand, V from shared memory as it lies
 //               there (its rows are the product's K), O in tensor memory.
 // While the tensor cores work for one block, the other's four softmax warps
-// turn its scores into probabilities: products go block 0's O, its next S,
-// block 1's O, its next S, in the order they are issued, so that a block's next S
-// overwrites its P after the product that read it. O is rescaled only when a row's
-// maximum has risen by more than 2^8 since its reference.
+// turn its scores into probabilities. Each block has a warp that issues its
+// products, in their order: O of a tile (either half as soon as its P is there),
+// then the next S, which overwrites the P that the O before it has read. O is
+// rescaled only when a row's maximum has risen by more than 2^8 since its
+// reference.
 //
 // Shared memory is full: queries 96 KB, a ring of five 16 KB panels of keys (64
 // values of 128 keys), one of three 16 KB halves of values (64 keys).
 //
-// At the end of what is seen scores are masked, and since 0 x NaN is NaN, two
-// warps clean the tiles there: values that no row of the CTA sees become zeros;
+// At the end of what is seen scores are masked, and since 0 x NaN is NaN, a
+// warp cleans the tiles there: values that no row of the CTA sees become zeros;
 // so do values that are not finite and that only some rows see, and rows that
 // do see them get NaN.
 //
@@ -48,7 +49,7 @@ constexpr int Q_B = PANELS * PANEL_B;           // a block's queries
 constexpr int KS = 5, VS = 3;                   // ring slots: panels of keys, halves of values
 constexpr int VHALF_B = 64 * VD * 2;
 constexpr int K_OFF = 2 * Q_B, V_OFF = K_OFF + KS * PANEL_B, MISC_OFF = V_OFF + VS * VHALF_B;
-constexpr int NT = 384;                         // warps: softmax 2 x 4, copies, products, cleaning 2
+constexpr int NT = 384;                         // warps: softmax 2 x 4, copies, products 2, cleaning
 // registers of a softmax thread's row and of the others: of the launch's 384 x 168
 constexpr int REGS_SOFTMAX = 208, REGS_REST = 80;
 static_assert(256 * REGS_SOFTMAX + 128 * REGS_REST <= NT * 168, "");
@@ -56,8 +57,8 @@ constexpr int T_S = 0, T_O = 2 * TILE, T_ALL = 512;  // tensor memory: S (and P)
 static_assert(T_O + 2 * VD <= T_ALL && PANEL_B == VHALF_B, "");
 
 struct PromptMisc {
-    unsigned long long q_full[2], k_full[KS], k_free[KS], v_full[VS], v_ok[VS], v_free[VS], s_full[2], p_ready[2], o_done[2],
-        drained;
+    unsigned long long q_full[2], k_full[2], k_free[KS], v_full[VS], v_ok[VS], v_free[VS], s_full[2], p_ready[2][2], o_done[2],
+        turn[2], drained;
     unsigned tmem, abort;
     int scan[NT / 32], seq, pair, bad;
 };
@@ -89,12 +90,6 @@ __device__ __forceinline__ void tma_2d(uint32_t dst, const CUtensorMap* map, int
 template <bool F16>
 __device__ __forceinline__ uint32_t pack16(float lo, float hi) {
     return F16 ? pack_f16(lo, hi) : pack_bf16(lo, hi);
-}
-// one 32-bit word with either 16-bit half not finite
-template <bool F16>
-__device__ __forceinline__ bool not_finite(uint32_t w) {
-    constexpr uint32_t E = F16 ? 0x7c00u : 0x7f80u;
-    return (w & E) == E || (w & (E << 16)) == E << 16;
 }
 // a ring slot and its turn
 template <int N>
@@ -157,13 +152,16 @@ __global__ void __launch_bounds__(NT, 1)
     if (tid == 0) {
         for (int i = 0; i < 2; ++i) {
             bar_init(&ms.q_full[i], 1);
+            bar_init(&ms.k_full[i], 1);
             bar_init(&ms.s_full[i], 1);
-            bar_init(&ms.p_ready[i], 128);
+            bar_init(&ms.turn[i], 1);
+            bar_init(&ms.p_ready[i][0], 128);
+            bar_init(&ms.p_ready[i][1], 128);
             bar_init(&ms.o_done[i], 1);
         }
-        for (int i = 0; i < KS; ++i) bar_init(&ms.k_full[i], 1), bar_init(&ms.k_free[i], 1);
-        for (int i = 0; i < VS; ++i) bar_init(&ms.v_full[i], 1), bar_init(&ms.v_ok[i], 2), bar_init(&ms.v_free[i], 1);
-        bar_init(&ms.drained, 1);
+        for (int i = 0; i < KS; ++i) bar_init(&ms.k_free[i], 2);
+        for (int i = 0; i < VS; ++i) bar_init(&ms.v_full[i], 1), bar_init(&ms.v_ok[i], 1), bar_init(&ms.v_free[i], 2);
+        bar_init(&ms.drained, 2);
         ms.abort = 0;
         ms.bad = INT_MAX;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -251,19 +249,24 @@ __global__ void __launch_bounds__(NT, 1)
                 uint32_t x[16];
 #pragma unroll
                 for (int e = 0; e < 32; e += 2) {
-                    float a = ex2(fmaf(__uint_as_float(s[c + e]), scale2, -ref));
-                    float d = ex2(fmaf(__uint_as_float(s[c + e + 1]), scale2, -ref));
+                    float a, d;
+                    fma2(a, d, __uint_as_float(s[c + e]), __uint_as_float(s[c + e + 1]), scale2, scale2, -ref, -ref);
+                    a = ex2(a), d = ex2(d);
                     if constexpr (edge) {  // (a scale of 0 again)
                         if (j0 + c + e > last) a = 0.f;
                         if (j0 + c + e + 1 > last) d = 0.f;
                     }
-                    sum[(e >> 1) & 3] += a + d;
+                    add2(sum[e & 2], sum[(e & 2) + 1], a, d);
                     x[e >> 1] = pack16<F16>(a, d);
                 }
                 tm_st16(my_s + (c >> 1), x);
+                if (c & 32) {  // half of the keys: its product need not wait for the other half
+                    tm_wait_st();
+                    tm_before();
+                    bar_arrive(&ms.p_ready[g][c >> 6]);
+                }
             }
             l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
-            tm_wait_st();
         };
         for (int j = 0; j < mine_nt; ++j) {
             if (!(ok = warp_wait(&ms.s_full[g], j & 1, limit))) break;
@@ -271,8 +274,6 @@ __global__ void __launch_bounds__(NT, 1)
             if (j * TILE + TILE - 1 > least) tile(std::true_type(), j);
             else tile(std::false_type(), j);
             if (!ok) break;
-            tm_before();
-            bar_arrive(&ms.p_ready[g]);
         }
         // ---- the block's end
         if (ok && mine_nt) ok = warp_wait(&ms.o_done[g], (mine_nt - 1) & 1, limit);
@@ -312,11 +313,12 @@ __global__ void __launch_bounds__(NT, 1)
         for (int j = 0; j < nt && ok; ++j) {
             const int key = k0 + j * TILE;
             for (int c = 0; c < PANELS; ++c, ks.next()) {
-                if (!(ok = !ks.turn || warp_wait(&ms.k_free[ks.i], (ks.turn - 1) & 1, limit))) break;
+                ok = ok && (!ks.turn || warp_wait(&ms.k_free[ks.i], (ks.turn - 1) & 1, limit));
+                if (!ok && c == 0) break;  // (a tile that has begun is finished all the same: its barrier counts all of it)
                 ++sent_k;
                 if (lane == 0) {
-                    unsigned long long* const bar = &ms.k_full[ks.i];
-                    bar_expect(bar, PANEL_B);
+                    unsigned long long* const bar = &ms.k_full[j & 1];  // a tile's panels meet there
+                    if (c == 0) bar_expect(bar, Q_B);
                     const uint32_t to = qs + K_OFF + ks.i * PANEL_B;
                     if (c < NOPE / 64) tma_3d(to, &maps.k, 64 * c, p.k_heads ? h : 0, key, bar);
                     else tma_2d(to, &maps.r, 0, key, bar);
@@ -341,7 +343,7 @@ __global__ void __launch_bounds__(NT, 1)
                 }
             }
         }
-    } else if (warp >= 10) {
+    } else if (warp == 11) {
         // ================ values that must not reach the output ================
         Slot<VS> vs;
         bool ok = true;
@@ -350,21 +352,36 @@ __global__ void __launch_bounds__(NT, 1)
             if (!(ok = warp_wait(&ms.v_full[vs.i], vs.turn & 1, limit))) break;
             const int j0 = 64 * j;
             if (j0 + 63 > all) {
-                uint8_t* const at = smem + V_OFF + vs.i * VHALF_B;
+                // 16-byte piece c: value panel c / 512, key c / 8 % 64 of the half
+                uint4* const at = reinterpret_cast<uint4*>(smem + V_OFF + vs.i * VHALF_B) + lane;
                 int bad = INT_MAX;
-                for (int c = (warp - 10) * 32 + lane; c < VHALF_B / 16; c += 64) {
-                    const int key = j0 + ((c >> 3) & 63);
-                    if (key <= all) continue;
-                    uint4* const x = reinterpret_cast<uint4*>(at) + c;
-                    if (key > some) {
-                        *x = make_uint4(0, 0, 0, 0);
-                    } else {
-                        const uint4 v = *x;
-                        if (not_finite<F16>(v.x) || not_finite<F16>(v.y) || not_finite<F16>(v.z) || not_finite<F16>(v.w)) {
-                            *x = make_uint4(0, 0, 0, 0);
+                // keys that some rows see, eight pieces a thread at a time: an exponent of ones carries into the sign
+                constexpr uint32_t E = F16 ? 0x7c007c00u : 0x7f807f80u, ONE = F16 ? 0x04000400u : 0x00800080u;
+                if (j0 <= some) {
+#pragma unroll 1
+                    for (int i = 0; i < VHALF_B / 512; i += 8) {
+                        uint4 v[8];
+                        uint32_t ones = 0;
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) v[e] = at[(i + e) * 32];
+#pragma unroll
+                        for (int e = 0; e < 8; ++e)
+                            ones |= ((v[e].x & E) + ONE) | ((v[e].y & E) + ONE) | ((v[e].z & E) + ONE) | ((v[e].w & E) + ONE);
+                        if (!(ones & 0x80008000u)) continue;
+                        for (int e = 0; e < 8; ++e) {
+                            const int key = j0 + (((i + e) * 32 + lane) >> 3 & 63);
+                            const uint4 x = at[(i + e) * 32];
+                            if (key <= all || key > some ||
+                                !((((x.x & E) + ONE) | ((x.y & E) + ONE) | ((x.z & E) + ONE) | ((x.w & E) + ONE)) & 0x80008000u))
+                                continue;
+                            at[(i + e) * 32] = make_uint4(0, 0, 0, 0);
                             bad = min(bad, key);
                         }
                     }
+                }
+                if (j0 + 63 > some) {
+                    for (int i = 0; i < VHALF_B / 512; ++i)
+                        if (j0 + ((i * 32 + lane) >> 3 & 63) > some) at[i * 32] = make_uint4(0, 0, 0, 0);
                 }
                 if (bad != INT_MAX) atomicMin(&ms.bad, bad);
                 fence_async();
@@ -373,66 +390,73 @@ __global__ void __launch_bounds__(NT, 1)
             if (lane == 0) bar_arrive(&ms.v_ok[vs.i]);
         }
     } else {
-        // ================ products, an elected lane issues ================
+        // ================ products: a warp for each block, an elected lane issues ================
+        // (a constant block: operands then stay in uniform registers)
+        auto products = [&](auto G) {
+        constexpr int g = decltype(G)::value;
+        const int mine_nt = g ? nt1 : nt0;
         const uint32_t tmu = __shfl_sync(0xffffffffu, tm, 0);
         constexpr uint32_t QK = mma_desc(ROWS, TILE, false, false, F16), PV = mma_desc(ROWS, VD, true, false, F16);
-        const uint64_t qd = smem_desc(qs, 16, 1024), kd = smem_desc(qs + K_OFF, 16, 1024), vd = smem_desc(qs + V_OFF, 8192, 1024);
+        const uint64_t qd = smem_desc(qs + g * Q_B, 16, 1024), kd = smem_desc(qs + K_OFF, 16, 1024), vd = smem_desc(qs + V_OFF, 8192, 1024);
+        const uint32_t ts = tmu + T_S + g * TILE, to = tmu + T_O + g * VD;
         bool ok = true;
-        // S of block g for tile j, whose keys' first panel is in slot `at`
-        auto scores = [&](int g, int j, Slot<KS> at, bool free) {
-            if (j == 0) ok = ok && warp_wait(&ms.q_full[g], 0, limit);
-            Slot<KS> s = at;
-            for (int c = 0; c < PANELS; ++c, s.next()) ok = ok && warp_wait(&ms.k_full[s.i], s.turn & 1, limit);
-            if (!ok) return;
-            tm_after();
-            if (elect_one()) {
-                s = at;
-#pragma unroll
-                for (int c = 0; c < PANELS; ++c, s.next()) {
-#pragma unroll
-                    for (int k = 0; k < 4; ++k)
-                        mma_ss(tmu + T_S + g * TILE, desc_on(qd, g * Q_B + c * PANEL_B + k * 32),
-                               desc_on(kd, s.i * PANEL_B + k * 32), QK, c > 0 || k > 0);
-                    if (free) mma_commit(&ms.k_free[s.i]);
-                }
-                mma_commit(&ms.s_full[g]);
-            }
-            __syncwarp();
-        };
-        auto outputs = [&](int g, int j, Slot<VS> at, bool free) {
-            ok = ok && warp_wait(&ms.p_ready[g], j & 1, limit);
-            Slot<VS> s = at;
-            for (int c = 0; c < 2; ++c, s.next()) ok = ok && warp_wait(&ms.v_ok[s.i], s.turn & 1, limit);
-            if (!ok) return;
-            tm_after();
-            if (elect_one()) {
-                s = at;
-#pragma unroll
-                for (int c = 0; c < 2; ++c, s.next()) {
-#pragma unroll
-                    for (int k = 0; k < 4; ++k)
-                        mma_ts(tmu + T_O + g * VD, tmu + T_S + g * TILE + (4 * c + k) * 8, desc_on(vd, s.i * VHALF_B + k * 2048),
-                               PV, j > 0 || c > 0 || k > 0);
-                    if (free) mma_commit(&ms.v_free[s.i]);
-                }
-                if (!p.skip_signal) mma_commit(&ms.o_done[g]);
-            }
-            __syncwarp();
-        };
         Slot<KS> ks;
         Slot<VS> vs;
-        if (nt0) scores(0, 0, ks, !nt1);
-        if (nt1) scores(1, 0, ks, true);
-        for (int c = 0; c < PANELS; ++c) ks.next();
-        for (int j = 0; j < nt && ok; ++j) {
-            // what is read last for the tile frees it
-            if (j < nt0) outputs(0, j, vs, j >= nt1);
-            if (j + 1 < nt0) scores(0, j + 1, ks, j + 1 >= nt1);
-            if (j < nt1) outputs(1, j, vs, true);
-            if (j + 1 < nt1) scores(1, j + 1, ks, true);
+        // a tile that the block does not see is let go as it comes
+        auto scores = [&](int j) {
+            if (j == 0 && mine_nt) ok = ok && warp_wait(&ms.q_full[g], 0, limit);
+            if (j == 0 && g) ok = ok && warp_wait(&ms.turn[1], 0, limit);
+            if (!(ok = ok && warp_wait(&ms.k_full[j & 1], (unsigned)j >> 1 & 1u, limit))) return;
+            tm_after();
+            if (elect_one()) {
+                Slot<KS> at = ks;
+                if (j < mine_nt) {
+#pragma unroll
+                    for (int c = 0; c < PANELS; ++c, at.next()) {
+                        if (c == PANELS - 1) bar_arrive(&ms.turn[g ^ 1]);  // (the other's first products follow these)
+#pragma unroll
+                        for (int k = 0; k < 4; ++k)
+                            mma_ss(ts, desc_on(qd, c * PANEL_B + k * 32), desc_on(kd, at.i * PANEL_B + k * 32), QK, c > 0 || k > 0);
+                        mma_commit(&ms.k_free[at.i]);
+                    }
+                    mma_commit(&ms.s_full[g]);
+                } else {
+                    bar_arrive(&ms.turn[g ^ 1]);
+                    for (int c = 0; c < PANELS; ++c, at.next()) bar_arrive(&ms.k_free[at.i]);
+                }
+            }
+            __syncwarp();
             for (int c = 0; c < PANELS; ++c) ks.next();
-            vs.next(), vs.next();
+        };
+        auto outputs = [&](int j) {
+            for (int c = 0; c < 2; ++c, vs.next()) {
+                ok = ok && (j >= mine_nt || warp_wait(&ms.p_ready[g][c], j & 1, limit)) && warp_wait(&ms.v_ok[vs.i], vs.turn & 1, limit);
+                // block 0's turn is after block 1's S of this tile, block 1's after block 0's S of the next one
+                if (c == 0 && j + g < nt) ok = ok && warp_wait(&ms.turn[g], (j + g) & 1, limit);
+                if (!ok) return;
+                tm_after();
+                if (elect_one()) {
+                    if (j < mine_nt) {
+#pragma unroll
+                        for (int k = 0; k < 4; ++k)
+                            mma_ts(to, ts + (4 * c + k) * 8, desc_on(vd, vs.i * VHALF_B + k * 2048), PV, j > 0 || c > 0 || k > 0);
+                        mma_commit(&ms.v_free[vs.i]);
+                        if (c == 1 && !p.skip_signal) mma_commit(&ms.o_done[g]);
+                    } else {
+                        bar_arrive(&ms.v_free[vs.i]);
+                    }
+                }
+                __syncwarp();
+            }
+        };
+        if (nt) scores(0);
+        for (int j = 0; j < nt && ok; ++j) {
+            outputs(j);
+            if (j + 1 < nt) scores(j + 1);
         }
+        };
+        if (warp == 9) products(std::integral_constant<int, 0>());
+        else products(std::integral_constant<int, 1>());
         // the last products end before the tensor memory goes, also when a role gave up
         if (elect_one()) mma_commit(&ms.drained);
         const long long t0 = now_ns();
@@ -453,7 +477,7 @@ __global__ void __launch_bounds__(NT, 1)
             };
             if (nt0) gone(&ms.q_full[0], 0);
             if (nt1) gone(&ms.q_full[1], 0);
-            for (int c = max(0, sent_k - KS); c < sent_k; ++c) gone(&ms.k_full[c % KS], (unsigned)(c / KS) & 1u);
+            for (int c = max(0, sent_k / PANELS - 2); c < sent_k / PANELS; ++c) gone(&ms.k_full[c & 1], (unsigned)c >> 1 & 1u);
             for (int c = max(0, sent_v - VS); c < sent_v; ++c) gone(&ms.v_full[c % VS], (unsigned)(c / VS) & 1u);
         }
         if (tid == 0 && p.status) *p.status = MK_ERR_TIMEOUT;

@@ -25,6 +25,22 @@ __device__ __forceinline__ float ex2(float x) {
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
 }
+// pairs of 32-bit numbers, one instruction a pair
+__device__ __forceinline__ void fma2(float& a, float& b, float x, float y, float s, float t, float u, float v) {
+    unsigned long long d, p, q, r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(p) : "f"(x), "f"(y));
+    asm("mov.b64 %0, {%1, %2};" : "=l"(q) : "f"(s), "f"(t));
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(u), "f"(v));
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(p), "l"(q), "l"(r));
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(d));
+}
+__device__ __forceinline__ void add2(float& a, float& b, float x, float y) {
+    unsigned long long d, p;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "f"(a), "f"(b));
+    asm("mov.b64 %0, {%1, %2};" : "=l"(p) : "f"(x), "f"(y));
+    asm("add.rn.f32x2 %0, %0, %1;" : "+l"(d) : "l"(p));
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(d));
+}
 __device__ __forceinline__ void bar_init(unsigned long long* b, unsigned n) {
     asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(sm32(b)), "r"(n) : "memory");
 }
