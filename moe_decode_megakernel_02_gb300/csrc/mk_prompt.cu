@@ -402,7 +402,9 @@ __global__ void __launch_bounds__(NT, 1)
         bool ok = true;
         Slot<KS> ks;
         Slot<VS> vs;
-        // a tile that the block does not see is let go as it comes
+        // (the whole warp waits, then one lane issues: a role that ran in one thread altogether hung)
+        auto here = [&](unsigned long long* bar, unsigned parity) { return bar_wait(bar, parity & 1u, limit); };
+        // S of a tile; one that the block does not see is let go as it comes
         auto scores = [&](int j) {
             if (j == 0 && mine_nt) ok = ok && warp_wait(&ms.q_full[g], 0, limit);
             if (j == 0 && g) ok = ok && warp_wait(&ms.turn[1], 0, limit);
@@ -413,7 +415,7 @@ __global__ void __launch_bounds__(NT, 1)
                 if (j < mine_nt) {
 #pragma unroll
                     for (int c = 0; c < PANELS; ++c, at.next()) {
-                        if (c == PANELS - 1) bar_arrive(&ms.turn[g ^ 1]);  // (the other's first products follow these)
+                        if (c == PANELS - 1) bar_arrive(&ms.turn[g ^ 1]);  // (the other's next products follow these)
 #pragma unroll
                         for (int k = 0; k < 4; ++k)
                             mma_ss(ts, desc_on(qd, c * PANEL_B + k * 32), desc_on(kd, at.i * PANEL_B + k * 32), QK, c > 0 || k > 0);
@@ -428,30 +430,36 @@ __global__ void __launch_bounds__(NT, 1)
             __syncwarp();
             for (int c = 0; c < PANELS; ++c) ks.next();
         };
-        auto outputs = [&](int j) {
-            for (int c = 0; c < 2; ++c, vs.next()) {
-                ok = ok && (j >= mine_nt || warp_wait(&ms.p_ready[g][c], j & 1, limit)) && warp_wait(&ms.v_ok[vs.i], vs.turn & 1, limit);
-                // block 0's turn is after block 1's S of this tile, block 1's after block 0's S of the next one
-                if (c == 0 && j + g < nt) ok = ok && warp_wait(&ms.turn[g], (j + g) & 1, limit);
-                if (!ok) return;
-                tm_after();
-                if (elect_one()) {
-                    if (j < mine_nt) {
+        // O of half a tile
+        auto half = [&](int j, int c) {
+            tm_after();
+            if (elect_one()) {
+                if (j < mine_nt) {
 #pragma unroll
-                        for (int k = 0; k < 4; ++k)
-                            mma_ts(to, ts + (4 * c + k) * 8, desc_on(vd, vs.i * VHALF_B + k * 2048), PV, j > 0 || c > 0 || k > 0);
-                        mma_commit(&ms.v_free[vs.i]);
-                        if (c == 1 && !p.skip_signal) mma_commit(&ms.o_done[g]);
-                    } else {
-                        bar_arrive(&ms.v_free[vs.i]);
-                    }
+                    for (int k = 0; k < 4; ++k)
+                        mma_ts(to, ts + (4 * c + k) * 8, desc_on(vd, vs.i * VHALF_B + k * 2048), PV, j > 0 || c > 0 || k > 0);
+                    mma_commit(&ms.v_free[vs.i]);
+                    if (c == 1 && !p.skip_signal) mma_commit(&ms.o_done[g]);
+                } else {
+                    bar_arrive(&ms.v_free[vs.i]);
                 }
-                __syncwarp();
             }
+            __syncwarp();
+            vs.next();
         };
         if (nt) scores(0);
         for (int j = 0; j < nt && ok; ++j) {
-            outputs(j);
+            // V and the first half's weights are here; block 0's turn is after block 1's S of this tile, block 1's after
+            // block 0's S of the next one
+            const unsigned turn1 = vs.i == VS - 1 ? vs.turn + 1 : vs.turn;
+            const int i1 = vs.i == VS - 1 ? 0 : vs.i + 1;
+            ok = __all_sync(0xffffffffu, here(&ms.v_ok[vs.i], vs.turn) && here(&ms.v_ok[i1], turn1) && (j >= mine_nt || here(&ms.p_ready[g][0], j)) &&
+                                             (j + g >= nt || here(&ms.turn[g], j + g)));
+            if (!ok) break;
+            half(j, 0);
+            if (j < mine_nt) ok = __all_sync(0xffffffffu, here(&ms.p_ready[g][1], j));
+            if (!ok) break;
+            half(j, 1);
             if (j + 1 < nt) scores(j + 1);
         }
         };
