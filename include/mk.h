@@ -662,7 +662,7 @@ int mk_prompt_attend(const mk_prompt_attention* args, void* stream);
  *   top_ids[r], top_logprobs[r]: the `top` tokens of the largest logits, by
  *                    (logit descending, id ascending), and their log p.
  * -infinity masks a token (log p -infinity). A row with a NaN or +infinity,
- * with no token unmasked, or whose temperature is not above 0, has no
+ * with no token unmasked, or whose temperature is not above 2^-120, has no
  * distribution: NaN, and ids -1. Sums are 32-bit. */
 typedef struct mk_logprob {
     const void* logits;       /* device [rows][row_stride], `dtype` */

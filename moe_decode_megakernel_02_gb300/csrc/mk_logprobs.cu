@@ -17,6 +17,8 @@
 //
 // Bound by HBM for batches (some 7 instructions a value), by latency for single
 // rows: a trip to memory, three votes, the cluster's meeting.
+#include <climits>
+#include <mutex>
 #include <type_traits>
 
 #include "mk_tensor.cuh"
@@ -29,10 +31,11 @@ typedef unsigned long long u64;
 
 constexpr int MAX_TOP = 64;
 constexpr int GT = 512, BATCH = 16;       // threads, values of a thread's round
-constexpr int GROUPS = GT / 4;
-// the list: what may be left of it, and what a round may add (k groups of four threads)
-constexpr int KEEP = 256, CAP = KEEP + MAX_TOP * 4 * BATCH;
+constexpr int GROUPS = GT / 4;            // of four threads; up to k = 32 half as many, of eight
+// the list: what may be left of it, and what a round may add (the values of k groups)
+constexpr int SLACK = 8, CAP = MAX_TOP + SLACK + MAX_TOP * 4 * BATCH;
 constexpr int MAX_CLUSTER = 8;
+constexpr int AHEAD = 4;  // rounds in flight
 
 struct LogprobP {
     const uint8_t* logits;
@@ -49,8 +52,8 @@ struct LogprobShared {
     u64 best[MAX_TOP];  // sorted
     u64 group[GROUPS];
     u64 merge[MAX_CLUSTER * MAX_TOP];
-    float4 part[GT / 32];  // (m, s, t, -) of the warps
-    float4 cta[MAX_CLUSTER];
+    float4 part[GT / 32];  // Part of the warps
+    float4 cta[MAX_CLUSTER], mine;
     int n;
     u64 limit;
 };
@@ -76,16 +79,75 @@ __device__ __forceinline__ float max_nan(float a, float b) {
     return y;
 }
 
-// (m, s, t) of two parts; c: exponents of 2 a unit of logits
-__device__ __forceinline__ void join(float& m, float& s, float& t, float m2, float s2, float t2, float c) {
-    const float mn = max_nan(m, m2);
-    // a part without an unmasked logit has sums of 0
-    const float d = m == -INFINITY ? 0.f : (m - mn) * c, e = m2 == -INFINITY ? 0.f : (m2 - mn) * c;
-    const float f = ex2(d), g = ex2(e);
-    // (a sum whose weights vanish: its t, 0 times a large d, vanishes too)
-    t = f * t + (f > 0.f ? f * d * s : 0.f) + g * t2 + (g > 0.f ? g * e * s2 : 0.f);
-    s = f * s + g * s2;
-    m = mn;
+// the larger of two pairs of 16-bit values, each; no number stays none
+template <int DT>
+__device__ __forceinline__ uint32_t larger_pair(uint32_t a, uint32_t b) {
+    uint32_t y;
+    if constexpr (DT == MK_DT_BF16) asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(y) : "r"(a), "r"(b));
+    else asm("max.NaN.f16x2 %0, %1, %2;" : "=r"(y) : "r"(a), "r"(b));
+    return y;
+}
+
+// the values of a 16-byte word, and their largest
+template <int DT, int N>
+__device__ __forceinline__ void unpack(const uint4& z, float (&v)[N]) {
+    const uint32_t y[4] = {z.x, z.y, z.z, z.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        if constexpr (DT == MK_DT_F32) {
+            v[i] = __uint_as_float(y[i]);
+        } else if constexpr (DT == MK_DT_BF16) {
+            v[2 * i] = __uint_as_float(y[i] << 16);
+            v[2 * i + 1] = __uint_as_float(y[i] & 0xffff0000u);
+        } else {
+            const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&y[i]));
+            v[2 * i] = f.x, v[2 * i + 1] = f.y;
+        }
+    }
+}
+template <int DT>
+__device__ __forceinline__ float largest(const uint4& z) {
+    if constexpr (DT == MK_DT_F32) {
+        return max_nan(max_nan(__uint_as_float(z.x), __uint_as_float(z.y)), max_nan(__uint_as_float(z.z), __uint_as_float(z.w)));
+    } else {
+        const uint32_t y = larger_pair<DT>(larger_pair<DT>(z.x, z.y), larger_pair<DT>(z.z, z.w));
+        float v[8];
+        unpack<DT>(make_uint4(y, y, y, y), v);
+        return max_nan(v[0], v[1]);
+    }
+}
+
+// Sums of a part of the row, against its largest logit (in exponents of 2, c a unit of logits).
+struct Part {
+    float m, s, t;
+};
+__device__ __forceinline__ Part join(const Part& x, const Part& y, float c) {
+    const bool swap = y.m > x.m;
+    const Part a = swap ? y : x, b = swap ? x : y;
+    // a part without an unmasked logit has sums of 0; one that vanishes against the other adds nothing
+    const float d = b.m == -INFINITY ? 0.f : (b.m - a.m) * c, f = ex2(d);
+    return {max_nan(a.m, b.m), a.s + f * b.s, a.t + (f > 0.f ? f * (b.t + d * b.s) : 0.f)};
+}
+
+// Ranks of up to 32 M keys (how many are larger): a warp holds all of them, M a lane, and ranks its share by votes.
+// found(key, rank) runs in one lane for each key.
+template <int M, typename F>
+__device__ __forceinline__ void ranks(const u64* keys, int n, F found) {
+    constexpr int EACH = 32 * M / (GT / 32);
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    if (warp * EACH >= n) return;
+    u64 mine[M];
+#pragma unroll
+    for (int i = 0; i < M; ++i) mine[i] = i * 32 + lane < n ? keys[i * 32 + lane] : 0;
+#pragma unroll
+    for (int g = 0; g < EACH; ++g) {
+        const int at = warp * EACH + g;
+        const u64 x = at < n ? keys[at] : 0;
+        int rank = 0;
+#pragma unroll
+        for (int i = 0; i < M; ++i) rank += __popc(__ballot_sync(0xffffffffu, mine[i] > x));
+        if (lane == 0 && x) found(x, rank);
+    }
 }
 
 // The first k keys of `n` in sh.list, sorted, to sh.best; returns how many there are.
@@ -103,12 +165,9 @@ __device__ int first_keys(LogprobShared& sh, int n, int k) {
         top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
         if ((tid & 3) == 0) sh.group[tid >> 2] = top;
         __syncthreads();
-        if (tid < GROUPS) {
-            const u64 x = sh.group[tid];
-            int rank = 0;
-            for (int i = 0; i < GROUPS; ++i) rank += sh.group[i] > x;
+        ranks<4>(sh.group, GROUPS, [&](u64 x, int rank) {
             if (rank == k - 1) sh.limit = x;
-        }
+        });
         if (tid == 0) sh.n = 0;
         __syncthreads();
 #pragma unroll
@@ -120,12 +179,22 @@ __device__ int first_keys(LogprobShared& sh, int n, int k) {
         if (left == n) break;  // (then nothing is cut any more)
         n = left;
     }
-    for (int i = tid; i < n; i += GT) {
-        const u64 x = sh.list[i];
-        int rank = 0;
+    if (n <= 32) {
+        ranks<1>(sh.list, n, [&](u64 x, int rank) {
+            if (rank < k) sh.best[rank] = x;
+        });
+    } else if (n <= 128) {
+        ranks<4>(sh.list, n, [&](u64 x, int rank) {
+            if (rank < k) sh.best[rank] = x;
+        });
+    } else {
+        for (int i = tid; i < n; i += GT) {
+            const u64 x = sh.list[i];
+            int rank = 0;
 #pragma unroll 4
-        for (int j = 0; j < n; ++j) rank += sh.list[j] > x;
-        if (rank < k) sh.best[rank] = x;
+            for (int j = 0; j < n; ++j) rank += sh.list[j] > x;
+            if (rank < k) sh.best[rank] = x;
+        }
     }
     __syncthreads();
     return min(n, k);
@@ -147,6 +216,7 @@ template <int DT, bool TOP>
 __global__ void __launch_bounds__(GT, 2) logprob_kernel(const __grid_constant__ LogprobP p) {
     constexpr int VEC = DT == MK_DT_F32 ? 4 : 8, U = BATCH / VEC;  // values of 16 bytes, words of a round
     __shared__ LogprobShared sh;
+    extern __shared__ __align__(16) uint8_t ring[];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, split = p.split;
     const int r = blockIdx.x / split, part = blockIdx.x - r * split;
     const uint8_t* const x = p.logits + (long long)r * p.row_s * (DT == MK_DT_F32 ? 4 : 2);
@@ -155,175 +225,171 @@ __global__ void __launch_bounds__(GT, 2) logprob_kernel(const __grid_constant__ 
     const int words = (p.V - head) / VEC, tail = p.V - head - words * VEC;
     const int w0 = (int)((long long)words * part / split), w1 = (int)((long long)words * (part + 1) / split);
     const float T = p.temperature ? p.temperature[r] : 1.f;
-    const bool cold = !(T > 0.f);
-    const float c = cold ? 0.f : fminf(LOG2E / T, 1e38f);
+    const bool cold = !(T > 0x1p-120f);
+    const float c = cold ? 0.f : LOG2E / T;
     const int k = p.top;
     if (TOP && tid == 0) sh.n = 0;
 
-    float m = -INFINITY, s = 0.f, t = 0.f, tt[2] = {0.f, 0.f};  // (t's parts since m last rose)
-    bool have = false;  // k keys have been found
+    // the sums of e = 2^(c (x - m)) and of e c (x - m)
+    float m = -INFINITY, s = 0.f, t = 0.f;
+    auto rise = [&](float top) {
+        if (m != -INFINITY) {
+            const float d = (m - top) * c, f = ex2(d);
+            t = f > 0.f ? f * (t + d * s) : 0.f;
+            s *= f;
+        }
+        m = max_nan(m, top);  // (no number stays one)
+    };
+    bool have = false, sorted = false;  // k keys have been found; and nothing since
     u64 limit = 0;  // a key that the k-th largest one is not below; 0: none yet
     float limit_x = -INFINITY;
     int n = 0;      // of the list
     if (TOP) __syncthreads();
 
-    // N values a thread, ids from `id` in words of VEC that lie GT words apart; `in`: this thread has them
-    auto round = [&](auto COUNT, const float (&v)[BATCH], int id, bool in) {
-        constexpr int N = decltype(COUNT)::value;
-        auto id_of = [&](int i) { return id + i / VEC * GT * VEC + i % VEC; };
-        float top = -INFINITY;
-        if (in) {
-            top = v[0];
-#pragma unroll
-            for (int i = 1; i < N; ++i) top = max_nan(top, v[i]);
-            const float mn = max_nan(m, top);
-            if (!(mn == m)) {
-                if (m != -INFINITY) {
-                    const float d = (m - mn) * c, f = ex2(d);
-                    t = f > 0.f ? f * (t + (tt[0] + tt[1]) + d * s) : 0.f;
-                    tt[0] = tt[1] = 0.f;
-                    s *= f;
-                }
-                m = mn;
-            }
-            const float less = m == -INFINITY ? 0.f : -m;
-            float sum[2] = {0.f, 0.f};
-#pragma unroll
-            for (int i = 0; i < N; i += 2) {
-                float a = v[i], b = i + 1 < N ? v[i + 1] : -INFINITY;
-                add2(a, b, less, less);
-                fma2(a, b, a, b, c, c, 0.f, 0.f);
-                // (below 2^-150 a weight is 0; a masked logit times an infinite temperature's 0 is no number, and so too)
-                a = fmaxf(a, -150.f), b = fmaxf(b, -150.f);
-                const float e = ex2(a), g = ex2(b);
-                add2(sum[0], sum[1], e, g);
-                fma2(tt[0], tt[1], e, g, a, b, tt[0], tt[1]);
-            }
-            s += sum[0] + sum[1];
+    auto add = [&](float x) {
+        // (below 2^-150 a weight is 0; a masked logit times an infinite temperature's 0 is no number, and so too)
+        const float z = fmaxf((x - m) * c, -150.f), e = ex2(z);
+        s += e;
+        t = fmaf(e, z, t);
+    };
+    // A round's most probable tokens: `top` is this thread's largest logit of the round (`in`: it has any), each(f) calls
+    // f(logit, id) for all of them.
+    auto pick = [&](float top, bool in, auto each) {
+        const int some = __syncthreads_count(in && (!limit || top > limit_x));
+        if (!some) return;
+        if (some > k) {
+            // a threshold from the groups' largest keys
+            int first = INT_MAX;
+            each([&](float x, int id) {
+                if (x == top) first = min(first, id);
+            });
+            u64 best = in ? key_of(top, first) : 0;
+            best = max(best, __shfl_xor_sync(0xffffffffu, best, 1));
+            best = max(best, __shfl_xor_sync(0xffffffffu, best, 2));
+            if (k <= 32) best = max(best, __shfl_xor_sync(0xffffffffu, best, 4));
+            const int by = k <= 32 ? 3 : 2;
+            if ((lane & ((1 << by) - 1)) == 0) sh.group[tid >> by] = best;
+            if (tid == 0) sh.limit = 0;
+            __syncthreads();
+            auto found = [&](u64 x, int rank) {
+                if (rank == k - 1) sh.limit = x;
+            };
+            if (k <= 32) ranks<2>(sh.group, GROUPS / 2, found);
+            else ranks<4>(sh.group, GROUPS, found);
+            __syncthreads();
+            limit = max(limit, sh.limit);  // (keys from it on)
         }
-        if constexpr (TOP) {
-            const int some = __syncthreads_count(in && (!limit || top > limit_x));
-            if (!some) return;
-            if (some > k) {
-                // a threshold from the groups' largest keys
-                u64 best = 0;
-                if (in) {
-#pragma unroll
-                    for (int i = 0; i < N; ++i) best = max(best, key_of(v[i], id_of(i)));
-                }
-                best = max(best, __shfl_xor_sync(0xffffffffu, best, 1));
-                best = max(best, __shfl_xor_sync(0xffffffffu, best, 2));
-                if ((lane & 3) == 0) sh.group[tid >> 2] = best;
-                if (tid == 0) sh.limit = 0;
-                __syncthreads();
-                if (tid < GROUPS) {
-                    const u64 y = sh.group[tid];
-                    int rank = 0;
-#pragma unroll 8
-                    for (int i = 0; i < GROUPS; ++i) rank += sh.group[i] > y;
-                    if (rank == k - 1 && y) sh.limit = y;
-                }
-                __syncthreads();
-                limit = max(limit, sh.limit);  // (keys from it on)
-            }
-            if (in && (!limit || top >= logit_of(limit))) {
-#pragma unroll
-                for (int i = 0; i < N; ++i) {
-                    const u64 y = key_of(v[i], id_of(i));
-                    if (y >= limit) sh.list[atomicAdd(&sh.n, 1)] = y;
-                }
-            }
+        if (in && (!limit || top >= logit_of(limit)))
+            each([&](float x, int id) {
+                const u64 y = key_of(x, id);
+                if (y >= limit) sh.list[atomicAdd(&sh.n, 1)] = y;
+            });
+        __syncthreads();
+        n = sh.n;
+        __syncthreads();
+        sorted = false;
+        // (a threshold that follows closely spares the next rounds more than it costs)
+        if (n > k + SLACK || (!have && n >= k)) {
+            n = first_keys(sh, n, k);
+            if (tid < n) sh.list[tid] = sh.best[tid];
+            if (tid == 0) sh.n = n;
             __syncthreads();
-            n = sh.n;
-            __syncthreads();
-            if (n > KEEP || (!have && n >= k)) {
-                n = first_keys(sh, n, k);
-                if (tid < n) sh.list[tid] = sh.best[tid];
-                if (tid == 0) sh.n = n;
-                __syncthreads();
-                have = true;
-            }
-            if (have) {
-                limit = max(limit, sh.best[k - 1]);
-                limit_x = logit_of(limit);
-            }
+            have = sorted = true;
+        }
+        if (have) {
+            limit = max(limit, sh.best[k - 1]);
+            limit_x = logit_of(limit);
         }
     };
     auto single = [&](int id, bool in) {
-        float v[BATCH];
-        v[0] = in ? at1<DT>(x, id) : 0.f;
-        round(std::integral_constant<int, 1>(), v, id, in);
+        const float x0 = in ? at1<DT>(x, id) : -INFINITY;
+        if (in) {
+            if (!(x0 <= m)) rise(x0);
+            add(x0);
+        }
+        if constexpr (TOP)
+            pick(x0, in, [&](auto f) {
+                if (in) f(x0, id);
+            });
     };
     if (part == 0 && head) single(tid, tid < head);
     {
         const int id0 = head + w0 * VEC, all = w1 - w0;
-        const uint4* const q = reinterpret_cast<const uint4*>(x + (long long)id0 * (DT == MK_DT_F32 ? 4 : 2));
-        uint4 next[U];
-        auto load = [&](int w) {
-#pragma unroll
-            for (int u = 0; u < U; ++u)
-                if (w + u * GT < all) next[u] = __ldcs(q + w + u * GT);
-        };
-#pragma unroll
-        for (int u = 0; u < U; ++u) next[u] = make_uint4(0, 0, 0, 0);
-        load(tid);
-        for (int w = 0; w < all; w += U * GT) {
-            float v[BATCH];
+        const uint8_t* const q = x + (long long)id0 * (DT == MK_DT_F32 ? 4 : 2);
+        // a thread's own words come through its own places in shared memory, some rounds ahead
+        const uint32_t mine = sm32(ring) + tid * 16;
+        int into = 0;
+        auto load = [&](int i) {
 #pragma unroll
             for (int u = 0; u < U; ++u) {
-                const uint32_t y[4] = {next[u].x, next[u].y, next[u].z, next[u].w};
+                const int w = (i * U + u) * GT + tid;
+                if (w < all) cp16(mine + (into * U + u) * GT * 16, q + 16ll * w, true);
+            }
+            if (++into == AHEAD) into = 0;
+            cp_commit();
+        };
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    if constexpr (DT == MK_DT_F32) {
-                        v[4 * u + i] = __uint_as_float(y[i]);
-                    } else if constexpr (DT == MK_DT_BF16) {
-                        v[8 * u + 2 * i] = __uint_as_float(y[i] << 16);
-                        v[8 * u + 2 * i + 1] = __uint_as_float(y[i] & 0xffff0000u);
-                    } else {
-                        const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&y[i]));
-                        v[8 * u + 2 * i] = f.x, v[8 * u + 2 * i + 1] = f.y;
+        for (int i = 0; i < AHEAD - 1; ++i) load(i);
+        int stage = 0;
+        for (int w = 0, i = 0; w < all; w += U * GT, ++i) {
+            load(i + AHEAD - 1);
+            cp_wait<AHEAD - 1>();
+            const uint8_t* const words = ring + stage * U * GT * 16 + tid * 16;
+            float top = -INFINITY;
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                if (w + u * GT + tid >= all) break;
+                const uint4 z = *reinterpret_cast<const uint4*>(words + u * GT * 16);
+                const float mx = largest<DT>(z);
+                if (!(mx <= m)) rise(mx);
+                top = max_nan(top, mx);
+                float y[VEC];
+                unpack<DT>(z, y);
+#pragma unroll
+                for (int e = 0; e < VEC; ++e) add(y[e]);
+            }
+            if constexpr (TOP)
+                pick(top, w + tid < all, [&](auto f) {
+#pragma unroll 1
+                    for (int u = 0; u < U; ++u) {
+                        if (w + u * GT + tid >= all) break;
+                        float y[VEC];
+                        unpack<DT>(*reinterpret_cast<const uint4*>(words + u * GT * 16), y);
+#pragma unroll
+                        for (int e = 0; e < VEC; ++e) f(y[e], id0 + (w + u * GT + tid) * VEC + e);
                     }
-                }
-            }
-            load(w + U * GT + tid);
-            if (w + U * GT <= all) {
-                round(std::integral_constant<int, BATCH>(), v, id0 + (w + tid) * VEC, true);
-            } else {  // the last round, word by word
-#pragma unroll
-                for (int u = 0; u < U; ++u) {
-                    if (w + u * GT >= all) break;
-                    float y[BATCH];
-#pragma unroll
-                    for (int i = 0; i < VEC; ++i) y[i] = v[u * VEC + i];
-                    round(std::integral_constant<int, VEC>(), y, id0 + (w + u * GT + tid) * VEC, w + u * GT + tid < all);
-                }
-            }
+                });
+            if (++stage == AHEAD) stage = 0;
         }
     }
     if (part == split - 1 && tail) single(p.V - tail + tid, tid < tail);
 
     // ---- the CTA's part, to the row's first CTA
-    t += tt[0] + tt[1];
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const float m2 = __shfl_xor_sync(0xffffffffu, m, o), s2 = __shfl_xor_sync(0xffffffffu, s, o),
-                    t2 = __shfl_xor_sync(0xffffffffu, t, o);
-        join(m, s, t, m2, s2, t2, c);
+    auto meet = [&](Part a, int lanes) {  // over the first lanes of a warp
+        for (int o = 1; o < lanes; o <<= 1)
+            a = join(a, Part{__shfl_xor_sync(0xffffffffu, a.m, o), __shfl_xor_sync(0xffffffffu, a.s, o),
+                             __shfl_xor_sync(0xffffffffu, a.t, o)}, c);
+        return a;
+    };
+    Part all = meet(Part{m, s, t}, 32);
+    if (lane == 0) sh.part[warp] = make_float4(all.m, all.s, all.t, 0.f);
+    int found = k;
+    if (TOP && !sorted) found = first_keys(sh, n, k);
+    __syncthreads();
+    if (warp == 0) {
+        const float4 y = sh.part[lane & (GT / 32 - 1)];
+        all = meet(Part{y.x, y.y, y.z}, GT / 32);
+        if (lane == 0) {
+            if (split > 1) sh.mine = make_float4(all.m, all.s, all.t, 0.f);
+            else sh.cta[0] = make_float4(all.m, all.s, all.t, 0.f);
+        }
     }
-    if (lane == 0) sh.part[warp] = make_float4(m, s, t, 0.f);
-    int found = 0;
-    if (TOP) found = first_keys(sh, n, k);  // (and a barrier)
-    else __syncthreads();
-    m = -INFINITY, s = t = 0.f;
-    for (int w = 0; w < GT / 32; ++w) join(m, s, t, sh.part[w].x, sh.part[w].y, sh.part[w].z, c);
     if (split > 1) {
         asm volatile("barrier.cluster.arrive.relaxed.aligned;\n\tbarrier.cluster.wait.aligned;" ::: "memory");  // all have begun
-        if (tid == 0) put_remote(&sh.cta[part], 0, make_float4(m, s, t, 0.f));
+        if (tid == 0) put_remote(&sh.cta[part], 0, sh.mine);
         if (TOP && tid < k) put_remote(&sh.merge[part * k + tid], 0, tid < found ? sh.best[tid] : 0);
         asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
         if (part) return;
-        m = -INFINITY, s = t = 0.f;
-        for (int i = 0; i < split; ++i) join(m, s, t, sh.cta[i].x, sh.cta[i].y, sh.cta[i].z, c);
         if (TOP) {
             for (int i = tid; i < split * k; i += GT) {
                 const u64 y = sh.merge[i];
@@ -332,13 +398,16 @@ __global__ void __launch_bounds__(GT, 2) logprob_kernel(const __grid_constant__ 
                 for (int j = 0; j < split * k; ++j) rank += sh.merge[j] > y;
                 if (rank < k && y) sh.best[rank] = y;
             }
-            __syncthreads();
         }
     }
-    const float nan = __uint_as_float(0x7fffffffu), ls = logf(s);
+    __syncthreads();
+    all = {-INFINITY, 0.f, 0.f};
+    for (int i = 0; i < split; ++i) all = join(all, Part{sh.cta[i].x, sh.cta[i].y, sh.cta[i].z}, c);
+    m = all.m;
+    const float nan = __uint_as_float(0x7fffffffu), ls = logf(all.s);
     const bool bad = cold || !(m < INFINITY) || m == -INFINITY;
     auto logp = [&](float y) { return bad ? nan : y == -INFINITY ? y : (y - m) / T - ls; };
-    if (tid == 0 && p.entropy) p.entropy[r] = bad ? nan : ls - t / s * LN2;
+    if (tid == 0 && p.entropy) p.entropy[r] = bad ? nan : ls - all.t / all.s * LN2;
     for (int g = tid; g < p.given; g += GT) {
         const int id = p.tokens[(long long)r * p.given + g];
         p.logprobs[(long long)r * p.given + g] = (unsigned)id < (unsigned)p.V ? logp(at1<DT>(x, id)) : nan;
@@ -352,9 +421,25 @@ __global__ void __launch_bounds__(GT, 2) logprob_kernel(const __grid_constant__ 
 
 template <int DT>
 int run(const LogprobP& p, int rows, cudaStream_t s) {
+    constexpr int SMEM = AHEAD * GT * BATCH * (DT == MK_DT_F32 ? 4 : 2);
+    static std::mutex lock;
+    static bool have[32];
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return cuda_status(e, "mk_logprobs");
+    {
+        std::lock_guard<std::mutex> hold(lock);
+        if (dev >= 32 || !have[dev]) {
+            e = cudaFuncSetAttribute(logprob_kernel<DT, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM);
+            if (e == cudaSuccess) e = cudaFuncSetAttribute(logprob_kernel<DT, false>, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM);
+            if (e != cudaSuccess) return cuda_status(e, "mk_logprobs");
+            if (dev < 32) have[dev] = true;
+        }
+    }
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(rows * p.split));
     cfg.blockDim = dim3(GT);
+    cfg.dynamicSmemBytes = SMEM;
     cfg.stream = s;
     cudaLaunchAttribute at[1];
     at[0].id = cudaLaunchAttributeClusterDimension;

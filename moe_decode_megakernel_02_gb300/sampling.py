@@ -67,7 +67,7 @@ def logprobs(logits, tokens, top=0, temperature=None, stream=None):
     Returns (log probabilities, float32 shaped as tokens, or None; entropies, float32 [rows]; the top tokens, int32
     [rows, top], by descending logit, the lower id first where logits are equal; their log probabilities, float32
     [rows, top]). An id outside the vocabulary gets NaN. -inf masks a token; a row with a NaN, +inf, no unmasked token
-    or a temperature that is not above 0 gives NaN throughout, and ids -1."""
+    or a temperature that is not above 2^-120 gives NaN throughout, and ids -1."""
     dt = _DTYPE.get(logits.dtype)
     if dt is None or logits.dim() != 2 or not logits.is_cuda or (logits.stride(1) != 1 and logits.shape[1] > 1):
         raise ValueError("logits must be a float32, bfloat16 or float16 CUDA tensor [rows, vocab] with contiguous rows, "
