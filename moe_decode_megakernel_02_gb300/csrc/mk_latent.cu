@@ -35,6 +35,7 @@
 // tensor map: a block a row takes them, a position a warp at a time.
 #include <climits>
 #include <mutex>
+#include <type_traits>
 
 #include "mk_tensor.cuh"
 #include "mk_values.cuh"
@@ -61,7 +62,6 @@ struct LatentP {
     int nr;          // rows of a block, padded to 16
     int rows_blk;    // rows of a block
     int RB;          // row blocks of a sequence
-    int stages;      // tiles in flight
     int min_units;   // a CTA's least stretch of tiles
     float* slots;    // two of each CTA: its first and its last piece
     int* base;       // [items + 1]: first tile of each item, for the joining launch
@@ -153,9 +153,9 @@ __global__ void __launch_bounds__(LT) latent_rows(const __grid_constant__ Latent
 // ---------------------------------------------------------------- tensor cores
 
 constexpr int NT = 256, SMEM_MOST = 227 * 1024;
+constexpr int TILE = 32;  // positions
 
-// A sequence's row block and the tiles its rows see.
-template <int TILE>
+// A row block of a sequence and the tiles its rows see.
 struct Item {
     int b, rb, row0, rows;  // rows of the block: row0 .. row0 + rows - 1, token-major
     int lo, hi, common;     // positions: [lo, hi) are seen by some row, [lo, common) by all
@@ -174,9 +174,8 @@ struct Item {
     }
 };
 
-template <int TILE>
 struct Line {  // a role's place in the line of tiles
-    Item<TILE> it;
+    Item it;
     int item, tile;
     __device__ __forceinline__ void start(const LatentP& p, int i, int t) {
         item = i;
@@ -199,9 +198,10 @@ struct Line {  // a role's place in the line of tiles
 struct Spot {
     int stage = 0;
     unsigned turn = 0, c = 0;
-    __device__ __forceinline__ void next(int stages) {
+    template <int STAGES>
+    __device__ __forceinline__ void next() {
         ++c;
-        if (++stage == stages) stage = 0, ++turn;
+        if (++stage == STAGES) stage = 0, ++turn;
     }
     __device__ __forceinline__ int buf() const { return (int)(c & 1u); }
     __device__ __forceinline__ unsigned full() const { return turn & 1u; }
@@ -211,7 +211,7 @@ struct Spot {
 };
 
 struct LatentMisc {
-    unsigned long long kv_full[12], v_ok[12], pv_done[12], s_full[2], s_free[2], p_ready[2], q_ready, drained;
+    unsigned long long kv_full[8], v_ok[8], pv_done[8], s_full[2], s_free[2], p_ready[2], q_ready, drained;
     unsigned tmem, abort;
     int scan[NT / 32], found_item, found_base;
     int bad[16];           // of a piece: the first position of it that is not finite and that only some rows see
@@ -220,19 +220,17 @@ struct LatentMisc {
     long long to[64];
 };
 
-template <int MT, int TILE>
+template <int MT, int NR>
 struct LatentShape {
     static constexpr int RANK = 128 * MT, KP = 2 * MT + 1;  // 128-byte panels of a position
-    static constexpr int STAGE_B = KP * TILE * 128;
+    static constexpr int Q_B = KP * NR * 128, STAGE_B = KP * TILE * 128, P_B = NR * 128;  // P: two tiles' side by side
     static constexpr int MISC_B = 1984;
-    static constexpr int T_S = 0, T_O = 128, T_ALL = 512;
     // shared memory: queries, the ring, probabilities, the rest; and room to align to 1024
-    static int stages(int nr) {
-        const int n = (SMEM_MOST - 1024 - MISC_B - KP * nr * 128 - nr * 128) / STAGE_B;
-        return n < 12 ? n : 12;
-    }
-    static int smem(int nr) { return 1024 + MISC_B + KP * nr * 128 + nr * 128 + stages(nr) * STAGE_B; }
-    static_assert(sizeof(LatentMisc) <= MISC_B, "");
+    static constexpr int FIT = (SMEM_MOST - 1024 - MISC_B - Q_B - P_B) / STAGE_B, STAGES = FIT < 8 ? FIT : 8;
+    static constexpr int RING_OFF = Q_B, P_OFF = RING_OFF + STAGES * STAGE_B, MISC_OFF = P_OFF + P_B;
+    static constexpr int SMEM = 1024 + MISC_OFF + MISC_B;
+    static constexpr int T_S = 0, T_O = 2 * TILE, T_ALL = T_O + MT * NR <= 128 ? 128 : T_O + MT * NR <= 256 ? 256 : 512;
+    static_assert(sizeof(LatentMisc) <= MISC_B && STAGES >= 2 && T_O + MT * NR <= T_ALL, "");
 };
 
 struct LatentMaps {
@@ -255,16 +253,16 @@ __device__ __forceinline__ bool not_finite(uint32_t w) {
     return (w & E) == E || (w & (E << 16)) == E << 16;
 }
 
-template <int MT, int TILE, bool F16>
+template <int MT, int NR, bool F16>
 __global__ void __launch_bounds__(NT, 1)
     latent_kernel(const __grid_constant__ LatentP p, const __grid_constant__ LatentMaps maps) {
-    using S = LatentShape<MT, TILE>;
+    using S = LatentShape<MT, NR>;
+    constexpr int STAGES = S::STAGES;
     extern __shared__ uint8_t raw_smem[];
     uint8_t* const smem = raw_smem + ((1024u - (sm32(raw_smem) & 1023u)) & 1023u);
-    const int nr = p.nr, q_b = S::KP * nr * 128, stages = p.stages;
-    const uint32_t qs = sm32(smem), ring = qs + q_b, ps = ring + stages * S::STAGE_B;
-    uint8_t* const psm = smem + q_b + stages * S::STAGE_B;
-    LatentMisc& ms = *reinterpret_cast<LatentMisc*>(psm + nr * 128);
+    const uint32_t qs = sm32(smem), ring = qs + S::RING_OFF, ps = qs + S::P_OFF;
+    uint8_t* const psm = smem + S::P_OFF;
+    LatentMisc& ms = *reinterpret_cast<LatentMisc*>(smem + S::MISC_OFF);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const Limit limit = {&ms.abort, p.wait_ns};
 
@@ -273,7 +271,7 @@ __global__ void __launch_bounds__(NT, 1)
     const int items = p.B * p.RB, each = (items + NT - 1) / NT, i0 = min(items, tid * each), i1 = min(items, i0 + each);
     int mine = 0, own = 0;
     for (int i = i0; i < i1; ++i) {
-        Item<TILE> it;
+        Item it;
         it.set(p, i);
         own = it.n;
         mine += own;
@@ -286,7 +284,7 @@ __global__ void __launch_bounds__(NT, 1)
     }
     if (lane == 31) ms.scan[warp] = inc;
     if (tid == 0) {
-        for (int i = 0; i < stages; ++i) {
+        for (int i = 0; i < STAGES; ++i) {
             bar_init(&ms.kv_full[i], 1);
             bar_init(&ms.v_ok[i], 1);
             bar_init(&ms.pv_done[i], 1);
@@ -320,7 +318,7 @@ __global__ void __launch_bounds__(NT, 1)
         int at = before;
         for (int i = i0; i < i1; ++i) {
             if (each > 1) {
-                Item<TILE> it;
+                Item it;
                 it.set(p, i);
                 own = it.n;
             }
@@ -339,12 +337,12 @@ __global__ void __launch_bounds__(NT, 1)
     const uint32_t tm = ms.tmem;
     int sent = 0;  // tiles that the copying warp has asked for
     if (first < end) {
-        Line<TILE> w;
+        Line w;
         w.start(p, ms.found_item, first - ms.found_base);
         if (warp < 4) {
             // ================ softmax, and the pieces' ends ================
             const int r0 = 16 * warp + (lane >> 2);  // this thread's rows: r0 and r0 + 8
-            const bool act = 16 * warp < nr;
+            const bool act = 16 * warp < NR;
             const uint32_t my = tm + ((uint32_t)(warp * 32) << 16);
             const float scale2 = p.scale * LOG2E;
             Spot at_c, back;
@@ -352,9 +350,9 @@ __global__ void __launch_bounds__(NT, 1)
             unsigned piece = 0;
             for (int u = first; u < end; ++piece) {
                 const int take = min(w.it.n - w.tile, end - u);
-                const Item<TILE>& it = w.it;
+                const Item& it = w.it;
                 // queries, a row a warp: every product that read the last ones has ended (all its scores came)
-                for (int r = warp; r < nr; r += 4) {
+                for (int r = warp; r < NR; r += 4) {
                     const int g = it.row0 + r, t = g / p.H, h = g - t * p.H;
                     const uint8_t* const a = p.q + 2 * (it.b * p.qb + t * p.qt + h * p.qh);
                     const uint8_t* const e = p.qr + 2 * (it.b * p.rb + t * p.rt + h * p.rh);
@@ -362,7 +360,7 @@ __global__ void __launch_bounds__(NT, 1)
                     if (p.q_vec) {
 #pragma unroll
                         for (int c = lane; c < 8 * S::KP; c += 32)
-                            cp16(qs + panel_at(0, nr, r, c), in ? (c < 16 * MT ? a + 16 * c : e + 16 * (c - 16 * MT)) : p.q, in);
+                            cp16(qs + panel_at(0, NR, r, c), in ? (c < 16 * MT ? a + 16 * c : e + 16 * (c - 16 * MT)) : p.q, in);
                     } else {
                         for (int c = lane; c < 8 * S::KP; c += 32) {
                             uint32_t x[4] = {0, 0, 0, 0};
@@ -372,7 +370,7 @@ __global__ void __launch_bounds__(NT, 1)
 #pragma unroll
                                 for (int i = 0; i < 4; ++i) x[i] = s2[2 * i] | (uint32_t)s2[2 * i + 1] << 16;
                             }
-                            *reinterpret_cast<uint4*>(smem + panel_at(0, nr, r, c)) = make_uint4(x[0], x[1], x[2], x[3]);
+                            *reinterpret_cast<uint4*>(smem + panel_at(0, NR, r, c)) = make_uint4(x[0], x[1], x[2], x[3]);
                         }
                     }
                 }
@@ -458,29 +456,24 @@ __global__ void __launch_bounds__(NT, 1)
 #pragma unroll 1
                         for (int mb = 0; mb < MT; ++mb)
 #pragma unroll 1
-                            for (int c = 0; c < nr; c += 16) {
+                            for (int c = 0; c < NR; c += 16) {
                                 uint32_t o[16];
-                                tm_ld16(o, my + S::T_O + mb * nr + c);
+                                tm_ld16(o, my + S::T_O + mb * NR + c);
                                 tm_wait_ld();
 #pragma unroll
                                 for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * ms.f[c + e]);
-                                tm_st16(my + S::T_O + mb * nr + c, o);
+                                tm_st16(my + S::T_O + mb * NR + c, o);
                             }
                         tm_wait_st();
                         tm_before();
                         bar_named(1, 128);
                     }
                     // the buffer is free when the product of the tile that it held last has read it
-                    if (TILE == 32) {
-                        if (at_c.c >= 2) {
-                            // (of the tile before the last one: its stage is the one before `back`)
-                            Spot two = back;
-                            if (two.stage == 0) two.stage = stages - 1, --two.turn;
-                            else --two.stage;
-                            ok = ok && warp_wait(&ms.pv_done[two.stage], two.full(), limit);
-                        }
-                    } else if (at_c.c >= 1) {
-                        ok = ok && warp_wait(&ms.pv_done[back.stage], back.full(), limit);
+                    if (at_c.c >= 2) {  // (its stage is the one before `back`)
+                        Spot two = back;
+                        if (two.stage == 0) two.stage = STAGES - 1, --two.turn;
+                        else --two.stage;
+                        ok = ok && warp_wait(&ms.pv_done[two.stage], two.full(), limit);
                     }
                     if (act) {
 #pragma unroll
@@ -493,7 +486,7 @@ __global__ void __launch_bounds__(NT, 1)
                             for (int k = 0; k < TILE / 8; ++k) {
                                 const float a = ex2(x[e][2 * k] - ref), b = ex2(x[e][2 * k + 1] - ref);
                                 s0 += a, s1 += b;
-                                const int c = (TILE == 32 ? at_c.buf() * 4 : 0) + k;
+                                const int c = at_c.buf() * 4 + k;
                                 *reinterpret_cast<uint32_t*>(row + ((c ^ (r & 7)) << 4)) = pack16<F16>(a, b);
                             }
                             l[e] += s0 + s1;
@@ -503,7 +496,7 @@ __global__ void __launch_bounds__(NT, 1)
                     tm_before();
                     bar_arrive(&ms.p_ready[at_c.buf()]);
                     back = at_c;
-                    at_c.next(stages);
+                    at_c.next<STAGES>();
                 }
                 // ---- the piece: maxima and sums by row, then the output out of tensor memory
                 if (act) {
@@ -529,13 +522,13 @@ __global__ void __launch_bounds__(NT, 1)
                 bar_named(1, 128);
                 tm_after();
                 const bool whole = take == it.n;
-                float* const slot = p.slots + (2ll * blockIdx.x + (u == first ? 0 : 1)) * ((long long)nr * (S::RANK + 2));
+                float* const slot = p.slots + (2ll * blockIdx.x + (u == first ? 0 : 1)) * ((long long)NR * (S::RANK + 2));
 #pragma unroll 1
                 for (int c = 0; c < it.rows; c += 16) {
 #pragma unroll 2
                     for (int mb = 0; mb < MT; ++mb) {
                         uint32_t o[16];
-                        tm_ld16(o, my + S::T_O + mb * nr + c);
+                        tm_ld16(o, my + S::T_O + mb * NR + c);
                         tm_wait_ld();
                         const int d = mb * 128 + warp * 32 + lane;
                         if (whole) {
@@ -552,7 +545,7 @@ __global__ void __launch_bounds__(NT, 1)
                 if (tid < it.rows) {
                     const float l2 = ms.sum[tid];
                     if (!whole)
-                        *reinterpret_cast<float2*>(slot + (long long)nr * S::RANK + 2 * tid) = make_float2(ms.m[tid], l2);
+                        *reinterpret_cast<float2*>(slot + (long long)NR * S::RANK + 2 * tid) = make_float2(ms.m[tid], l2);
                     else if (p.lse)
                         p.lse[(long long)it.b * p.T * p.H + it.row0 + tid] = l2 == 0.f ? -INFINITY : (ms.m[tid] + log2f(l2)) * LN2;
                 }
@@ -567,7 +560,7 @@ __global__ void __launch_bounds__(NT, 1)
             // of the 32 after them.
             const int rows = min(TILE, 1 << p.ps_shift), parts = TILE / rows, mask = (1 << p.ps_shift) - 1;
             const int tiles = end - first, pshift = __ffs(parts) - 1;
-            Line<TILE> ahead = w;
+            Line ahead = w;
             int ahead_c = lane >> pshift;
             ahead.on(p, ahead_c);
             auto page_next = [&] {  // of this lane's box of the next 32; one that nothing sees reads as zeros
@@ -589,12 +582,12 @@ __global__ void __launch_bounds__(NT, 1)
             int now = page_next(), next = 0;
             int box = 0;
             Spot pl;
-            for (int c = 0; c < tiles; ++c, pl.next(stages)) {
+            for (int c = 0; c < tiles; ++c, pl.next<STAGES>()) {
                 const int j0 = w.at();
                 w.on(p, 1);
                 const uint32_t st = ring + pl.stage * S::STAGE_B;
                 unsigned long long* const bar = &ms.kv_full[pl.stage];
-                if (c >= stages && !warp_wait(&ms.pv_done[pl.stage], pl.free(), limit)) break;
+                if (c >= STAGES && !warp_wait(&ms.pv_done[pl.stage], pl.free(), limit)) break;
                 if (lane == 0) bar_expect(bar, S::STAGE_B);
                 sent = c + 1;
                 for (int i = 0; i < parts; ++i, ++box) {
@@ -617,13 +610,13 @@ __global__ void __launch_bounds__(NT, 1)
             bool ok = true;
             for (int u = first; u < end && ok; ++piece) {
                 const int take = min(w.it.n - w.tile, end - u);
-                const Item<TILE>& it = w.it;
+                const Item& it = w.it;
                 int bad = INT_MAX;
-                for (int i = 0; i < take; ++i, pl.next(stages)) {
+                for (int i = 0; i < take; ++i, pl.next<STAGES>()) {
                     const int j0 = (it.t0 + w.tile + i) * TILE;
                     if (!(ok = warp_wait(&ms.kv_full[pl.stage], pl.full(), limit))) break;
                     if (j0 < it.lo || j0 + TILE > it.common) {
-                        uint8_t* const st = smem + q_b + pl.stage * S::STAGE_B;
+                        uint8_t* const st = smem + S::RING_OFF + pl.stage * S::STAGE_B;
                         for (int r = 0; r < TILE; ++r) {
                             const int j = j0 + r;
                             const bool hidden = j < it.lo || j >= it.hi;
@@ -678,16 +671,16 @@ __global__ void __launch_bounds__(NT, 1)
                             const uint32_t d = tmu + S::T_S + at_c.buf() * TILE;
 #pragma unroll
                             for (int j = 0; j < 4 * S::KP; ++j)
-                                mma_ss(d, desc_on(q, (j >> 2) * nr * 128 + (j & 3) * 32),
+                                mma_ss(d, desc_on(q, (j >> 2) * NR * 128 + (j & 3) * 32),
                                        desc_on(k, (j >> 2) * TILE * 128 + (j & 3) * 32), QK, j > 0);
                             mma_commit(&ms.s_full[at_c.buf()]);
                         }
                         __syncwarp();
-                        at_c.next(stages);
+                        at_c.next<STAGES>();
                     }
                 }
             } else {
-                const uint32_t PV = mma_desc(128, nr, false, true, F16);
+                constexpr uint32_t PV = mma_desc(128, NR, false, true, F16);
                 const uint64_t v0 = smem_desc(ring, TILE * 128, 1024), p0 = smem_desc(ps, 16, 1024);
                 for (int u = first; u < end && ok; ++piece) {
                     const int take = min(w.it.n - w.tile, end - u);
@@ -700,18 +693,18 @@ __global__ void __launch_bounds__(NT, 1)
                         tm_after();
                         if (elect_one()) {
                             const uint64_t v = desc_on(v0, at_c.stage * S::STAGE_B);
-                            const uint64_t pb = desc_on(p0, TILE == 32 ? at_c.buf() * 64 : 0);
+                            const uint64_t pb = desc_on(p0, at_c.buf() * 64);
                             // the first tile of a piece overwrites
 #pragma unroll
                             for (int mb = 0; mb < MT; ++mb)
 #pragma unroll
                                 for (int j = 0; j < TILE / 16; ++j)
-                                    mma_ss(tmu + S::T_O + mb * nr, desc_on(v, mb * 2 * TILE * 128 + j * 2048),
+                                    mma_ss(tmu + S::T_O + mb * NR, desc_on(v, mb * 2 * TILE * 128 + j * 2048),
                                            desc_on(pb, j * 32), PV, i > 0 || j > 0);
                             if (!p.skip_signal) mma_commit(&ms.pv_done[at_c.stage]);
                         }
                         __syncwarp();
-                        at_c.next(stages);
+                        at_c.next<STAGES>();
                     }
                 }
             }
@@ -730,8 +723,8 @@ __global__ void __launch_bounds__(NT, 1)
         // copies may still be on their way into this CTA's memory: at most the ring's last tiles
         if (warp == 4) {
             const long long t0 = now_ns();
-            for (int c = max(0, sent - stages); c < sent; ++c)
-                while (!bar_try(&ms.kv_full[c % stages], (unsigned)(c / stages) & 1u) && now_ns() - t0 < DRAIN_NS) {
+            for (int c = max(0, sent - STAGES); c < sent; ++c)
+                while (!bar_try(&ms.kv_full[c % STAGES], (unsigned)(c / STAGES) & 1u) && now_ns() - t0 < DRAIN_NS) {
                 }
         }
         if (tid == 0 && p.status) *p.status = MK_ERR_TIMEOUT;
@@ -792,12 +785,12 @@ __global__ void __launch_bounds__(JT) latent_join(const __grid_constant__ Latent
 
 // latents or rope parts as a tensor [page][row][value]; a box is up to TILE rows of a page by 64 values, in the 128-byte
 // swizzled order the products read
-int map_of(const void* base, int width, int tile, const mk_latent_pages& g, int64_t page_s, int64_t row_s, CUtensorMap* out) {
+int map_of(const void* base, int width, const mk_latent_pages& g, int64_t page_s, int64_t row_s, CUtensorMap* out) {
     const EncodeFn encode = encode_fn();
     if (!encode) return fail(MK_ERR_CUDA, "latent attend: the driver has no cuTensorMapEncodeTiled");
     const cuuint64_t dims[3] = {(cuuint64_t)width, (cuuint64_t)g.page_size, (cuuint64_t)g.n_pages};
     const cuuint64_t strides[2] = {(cuuint64_t)row_s * 2, (cuuint64_t)page_s * 2};
-    const cuuint32_t box[3] = {64, (cuuint32_t)(g.page_size < tile ? g.page_size : tile), 1}, one[3] = {1, 1, 1};
+    const cuuint32_t box[3] = {64, (cuuint32_t)(g.page_size < TILE ? g.page_size : TILE), 1}, one[3] = {1, 1, 1};
     const CUresult r = encode(out, g.dtype == MK_DT_F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3,
                               const_cast<void*>(base), dims, strides, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
                               CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
@@ -808,16 +801,16 @@ int map_of(const void* base, int width, int tile, const mk_latent_pages& g, int6
 
 struct Plan {
     bool rows;  // a block a row
-    int nr, rows_blk, RB, tile, grid, stages;
+    int nr, rows_blk, RB, grid;
     int64_t slots_off, bytes;
 };
 
 constexpr int MIN_UNITS = 4;  // positions a CTA takes at least: 4 tiles
 
-template <int MT, int TILE, bool F16>
+template <int MT, int NR, bool F16>
 int run(const LatentP* p, const mk_latent_pages* g, int grid, cudaStream_t s) {
-    using S = LatentShape<MT, TILE>;
-    auto kern = latent_kernel<MT, TILE, F16>;
+    using S = LatentShape<MT, NR>;
+    auto kern = latent_kernel<MT, NR, F16>;
     static std::mutex lock;
     static bool have[32];
     int dev = 0;
@@ -826,15 +819,15 @@ int run(const LatentP* p, const mk_latent_pages* g, int grid, cudaStream_t s) {
     {
         std::lock_guard<std::mutex> hold(lock);
         if (dev >= 32 || !have[dev]) {
-            e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_MOST);
+            e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, S::SMEM);
             if (e != cudaSuccess) return cuda_status(e, "mk_latent_attend");
             if (dev < 32) have[dev] = true;
         }
     }
     LatentMaps maps;
-    if (const int rc = map_of(g->latent, g->rank, TILE, *g, g->page_stride, g->row_stride, &maps.latent)) return rc;
-    if (const int rc = map_of(g->rope, 64, TILE, *g, g->rope_page_stride, g->rope_row_stride, &maps.rope)) return rc;
-    kern<<<grid, NT, S::smem(p->nr), s>>>(*p, maps);
+    if (const int rc = map_of(g->latent, g->rank, *g, g->page_stride, g->row_stride, &maps.latent)) return rc;
+    if (const int rc = map_of(g->rope, 64, *g, g->rope_page_stride, g->rope_row_stride, &maps.rope)) return rc;
+    kern<<<grid, NT, S::SMEM, s>>>(*p, maps);
     if (const int rc = cuda_status(cudaGetLastError(), "mk_latent_attend")) return rc;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(p->B * p->T * p->H * MT));
@@ -883,12 +876,9 @@ int make_plan(const mk_latent_attention* a, Plan& pl) {
     pl.RB = (rows + 63) / 64;
     pl.rows_blk = (rows + pl.RB - 1) / pl.RB;
     pl.RB = (rows + pl.rows_blk - 1) / pl.rows_blk;
-    pl.nr = (pl.rows_blk + 15) / 16 * 16;
-    pl.tile = pl.nr <= 32 ? 32 : 64;
-    pl.stages = g.rank == 512 ? (pl.tile == 32 ? LatentShape<4, 32>::stages(pl.nr) : LatentShape<4, 64>::stages(pl.nr))
-                              : (pl.tile == 32 ? LatentShape<2, 32>::stages(pl.nr) : LatentShape<2, 64>::stages(pl.nr));
+    pl.nr = pl.rows_blk <= 16 ? 16 : pl.rows_blk <= 32 ? 32 : 64;
     const int64_t items = (int64_t)t.batch * pl.RB, cap = (int64_t)t.pages_per_seq * g.page_size;
-    const int64_t most = items * ((cap + pl.tile - 1) / pl.tile + 1);
+    const int64_t most = items * ((cap + TILE - 1) / TILE + 1);
     if (most > (1 << 30)) return fail(MK_ERR_UNSUPPORTED, "latent attend: too many positions in one call");
     const int64_t want = (most + MIN_UNITS - 1) / MIN_UNITS;
     pl.grid = (int)(want < sms ? want : sms);
@@ -933,16 +923,20 @@ extern "C" int mk_latent_attend(const mk_latent_attention* a, void* workspace, i
         else wide ? latent_rows<MK_DT_BF16, 512, 64><<<grid, LT, 0, s>>>(p) : latent_rows<MK_DT_BF16, 256, 64><<<grid, LT, 0, s>>>(p);
         return cuda_status(cudaGetLastError(), "mk_latent_attend");
     }
-    p.nr = pl.nr, p.rows_blk = pl.rows_blk, p.RB = pl.RB, p.stages = pl.stages, p.min_units = MIN_UNITS;
+    p.nr = pl.nr, p.rows_blk = pl.rows_blk, p.RB = pl.RB, p.min_units = MIN_UNITS;
     p.base = (int*)workspace, p.slots = (float*)((uint8_t*)workspace + pl.slots_off);
     const long long ns = mk_wait_ns_();
     p.wait_ns = (unsigned)(ns < 4000000000ll ? ns : 4000000000ll);
     p.skip_signal = mk_fault_("skip_attend_signal");
     p.q_vec = rows_vec(a->q) && rows_vec(a->q_rope);
-    if (pl.tile == 32) {
-        if (wide) return f16 ? run<4, 32, true>(&p, &g, pl.grid, s) : run<4, 32, false>(&p, &g, pl.grid, s);
-        return f16 ? run<2, 32, true>(&p, &g, pl.grid, s) : run<2, 32, false>(&p, &g, pl.grid, s);
-    }
-    if (wide) return f16 ? run<4, 64, true>(&p, &g, pl.grid, s) : run<4, 64, false>(&p, &g, pl.grid, s);
-    return f16 ? run<2, 64, true>(&p, &g, pl.grid, s) : run<2, 64, false>(&p, &g, pl.grid, s);
+    auto go = [&](auto MT, auto NR) {
+        constexpr int mt = decltype(MT)::value, nr = decltype(NR)::value;
+        return f16 ? run<mt, nr, true>(&p, &g, pl.grid, s) : run<mt, nr, false>(&p, &g, pl.grid, s);
+    };
+    using std::integral_constant;
+    auto rank = [&](auto MT) {
+        if (pl.nr == 16) return go(MT, integral_constant<int, 16>());
+        return pl.nr == 32 ? go(MT, integral_constant<int, 32>()) : go(MT, integral_constant<int, 64>());
+    };
+    return wide ? rank(integral_constant<int, 4>()) : rank(integral_constant<int, 2>());
 }

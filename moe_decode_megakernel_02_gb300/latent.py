@@ -27,12 +27,14 @@ from .rotary import _ROTARY, _RotaryBytes, _freq, _layout
 
 _TYPES = {torch.bfloat16: DT_BF16, torch.float16: DT_F16}
 _byref = ctypes.byref
+_PAGES = struct.Struct("PP qqqq iiiiii")
 _WRITE = struct.Struct("Pqii Pqqqii Pii fi")
-_ATTEND = struct.Struct("PP PP PPP PP ii fi Pqii Pqqqii Pqqqii Pqqqii")
+_ATTEND = struct.Struct("PP PP PPP PP ii fi Pqii Pqqqii Pqqqii Pqqqii 72s")
 _PROMPT = struct.Struct("PP PPPPP PP qqqqqqqqq iiiiiiii fi")
 _WriteBytes, _AttendBytes = ctypes.c_char * _WRITE.size, ctypes.c_char * _ATTEND.size
-assert _WRITE.size == 24 + 40 + _ROTARY.size
-assert _ATTEND.size == 88 + 24 + 3 * 40 and ctypes.sizeof(LatentAttentionStruct) == 88
+_NEED = {}  # workspace bytes by device and shapes
+assert _PAGES.size == ctypes.sizeof(LatentPagesStruct) == 72 and _WRITE.size == 24 + 40 + _ROTARY.size
+assert _ATTEND.size == 88 + 24 + 3 * 40 + 72 and ctypes.sizeof(LatentAttentionStruct) == 88
 assert _PROMPT.size == ctypes.sizeof(PromptAttentionStruct) == 184
 
 
@@ -41,23 +43,24 @@ class LatentPages:
     or both float16, last dimensions contiguous (the two may be parts of one tensor)."""
 
     def __init__(self, latent, rope):
-        dt = _TYPES.get(latent.dtype)
-        if dt is None or rope.dtype != latent.dtype:
+        dtype, shape, rs = latent.dtype, latent.shape, rope.shape
+        dt = _TYPES.get(dtype)
+        if dt is None or rope.dtype is not dtype:
             raise ValueError(f"latent and rope must both be bfloat16 or float16, got {latent.dtype} and {rope.dtype}")
-        if latent.dim() != 3 or rope.dim() != 3 or rope.shape[:2] != latent.shape[:2] or latent.stride(2) != 1 or \
-                rope.stride(2) != 1:
+        ls, ss = latent.stride(), rope.stride()
+        if len(shape) != 3 or len(rs) != 3 or rs[:2] != shape[:2] or ls[2] != 1 or ss[2] != 1:
             raise ValueError("latent must be [n_pages, page_size, rank], rope [n_pages, page_size, rope_dim], with "
                              "contiguous last dimensions")
-        if not latent.is_cuda or rope.device != latent.device:
+        self.device = latent.device
+        if not latent.is_cuda or rope.device != self.device:
             raise ValueError("latent and rope must be CUDA tensors of one device")
         self.latent, self.rope = latent, rope
-        self.device = latent.device
-        self.rank, self.rope_dim = latent.shape[2], rope.shape[2]
-        self._need = {}  # workspace bytes by shapes
-        ls, rs = latent.stride(), rope.stride()
-        self._s = LatentPagesStruct(latent.data_ptr(), rope.data_ptr(), ls[0], ls[1], rs[0], rs[1], dt, latent.shape[0],
-                                    latent.shape[1], latent.shape[2], rope.shape[2], 0)
-        self._at = ctypes.addressof(self._s)
+        n, ps, self.rank = shape
+        self.rope_dim = rs[2]
+        # the mk_latent_pages of the calls
+        self._s = _PAGES.pack(latent.data_ptr(), rope.data_ptr(), ls[0], ls[1], ss[0], ss[1], dt, n, ps, self.rank,
+                              self.rope_dim, 0)
+        self._key = (self.device.index, ps, self.rank, dt, min(ls[0], ls[1], ss[0], ss[1]) > 0)
 
     def _table(self, table):
         s, shape = table.stride(), table.shape
@@ -110,7 +113,7 @@ class LatentPages:
     def _write(self, h, packed, pos, cnt, n, g, gdt, eps, turned, st):
         buf = _WriteBytes.from_buffer_copy(packed)
         at = ctypes.addressof(buf)
-        rc = lib().mk_latent_write(self._at, at, pos, cnt, n, at + 24, g, gdt, eps, at + 64 if turned else 0, st, h)
+        rc = lib().mk_latent_write(self._s, at, pos, cnt, n, at + 24, g, gdt, eps, at + 64 if turned else 0, st, h)
         if rc:
             _check(rc)
 
@@ -156,17 +159,17 @@ class LatentPages:
             buf = _AttendBytes()
             at = ctypes.addressof(buf)
             try:
-                _ATTEND.pack_into(buf, 0, self._at, at + 88, n, first, at + 112, at + 152, at + 192,
-                                  lse.data_ptr() if return_lse else 0, st, T, H, scale, 0, *t, *rq, *rr, *ro)
+                _ATTEND.pack_into(buf, 0, at + 232, at + 88, n, first, at + 112, at + 152, at + 192,
+                                  lse.data_ptr() if return_lse else 0, st, T, H, scale, 0, *t, *rq, *rr, *ro, self._s)
             except (struct.error, OverflowError) as e:
                 raise ValueError(f"scale must be a number in range: {e}") from None
             L = lib()
-            key = (B, T, H, t[3])  # the workspace's size depends on shapes alone
-            need = self._need.get(key)
+            key = (self._key, B, T, H, t[3])  # the workspace's size depends on shapes alone
+            need = _NEED.get(key)
             if need is None:
                 c = ctypes.c_int64()
                 _check(L.mk_latent_attend_workspace(at, _byref(c)))
-                need = self._need[key] = c.value
+                need = _NEED[key] = c.value
             w = torch.empty((need,), dtype=torch.uint8, device=dev) if need else None
             rc = L.mk_latent_attend(at, w.data_ptr() if need else 0, need, h)
             if rc:
