@@ -34,7 +34,6 @@
 // Pages of fewer than 8 positions, or overlapping ones (a stride of 0), have no
 // tensor map: a block a row takes them, a position a warp at a time.
 #include <climits>
-#include <mutex>
 #include <type_traits>
 
 #include "mk_tensor.cuh"
@@ -801,29 +800,18 @@ int map_of(const void* base, int width, const mk_latent_pages& g, int64_t page_s
 
 struct Plan {
     bool rows;  // a block a row
-    int nr, rows_blk, RB, grid;
+    int nr, rows_blk, RB, grid, dev;
     int64_t slots_off, bytes;
 };
 
 constexpr int MIN_UNITS = 4;  // positions a CTA takes at least: 4 tiles
 
 template <int MT, int NR, bool F16>
-int run(const LatentP* p, const mk_latent_pages* g, int grid, cudaStream_t s) {
+int run(const LatentP* p, const mk_latent_pages* g, int dev, int grid, cudaStream_t s) {
     using S = LatentShape<MT, NR>;
     auto kern = latent_kernel<MT, NR, F16>;
-    static std::mutex lock;
-    static bool have[32];
-    int dev = 0;
-    cudaError_t e = cudaGetDevice(&dev);
-    if (e != cudaSuccess) return cuda_status(e, "mk_latent_attend");
-    {
-        std::lock_guard<std::mutex> hold(lock);
-        if (dev >= 32 || !have[dev]) {
-            e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, S::SMEM);
-            if (e != cudaSuccess) return cuda_status(e, "mk_latent_attend");
-            if (dev < 32) have[dev] = true;
-        }
-    }
+    static std::atomic<uint64_t> done;
+    if (const int rc = allow_smem(kern, S::SMEM, dev, done, "mk_latent_attend")) return rc;
     LatentMaps maps;
     if (const int rc = map_of(g->latent, g->rank, *g, g->page_stride, g->row_stride, &maps.latent)) return rc;
     if (const int rc = map_of(g->rope, 64, *g, g->rope_page_stride, g->rope_row_stride, &maps.rope)) return rc;
@@ -868,10 +856,8 @@ int make_plan(const mk_latent_attention* a, Plan& pl) {
     pl = {};
     pl.rows = g.page_size < 8 || !g.page_stride || !g.row_stride || !g.rope_page_stride || !g.rope_row_stride;
     if (pl.rows) return MK_OK;
-    int dev = 0, sms = 0;
-    cudaError_t e = cudaGetDevice(&dev);
-    if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-    if (e != cudaSuccess) return cuda_status(e, "mk_latent_attend");
+    int sms;
+    if (const int rc = device_sms(pl.dev, sms, "mk_latent_attend")) return rc;
     const int rows = a->n_tokens * a->n_heads;
     pl.RB = (rows + 63) / 64;
     pl.rows_blk = (rows + pl.RB - 1) / pl.RB;
@@ -931,7 +917,7 @@ extern "C" int mk_latent_attend(const mk_latent_attention* a, void* workspace, i
     p.q_vec = rows_vec(a->q) && rows_vec(a->q_rope);
     auto go = [&](auto MT, auto NR) {
         constexpr int mt = decltype(MT)::value, nr = decltype(NR)::value;
-        return f16 ? run<mt, nr, true>(&p, &g, pl.grid, s) : run<mt, nr, false>(&p, &g, pl.grid, s);
+        return f16 ? run<mt, nr, true>(&p, &g, pl.dev, pl.grid, s) : run<mt, nr, false>(&p, &g, pl.dev, pl.grid, s);
     };
     using std::integral_constant;
     auto rank = [&](auto MT) {

@@ -18,7 +18,6 @@
 // Bound by HBM for batches (some 7 instructions a value), by latency for single
 // rows: a trip to memory, three votes, the cluster's meeting.
 #include <climits>
-#include <mutex>
 #include <type_traits>
 
 #include "mk_tensor.cuh"
@@ -420,22 +419,12 @@ __global__ void __launch_bounds__(GT, 2) logprob_kernel(const __grid_constant__ 
 }
 
 template <int DT>
-int run(const LogprobP& p, int rows, cudaStream_t s) {
+int run(const LogprobP& p, int rows, int dev, cudaStream_t s) {
     constexpr int SMEM = AHEAD * GT * BATCH * (DT == MK_DT_F32 ? 4 : 2);
-    static std::mutex lock;
-    static bool have[32];
-    int dev = 0;
-    cudaError_t e = cudaGetDevice(&dev);
-    if (e != cudaSuccess) return cuda_status(e, "mk_logprobs");
-    {
-        std::lock_guard<std::mutex> hold(lock);
-        if (dev >= 32 || !have[dev]) {
-            e = cudaFuncSetAttribute(logprob_kernel<DT, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM);
-            if (e == cudaSuccess) e = cudaFuncSetAttribute(logprob_kernel<DT, false>, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM);
-            if (e != cudaSuccess) return cuda_status(e, "mk_logprobs");
-            if (dev < 32) have[dev] = true;
-        }
-    }
+    static std::atomic<uint64_t> done[2];
+    if (const int rc = p.top ? allow_smem(logprob_kernel<DT, true>, SMEM, dev, done[1], "mk_logprobs")
+                             : allow_smem(logprob_kernel<DT, false>, SMEM, dev, done[0], "mk_logprobs"))
+        return rc;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(rows * p.split));
     cfg.blockDim = dim3(GT);
@@ -468,10 +457,8 @@ extern "C" int mk_logprobs(const mk_logprob* a, void* stream) {
         return fail(MK_ERR_INVALID_ARG, "logprobs: an argument is not aligned to 4 bytes");
     if (a->rows == 0) return MK_OK;
     if ((int64_t)a->rows * MAX_CLUSTER > INT32_MAX) return fail(MK_ERR_UNSUPPORTED, "logprobs: too many rows in one call");
-    int dev = 0, sms = 0;
-    cudaError_t err = cudaGetDevice(&dev);
-    if (err == cudaSuccess) err = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-    if (err != cudaSuccess) return cuda_status(err, "mk_logprobs");
+    int dev, sms;
+    if (const int rc = device_sms(dev, sms, "mk_logprobs")) return rc;
     LogprobP p = {};
     p.logits = (const uint8_t*)a->logits, p.row_s = a->row_stride, p.temperature = a->temperature, p.tokens = a->tokens;
     p.logprobs = a->logprobs, p.entropy = a->entropy, p.top_ids = a->top_ids, p.top_logprobs = a->top_logprobs;
@@ -480,6 +467,6 @@ extern "C" int mk_logprobs(const mk_logprob* a, void* stream) {
     p.split = 1;
     while (p.split < MAX_CLUSTER && (int64_t)a->rows * p.split < 2 * sms && a->vocab / p.split > GT * BATCH / 4) p.split *= 2;
     cudaStream_t s = (cudaStream_t)stream;
-    if (a->dtype == MK_DT_F32) return run<MK_DT_F32>(p, a->rows, s);
-    return a->dtype == MK_DT_BF16 ? run<MK_DT_BF16>(p, a->rows, s) : run<MK_DT_F16>(p, a->rows, s);
+    if (a->dtype == MK_DT_F32) return run<MK_DT_F32>(p, a->rows, dev, s);
+    return a->dtype == MK_DT_BF16 ? run<MK_DT_BF16>(p, a->rows, dev, s) : run<MK_DT_F16>(p, a->rows, dev, s);
 }

@@ -6,6 +6,7 @@
 #include <cuda_fp8.h>
 #include <cuda_runtime.h>
 
+#include <atomic>
 #include <cstdarg>
 #include <cstdint>
 #include <cstdio>
@@ -30,6 +31,25 @@ inline int fail(int code, const char* fmt, ...) {
 inline int cuda_status(cudaError_t e, const char* what) {
     if (e == cudaSuccess) return MK_OK;
     return fail(e == cudaErrorMemoryAllocation ? MK_ERR_OOM : MK_ERR_CUDA, "%s: %s", what, cudaGetErrorString(e));
+}
+// the current device and how many SMs it has, asked for once each
+inline int device_sms(int& dev, int& sms, const char* what) {
+    static std::atomic<int> known[64];
+    cudaError_t e = cudaGetDevice(&dev);
+    sms = e == cudaSuccess && dev < 64 ? known[dev].load(std::memory_order_relaxed) : 0;
+    if (e == cudaSuccess && !sms) {
+        e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+        if (e == cudaSuccess && dev < 64) known[dev].store(sms, std::memory_order_relaxed);
+    }
+    return cuda_status(e, what);
+}
+// Dynamic shared memory a kernel is allowed, set once on each device. `done`: a bit a device, one word a kernel.
+template <typename K>
+inline int allow_smem(K* kern, int bytes, int dev, std::atomic<uint64_t>& done, const char* what) {
+    if (dev < 64 && (done.load(std::memory_order_acquire) >> dev & 1)) return MK_OK;
+    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e == cudaSuccess && dev < 64) done.fetch_or(1ull << dev, std::memory_order_release);
+    return cuda_status(e, what);
 }
 inline int dtype_bytes(int dt) { return dt == MK_DT_F32 ? 4 : (dt == MK_DT_BF16 || dt == MK_DT_F16) ? 2 : 0; }
 inline int code_bytes(int format) { return format == MK_KV_BF16 ? 2 : 1; }

@@ -32,7 +32,6 @@
 // Longest CTAs first: blocks of a sequence in falling order, all heads of one
 // after another, so that short ones fill the end. All waits have a limit.
 #include <climits>
-#include <mutex>
 #include <type_traits>
 
 #include "mk_tensor.cuh"
@@ -516,19 +515,10 @@ int map_of(const void* base, int dtype, int width, int heads, int rows, int64_t 
 template <bool F16>
 int run(const PromptP& p, const PromptMaps& maps, int grid, cudaStream_t s) {
     auto kern = prompt_kernel<F16>;
-    static std::mutex lock;
-    static bool have[32];
-    int dev = 0;
-    cudaError_t e = cudaGetDevice(&dev);
-    if (e != cudaSuccess) return cuda_status(e, "mk_prompt_attend");
-    {
-        std::lock_guard<std::mutex> hold(lock);
-        if (dev >= 32 || !have[dev]) {
-            e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM);
-            if (e != cudaSuccess) return cuda_status(e, "mk_prompt_attend");
-            if (dev < 32) have[dev] = true;
-        }
-    }
+    static std::atomic<uint64_t> done;
+    int dev, sms;
+    if (const int rc = device_sms(dev, sms, "mk_prompt_attend")) return rc;
+    if (const int rc = allow_smem(kern, SMEM, dev, done, "mk_prompt_attend")) return rc;
     kern<<<grid, NT, SMEM, s>>>(p, maps);
     return cuda_status(cudaGetLastError(), "mk_prompt_attend");
 }

@@ -73,90 +73,98 @@ struct RotateP {
     uint8_t* out;
     long long xb, xt, xh, ob, ot, oh;  // elements
     float magnitude, sign;
-    int B, T, half, first, n, pairs;  // pairs: neighbours turn together
-    int turned, units, upt;           // of a head: units that turn, all of them; of a token
-    unsigned magic_h, magic_t;        // u / units and u / upt by the high word of a product
-    int toks, tokens;                 // of a block's turn, of the call
+    int T, H, half, first, n, pairs;  // pairs: neighbours turn together
+    int turned, units;                // of a head: units that turn, all of them
+    int heads, chunks;                // heads that one thread takes in turn, such parts of a token
+    long long items;                  // units of all parts of all tokens
 };
 
 constexpr int RT = 256;
 
-// A block's turn is some tokens: their cosines and sines once, in shared
-// memory, then units of 8 pairs (VEC; two 16-byte words in, two out) or of one
-// pair. Values of a head that do not turn are copied in units of 8 or one.
-// Bound by HBM for prompts (the angles are an n-th of a head's work for each of
-// the heads), by a launch and three trips to memory for single tokens.
+// A thread takes a unit (8 pairs: two 16-byte words in, two out; without VEC one pair) of a token through some of its heads:
+// its sines and cosines are computed once and stay in registers. Values of a head that do not turn are copied, 8 or one a
+// unit. A block's frequencies become turns once, in shared memory (64-bit arithmetic is slow here). Bound by HBM for
+// prompts, by a launch and two trips to memory for single tokens.
 template <int DT, bool VEC>
 __global__ void __launch_bounds__(RT) rotate_kernel(const __grid_constant__ RotateP p) {
-    extern __shared__ float2 cs[];  // [toks][half]
+    constexpr int E = VEC ? 8 : 1, HEADS = DT == MK_DT_F32 ? 2 : 4;  // pairs of a unit, heads in flight
     __shared__ unsigned long long turns[MAX_HALF];
     for (int i = threadIdx.x; i < p.half; i += RT) turns[i] = turns_of(p.freq[i]);
     __syncthreads();
-    constexpr int E = VEC ? 8 : 1;
-    for (int n0 = blockIdx.x * p.toks; n0 < p.tokens; n0 += gridDim.x * p.toks) {
-        const int toks = min(p.toks, p.tokens - n0);
-        for (int i = threadIdx.x; i < toks * p.half; i += RT) {
-            const int tok = i / p.half, j = i - tok * p.half;
-            const int b = (n0 + tok) / p.T, t = n0 + tok - b * p.T;
+    for (long long item = (long long)blockIdx.x * RT + threadIdx.x; item < p.items; item += (long long)gridDim.x * RT) {
+        const long long part = item / p.units;
+        const int c = (int)(item - part * p.units), tok = (int)(part / p.chunks), ch = (int)(part - (long long)tok * p.chunks);
+        const int b = tok / p.T, t = tok - b * p.T, h0 = ch * p.heads, h1 = min(p.H, h0 + p.heads);
+        const uint8_t* const x = p.x;
+        const long long xr = b * p.xb + t * p.xt, orow = b * p.ob + t * p.ot;
+        if (c < p.turned) {
             const long long at = p.position_s ? p.positions[b * p.position_s + t] : (long long)p.positions[b] + t;
-            cs[i] = turn(turns[j], at, p.magnitude, p.sign);
-        }
-        __syncthreads();
-        for (int u = threadIdx.x; u < toks * p.upt; u += RT) {
-            const int tok = toks > 1 ? (p.upt > 1 ? (int)__umulhi((unsigned)u, p.magic_t) : u) : 0;
-            const int r = u - tok * p.upt, h = p.units > 1 ? (int)__umulhi((unsigned)r, p.magic_h) : r;
-            const int c = r - h * p.units;
-            const int b = (n0 + tok) / p.T, t = n0 + tok - b * p.T;
-            const long long xr = b * p.xb + t * p.xt + h * p.xh, orow = b * p.ob + t * p.ot + h * p.oh;
-            if (c < p.turned) {
-                // values a .. and b .. : of a half layout the two halves' parts, else neighbours
-                const int ia = p.first + (p.pairs ? 2 * E * c : E * c), ib = p.pairs ? ia + E : ia + p.half;
-                const float2* const w = cs + tok * p.half + E * c;
-                if constexpr (VEC) {
-                    Values8<DT, true> va, vb;
-                    va.load(p.x, xr + ia);
-                    vb.load(p.x, xr + ib);
-                    float x[8], y[8];
-                    va.floats(x);
-                    vb.floats(y);
-                    if (p.pairs) {
+            float2 w[E];
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            const float2 f = w[i], g = w[4 + i];
-                            const float x0 = x[2 * i], x1 = x[2 * i + 1], y0 = y[2 * i], y1 = y[2 * i + 1];
-                            x[2 * i] = x0 * f.x - x1 * f.y, x[2 * i + 1] = x0 * f.y + x1 * f.x;
-                            y[2 * i] = y0 * g.x - y1 * g.y, y[2 * i + 1] = y0 * g.y + y1 * g.x;
-                        }
-                    } else {
+            for (int i = 0; i < E; ++i) w[i] = turn(turns[E * c + i], at, p.magnitude, p.sign);
+            // values from ia and ib on: of a half layout the two halves' parts, else neighbours
+            const int ia = p.first + (p.pairs ? 2 * E * c : E * c), ib = p.pairs ? ia + E : ia + p.half;
+            if constexpr (VEC) {
+                for (int h = h0; h < h1; h += HEADS) {
+                    Values8<DT, true> va[HEADS], vb[HEADS];
 #pragma unroll
-                        for (int i = 0; i < 8; ++i) {
-                            const float2 f = w[i];
-                            const float a = x[i], e = y[i];
-                            x[i] = a * f.x - e * f.y, y[i] = a * f.y + e * f.x;
+                    for (int k = 0; k < HEADS; ++k)
+                        if (h + k < h1) {
+                            va[k].load(x, xr + (h + k) * p.xh + ia);
+                            vb[k].load(x, xr + (h + k) * p.xh + ib);
                         }
+#pragma unroll
+                    for (int k = 0; k < HEADS; ++k) {
+                        if (h + k >= h1) break;
+                        float a[8], e[8];
+                        va[k].floats(a);
+                        vb[k].floats(e);
+                        if (p.pairs) {
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) {
+                                const float a0 = a[2 * i], a1 = a[2 * i + 1], e0 = e[2 * i], e1 = e[2 * i + 1];
+                                a[2 * i] = a0 * w[i].x - a1 * w[i].y, a[2 * i + 1] = a0 * w[i].y + a1 * w[i].x;
+                                e[2 * i] = e0 * w[4 + i].x - e1 * w[4 + i].y, e[2 * i + 1] = e0 * w[4 + i].y + e1 * w[4 + i].x;
+                            }
+                        } else {
+#pragma unroll
+                            for (int i = 0; i < 8; ++i) {
+                                const float a0 = a[i], e0 = e[i];
+                                a[i] = a0 * w[i].x - e0 * w[i].y, e[i] = a0 * w[i].y + e0 * w[i].x;
+                            }
+                        }
+                        store8<DT, true>(p.out, orow + (h + k) * p.oh + ia, a);
+                        store8<DT, true>(p.out, orow + (h + k) * p.oh + ib, e);
                     }
-                    store8<DT, true>(p.out, orow + ia, x);
-                    store8<DT, true>(p.out, orow + ib, y);
-                } else {
-                    const float a = load1<DT>(p.x, xr + ia), e = load1<DT>(p.x, xr + ib);
-                    store1<DT>(p.out, orow + ia, a * w->x - e * w->y);
-                    store1<DT>(p.out, orow + ib, a * w->y + e * w->x);
                 }
             } else {
-                int i = (c - p.turned) * E;
-                if (i >= p.first) i += p.n;
-                if constexpr (VEC) {
-                    Values8<DT, true> v;
-                    v.load(p.x, xr + i);
-                    float x[8];
-                    v.floats(x);
-                    store8<DT, true>(p.out, orow + i, x);
-                } else {
-                    store1<DT>(p.out, orow + i, load1<DT>(p.x, xr + i));
+                for (int h = h0; h < h1; ++h) {
+                    const float a = load1<DT>(x, xr + h * p.xh + ia), e = load1<DT>(x, xr + h * p.xh + ib);
+                    store1<DT>(p.out, orow + h * p.oh + ia, a * w[0].x - e * w[0].y);
+                    store1<DT>(p.out, orow + h * p.oh + ib, a * w[0].y + e * w[0].x);
                 }
             }
+        } else {
+            int i = (c - p.turned) * E;
+            if (i >= p.first) i += p.n;
+            if constexpr (VEC) {
+                for (int h = h0; h < h1; h += 2 * HEADS) {
+                    Values8<DT, true> v[2 * HEADS];
+#pragma unroll
+                    for (int k = 0; k < 2 * HEADS; ++k)
+                        if (h + k < h1) v[k].load(x, xr + (h + k) * p.xh + i);
+#pragma unroll
+                    for (int k = 0; k < 2 * HEADS; ++k) {
+                        if (h + k >= h1) break;
+                        float y[8];
+                        v[k].floats(y);
+                        store8<DT, true>(p.out, orow + (h + k) * p.oh + i, y);
+                    }
+                }
+            } else {
+                for (int h = h0; h < h1; ++h) store1<DT>(p.out, orow + h * p.oh + i, load1<DT>(x, xr + h * p.xh + i));
+            }
         }
-        __syncthreads();
     }
 }
 
@@ -169,18 +177,10 @@ int check_rotary(const mk_rotary* r, const char* what) {
     return MK_OK;
 }
 
-int sm_count(int& sms, const char* what) {
-    int dev = 0;
-    cudaError_t e = cudaGetDevice(&dev);
-    if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-    return cuda_status(e, what);
-}
-
 template <int DT>
 void rotate_go(const RotateP& p, bool vec, int grid, cudaStream_t s) {
-    const size_t smem = sizeof(float2) * p.toks * p.half;
-    if (vec) rotate_kernel<DT, true><<<grid, RT, smem, s>>>(p);
-    else rotate_kernel<DT, false><<<grid, RT, smem, s>>>(p);
+    if (vec) rotate_kernel<DT, true><<<grid, RT, 0, s>>>(p);
+    else rotate_kernel<DT, false><<<grid, RT, 0, s>>>(p);
 }
 
 // ---------------------------------------------------------------- mk_latent_write
@@ -207,96 +207,113 @@ __device__ __forceinline__ float gain_at(const LatentWriteP& p, int i) {
     return p.gain_dt == MK_DT_BF16 ? load1<MK_DT_BF16>(p.gain, i) : load1<MK_DT_F16>(p.gain, i);
 }
 
-// A warp a row: V pieces of 8 latent values a lane, their squares summed by
-// shuffles; a pair of the rope part a lane. A warp's gains and frequencies are
-// loaded once for all its rows. Bound by HBM for prompts.
-template <int DT, bool VEC, int V>
-__global__ void __launch_bounds__(WT) latent_write_kernel(const __grid_constant__ LatentWriteP p) {
-    const int lane = threadIdx.x & 31, warps = gridDim.x * (WT / 32);
+// A warp a row, two rows in flight: V pieces of 8 latent values a lane, their squares summed by shuffles; a pair of the rope
+// part a lane. Gains and frequencies are loaded once for all of a block's rows. Bound by HBM for prompts.
+template <int DT, bool VEC, int V, int RP>
+__global__ void __launch_bounds__(WT, V <= 2 && RP == 1 ? 8 : 4) latent_write_kernel(const __grid_constant__ LatentWriteP p) {
+    constexpr int R = V <= 2 ? 2 : 1;  // rows in flight; RP: pairs of a lane at most
+    const int lane = threadIdx.x & 31, warps = gridDim.x * (WT / 32), half = p.rope_dim / 2;
     const long long total = (long long)p.B * p.n;
-    float gain[V][8];
-    unsigned long long turns[4];
+    // gains lie in shared memory by lanes: value e of piece v of lane l at (v 8 + e) 32 + l
+    __shared__ float gain[V * 256];
+    unsigned long long turns[RP];
     if (p.gain) {
-#pragma unroll
-        for (int v = 0; v < V; ++v) {
-            const int i = 8 * (v * 32 + lane);
-            if (i < p.rank) {
-#pragma unroll
-                for (int e = 0; e < 8; ++e) gain[v][e] = gain_at(p, i + e);
-            }
-        }
+        for (int i = threadIdx.x; i < p.rank; i += WT) gain[(i >> 8) * 256 + (i & 7) * 32 + (i >> 3 & 31)] = gain_at(p, i);
+        __syncthreads();
     }
     if (p.freq) {
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
-            if (j * 32 + lane < p.rope_dim / 2) turns[j] = turns_of(p.freq[j * 32 + lane]);
+        for (int j = 0; j < RP; ++j)
+            if (j * 32 + lane < half) turns[j] = turns_of(p.freq[j * 32 + lane]);
     }
-    for (long long row = (long long)blockIdx.x * (WT / 32) + (threadIdx.x >> 5); row < total; row += warps) {
-        const int b = (int)(row / p.n), t = (int)(row - (long long)b * p.n);
-        if (p.counts && t >= p.counts[b]) continue;
-        const long long src = b * p.rb + t * p.rt;
-        Values8<DT, VEC> x[V];
+    auto pair_of = [&](int j, int& ia, int& ib) {
+        const int i = j * 32 + lane;
+        ia = p.pairs ? 2 * i : i, ib = p.pairs ? ia + 1 : i + half;
+        return i < half;
+    };
+    for (long long row0 = (long long)blockIdx.x * (WT / 32) + (threadIdx.x >> 5); row0 < total; row0 += (long long)warps * R) {
+        Values8<DT, VEC> x[R][V];
+        float ra[R], rb[R];  // the first pair of the rope part
+        long long src[R], pos[R];
+        int page[R];         // -1: no row, -2: out of range
 #pragma unroll
-        for (int v = 0; v < V; ++v) {
-            const int i = 8 * (v * 32 + lane);
-            if (i < p.rank) x[v].load(p.rows, src + i);
-            else x[v].zero();
-        }
-        const long long pos = (long long)p.positions[b] + t, col = pos >> p.ps_shift;
-        const int page = pos >= 0 && col < p.pps ? p.table[b * p.table_s + col] : -1;
-        if ((unsigned)page >= (unsigned)p.n_pages) {
-            if (p.status) *p.status = MK_ERR_INVALID_ARG;
-            continue;
-        }
-        const int r = (int)(pos & ((1 << p.ps_shift) - 1));
-        float f = 1.f;
-        if (p.gain) {
-            float sum = 0.f;
+        for (int k = 0; k < R; ++k) {
+            const long long row = row0 + (long long)k * warps;
+            page[k] = -1;
+            if (row >= total) continue;
+            const int b = (int)((unsigned)row / (unsigned)p.n), t = (int)((unsigned)row - (unsigned)b * (unsigned)p.n);
+            if (p.counts && t >= p.counts[b]) continue;
+            src[k] = b * p.rb + t * p.rt;
+            pos[k] = (long long)p.positions[b] + t;
 #pragma unroll
             for (int v = 0; v < V; ++v) {
-                float y[8];
-                x[v].floats(y);
-#pragma unroll
-                for (int e = 0; e < 8; ++e) sum += y[e] * y[e];
+                const int i = 8 * (v * 32 + lane);
+                if (i < p.rank) x[k][v].load(p.rows, src[k] + i);
+                else x[k][v].zero();
             }
-#pragma unroll
-            for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-            f = rsqrtf(sum / (float)p.rank + p.eps);
+            int ia, ib;
+            if (pair_of(0, ia, ib)) {
+                ra[k] = load1<DT>(p.rows, src[k] + p.rank + ia);
+                rb[k] = load1<DT>(p.rows, src[k] + p.rank + ib);
+            }
+            const long long col = pos[k] >> p.ps_shift;
+            page[k] = pos[k] >= 0 && col < p.pps ? p.table[b * p.table_s + col] : -2;
+            if ((unsigned)page[k] >= (unsigned)p.n_pages) page[k] = -2;
         }
-        const long long to = page * p.page_s + r * p.row_s;
 #pragma unroll
-        for (int v = 0; v < V; ++v) {
-            const int i = 8 * (v * 32 + lane);
-            if (i >= p.rank) continue;
-            float y[8];
-            x[v].floats(y);
+        for (int k = 0; k < R; ++k) {
+            if (page[k] < 0) {
+                if (page[k] == -2 && p.status) *p.status = MK_ERR_INVALID_ARG;
+                continue;
+            }
+            const int r = (int)(pos[k] & ((1 << p.ps_shift) - 1));
+            float f = 1.f;
             if (p.gain) {
+                float sum = 0.f;
 #pragma unroll
-                for (int e = 0; e < 8; ++e) y[e] = y[e] * f * gain[v][e];
-            }
-            if (p.f16) store8<MK_DT_F16, true>(p.latent, to + i, y);
-            else store8<MK_DT_BF16, true>(p.latent, to + i, y);
-        }
-        const long long rto = page * p.rope_page_s + r * p.rope_row_s;
-        const int half = p.rope_dim / 2;
+                for (int v = 0; v < V; ++v) {
+                    float y[8];
+                    x[k][v].floats(y);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const int i = j * 32 + lane;
-            if (i >= half) break;
-            const int ia = p.pairs ? 2 * i : i, ib = p.pairs ? ia + 1 : i + half;
-            float a = load1<DT>(p.rows, src + p.rank + ia), e = load1<DT>(p.rows, src + p.rank + ib);
-            if (p.freq) {
-                const float2 w = turn(turns[j], pos, p.magnitude, p.sign);
-                const float y = a * w.x - e * w.y;
-                e = a * w.y + e * w.x;
-                a = y;
+                    for (int e = 0; e < 8; ++e) sum += y[e] * y[e];
+                }
+#pragma unroll
+                for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+                f = rsqrtf(sum / (float)p.rank + p.eps);
             }
-            if (p.f16) {
-                store1<MK_DT_F16>(p.rope, rto + ia, a);
-                store1<MK_DT_F16>(p.rope, rto + ib, e);
-            } else {
-                store1<MK_DT_BF16>(p.rope, rto + ia, a);
-                store1<MK_DT_BF16>(p.rope, rto + ib, e);
+            const long long to = page[k] * p.page_s + r * p.row_s;
+#pragma unroll
+            for (int v = 0; v < V; ++v) {
+                const int i = 8 * (v * 32 + lane);
+                if (i >= p.rank) continue;
+                float y[8];
+                x[k][v].floats(y);
+                if (p.gain) {
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) y[e] = y[e] * f * gain[(v * 8 + e) * 32 + lane];
+                }
+                if (p.f16) store8<MK_DT_F16, true>(p.latent, to + i, y);
+                else store8<MK_DT_BF16, true>(p.latent, to + i, y);
+            }
+            const long long rto = page[k] * p.rope_page_s + r * p.rope_row_s;
+#pragma unroll
+            for (int j = 0; j < RP; ++j) {
+                int ia, ib;
+                if (!pair_of(j, ia, ib)) break;
+                float a = j ? load1<DT>(p.rows, src[k] + p.rank + ia) : ra[k], e = j ? load1<DT>(p.rows, src[k] + p.rank + ib) : rb[k];
+                if (p.freq) {
+                    const float2 w = turn(turns[j], pos[k], p.magnitude, p.sign);
+                    const float y = a * w.x - e * w.y;
+                    e = a * w.y + e * w.x;
+                    a = y;
+                }
+                if (p.f16) {
+                    store1<MK_DT_F16>(p.rope, rto + ia, a);
+                    store1<MK_DT_F16>(p.rope, rto + ib, e);
+                } else {
+                    store1<MK_DT_BF16>(p.rope, rto + ia, a);
+                    store1<MK_DT_BF16>(p.rope, rto + ib, e);
+                }
             }
         }
     }
@@ -304,9 +321,14 @@ __global__ void __launch_bounds__(WT) latent_write_kernel(const __grid_constant_
 
 template <int DT, bool VEC>
 void write_go(const LatentWriteP& p, int grid, cudaStream_t s) {
-    if (p.rank <= 256) latent_write_kernel<DT, VEC, 1><<<grid, WT, 0, s>>>(p);
-    else if (p.rank <= 512) latent_write_kernel<DT, VEC, 2><<<grid, WT, 0, s>>>(p);
-    else latent_write_kernel<DT, VEC, 4><<<grid, WT, 0, s>>>(p);
+    const bool one = p.rope_dim <= 64;
+    if (p.rank <= 512) {
+        if (one) latent_write_kernel<DT, VEC, 2, 1><<<grid, WT, 0, s>>>(p);
+        else latent_write_kernel<DT, VEC, 2, 4><<<grid, WT, 0, s>>>(p);
+    } else {
+        if (one) latent_write_kernel<DT, VEC, 4, 1><<<grid, WT, 0, s>>>(p);
+        else latent_write_kernel<DT, VEC, 4, 4><<<grid, WT, 0, s>>>(p);
+    }
 }
 
 }  // namespace
@@ -332,7 +354,7 @@ extern "C" int mk_rotate(const mk_rotation* a, void* stream) {
     p.x = (const uint8_t*)x.data, p.xb = x.seq_stride, p.xt = x.token_stride, p.xh = x.head_stride;
     p.out = (uint8_t*)o.data, p.ob = o.seq_stride, p.ot = o.token_stride, p.oh = o.head_stride;
     p.magnitude = r.magnitude, p.sign = r.inverse ? -1.f : 1.f;
-    p.B = a->batch, p.T = a->n_tokens, p.half = r.n / 2, p.first = a->first, p.n = r.n;
+    p.T = a->n_tokens, p.H = a->n_heads, p.half = r.n / 2, p.first = a->first, p.n = r.n;
     p.pairs = r.layout == MK_ROTARY_PAIRS;
     const bool in_place = x.data == o.data && x.seq_stride == o.seq_stride && x.token_stride == o.token_stride &&
                           x.head_stride == o.head_stride;
@@ -340,21 +362,17 @@ extern "C" int mk_rotate(const mk_rotation* a, void* stream) {
     const int e = vec ? 8 : 1;
     p.turned = p.half / e;
     p.units = p.turned + (in_place ? 0 : (a->head_dim - r.n) / e);
-    p.upt = a->n_heads * p.units;
-    p.tokens = a->batch * a->n_tokens;
-    int sms = 0;
-    if (const int rc = sm_count(sms, "mk_rotate")) return rc;
-    // a block's turn: four units a thread, as long as every SM has a block, and its angles fit 16 KB
-    int toks = 4 * RT / p.upt, most = 2048 / p.half, spread = (p.tokens + sms - 1) / sms;
-    toks = toks < most ? toks : most;
-    toks = toks < spread ? toks : spread;
-    p.toks = toks < 1 ? 1 : toks;
-    // exact for units of a token (some below 2^28) only where the product with the divisor stays below 2^32
-    if ((int64_t)p.toks * p.upt * (int64_t)p.upt >= (1ll << 32) && p.toks > 1) p.toks = 1;
-    if ((int64_t)p.upt * p.units >= (1ll << 32)) return fail(MK_ERR_UNSUPPORTED, "rotate: heads too many or too wide");
-    p.magic_h = (unsigned)(0x100000000ull / p.units + 1);
-    p.magic_t = (unsigned)(0x100000000ull / p.upt + 1);
-    const int turns = (p.tokens + p.toks - 1) / p.toks, grid = turns < 8 * sms ? turns : 8 * sms;
+    int dev, sms;
+    if (const int rc = device_sms(dev, sms, "mk_rotate")) return rc;
+    // as many heads a thread (whose angles they share) as leave the device 1024 threads an SM
+    const int64_t tokens = (int64_t)a->batch * a->n_tokens, all = tokens * p.units;
+    p.chunks = (int)(1024ll * sms / all);
+    if (p.chunks < 1) p.chunks = 1;
+    p.heads = (p.H + p.chunks - 1) / p.chunks;
+    p.chunks = (p.H + p.heads - 1) / p.heads;
+    p.items = all * p.chunks;
+    const int64_t want = (p.items + RT - 1) / RT;
+    const int grid = (int)(want < 8 * sms ? want : 8 * sms);
     cudaStream_t s = (cudaStream_t)stream;
     if (x.dtype == MK_DT_F32) rotate_go<MK_DT_F32>(p, vec, grid, s);
     else if (x.dtype == MK_DT_BF16) rotate_go<MK_DT_BF16>(p, vec, grid, s);
@@ -381,6 +399,7 @@ extern "C" int mk_latent_write(const mk_latent_pages* g, const mk_page_table* t,
         if (rotary->n != g->rope_dim) return fail(MK_ERR_INVALID_ARG, "latent: rotary n %d, rope_dim %d", rotary->n, g->rope_dim);
     }
     if (n == 0) return MK_OK;
+    if ((int64_t)t->batch * n > INT32_MAX) return fail(MK_ERR_UNSUPPORTED, "latent: too many rows in one call");
     LatentWriteP p = {};
     p.latent = (uint8_t*)g->latent, p.rope = (uint8_t*)g->rope;
     p.page_s = g->page_stride, p.row_s = g->row_stride, p.rope_page_s = g->rope_page_stride, p.rope_row_s = g->rope_row_stride;
@@ -393,12 +412,12 @@ extern "C" int mk_latent_write(const mk_latent_pages* g, const mk_page_table* t,
     p.pairs = rotary && rotary->layout == MK_ROTARY_PAIRS;
     p.ps_shift = log2_exact(g->page_size), p.n_pages = g->n_pages, p.rank = g->rank, p.rope_dim = g->rope_dim;
     p.B = t->batch, p.n = n, p.f16 = g->dtype == MK_DT_F16, p.status = status;
-    int sms = 0;
-    if (const int rc = sm_count(sms, "mk_latent_write")) return rc;
+    int dev, sms;
+    if (const int rc = device_sms(dev, sms, "mk_latent_write")) return rc;
     const int unit = rows->dtype == MK_DT_F32 ? 4 : 8;
     const bool vec = (uintptr_t)rows->data % 16 == 0 && rows->seq_stride % unit == 0 && rows->token_stride % unit == 0;
     const int64_t want = ((int64_t)t->batch * n + WT / 32 - 1) / (WT / 32);
-    const int grid = (int)(want < 16 * sms ? want : 16 * sms);
+    const int grid = (int)(want < 8 * sms ? want : 8 * sms);
     cudaStream_t s = (cudaStream_t)stream;
     auto go = [&](auto f, auto slow) { vec ? f(p, grid, s) : slow(p, grid, s); };
     if (rows->dtype == MK_DT_F32) go(write_go<MK_DT_F32, true>, write_go<MK_DT_F32, false>);
