@@ -7,8 +7,8 @@
 // and at the end log p_i = z_i - log s, entropy = log s - t / s.
 //
 // The most probable tokens come out of the same pass. Tokens are ordered by one
-// 64-bit key (logit, then the lower id). A round is 16 values a thread; before a
-// CTA has a threshold, the largest keys of 128 groups of four threads give one
+// 64-bit key (logit, then the lower id). A round is 64 bytes a thread; before a
+// CTA has a threshold, the largest keys of groups of threads give one
 // (the k-th largest of them is no more than the k-th largest of all), after that
 // a round whose values all lie below it costs one vote. What lies above goes to
 // a list, whose first k are found by counting, for each, how many are larger.
@@ -29,12 +29,12 @@ using namespace mkop;
 typedef unsigned long long u64;
 
 constexpr int MAX_TOP = 64;
-constexpr int GT = 512, BATCH = 16;       // threads, values of a thread's round
-constexpr int GROUPS = GT / 4;            // of four threads; up to k = 32 half as many, of eight
+constexpr int GT = 512, U = 4;            // threads, 16-byte words of a thread's round
+constexpr int GROUPS = GT / 2;            // of two threads; up to k = 32 half as many, of four
 // the list: what may be left of it, and what a round may add (the values of k groups)
-constexpr int SLACK = 8, CAP = MAX_TOP + SLACK + MAX_TOP * 4 * BATCH;
+constexpr int SLACK = 8, CAP = MAX_TOP + SLACK + MAX_TOP * 2 * U * 8;
 constexpr int MAX_CLUSTER = 8;
-constexpr int AHEAD = 4;  // rounds in flight
+constexpr int AHEAD = 2;  // rounds in flight
 
 struct LogprobP {
     const uint8_t* logits;
@@ -161,10 +161,9 @@ __device__ int first_keys(LogprobShared& sh, int n, int k) {
             top = max(top, mine[i]);
         }
         top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
-        top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
-        if ((tid & 3) == 0) sh.group[tid >> 2] = top;
+        if ((tid & 1) == 0) sh.group[tid >> 1] = top;
         __syncthreads();
-        ranks<4>(sh.group, GROUPS, [&](u64 x, int rank) {
+        ranks<8>(sh.group, GROUPS, [&](u64 x, int rank) {
             if (rank == k - 1) sh.limit = x;
         });
         if (tid == 0) sh.n = 0;
@@ -213,7 +212,7 @@ __device__ __forceinline__ void put_remote(float4* p, int cta, float4 v) {
 
 template <int DT, bool TOP>
 __global__ void __launch_bounds__(GT, 2) logprob_kernel(const __grid_constant__ LogprobP p) {
-    constexpr int VEC = DT == MK_DT_F32 ? 4 : 8, U = BATCH / VEC;  // values of 16 bytes, words of a round
+    constexpr int VEC = DT == MK_DT_F32 ? 4 : 8;  // values of 16 bytes
     __shared__ LogprobShared sh;
     extern __shared__ __align__(16) uint8_t ring[];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, split = p.split;
@@ -264,24 +263,26 @@ __global__ void __launch_bounds__(GT, 2) logprob_kernel(const __grid_constant__ 
             });
             u64 best = in ? key_of(top, first) : 0;
             best = max(best, __shfl_xor_sync(0xffffffffu, best, 1));
-            best = max(best, __shfl_xor_sync(0xffffffffu, best, 2));
-            if (k <= 32) best = max(best, __shfl_xor_sync(0xffffffffu, best, 4));
-            const int by = k <= 32 ? 3 : 2;
+            if (k <= 32) best = max(best, __shfl_xor_sync(0xffffffffu, best, 2));
+            const int by = k <= 32 ? 2 : 1;
             if ((lane & ((1 << by) - 1)) == 0) sh.group[tid >> by] = best;
             if (tid == 0) sh.limit = 0;
             __syncthreads();
             auto found = [&](u64 x, int rank) {
                 if (rank == k - 1) sh.limit = x;
             };
-            if (k <= 32) ranks<2>(sh.group, GROUPS / 2, found);
-            else ranks<4>(sh.group, GROUPS, found);
+            if (k <= 32) ranks<4>(sh.group, GROUPS / 2, found);
+            else ranks<8>(sh.group, GROUPS, found);
             __syncthreads();
             limit = max(limit, sh.limit);  // (keys from it on)
         }
-        if (in && (!limit || top >= logit_of(limit)))
+        const float least = limit ? logit_of(limit) : -INFINITY;
+        if (in && top >= least)
             each([&](float x, int id) {
-                const u64 y = key_of(x, id);
-                if (y >= limit) sh.list[atomicAdd(&sh.n, 1)] = y;
+                if (x >= least) {
+                    const u64 y = key_of(x, id);
+                    if (y >= limit) sh.list[atomicAdd(&sh.n, 1)] = y;
+                }
             });
         __syncthreads();
         n = sh.n;
@@ -420,7 +421,7 @@ __global__ void __launch_bounds__(GT, 2) logprob_kernel(const __grid_constant__ 
 
 template <int DT>
 int run(const LogprobP& p, int rows, int dev, cudaStream_t s) {
-    constexpr int SMEM = AHEAD * GT * BATCH * (DT == MK_DT_F32 ? 4 : 2);
+    constexpr int SMEM = AHEAD * GT * U * 16;
     static std::atomic<uint64_t> done[2];
     if (const int rc = p.top ? allow_smem(logprob_kernel<DT, true>, SMEM, dev, done[1], "mk_logprobs")
                              : allow_smem(logprob_kernel<DT, false>, SMEM, dev, done[0], "mk_logprobs"))
@@ -463,9 +464,10 @@ extern "C" int mk_logprobs(const mk_logprob* a, void* stream) {
     p.logits = (const uint8_t*)a->logits, p.row_s = a->row_stride, p.temperature = a->temperature, p.tokens = a->tokens;
     p.logprobs = a->logprobs, p.entropy = a->entropy, p.top_ids = a->top_ids, p.top_logprobs = a->top_logprobs;
     p.V = a->vocab, p.given = a->given, p.top = a->top;
-    // CTAs of a row: two or more an SM, as long as each has a part of a round
+    // CTAs of a row: one or more an SM, as long as each has a part of a round (a CTA's first threshold and its end cost as
+    // much as two rounds: 256 rows of 151936 bf16 logits take 45 us in one part each, 57 in two)
     p.split = 1;
-    while (p.split < MAX_CLUSTER && (int64_t)a->rows * p.split < 2 * sms && a->vocab / p.split > GT * BATCH / 4) p.split *= 2;
+    while (p.split < MAX_CLUSTER && (int64_t)a->rows * p.split < sms && a->vocab / p.split > GT * 4) p.split *= 2;
     cudaStream_t s = (cudaStream_t)stream;
     if (a->dtype == MK_DT_F32) return run<MK_DT_F32>(p, a->rows, dev, s);
     return a->dtype == MK_DT_BF16 ? run<MK_DT_BF16>(p, a->rows, dev, s) : run<MK_DT_F16>(p, a->rows, dev, s);
