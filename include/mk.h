@@ -268,8 +268,9 @@ int mk_decode_step_noalloc(mk_model* m, mk_kv* kv, const int32_t* tokens, const 
  *                 guard before checking them and reports MK_ERR_STATE;
  *   "skip_attend_signal" the launch of mk_pages_attend that reads a shared
  *                 prefix (or the whole tiles of many rows) on the tensor
- *                 memory leaves out one of its roles' signals: another waits
- *                 until the wait limit, and `status` gets MK_ERR_TIMEOUT.
+ *                 memory, mk_latent_attend and mk_prompt_attend leave out one
+ *                 of their roles' signals: another waits until the wait
+ *                 limit, and `status` gets MK_ERR_TIMEOUT.
  * Each host failure sets mk_last_error() to a message naming MK_FAULT.
  *
  * Debug mode: with MK_DEBUG=1 when the model is loaded, every CTA writes a

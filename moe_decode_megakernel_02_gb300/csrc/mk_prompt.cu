@@ -420,7 +420,7 @@ __global__ void __launch_bounds__(NT, 1)
                             mma_ss(ts, desc_on(qd, c * PANEL_B + k * 32), desc_on(kd, at.i * PANEL_B + k * 32), QK, c > 0 || k > 0);
                         mma_commit(&ms.k_free[at.i]);
                     }
-                    mma_commit(&ms.s_full[g]);
+                    if (!p.skip_signal) mma_commit(&ms.s_full[g]);
                 } else {
                     bar_arrive(&ms.turn[g ^ 1]);
                     for (int c = 0; c < PANELS; ++c, at.next()) bar_arrive(&ms.k_free[at.i]);
@@ -438,7 +438,7 @@ __global__ void __launch_bounds__(NT, 1)
                     for (int k = 0; k < 4; ++k)
                         mma_ts(to, ts + (4 * c + k) * 8, desc_on(vd, vs.i * VHALF_B + k * 2048), PV, j > 0 || c > 0 || k > 0);
                     mma_commit(&ms.v_free[vs.i]);
-                    if (c == 1 && !p.skip_signal) mma_commit(&ms.o_done[g]);
+                    if (c == 1) mma_commit(&ms.o_done[g]);
                 } else {
                     bar_arrive(&ms.v_free[vs.i]);
                 }

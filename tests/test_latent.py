@@ -43,8 +43,9 @@ def queries(dtype, B, T, H, rank=512, rope=64, seed=1):
     return tuple(torch.randn((B, T, H, w), generator=g, device="cuda").to(dtype) for w in (rank, rope))
 
 
-def check_attend(cache, table, lens, q, qr, scale, starts=None, **kw):
-    out, lse = cache.attend(table, lens, q, qr, scale, starts=starts, return_lse=True, **kw)
+def check_attend(cache, table, lens, q, qr, scale, starts=None, given=None, **kw):
+    """A call (or what one gave) against the definition."""
+    out, lse = given or cache.attend(table, lens, q, qr, scale, starts=starts, return_lse=True, **kw)
     B, T, H, R = q.shape
     ps = cache.latent.shape[1]
     dtype = q.dtype
