@@ -29,6 +29,9 @@
 // so do values that are not finite and that only some rows see, and rows that
 // do see them get NaN.
 //
+// A few blocks with long contexts share each block's tiles out to a cluster of 2 to
+// 8 CTAs, whose outputs, maxima and sums meet through distributed shared memory.
+//
 // Longest CTAs first: blocks of a sequence in falling order, all heads of one
 // after another, so that short ones fill the end. All waits have a limit.
 #include <climits>
@@ -61,8 +64,10 @@ struct PromptMisc {
     unsigned tmem, abort;
     int scan[NT / 32], seq, pair, bad;
 };
-constexpr int SMEM = 1024 + MISC_OFF + 1024;
-static_assert(sizeof(PromptMisc) <= 1024 && SMEM <= 227 * 1024, "");
+constexpr int MISC_B = 1024, SMEM = 1024 + MISC_OFF + MISC_B;
+// A row among the CTAs of a block: its output, maximum and sum, floats.
+constexpr int OUT_ROW = VD + 4;
+static_assert(PAIR * OUT_ROW * 4 <= MISC_OFF && sizeof(PromptMisc) <= MISC_B && SMEM <= 227 * 1024, "");
 
 struct PromptP {
     const int *q_starts, *k_starts;
@@ -73,6 +78,7 @@ struct PromptP {
     int B, n_q, n_k, H;
     int q_heads, k_heads, v_heads;  // 0: all heads are one (a stride of 0)
     float scale;
+    int split;                  // CTAs of a block, a cluster: each takes a part of its tiles
     unsigned wait_ns;
     int skip_signal;            // for tests
 };
@@ -89,6 +95,10 @@ __device__ __forceinline__ void tma_2d(uint32_t dst, const CUtensorMap* map, int
 template <bool F16>
 __device__ __forceinline__ uint32_t pack16(float lo, float hi) {
     return F16 ? pack_f16(lo, hi) : pack_bf16(lo, hi);
+}
+// all CTAs of the cluster, their shared memory with them
+__device__ __forceinline__ void cluster_meet() {
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 // a ring slot and its turn
 template <int N>
@@ -118,7 +128,8 @@ __global__ void __launch_bounds__(NT, 1)
     const Limit limit = {&ms.abort, p.wait_ns};
 
     // the CTA's block: each thread counts a stretch of sequences; sums before it by shuffles
-    const int h = blockIdx.x % p.H, u = blockIdx.x / p.H;
+    const int block = blockIdx.x / p.split, part = blockIdx.x - block * p.split;
+    const int h = block % p.H, u = block / p.H;
     const int each = (p.B + NT - 1) / NT, b0 = min(p.B, tid * each), b1 = min(p.B, b0 + each);
     int mine = 0;
     for (int b = b0; b < b1; ++b) {
@@ -183,7 +194,11 @@ __global__ void __launch_bounds__(NT, 1)
         const int first = i0 + g * ROWS, last = min(first + ROWS, n) - 1;
         return first < n && behind + last >= 0 ? (behind + last) / TILE + 1 : 0;
     };
-    const int nt0 = tiles_of(0), nt1 = tiles_of(1), nt = max(nt0, nt1);
+    // of them this CTA's: from tile `from` on, counted from there
+    const int all0 = tiles_of(0), all1 = tiles_of(1), most = max(all0, all1);
+    const int from = (int)((long long)most * part / p.split), to_tile = (int)((long long)most * (part + 1) / p.split);
+    const int nt0 = max(0, min(all0, to_tile) - from), nt1 = max(0, min(all1, to_tile) - from), nt = max(nt0, nt1);
+    float row_m = -INFINITY, row_l = 0.f;  // of a softmax thread's row
     int sent_k = 0, sent_v = 0;  // panels and halves that the copying warp has asked for
 
     if (warp < 8) {
@@ -199,7 +214,7 @@ __global__ void __launch_bounds__(NT, 1)
         // one tile; EDGE: some row of the block does not see all of it
         auto tile = [&](auto EDGE, int j) {
             constexpr bool edge = decltype(EDGE)::value;
-            const int j0 = j * TILE;
+            const int j0 = (from + j) * TILE;
             uint32_t s[TILE];
 #pragma unroll
             for (int c = 0; c < TILE; c += 32) tm_ld32(*reinterpret_cast<uint32_t(*)[32]>(s + c), my_s + c);
@@ -270,7 +285,7 @@ __global__ void __launch_bounds__(NT, 1)
         for (int j = 0; j < mine_nt; ++j) {
             if (!(ok = warp_wait(&ms.s_full[g], j & 1, limit))) break;
             tm_after();
-            if (j * TILE + TILE - 1 > least) tile(std::true_type(), j);
+            if ((from + j) * TILE + TILE - 1 > least) tile(std::true_type(), j);
             else tile(std::false_type(), j);
             if (!ok) break;
         }
@@ -279,11 +294,12 @@ __global__ void __launch_bounds__(NT, 1)
         tm_after();
         // what a CTA that gave up leaves is no number, nor what sees a value that is none
         if (!ok || last >= ms.bad) l = __uint_as_float(0x7fffffffu);
+        row_m = mx, row_l = l;
         const float inv = l == 0.f ? 0.f : 1.f / l;
         const bool real = row < n;
         uint4* const to = reinterpret_cast<uint4*>(p.out + 2 * ((long long)(q0 + row) * p.ot + (long long)h * p.oh));
 #pragma unroll 1
-        for (int d = 0; d < VD; d += 32) {
+        for (int d = 0; d < VD && p.split == 1; d += 32) {
             uint32_t o[32];
             tm_ld32(o, my_o + d);
             tm_wait_ld();
@@ -299,7 +315,7 @@ __global__ void __launch_bounds__(NT, 1)
                 }
             }
         }
-        if (real && p.lse) p.lse[(long long)(q0 + row) * p.H + h] = l == 0.f ? -INFINITY : (mx + log2f(l)) * LN2;
+        if (real && p.lse && p.split == 1) p.lse[(long long)(q0 + row) * p.H + h] = l == 0.f ? -INFINITY : (mx + log2f(l)) * LN2;
     } else {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(REGS_REST));
     }
@@ -310,7 +326,7 @@ __global__ void __launch_bounds__(NT, 1)
         Slot<VS> vs;
         bool ok = true;
         for (int j = 0; j < nt && ok; ++j) {
-            const int key = k0 + j * TILE;
+            const int key = k0 + (from + j) * TILE;
             for (int c = 0; c < PANELS; ++c, ks.next()) {
                 ok = ok && (!ks.turn || warp_wait(&ms.k_free[ks.i], (ks.turn - 1) & 1, limit));
                 if (!ok && c == 0) break;  // (a tile that has begun is finished all the same: its barrier counts all of it)
@@ -349,7 +365,7 @@ __global__ void __launch_bounds__(NT, 1)
         const int all = behind + i0, some = behind + min(i0 + PAIR, n) - 1;  // keys up to which all rows, and any row, see
         for (int j = 0; j < 2 * nt && ok; ++j, vs.next()) {
             if (!(ok = warp_wait(&ms.v_full[vs.i], vs.turn & 1, limit))) break;
-            const int j0 = 64 * j;
+            const int j0 = from * TILE + 64 * j;
             if (j0 + 63 > all) {
                 // 16-byte piece c: value panel c / 512, key c / 8 % 64 of the half
                 uint4* const at = reinterpret_cast<uint4*>(smem + V_OFF + vs.i * VHALF_B) + lane;
@@ -474,6 +490,54 @@ __global__ void __launch_bounds__(NT, 1)
     tm_before();
     __syncthreads();
     tm_after();
+    if (p.split > 1) {
+        // ================ the block's parts meet: outputs over the queries and rings, which nothing uses any more ================
+        float* const outs = reinterpret_cast<float*>(smem);
+        if (warp < 8) {
+            const uint32_t my_o = tm + ((uint32_t)((warp & 3) * 32) << 16) + T_O + (warp >> 2) * VD;
+            const bool some = (warp >> 2) ? nt1 : nt0;
+            float* const row = outs + tid * OUT_ROW;
+#pragma unroll 1
+            for (int d = 0; d < VD; d += 16) {
+                uint32_t o[16];
+                tm_ld16(o, my_o + d);
+                tm_wait_ld();
+#pragma unroll
+                for (int e = 0; e < 16; e += 4)  // (without a tile: what lies in the tensor memory may be anything)
+                    *reinterpret_cast<float4*>(row + d + e) =
+                        some ? make_float4(__uint_as_float(o[e]), __uint_as_float(o[e + 1]), __uint_as_float(o[e + 2]), __uint_as_float(o[e + 3]))
+                             : make_float4(0.f, 0.f, 0.f, 0.f);
+            }
+            // (where a role gave up, copies may still land on what lies here)
+            *reinterpret_cast<float2*>(row + VD) = make_float2(row_m, ms.abort ? __uint_as_float(0x7fffffffu) : row_l);
+        }
+        cluster_meet();
+        // a warp a row, four values a lane
+        const int r1 = PAIR * (part + 1) / p.split;
+        for (int r = PAIR * part / p.split + warp; r < r1; r += NT / 32) {
+            const int row = i0 + r;
+            if (row >= n) break;
+            float mx = -INFINITY, l = 0.f;
+            float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+            for (int c = 0; c < p.split; ++c) {
+                float2 st;
+                float4 y;
+                uint32_t a;
+                asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(sm32(outs + r * OUT_ROW)), "r"(c));
+                asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];" : "=f"(st.x), "=f"(st.y) : "r"(a + VD * 4) : "memory");
+                asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(y.x), "=f"(y.y), "=f"(y.z), "=f"(y.w) : "r"(a + 16 * lane) : "memory");
+                const float mn = fmaxf(mx, st.x), ref = mn == -INFINITY ? 0.f : mn, f = ex2(mx - ref), w = ex2(st.x - ref);
+                mx = mn;
+                l = l * f + st.y * w;
+                o.x = o.x * f + y.x * w, o.y = o.y * f + y.y * w, o.z = o.z * f + y.z * w, o.w = o.w * f + y.w * w;
+            }
+            const float inv = l == 0.f ? 0.f : 1.f / l;
+            *reinterpret_cast<uint2*>(p.out + 2 * ((long long)(q0 + row) * p.ot + (long long)h * p.oh + 4 * lane)) =
+                make_uint2(pack16<F16>(o.x * inv, o.y * inv), pack16<F16>(o.z * inv, o.w * inv));
+            if (lane == 0 && p.lse) p.lse[(long long)(q0 + row) * p.H + h] = l == 0.f ? -INFINITY : (mx + log2f(l)) * LN2;
+        }
+        cluster_meet();  // the others have read what lies here
+    }
     if (ms.abort) {
         // copies may still be on their way into this CTA's memory: the queries, at most the rings' last ones
         if (warp == 8 && sent_k) {
@@ -513,14 +577,27 @@ int map_of(const void* base, int dtype, int width, int heads, int rows, int64_t 
 }
 
 template <bool F16>
-int run(const PromptP& p, const PromptMaps& maps, int grid, cudaStream_t s) {
+int run(PromptP& p, const PromptMaps& maps, int64_t blocks, cudaStream_t s) {
     auto kern = prompt_kernel<F16>;
     static std::atomic<uint64_t> done;
     int dev, sms;
     if (const int rc = device_sms(dev, sms, "mk_prompt_attend")) return rc;
     if (const int rc = allow_smem(kern, SMEM, dev, done, "mk_prompt_attend")) return rc;
-    kern<<<grid, NT, SMEM, s>>>(p, maps);
-    return cuda_status(cudaGetLastError(), "mk_prompt_attend");
+    // few blocks share their tiles out to clusters, while a CTA has four of them or more (of a sequence's average)
+    p.split = 1;
+    while (p.split < 8 && blocks * p.split * 2 <= sms && p.n_k / p.B >= 4 * TILE * p.split * 2) p.split *= 2;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(blocks * p.split));
+    cfg.blockDim = dim3(NT);
+    cfg.dynamicSmemBytes = SMEM;
+    cfg.stream = s;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeClusterDimension;
+    at[0].val.clusterDim.x = p.split;
+    at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = p.split > 1;
+    return cuda_status(cudaLaunchKernelEx(&cfg, kern, p, maps), "mk_prompt_attend");
 }
 
 }  // namespace
@@ -547,8 +624,8 @@ extern "C" int mk_prompt_attend(const mk_prompt_attention* a, void* stream) {
     if ((a->n_tokens > 1 && (!a->q_token || !a->out_token)) || (a->n_keys > 1 && (!a->k_token || !a->rope_token || !a->v_token)) ||
         (a->n_heads > 1 && !a->out_head))
         return fail(MK_ERR_UNSUPPORTED, "prompt: tokens must not share their rows (a stride of 0), nor heads those of out");
-    const int64_t blocks = ((int64_t)a->n_tokens / PAIR + a->batch) * a->n_heads;
-    if (blocks > INT32_MAX) return fail(MK_ERR_UNSUPPORTED, "prompt: too many sequences or queries in one call");
+    const int64_t blocks = (a->n_tokens + (int64_t)(PAIR - 1) * a->batch) / PAIR * a->n_heads;
+    if (blocks > INT32_MAX / 8) return fail(MK_ERR_UNSUPPORTED, "prompt: too many sequences or queries in one call");
     PromptP p = {};
     p.q_starts = a->q_starts, p.k_starts = a->k_starts;
     p.out = (uint8_t*)a->out, p.lse = a->lse, p.status = a->status, p.ot = a->out_token, p.oh = a->out_head;
@@ -566,5 +643,5 @@ extern "C" int mk_prompt_attend(const mk_prompt_attention* a, void* stream) {
         if (const int rc = map_of(a->v, dt, VD, p.v_heads ? H : 0, M, a->v_head, a->v_token, 64, &maps.v)) return rc;
     }
     cudaStream_t s = (cudaStream_t)stream;
-    return dt == MK_DT_F16 ? run<true>(p, maps, (int)blocks, s) : run<false>(p, maps, (int)blocks, s);
+    return dt == MK_DT_F16 ? run<true>(p, maps, blocks, s) : run<false>(p, maps, blocks, s);
 }

@@ -256,3 +256,22 @@ def test_the_bindings_refusals():
     with pytest.raises(mk.MKError):  # heads of another size
         latent.attend_prompt(q[..., :128], k[..., :64], r, v, at, at, 0.1)
     assert latent.attend_prompt(q[:0], k, r, v, ints(0, 0), at, 0.1).shape == (0, 2, 128)
+
+
+@gpu
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("nq,ctx,H", [
+    ([1], [3000], 1), ([1], [20000], 2), ([200], [9000], 3), ([64, 1], [5000, 1000], 1), ([300], [2000], 5), ([257], [1024], 1),
+    ([5, 5, 5], [2100, 0, 4000], 2), ([130], [16000], 1), ([1000], [0], 3),
+])
+def test_few_queries_behind_long_contexts(dtype, nq, ctx, H):
+    """Blocks whose keys several CTAs share, parts without a tile of a block among them."""
+    nk = [n + c for n, c in zip(nq, ctx)]
+    q, k, r, v = make(dtype, nq, nk, H)
+    q_at, k_at = starts(nq), starts(nk)
+    out, lse = latent.attend_prompt(q, k, r, v, q_at, k_at, 192 ** -0.5, return_lse=True)
+    check(q, k, r, v, q_at, k_at, 192 ** -0.5, out, lse)
+    if len(nq) == 1 and nq[0] > 1:  # the newest key is the last query's alone
+        k[-1] = r[-1] = v[-1] = math.nan
+        again = latent.attend_prompt(q, k, r, v, q_at, k_at, 192 ** -0.5)
+        assert torch.equal(again[:-1], out[:-1]) and again[-1].isnan().all()
