@@ -583,19 +583,34 @@ int run(PromptP& p, const PromptMaps& maps, int64_t blocks, cudaStream_t s) {
     int dev, sms;
     if (const int rc = device_sms(dev, sms, "mk_prompt_attend")) return rc;
     if (const int rc = allow_smem(kern, SMEM, dev, done, "mk_prompt_attend")) return rc;
-    // few blocks share their tiles out to clusters, while a CTA has four of them or more (of a sequence's average)
-    p.split = 1;
-    while (p.split < 8 && blocks * p.split * 2 <= sms && p.n_k / p.B >= 4 * TILE * p.split * 2) p.split *= 2;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)(blocks * p.split));
     cfg.blockDim = dim3(NT);
     cfg.dynamicSmemBytes = SMEM;
     cfg.stream = s;
     cudaLaunchAttribute at[1];
     at[0].id = cudaLaunchAttributeClusterDimension;
-    at[0].val.clusterDim.x = p.split;
     at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
     cfg.attrs = at;
+    cfg.numAttrs = 1;
+    // how many clusters of 2, 4, 8 CTAs the device holds at once, asked for once
+    static std::atomic<int> room[64][3];
+    auto fits = [&](int i) {
+        int n = dev < 64 ? room[dev][i].load(std::memory_order_relaxed) : 0;
+        if (!n) {
+            at[0].val.clusterDim.x = 2 << i;
+            cfg.gridDim = dim3((unsigned)(2 << i));
+            if (cudaOccupancyMaxActiveClusters(&n, kern, &cfg) != cudaSuccess || n < 1) n = 1, cudaGetLastError();
+            if (dev < 64) room[dev][i].store(n, std::memory_order_relaxed);
+        }
+        return n;
+    };
+    // Few blocks share their tiles out to clusters, as long as these run all at once and a CTA has four tiles or more (of a
+    // sequence's average). 256 tokens at 8192 positions, 16 heads: 136 us by one CTA a block, 48 by four; by eight, which
+    // do not all find room at once, 63.
+    p.split = 1;
+    for (int i = 0; i < 3 && p.n_k / p.B >= (4 * TILE << (i + 1)) && blocks <= fits(i); ++i) p.split = 2 << i;
+    cfg.gridDim = dim3((unsigned)(blocks * p.split));
+    at[0].val.clusterDim.x = p.split;
     cfg.numAttrs = p.split > 1;
     return cuda_status(cudaLaunchKernelEx(&cfg, kern, p, maps), "mk_prompt_attend");
 }
