@@ -733,15 +733,17 @@ __global__ void __launch_bounds__(NT, 1)
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tm), "n"(S::T_ALL) : "memory");
 }
 
-// Joins the pieces of an output row, a block 128 values of it: four warps take every fourth piece. Rows without a piece
-// get their zeros, rows whose only piece went straight to the output are left alone.
+// Joins the pieces of an output row. MANY rows: a block a row, a warp 128 values of it, piece after piece; else a block takes
+// 128 values of a row and its four warps every fourth piece each, whose trips to memory would follow one another. Rows
+// without a piece get their zeros, rows whose only piece went straight to the output are left alone.
 constexpr int JT = 128;
-template <int RANK, bool F16>
+template <int RANK, bool F16, bool MANY>
 __global__ void __launch_bounds__(JT) latent_join(const __grid_constant__ LatentP p, int main_grid) {
-    __shared__ float4 om[JT / 32][32];
-    __shared__ float2 oml[JT / 32];
-    constexpr int CH = RANK / 128;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, row = blockIdx.x / CH, d0 = (blockIdx.x - row * CH) * 128;
+    constexpr int CH = RANK / 128, W = MANY ? 1 : JT / 32;  // parts of a row; warps that share its pieces
+    __shared__ float4 om[W][32];
+    __shared__ float2 oml[W];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int row = MANY ? blockIdx.x : blockIdx.x / CH, d0 = (MANY ? warp : (int)blockIdx.x - row * CH) * 128, first = MANY ? 0 : warp;
     const int rows = p.T * p.H, b = row / rows, g = row - b * rows, rb = g / p.rows_blk, r = g - rb * p.rows_blk;
     const int item = b * p.RB + rb, t = g / p.H, h = g - t * p.H;
     asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -753,7 +755,7 @@ __global__ void __launch_bounds__(JT) latent_join(const __grid_constant__ Latent
     float m = -INFINITY, l = 0.f;
     float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 8
-    for (int c = c0 + warp; c <= c1; c += JT / 32) {
+    for (int c = c0 + first; c <= c1; c += W) {
         // a CTA's first piece is the one that its stretch begins with
         const float* const s = p.slots + (2ll * c + (t0 <= c * per ? 0 : 1)) * slot_f;
         const float2 ml = *reinterpret_cast<const float2*>(s + p.nr * RANK + 2 * r);
@@ -763,20 +765,36 @@ __global__ void __launch_bounds__(JT) latent_join(const __grid_constant__ Latent
         l = l * f + ml.y * w;
         o.x = o.x * f + y.x * w, o.y = o.y * f + y.y * w, o.z = o.z * f + y.z * w, o.w = o.w * f + y.w * w;
     }
-    om[warp][lane] = o;
-    if (lane == 0) oml[warp] = make_float2(m, l);
+    const long long to = b * p.ob + t * p.ot + h * p.oh + d0;
+    if constexpr (MANY) {
+        const float x[4] = {o.x, o.y, o.z, o.w};
+        uint16_t z[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) put16<F16>(reinterpret_cast<uint8_t*>(z), i, l == 0.f ? 0.f : x[i] / l);
+        uint16_t* const at = reinterpret_cast<uint16_t*>(p.out) + to + 4 * lane;
+        if (((uintptr_t)at & 7) == 0) {
+            *reinterpret_cast<uint2*>(at) = make_uint2(z[0] | (uint32_t)z[1] << 16, z[2] | (uint32_t)z[3] << 16);
+        } else {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) at[i] = z[i];
+        }
+        if (threadIdx.x == 0 && p.lse) p.lse[row] = l == 0.f ? -INFINITY : (m + log2f(l)) * LN2;
+        return;
+    }
+    om[first][lane] = o;
+    if (lane == 0) oml[first] = make_float2(m, l);
     __syncthreads();
     float mm = -INFINITY, ll = 0.f, y = 0.f;
 #pragma unroll
-    for (int i = 0; i < JT / 32; ++i) mm = fmaxf(mm, oml[i].x);
+    for (int i = 0; i < W; ++i) mm = fmaxf(mm, oml[i].x);
     const float ref = mm == -INFINITY ? 0.f : mm;
 #pragma unroll
-    for (int i = 0; i < JT / 32; ++i) {
+    for (int i = 0; i < W; ++i) {
         const float w = ex2(oml[i].x - ref);
         ll += oml[i].y * w;
         y += reinterpret_cast<const float*>(om[i])[threadIdx.x] * w;
     }
-    put16<F16>(p.out, b * p.ob + t * p.ot + h * p.oh + d0 + threadIdx.x, ll == 0.f ? 0.f : y / ll);
+    put16<F16>(p.out, to + threadIdx.x, ll == 0.f ? 0.f : y / ll);
     if (threadIdx.x == 0 && d0 == 0 && p.lse) p.lse[row] = ll == 0.f ? -INFINITY : (mm + log2f(ll)) * LN2;
 }
 
@@ -800,14 +818,14 @@ int map_of(const void* base, int width, const mk_latent_pages& g, int64_t page_s
 
 struct Plan {
     bool rows;  // a block a row
-    int nr, rows_blk, RB, grid, dev;
+    int nr, rows_blk, RB, grid, dev, sms;
     int64_t slots_off, bytes;
 };
 
 constexpr int MIN_UNITS = 4;  // positions a CTA takes at least: 4 tiles
 
 template <int MT, int NR, bool F16>
-int run(const LatentP* p, const mk_latent_pages* g, int dev, int grid, cudaStream_t s) {
+int run(const LatentP* p, const mk_latent_pages* g, int dev, int sms, int grid, cudaStream_t s) {
     using S = LatentShape<MT, NR>;
     auto kern = latent_kernel<MT, NR, F16>;
     static std::atomic<uint64_t> done;
@@ -818,15 +836,20 @@ int run(const LatentP* p, const mk_latent_pages* g, int dev, int grid, cudaStrea
     kern<<<grid, NT, S::SMEM, s>>>(*p, maps);
     if (const int rc = cuda_status(cudaGetLastError(), "mk_latent_attend")) return rc;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)(p->B * p->T * p->H * MT));
-    cfg.blockDim = dim3(JT);
+    // Many rows of a few pieces each. Whole calls with and without: 64 sequences of 7 tokens at up to 8192 (7168 rows, 2 pieces)
+    // 161 and 182 us, 16 of 128 heads (2048 rows, 5 pieces) 53 and 57; 8 of 7 tokens (896 rows, 10 pieces) 43 and 38.
+    const int rows = p->B * p->T * p->H;
+    const bool many = rows >= 4 * sms && grid <= 6 * (int64_t)p->B * p->RB;
+    cfg.gridDim = dim3((unsigned)(many ? rows : rows * MT));
+    cfg.blockDim = dim3(many ? 32 * MT : JT);
     cfg.stream = s;
     cudaLaunchAttribute at[1];
     at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     at[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = at;
     cfg.numAttrs = 1;
-    return cuda_status(cudaLaunchKernelEx(&cfg, latent_join<128 * MT, F16>, *p, grid), "mk_latent_attend");
+    return cuda_status(many ? cudaLaunchKernelEx(&cfg, latent_join<128 * MT, F16, true>, *p, grid)
+                            : cudaLaunchKernelEx(&cfg, latent_join<128 * MT, F16, false>, *p, grid), "mk_latent_attend");
 }
 
 int check(const mk_latent_attention* a) {
@@ -856,8 +879,7 @@ int make_plan(const mk_latent_attention* a, Plan& pl) {
     pl = {};
     pl.rows = g.page_size < 8 || !g.page_stride || !g.row_stride || !g.rope_page_stride || !g.rope_row_stride;
     if (pl.rows) return MK_OK;
-    int sms;
-    if (const int rc = device_sms(pl.dev, sms, "mk_latent_attend")) return rc;
+    if (const int rc = device_sms(pl.dev, pl.sms, "mk_latent_attend")) return rc;
     const int rows = a->n_tokens * a->n_heads;
     pl.RB = (rows + 63) / 64;
     pl.rows_blk = (rows + pl.RB - 1) / pl.RB;
@@ -867,7 +889,7 @@ int make_plan(const mk_latent_attention* a, Plan& pl) {
     const int64_t most = items * ((cap + TILE - 1) / TILE + 1);
     if (most > (1 << 30)) return fail(MK_ERR_UNSUPPORTED, "latent attend: too many positions in one call");
     const int64_t want = (most + MIN_UNITS - 1) / MIN_UNITS;
-    pl.grid = (int)(want < sms ? want : sms);
+    pl.grid = (int)(want < pl.sms ? want : pl.sms);
     pl.slots_off = ((items + 1) * 4 + 255) / 256 * 256;
     pl.bytes = pl.slots_off + 2ll * pl.grid * pl.nr * (g.rank + 2) * 4;
     pl.bytes = (pl.bytes + 255) / 256 * 256;
@@ -917,7 +939,7 @@ extern "C" int mk_latent_attend(const mk_latent_attention* a, void* workspace, i
     p.q_vec = rows_vec(a->q) && rows_vec(a->q_rope);
     auto go = [&](auto MT, auto NR) {
         constexpr int mt = decltype(MT)::value, nr = decltype(NR)::value;
-        return f16 ? run<mt, nr, true>(&p, &g, pl.dev, pl.grid, s) : run<mt, nr, false>(&p, &g, pl.dev, pl.grid, s);
+        return f16 ? run<mt, nr, true>(&p, &g, pl.dev, pl.sms, pl.grid, s) : run<mt, nr, false>(&p, &g, pl.dev, pl.sms, pl.grid, s);
     };
     using std::integral_constant;
     auto rank = [&](auto MT) {
