@@ -34,7 +34,6 @@ constexpr int GROUPS = GT / 2;            // of two threads; up to k = 32 half a
 // the list: what may be left of it, and what a round may add (the values of k groups)
 constexpr int SLACK = 8, CAP = MAX_TOP + SLACK + MAX_TOP * 2 * U * 8;
 constexpr int MAX_CLUSTER = 8;
-constexpr int AHEAD = 2;  // rounds in flight
 
 struct LogprobP {
     const uint8_t* logits;
@@ -315,30 +314,27 @@ __global__ void __launch_bounds__(GT, 2) logprob_kernel(const __grid_constant__ 
     if (part == 0 && head) single(tid, tid < head);
     {
         const int id0 = head + w0 * VEC, all = w1 - w0;
-        const uint8_t* const q = x + (long long)id0 * (DT == MK_DT_F32 ? 4 : 2);
-        // a thread's own words come through its own places in shared memory, some rounds ahead
+        // a thread's own words come through its own places in shared memory, a round ahead
+        constexpr int STAGE_B = U * GT * 16;
         const uint32_t mine = sm32(ring) + tid * 16;
-        int into = 0;
-        auto load = [&](int i) {
+        const uint8_t* src = x + (long long)id0 * (DT == MK_DT_F32 ? 4 : 2) + tid * 16;
+        int ahead = all - tid;  // words from the next one to ask for on (every GT-th is this thread's)
+        auto load = [&](uint32_t to) {
 #pragma unroll
-            for (int u = 0; u < U; ++u) {
-                const int w = (i * U + u) * GT + tid;
-                if (w < all) cp16(mine + (into * U + u) * GT * 16, q + 16ll * w, true);
-            }
-            if (++into == AHEAD) into = 0;
+            for (int u = 0; u < U; ++u)
+                if (ahead > u * GT) cp16(to + u * GT * 16, src + u * GT * 16, true);
+            src += STAGE_B;
+            ahead -= U * GT;
             cp_commit();
         };
-#pragma unroll
-        for (int i = 0; i < AHEAD - 1; ++i) load(i);
-        int stage = 0;
-        for (int w = 0, i = 0; w < all; w += U * GT, ++i) {
-            load(i + AHEAD - 1);
-            cp_wait<AHEAD - 1>();
-            const uint8_t* const words = ring + stage * U * GT * 16 + tid * 16;
+        load(mine);
+        uint32_t stage = 0;
+        for (int left = all - tid, id = id0 + tid * VEC; left > -tid; left -= U * GT, id += U * GT * VEC) {
+            load(mine + (stage ^ STAGE_B));
+            cp_wait<1>();
+            const uint8_t* const words = ring + stage + tid * 16;
             float top = -INFINITY;
-#pragma unroll
-            for (int u = 0; u < U; ++u) {
-                if (w + u * GT + tid >= all) break;
+            auto word = [&](int u) {
                 const uint4 z = *reinterpret_cast<const uint4*>(words + u * GT * 16);
                 const float mx = largest<DT>(z);
                 if (!(mx <= m)) rise(mx);
@@ -347,19 +343,25 @@ __global__ void __launch_bounds__(GT, 2) logprob_kernel(const __grid_constant__ 
                 unpack<DT>(z, y);
 #pragma unroll
                 for (int e = 0; e < VEC; ++e) add(y[e]);
+            };
+            if (left > (U - 1) * GT) {
+#pragma unroll
+                for (int u = 0; u < U; ++u) word(u);
+            } else {
+#pragma unroll 1
+                for (int u = 0; u < U && left > u * GT; ++u) word(u);
             }
             if constexpr (TOP)
-                pick(top, w + tid < all, [&](auto f) {
+                pick(top, left > 0, [&](auto f) {
 #pragma unroll 1
-                    for (int u = 0; u < U; ++u) {
-                        if (w + u * GT + tid >= all) break;
+                    for (int u = 0; u < U && left > u * GT; ++u) {
                         float y[VEC];
                         unpack<DT>(*reinterpret_cast<const uint4*>(words + u * GT * 16), y);
 #pragma unroll
-                        for (int e = 0; e < VEC; ++e) f(y[e], id0 + (w + u * GT + tid) * VEC + e);
+                        for (int e = 0; e < VEC; ++e) f(y[e], id + u * GT * VEC + e);
                     }
                 });
-            if (++stage == AHEAD) stage = 0;
+            stage ^= STAGE_B;
         }
     }
     if (part == split - 1 && tail) single(p.V - tail + tid, tid < tail);
@@ -421,7 +423,7 @@ __global__ void __launch_bounds__(GT, 2) logprob_kernel(const __grid_constant__ 
 
 template <int DT>
 int run(const LogprobP& p, int rows, int dev, cudaStream_t s) {
-    constexpr int SMEM = AHEAD * GT * U * 16;
+    constexpr int SMEM = 2 * GT * U * 16;
     static std::atomic<uint64_t> done[2];
     if (const int rc = p.top ? allow_smem(logprob_kernel<DT, true>, SMEM, dev, done[1], "mk_logprobs")
                              : allow_smem(logprob_kernel<DT, false>, SMEM, dev, done[0], "mk_logprobs"))
