@@ -6,7 +6,7 @@
 //   out = sum_j e^(x_j - m) c_j / sum_j e^(x_j - m):
 // one vector a position is key and value of all heads, so the rows of all heads
 // (and of a few tokens) stand against one copy of it, up to 64 rows a CTA. A
-// tile of positions lies in shared memory once, in the 128-byte-swizzled order
+// tile of 32 positions lies in shared memory once, in the 128-byte-swizzled order
 // of tensor maps, and feeds both products on the fifth-generation tensor cores:
 //   S  = Q C^T      64 rows x the tile's positions, over rank + 64 values;
 //   O' = C^T P^T    rank values x rows: the output transposed, C as the
@@ -30,6 +30,16 @@
 // and a second launch joins them. All waits have a limit, after which the CTA
 // frees its tensor memory and leaves (MK_ERR_TIMEOUT in `status`, NaN in its
 // rows).
+//
+// Measured, 16 heads on 512 + 64 values, bf16: 64 sequences of up to 32768
+// positions 237 us (6.5 TB/s, 95 % of what a copy reaches: HBM). One sequence of
+// 8192 15 us, all latency (4 tiles a CTA: 2 us to the first tile's copy, 1 its way,
+// 1.7 to its weights, 0.9 a tile, 1 the piece's end; the launches, and 3 us of
+// join). Rows past 16 are bound by what feeds the products from shared memory: 64
+// rows take 1030 cycles a tile for S (36 steps of 28) and 410 for O', 1600 in
+// all: 8 sequences of 8192 with 7 tokens 38 us (9 of them pieces and join), 64 of
+// them 161. Tiles of 64 positions feed S better (36 cycles a step of twice the
+// positions) but two of them fill shared memory, and copies then wait: 192 us.
 //
 // Pages of fewer than 8 positions, or overlapping ones (a stride of 0), have no
 // tensor map: a block a row takes them, a position a warp at a time.
