@@ -15,8 +15,10 @@
 // Ids rise from round to round, so that an equal logit of a later round never
 // counts.
 //
-// Bound by HBM for batches (some 7 instructions a value), by latency for single
-// rows: a trip to memory, three votes, the cluster's meeting.
+// Bound by issue for batches: 256 rows of 151936 bf16 logits take 19 us without
+// alternatives (12 instructions a value, 60 % of a copy's rate), 45 with 20 of them
+// (21 a value, and the rounds' votes). Single rows by latency, a trip to memory,
+// the threshold's and the ranks' votes, the cluster's meeting: 32000 fp32 logits 7 us.
 #include <climits>
 #include <type_traits>
 
