@@ -257,12 +257,13 @@ __global__ void __launch_bounds__(GT, 2) logprob_kernel(const __grid_constant__ 
         const int some = __syncthreads_count(in && (!limit || top > limit_x));
         if (!some) return;
         if (some > k) {
-            // a threshold from the groups' largest keys
+            // A threshold from the groups' largest keys, which must differ, or none has rank k - 1 and all values would go to
+            // the list: a largest logit that is no number equals none of them, and takes the thread's number for its id.
             int first = INT_MAX;
             each([&](float x, int id) {
                 if (x == top) first = min(first, id);
             });
-            u64 best = in ? key_of(top, first) : 0;
+            u64 best = in ? key_of(top, first == INT_MAX ? tid : first) : 0;
             best = max(best, __shfl_xor_sync(0xffffffffu, best, 1));
             if (k <= 32) best = max(best, __shfl_xor_sync(0xffffffffu, best, 2));
             const int by = k <= 32 ? 2 : 1;

@@ -233,3 +233,23 @@ def test_a_loop_keeps_its_tokens_probabilities():
             assert torch.allclose(h[:, i].double(), entropy.cpu(), atol=1e-5)
             assert torch.equal(ids[:, i].long(), x.sort(dim=-1, descending=True, stable=True).indices[:, :3].cpu())
     assert runs[0] == runs[1]
+
+
+@gpu
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("top", [1, 2, 7, 32, 33, 64])
+@pytest.mark.parametrize("rows,V", [(3, 1000), (2, 32000), (200, 40011)])
+def test_rows_full_of_nan(dtype, top, rows, V):
+    """NaNs of many threads at once, also in later rounds with logits that rise, beside rows without any."""
+    g = torch.Generator("cuda").manual_seed(11)
+    x = torch.randn(rows, V, device="cuda", generator=g)
+    x[0] = torch.arange(V, device="cuda") * (64.0 / V)
+    x[0][torch.rand(V, device="cuda", generator=g) < 0.3] = math.nan
+    x[1] = torch.arange(V, device="cuda") * (64.0 / V)
+    x[1, V // 2::37] = math.nan
+    x = x.to(dtype)
+    tokens = torch.arange(rows, device="cuda", dtype=torch.int32)
+    got, h, ids, best = sampling.logprobs(x, tokens, top=top)
+    assert got[:2].isnan().all() and h[:2].isnan().all() and (ids[:2] == -1).all() and best[:2].isnan().all()
+    if rows > 2:
+        check(x[2:], tokens[2:], top)
