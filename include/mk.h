@@ -650,9 +650,11 @@ typedef struct mk_prompt_attention {
     int32_t reserved;
 } mk_prompt_attention;
 
-/* Errors: INVALID_ARG; UNSUPPORTED (dims other than nope 128, rope 64, v 128).
+/* Errors: INVALID_ARG; UNSUPPORTED (dims other than nope 128, rope 64, v 128;
+ * more than 2^30 keys, 2^20 sequences or 2^27 queries of heads).
  * Bounds that descend or leave the rows are reported through `status` (as
- * MK_ERR_INVALID_ARG) and the sequence is skipped. */
+ * MK_ERR_INVALID_ARG) and the sequence is skipped; where other sequences then
+ * overlap, their outputs are undefined. */
 int mk_prompt_attend(const mk_prompt_attention* args, void* stream);
 
 /* Log probabilities. With z = logits / temperature of a row and
@@ -678,7 +680,7 @@ typedef struct mk_logprob {
 } mk_logprob;
 
 /* Errors: INVALID_ARG (NULL, sizes, alignment, top above vocab); UNSUPPORTED
- * (top above 64). Deterministic. */
+ * (top above 64, vocab above 2^30). Deterministic. */
 int mk_logprobs(const mk_logprob* args, void* stream);
 
 #ifdef __cplusplus

@@ -455,6 +455,7 @@ extern "C" int mk_logprobs(const mk_logprob* a, void* stream) {
     if (a->rows < 0 || a->vocab < 1 || a->given < 0 || a->top < 0 || a->row_stride < 0)
         return fail(MK_ERR_INVALID_ARG, "logprobs: rows, given, top or row_stride negative, or vocab below 1");
     if (a->top > a->vocab) return fail(MK_ERR_INVALID_ARG, "logprobs: top %d of a vocabulary of %d", a->top, a->vocab);
+    if (a->vocab > 1 << 30) return fail(MK_ERR_UNSUPPORTED, "logprobs: vocab above 2^30");
     if (a->top > MAX_TOP) return fail(MK_ERR_UNSUPPORTED, "logprobs: top above %d", MAX_TOP);
     if (!a->logits || (a->given && (!a->tokens || !a->logprobs)) || (a->top && (!a->top_ids || !a->top_logprobs)))
         return fail(MK_ERR_INVALID_ARG, "logprobs: logits, tokens, logprobs, top_ids or top_logprobs is NULL");

@@ -640,6 +640,7 @@ extern "C" int mk_prompt_attend(const mk_prompt_attention* a, void* stream) {
     if (a->q_token < 0 || a->q_head < 0 || a->k_token < 0 || a->k_head < 0 || a->rope_token < 0 || a->v_token < 0 ||
         a->v_head < 0 || a->out_token < 0 || a->out_head < 0)
         return fail(MK_ERR_INVALID_ARG, "prompt: negative stride");
+    if (a->n_keys > 1 << 30) return fail(MK_ERR_UNSUPPORTED, "prompt: more than 2^30 keys in one call");
     if (a->batch > (1 << 20) || (int64_t)a->n_tokens * a->n_heads > INT32_MAX / 16)
         return fail(MK_ERR_UNSUPPORTED, "prompt: too many sequences or queries in one call");
     if ((a->n_tokens > 1 && (!a->q_token || !a->out_token)) || (a->n_keys > 1 && (!a->k_token || !a->rope_token || !a->v_token)) ||

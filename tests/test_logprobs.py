@@ -65,6 +65,7 @@ def _args(**over):
     (dict(logits=None), mk.ERR_INVALID_ARG), (dict(logits=4098), mk.ERR_INVALID_ARG), (dict(dtype=5), mk.ERR_INVALID_ARG),
     (dict(rows=-1), mk.ERR_INVALID_ARG), (dict(vocab=0), mk.ERR_INVALID_ARG), (dict(given=-1), mk.ERR_INVALID_ARG),
     (dict(top=-1), mk.ERR_INVALID_ARG), (dict(top=101), mk.ERR_INVALID_ARG), (dict(top=65), mk.ERR_UNSUPPORTED),
+    (dict(vocab=(1 << 30) + 1), mk.ERR_UNSUPPORTED),
     (dict(tokens=None), mk.ERR_INVALID_ARG), (dict(logprobs=None), mk.ERR_INVALID_ARG),
     (dict(top_ids=None), mk.ERR_INVALID_ARG), (dict(top_logprobs=None), mk.ERR_INVALID_ARG),
     (dict(tokens=4098), mk.ERR_INVALID_ARG), (dict(temperature=4097), mk.ERR_INVALID_ARG),
