@@ -93,7 +93,8 @@ def _args(**over):
     (dict(n_heads=0), mk.ERR_INVALID_ARG), (dict(scale=math.nan), mk.ERR_INVALID_ARG),
     (dict(scale=math.inf), mk.ERR_INVALID_ARG), (dict(nope_dim=64), mk.ERR_UNSUPPORTED),
     (dict(rope_dim=32), mk.ERR_UNSUPPORTED), (dict(v_dim=64), mk.ERR_UNSUPPORTED),
-    (dict(n_tokens=1 << 30), mk.ERR_UNSUPPORTED), (dict(n_keys=(1 << 30) + 1), mk.ERR_UNSUPPORTED), (dict(batch=1 << 21), mk.ERR_UNSUPPORTED), (dict(n_tokens=0), mk.OK),
+    (dict(n_tokens=1 << 30), mk.ERR_UNSUPPORTED), (dict(n_keys=(1 << 30) + 1), mk.ERR_UNSUPPORTED),
+    (dict(batch=1 << 21), mk.ERR_UNSUPPORTED), (dict(n_tokens=0), mk.OK),
 ])
 def test_refusals(over, code):
     assert mk.lib().mk_prompt_attend(ctypes.byref(_args(**over)), None) == code
