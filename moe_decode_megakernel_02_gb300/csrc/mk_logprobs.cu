@@ -33,7 +33,7 @@ typedef unsigned long long u64;
 constexpr int MAX_TOP = 64;
 constexpr int GT = 512, U = 4;            // threads, 16-byte words of a thread's round
 constexpr int GROUPS = GT / 2;            // of two threads; up to k = 32 half as many, of four
-// the list: what may be left of it, and what a round may add (the values of k groups)
+// the list: what may be left of it, and what a round may add (the values of k groups, or of as many threads)
 constexpr int SLACK = 8, CAP = MAX_TOP + SLACK + MAX_TOP * 2 * U * 8;
 constexpr int MAX_CLUSTER = 8;
 
@@ -259,16 +259,17 @@ __global__ void __launch_bounds__(GT, 2) logprob_kernel(const __grid_constant__ 
         add2(s[0], s[1], e0, e1);
         fma2(t[0], t[1], e0, e1, z0, z1, t[0], t[1]);
     };
-    // A round's most probable tokens: `top` is this thread's largest logit of the round (`in`: it has any), each(f) calls
-    // f(logit, id) for all of them.
+    // A round's most probable tokens: `top` is this thread's largest logit of the round (`in`: it has any), each(least, f)
+    // calls f(logit, id) for all of them, or at least those from `least` on.
     auto pick = [&](float top, bool in, auto each) {
         const int some = __syncthreads_count(in && (!limit || top > limit_x));
         if (!some) return;
-        if (some > k) {
+        // (the values of 2 MAX_TOP threads find room in the list)
+        if (some > (limit ? max(2 * k, 64) : k)) {
             // A threshold from the groups' largest keys, which must differ, or none has rank k - 1 and all values would go to
             // the list: a largest logit that is no number equals none of them, and takes the thread's number for its id.
             int first = INT_MAX;
-            each([&](float x, int id) {
+            each(top, [&](float x, int id) {
                 if (x == top) first = min(first, id);
             });
             u64 best = in ? key_of(top, first == INT_MAX ? tid : first) : 0;
@@ -288,22 +289,20 @@ __global__ void __launch_bounds__(GT, 2) logprob_kernel(const __grid_constant__ 
         }
         const float least = limit ? logit_of(limit) : -INFINITY;
         if (in && top >= least)
-            each([&](float x, int id) {
+            each(least, [&](float x, int id) {
                 if (x >= least) {
                     const u64 y = key_of(x, id);
                     if (y >= limit) sh.list[atomicAdd(&sh.n, 1)] = y;
                 }
             });
         __syncthreads();
-        n = sh.n;
-        __syncthreads();
+        n = sh.n;  // (what is written to it or the list from here on is behind another barrier)
         sorted = false;
         // (a threshold that follows closely spares the next rounds more than it costs)
         if (n > k + SLACK || (!have && n >= k)) {
             n = first_keys(sh, n, k);
             if (tid < n) sh.list[tid] = sh.best[tid];
-            if (tid == 0) sh.n = n;
-            __syncthreads();
+            if (tid == 0) sh.n = n;  // (read behind the next round's barrier)
             have = sorted = true;
         }
         if (have) {
@@ -318,7 +317,7 @@ __global__ void __launch_bounds__(GT, 2) logprob_kernel(const __grid_constant__ 
             add(x0, -INFINITY);
         }
         if constexpr (TOP)
-            pick(x0, in, [&](auto f) {
+            pick(x0, in, [&](float, auto f) {
                 if (in) f(x0, id);
             });
     };
@@ -363,11 +362,13 @@ __global__ void __launch_bounds__(GT, 2) logprob_kernel(const __grid_constant__ 
                 for (int u = 0; u < U && left > u * GT; ++u) word(u);
             }
             if constexpr (TOP)
-                pick(top, left > 0, [&](auto f) {
+                pick(top, left > 0, [&](float least, auto f) {
 #pragma unroll 1
                     for (int u = 0; u < U && left > u * GT; ++u) {
+                        const uint4 z = *reinterpret_cast<const uint4*>(words + u * GT * 16);
+                        if (!(largest<DT>(z) >= least)) continue;
                         float y[VEC];
-                        unpack<DT>(*reinterpret_cast<const uint4*>(words + u * GT * 16), y);
+                        unpack<DT>(z, y);
 #pragma unroll
                         for (int e = 0; e < VEC; ++e) f(y[e], id + u * GT * VEC + e);
                     }
