@@ -16,8 +16,8 @@
 // counts.
 //
 // Bound by issue for batches: 256 rows of 151936 bf16 logits take 19 us without
-// alternatives (12 instructions a value, 60 % of a copy's rate), 45 with 20 of them
-// (21 a value, and the rounds' votes). Single rows by latency, a trip to memory,
+// alternatives (11 instructions a value, 61 % of a copy's rate), 40 with 20 of them
+// (18 a value, and the rounds' votes). Single rows by latency, a trip to memory,
 // the threshold's and the ranks' votes, the cluster's meeting: 32000 fp32 logits 7 us.
 #include <climits>
 #include <type_traits>
@@ -480,7 +480,7 @@ extern "C" int mk_logprobs(const mk_logprob* a, void* stream) {
     p.logprobs = a->logprobs, p.entropy = a->entropy, p.top_ids = a->top_ids, p.top_logprobs = a->top_logprobs;
     p.V = a->vocab, p.given = a->given, p.top = a->top;
     // CTAs of a row: one or more an SM, as long as each has a part of a round (a CTA's first threshold and its end cost as
-    // much as two rounds: 256 rows of 151936 bf16 logits take 45 us in one part each, 57 in two)
+    // much as two rounds: 256 rows of 151936 bf16 logits take 40 us in one part each, 51 in two)
     p.split = 1;
     while (p.split < MAX_CLUSTER && (int64_t)a->rows * p.split < sms && a->vocab / p.split > GT * 4) p.split *= 2;
     cudaStream_t s = (cudaStream_t)stream;
