@@ -496,6 +496,23 @@ __global__ void __launch_bounds__(NT, 1)
     tm_before();
     __syncthreads();
     tm_after();
+    if (ms.abort) {
+        // copies may still be on their way into this CTA's memory (the queries, at most the rings' last ones): they land before
+        // anything else is written there, the marks of rows without a number among it
+        if (warp == 8 && sent_k) {
+            const long long t0 = now_ns();
+            auto gone = [&](unsigned long long* bar, unsigned parity) {
+                while (!bar_try(bar, parity) && now_ns() - t0 < DRAIN_NS) {
+                }
+            };
+            if (nt0) gone(&ms.q_full[0], 0);
+            if (nt1) gone(&ms.q_full[1], 0);
+            for (int c = max(0, sent_k / PANELS - 2); c < sent_k / PANELS; ++c) gone(&ms.k_full[c & 1], (unsigned)c >> 1 & 1u);
+            for (int c = max(0, sent_v - VS); c < sent_v; ++c) gone(&ms.v_full[c % VS], (unsigned)(c / VS) & 1u);
+        }
+        if (tid == 0 && p.status) *p.status = MK_ERR_TIMEOUT;
+        __syncthreads();
+    }
     if (p.split > 1) {
         // ================ the block's parts meet: outputs over the queries and rings, which nothing uses any more ================
         float* const outs = reinterpret_cast<float*>(smem);
@@ -514,7 +531,6 @@ __global__ void __launch_bounds__(NT, 1)
                         some ? make_float4(__uint_as_float(o[e]), __uint_as_float(o[e + 1]), __uint_as_float(o[e + 2]), __uint_as_float(o[e + 3]))
                              : make_float4(0.f, 0.f, 0.f, 0.f);
             }
-            // (where a role gave up, copies may still land on what lies here)
             *reinterpret_cast<float2*>(row + VD) = make_float2(row_m, ms.abort ? __uint_as_float(0x7fffffffu) : row_l);
         }
         cluster_meet();
@@ -543,22 +559,6 @@ __global__ void __launch_bounds__(NT, 1)
             if (lane == 0 && p.lse) p.lse[(long long)(q0 + row) * p.H + h] = l == 0.f ? -INFINITY : (mx + log2f(l)) * LN2;
         }
         cluster_meet();  // the others have read what lies here
-    }
-    if (ms.abort) {
-        // copies may still be on their way into this CTA's memory: the queries, at most the rings' last ones
-        if (warp == 8 && sent_k) {
-            const long long t0 = now_ns();
-            auto gone = [&](unsigned long long* bar, unsigned parity) {
-                while (!bar_try(bar, parity) && now_ns() - t0 < DRAIN_NS) {
-                }
-            };
-            if (nt0) gone(&ms.q_full[0], 0);
-            if (nt1) gone(&ms.q_full[1], 0);
-            for (int c = max(0, sent_k / PANELS - 2); c < sent_k / PANELS; ++c) gone(&ms.k_full[c & 1], (unsigned)c >> 1 & 1u);
-            for (int c = max(0, sent_v - VS); c < sent_v; ++c) gone(&ms.v_full[c % VS], (unsigned)(c / VS) & 1u);
-        }
-        if (tid == 0 && p.status) *p.status = MK_ERR_TIMEOUT;
-        __syncthreads();
     }
     if (warp == 9)
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tm), "n"(T_ALL) : "memory");
