@@ -270,7 +270,9 @@ int mk_decode_step_noalloc(mk_model* m, mk_kv* kv, const int32_t* tokens, const 
  *                 prefix (or the whole tiles of many rows) on the tensor
  *                 memory, mk_latent_attend and mk_prompt_attend leave out one
  *                 of their roles' signals: another waits until the wait
- *                 limit, and `status` gets MK_ERR_TIMEOUT.
+ *                 limit, and `status` gets MK_ERR_TIMEOUT;
+ *   "skip_late_attend_signal" in mk_latent_attend and mk_prompt_attend, the
+ *                 same from each CTA's fourth tile on.
  * Each host failure sets mk_last_error() to a message naming MK_FAULT.
  *
  * Debug mode: with MK_DEBUG=1 when the model is loaded, every CTA writes a

@@ -75,7 +75,7 @@ struct LatentP {
     float* slots;    // two of each CTA: its first and its last piece
     int* base;       // [items + 1]: first tile of each item, for the joining launch
     unsigned wait_ns;
-    int skip_signal;  // for tests: a role's signals are left out
+    unsigned signals;  // for tests: the tiles of a CTA after which a role's signals are left out
     int q_vec;        // queries can be copied 16 bytes at a time
 };
 
@@ -519,16 +519,16 @@ __global__ void __launch_bounds__(NT, 1)
                 if (act && (lane & 3) == 0) {
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
-                        // what a CTA that gave up leaves is no number, nor what sees a latent that is none
-                        const bool none = !ok || last[e] >= ms.bad[piece & 15];
+                        // what sees a latent that is no number is none
+                        const float l2 = last[e] >= ms.bad[piece & 15] ? __uint_as_float(0x7fffffffu) : l[e];
                         ms.m[r0 + 8 * e] = m[e];
-                        const float l2 = none ? __uint_as_float(0x7fffffffu) : l[e];
                         ms.sum[r0 + 8 * e] = l2;
                         ms.f[r0 + 8 * e] = l2 == 0.f ? 0.f : 1.f / l2;
                     }
                 }
                 tm_before();
-                bar_named(1, 128);
+                // nor what a CTA that gave up leaves: a row's weights are one warp's, its outputs all four's
+                const bool none = bar_any(1, 128, !ok);
                 tm_after();
                 const bool whole = take == it.n;
                 float* const slot = p.slots + (2ll * blockIdx.x + (u == first ? 0 : 1)) * ((long long)NR * (S::RANK + 2));
@@ -543,7 +543,8 @@ __global__ void __launch_bounds__(NT, 1)
                         if (whole) {
 #pragma unroll
                             for (int e = 0; e < 16; ++e)
-                                if (c + e < it.rows) put16<F16>(p.out, ms.to[c + e] + d, __uint_as_float(o[e]) * ms.f[c + e]);
+                                if (c + e < it.rows)
+                                    put16<F16>(p.out, ms.to[c + e] + d, none ? __uint_as_float(0x7fffffffu) : __uint_as_float(o[e]) * ms.f[c + e]);
                         } else {
 #pragma unroll
                             for (int e = 0; e < 16; ++e)
@@ -552,7 +553,7 @@ __global__ void __launch_bounds__(NT, 1)
                     }
                 }
                 if (tid < it.rows) {
-                    const float l2 = ms.sum[tid];
+                    const float l2 = none ? __uint_as_float(0x7fffffffu) : ms.sum[tid];
                     if (!whole)
                         *reinterpret_cast<float2*>(slot + (long long)NR * S::RANK + 2 * tid) = make_float2(ms.m[tid], l2);
                     else if (p.lse)
@@ -710,7 +711,7 @@ __global__ void __launch_bounds__(NT, 1)
                                 for (int j = 0; j < TILE / 16; ++j)
                                     mma_ss(tmu + S::T_O + mb * NR, desc_on(v, mb * 2 * TILE * 128 + j * 2048),
                                            desc_on(pb, j * 32), PV, i > 0 || j > 0);
-                            if (!p.skip_signal) mma_commit(&ms.pv_done[at_c.stage]);
+                            if (at_c.c < p.signals) mma_commit(&ms.pv_done[at_c.stage]);
                         }
                         __syncwarp();
                         at_c.next<STAGES>();
@@ -947,7 +948,7 @@ extern "C" int mk_latent_attend(const mk_latent_attention* a, void* workspace, i
     p.base = (int*)workspace, p.slots = (float*)((uint8_t*)workspace + pl.slots_off);
     const long long ns = mk_wait_ns_();
     p.wait_ns = (unsigned)(ns < 4000000000ll ? ns : 4000000000ll);
-    p.skip_signal = mk_fault_("skip_attend_signal");
+    p.signals = signalled_tiles();
     p.q_vec = rows_vec(a->q) && rows_vec(a->q_rope);
     auto go = [&](auto MT, auto NR) {
         constexpr int mt = decltype(MT)::value, nr = decltype(NR)::value;

@@ -86,7 +86,7 @@ struct PromptP {
     float scale;
     int split;                  // CTAs of a block, a cluster: each takes a part of its tiles
     unsigned wait_ns;
-    int skip_signal;            // for tests
+    unsigned signals;           // for tests: the tiles of a CTA after which a role's signals are left out
 };
 struct PromptMaps {
     CUtensorMap q, k, r, v;
@@ -442,7 +442,7 @@ __global__ void __launch_bounds__(NT, 1)
                             mma_ss(ts, desc_on(qd, c * PANEL_B + k * 32), desc_on(kd, at.i * PANEL_B + k * 32), QK, c > 0 || k > 0);
                         mma_commit(&ms.k_free[at.i]);
                     }
-                    if (!p.skip_signal) mma_commit(&ms.s_full[g]);
+                    if ((unsigned)j < p.signals) mma_commit(&ms.s_full[g]);
                 } else {
                     bar_arrive(&ms.turn[g ^ 1]);
                     for (int c = 0; c < PANELS; ++c, at.next()) bar_arrive(&ms.k_free[at.i]);
@@ -655,7 +655,7 @@ extern "C" int mk_prompt_attend(const mk_prompt_attention* a, void* stream) {
     p.q_heads = a->q_head != 0, p.k_heads = a->k_head != 0, p.v_heads = a->v_head != 0;
     const long long ns = mk_wait_ns_();
     p.wait_ns = (unsigned)(ns < 4000000000ll ? ns : 4000000000ll);
-    p.skip_signal = mk_fault_("skip_attend_signal");
+    p.signals = signalled_tiles();
     const int H = a->n_heads, dt = a->dtype, M = a->n_keys;
     PromptMaps maps = {};
     if (const int rc = map_of(a->q, dt, NOPE + ROPE, p.q_heads ? H : 0, a->n_tokens, a->q_head, a->q_token, ROWS, &maps.q)) return rc;

@@ -232,7 +232,11 @@ __device__ __forceinline__ bool bar_any(int id, int n, bool x) {
 }
 __device__ __forceinline__ void bar_named(int id, int n) { asm volatile("barrier.cta.sync %0, %1;" ::"r"(id), "r"(n) : "memory"); }
 
-// ---- host: tensor maps
+// ---- host
+// the tiles of a CTA that its roles signal: injected failures leave out all, or those behind the third
+inline unsigned signalled_tiles() { return mk_fault_("skip_attend_signal") ? 0u : mk_fault_("skip_late_attend_signal") ? 3u : ~0u; }
+
+// tensor maps
 typedef CUresult (*EncodeFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*, const cuuint64_t*,
                              const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
                              CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
