@@ -534,8 +534,9 @@ int mk_sample(const mk_sampling* args, void* stream);
  *   (x, y) -> magnitude (x cos a - y sin a, x sin a + y cos a),
  * with `inverse` by -a (for magnitude 1 the way back, and the gradient's).
  * inv_freq holds 64-bit numbers (finite) in device memory, so that scaled
- * frequencies of any recipe are the caller's to choose; angles keep 2^-60 of a
- * turn a position however far it is, negative positions turn the other way. */
+ * frequencies of any recipe are the caller's to choose; for those up to 2^40
+ * an angle keeps 2^-60 of a turn a position however far it is. Negative
+ * positions turn the other way. */
 enum mk_rotary_layout { MK_ROTARY_HALF = 0, MK_ROTARY_PAIRS = 1 };
 typedef struct mk_rotary {
     const double* inv_freq; /* device [n / 2] */

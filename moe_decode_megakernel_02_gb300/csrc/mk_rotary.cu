@@ -1,10 +1,11 @@
 // mk_rotary.cu -- rotation by positions (mk_rotate), and rows into a latent
 // cache, normalised and rotated on the way (mk_latent_write).
 //
-// Angles. A frequency becomes 2^-64ths of a turn a position, an integer; times
-// the position, modulo 2^64, it is the angle exactly, however far the position
-// is (a 32-bit product of radians would be 0.06 off at position 10^6). Its upper
-// 32 bits, rounded to 24, go to the half-turn sine and cosine: 2^-25 half turns.
+// Angles. A frequency becomes 2^-64ths of a turn a position, an integer, out of
+// a product kept as the sum of two 64-bit numbers; times the position, modulo
+// 2^64, it is the angle, however far the position is (a 32-bit product of
+// radians would be 0.06 off at position 10^6). Its upper 32 bits, rounded to 24,
+// go to the half-turn sine and cosine: 2^-25 half turns.
 //
 // Measured: 16004 tokens of 40 heads of 128, bf16, 56 us (5.9 TB/s, 86 % of a copy's
 // rate); the last 64 values of 4096 tokens' 16 heads of 192 with the rest copied 18
@@ -43,10 +44,12 @@ using namespace mkop;
 
 constexpr int MAX_HALF = 128;  // pairs of a rotation
 
-// 2^-64ths of a turn a position
+// 2^-64ths of a turn a position, off by less than 2 (and 2^-40 |radians|): the quotient by 2 pi is high + low, the product's
+// rounded value and what it left, each reduced to half a turn without loss (the sums of their 2^-64ths come round at 2^64)
 __device__ __forceinline__ unsigned long long turns_of(double radians) {
-    const double t = radians * 0.15915494309189533577;  // 1 / (2 pi)
-    return __double2ull_rn((t - floor(t)) * 18446744073709551616.0);
+    constexpr double INV = 0.15915494309189535, INV_LOW = -9.839338337591243e-18;  // 1 / (2 pi)
+    const double high = radians * INV, low = fma(radians, INV_LOW, fma(radians, INV, -high));
+    return (unsigned long long)__double2ll_rn((high - rint(high)) * 0x1p64) + (unsigned long long)__double2ll_rn((low - rint(low)) * 0x1p64);
 }
 // (cos, sin) at a position; sign -1: of the angle turned back
 __device__ __forceinline__ float2 turn(unsigned long long turns, long long position, float magnitude, float sign) {
@@ -222,15 +225,16 @@ __global__ void __launch_bounds__(WT, V <= 2 && RP == 1 ? 8 : 4) latent_write_ke
     const long long total = (long long)p.B * p.n;
     // gains lie in shared memory by lanes: value e of piece v of lane l at (v 8 + e) 32 + l
     __shared__ float gain[V * 256];
+    __shared__ unsigned long long all_turns[RP * 32];
     unsigned long long turns[RP];
-    if (p.gain) {
+    if (p.gain)
         for (int i = threadIdx.x; i < p.rank; i += WT) gain[(i >> 8) * 256 + (i & 7) * 32 + (i >> 3 & 31)] = gain_at(p, i);
-        __syncthreads();
-    }
+    if (p.freq && threadIdx.x < half) all_turns[threadIdx.x] = turns_of(p.freq[threadIdx.x]);  // (64-bit arithmetic: once a block)
+    __syncthreads();
     if (p.freq) {
 #pragma unroll
         for (int j = 0; j < RP; ++j)
-            if (j * 32 + lane < half) turns[j] = turns_of(p.freq[j * 32 + lane]);
+            if (j * 32 + lane < half) turns[j] = all_turns[j * 32 + lane];
     }
     auto pair_of = [&](int j, int& ia, int& ib) {
         const int i = j * 32 + lane;
