@@ -605,7 +605,8 @@ int mk_kv_latent_view(const mk_kv* kv, int32_t layer, mk_latent_pages* pages, mk
  * and what a token that sees nothing gets are as in mk_attention; latents that
  * a token does not see, NaN and infinities among them, do not reach its row.
  * What it sees is finite, scores below 2^100 in magnitude. Sums are 32-bit; a
- * probability goes into the second product rounded to the cache's type. */
+ * weight goes into the second product rounded to the cache's type, which loses
+ * half a step of it (in fp16 at least 2^-32 of the row's largest weight). */
 typedef struct mk_latent_attention {
     const mk_latent_pages* pages;
     const mk_page_table* table;
@@ -639,8 +640,9 @@ int mk_latent_attend(const mk_latent_attention* args, void* workspace, int64_t w
  *   out = sum_j softmax(x)_j v_j,    lse = log sum_j exp(x_j);
  * a query that sees nothing (n > m) gets zeros and lse -infinity. k_rope is
  * shared by the heads. Keys and values behind a query's own do not reach its
- * row; what it sees is finite, scores below 2^100. All pointers are multiples
- * of 16 bytes, so are the strides. Rows of no sequence stay as they are. */
+ * row; what it sees is finite, scores below 2^100. Sums and weights as in
+ * mk_latent_attention. All pointers are multiples of 16 bytes, so are the
+ * strides. Rows of no sequence stay as they are. */
 typedef struct mk_prompt_attention {
     const int32_t *q_starts, *k_starts; /* device [batch + 1], ascending */
     const void *q, *k, *k_rope, *v;     /* [n_tokens][n_heads][nope+rope], [n_keys][n_heads][nope], [n_keys][rope], */

@@ -16,7 +16,9 @@
 //
 // Roles: four warps softmax (S comes as 16-row fragments, a quad of threads a
 // row; P goes back through shared memory, rounded to the cache's type: what it
-// loses, half a step of each weight, is of the output's own rounding), one warp
+// loses, half a step of each weight, is of the output's own rounding. fp16 has no
+// steps of its own for small weights: they are taken 2^7 larger, so that half a
+// step is at least 2^-32 of the row's largest), one warp
 // copies, one cleans (below), two issue S and O'. O' is rescaled only when some
 // row's maximum has risen by more than 2^8 since its reference.
 //
@@ -162,6 +164,7 @@ __global__ void __launch_bounds__(LT) latent_rows(const __grid_constant__ Latent
 // ---------------------------------------------------------------- tensor cores
 
 constexpr int NT = 256, SMEM_MOST = 227 * 1024;
+constexpr float RISE = 8.f;  // powers of 2 that a maximum rises above its reference before the output is rescaled
 constexpr int TILE = 32;  // positions
 
 // A row block of a sequence and the tiles its rows see.
@@ -274,6 +277,8 @@ __global__ void __launch_bounds__(NT, 1)
     LatentMisc& ms = *reinterpret_cast<LatentMisc*>(smem + S::MISC_OFF);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const Limit limit = {&ms.abort, p.wait_ns};
+    // weights are 2^(x - m), m being UP below a maximum: in fp16 up to 2^15, of 65504
+    constexpr float UP = F16 ? 7.f : 0.f;
 
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     // the line: each thread counts a stretch of items; sums before it by shuffles
@@ -442,16 +447,16 @@ __global__ void __launch_bounds__(NT, 1)
                             a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, 1));
                             mx[e] = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, 2));
                         }
-                        rise = mx[0] > m[0] + 8.f || mx[1] > m[1] + 8.f;
+                        rise = mx[0] > m[0] + (UP + RISE) || mx[1] > m[1] + (UP + RISE);
                     }
                     if (i == 0) {
-                        m[0] = mx[0], m[1] = mx[1];
+                        m[0] = mx[0] - UP, m[1] = mx[1] - UP;
                     } else if (bar_any(1, 128, rise)) {
                         // rows whose maximum rose: their outputs so far shrink
                         if (act) {
 #pragma unroll
                             for (int e = 0; e < 2; ++e) {
-                                const float mn = mx[e] > m[e] + 8.f ? mx[e] : m[e];
+                                const float mn = mx[e] > m[e] + (UP + RISE) ? mx[e] - UP : m[e];
                                 const float f = m[e] == -INFINITY ? 1.f : ex2(m[e] - mn);  // (nothing so far: zeros)
                                 m[e] = mn;
                                 l[e] *= f;

@@ -11,7 +11,9 @@
 //               tensor maps, S in tensor memory;
 //   P = 2^(x - m), a row a thread, over the columns that S took, rounded to the
 //               values' type (what a weight loses, half a step, is of the
-//               output's own rounding);
+//               output's own rounding; fp16 has no steps of its own for small
+//               weights, which are taken 2^7 larger: half a step is at least
+//               2^-32 of the row's largest);
 //   O += P V    P as the tensor-memory operand, V from shared memory as it lies
 //               there (its rows are the product's K), O in tensor memory.
 // While the tensor cores work for one block, the other's four softmax warps
@@ -215,6 +217,8 @@ __global__ void __launch_bounds__(NT, 1)
         const int last = behind + row, least = behind + i0 + g * ROWS;  // the row's last key, and the block's first row's
         const bool neg = p.scale < 0.f;  // (then the smallest product counts: signs turned)
         const float scale2 = fabsf(p.scale) * LOG2E;
+        // the row's reference: UP below a maximum (weights in fp16 are up to 2^15, of 65504)
+        constexpr float UP = F16 ? 7.f : 0.f, RISE = 8.f;
         float mx = -INFINITY, l = 0.f;
         bool ok = true;
         // one tile; EDGE: some row of the block does not see all of it
@@ -241,11 +245,11 @@ __global__ void __launch_bounds__(NT, 1)
                 for (int i = 0; i < 4; ++i) t[i] = fmaxf(t[i], fmaxf(__uint_as_float(s[e + 2 * i]), __uint_as_float(s[e + 2 * i + 1])));
             // (a scale of 0 times a masked -infinity is no number)
             const float top = fmaxf(fmaxf(t[0], t[1]), fmaxf(t[2], t[3])), tile_m = top == -INFINITY ? top : top * scale2;
-            const bool rise = tile_m > mx + 8.f;
+            const bool rise = tile_m > mx + (UP + RISE);
             if (j == 0) {
-                mx = tile_m;
+                mx = tile_m - UP;
             } else if (__any_sync(0xffffffffu, rise)) {
-                const float mn = rise ? tile_m : mx, f = mx == -INFINITY ? 1.f : ex2(mx - mn);
+                const float mn = rise ? tile_m - UP : mx, f = mx == -INFINITY ? 1.f : ex2(mx - mn);
                 mx = mn;
                 l *= f;
                 // the last product is in the output
