@@ -131,7 +131,7 @@ __global__ void __launch_bounds__(LT) latent_rows(const __grid_constant__ Latent
         }
 #pragma unroll
         for (int d = 16; d; d >>= 1) s += __shfl_xor_sync(0xffffffffu, s, d);
-        s *= p.scale;
+        s = __fmul_rn(s, p.scale);  // (as below: rounded before a maximum is taken off)
         const float mn = fmaxf(m, s), f = __expf(m - mn), w = __expf(s - mn);
         m = mn;
         l = l * f + w;
@@ -418,10 +418,11 @@ __global__ void __launch_bounds__(NT, 1)
                             tm_wait_ld();
 #pragma unroll
                             for (int k = 0; k < 4; ++k) {
-                                x[0][8 * h + 2 * k] = __uint_as_float(s[4 * k]) * scale2;
-                                x[0][8 * h + 2 * k + 1] = __uint_as_float(s[4 * k + 1]) * scale2;
-                                x[1][8 * h + 2 * k] = __uint_as_float(s[4 * k + 2]) * scale2;
-                                x[1][8 * h + 2 * k + 1] = __uint_as_float(s[4 * k + 3]) * scale2;
+                                // (rounded before a maximum is taken off: of large scores a fused step would leave their rounding)
+                                x[0][8 * h + 2 * k] = __fmul_rn(__uint_as_float(s[4 * k]), scale2);
+                                x[0][8 * h + 2 * k + 1] = __fmul_rn(__uint_as_float(s[4 * k + 1]), scale2);
+                                x[1][8 * h + 2 * k] = __fmul_rn(__uint_as_float(s[4 * k + 2]), scale2);
+                                x[1][8 * h + 2 * k + 1] = __fmul_rn(__uint_as_float(s[4 * k + 3]), scale2);
                             }
                         }
                     }
@@ -447,7 +448,7 @@ __global__ void __launch_bounds__(NT, 1)
                             a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, 1));
                             mx[e] = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, 2));
                         }
-                        rise = mx[0] > m[0] + (UP + RISE) || mx[1] > m[1] + (UP + RISE);
+                        rise = mx[0] - m[0] > UP + RISE || mx[1] - m[1] > UP + RISE;
                     }
                     if (i == 0) {
                         m[0] = mx[0] - UP, m[1] = mx[1] - UP;
@@ -456,7 +457,7 @@ __global__ void __launch_bounds__(NT, 1)
                         if (act) {
 #pragma unroll
                             for (int e = 0; e < 2; ++e) {
-                                const float mn = mx[e] > m[e] + (UP + RISE) ? mx[e] - UP : m[e];
+                                const float mn = mx[e] - m[e] > UP + RISE ? mx[e] - UP : m[e];
                                 const float f = m[e] == -INFINITY ? 1.f : ex2(m[e] - mn);  // (nothing so far: zeros)
                                 m[e] = mn;
                                 l[e] *= f;

@@ -220,8 +220,74 @@ __global__ void __launch_bounds__(NT, 1)
         // the row's reference: UP below a maximum (weights in fp16 are up to 2^15, of 65504)
         constexpr float UP = F16 ? 7.f : 0.f, RISE = 8.f;
         float mx = -INFINITY, l = 0.f;
-        bool ok = true;
-        // one tile; EDGE: some row of the block does not see all of it
+        bool ok = true, large = false;  // large: some row's reference in the warp is, so that its own rounding counts
+        auto is_large = [&] { return __any_sync(0xffffffffu, mx != -INFINITY && fabsf(mx) >= 0x1p20f); };
+        // a reference moves: the output so far shrinks
+        auto raise = [&](bool rise, float to, int j) {
+            const float mn = rise ? to : mx, f = mx == -INFINITY ? 1.f : ex2(mx - mn);
+            mx = mn;
+            l *= f;
+            // the last product is in the output
+            if (!warp_wait(&ms.o_done[g], (j - 1) & 1, limit)) return false;
+            tm_after();
+#pragma unroll 1
+            for (int d = 0; d < VD; d += 16) {
+                uint32_t o[16];
+                tm_ld16(o, my_o + d);
+                tm_wait_ld();
+#pragma unroll
+                for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+                tm_st16(my_o + d, o);
+            }
+            tm_wait_st();
+            return true;
+        };
+        // A tile where references are large: products are rounded as those were before they are taken off (a fused step would
+        // leave their rounding, which at 2^31 is past any exponent). Rare, so in parts out of the tensor memory, where a
+        // part's weights only replace scores that have been read. (8192 tokens, 16 heads, none large: 257 us without it.)
+        auto large_tile = [&](int j) {
+            const int j0 = (from + j) * TILE;
+            auto part = [&](int c, float (&x)[32]) {
+                uint32_t y[32];
+                tm_ld32(y, my_s + c);
+                tm_wait_ld();
+#pragma unroll
+                for (int e = 0; e < 32; ++e)
+                    x[e] = j0 + c + e > last ? -INFINITY : __fmul_rn(__uint_as_float(neg ? y[e] ^ 0x80000000u : y[e]), scale2);
+            };
+            float x[32], tile_m = -INFINITY;
+#pragma unroll 1
+            for (int c = 0; c < TILE; c += 32) {
+                part(c, x);
+#pragma unroll
+                for (int e = 0; e < 32; ++e) tile_m = fmaxf(tile_m, x[e]);
+            }
+            const bool rise = tile_m - mx > UP + RISE;
+            if (j && __any_sync(0xffffffffu, rise)) {
+                if (!(ok = raise(rise, tile_m - UP, j))) return;
+            }
+            large = is_large();
+            const float ref = mx == -INFINITY ? 0.f : mx;
+#pragma unroll 1
+            for (int c = 0; c < TILE; c += 32) {
+                part(c, x);
+                uint32_t y[16];
+#pragma unroll
+                for (int e = 0; e < 16; ++e) {
+                    const float a = ex2(x[2 * e] - ref), d = ex2(x[2 * e + 1] - ref);
+                    l += a + d;
+                    y[e] = pack16<F16>(a, d);
+                }
+                tm_st16(my_s + (c >> 1), y);
+                if (c & 32) {
+                    tm_wait_st();
+                    tm_before();
+                    bar_arrive(&ms.p_ready[g][c >> 6]);
+                }
+            }
+        };
+        // one tile; EDGE: some row of the block does not see all of it. A reference that turns out large leaves the tile to
+        // large_tile (which finds nothing risen any more).
         auto tile = [&](auto EDGE, int j) {
             constexpr bool edge = decltype(EDGE)::value;
             const int j0 = (from + j) * TILE;
@@ -244,27 +310,14 @@ __global__ void __launch_bounds__(NT, 1)
 #pragma unroll
                 for (int i = 0; i < 4; ++i) t[i] = fmaxf(t[i], fmaxf(__uint_as_float(s[e + 2 * i]), __uint_as_float(s[e + 2 * i + 1])));
             // (a scale of 0 times a masked -infinity is no number)
-            const float top = fmaxf(fmaxf(t[0], t[1]), fmaxf(t[2], t[3])), tile_m = top == -INFINITY ? top : top * scale2;
-            const bool rise = tile_m > mx + (UP + RISE);
+            const float top = fmaxf(fmaxf(t[0], t[1]), fmaxf(t[2], t[3])), tile_m = top == -INFINITY ? top : __fmul_rn(top, scale2);
+            const bool rise = tile_m - mx > UP + RISE;
             if (j == 0) {
                 mx = tile_m - UP;
+                if ((large = is_large())) return;
             } else if (__any_sync(0xffffffffu, rise)) {
-                const float mn = rise ? tile_m - UP : mx, f = mx == -INFINITY ? 1.f : ex2(mx - mn);
-                mx = mn;
-                l *= f;
-                // the last product is in the output
-                if (!(ok = warp_wait(&ms.o_done[g], (j - 1) & 1, limit))) return;
-                tm_after();
-#pragma unroll 1
-                for (int d = 0; d < VD; d += 16) {
-                    uint32_t o[16];
-                    tm_ld16(o, my_o + d);
-                    tm_wait_ld();
-#pragma unroll
-                    for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
-                    tm_st16(my_o + d, o);
-                }
-                tm_wait_st();
+                if (!(ok = raise(rise, tile_m - UP, j))) return;
+                if ((large = is_large())) return;
             }
             const float ref = mx == -INFINITY ? 0.f : mx;
             float sum[4] = {0.f, 0.f, 0.f, 0.f};
@@ -295,8 +348,11 @@ __global__ void __launch_bounds__(NT, 1)
         for (int j = 0; j < mine_nt; ++j) {
             if (!(ok = warp_wait(&ms.s_full[g], j & 1, limit))) break;
             tm_after();
-            if ((from + j) * TILE + TILE - 1 > least) tile(std::true_type(), j);
-            else tile(std::false_type(), j);
+            if (!large) {
+                if ((from + j) * TILE + TILE - 1 > least) tile(std::true_type(), j);
+                else tile(std::false_type(), j);
+            }
+            if (ok && large) large_tile(j);
             if (!ok) break;
         }
         // ---- the block's end
