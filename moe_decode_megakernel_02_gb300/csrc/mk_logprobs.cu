@@ -117,7 +117,10 @@ __device__ __forceinline__ float largest(const uint4& z) {
     }
 }
 
-// Sums of a part of the row, against its largest logit (in exponents of 2, c a unit of logits).
+// Half of x - y: the difference may be beyond the range of 32 bits, where a temperature brings it back.
+__device__ __forceinline__ float half_of(float x, float y) { return __fmaf_rn(x, 0.5f, -0.5f * y); }
+
+// Sums of a part of the row, against its largest logit (in exponents of 2, c two units of logits).
 struct Part {
     float m, s, t;
 };
@@ -125,7 +128,7 @@ __device__ __forceinline__ Part join(const Part& x, const Part& y, float c) {
     const bool swap = y.m > x.m;
     const Part a = swap ? y : x, b = swap ? x : y;
     // a part without an unmasked logit has sums of 0; one that vanishes against the other adds nothing
-    const float d = b.m == -INFINITY ? 0.f : (b.m - a.m) * c, f = ex2(d);
+    const float d = b.m == -INFINITY ? 0.f : half_of(b.m, a.m) * c, f = ex2(d);
     return {max_nan(a.m, b.m), a.s + f * b.s, a.t + (f > 0.f ? f * (b.t + d * b.s) : 0.f)};
 }
 
@@ -225,16 +228,16 @@ __global__ void __launch_bounds__(GT, 2) logprob_kernel(const __grid_constant__ 
     const int w0 = (int)((long long)words * part / split), w1 = (int)((long long)words * (part + 1) / split);
     const float T = p.temperature ? p.temperature[r] : 1.f;
     const bool cold = !(T > 0x1p-120f);
-    const float c = cold ? 0.f : LOG2E / T;
+    const float c = cold ? 0.f : 2.f * (LOG2E / T);  // (times half a difference)
     const int k = p.top;
     if (TOP && tid == 0) sh.n = 0;
 
-    // the sums of e = 2^(c (x - m)) and of e c (x - m), of two lines of values whose arithmetic is paired (two values an
+    // the sums of e = 2^(c (x - m) / 2) and of e c (x - m) / 2, of two lines of values whose arithmetic is paired (two values an
     // instruction; 256 rows of 151936 bf16 logits without pairs 19.2 us)
-    float m = -INFINITY, s[2] = {0.f, 0.f}, t[2] = {0.f, 0.f};
+    float m = -INFINITY, half_m = m, s[2] = {0.f, 0.f}, t[2] = {0.f, 0.f};
     auto rise = [&](float top) {
         if (m != -INFINITY) {
-            const float d = (m - top) * c, f = ex2(d);
+            const float d = half_of(m, top) * c, f = ex2(d);
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
                 t[i] = f > 0.f ? f * (t[i] + d * s[i]) : 0.f;
@@ -242,6 +245,7 @@ __global__ void __launch_bounds__(GT, 2) logprob_kernel(const __grid_constant__ 
             }
         }
         m = max_nan(m, top);  // (no number stays one)
+        half_m = 0.5f * m;
     };
     bool have = false, sorted = false;  // k keys have been found; and nothing since
     u64 limit = 0;  // a key that the k-th largest one is not below; 0: none yet
@@ -250,8 +254,8 @@ __global__ void __launch_bounds__(GT, 2) logprob_kernel(const __grid_constant__ 
     if (TOP) __syncthreads();
 
     auto add = [&](float x, float y) {
-        float z0 = x, z1 = y, e0, e1;
-        add2(z0, z1, -m, -m);
+        float z0, z1, e0, e1;
+        fma2(z0, z1, x, y, 0.5f, 0.5f, -half_m, -half_m);
         fma2(z0, z1, z0, z1, c, c, 0.f, 0.f);
         // (below 2^-150 a weight is 0; a masked logit times an infinite temperature's 0 is no number, and so too)
         z0 = fmaxf(z0, -150.f), z1 = fmaxf(z1, -150.f);
@@ -420,7 +424,7 @@ __global__ void __launch_bounds__(GT, 2) logprob_kernel(const __grid_constant__ 
     m = all.m;
     const float nan = __uint_as_float(0x7fffffffu), ls = logf(all.s);
     const bool bad = cold || !(m < INFINITY) || m == -INFINITY;
-    auto logp = [&](float y) { return bad ? nan : y == -INFINITY ? y : (y - m) / T - ls; };
+    auto logp = [&](float y) { return bad ? nan : y == -INFINITY ? y : half_of(y, m) / T * 2.f - ls; };
     if (tid == 0 && p.entropy) p.entropy[r] = bad ? nan : ls - all.t / all.s * LN2;
     for (int g = tid; g < p.given; g += GT) {
         const int id = p.tokens[(long long)r * p.given + g];
