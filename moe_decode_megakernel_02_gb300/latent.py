@@ -32,7 +32,7 @@ _WRITE = struct.Struct("Pqii Pqqqii Pii fi")
 _ATTEND = struct.Struct("PP PP PPP PP ii fi Pqii Pqqqii Pqqqii Pqqqii 72s")
 _PROMPT = struct.Struct("PP PPPPP PP qqqqqqqqq iiiiiiii fi")
 _WriteBytes, _AttendBytes = ctypes.c_char * _WRITE.size, ctypes.c_char * _ATTEND.size
-_NEED = {}  # workspace bytes by device and shapes
+_NEED, _KEPT = {}, 256  # workspace bytes by device and shapes, of so many at most
 assert _PAGES.size == ctypes.sizeof(LatentPagesStruct) == 72 and _WRITE.size == 24 + 40 + _ROTARY.size
 assert _ATTEND.size == 88 + 24 + 3 * 40 + 72 and ctypes.sizeof(LatentAttentionStruct) == 88
 assert _PROMPT.size == ctypes.sizeof(PromptAttentionStruct) == 184
@@ -169,6 +169,8 @@ class LatentPages:
             if need is None:
                 c = ctypes.c_int64()
                 _check(L.mk_latent_attend_workspace(at, _byref(c)))
+                if len(_NEED) >= _KEPT:
+                    _NEED.clear()
                 need = _NEED[key] = c.value
             w = torch.empty((need,), dtype=torch.uint8, device=dev) if need else None
             rc = L.mk_latent_attend(at, w.data_ptr() if need else 0, need, h)
