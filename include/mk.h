@@ -558,7 +558,8 @@ typedef struct mk_rotation {
     int32_t batch, n_tokens, n_heads, head_dim, first, reserved;
 } mk_rotation;
 
-/* Errors: INVALID_ARG (NULL, shapes, alignment). */
+/* Errors: INVALID_ARG (NULL, shapes, alignment); UNSUPPORTED (2^25 tokens and
+ * more in a call, more than 4096 heads, heads of more than 65536 values). */
 int mk_rotate(const mk_rotation* args, void* stream);
 
 /* One layer's latent cache: position r of page p has its latent (rank values,
@@ -656,7 +657,8 @@ typedef struct mk_prompt_attention {
 } mk_prompt_attention;
 
 /* Errors: INVALID_ARG; UNSUPPORTED (dims other than nope 128, rope 64, v 128;
- * more than 2^30 keys, 2^20 sequences or 2^27 queries of heads).
+ * more than 2^30 keys, 2^20 sequences or 2^27 queries of heads; rows of
+ * several tokens, or out's of several heads, in one place: a stride of 0).
  * Bounds that descend or leave the rows are reported through `status` (as
  * MK_ERR_INVALID_ARG) and the sequence is skipped; where other sequences then
  * overlap, their outputs are undefined. */

@@ -878,9 +878,9 @@ int check(const mk_latent_attention* a) {
     if (a->n_tokens < 1 || a->n_heads < 1) return fail(MK_ERR_INVALID_ARG, "latent attend: n_tokens or n_heads below 1");
     if (!a->lens || off_by4(a->lens, a->starts, a->lse, a->status))
         return fail(MK_ERR_INVALID_ARG, "latent attend: lens is NULL, or lens, starts, lse or status not aligned to 4 bytes");
-    if (const int rc = check_rows(a->q, "q")) return rc;
-    if (const int rc = check_rows(a->q_rope, "q_rope")) return rc;
-    if (const int rc = check_rows(a->out, "out")) return rc;
+    if (const int rc = check_rows(a->q, "latent attend", "q")) return rc;
+    if (const int rc = check_rows(a->q_rope, "latent attend", "q_rope")) return rc;
+    if (const int rc = check_rows(a->out, "latent attend", "out")) return rc;
     if (a->q->dtype != g.dtype || a->q_rope->dtype != g.dtype || a->out->dtype != g.dtype)
         return fail(MK_ERR_INVALID_ARG, "latent attend: q, q_rope and out must have the cache's type");
     if (!(a->scale >= -1e30f && a->scale <= 1e30f)) return fail(MK_ERR_INVALID_ARG, "latent attend: scale is not a number in range");

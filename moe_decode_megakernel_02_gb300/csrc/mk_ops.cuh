@@ -64,7 +64,7 @@ inline bool off_by4(const P*... p) {
 // what every operator on pages asks of its cache and table
 int check_pages(const mk_pages* p, const mk_page_table* t);
 int check_latent(const mk_latent_pages* p, const mk_page_table* t);
-int check_rows(const mk_rows* r, const char* name);
+int check_rows(const mk_rows* r, const char* what, const char* name);
 // whether rows can be read 16 bytes at a time
 bool rows_vec(const mk_rows* r);
 

@@ -42,11 +42,11 @@ int check_pages(const mk_pages* p, const mk_page_table* t) {
     return MK_OK;
 }
 
-int check_rows(const mk_rows* r, const char* name) {
-    if (!r || !r->data) return fail(MK_ERR_INVALID_ARG, "pages: %s is NULL", name);
+int check_rows(const mk_rows* r, const char* what, const char* name) {
+    if (!r || !r->data) return fail(MK_ERR_INVALID_ARG, "%s: %s is NULL", what, name);
     const int e = dtype_bytes(r->dtype);
-    if (!e) return fail(MK_ERR_INVALID_ARG, "pages: unknown dtype %d of %s", r->dtype, name);
-    if ((uintptr_t)r->data % e) return fail(MK_ERR_INVALID_ARG, "pages: %s is not aligned to its type", name);
+    if (!e) return fail(MK_ERR_INVALID_ARG, "%s: unknown dtype %d of %s", what, r->dtype, name);
+    if ((uintptr_t)r->data % e) return fail(MK_ERR_INVALID_ARG, "%s: %s is not aligned to its type", what, name);
     return MK_OK;
 }
 
@@ -380,8 +380,8 @@ int copy(const mk_pages* g, const mk_page_table* t, const int32_t* positions, co
     if (off_by4(positions, counts, status))
         return fail(MK_ERR_INVALID_ARG, "pages: positions, counts or status not aligned to 4 bytes");
     if (n < 0) return fail(MK_ERR_INVALID_ARG, "pages: negative token count");
-    if (const int rc = check_rows(k, "k")) return rc;
-    if (const int rc = check_rows(v, "v")) return rc;
+    if (const int rc = check_rows(k, "pages", "k")) return rc;
+    if (const int rc = check_rows(v, "pages", "v")) return rc;
     if (k->dtype != v->dtype) return fail(MK_ERR_INVALID_ARG, "pages: k and v rows must have one type");
     if (n == 0) return MK_OK;
     CopyP p;

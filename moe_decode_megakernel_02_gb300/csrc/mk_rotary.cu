@@ -348,8 +348,8 @@ extern "C" int mk_rotate(const mk_rotation* a, void* stream) {
     if (const int rc = check_rotary(a->rotary, "rotate")) return rc;
     const mk_rotary& r = *a->rotary;
     if (!a->positions || off_by4(a->positions)) return fail(MK_ERR_INVALID_ARG, "rotate: positions is NULL or not aligned to 4 bytes");
-    if (const int rc = check_rows(a->x, "x")) return rc;
-    if (const int rc = check_rows(a->out, "out")) return rc;
+    if (const int rc = check_rows(a->x, "rotate", "x")) return rc;
+    if (const int rc = check_rows(a->out, "rotate", "out")) return rc;
     const mk_rows &x = *a->x, &o = *a->out;
     if (x.dtype != o.dtype) return fail(MK_ERR_INVALID_ARG, "rotate: x and out must have one type");
     if (a->batch < 0 || a->n_tokens < 0 || a->n_heads < 0 || a->head_dim < 1 || a->position_stride < 0)
@@ -398,7 +398,7 @@ extern "C" int mk_latent_write(const mk_latent_pages* g, const mk_page_table* t,
     if (off_by4(positions, counts, status))
         return fail(MK_ERR_INVALID_ARG, "latent: positions, counts or status not aligned to 4 bytes");
     if (n < 0) return fail(MK_ERR_INVALID_ARG, "latent: negative token count");
-    if (const int rc = check_rows(rows, "rows")) return rc;
+    if (const int rc = check_rows(rows, "latent", "rows")) return rc;
     if (gain) {
         const int e = dtype_bytes(gain_dtype);
         if (!e || (uintptr_t)gain % e) return fail(MK_ERR_INVALID_ARG, "latent: gain's type is unknown, or it is not aligned to it");
