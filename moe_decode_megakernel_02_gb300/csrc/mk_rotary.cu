@@ -287,9 +287,10 @@ __global__ void __launch_bounds__(WT, V <= 2 && RP == 1 ? 8 : 4) latent_write_ke
 #pragma unroll
                     for (int e = 0; e < 8; ++e) sum += y[e] * y[e];
                 }
+                sum *= 0x1p-8f;  // (a lane's 32 squares below 2^120 are in range, a row's 1024 would not be)
 #pragma unroll
                 for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-                f = rsqrtf(sum / (float)p.rank + p.eps);
+                f = rsqrtf(sum / ((float)p.rank * 0x1p-8f) + p.eps);
             }
             const long long to = page[k] * p.page_s + r * p.row_s;
 #pragma unroll
