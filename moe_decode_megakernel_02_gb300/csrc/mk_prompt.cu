@@ -227,6 +227,7 @@ __global__ void __launch_bounds__(NT, 1)
             const float mn = rise ? to : mx, f = mx == -INFINITY ? 1.f : ex2(mx - mn);
             mx = mn;
             l *= f;
+            if (j == 0) return true;
             // the last product is in the output
             if (!warp_wait(&ms.o_done[g], (j - 1) & 1, limit)) return false;
             tm_after();
@@ -243,43 +244,43 @@ __global__ void __launch_bounds__(NT, 1)
             return true;
         };
         // A tile where references are large: products are rounded as those were before they are taken off (a fused step would
-        // leave their rounding, which at 2^31 is past any exponent). Rare, so in parts out of the tensor memory, where a
-        // part's weights only replace scores that have been read. (8192 tokens, 16 heads, none large: 257 us without it.)
+        // leave their rounding, which at 2^31 is past any exponent). Rare, so in small parts out of the tensor memory,
+        // where a part's weights only replace scores that have been read. (Its being here costs prompts without any up to 1 %.)
         auto large_tile = [&](int j) {
             const int j0 = (from + j) * TILE;
-            auto part = [&](int c, float (&x)[32]) {
-                uint32_t y[32];
-                tm_ld32(y, my_s + c);
+            auto part = [&](int c, float (&x)[16]) {
+                uint32_t y[16];
+                tm_ld16(y, my_s + c);
                 tm_wait_ld();
 #pragma unroll
-                for (int e = 0; e < 32; ++e)
+                for (int e = 0; e < 16; ++e)
                     x[e] = j0 + c + e > last ? -INFINITY : __fmul_rn(__uint_as_float(neg ? y[e] ^ 0x80000000u : y[e]), scale2);
             };
-            float x[32], tile_m = -INFINITY;
+            float x[16], tile_m = -INFINITY;
 #pragma unroll 1
-            for (int c = 0; c < TILE; c += 32) {
+            for (int c = 0; c < TILE; c += 16) {
                 part(c, x);
 #pragma unroll
-                for (int e = 0; e < 32; ++e) tile_m = fmaxf(tile_m, x[e]);
+                for (int e = 0; e < 16; ++e) tile_m = fmaxf(tile_m, x[e]);
             }
             const bool rise = tile_m - mx > UP + RISE;
-            if (j && __any_sync(0xffffffffu, rise)) {
+            if (__any_sync(0xffffffffu, rise)) {
                 if (!(ok = raise(rise, tile_m - UP, j))) return;
             }
             large = is_large();
             const float ref = mx == -INFINITY ? 0.f : mx;
 #pragma unroll 1
-            for (int c = 0; c < TILE; c += 32) {
+            for (int c = 0; c < TILE; c += 16) {
                 part(c, x);
-                uint32_t y[16];
+                uint32_t y[8];
 #pragma unroll
-                for (int e = 0; e < 16; ++e) {
+                for (int e = 0; e < 8; ++e) {
                     const float a = ex2(x[2 * e] - ref), d = ex2(x[2 * e + 1] - ref);
                     l += a + d;
                     y[e] = pack16<F16>(a, d);
                 }
-                tm_st16(my_s + (c >> 1), y);
-                if (c & 32) {
+                tm_st8(my_s + (c >> 1), y);
+                if ((c & 48) == 48) {
                     tm_wait_st();
                     tm_before();
                     bar_arrive(&ms.p_ready[g][c >> 6]);
@@ -312,10 +313,7 @@ __global__ void __launch_bounds__(NT, 1)
             // (a scale of 0 times a masked -infinity is no number)
             const float top = fmaxf(fmaxf(t[0], t[1]), fmaxf(t[2], t[3])), tile_m = top == -INFINITY ? top : __fmul_rn(top, scale2);
             const bool rise = tile_m - mx > UP + RISE;
-            if (j == 0) {
-                mx = tile_m - UP;
-                if ((large = is_large())) return;
-            } else if (__any_sync(0xffffffffu, rise)) {
+            if (__any_sync(0xffffffffu, rise)) {
                 if (!(ok = raise(rise, tile_m - UP, j))) return;
                 if ((large = is_large())) return;
             }

@@ -195,6 +195,12 @@ __device__ __forceinline__ void tm_st16(uint32_t a, const uint32_t (&r)[16]) {
         "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
         : "memory");
 }
+// 8 columns of this thread's row
+__device__ __forceinline__ void tm_st8(uint32_t a, const uint32_t (&r)[8]) {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(a), "r"(r[0]), "r"(r[1]),
+                 "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+                 : "memory");
+}
 // 16 rows by 32 columns over a warp, as fragments: r[4 k + i] is row lane / 4 + 8 (i / 2), column 8 k + 2 (lane % 4) + i % 2
 __device__ __forceinline__ void tm_frag32(uint32_t (&r)[16], uint32_t a) {
     asm volatile(
