@@ -40,7 +40,7 @@
 // join). Rows past 16 are bound by what feeds the products from shared memory: 64
 // rows take 1030 cycles a tile for S (36 steps of 28) and 410 for O', 1600 in
 // all: 8 sequences of 8192 with 7 tokens 38 us (9 of them pieces and join), 64 of
-// them 161. Tiles of 64 positions feed S better (36 cycles a step of twice the
+// them 160. Tiles of 64 positions feed S better (36 cycles a step of twice the
 // positions) but two of them fill shared memory, and copies then wait: 192 us.
 //
 // Pages of fewer than 8 positions, or overlapping ones (a stride of 0), have no

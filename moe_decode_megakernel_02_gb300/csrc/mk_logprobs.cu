@@ -15,10 +15,13 @@
 // Ids rise from round to round, so that an equal logit of a later round never
 // counts.
 //
-// Bound by issue for batches: 256 rows of 151936 bf16 logits take 19 us without
-// alternatives (11 instructions a value, 61 % of a copy's rate), 40 with 20 of them
-// (18 a value, and the rounds' votes). Single rows by latency, a trip to memory,
-// the threshold's and the ranks' votes, the cluster's meeting: 32000 fp32 logits 7 us.
+// 256 rows of 151936 bf16 logits take 19 us without alternatives (60 % of a copy's
+// rate): a row a CTA leaves 104 of 152 SMs two rows and 48 one, and 11 instructions a
+// value are 10.6 us of all SMs' issue slots, as long as the copy. With 20 alternatives
+// 41: 18 instructions a value are 17.4 us; the rest is each round's barrier, at which
+// all warps meet also where nothing qualifies, and the list's cuts. Single rows are
+// bound by latency, a trip to memory, the threshold's and the ranks' votes, the
+// cluster's meeting: 32000 fp32 logits 7.5 us.
 #include <climits>
 #include <type_traits>
 
@@ -233,7 +236,7 @@ __global__ void __launch_bounds__(GT, 2) logprob_kernel(const __grid_constant__ 
     if (TOP && tid == 0) sh.n = 0;
 
     // the sums of e = 2^(c (x - m) / 2) and of e c (x - m) / 2, of two lines of values whose arithmetic is paired (two values an
-    // instruction; 256 rows of 151936 bf16 logits without pairs 19.2 us)
+    // instruction; without pairs 256 rows of 151936 bf16 logits take 3 % longer)
     float m = -INFINITY, half_m = m, s[2] = {0.f, 0.f}, t[2] = {0.f, 0.f};
     auto rise = [&](float top) {
         if (m != -INFINITY) {
@@ -484,7 +487,7 @@ extern "C" int mk_logprobs(const mk_logprob* a, void* stream) {
     p.logprobs = a->logprobs, p.entropy = a->entropy, p.top_ids = a->top_ids, p.top_logprobs = a->top_logprobs;
     p.V = a->vocab, p.given = a->given, p.top = a->top;
     // CTAs of a row: one or more an SM, as long as each has a part of a round (a CTA's first threshold and its end cost as
-    // much as two rounds: 256 rows of 151936 bf16 logits take 40 us in one part each, 51 in two)
+    // much as two rounds: 256 rows of 151936 bf16 logits take 41 us in one part each, 51 in two)
     p.split = 1;
     while (p.split < MAX_CLUSTER && (int64_t)a->rows * p.split < sms && a->vocab / p.split > GT * 4) p.split *= 2;
     cudaStream_t s = (cudaStream_t)stream;

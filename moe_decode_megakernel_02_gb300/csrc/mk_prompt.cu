@@ -37,11 +37,13 @@
 // Longest CTAs first: blocks of a sequence in falling order, all heads of one
 // after another, so that short ones fill the end. All waits have a limit.
 //
-// Measured, 16 heads, bf16: 8192 tokens 250 us (1.37 PFLOP/s of what is seen, 72 %
-// of a large product's rate), 4 x 4096 282, 8 x 2048 181, 1 x 1024 23. A tile of
+// Measured, 16 heads, bf16: 8192 tokens 251 us (1.37 PFLOP/s of what is seen, 71 %
+// of a large product's rate), 4 x 4096 283, 8 x 2048 183, 1 x 1024 23. A tile of
 // both blocks takes 3500 cycles, 2590 of them products; the rest is the turns'
-// hand-over and waits (a wait that is already over costs some 100). Short prompts
-// are bound by latency: 8 us before the first scores and after the last ones.
+// hand-over and waits (a wait that is already over costs some 100). A CTA has all
+// of an SM's memory and nothing runs beside its 8 us before the first scores and
+// after the last ones: these bound short prompts, and are some 50 of the 183 us of
+// 8 x 2048 (6.7 CTAs an SM).
 #include <climits>
 #include <type_traits>
 
@@ -481,7 +483,7 @@ __global__ void __launch_bounds__(NT, 1)
         bool ok = true;
         Slot<KS> ks;
         Slot<VS> vs;
-        // (the whole warp waits, then one lane issues: a role that ran in one thread altogether hung)
+        // (the whole warp runs this and one lane issues: the shuffle above and the votes of a wait need all 32)
         auto here = [&](unsigned long long* bar, unsigned parity) { return bar_wait(bar, parity & 1u, limit); };
         // S of a tile; one that the block does not see is let go as it comes
         auto scores = [&](int j) {
@@ -670,8 +672,9 @@ int run(PromptP& p, const PromptMaps& maps, int some, int64_t blocks, cudaStream
     };
     // Few blocks share their tiles out to clusters, as long as these run all at once and a CTA has four tiles or more (of an
     // average over the sequences that may have queries: the lengths are on the device, so one long context among many short
-    // ones is not shared). One token behind 16000 keys and 15 sequences without any, 16 heads: 204 us unshared, 59 so. 256 tokens at 8192 positions, 16 heads: 136 us by one CTA a block, 48 by four; by eight, which
-    // do not all find room at once, 63.
+    // ones is not shared, nor where a ragged batch's bound on blocks is past the room). 16 heads, 256 tokens at 8192
+    // positions: 136 us by one CTA a block, 48 by four; by eight, which do not all find room at once, 63. One token behind
+    // 16000 keys beside 15 sequences without any: 204 us by one, 59 by eight.
     p.split = 1;
     for (int i = 0; i < 3 && p.n_k / some >= (4 * TILE << (i + 1)) && blocks <= fits(i); ++i) p.split = 2 << i;
     cfg.gridDim = dim3((unsigned)(blocks * p.split));

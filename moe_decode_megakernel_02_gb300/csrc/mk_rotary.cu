@@ -8,10 +8,12 @@
 // go to the half-turn sine and cosine: 2^-25 half turns.
 //
 // Measured: 16004 tokens of 40 heads of 128, bf16, 56 us (5.9 TB/s, 86 % of a copy's
-// rate); the last 64 values of 4096 tokens' 16 heads of 192 with the rest copied 18
-// (41 %); 8 tokens 3 us, a launch. Rows into a latent cache, 16 ragged prompts of up
-// to 4096 tokens from fp32 28 us (5.2 TB/s, 77 %), from bf16 32 for 65536 rows; 8
-// tokens 2.7 us.
+// rate); 8 tokens 3 us, a launch. The last 64 values of 4096 tokens' 16 heads of 192
+// with the rest copied 18 (40 %): 320 blocks on 304 places (124 registers a thread),
+// and a warp's turning and copying units run one after the other. Rows into a latent
+// cache, 16 ragged prompts of up to 4096 tokens from fp32 28 us (5.2 TB/s, 77 %); 65536
+// rows from bf16 32 (4.7 TB/s: as many instructions a row for fewer bytes, the rope
+// part's of two bytes a lane); 8 tokens 2.7 us.
 #include "mk_values.cuh"
 
 namespace mkop {

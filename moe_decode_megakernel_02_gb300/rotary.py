@@ -32,7 +32,9 @@ def frequencies(n, theta=1e4, factor=1.0, original=None, low=1.0, high=32.0, dev
     factor > 1 stretches positions for contexts longer than a model was trained on. Without `original` every
     frequency is divided by it. With it (the trained context's length) a pair that turns more than `high` times within
     that length keeps its frequency, one that turns less than `low` times is divided by factor, and between them the
-    share that is kept falls linearly with the number of turns; magnitude(factor) goes with it."""
+    share that is kept falls linearly with the number of turns; magnitude(factor) goes with it. Recipes whose
+    share falls linearly with the pair's index give other angles between the two: for a model trained with one of them,
+    pass frequencies of your own."""
     if n < 2 or n % 2:
         raise ValueError(f"n must be even and at least 2, got {n}")
     if not (theta > 0 and factor > 0):
