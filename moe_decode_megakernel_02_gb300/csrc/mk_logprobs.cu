@@ -50,11 +50,12 @@ struct LogprobP {
     int V, given, top, split;  // split: CTAs of a row
 };
 
+template <bool TOP>
 struct LogprobShared {
-    u64 list[CAP];
-    u64 best[MAX_TOP];  // sorted
-    u64 group[GROUPS];
-    u64 merge[MAX_CLUSTER * MAX_TOP];
+    u64 list[TOP ? CAP : 1];
+    u64 best[TOP ? MAX_TOP : 1];  // sorted
+    u64 group[TOP ? GROUPS : 1];
+    u64 merge[TOP ? MAX_CLUSTER * MAX_TOP : 1];
     float4 part[GT / 32];  // Part of the warps
     float4 cta[MAX_CLUSTER], mine;
     int n;
@@ -157,7 +158,8 @@ __device__ __forceinline__ void ranks(const u64* keys, int n, F found) {
 }
 
 // The first k keys of `n` in sh.list, sorted, to sh.best; returns how many there are.
-__device__ int first_keys(LogprobShared& sh, int n, int k) {
+template <typename S>
+__device__ int first_keys(S& sh, int n, int k) {
     const int tid = threadIdx.x;
     // long lists (adverse orders) are cut by a threshold of theirs first
     while (n > GT) {
@@ -220,7 +222,7 @@ __device__ __forceinline__ void put_remote(float4* p, int cta, float4 v) {
 template <int DT, bool TOP>
 __global__ void __launch_bounds__(GT, 2) logprob_kernel(const __grid_constant__ LogprobP p) {
     constexpr int VEC = DT == MK_DT_F32 ? 4 : 8;  // values of 16 bytes
-    __shared__ LogprobShared sh;
+    __shared__ LogprobShared<TOP> sh;
     extern __shared__ __align__(16) uint8_t ring[];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, split = p.split;
     const int r = blockIdx.x / split, part = blockIdx.x - r * split;
@@ -395,7 +397,9 @@ __global__ void __launch_bounds__(GT, 2) logprob_kernel(const __grid_constant__ 
     Part all = meet(Part{m, s[0] + s[1], t[0] + t[1]}, 32);
     if (lane == 0) sh.part[warp] = make_float4(all.m, all.s, all.t, 0.f);
     int found = k;
-    if (TOP && !sorted) found = first_keys(sh, n, k);
+    if constexpr (TOP) {
+        if (!sorted) found = first_keys(sh, n, k);
+    }
     __syncthreads();
     if (warp == 0) {
         const float4 y = sh.part[lane & (GT / 32 - 1)];
@@ -408,10 +412,12 @@ __global__ void __launch_bounds__(GT, 2) logprob_kernel(const __grid_constant__ 
     if (split > 1) {
         asm volatile("barrier.cluster.arrive.relaxed.aligned;\n\tbarrier.cluster.wait.aligned;" ::: "memory");  // all have begun
         if (tid == 0) put_remote(&sh.cta[part], 0, sh.mine);
-        if (TOP && tid < k) put_remote(&sh.merge[part * k + tid], 0, tid < found ? sh.best[tid] : 0);
+        if constexpr (TOP) {
+            if (tid < k) put_remote(&sh.merge[part * k + tid], 0, tid < found ? sh.best[tid] : 0);
+        }
         asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
         if (part) return;
-        if (TOP) {
+        if constexpr (TOP) {
             for (int i = tid; i < split * k; i += GT) {
                 const u64 y = sh.merge[i];
                 int rank = 0;
@@ -433,10 +439,12 @@ __global__ void __launch_bounds__(GT, 2) logprob_kernel(const __grid_constant__ 
         const int id = p.tokens[(long long)r * p.given + g];
         p.logprobs[(long long)r * p.given + g] = (unsigned)id < (unsigned)p.V ? logp(at1<DT>(x, id)) : nan;
     }
-    if (TOP && tid < k) {
-        const u64 y = sh.best[tid];
-        p.top_ids[(long long)r * k + tid] = bad ? -1 : (int)~(uint32_t)y;
-        p.top_logprobs[(long long)r * k + tid] = logp(logit_of(y));
+    if constexpr (TOP) {
+        if (tid < k) {
+            const u64 y = sh.best[tid];
+            p.top_ids[(long long)r * k + tid] = bad ? -1 : (int)~(uint32_t)y;
+            p.top_logprobs[(long long)r * k + tid] = logp(logit_of(y));
+        }
     }
 }
 
