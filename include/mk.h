@@ -584,8 +584,9 @@ typedef struct mk_latent_pages {
  *   c_i = x_i / sqrt(mean x^2 + eps) gain_i,
  * without (NULL) it is kept; with `rotary` (n = rope_dim) the rope part turns
  * by its position, without (NULL) it is kept. In 32 bits (magnitudes below
- * 2^60 and, where eps is 0, not all below 2^-50), rounded once. Rows past counts[b], and every other row of the cache,
- * stay as they are; positions or pages out of range as in mk_pages_write.
+ * 2^60 and, where eps is 0, not all below 2^-50), rounded once. Rows past
+ * counts[b], and every other row of the cache, stay as they are; positions or
+ * pages out of range as in mk_pages_write.
  * Errors: INVALID_ARG; UNSUPPORTED (rank, rope_dim, page_size). */
 int mk_latent_write(const mk_latent_pages* pages, const mk_page_table* table, const int32_t* positions,
                     const int32_t* counts, int32_t n, const mk_rows* rows, const void* gain, int32_t gain_dtype,

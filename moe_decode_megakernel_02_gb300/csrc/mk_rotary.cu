@@ -50,7 +50,7 @@ constexpr int MAX_HALF = 128;  // pairs of a rotation
 // rounded value and what it left, each reduced to half a turn without loss (the sums of their 2^-64ths come round at 2^64)
 __device__ __forceinline__ unsigned long long turns_of(double radians) {
     constexpr double INV = 0.15915494309189535, INV_LOW = -9.839338337591243e-18;  // 1 / (2 pi)
-    const double high = radians * INV, low = fma(radians, INV_LOW, fma(radians, INV, -high));
+    const double high = __dmul_rn(radians, INV), low = fma(radians, INV_LOW, fma(radians, INV, -high));
     return (unsigned long long)__double2ll_rn((high - rint(high)) * 0x1p64) + (unsigned long long)__double2ll_rn((low - rint(low)) * 0x1p64);
 }
 // (cos, sin) at a position; sign -1: of the angle turned back
